@@ -163,6 +163,13 @@ def load() -> C.CDLL:
         _sig(lib, "paged_attention_step_fp8", C.c_int32,
              [_vp, _vp, _vp, _vp, C.c_int32, _vp, _vp, C.c_int32, C.c_int32, C.c_int32,
               _vp, C.c_int32, C.c_float, C.c_float, _vp, C.c_size_t, _vp, sp, _vp, _vp])
+        norm_rope = [_vp, C.c_int64, _vp, C.c_int64, _vp, C.c_int64, _vp, _vp, C.c_float, _vp,
+                     C.c_int32, C.c_int32, _vp, C.c_int32, _vp, C.c_int32, _vp, _vp, _vp]
+        _sig(lib, "pa_rope_pairs", C.c_int32,
+             [C.POINTER(C.c_double), _i32p, C.c_int32, C.c_int32, _vp])
+        _sig(lib, "paged_qk_norm_rope_write", C.c_int32, norm_rope + [sp, _vp, _vp])
+        _sig(lib, "paged_qk_norm_rope_write_fp8", C.c_int32,
+             norm_rope + [C.c_float, C.c_float, sp, _vp, _vp])
         _lib = lib
         return lib
 
@@ -499,6 +506,138 @@ def paged_attention_step_fp8(q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_l
         float(k_scale), float(v_scale), _dev(workspace), ws_bytes, _dev(out), C.byref(shape),
         _dev(err), _stream(stream)),
         "paged_attention_step_fp8")
+
+
+def _here() -> int:
+    """The current CUDA device, which every tensor of a call has to be on."""
+    import torch
+    return torch.cuda.current_device()
+
+
+def _tensor(t, dtype, dev: int, what: str) -> int:
+    """Device address of a dense tensor of the given type on device `dev`."""
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: expected a tensor on the current CUDA device ({dev})")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _dims(t, shape: tuple, what: str) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def _pools(k_pool, v_pool, shape: Shape, dtype, dev: int):
+    """Addresses of K and V pools of this shape (v_pool may be None)."""
+    want = (shape.num_blocks, shape.block_size, shape.num_kv_heads, shape.head_dim)
+    out = []
+    for t, what in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        if t is None:
+            continue
+        _dims(t, want, what)
+        out.append(_tensor(t, dtype, dev, what))
+    return out
+
+
+# ------------------------------------------------------- norm, rotation and KV write
+
+ROPE_PAIR_DTYPE = np.dtype([("step", np.uint64), ("axis", np.int32), ("reserved", np.int32)])
+
+
+def pa_rope_pairs(inv_freq, axes=None, n_axes: Optional[int] = None, device=None):
+    """The rotation table of paged_qk_norm_rope_write: frequencies in radians per position, one per
+    column pair, and the axis (row of positions) that turns each. Returns the records as a numpy
+    array, or with `device` as the device int64 tensor [n, 2] that the call takes."""
+    f = np.ascontiguousarray(inv_freq, np.float64)
+    a = None if axes is None else _i32(axes)
+    if f.ndim != 1 or (a is not None and a.shape != f.shape):
+        raise ValueError("inv_freq and axes: one value per pair")
+    if n_axes is None:
+        n_axes = 1 if a is None or not len(a) else int(a.max()) + 1
+    out = np.zeros(len(f), ROPE_PAIR_DTYPE)
+    _check(load().pa_rope_pairs(f.ctypes.data_as(C.POINTER(C.c_double)), _p32(a), len(f),
+                                int(n_axes), out.ctypes.data_as(_vp)), "pa_rope_pairs")
+    if device is None:
+        return out
+    import torch
+    return torch.from_numpy(out.view(np.int64).reshape(-1, 2).copy()).to(device)
+
+
+def _token_rows(t, heads: int, D: int, T: int, dev: int, what: str):
+    """(address, elements between tokens) of [T, heads, D] bf16 with dense heads and columns."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{what}: expected torch.bfloat16, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: expected a tensor on the current CUDA device ({dev})")
+    _dims(t, (T, heads, D), what)
+    s = t.stride()
+    if s[2] != 1 or (s[1] != D and heads > 1):
+        raise ValueError(f"{what}: heads and columns have to be dense")
+    return t.data_ptr(), (s[0] if T > 1 else heads * D)
+
+
+def _norm_rope(q, k_new, v_new, q_weight, k_weight, eps, rope, positions, slot_mapping, q_out,
+               k_pool, v_pool, shape, interleaved, err, stream, scales):
+    import torch
+    dev = _here()
+    T = int(slot_mapping.shape[0])
+    Hq, Hkv, D = shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    i32 = torch.int32
+    qp, qs = _token_rows(q, Hq, D, T, dev, "q")
+    kp, ks = _token_rows(k_new, Hkv, D, T, dev, "k_new")
+    vp, vs = _token_rows(v_new, Hkv, D, T, dev, "v_new")
+    w = []
+    for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _dims(t, (D,), what)
+        w.append(None if t is None else _tensor(t, torch.bfloat16, dev, what))
+    n_pairs, n_axes, rp, pp = 0, 1, None, None
+    if rope is not None:
+        if positions is None:
+            raise ValueError("positions: needed with a rotation")
+        n_pairs = int(rope.shape[0])
+        rp = _tensor(rope, torch.int64, dev, "rope")
+        _dims(rope, (n_pairs, 2), "rope")
+        n_axes = 1 if positions.dim() == 1 else int(positions.shape[0])
+        _dims(positions, (T,) if positions.dim() == 1 else (n_axes, T), "positions")
+        pp = _tensor(positions, i32, dev, "positions")
+    _dims(slot_mapping, (T,), "slot_mapping")
+    _dims(q_out, (T, Hq, D), "q_out")
+    pools = _pools(k_pool, v_pool, shape, torch.bfloat16 if scales is None else torch.uint8, dev)
+    args = [qp, qs, kp, ks, vp, vs, w[0], w[1], eps, rp, n_pairs, 1 if interleaved else 0, pp,
+            n_axes, _tensor(slot_mapping, i32, dev, "slot_mapping"), T,
+            _tensor(q_out, torch.bfloat16, dev, "q_out"), *pools]
+    tail = [C.byref(shape), None if err is None else _tensor(err, i32, dev, "err"),
+            _stream(stream)]
+    if scales is None:
+        _check(load().paged_qk_norm_rope_write(*args, *tail), "paged_qk_norm_rope_write")
+    else:
+        _check(load().paged_qk_norm_rope_write_fp8(*args, *scales, *tail),
+               "paged_qk_norm_rope_write_fp8")
+
+
+def paged_qk_norm_rope_write(q, k_new, v_new, q_weight, k_weight, eps: float, rope, positions,
+                             slot_mapping, q_out, k_pool, v_pool, shape: Shape,
+                             interleaved: bool = False, err=None, stream=None) -> None:
+    """Per-head RMS norm of q and k, rotation by position, q to q_out and K / V to their slots.
+    q, k_new, v_new: bf16 [T, heads, D], strided between tokens (parts of one projection).
+    q_weight / k_weight: bf16 [D] or None for no norm. rope: from pa_rope_pairs, or None for no
+    rotation; positions: int32 [T], or [n_axes, T]."""
+    _norm_rope(q, k_new, v_new, q_weight, k_weight, eps, rope, positions, slot_mapping, q_out,
+               k_pool, v_pool, shape, interleaved, err, stream, None)
+
+
+def paged_qk_norm_rope_write_fp8(q, k_new, v_new, q_weight, k_weight, eps: float, rope, positions,
+                                 slot_mapping, q_out, k_pool, v_pool, k_scale: float,
+                                 v_scale: float, shape: Shape, interleaved: bool = False,
+                                 err=None, stream=None) -> None:
+    """paged_qk_norm_rope_write into uint8 float8_e4m3fn pools with per-tensor scales."""
+    _norm_rope(q, k_new, v_new, q_weight, k_weight, eps, rope, positions, slot_mapping, q_out,
+               k_pool, v_pool, shape, interleaved, err, stream, (k_scale, v_scale))
 
 
 class StepLimits:

@@ -472,6 +472,61 @@ int32_t paged_attention_step_fp8(const void* q, const void* k_pool, const void* 
                                  float v_scale, void* workspace, size_t ws_bytes, void* out,
                                  const pa_shape* shape, int32_t* err_flag, pa_stream_t stream);
 
+/* ------------------------------------------------------- norm, rotation and KV write
+ * What stands between a layer's q / k / v projections and the step, in one pass (no counterpart
+ * on the pages, whose sampler takes rotated q and k): the RMS norm of every q and k head, the
+ * rotation of q and k by position, q to its buffer and k, v to their slots of the pools. It takes
+ * the place of paged_kv_write before paged_attention_step. */
+
+/* One pair of rotated columns: it turns by step / 2^64 of a full turn per position of its axis. */
+typedef struct pa_rope_pair {
+    uint64_t step;
+    int32_t axis;       /* row of positions, 0 .. n_axes - 1 */
+    int32_t reserved;   /* 0 */
+} pa_rope_pair;
+
+/* Fills out[n_pairs] (host) from frequencies in radians per position (host doubles; any finite
+ * value: scaled or interpolated frequencies are passed as they come out). axes (host, may be NULL:
+ * all 0) says which row of positions turns each pair, in any arrangement: sections, interleaved.
+ * PA_ERR_BOUNDS for an axis outside [0, n_axes). Upload it once; a model's layers share it. */
+int32_t pa_rope_pairs(const double* inv_freq, const int32_t* axes, int32_t n_pairs,
+                      int32_t n_axes, pa_rope_pair* out);
+
+/* For every token t and q or k head x (D values):
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (weight NULL: y = x)
+ *   (y_i, y_j) = (y_i cos a - y_j sin a, y_i sin a + y_j cos a), a = positions[axis][t] * f_i,
+ * for the n_pairs column pairs (i, i + n_pairs), or (2i, 2i + 1) with interleaved != 0; columns
+ * from 2 n_pairs on pass through. q goes to q_out[t], k to k_pool[slot_mapping[t]], v unchanged to
+ * v_pool[slot_mapping[t]]; a slot < 0 writes no K and V, one outside the pool is skipped and sets
+ * PA_DEVERR_SLOT. fp32 in between, one rounding to bf16 (k over an fp8 pool: to e4m3(y / k_scale),
+ * v as paged_kv_write_fp8). The phase is kept modulo a turn in 64-bit integers: positions of any
+ * size (negative ones too) turn exactly.
+ * Device: q [T, Hq, D], k, v [T, Hkv, D] bf16, each with its own stride in elements between tokens
+ * (heads and columns dense), so the three may be parts of one projection; q_weight, k_weight [D]
+ * bf16 or NULL; rope [n_pairs]; positions [n_axes, T] int32; slot_mapping [T]; q_out [T, Hq, D]
+ * dense (q itself if that is dense, else no overlap with q, k or v). Tokens with the same slot >= 0
+ * leave one of them there. An axis outside [0, n_axes) turns by axis 0 and sets PA_DEVERR_META.
+ * Host checks: n_pairs a multiple of 4, at most D / 2, or 0 for no rotation (PA_ERR_SHAPE; rope and
+ * positions may then be NULL); eps finite and >= 0; pointers 16-byte aligned, strides multiples of
+ * 8 elements and at least a token long. Launched as a programmatic dependent of what precedes it on
+ * the stream, which it waits for. */
+int32_t paged_qk_norm_rope_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, const void* q_weight,
+                                 const void* k_weight, float eps, const pa_rope_pair* rope,
+                                 int32_t n_pairs, int32_t interleaved, const int32_t* positions,
+                                 int32_t n_axes, const int32_t* slot_mapping, int32_t T,
+                                 void* q_out, void* k_pool, void* v_pool, const pa_shape* shape,
+                                 int32_t* err_flag, pa_stream_t stream);
+int32_t paged_qk_norm_rope_write_fp8(const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     const void* q_weight, const void* k_weight, float eps,
+                                     const pa_rope_pair* rope, int32_t n_pairs,
+                                     int32_t interleaved, const int32_t* positions, int32_t n_axes,
+                                     const int32_t* slot_mapping, int32_t T, void* q_out,
+                                     void* k_pool, void* v_pool, float k_scale, float v_scale,
+                                     const pa_shape* shape, int32_t* err_flag,
+                                     pa_stream_t stream);
+
 /* Allocation-free variant of paged_attention_step (no counterpart on the pages: it is a
  * deployment convenience of this library). Same arguments, meaning and result as
  * paged_attention_step, minus the workspace: the split partials go to a fixed device array of
