@@ -141,13 +141,13 @@ def load_peaks() -> dict:
 
 
 def kernel_source_hash() -> str:
-    """Hash of the attention kernel's code (its sources and the ABI header it includes) with
+    """Hash of the attention kernel's code (its sources and the headers they include) with
     comments and blank space removed, so that a comment edit does not void the traffic records
     taken on the same code."""
     h = hashlib.sha256()
     csrc = "continuous_batching_gb300/csrc/"
-    for f in (csrc + "attention.cu", csrc + "tmem_ldst.h", csrc + "common.h",
-              "include/pagedattn.h"):
+    for f in (csrc + "attention.cu", csrc + "sm103.h", csrc + "tensor_map.h",
+              csrc + "tmem_ldst.h", csrc + "common.h", "include/pagedattn.h"):
         src = open(os.path.join(ROOT, f)).read()
         src = re.sub(r"/\*.*?\*/", " ", src, flags=re.S)
         src = re.sub(r"//[^\n]*", " ", src)

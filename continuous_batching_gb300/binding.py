@@ -170,6 +170,10 @@ def load() -> C.CDLL:
         _sig(lib, "paged_qk_norm_rope_write", C.c_int32, norm_rope + [sp, _vp, _vp])
         _sig(lib, "paged_qk_norm_rope_write_fp8", C.c_int32,
              norm_rope + [C.c_float, C.c_float, sp, _vp, _vp])
+        weights = [_vp, _vp, _vp, _vp, C.c_int32, _vp, _vp, C.c_int32, C.c_int32, _vp, _vp, _vp,
+                   C.c_int32, C.c_int32]
+        _sig(lib, "paged_attention_weights", C.c_int32, weights + [sp, _vp, _vp])
+        _sig(lib, "paged_attention_weights_fp8", C.c_int32, weights + [C.c_float, sp, _vp, _vp])
         _lib = lib
         return lib
 
@@ -638,6 +642,77 @@ def paged_qk_norm_rope_write_fp8(q, k_new, v_new, q_weight, k_weight, eps: float
     """paged_qk_norm_rope_write into uint8 float8_e4m3fn pools with per-tensor scales."""
     _norm_rope(q, k_new, v_new, q_weight, k_weight, eps, rope, positions, slot_mapping, q_out,
                k_pool, v_pool, shape, interleaved, err, stream, (k_scale, v_scale))
+
+
+# ---------------------------------------------------------- attention weights per key
+
+def _step_meta(q, block_table, cu_seqlens_q, ctx_lens, shape: Shape, dev: int):
+    """(B, T, max_blocks and the addresses of q, block_table, cu_seqlens_q, ctx_lens)."""
+    import torch
+    i32 = torch.int32
+    B, T = int(ctx_lens.shape[0]), int(q.shape[0])
+    _dims(q, (T, shape.num_q_heads, shape.head_dim), "q")
+    _dims(cu_seqlens_q, (B + 1,), "cu_seqlens_q")
+    _dims(ctx_lens, (B,), "ctx_lens")
+    mb = int(block_table.shape[1])
+    _dims(block_table, (B, mb), "block_table")
+    return (B, T, mb, _tensor(q, torch.bfloat16, dev, "q"),
+            _tensor(block_table, i32, dev, "block_table"),
+            _tensor(cu_seqlens_q, i32, dev, "cu_seqlens_q"),
+            _tensor(ctx_lens, i32, dev, "ctx_lens"))
+
+
+def _per_seq(t, B: int, dev: int, what: str):
+    """Address of an int32 value per sequence, or None."""
+    import torch
+    if t is None:
+        return None
+    _dims(t, (B,), what)
+    return _tensor(t, torch.int32, dev, what)
+
+
+def _state(t, dtype, shape: Shape, dev: int, what: str):
+    """(address, rows, max_len) of a [rows, Hkv, max_len] state tensor."""
+    n, m = int(t.shape[0]), int(t.shape[-1])
+    _dims(t, (n, shape.num_kv_heads, m), what)
+    return _tensor(t, dtype, dev, what), n, m
+
+
+def _weights(q, k_pool, lse, block_table, cu_seqlens_q, ctx_lens, rows, weights, shape, held, err,
+             stream, k_scale):
+    import torch
+    dev = _here()
+    B, T, mb, qp, tp, cup, ctxp = _step_meta(q, block_table, cu_seqlens_q, ctx_lens, shape, dev)
+    kp, = _pools(k_pool, None, shape, torch.bfloat16 if k_scale is None else torch.uint8, dev)
+    _dims(lse, (T, shape.num_q_heads), "lse")
+    wp, n_rows, max_len = _state(weights, torch.float32, shape, dev, "weights")
+    args = [qp, kp, _tensor(lse, torch.float32, dev, "lse"), tp, mb, cup, ctxp, B, T,
+            _per_seq(held, B, dev, "held"), _per_seq(rows, B, dev, "rows"), wp, n_rows, max_len]
+    tail = [C.byref(shape), None if err is None else _tensor(err, torch.int32, dev, "err"),
+            _stream(stream)]
+    if k_scale is None:
+        _check(load().paged_attention_weights(*args, *tail), "paged_attention_weights")
+    else:
+        _check(load().paged_attention_weights_fp8(*args, k_scale, *tail),
+               "paged_attention_weights_fp8")
+
+
+def paged_attention_weights(q, k_pool, lse, block_table, cu_seqlens_q, ctx_lens, rows, weights,
+                            shape: Shape, held=None, err=None, stream=None) -> None:
+    """Adds the attention weight every cached key received from the step's query rows to
+    weights [n_rows, Hkv, max_len] fp32. lse: fp32 [T, Hq] log-sum-exp of the rows. rows: int32 [B],
+    each sequence's state row (None: its index; negative: no part). held: int32 [B], how many
+    entries hold a sum already (None: ctx - n_q); the others up to ctx are set."""
+    _weights(q, k_pool, lse, block_table, cu_seqlens_q, ctx_lens, rows, weights, shape, held, err,
+             stream, None)
+
+
+def paged_attention_weights_fp8(q, k_pool, lse, block_table, cu_seqlens_q, ctx_lens, rows, weights,
+                                k_scale: float, shape: Shape, held=None, err=None,
+                                stream=None) -> None:
+    """paged_attention_weights over a uint8 float8_e4m3fn pool with its per-tensor scale."""
+    _weights(q, k_pool, lse, block_table, cu_seqlens_q, ctx_lens, rows, weights, shape, held, err,
+             stream, float(k_scale))
 
 
 class StepLimits:

@@ -1,0 +1,59 @@
+// Tensor maps (TMA descriptors) of q and of the paged pools, encoded on the host per call.
+#pragma once
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include "common.h"
+
+namespace pa_detail {
+
+// The driver's tensor-map encoder, looked up once per process (a function-local static is
+// initialised exactly once even when several host threads call this at the same time).
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+        return PFN_cuTensorMapEncodeTiled_v12000(nullptr);
+    }();
+    return fn;
+}
+
+// A bf16 3-D tensor {D, heads, rows} with 128-byte swizzled boxes {64, box_heads, box_rows}.
+inline int32_t make_map(CUtensorMap* m, const void* base, int D, int heads, int64_t rows,
+                 int box_heads, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return PA_ERR_CUDA;
+    const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(heads) * D * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+}
+
+// An fp8 pool as {D, heads, rows} bytes: one box is one block of one KV head, bs rows of D
+// code bytes, unswizzled (the loader expands it in shared memory).
+inline int32_t make_map_codes(CUtensorMap* m, const void* base, int D, int heads, int64_t rows,
+                       int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return PA_ERR_CUDA;
+    const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(D), cuuint64_t(heads) * D};
+    const cuuint32_t box[3] = {cuuint32_t(D), 1, cuuint32_t(box_rows)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace pa_detail

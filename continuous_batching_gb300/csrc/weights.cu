@@ -1,0 +1,890 @@
+// The attention weight every cached key received from a step's query rows:
+//
+//   w[row(s)][kvh][j] (+)= sum over rows i of s with pos_i >= j, q heads h of the group, of
+//                          exp(q_ih . k_j / sqrt(D) - lse_ih)
+//
+// lse being the rows' log-sum-exp, which the attention step gives. With it a key's sum needs one
+// look at the key and no second pass over the row.
+//
+// S^T = K Q^T: the MMA's 128 rows (A) are the keys of one tile and its columns (B) the (token,
+// head-in-group) pairs of one KV head, so that a key is a TMEM lane. The thread that reads the
+// lane adds its columns' exponentials in a register: no exchange between lanes, no atomics, one
+// writer per entry, and an order of additions that is fixed. A stale key behind ctx (NaN even)
+// stays in its own lane, which is not written; a stale or foreign query stays in its own column,
+// which is not read.
+//
+// Two forms, chosen per sequence:
+//   FEW   all its columns fit one query tile (n_q * g <= 128; a decode row among them): the query
+//         tile stays, key tiles stream past it. Bound by the read of K (a 32 KB tile per 128 keys
+//         against 16 .. 128 MMA columns); K is read once, no other pass touches it.
+//   MANY  a prefill chunk: one or two key tiles stay, query tiles (128 columns) stream past them
+//         from L2. Bound by the tensor pipe and the exponentials (per element one fused
+//         multiply-add and one addition, packed in pairs, and one ex2).
+// Work is dealt by cost, on the device: every (sequence, KV head, key tile) in order has a cost
+// (4 for a FEW tile, 2 for each query tile a MANY tile meets), CTA c takes the tiles that start in
+// its 1/G of the total. No plan is made or uploaded, so a captured graph needs nothing renewed but
+// its metadata.
+//
+// Warps: 0-7 two epilogue warpgroups, 8 scheduler and loader of what stays, 9 MMA issuer, 10
+// loader of what streams, 11 log-sum-exps; over an fp8 cache 12-15 turn codes and q to f16.
+// Shared memory: two sets of two 32 KB slots for what stays (an item loads while the one before
+// it runs), three 32 KB stages for what streams. TMEM: two accumulators of 128 columns for each
+// warpgroup. Every wait is bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "common.h"
+#include "sm103.h"
+#include "tensor_map.h"
+#include "tmem_ldst.h"
+
+using namespace pa_detail;
+
+namespace {
+
+constexpr int kBaseThreads = 384;
+template <bool F8>
+constexpr int kThreadsFor = F8 ? kBaseThreads + 128 : kBaseThreads;
+constexpr int kCols = 128;                     // columns of a query tile
+constexpr int kSlot = 32768;                   // one tile, 128 rows of D = 128
+constexpr int kHalf = 16384;                   // its 64-column halves
+constexpr int kStay = 0;                       // 2 sets x 2 slots
+constexpr int kStream = 4 * kSlot;             // stages
+constexpr int kStages = 3;
+constexpr int kCtl = kStream + kStages * kSlot;
+constexpr int kBytes = kCtl + 3072;
+static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
+constexpr int kLseSlots = 3;
+constexpr int kMaxRows = 1 << 18;              // state rows whose repeats are looked for
+constexpr int64_t kCostFew = 4, kCostMany = 2; // of a key tile; of a key tile and query tile
+
+enum Bar {
+    kStayFull = 0,     // + set: TMA -> MMA (or the f16 warps)
+    kStayEmpty = 2,    // + set: MMA -> loader
+    kStreamFull = 4,   // + stage
+    kStreamEmpty = 7,  // + stage
+    kAccFull = 10,     // + accumulator: MMA -> its warpgroup
+    kAccEmpty = 14,    // + accumulator: 128 arrivals -> MMA
+    kLseFull = 18,     // + slot: 32 arrivals -> both warpgroups
+    kLseEmpty = 21,    // + slot: 256 arrivals
+    kItemFull = 24,    // + slot (4)
+    kItemEmpty = 28,   // + slot: every consumer thread
+    kStayReady = 32,   // + set, fp8 only: 128 arrivals of the f16 warps
+    kStreamReady = 34, // + stage
+    kDrain = 37,
+    kNumBars = 38
+};
+constexpr int kHolderOff = 8 * kNumBars;
+constexpr int kAbortOff = kHolderOff + 4;
+constexpr int kRingOff = 320;                  // 4 items of 64 bytes
+constexpr int kLseOff = kRingOff + 4 * 64;     // kLseSlots x 128 floats
+constexpr int kScanOff = kLseOff;              // before the pipeline starts
+static_assert(kAbortOff + 4 <= kRingOff && kLseOff + kLseSlots * 512 <= 3072, "control area");
+
+struct Params {
+    const float* lse;            // [T][Hq]
+    const int32_t* block_table;
+    const int32_t* cu;
+    const int32_t* ctx;
+    const int32_t* held;         // entries that hold a sum already; NULL: ctx - n_q
+    const int32_t* rows;         // state rows; NULL: the sequence's index
+    float* weights;              // [n_rows][Hkv][max_len]
+    int32_t* err;
+    int32_t B, T, max_blocks, Hq, Hkv, g, bs, num_blocks, n_rows, max_len;
+    float c;                     // log2(e) / sqrt(D), times the K scale of an fp8 cache
+};
+
+// What the sequences' metadata says, checked. cost 0: nothing to do (no rows, no state row, or
+// metadata that does not fit, which sets bad).
+struct Seq {
+    int n_q, ctx, pos0, cu0, row, held;
+    int n_tiles, n_qt;           // key tiles; query tiles
+    bool few, bad;
+    int64_t head_cost;
+};
+
+// Query tiles that key tile t does not meet: their rows all come before it.
+__device__ __forceinline__ int first_qt(const Seq& q, int t, int log2qt) {
+    return max(0, t * kTileKeys - q.pos0) >> log2qt;
+}
+
+// Cost of a head's key tiles before tile t.
+__device__ __forceinline__ int64_t cost_before(const Seq& q, int t, int log2qt) {
+    if (q.few) return kCostFew * t;
+    // tiles up to u meet every query tile
+    const int u = min(t, (q.pos0 + (1 << log2qt) - 1) / kTileKeys + 1);
+    int64_t f = int64_t(u) * q.n_qt;
+    for (int i = u; i < t; ++i) f += q.n_qt - first_qt(q, i, log2qt);
+    return kCostMany * f;
+}
+
+// The first tile whose start is at or behind x.
+__device__ __forceinline__ int tile_at(const Seq& q, int64_t x, int log2qt) {
+    if (x <= 0) return 0;
+    if (x >= q.head_cost) return q.n_tiles;
+    if (q.few) return int((x + kCostFew - 1) / kCostFew);
+    const int u = min(q.n_tiles, (q.pos0 + (1 << log2qt) - 1) / kTileKeys + 1);
+    const int64_t per = kCostMany * q.n_qt;
+    if (x <= per * u) return int((x + per - 1) / per);
+    int64_t f = per * u;
+    int t = u;
+    for (; t < q.n_tiles && f < x; ++t) f += kCostMany * (q.n_qt - first_qt(q, t, log2qt));
+    return t;
+}
+
+__device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt) {
+    Seq q;
+    const int c0 = p.cu[s], c1 = p.cu[s + 1];
+    q.row = p.rows ? p.rows[s] : s;
+    q.ctx = p.ctx[s];
+    const int64_t n = int64_t(c1) - c0;
+    q.bad = false;
+    q.head_cost = 0;
+    if (n == 0 || q.row < 0) return q;
+    q.n_q = int(n);
+    q.cu0 = c0;
+    q.held = p.held ? p.held[s] : q.ctx - q.n_q;
+    if (n < 0 || c0 < 0 || c1 > p.T || q.n_q > q.ctx || q.ctx > p.max_len ||
+        (int64_t(q.ctx) + p.bs - 1) / p.bs > p.max_blocks || q.row >= p.n_rows || q.held < 0 ||
+        q.held > q.ctx) {
+        q.bad = true;
+        return q;
+    }
+    q.pos0 = q.ctx - q.n_q;
+    q.n_tiles = (q.ctx + kTileKeys - 1) / kTileKeys;
+    q.n_qt = (q.n_q + (1 << log2qt) - 1) >> log2qt;
+    q.few = q.n_qt == 1;
+    q.head_cost = cost_before(q, q.n_tiles, log2qt);
+    return q;
+}
+
+// One unit of work, published by the scheduler: FEW: query tile 0 against key tiles t0 .. t0 + nt
+// - 1; MANY: key tiles t0 (and t0 + 1 with nt 2) against query tiles qt0 .. n_qt - 1.
+struct Item {
+    int seq, kvh, t0, nt, qt0, n_qt, cu0, n_q, pos0, ctx, held, last;
+    int64_t state;               // index of entry 0 in weights
+    int pad[2];
+};
+static_assert(sizeof(Item) == 64, "item slot size");
+
+__device__ __forceinline__ Item read_item(const volatile Item* v) {
+    Item i;
+    i.seq = v->seq;
+    i.kvh = v->kvh;
+    i.t0 = v->t0;
+    i.nt = v->nt;
+    i.qt0 = v->qt0;
+    i.n_qt = v->n_qt;
+    i.cu0 = v->cu0;
+    i.n_q = v->n_q;
+    i.pos0 = v->pos0;
+    i.ctx = v->ctx;
+    i.held = v->held;
+    i.last = v->last;
+    i.state = v->state;
+    return i;
+}
+
+__device__ __forceinline__ float ld_shared_f32x2(uint32_t a, float& y) {
+    float x;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(a) : "memory");
+    return x;
+}
+
+// Adds 2^(s c + nl) of 32 columns (nl: minus the columns' log-sum-exp in base 2, at shared address
+// la) to two packed pairs of sums.
+__device__ __forceinline__ void add32(const uint32_t (&s)[32], uint32_t la, uint64_t c2,
+                                      uint64_t& a0, uint64_t& a1) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const uint4 n = ld_shared_v4(la + 4 * i);
+        float x0, x1, x2, x3;
+        f2_split(fma2(f2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2,
+                      f2(__uint_as_float(n.x), __uint_as_float(n.y))), x0, x1);
+        f2_split(fma2(f2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c2,
+                      f2(__uint_as_float(n.z), __uint_as_float(n.w))), x2, x3);
+        a0 = add2(a0, f2(ex2(x0), ex2(x1)));
+        a1 = add2(a1, f2(ex2(x2), ex2(x3)));
+    }
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreadsFor<F8>, 1)
+    attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_q1,
+                        const __grid_constant__ CUtensorMap tm_qn, const Params p) {
+    static_assert(!F8 || D == 128, "the fp8 cache is supported at head_dim 128");
+    constexpr int kChunks = D / 64;
+    constexpr int kThreads = kThreadsFor<F8>;
+    constexpr int kStayUse = F8 ? kStayReady : kStayFull;
+    constexpr int kStreamUse = F8 ? kStreamReady : kStreamFull;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sb = smem_u32(smem);
+    const uint32_t bars = sb + kCtl;
+    volatile int* abort_word = reinterpret_cast<volatile int*>(smem + kCtl + kAbortOff);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const auto bar = [&](int b) { return bars + 8 * b; };
+    const int log2qt = 7 - (__ffs(p.g) - 1);         // tokens of a query tile: 128 / g
+    const int log2bs = __ffs(p.bs) - 1;
+    if (sb & 1023) {                                 // the swizzled tiles need this alignment
+        if (threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+        return;
+    }
+
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < kNumBars; ++b)
+            mbar_init(bar(b), (b >= kAccEmpty && b < kLseFull)        ? 128
+                              : (b >= kLseFull && b < kLseEmpty)      ? 32
+                              : (b >= kLseEmpty && b < kItemFull)     ? 256
+                              // MMA 1, stream loader 32, log-sum-exps 32, epilogue 256, f16 128
+                              : (b >= kItemEmpty && b < kStayReady)   ? 1 + 64 + 256 + (F8 ? 128 : 0)
+                              : (b >= kStayReady && b < kDrain)       ? 128
+                                                                      : 1);
+        *abort_word = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         bars + kHolderOff),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // a programmatic dependent: nothing the kernel before it wrote is read before this point
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- this CTA's share: repeated state rows, the total cost, where the share starts
+    uint32_t* once = reinterpret_cast<uint32_t*>(smem + kStay);
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + kCtl + kScanOff);   // [16] warps
+    int64_t* found = scan + 16;                      // start offset of the first sequence
+    int* found_s = reinterpret_cast<int*>(scan + 17);
+    int* repeated = found_s + 1;
+    if (threadIdx.x == 0) {
+        *found_s = p.B;
+        *found = 0;
+        *repeated = 0;
+    }
+    if (p.rows)
+        for (int i = threadIdx.x; i < (p.n_rows + 31) / 32; i += kThreads) once[i] = 0;
+    __syncthreads();
+    if (p.rows) {
+        for (int s = threadIdx.x; s < p.B; s += kThreads) {
+            const int row = p.rows[s];
+            if (row < 0 || row >= p.n_rows || p.cu[s + 1] == p.cu[s]) continue;
+            const uint32_t bit = 1u << (row & 31);
+            if (atomicOr(once + (row >> 5), bit) & bit) *repeated = 1;
+        }
+        __syncthreads();
+    }
+    // two sequences over one state row would race on it: the call then does nothing
+    const bool refused = *repeated != 0;
+    int64_t total = 0;
+    bool bad = refused;
+    // inclusive sums over the sequences of one round of kThreads; returns the thread's own
+    const auto round_scan = [&](int64_t x, int64_t& sum) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        sum = 0;
+        int64_t before = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w == warp) before = sum;
+            sum += scan[w];
+        }
+        return x + before;
+    };
+    int64_t mine = 0, upto = 0;
+    for (int s0 = 0; s0 < p.B && !refused; s0 += kThreads) {
+        const int s = s0 + int(threadIdx.x);
+        mine = 0;
+        if (s < p.B) {
+            const Seq q = load_seq(p, s, log2qt);
+            mine = q.head_cost * p.Hkv;
+            bad = bad || q.bad;
+        }
+        int64_t sum;
+        upto = round_scan(mine, sum) + total;
+        total += sum;
+    }
+    if (bad && blockIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+    const int64_t lo = total * int64_t(blockIdx.x) / int64_t(gridDim.x);
+    const int64_t hi = total * (int64_t(blockIdx.x) + 1) / int64_t(gridDim.x);
+    if (p.B <= kThreads) {
+        if (mine > 0 && upto - mine <= lo && lo < upto) {
+            *found_s = int(threadIdx.x);
+            *found = upto - mine;
+        }
+    } else if (lo < hi) {
+        int64_t run = 0;
+        for (int s0 = 0; s0 < p.B && run <= lo; s0 += kThreads) {
+            const int s = s0 + int(threadIdx.x);
+            mine = s < p.B ? load_seq(p, s, log2qt).head_cost * p.Hkv : 0;
+            int64_t sum;
+            upto = round_scan(mine, sum) + run;
+            if (mine > 0 && upto - mine <= lo && lo < upto) {
+                *found_s = s;
+                *found = upto - mine;
+            }
+            run += sum;
+        }
+    }
+    // the rows' bits were written through the generic proxy where TMA writes next
+    fence_proxy_async();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kCtl + kHolderOff);
+    const int start_s = *reinterpret_cast<volatile int*>(found_s);
+    const int64_t start_at = *reinterpret_cast<volatile int64_t*>(found);
+    __syncthreads();                                 // the scan's words belong to the ring now
+
+    volatile Item* ring = reinterpret_cast<volatile Item*>(smem + kCtl + kRingOff);
+    // takes the next item: every consumer thread (or the one lane that stands for a warp) calls it
+    const auto next_item = [&](int ic, Item& I) {
+        if (!wait_bounded(bar(kItemFull + (ic & 3)), (ic >> 2) & 1, abort_word)) return false;
+        I = read_item(ring + (ic & 3));
+        mbar_arrive(bar(kItemEmpty + (ic & 3)));
+        return I.last == 0;
+    };
+    // the K tile of key tile t into `slot` (all lanes; lane 0 has waited for the slot): one box per
+    // block and 64-column half, or over an fp8 cache one box of codes per block into the second
+    // half, where they are expanded. `id`: the lane's table entry.
+    const auto load_k = [&](uint32_t slot, uint32_t full, const Item& I, int t, int id) {
+        const int nblk = (min(kTileKeys, I.ctx - t * kTileKeys) + p.bs - 1) >> log2bs;
+        if (lane == 0) mbar_expect_tx(full, uint32_t(nblk) * p.bs * (F8 ? 128 : 128 * kChunks));
+        __syncwarp();
+        if (lane < nblk) {
+            if constexpr (F8) {
+                tma_load_3d(slot + kHalf + lane * p.bs * 128, &tm_k, full, 0, I.kvh, id * p.bs);
+            } else {
+#pragma unroll
+                for (int h = 0; h < kChunks; ++h)
+                    tma_load_3d(slot + h * kHalf + lane * p.bs * 128, &tm_k, full, 64 * h, I.kvh,
+                                id * p.bs);
+            }
+        }
+    };
+    // the lane's block id of key tile t; one outside the pool reads zeros
+    const auto block_id = [&](const Item& I, int t) {
+        const int e = (t << (7 - log2bs)) + lane;
+        if (lane >= (kTileKeys >> log2bs) || e << log2bs >= I.ctx) return -1;
+        const int b = __ldg(p.block_table + int64_t(I.seq) * p.max_blocks + e);
+        if (b >= 0 && b < p.num_blocks) return b;
+        if (p.err) atomicOr(p.err, PA_DEVERR_BLOCK);
+        return -1;
+    };
+    // query tile qt: 128 rows (token, head-in-group), or one token's g rows
+    const auto load_q = [&](uint32_t slot, uint32_t full, const Item& I, int qt) {
+        const bool one = I.n_q == 1;
+        mbar_expect_tx(full, uint32_t(one ? p.g : kCols) * 128 * kChunks);
+        for (int h = 0; h < kChunks; ++h)
+            tma_load_3d(slot + h * kHalf, one ? &tm_q1 : &tm_qn, full, 64 * h, I.kvh * p.g,
+                        I.cu0 + (qt << log2qt));
+    };
+
+    if (warp == 8) {
+        // ------------------------------------------------ scheduler, loader of what stays
+        int ic = 0, ok = 1;
+        // publishes an item and loads its query tile or key tiles
+        const auto emit = [&](Item& I, bool few) {
+            if (lane == 0) {
+                if (ic >= 4)
+                    ok = wait_bounded(bar(kItemEmpty + (ic & 3)), ((ic >> 2) - 1) & 1, abort_word);
+                if (ok) {
+                    volatile Item* v = ring + (ic & 3);
+                    v->seq = I.seq;
+                    v->kvh = I.kvh;
+                    v->t0 = I.t0;
+                    v->nt = I.nt;
+                    v->qt0 = I.qt0;
+                    v->n_qt = I.n_qt;
+                    v->cu0 = I.cu0;
+                    v->n_q = I.n_q;
+                    v->pos0 = I.pos0;
+                    v->ctx = I.ctx;
+                    v->held = I.held;
+                    v->last = I.last;
+                    v->state = I.state;
+                    mbar_arrive(bar(kItemFull + (ic & 3)));
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok || I.last) return;
+            const int set = ic & 1;
+            int id[2] = {-1, -1};
+            if (!few)
+                for (int r = 0; r < I.nt; ++r) id[r] = block_id(I, I.t0 + r);
+            if (lane == 0 && ic >= 2)
+                ok = wait_bounded(bar(kStayEmpty + set), ((ic >> 1) - 1) & 1, abort_word);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) return;
+            const uint32_t slot = sb + kStay + set * 2 * kSlot;
+            if (few) {
+                if (lane == 0) load_q(slot, bar(kStayFull + set), I, 0);
+            } else {
+                // one barrier for both tiles: its one arrival carries the bytes of both
+                const int n0 = (min(kTileKeys, I.ctx - I.t0 * kTileKeys) + p.bs - 1) >> log2bs;
+                const int n1 = I.nt == 2
+                    ? (min(kTileKeys, I.ctx - (I.t0 + 1) * kTileKeys) + p.bs - 1) >> log2bs : 0;
+                if (lane == 0)
+                    mbar_expect_tx(bar(kStayFull + set),
+                                   uint32_t(n0 + n1) * p.bs * (F8 ? 128 : 128 * kChunks));
+                __syncwarp();
+                for (int r = 0; r < I.nt; ++r) {
+                    if (lane >= (r ? n1 : n0)) continue;
+                    const uint32_t dst = slot + r * kSlot + lane * p.bs * 128;
+                    if constexpr (F8) {
+                        tma_load_3d(dst + kHalf, &tm_k, bar(kStayFull + set), 0, I.kvh,
+                                    id[r] * p.bs);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < kChunks; ++h)
+                            tma_load_3d(dst + h * kHalf, &tm_k, bar(kStayFull + set), 64 * h,
+                                        I.kvh, id[r] * p.bs);
+                    }
+                }
+            }
+            ++ic;
+        };
+        int64_t base = start_at;
+        for (int s = start_s; s < p.B && base < hi && ok; ++s) {
+            const Seq q = load_seq(p, s, log2qt);
+            if (q.head_cost == 0) continue;
+            Item I;
+            I.seq = s;
+            I.cu0 = q.cu0;
+            I.n_q = q.n_q;
+            I.pos0 = q.pos0;
+            I.ctx = q.ctx;
+            I.held = q.held;
+            I.last = 0;
+            I.n_qt = q.n_qt;
+            for (int h = base < lo ? int((lo - base) / q.head_cost) : 0; h < p.Hkv && ok; ++h) {
+                const int64_t hb = base + h * q.head_cost;
+                if (hb >= hi) break;
+                const int ta = tile_at(q, lo - hb, log2qt), tb = tile_at(q, hi - hb, log2qt);
+                I.kvh = h;
+                I.state = (int64_t(q.row) * p.Hkv + h) * p.max_len;
+                if (q.few) {
+                    if (ta >= tb) continue;
+                    I.t0 = ta;
+                    I.nt = tb - ta;
+                    I.qt0 = 0;
+                    emit(I, true);
+                } else {
+                    for (int t = ta; t < tb && ok; t += 2) {
+                        I.t0 = t;
+                        I.nt = min(2, tb - t);
+                        I.qt0 = first_qt(q, t, log2qt);
+                        emit(I, false);
+                    }
+                }
+            }
+            base += q.head_cost * p.Hkv;
+        }
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (ok) {
+            Item I = {};
+            I.last = 1;
+            emit(I, true);
+        }
+        if (lane == 0) {
+            // never leave with copies in flight into this CTA's shared memory
+            for (int i = max(0, ic - 2); i < ic; ++i)
+                wait_drain(bar(kStayFull + (i & 1)), (i >> 1) & 1);
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int st = 0, ph = 0;              // stream stage and its phase
+            int m[2] = {0, 0};               // products of each warpgroup
+            int turn = 0;                    // the warpgroup of the next FEW tile
+            bool ok = true;
+            // accumulator of the next product of warpgroup w: columns 128 (2 w + (m & 1))
+            const auto product = [&](int w, uint32_t a, uint32_t b, int cols) {
+                const int acc = 2 * w + (m[w] & 1);
+                if (m[w] >= 2 &&
+                    !(ok = wait_bounded(bar(kAccEmpty + acc), ((m[w] >> 1) - 1) & 1, abort_word)))
+                    return;
+                tc_fence_after();
+                issue_s_group<D>(1u, tmem + acc * 128, make_sdesc(a, 16, 1024),
+                                 make_sdesc(b, 16, 1024),
+                                 make_idesc(128, (cols + 15) & ~15, false, F8));
+                tc_commit_if(1u, bar(kAccFull + acc));
+                ++m[w];
+            };
+            for (int ic = 0;; ++ic) {
+                Item I;
+                if (!next_item(ic, I)) break;
+                const int set = ic & 1;
+                const bool few = I.n_qt == 1;
+                const uint32_t stay = sb + kStay + set * 2 * kSlot;
+                if (!(ok = wait_bounded(bar(kStayUse + set), (ic >> 1) & 1, abort_word))) break;
+                const int n = few ? I.nt : I.n_qt - I.qt0;
+                for (int i = 0; i < n && ok; ++i) {
+                    if (!(ok = wait_bounded(bar(kStreamUse + st), ph, abort_word))) break;
+                    const uint32_t stage = sb + kStream + st * kSlot;
+                    if (few) {
+                        product(turn, stage, stay, I.n_q * p.g);
+                        turn ^= 1;
+                    } else {
+                        const int cols = min(kCols, (I.n_q - ((I.qt0 + i) << log2qt)) * p.g);
+                        for (int r = 0; r < I.nt && ok; ++r)
+                            product(r, stay + r * kSlot, stage, cols);
+                    }
+                    tc_commit_if(1u, bar(kStreamEmpty + st));
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+                if (!ok) break;
+                tc_commit_if(1u, bar(kStayEmpty + set));
+            }
+            // every MMA has finished before TMEM is released
+            tc_commit_if(1u, bar(kDrain));
+            wait_drain(bar(kDrain), 0);
+        }
+    } else if (warp == 10) {
+        // ------------------------------------------------ loader of what streams
+        int n_done = 0, ok = 1;
+        for (int ic = 0; ok; ++ic) {
+            Item I;
+            ok = next_item(ic, I);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const bool few = I.n_qt == 1;
+            const int n = few ? I.nt : I.n_qt - I.qt0;
+            int id = few ? block_id(I, I.t0) : -1;
+            for (int i = 0; i < n; ++i) {
+                const int st = n_done % kStages;
+                const int id_next = few && i + 1 < n ? block_id(I, I.t0 + i + 1) : -1;
+                if (lane == 0 && n_done >= kStages)
+                    ok = wait_bounded(bar(kStreamEmpty + st), (n_done / kStages - 1) & 1,
+                                      abort_word);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                const uint32_t slot = sb + kStream + st * kSlot;
+                if (few) load_k(slot, bar(kStreamFull + st), I, I.t0 + i, id);
+                else if (lane == 0) load_q(slot, bar(kStreamFull + st), I, I.qt0 + i);
+                id = id_next;
+                ++n_done;
+            }
+        }
+        if (lane == 0) {
+            for (int i = max(0, n_done - kStages); i < n_done; ++i)
+                wait_drain(bar(kStreamFull + i % kStages), (i / kStages) & 1);
+        }
+    } else if (warp == 11) {
+        // ------------------------------------------------ log-sum-exps, negated, in base 2
+        int n_done = 0, ok = 1;
+        for (int ic = 0; ok; ++ic) {
+            Item I;
+            ok = next_item(ic, I);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const auto fetch = [&](int qt) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int col = 4 * lane + e;
+                    const int tok = (qt << log2qt) + (col >> (7 - log2qt));
+                    v[e] = 0.f;
+                    if (tok < I.n_q)
+                        v[e] = -1.4426950408889634f *
+                               __ldg(p.lse + int64_t(I.cu0 + tok) * p.Hq + I.kvh * p.g +
+                                     (col & (p.g - 1)));
+                }
+                return make_float4(v[0], v[1], v[2], v[3]);
+            };
+            float4 next = fetch(I.qt0);
+            for (int qt = I.qt0; qt < I.n_qt; ++qt, ++n_done) {
+                const float4 v = next;
+                if (qt + 1 < I.n_qt) next = fetch(qt + 1);
+                const int slot = n_done % kLseSlots;
+                if (lane == 0 && n_done >= kLseSlots)
+                    ok = wait_bounded(bar(kLseEmpty + slot), (n_done / kLseSlots - 1) & 1,
+                                      abort_word);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                *reinterpret_cast<float4*>(smem + kCtl + kLseOff + slot * 512 + lane * 16) = v;
+                mbar_arrive(bar(kLseFull + slot));
+            }
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------ codes and q to f16 (fp8 cache)
+        if constexpr (F8) {
+            const int w = warp - 12;
+            // the MMAs take f16 operands: 32 rows a warp of a K tile's codes are expanded, or of a
+            // query tile rounded in place (a 16-byte chunk keeps its place, so the swizzle holds)
+            const auto turn_k = [&](uint32_t slot, const Item& I, int t) {
+                const int rows =
+                    ((min(kTileKeys, I.ctx - t * kTileKeys) + p.bs - 1) >> log2bs) << log2bs;
+                expand_codes<false>(slot, 32 * w, min(rows, 32 * w + 32), p.bs, log2bs, lane);
+            };
+            const auto turn_q = [&](uint32_t slot, int rows) {
+                for (int i = threadIdx.x - kBaseThreads; i < rows * 16; i += 128) {
+                    const uint32_t a = slot + ((i >> 3) & 1) * kHalf + (i >> 4) * 128 + (i & 7) * 16;
+                    const uint4 v = ld_shared_v4(a);
+                    st_shared_v4(a, bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y),
+                                 bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+                }
+            };
+            int n_done = 0;
+            bool ok = true;
+            for (int ic = 0; ok; ++ic) {
+                Item I;
+                if (!next_item(ic, I)) break;
+                const bool few = I.n_qt == 1;
+                const int set = ic & 1;
+                const uint32_t stay = sb + kStay + set * 2 * kSlot;
+                if (!(ok = wait_bounded(bar(kStayFull + set), (ic >> 1) & 1, abort_word))) break;
+                if (few) turn_q(stay, I.n_q == 1 ? p.g : kCols);
+                else
+                    for (int r = 0; r < I.nt; ++r) turn_k(stay + r * kSlot, I, I.t0 + r);
+                fence_proxy_async();
+                mbar_arrive(bar(kStayReady + set));
+                const int n = few ? I.nt : I.n_qt - I.qt0;
+                for (int i = 0; i < n; ++i, ++n_done) {
+                    const int st = n_done % kStages;
+                    if (!(ok = wait_bounded(bar(kStreamFull + st), (n_done / kStages) & 1,
+                                            abort_word)))
+                        break;
+                    const uint32_t slot = sb + kStream + st * kSlot;
+                    if (few) turn_k(slot, I, I.t0 + i);
+                    else turn_q(slot, kCols);
+                    fence_proxy_async();
+                    mbar_arrive(bar(kStreamReady + st));
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue warpgroups
+        const int w = warp >> 2;
+        const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+        const int key_in_tile = 32 * (warp & 3) + lane;
+        const uint64_t c2 = f2(p.c, p.c);
+        int m = 0, turn = 0, n_lse = 0;
+        bool ok = true;
+        // the sum over the columns of this warpgroup's next product: query rows from position
+        // `at` on, `cols` columns, key j
+        const auto column_sum = [&](uint32_t la, int cols, int at, int j, int tile_end, float& sum) {
+            const int acc = 2 * w + (m & 1);
+            if (!(ok = wait_bounded(bar(kAccFull + acc), (m >> 1) & 1, abort_word))) return;
+            tc_fence_after();
+            ++m;
+            const uint32_t tm = tmem + acc * 128 + lanes;
+            uint64_t a0 = f2(0.f, 0.f), a1 = a0;
+            if (cols == kCols && tile_end <= at + 1) {
+                uint32_t s0[32], s1[32];
+                tmem_ld_32x32b_x32(tm, s0);
+                tmem_wait_ld();
+                tmem_ld_32x32b_x32(tm + 32, s1);
+                add32(s0, la, c2, a0, a1);
+                tmem_wait_ld();
+                tmem_ld_32x32b_x32(tm + 64, s0);
+                add32(s1, la + 128, c2, a0, a1);
+                tmem_wait_ld();
+                tmem_ld_32x32b_x32(tm + 96, s1);
+                add32(s0, la + 256, c2, a0, a1);
+                tmem_wait_ld();
+                tc_fence_before();
+                mbar_arrive(bar(kAccEmpty + acc));
+                add32(s1, la + 384, c2, a0, a1);
+            } else {
+                // the first column whose row comes at or after the key
+                const int from = max(0, j - at) << (7 - log2qt);
+                for (int c0 = 0; c0 < cols; c0 += 16) {
+                    uint32_t s[16];
+                    tmem_ld_32x32b_x16(tm + c0, s);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        float n1;
+                        const float n0 = ld_shared_f32x2(la + 4 * (c0 + i), n1);
+                        const int col = c0 + i;
+                        const float e0 = ex2(fmaf(__uint_as_float(s[i]), p.c, n0));
+                        const float e1 = ex2(fmaf(__uint_as_float(s[i + 1]), p.c, n1));
+                        a0 = add2(a0, f2(col >= from && col < cols ? e0 : 0.f,
+                                         col + 1 >= from && col + 1 < cols ? e1 : 0.f));
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(bar(kAccEmpty + acc));
+            }
+            float x0, x1;
+            f2_split(add2(a0, a1), x0, x1);
+            sum += x0 + x1;
+        };
+        for (int ic = 0; ok; ++ic) {
+            Item I;
+            if (!next_item(ic, I)) break;
+            const auto wait_lse = [&]() {
+                return ok = wait_bounded(bar(kLseFull + n_lse % kLseSlots), (n_lse / kLseSlots) & 1,
+                                         abort_word);
+            };
+            const auto done_lse = [&]() { mbar_arrive(bar(kLseEmpty + n_lse++ % kLseSlots)); };
+            if (I.n_qt == 1) {
+                if (!wait_lse()) break;
+                const uint32_t la = sb + kCtl + kLseOff + (n_lse % kLseSlots) * 512;
+                for (int i = 0; i < I.nt; ++i) {
+                    const bool my = turn == w;
+                    turn ^= 1;
+                    if (!my) continue;
+                    const int kb = (I.t0 + i) * kTileKeys, j = kb + key_in_tile;
+                    float* dst = p.weights + I.state + j;
+                    const float old = j < I.held ? *dst : 0.f;
+                    float sum = 0.f;
+                    column_sum(la, I.n_q * p.g, I.pos0, j, kb + kTileKeys, sum);
+                    if (!ok) break;
+                    if (j < I.ctx) *dst = old + sum;
+                }
+                if (!ok) break;
+                done_lse();
+            } else {
+                const bool my = w < I.nt;
+                const int kb = (I.t0 + w) * kTileKeys, j = kb + key_in_tile;
+                float* dst = p.weights + I.state + j;
+                const float old = my && j < I.held ? *dst : 0.f;
+                float sum = 0.f;
+                for (int qt = I.qt0; qt < I.n_qt; ++qt) {
+                    if (!wait_lse()) break;
+                    if (my)
+                        column_sum(sb + kCtl + kLseOff + (n_lse % kLseSlots) * 512,
+                                   min(kCols, (I.n_q - (qt << log2qt)) * p.g),
+                                   I.pos0 + (qt << log2qt), j, kb + kTileKeys, sum);
+                    if (!ok) break;
+                    done_lse();
+                }
+                if (!ok) break;
+                if (my && j < I.ctx) *dst = old + sum;
+            }
+        }
+    }
+    if (*abort_word && threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                     : "memory");
+    }
+}
+
+constexpr int kMaxDevices = 64;
+
+template <int D, bool F8>
+int32_t launch_weights(const CUtensorMap& k, const CUtensorMap& q1, const CUtensorMap& qn,
+                       const Params& p, cudaStream_t stream) {
+    int dev = 0;
+    int32_t st = note_cuda(cudaGetDevice(&dev));
+    if (st) return st;
+    // the shared-memory limit is raised once per device (idempotent: threads may race to it)
+    static std::atomic<bool> raised[kMaxDevices];
+    if (dev < 0 || dev >= kMaxDevices) return PA_ERR_INVALID;
+    if (!raised[dev].load(std::memory_order_acquire)) {
+        if ((st = note_cuda(cudaFuncSetAttribute(attn_weights_kernel<D, F8>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kBytes))))
+            return st;
+        raised[dev].store(true, std::memory_order_release);
+    }
+    const int64_t tiles =
+        int64_t(p.B) * p.Hkv * ((int64_t(p.max_len) + kTileKeys - 1) / kTileKeys);
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(tiles, PA_PLAN_CTAS)));
+    cfg.blockDim = dim3(kThreadsFor<F8>);
+    cfg.dynamicSmemBytes = kBytes;
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return note_cuda(cudaLaunchKernelEx(&cfg, attn_weights_kernel<D, F8>, k, q1, qn, p));
+}
+
+int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
+                          const int32_t* block_table, int32_t max_blocks, const int32_t* cu,
+                          const int32_t* ctx, int32_t B, int32_t T, const int32_t* held,
+                          const int32_t* rows, float* weights, int32_t n_rows, int32_t max_len,
+                          bool fp8, float k_scale, const pa_shape* s, int32_t* err,
+                          cudaStream_t stream) {
+    int32_t st = check_shape(s);
+    if (st) return st;
+    if (fp8 && s->head_dim != 128) return PA_ERR_SHAPE;
+    if (B < 0 || T < 0 || max_blocks < 0 || n_rows < 0 || max_len < 0) return PA_ERR_INVALID;
+    if (T == 0 || B == 0) return PA_OK;
+    if (!q || !k_pool || !lse || !block_table || !cu || !ctx || !weights) return PA_ERR_INVALID;
+    if (max_len == 0 || (!rows && n_rows < B)) return PA_ERR_INVALID;
+    if (n_rows > kMaxRows || int64_t(s->num_blocks) * s->block_size > INT32_MAX ||
+        max_len > INT32_MAX - kTileKeys)
+        return PA_ERR_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pool)) & 15)
+        return PA_ERR_INVALID;
+    const int D = s->head_dim, g = s->num_q_heads / s->num_kv_heads;
+    const int64_t slots = int64_t(s->num_blocks) * s->block_size;
+    CUtensorMap k, q1, qn;
+    st = fp8 ? make_map_codes(&k, k_pool, D, s->num_kv_heads, slots, s->block_size)
+             : make_map(&k, k_pool, D, s->num_kv_heads, slots, 1, s->block_size);
+    if (st) return st;
+    if ((st = make_map(&q1, q, D, s->num_q_heads, T, g, 1))) return st;
+    if ((st = make_map(&qn, q, D, s->num_q_heads, T, g, kCols / g))) return st;
+    Params p;
+    p.lse = lse;
+    p.block_table = block_table;
+    p.cu = cu;
+    p.ctx = ctx;
+    p.held = held;
+    p.rows = rows;
+    p.weights = weights;
+    p.err = err;
+    p.B = B;
+    p.T = T;
+    p.max_blocks = max_blocks;
+    p.Hq = s->num_q_heads;
+    p.Hkv = s->num_kv_heads;
+    p.g = g;
+    p.bs = s->block_size;
+    p.num_blocks = s->num_blocks;
+    p.n_rows = n_rows;
+    p.max_len = max_len;
+    p.c = float(1.4426950408889634 / std::sqrt(double(D))) * k_scale;
+    if (fp8) return launch_weights<128, true>(k, q1, qn, p, stream);
+    if (D == 128) return launch_weights<128, false>(k, q1, qn, p, stream);
+    return launch_weights<64, false>(k, q1, qn, p, stream);
+}
+
+}  // namespace
+
+extern "C" int32_t paged_attention_weights(
+    const void* q, const void* k_pool, const float* lse, const int32_t* block_table,
+    int32_t max_blocks, const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t B,
+    int32_t T, const int32_t* held, const int32_t* rows, float* weights, int32_t n_rows,
+    int32_t max_len, const pa_shape* shape, int32_t* err_flag, pa_stream_t stream) {
+    return attention_weights(q, k_pool, lse, block_table, max_blocks, cu_seqlens_q, ctx_lens, B, T,
+                             held, rows, weights, n_rows, max_len, false, 1.f, shape, err_flag,
+                             stream);
+}
+
+extern "C" int32_t paged_attention_weights_fp8(
+    const void* q, const void* k_pool, const float* lse, const int32_t* block_table,
+    int32_t max_blocks, const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t B,
+    int32_t T, const int32_t* held, const int32_t* rows, float* weights, int32_t n_rows,
+    int32_t max_len, float k_scale, const pa_shape* shape, int32_t* err_flag,
+    pa_stream_t stream) {
+    if (!(k_scale > 0.f) || !(k_scale < INFINITY)) return PA_ERR_INVALID;
+    return attention_weights(q, k_pool, lse, block_table, max_blocks, cu_seqlens_q, ctx_lens, B, T,
+                             held, rows, weights, n_rows, max_len, true, k_scale, shape, err_flag,
+                             stream);
+}

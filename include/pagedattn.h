@@ -527,6 +527,46 @@ int32_t paged_qk_norm_rope_write_fp8(const void* q, int64_t q_stride, const void
                                      const pa_shape* shape, int32_t* err_flag,
                                      pa_stream_t stream);
 
+/* ---------------------------------------------------------- attention weights per key
+ * The weight every cached key received from a step's query rows, added to a running sum: what a
+ * bounded cache keeps its entries by (paged_evict). No counterpart on the pages.
+ *
+ *   weights[row][kvh][j] (+)= sum over the sequence's rows i with pos_i >= j and the q heads h of
+ *                             kvh's group of exp(q[i,h] . k[j,kvh] / sqrt(D) - lse[i,h])
+ *
+ * lse: the rows' log-sum-exp over their keys (natural logarithm), as paged_attention_step_lse
+ * gives it, or any other reference per (row, q head). Positions, causality and the GQA map as in
+ * paged_attention_step. cu_seqlens_q need not be the step's: with the last w rows of a sequence
+ * alone (their q and lse, ctx unchanged) those w rows alone give weight.
+ * State: weights [n_rows, Hkv, max_len] fp32, one row for life per sequence, whatever the order of
+ * the steps; rows[s] is sequence s's (NULL: s), a negative one takes no part. The first held[s]
+ * entries (NULL: ctx - n_q, the entries that steps before this one have seen) are added to; those
+ * from held[s] to ctx are set, whatever they held; the others are left as they were.
+ * Sums are fp32, one writer per entry and a fixed order: equal calls give equal bits.
+ * Device inputs: q [T, Hq, D] bf16; k_pool as in paged_attention_step; lse [T, Hq] fp32;
+ * block_table [B, max_blocks], cu_seqlens_q [B+1], ctx_lens [B], held [B] or NULL, rows [B] or
+ * NULL int32. A sequence whose metadata does not fit (n_q > ctx, ctx > max_len or the table, held
+ * outside [0, ctx], a row >= n_rows) is skipped and sets PA_DEVERR_META; if two sequences with
+ * query rows name one state row, the whole call does nothing and sets it. Weights whose lse or q
+ * is NaN are NaN.
+ * Host checks: as paged_attention_step; n_rows <= 2^18; n_rows >= B without rows. One launch, a
+ * programmatic dependent of what precedes it, no workspace, nothing planned on the host: a captured
+ * call follows its metadata. */
+int32_t paged_attention_weights(const void* q, const void* k_pool, const float* lse,
+                                const int32_t* block_table, int32_t max_blocks,
+                                const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t B,
+                                int32_t T, const int32_t* held, const int32_t* rows,
+                                float* weights, int32_t n_rows, int32_t max_len,
+                                const pa_shape* shape, int32_t* err_flag, pa_stream_t stream);
+/* Over an fp8 pool (head_dim 128): q is rounded to f16 as in paged_attention_step_fp8. */
+int32_t paged_attention_weights_fp8(const void* q, const void* k_pool, const float* lse,
+                                    const int32_t* block_table, int32_t max_blocks,
+                                    const int32_t* cu_seqlens_q, const int32_t* ctx_lens,
+                                    int32_t B, int32_t T, const int32_t* held,
+                                    const int32_t* rows, float* weights, int32_t n_rows,
+                                    int32_t max_len, float k_scale, const pa_shape* shape,
+                                    int32_t* err_flag, pa_stream_t stream);
+
 /* Allocation-free variant of paged_attention_step (no counterpart on the pages: it is a
  * deployment convenience of this library). Same arguments, meaning and result as
  * paged_attention_step, minus the workspace: the split partials go to a fixed device array of
