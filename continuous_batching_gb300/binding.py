@@ -174,6 +174,9 @@ def load() -> C.CDLL:
                    C.c_int32, C.c_int32]
         _sig(lib, "paged_attention_weights", C.c_int32, weights + [sp, _vp, _vp])
         _sig(lib, "paged_attention_weights_fp8", C.c_int32, weights + [C.c_float, sp, _vp, _vp])
+        _sig(lib, "paged_evict", C.c_int32,
+             [_vp, _vp, C.c_int32, _vp, C.c_int32, _vp, _vp, _vp, _vp, _vp, C.c_int32, C.c_int32,
+              C.c_int32, _vp, _vp, _vp, _vp, C.c_int32, C.c_int32, sp, _vp, _vp])
         _lib = lib
         return lib
 
@@ -713,6 +716,39 @@ def paged_attention_weights_fp8(q, k_pool, lse, block_table, cu_seqlens_q, ctx_l
     """paged_attention_weights over a uint8 float8_e4m3fn pool with its per-tensor scale."""
     _weights(q, k_pool, lse, block_table, cu_seqlens_q, ctx_lens, rows, weights, shape, held, err,
              stream, float(k_scale))
+
+
+# ------------------------------------------------------------------------- eviction
+
+def paged_evict(k_pool, v_pool, block_table, ctx_lens, budget, n_tokens, kept, rows, recent: int,
+                sink: int, weights, weights_out, positions, positions_out, shape: Shape, err=None,
+                stream=None) -> None:
+    """Cuts every sequence's cache (bf16, or uint8 float8_e4m3fn codes) to `budget` entries per KV
+    head by accumulated attention weight. ctx_lens, budget, n_tokens (tokens so far), kept (length
+    after the last eviction, None: 0), rows (state rows, None: the index): int32 [B]. weights fp32 and
+    positions int32 [n_rows, Hkv, max_len] go to weights_out and positions_out (the same tensors, or
+    others)."""
+    import torch
+    dev = _here()
+    i32, f32 = torch.int32, torch.float32
+    B, mb = int(ctx_lens.shape[0]), int(block_table.shape[1])
+    _dims(block_table, (B, mb), "block_table")
+    if k_pool.dtype not in (torch.bfloat16, torch.uint8):
+        raise ValueError(f"k_pool: expected torch.bfloat16 or torch.uint8, got {k_pool.dtype}")
+    kp, vp = _pools(k_pool, v_pool, shape, k_pool.dtype, dev)
+    wp, n_rows, max_len = _state(weights, f32, shape, dev, "weights")
+    want = (n_rows, shape.num_kv_heads, max_len)
+    for t, what in ((weights_out, "weights_out"), (positions, "positions"),
+                    (positions_out, "positions_out")):
+        _dims(t, want, what)
+    _check(load().paged_evict(
+        kp, vp, k_pool.element_size(), _tensor(block_table, i32, dev, "block_table"), mb,
+        _per_seq(ctx_lens, B, dev, "ctx_lens"), _per_seq(budget, B, dev, "budget"),
+        _per_seq(n_tokens, B, dev, "n_tokens"), _per_seq(kept, B, dev, "kept"),
+        _per_seq(rows, B, dev, "rows"), B, recent, sink, wp,
+        _tensor(weights_out, f32, dev, "weights_out"), _tensor(positions, i32, dev, "positions"),
+        _tensor(positions_out, i32, dev, "positions_out"), n_rows, max_len, C.byref(shape),
+        None if err is None else _tensor(err, i32, dev, "err"), _stream(stream)), "paged_evict")
 
 
 class StepLimits:

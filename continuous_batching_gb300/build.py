@@ -27,7 +27,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
 SOURCES = ["host.cpp", "sched.cpp", "pipeline.cpp", "kv_write.cu", "attention.cu",
-           "norm_rope.cu", "weights.cu"]
+           "norm_rope.cu", "weights.cu", "evict.cu"]
 
 
 def nvcc() -> str:

@@ -567,6 +567,44 @@ int32_t paged_attention_weights_fp8(const void* q, const void* k_pool, const flo
                                     int32_t max_len, float k_scale, const pa_shape* shape,
                                     int32_t* err_flag, pa_stream_t stream);
 
+/* ------------------------------------------------------------------------- eviction
+ * Cuts every sequence's cache to a budget, per KV head, by accumulated attention weight
+ * (paged_attention_weights). No counterpart on the pages, whose cache grows until it is freed.
+ *
+ * Of the ctx entries of a head min(ctx, budget) stay: first those whose token position is below
+ * `sink` or among the last `recent` of n_tokens, then those of larger weight, ties to the lower
+ * index (NaN ranks above every number; where more are protected than the budget holds, the lower
+ * indices stay). Those that stay and lie at or behind index min(ctx, budget) move into the places
+ * before it that come free, the k-th into the k-th, K, V, weight and position together; the others
+ * stay where they are. Entries are then out of token order, which attention does not notice: the
+ * rotation is in the keys, and every entry precedes the tokens still to come.
+ * Afterwards the sequence's context is min(ctx, budget): pa_alloc_trim gives the tail blocks back,
+ * new tokens are written behind it, and rotations go on from n_tokens.
+ *
+ * State: weights and positions [n_rows, Hkv, max_len] (fp32, int32), rows as in
+ * paged_attention_weights. kept[s] (NULL: all 0): the length that the last eviction of s left; the
+ * positions of the entries before it are read from `positions`, an entry j behind it holds token
+ * n_tokens - ctx + j. weights_out, positions_out receive the min(ctx, budget) entries of every
+ * sequence (the rest of them is left as it was); each is its input itself (in place) or does not
+ * overlap it.
+ * Device: k_pool, v_pool of elem_bytes 2 (bf16) or 1 (fp8 codes); block_table, ctx_lens, budget,
+ * n_tokens, kept, rows int32 per sequence. A sequence whose metadata does not fit (budget < 1,
+ * ctx > n_tokens, max_len or the table, kept > ctx, a row >= n_rows or named by two sequences) is
+ * skipped and sets PA_DEVERR_META; rows[s] < 0 takes no part; a row of a block outside the pool is
+ * not moved and sets PA_DEVERR_BLOCK. The first min(ctx, budget) entries are written: blocks that
+ * hold them and are shared have to be made private first (pa_alloc_slots over them answers
+ * PA_ERR_READONLY if there are any, pa_alloc_cow replaces them), and no two sequences of a call may
+ * share one.
+ * Host checks: max_len <= 2^19 and B <= 65535 (PA_ERR_SHAPE); n_rows >= B without rows. One launch,
+ * a programmatic dependent of what precedes it, no workspace; the result depends on no order. */
+int32_t paged_evict(void* k_pool, void* v_pool, int32_t elem_bytes, const int32_t* block_table,
+                    int32_t max_blocks, const int32_t* ctx_lens, const int32_t* budget,
+                    const int32_t* n_tokens, const int32_t* kept, const int32_t* rows, int32_t B,
+                    int32_t recent, int32_t sink, const float* weights, float* weights_out,
+                    const int32_t* positions, int32_t* positions_out, int32_t n_rows,
+                    int32_t max_len, const pa_shape* shape, int32_t* err_flag,
+                    pa_stream_t stream);
+
 /* Allocation-free variant of paged_attention_step (no counterpart on the pages: it is a
  * deployment convenience of this library). Same arguments, meaning and result as
  * paged_attention_step, minus the workspace: the split partials go to a fixed device array of

@@ -67,8 +67,9 @@ def evict(weights, positions, n_tokens, budget, recent, sink):
 
     def order(j):
         w = weights[j]
-        guarded = positions[j] < sink or positions[j] >= n_tokens - recent
-        return (0 if guarded else 1, 0 if math.isnan(w) else 1, 0.0 if math.isnan(w) else -w, j)
+        if positions[j] < sink or positions[j] >= n_tokens - recent:
+            return (0, 0, 0.0, j)
+        return (1, 0 if math.isnan(w) else 1, 0.0 if math.isnan(w) else -w, j)
 
     keep = set(sorted(range(ctx), key=order)[:length])
     source = list(range(length))
