@@ -10,11 +10,13 @@
 // were kept in order. Each entry's position is carried along for the next call's protection.
 //
 // A cluster of C CTAs takes one (sequence, head): each reads its slice of the weights once (held
-// as ordered 32-bit keys in shared memory), three radix passes (11, 11, 10 bits) over histograms
-// summed through distributed shared memory find the key of rank `budget`, and two bitmaps
-// (above it, equal to it) give the holes and strays. Nothing depends on the order of atomics:
-// they count. Then the CTAs share the moves. Bound by latency when few rows move (the passes'
-// barriers), by the strays' K and V rows otherwise.
+// as ordered 32-bit keys in shared memory; entries before the budget are copied to the output on
+// the way), three radix passes (11, 11, 10 bits) over histograms find the key of rank `budget`,
+// and two bitmaps (above it, equal to it) give the holes and strays. A pass's non-empty bins are
+// added up in the first CTA's shared memory, which finds the bin and tells the others: tens of
+// bins (pulling whole histograms from each other took 25 us a pass). Nothing depends on the order
+// of atomics: they count. Then the CTAs share the moves. Bound by latency when few rows move (the
+// passes' barriers), by the strays' K and V rows otherwise.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -28,10 +30,12 @@ using namespace pa_detail;
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;                // of a radix pass
+constexpr int kPer = kBins / kThreads;     // bins a thread scans
 constexpr int kWindow = 1024;              // moves listed at a time
+constexpr int kBatch = 8;                  // loads a thread has in flight
 constexpr int kCache = 8192;               // keys a CTA holds; a longer slice is read once a pass
 constexpr int kMaxLen = 1 << 19;           // entries: the bitmaps lie in shared memory
 constexpr int kMaxCluster = 8;
@@ -52,10 +56,11 @@ struct EvictParams {
 // Shared memory after the fixed part: the keep bitmap of all entries, the slice's equal bitmap,
 // the slice's keys.
 struct Fixed {
-    int32_t hist[kBins];
+    int32_t hist[kBins];                   // the CTA's own counts
+    int32_t all[kBins];                    // the cluster's, in the first CTA
     int32_t hole[kWindow], stray[kWindow];
     int32_t warp_sum[kWarps];
-    int32_t bin, need, equal, clash;
+    int32_t bin, need, count, equal, clash;
 };
 
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -86,22 +91,33 @@ __device__ __forceinline__ int block_scan(int x, int32_t* warp_sum, int& total) 
     return x + before;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
+// kMany: more than one CTA per (sequence, head).
+template <bool kMany>
+__global__ void __launch_bounds__(kThreads, 4) evict_kernel(const EvictParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     Fixed& sh = *reinterpret_cast<Fixed*>(smem);
     cg::cluster_group cluster = cg::this_cluster();
-    const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+    const int C = kMany ? int(cluster.num_blocks()) : 1;
+    const int rank = kMany ? int(cluster.block_rank()) : 0;
+    const auto sync_all = [&]() {
+        if constexpr (kMany) cluster.sync();
+        else __syncthreads();
+    };
     const int h = int(blockIdx.y), s = int(blockIdx.z);
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < kBins; i += kThreads) {
+        sh.hist[i] = 0;
+        if (kMany) sh.all[i] = 0;
+    }
+    if (tid == 0) sh.clash = 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- the sequence, the same for every CTA of the cluster
     const int row = p.rows ? p.rows[s] : s;
-    if (row < 0) return;                               // takes no part
     const int ctx = p.ctx[s], budget = p.budget[s], n_tokens = p.n_tokens[s];
     const int kept = p.kept ? p.kept[s] : 0;
-    if (tid == 0) sh.clash = 0;
+    if (row < 0) return;                               // takes no part
     __syncthreads();
     if (p.rows)
         for (int i = tid; i < p.B; i += kThreads)
@@ -123,105 +139,155 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     const int since = n_tokens - ctx;                  // position of entry j >= kept: since + j
     const int recent_from = n_tokens - min(p.recent, n_tokens);
     const auto position = [&](int j) { return j < kept ? pos_in[j] : since + j; };
-
-    const int words = (ctx + 31) / 32;
-    uint32_t* keep = reinterpret_cast<uint32_t*>(smem + sizeof(Fixed));
-    // what stays in its place
-    const auto settle = [&](bool all) {
-        const int i0 = int(int64_t(len) * rank / C), i1 = int(int64_t(len) * (rank + 1) / C);
-        for (int i = i0 + tid; i < i1; i += kThreads) {
-            if (!all && !(keep[i >> 5] >> (i & 31) & 1)) continue;
-            if (!same_w) w_out[i] = w_in[i];
-            if (!same_pos || i >= kept) pos_out[i] = position(i);
-        }
+    const auto rank_key = [&](int pos, float w) {
+        return pos < p.sink || pos >= recent_from ? 0xFFFFFFFFu : order_key(w);
     };
-    if (ctx <= budget) {
-        settle(true);
-        return;
-    }
+    const int words = (ctx + 31) / 32;
     const int w0 = int(int64_t(words) * rank / C), w1 = int(int64_t(words) * (rank + 1) / C);
     const int j0 = 32 * w0, j1 = min(ctx, 32 * w1);
+    uint32_t* keep = reinterpret_cast<uint32_t*>(smem + sizeof(Fixed));
     uint32_t* equal = keep + words;
     uint32_t* cached = equal + (words / C + 1);
     const bool hold = j1 - j0 <= p.cache;
-    const auto read_key = [&](int j) {
-        const int pos = position(j);
-        return pos < p.sink || pos >= recent_from ? 0xFFFFFFFFu : order_key(w_in[j]);
+    const bool cut = ctx > budget;                     // something goes
+    // the first CTA's counts start at zero before another adds to them (awaited below)
+    if constexpr (kMany)
+        if (cut) cluster.barrier_arrive();
+
+    // ---- the slice's keys, counted by their top bits; what lies before the budget goes to the
+    // output as if it stayed (an evicted entry's place is overwritten by its stray later, behind a
+    // barrier of the cluster)
+    for (int base = j0; base < j1; base += kThreads * kBatch) {
+        float w[kBatch];
+        int pos[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = base + i * kThreads + tid;
+            if (j < j1) {
+                w[i] = w_in[j];
+                pos[i] = position(j);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = base + i * kThreads + tid;
+            if (base + i * kThreads >= j1) break;
+            uint32_t k = 0;
+            if (j < j1) {
+                k = rank_key(pos[i], w[i]);
+                if (j < len) {
+                    if (!same_w) w_out[j] = w[i];
+                    if (!same_pos || j >= kept) pos_out[j] = pos[i];
+                }
+            }
+            if (!cut) continue;
+            if (j < j1 && hold) cached[j - j0] = k;
+            // the protected all fall in one bin: one count for a warp's
+            const bool guarded = j < j1 && k == 0xFFFFFFFFu;
+            const uint32_t all = __ballot_sync(0xffffffffu, guarded);
+            if (guarded) {
+                if (lane == __ffs(all) - 1) atomicAdd(&sh.hist[kBins - 1], __popc(all));
+            } else if (j < j1) {
+                atomicAdd(&sh.hist[k >> 21], 1);
+            }
+        }
+    }
+    if (!cut) return;
+    const auto key_of = [&](int j) {
+        return hold ? cached[j - j0] : rank_key(position(j), w_in[j]);
     };
-    const auto key_of = [&](int j) { return hold ? cached[j - j0] : read_key(j); };
 
     // ---- the key of rank `len`, and how many of its equals stay
     uint32_t prefix = 0;
-    int need = len;
+    int need = len, count = ctx;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const int bits = pass == 2 ? 10 : 11;
-        for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
-        __syncthreads();
-        if (pass == 0) {
-            for (int j = j0 + tid; j < j1; j += kThreads) {
-                const uint32_t k = read_key(j);
-                if (hold) cached[j - j0] = k;
-                atomicAdd(&sh.hist[k >> 21], 1);
-            }
-        } else {
+        if (pass > 0)
             for (int j = j0 + tid; j < j1; j += kThreads) {
                 const uint32_t k = key_of(j);
-                if (k >> (shift + bits) == prefix) atomicAdd(&sh.hist[k >> shift & ((1 << bits) - 1)], 1);
+                if (k >> (shift + bits) == prefix)
+                    atomicAdd(&sh.hist[k >> shift & ((1 << bits) - 1)], 1);
+            }
+        int4* own = reinterpret_cast<int4*>(sh.hist) + tid * (kPer / 4);
+        if constexpr (kMany) {
+            if (pass == 0) cluster.barrier_wait();
+            __syncthreads();
+            int32_t* all = cluster.map_shared_rank(sh.all, 0) + tid * kPer;
+#pragma unroll
+            for (int e = 0; e < kPer / 4; ++e) {
+                const int4 v = own[e];
+                if (v.x) atomicAdd(all + 4 * e, v.x);
+                if (v.y) atomicAdd(all + 4 * e + 1, v.y);
+                if (v.z) atomicAdd(all + 4 * e + 2, v.z);
+                if (v.w) atomicAdd(all + 4 * e + 3, v.w);
+                own[e] = make_int4(0, 0, 0, 0);
             }
         }
-        cluster.sync();
-        // from the highest bin down, kBins / kThreads bins a thread
-        constexpr int kPer = kBins / kThreads;
-        int count[kPer], sum = 0;
+        sync_all();
+        if (rank == 0) {
+            int4* from = kMany ? reinterpret_cast<int4*>(sh.all) + tid * (kPer / 4) : own;
+            int n[kPer], sum = 0, total;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) count[e] = 0;
-        for (int r = 0; r < C; ++r) {
-            const int32_t* other = C == 1 ? sh.hist : cluster.map_shared_rank(sh.hist, r);
+            for (int e = 0; e < kPer / 4; ++e) {
+                const int4 v = from[e];
+                from[e] = make_int4(0, 0, 0, 0);
+                n[4 * e] = v.x;
+                n[4 * e + 1] = v.y;
+                n[4 * e + 2] = v.z;
+                n[4 * e + 3] = v.w;
+                sum += v.x + v.y + v.z + v.w;
+            }
+            // rank `need` from the top is index count - need from the bottom
+            const int index = count - need;
+            int upto = block_scan(sum, sh.warp_sum, total);
+            int below = upto - sum;
+            if (below <= index && index < upto) {
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) count[e] += other[kBins - 1 - (tid * kPer + e)];
-        }
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) sum += count[e];
-        int total;
-        int above = block_scan(sum, sh.warp_sum, total) - sum;
-        if (above < need && need <= above + sum) {
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                if (above < need && need <= above + count[e]) {
-                    sh.bin = kBins - 1 - (tid * kPer + e);
-                    sh.need = need - above;
+                for (int e = 0; e < kPer; ++e) {
+                    if (below <= index && index < below + n[e])
+                        for (int r = 0; r < C; ++r) {
+                            Fixed* to = kMany ? cluster.map_shared_rank(&sh, r) : &sh;
+                            to->bin = tid * kPer + e;
+                            to->need = need - (count - below - n[e]);
+                            to->count = n[e];
+                        }
+                    below += n[e];
                 }
-                above += count[e];
             }
         }
-        cluster.sync();                                // the histograms have been read
+        sync_all();
         prefix = prefix << bits | uint32_t(sh.bin);
         need = sh.need;
+        count = sh.count;
     }
 
-    // ---- the slice's entries above it and equal to it
+    // ---- the slice's entries above it and equal to it; equal ones stay from the lowest index on
+    const bool ties = need < count;
     for (int w = w0 + warp; w < w1; w += kWarps) {
         const int j = 32 * w + lane;
         const uint32_t k = j < j1 ? key_of(j) : 0u;
         const uint32_t gt = __ballot_sync(0xffffffffu, j < j1 && k > prefix);
         const uint32_t eq = __ballot_sync(0xffffffffu, j < j1 && k == prefix);
         if (lane == 0) {
-            keep[w] = gt;
+            keep[w] = ties ? gt : gt | eq;
             equal[w - w0] = eq;
         }
     }
     __syncthreads();
-    {
-        const int n = w1 - w0, per = (n + kThreads - 1) / kThreads;
-        const int a = min(n, tid * per), b = min(n, a + per);
+    const int n_words = w1 - w0;
+    if (ties) {                                        // the same for the whole cluster
+        const int per = (n_words + kThreads - 1) / kThreads;
+        const int a = min(n_words, tid * per), b = min(n_words, a + per);
         int mine = 0, total;
         for (int w = a; w < b; ++w) mine += __popc(equal[w]);
         int before = block_scan(mine, sh.warp_sum, total) - mine;
-        if (tid == 0) sh.equal = total;
-        cluster.sync();
-        for (int r = 0; r < rank; ++r) before += *cluster.map_shared_rank(&sh.equal, r);
+        if constexpr (kMany) {
+            if (tid == 0) sh.equal = total;
+            cluster.sync();
+            for (int r = 0; r < rank; ++r) before += *cluster.map_shared_rank(&sh.equal, r);
+        }
         for (int w = a; w < b; ++w) {
             uint32_t e = equal[w];
             const int has = __popc(e), take = min(has, max(0, need - before));
@@ -229,18 +295,18 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
             keep[w0 + w] |= e;
             before += has;
         }
+        __syncthreads();
     }
-    cluster.sync();
-    // ---- every CTA takes the others' words
-    for (int r = 0; r < C; ++r) {
-        if (r == rank) continue;
-        const uint32_t* other = cluster.map_shared_rank(keep, r);
-        const int a = int(int64_t(words) * r / C), b = int(int64_t(words) * (r + 1) / C);
-        for (int w = a + tid; w < b; w += kThreads) keep[w] = other[w];
+    if constexpr (kMany) {
+        // every CTA gets the others' words; nothing of another CTA is touched after the barrier
+        for (int r = 0; r < C; ++r) {
+            if (r == rank) continue;
+            uint32_t* other = cluster.map_shared_rank(keep, r);
+            for (int w = w0 + tid; w < w1; w += kThreads) other[w] = keep[w];
+        }
+        cluster.sync();
     }
-    cluster.sync();                                    // no CTA leaves while another reads it
 
-    settle(false);
     // ---- holes and strays, this CTA's share of the moves a window at a time
     const int per = (words + kThreads - 1) / kThreads;
     const int wa = min(words, tid * per), wb = min(words, wa + per);
@@ -264,7 +330,14 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
                 if (at >= first && at < end) to[at - first] = 32 * w + __ffs(m) - 1;
     };
     const int32_t* table = p.table + int64_t(s) * p.max_blocks;
+    // the slot of entry j, -1 where the table leads outside the pool
+    const auto slot_of = [&](int j) {
+        const int b = table[j >> p.log2bs];
+        return b < 0 || b >= p.num_blocks ? -1
+                                          : (b << p.log2bs) + (j & ((1 << p.log2bs) - 1));
+    };
     const int log2_parts = p.log2_vecs + 1;            // vectors of a row's K and V
+    const int part_mask = (1 << log2_parts) - 1, vec_mask = (1 << p.log2_vecs) - 1;
     for (int first = m0; first < m1; first += kWindow) {
         const int end = min(m1, first + kWindow);
         __syncthreads();
@@ -273,47 +346,41 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
         __syncthreads();
         for (int e = tid; e < end - first; e += kThreads) {
             const int to = sh.hole[e], from = sh.stray[e];
+            const int dst = slot_of(to), src = slot_of(from);
             w_out[to] = w_in[from];
             pos_out[to] = position(from);
+            if ((dst < 0 || src < 0) && p.err) atomicOr(p.err, PA_DEVERR_BLOCK);
+            sh.hole[e] = src < 0 ? -1 : dst;           // the lists hold slots from here on
+            sh.stray[e] = src;
         }
-        // the vector of a block's entry j of this head: -1 where the table leads outside
-        const auto at = [&](int j, int part) -> int64_t {
-            const int b = table[j >> p.log2bs];
-            if (b < 0 || b >= p.num_blocks) return -1;
-            const int64_t slot = (int64_t(b) << p.log2bs) + (j & ((1 << p.log2bs) - 1));
-            return ((slot * p.Hkv + h) << p.log2_vecs) + (part & ((1 << p.log2_vecs) - 1));
-        };
+        __syncthreads();
         const int total = (end - first) << log2_parts;
-        constexpr int kFlight = 4;
-        for (int e0 = tid; e0 < total; e0 += kFlight * kThreads) {
-            uint4 v[kFlight];
-            int64_t dst[kFlight];
+        for (int e0 = tid; e0 < total; e0 += kBatch * kThreads) {
+            uint4 v[kBatch];
 #pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
+            for (int i = 0; i < kBatch; ++i) {
                 const int e = e0 + i * kThreads;
-                dst[i] = -1;
-                if (e >= total) continue;
-                const int m = e >> log2_parts, part = e & ((1 << log2_parts) - 1);
-                const int64_t src = at(sh.stray[m], part);
-                dst[i] = at(sh.hole[m], part);
-                if (src < 0 || dst[i] < 0) {
-                    dst[i] = -1;
-                    if (p.err) atomicOr(p.err, PA_DEVERR_BLOCK);
-                    continue;
-                }
-                v[i] = (part >> p.log2_vecs ? p.v_pool : p.k_pool)[src];
+                if (e >= total || sh.hole[e >> log2_parts] < 0) continue;
+                const int part = e & part_mask;
+                const int64_t at = (int64_t(sh.stray[e >> log2_parts]) * p.Hkv + h) << p.log2_vecs;
+                v[i] = (part > vec_mask ? p.v_pool : p.k_pool)[at + (part & vec_mask)];
             }
 #pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                if (dst[i] < 0) continue;
-                const int part = (e0 + i * kThreads) & ((1 << log2_parts) - 1);
-                (part >> p.log2_vecs ? p.v_pool : p.k_pool)[dst[i]] = v[i];
+            for (int i = 0; i < kBatch; ++i) {
+                const int e = e0 + i * kThreads;
+                if (e >= total || sh.hole[e >> log2_parts] < 0) continue;
+                const int part = e & part_mask;
+                const int64_t at = (int64_t(sh.hole[e >> log2_parts]) * p.Hkv + h) << p.log2_vecs;
+                (part > vec_mask ? p.v_pool : p.k_pool)[at + (part & vec_mask)] = v[i];
             }
         }
     }
 }
 
 constexpr int kMaxDevices = 64;
+// the largest: the fixed part, two bitmaps of kMaxLen and the keys
+constexpr int kMaxSmem = int(sizeof(Fixed)) + 2 * kMaxLen / 8 + 4 + 4 * kCache;
+static_assert(kMaxSmem <= 227 * 1024, "shared memory of one CTA");
 
 }  // namespace
 
@@ -334,7 +401,9 @@ extern "C" int32_t paged_evict(void* k_pool, void* v_pool, int32_t elem_bytes,
     if (!k_pool || !v_pool || !block_table || !ctx_lens || !budget || !n_tokens || !weights ||
         !weights_out || !positions || !positions_out || max_len == 0 || (!rows && n_rows < B))
         return PA_ERR_INVALID;
-    if (max_len > kMaxLen || B > 65535 || shape->num_kv_heads > 65535) return PA_ERR_SHAPE;
+    if (max_len > kMaxLen || B > 65535 || shape->num_kv_heads > 65535 ||
+        int64_t(shape->num_blocks) * shape->block_size > INT32_MAX)
+        return PA_ERR_SHAPE;
     const auto aligned = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
     if (!aligned(k_pool) || !aligned(v_pool)) return PA_ERR_INVALID;
     // weights and positions are replaced in place or written elsewhere, not half over themselves
@@ -350,9 +419,9 @@ extern "C" int32_t paged_evict(void* k_pool, void* v_pool, int32_t elem_bytes,
     if (dev < 0 || dev >= kMaxDevices) return PA_ERR_INVALID;
     static std::atomic<bool> raised[kMaxDevices];
     if (!raised[dev].load(std::memory_order_acquire)) {
-        if ((st = note_cuda(cudaFuncSetAttribute(
-                 evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024))))
-            return st;
+        constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        if ((st = note_cuda(cudaFuncSetAttribute(evict_kernel<false>, attr, kMaxSmem)))) return st;
+        if ((st = note_cuda(cudaFuncSetAttribute(evict_kernel<true>, attr, kMaxSmem)))) return st;
         raised[dev].store(true, std::memory_order_release);
     }
     EvictParams p;
@@ -401,6 +470,7 @@ extern "C" int32_t paged_evict(void* k_pool, void* v_pool, int32_t elem_bytes,
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attrs;
-    cfg.numAttrs = 2;
-    return note_cuda(cudaLaunchKernelEx(&cfg, evict_kernel, p));
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    return note_cuda(C > 1 ? cudaLaunchKernelEx(&cfg, evict_kernel<true>, p)
+                           : cudaLaunchKernelEx(&cfg, evict_kernel<false>, p));
 }
