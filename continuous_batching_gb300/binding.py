@@ -515,38 +515,48 @@ def paged_attention_step_fp8(q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_l
         "paged_attention_step_fp8")
 
 
-def _here() -> int:
-    """The current CUDA device, which every tensor of a call has to be on."""
-    import torch
-    return torch.cuda.current_device()
+class _Runtime:
+    """What the calls below need of torch, looked up once: a small call's time is this module's."""
+
+    def __init__(self):
+        import torch
+        self.lib = load()
+        self.bf16, self.u8, self.i32 = torch.bfloat16, torch.uint8, torch.int32
+        self.i64, self.f32 = torch.int64, torch.float32
+        self.device = torch.cuda.current_device
+        # the raw handle of the current stream, without a Stream object around it
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+    def stream(self, stream, dev: int):
+        return self.raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
-def _tensor(t, dtype, dev: int, what: str) -> int:
-    """Device address of a dense tensor of the given type on device `dev`."""
-    if t.dtype != dtype:
-        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: expected a tensor on the current CUDA device ({dev})")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor")
+_runtime = None
+
+
+def _rt() -> _Runtime:
+    global _runtime
+    if _runtime is None:
+        _runtime = _Runtime()
+    return _runtime
+
+
+def _arg(t, dtype, dev: int, shape: tuple, what: str) -> int:
+    """Device address of a dense tensor of this type and shape on the current device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(t, dtype, dev, shape, what)
     return t.data_ptr()
 
 
-def _dims(t, shape: tuple, what: str) -> None:
-    if tuple(t.shape) != shape:
+def _refuse(t, dtype, dev, shape, what):
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: expected a tensor on the current CUDA device ({dev})")
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-
-
-def _pools(k_pool, v_pool, shape: Shape, dtype, dev: int):
-    """Addresses of K and V pools of this shape (v_pool may be None)."""
-    want = (shape.num_blocks, shape.block_size, shape.num_kv_heads, shape.head_dim)
-    out = []
-    for t, what in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-        if t is None:
-            continue
-        _dims(t, want, what)
-        out.append(_tensor(t, dtype, dev, what))
-    return out
+    raise ValueError(f"{what}: expected a contiguous tensor")
 
 
 # ------------------------------------------------------- norm, rotation and KV write
@@ -573,14 +583,10 @@ def pa_rope_pairs(inv_freq, axes=None, n_axes: Optional[int] = None, device=None
     return torch.from_numpy(out.view(np.int64).reshape(-1, 2).copy()).to(device)
 
 
-def _token_rows(t, heads: int, D: int, T: int, dev: int, what: str):
-    """(address, elements between tokens) of [T, heads, D] bf16 with dense heads and columns."""
-    import torch
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{what}: expected torch.bfloat16, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: expected a tensor on the current CUDA device ({dev})")
-    _dims(t, (T, heads, D), what)
+def _token_rows(t, dtype, heads: int, D: int, T: int, dev: int, what: str):
+    """(address, elements between tokens) of [T, heads, D] with dense heads and columns."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (T, heads, D):
+        _refuse(t, dtype, dev, (T, heads, D), what)
     s = t.stride()
     if s[2] != 1 or (s[1] != D and heads > 1):
         raise ValueError(f"{what}: heads and columns have to be dense")
@@ -589,41 +595,38 @@ def _token_rows(t, heads: int, D: int, T: int, dev: int, what: str):
 
 def _norm_rope(q, k_new, v_new, q_weight, k_weight, eps, rope, positions, slot_mapping, q_out,
                k_pool, v_pool, shape, interleaved, err, stream, scales):
-    import torch
-    dev = _here()
-    T = int(slot_mapping.shape[0])
+    rt = _rt()
+    dev, bf16, i32 = rt.device(), rt.bf16, rt.i32
+    T = slot_mapping.shape[0]
     Hq, Hkv, D = shape.num_q_heads, shape.num_kv_heads, shape.head_dim
-    i32 = torch.int32
-    qp, qs = _token_rows(q, Hq, D, T, dev, "q")
-    kp, ks = _token_rows(k_new, Hkv, D, T, dev, "k_new")
-    vp, vs = _token_rows(v_new, Hkv, D, T, dev, "v_new")
-    w = []
-    for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _dims(t, (D,), what)
-        w.append(None if t is None else _tensor(t, torch.bfloat16, dev, what))
+    qp, qs = _token_rows(q, bf16, Hq, D, T, dev, "q")
+    kp, ks = _token_rows(k_new, bf16, Hkv, D, T, dev, "k_new")
+    vp, vs = _token_rows(v_new, bf16, Hkv, D, T, dev, "v_new")
     n_pairs, n_axes, rp, pp = 0, 1, None, None
     if rope is not None:
         if positions is None:
             raise ValueError("positions: needed with a rotation")
-        n_pairs = int(rope.shape[0])
-        rp = _tensor(rope, torch.int64, dev, "rope")
-        _dims(rope, (n_pairs, 2), "rope")
-        n_axes = 1 if positions.dim() == 1 else int(positions.shape[0])
-        _dims(positions, (T,) if positions.dim() == 1 else (n_axes, T), "positions")
-        pp = _tensor(positions, i32, dev, "positions")
-    _dims(slot_mapping, (T,), "slot_mapping")
-    _dims(q_out, (T, Hq, D), "q_out")
-    pools = _pools(k_pool, v_pool, shape, torch.bfloat16 if scales is None else torch.uint8, dev)
-    args = [qp, qs, kp, ks, vp, vs, w[0], w[1], eps, rp, n_pairs, 1 if interleaved else 0, pp,
-            n_axes, _tensor(slot_mapping, i32, dev, "slot_mapping"), T,
-            _tensor(q_out, torch.bfloat16, dev, "q_out"), *pools]
-    tail = [C.byref(shape), None if err is None else _tensor(err, i32, dev, "err"),
-            _stream(stream)]
+        n_pairs = rope.shape[0]
+        rp = _arg(rope, rt.i64, dev, (n_pairs, 2), "rope")
+        one = positions.dim() == 1
+        n_axes = 1 if one else positions.shape[0]
+        pp = _arg(positions, i32, dev, (T,) if one else (n_axes, T), "positions")
+    pool = (shape.num_blocks, shape.block_size, Hkv, D)
+    e = bf16 if scales is None else rt.u8
+    args = (qp, qs, kp, ks, vp, vs,
+            None if q_weight is None else _arg(q_weight, bf16, dev, (D,), "q_weight"),
+            None if k_weight is None else _arg(k_weight, bf16, dev, (D,), "k_weight"),
+            eps, rp, n_pairs, 1 if interleaved else 0, pp, n_axes,
+            _arg(slot_mapping, i32, dev, (T,), "slot_mapping"), T,
+            _arg(q_out, bf16, dev, (T, Hq, D), "q_out"), _arg(k_pool, e, dev, pool, "k_pool"),
+            _arg(v_pool, e, dev, pool, "v_pool"))
+    ep = None if err is None else _arg(err, i32, dev, (1,), "err")
     if scales is None:
-        _check(load().paged_qk_norm_rope_write(*args, *tail), "paged_qk_norm_rope_write")
+        _check(rt.lib.paged_qk_norm_rope_write(*args, C.byref(shape), ep, rt.stream(stream, dev)),
+               "paged_qk_norm_rope_write")
     else:
-        _check(load().paged_qk_norm_rope_write_fp8(*args, *scales, *tail),
+        _check(rt.lib.paged_qk_norm_rope_write_fp8(*args, *scales, C.byref(shape), ep,
+                                                   rt.stream(stream, dev)),
                "paged_qk_norm_rope_write_fp8")
 
 
@@ -644,59 +647,39 @@ def paged_qk_norm_rope_write_fp8(q, k_new, v_new, q_weight, k_weight, eps: float
                                  err=None, stream=None) -> None:
     """paged_qk_norm_rope_write into uint8 float8_e4m3fn pools with per-tensor scales."""
     _norm_rope(q, k_new, v_new, q_weight, k_weight, eps, rope, positions, slot_mapping, q_out,
-               k_pool, v_pool, shape, interleaved, err, stream, (k_scale, v_scale))
+               k_pool, v_pool, shape, interleaved, err, stream, (float(k_scale), float(v_scale)))
 
 
 # ---------------------------------------------------------- attention weights per key
 
-def _step_meta(q, block_table, cu_seqlens_q, ctx_lens, shape: Shape, dev: int):
-    """(B, T, max_blocks and the addresses of q, block_table, cu_seqlens_q, ctx_lens)."""
-    import torch
-    i32 = torch.int32
-    B, T = int(ctx_lens.shape[0]), int(q.shape[0])
-    _dims(q, (T, shape.num_q_heads, shape.head_dim), "q")
-    _dims(cu_seqlens_q, (B + 1,), "cu_seqlens_q")
-    _dims(ctx_lens, (B,), "ctx_lens")
-    mb = int(block_table.shape[1])
-    _dims(block_table, (B, mb), "block_table")
-    return (B, T, mb, _tensor(q, torch.bfloat16, dev, "q"),
-            _tensor(block_table, i32, dev, "block_table"),
-            _tensor(cu_seqlens_q, i32, dev, "cu_seqlens_q"),
-            _tensor(ctx_lens, i32, dev, "ctx_lens"))
-
-
-def _per_seq(t, B: int, dev: int, what: str):
+def _per_seq(t, rt: _Runtime, B: int, dev: int, what: str):
     """Address of an int32 value per sequence, or None."""
-    import torch
-    if t is None:
-        return None
-    _dims(t, (B,), what)
-    return _tensor(t, torch.int32, dev, what)
-
-
-def _state(t, dtype, shape: Shape, dev: int, what: str):
-    """(address, rows, max_len) of a [rows, Hkv, max_len] state tensor."""
-    n, m = int(t.shape[0]), int(t.shape[-1])
-    _dims(t, (n, shape.num_kv_heads, m), what)
-    return _tensor(t, dtype, dev, what), n, m
+    return None if t is None else _arg(t, rt.i32, dev, (B,), what)
 
 
 def _weights(q, k_pool, lse, block_table, cu_seqlens_q, ctx_lens, rows, weights, shape, held, err,
              stream, k_scale):
-    import torch
-    dev = _here()
-    B, T, mb, qp, tp, cup, ctxp = _step_meta(q, block_table, cu_seqlens_q, ctx_lens, shape, dev)
-    kp, = _pools(k_pool, None, shape, torch.bfloat16 if k_scale is None else torch.uint8, dev)
-    _dims(lse, (T, shape.num_q_heads), "lse")
-    wp, n_rows, max_len = _state(weights, torch.float32, shape, dev, "weights")
-    args = [qp, kp, _tensor(lse, torch.float32, dev, "lse"), tp, mb, cup, ctxp, B, T,
-            _per_seq(held, B, dev, "held"), _per_seq(rows, B, dev, "rows"), wp, n_rows, max_len]
-    tail = [C.byref(shape), None if err is None else _tensor(err, torch.int32, dev, "err"),
-            _stream(stream)]
+    rt = _rt()
+    dev, i32 = rt.device(), rt.i32
+    Hq, Hkv, D = shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    B, T, mb = ctx_lens.shape[0], q.shape[0], block_table.shape[1]
+    n_rows, max_len = weights.shape[0], weights.shape[-1]
+    args = (_arg(q, rt.bf16, dev, (T, Hq, D), "q"),
+            _arg(k_pool, rt.bf16 if k_scale is None else rt.u8, dev,
+                 (shape.num_blocks, shape.block_size, Hkv, D), "k_pool"),
+            _arg(lse, rt.f32, dev, (T, Hq), "lse"),
+            _arg(block_table, i32, dev, (B, mb), "block_table"), mb,
+            _arg(cu_seqlens_q, i32, dev, (B + 1,), "cu_seqlens_q"),
+            _arg(ctx_lens, i32, dev, (B,), "ctx_lens"), B, T, _per_seq(held, rt, B, dev, "held"),
+            _per_seq(rows, rt, B, dev, "rows"),
+            _arg(weights, rt.f32, dev, (n_rows, Hkv, max_len), "weights"), n_rows, max_len)
+    ep = None if err is None else _arg(err, i32, dev, (1,), "err")
     if k_scale is None:
-        _check(load().paged_attention_weights(*args, *tail), "paged_attention_weights")
+        _check(rt.lib.paged_attention_weights(*args, C.byref(shape), ep, rt.stream(stream, dev)),
+               "paged_attention_weights")
     else:
-        _check(load().paged_attention_weights_fp8(*args, k_scale, *tail),
+        _check(rt.lib.paged_attention_weights_fp8(*args, k_scale, C.byref(shape), ep,
+                                                  rt.stream(stream, dev)),
                "paged_attention_weights_fp8")
 
 
@@ -728,27 +711,27 @@ def paged_evict(k_pool, v_pool, block_table, ctx_lens, budget, n_tokens, kept, r
     after the last eviction, None: 0), rows (state rows, None: the index): int32 [B]. weights fp32 and
     positions int32 [n_rows, Hkv, max_len] go to weights_out and positions_out (the same tensors, or
     others)."""
-    import torch
-    dev = _here()
-    i32, f32 = torch.int32, torch.float32
-    B, mb = int(ctx_lens.shape[0]), int(block_table.shape[1])
-    _dims(block_table, (B, mb), "block_table")
-    if k_pool.dtype not in (torch.bfloat16, torch.uint8):
-        raise ValueError(f"k_pool: expected torch.bfloat16 or torch.uint8, got {k_pool.dtype}")
-    kp, vp = _pools(k_pool, v_pool, shape, k_pool.dtype, dev)
-    wp, n_rows, max_len = _state(weights, f32, shape, dev, "weights")
-    want = (n_rows, shape.num_kv_heads, max_len)
-    for t, what in ((weights_out, "weights_out"), (positions, "positions"),
-                    (positions_out, "positions_out")):
-        _dims(t, want, what)
-    _check(load().paged_evict(
-        kp, vp, k_pool.element_size(), _tensor(block_table, i32, dev, "block_table"), mb,
-        _per_seq(ctx_lens, B, dev, "ctx_lens"), _per_seq(budget, B, dev, "budget"),
-        _per_seq(n_tokens, B, dev, "n_tokens"), _per_seq(kept, B, dev, "kept"),
-        _per_seq(rows, B, dev, "rows"), B, recent, sink, wp,
-        _tensor(weights_out, f32, dev, "weights_out"), _tensor(positions, i32, dev, "positions"),
-        _tensor(positions_out, i32, dev, "positions_out"), n_rows, max_len, C.byref(shape),
-        None if err is None else _tensor(err, i32, dev, "err"), _stream(stream)), "paged_evict")
+    rt = _rt()
+    dev, i32 = rt.device(), rt.i32
+    B, mb = ctx_lens.shape[0], block_table.shape[1]
+    n_rows, max_len = weights.shape[0], weights.shape[-1]
+    state = (n_rows, shape.num_kv_heads, max_len)
+    pool = (shape.num_blocks, shape.block_size, shape.num_kv_heads, shape.head_dim)
+    e = k_pool.dtype
+    if e is not rt.bf16 and e is not rt.u8:
+        raise ValueError(f"k_pool: expected {rt.bf16} or {rt.u8}, got {e}")
+    _check(rt.lib.paged_evict(
+        _arg(k_pool, e, dev, pool, "k_pool"), _arg(v_pool, e, dev, pool, "v_pool"),
+        2 if e is rt.bf16 else 1, _arg(block_table, i32, dev, (B, mb), "block_table"), mb,
+        _arg(ctx_lens, i32, dev, (B,), "ctx_lens"), _arg(budget, i32, dev, (B,), "budget"),
+        _arg(n_tokens, i32, dev, (B,), "n_tokens"), _per_seq(kept, rt, B, dev, "kept"),
+        _per_seq(rows, rt, B, dev, "rows"), B, recent, sink,
+        _arg(weights, rt.f32, dev, state, "weights"),
+        _arg(weights_out, rt.f32, dev, state, "weights_out"),
+        _arg(positions, i32, dev, state, "positions"),
+        _arg(positions_out, i32, dev, state, "positions_out"), n_rows, max_len, C.byref(shape),
+        None if err is None else _arg(err, i32, dev, (1,), "err"), rt.stream(stream, dev)),
+        "paged_evict")
 
 
 class StepLimits:
