@@ -174,6 +174,17 @@ def load() -> C.CDLL:
                    C.c_int32, C.c_int32]
         _sig(lib, "paged_attention_weights", C.c_int32, weights + [sp, _vp, _vp])
         _sig(lib, "paged_attention_weights_fp8", C.c_int32, weights + [C.c_float, sp, _vp, _vp])
+        i32 = C.c_int32
+        step = [_vp, _vp, _vp, _vp, i32, _vp, _vp, i32, i32, i32, _vp, i32]
+        f8 = [C.c_float, C.c_float]
+        end = [sp, _vp, _vp]
+        lse = [_vp, C.c_size_t, _vp, _vp]
+        state = [_vp, _vp, _vp, i32, i32]
+        _sig(lib, "paged_attention_step_lse", i32, step + lse + end)
+        _sig(lib, "paged_attention_step_fp8_lse", i32, step + f8 + lse + end)
+        _sig(lib, "pa_step_weights_workspace_bytes", C.c_size_t, [sp, i32, i32, i32])
+        _sig(lib, "paged_attention_step_weights", i32, step + lse + state + end)
+        _sig(lib, "paged_attention_step_weights_fp8", i32, step + f8 + lse + state + end)
         _sig(lib, "paged_evict", C.c_int32,
              [_vp, _vp, C.c_int32, _vp, C.c_int32, _vp, _vp, _vp, _vp, _vp, C.c_int32, C.c_int32,
               C.c_int32, _vp, _vp, _vp, _vp, C.c_int32, C.c_int32, sp, _vp, _vp])
@@ -699,6 +710,80 @@ def paged_attention_weights_fp8(q, k_pool, lse, block_table, cu_seqlens_q, ctx_l
     """paged_attention_weights over a uint8 float8_e4m3fn pool with its per-tensor scale."""
     _weights(q, k_pool, lse, block_table, cu_seqlens_q, ctx_lens, rows, weights, shape, held, err,
              stream, float(k_scale))
+
+
+# ------------------------------------------------ the step of a bounded cache
+
+def pa_step_weights_workspace_bytes(shape: Shape, B: int, T: int, max_ctx: int) -> int:
+    return int(load().pa_step_weights_workspace_bytes(C.byref(shape), int(B), int(T), int(max_ctx)))
+
+
+def _step(name, q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_lens, max_ctx, items, scales,
+          workspace, out, lse, shape, err, stream, state=None):
+    """Any of the steps that keep statistics; state: (held, rows, weights) of the weights ones."""
+    rt = _rt()
+    dev, i32 = rt.device(), rt.i32
+    Hq, Hkv, D = shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    B, T, mb, n_words = ctx_lens.shape[0], q.shape[0], block_table.shape[1], items.shape[0]
+    pool = (shape.num_blocks, shape.block_size, Hkv, D)
+    e = rt.bf16 if scales is None else rt.u8
+    args = [_arg(q, rt.bf16, dev, (T, Hq, D), "q"), _arg(k_pool, e, dev, pool, "k_pool"),
+            _arg(v_pool, e, dev, pool, "v_pool"),
+            _arg(block_table, i32, dev, (B, mb), "block_table"), mb,
+            _arg(cu_seqlens_q, i32, dev, (B + 1,), "cu_seqlens_q"),
+            _arg(ctx_lens, i32, dev, (B,), "ctx_lens"), B, T, max_ctx,
+            _arg(items, i32, dev, (n_words,), "items"), n_words // ITEM_INTS, *(scales or ())]
+    if workspace is None:
+        args += [None, 0]
+    else:
+        n = workspace.shape[0]
+        args += [_arg(workspace, rt.f32, dev, (n,), "workspace"), 4 * n]
+    args += [_arg(out, rt.bf16, dev, (T, Hq, D), "out"), _arg(lse, rt.f32, dev, (T, Hq), "lse")]
+    if state is not None:
+        held, rows, weights = state
+        n_rows, max_len = weights.shape[0], weights.shape[-1]
+        args += [_per_seq(held, rt, B, dev, "held"), _per_seq(rows, rt, B, dev, "rows"),
+                 _arg(weights, rt.f32, dev, (n_rows, Hkv, max_len), "weights"), n_rows, max_len]
+    _check(getattr(rt.lib, name)(*args, C.byref(shape),
+                                 None if err is None else _arg(err, i32, dev, (1,), "err"),
+                                 rt.stream(stream, dev)), name)
+
+
+def paged_attention_step_lse(q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_lens, max_ctx: int,
+                             items, workspace, out, lse, shape: Shape, err=None,
+                             stream=None) -> None:
+    """paged_attention_step that also gives the rows' log-sum-exp, lse fp32 [T, Hq]. workspace: a
+    flat fp32 tensor (or None where pa_workspace_bytes asks for none)."""
+    _step("paged_attention_step_lse", q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_lens,
+          max_ctx, items, None, workspace, out, lse, shape, err, stream)
+
+
+def paged_attention_step_fp8_lse(q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_lens,
+                                 max_ctx: int, items, k_scale: float, v_scale: float, workspace,
+                                 out, lse, shape: Shape, err=None, stream=None) -> None:
+    """paged_attention_step_lse over uint8 float8_e4m3fn pools with per-tensor scales."""
+    _step("paged_attention_step_fp8_lse", q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_lens,
+          max_ctx, items, (k_scale, v_scale), workspace, out, lse, shape, err, stream)
+
+
+def paged_attention_step_weights(q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_lens,
+                                 max_ctx: int, items, workspace, out, lse, rows, weights,
+                                 shape: Shape, held=None, err=None, stream=None) -> None:
+    """The step of a bounded cache: paged_attention_step_lse and paged_attention_weights of its rows
+    in one call (decode rows read K once for both). workspace: a flat fp32 tensor of at least
+    pa_step_weights_workspace_bytes."""
+    _step("paged_attention_step_weights", q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_lens,
+          max_ctx, items, None, workspace, out, lse, shape, err, stream, (held, rows, weights))
+
+
+def paged_attention_step_weights_fp8(q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_lens,
+                                     max_ctx: int, items, k_scale: float, v_scale: float,
+                                     workspace, out, lse, rows, weights, shape: Shape, held=None,
+                                     err=None, stream=None) -> None:
+    """paged_attention_step_weights over uint8 float8_e4m3fn pools with per-tensor scales."""
+    _step("paged_attention_step_weights_fp8", q, k_pool, v_pool, block_table, cu_seqlens_q,
+          ctx_lens, max_ctx, items, (k_scale, v_scale), workspace, out, lse, shape, err, stream,
+          (held, rows, weights))
 
 
 # ------------------------------------------------------------------------- eviction

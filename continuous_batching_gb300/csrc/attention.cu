@@ -152,6 +152,10 @@ struct Params {
     float c;            // log2(e) / sqrt(D) (times the K scale of an fp8 cache): softmax
                         // works in base 2 on raw scores
     float v_scale;      // V scale of an fp8 cache (1 for bf16): out = O * (rcp(l) * v_scale)
+    // what the statistics-keeping instantiations give beside out (unused by the others)
+    float* lse;         // [T][Hq]: log-sum-exp of every row, natural logarithm
+    float* scores;      // [B][Hq][scores_ld] raw scores of the decode rows, or NULL
+    int64_t scores_ld;
     unsigned long long never_ns;   // nonzero only in the wait-timeout test: the softmax warps
                                    // first wait this long on kNever, which nothing completes
 };
@@ -221,13 +225,14 @@ struct Item {
     int kind;           // PA_ITEM_*
     int tile0;          // the item's first key tile within its split: a RESUME item's tile0
                         // (it continues split 0 there), 0 for every other item
+    int decode;         // its rows are decode rows (of sequences seq, seq + 1, ... g rows each)
 };
 
 // What the producer publishes in an item slot (64 bytes); `last` marks the end of the CTA's
 // item list.
 struct ItemSlot {
     int seq, ctx, q_start, n_q, kvh, split, n_splits, pos0, k_begin, n_tiles, rows_valid, last,
-        kind, tile0, pad[2];
+        kind, tile0, decode, pad;
 };
 static_assert(sizeof(ItemSlot) == 64, "item slot size");
 
@@ -247,6 +252,7 @@ __device__ __forceinline__ Item slot_item(const volatile ItemSlot* sl, bool* las
     I.rows_valid = sl->rows_valid;
     I.kind = sl->kind;
     I.tile0 = sl->tile0;
+    I.decode = sl->decode;
     *last = sl->last != 0;
     return I;
 }
@@ -282,6 +288,7 @@ __device__ __forceinline__ Item load_item(const Params& p, int idx, int lane) {
                   it.tile0 < kSplitTiles && p.ws_acc != nullptr));
     I.kind = good ? it.kind : PA_ITEM_PLAIN;
     I.tile0 = good && it.kind == PA_ITEM_RESUME ? it.tile0 : 0;
+    I.decode = 1;
     if (good && it.kind == PA_ITEM_GROUP) {
         good = group_members_ok(p.cu, p.ctx, p.B, p.bs, p.max_blocks, it.seq, it.n_q,
                                 it.q_start, it.tile0, lane);
@@ -317,6 +324,7 @@ __device__ __forceinline__ Item load_item(const Params& p, int idx, int lane) {
            (I.kind != PA_ITEM_RESUME || cu1 - cu0 == 1);
     const int k_end = min(it.split * kSplit + ns * kSplit, p_max + 1);
     I.good = good;
+    I.decode = cu1 - cu0 == 1;
     I.seq = seq;
     I.ctx = ctx_s;
     I.q_start = it.q_start;
@@ -357,9 +365,12 @@ __device__ __forceinline__ void rows_init(Rows2& R, int r0, int rs, int rows_val
 // rows' state is updated, their P, rounded to bf16, goes to pk (packed column 4 cc + q4 of row
 // sr is pk[2 cc + sr]) and alpha[sr] is the factor the row's O must be scaled by. The
 // arithmetic of a row depends on its own scores only.
-template <int NR, bool H16>
+// With STATS the raw scores (masked ones -infinity) of the rows whose sc is not NULL are stored
+// there: what a later kernel needs to turn them into weights once the row's sum is known.
+template <int NR, bool H16, bool STATS>
 __device__ __forceinline__ void softmax_rows(const uint32_t (&r)[64], uint32_t (&pk)[32], int q4,
-                                             int kb, float c, Rows2& R, float alpha[2]) {
+                                             int kb, float c, Rows2& R, float alpha[2],
+                                             float* const (&sc)[2]) {
     float sv[NR][32];
     float mx[NR];
 #pragma unroll
@@ -384,6 +395,14 @@ __device__ __forceinline__ void softmax_rows(const uint32_t (&r)[64], uint32_t (
                 }
         }
         mx[sr] = max32(sv[sr]);
+        if constexpr (STATS) {
+            if (sc[sr]) {
+#pragma unroll
+                for (int cc = 0; cc < 16; ++cc)
+                    *reinterpret_cast<float2*>(sc[sr] + kb + 8 * cc + 2 * q4) =
+                        make_float2(sv[sr][2 * cc], sv[sr][2 * cc + 1]);
+            }
+        }
     }
 #pragma unroll
     for (int sr = 0; sr < NR; ++sr) mx[sr] = fmaxf(mx[sr], __shfl_xor_sync(0xffffffffu, mx[sr], 1));
@@ -471,20 +490,21 @@ __device__ __forceinline__ void softmax_rows(const uint32_t (&r)[64], uint32_t (
 // alpha[sr] is the factor the row's O must be scaled by. A second 8-row block with no valid
 // row (the tail of a decode or of a ragged tile) needs no softmax: its P is never used for a
 // written output.
-template <bool H16>
+template <bool H16, bool STATS>
 __device__ __forceinline__ void softmax_half(uint32_t tm_s, int r0, int q4, int rows_valid,
-                                             int kb, float c, Rows2& R, float alpha[2]) {
+                                             int kb, float c, Rows2& R, float alpha[2],
+                                             float* const (&sc)[2]) {
     uint32_t r[64];
     tmem_ld_16x256b_x16(tm_s, r);
     tmem_wait_ld();
     uint32_t pk[32];                 // P rounded to bf16, packed in pairs
     if (r0 + 8 >= rows_valid) {
-        softmax_rows<1, H16>(r, pk, q4, kb, c, R, alpha);
+        softmax_rows<1, H16, STATS>(r, pk, q4, kb, c, R, alpha, sc);
         alpha[1] = 1.f;
 #pragma unroll
         for (int cc = 0; cc < 16; ++cc) pk[2 * cc + 1] = 0u;
     } else {
-        softmax_rows<2, H16>(r, pk, q4, kb, c, R, alpha);
+        softmax_rows<2, H16, STATS>(r, pk, q4, kb, c, R, alpha, sc);
     }
     // P replaces S in the first 64 columns of this tile's S buffer
     tmem_st_16x128b_x16(tm_s, pk);
@@ -512,13 +532,18 @@ __device__ __forceinline__ void rescale_half(uint32_t tm_o, const float alpha[2]
     else tmem_st_16x256b_x8(tm_o, o);
 }
 
+// Log-sum-exp of a row from its reference maximum (raw score units) and sum, natural logarithm.
+__device__ __forceinline__ float row_lse(float m, float l, float c) {
+    return fmaf(__fmul_rn(m, c), 0.693147180559945309f, logf(l));
+}
+
 // Epilogue of the half, O already in registers: a row whose position lies in one split is
 // finished here (out = bf16(O * (rcp(l) * v_scale))); a row spanning several splits stores this split's
 // partial (acc = O, m, l) for the fixed-order combine. Rows are those of a tile whose first
 // row is token q_start at position pos0 (rows_valid rows, g heads per token).
 // A GROUP item (save) stores every valid row as the partial of split 0, whatever the row's
 // own position: the state its RESUME item restores and continues.
-template <int D>
+template <int D, bool STATS>
 __device__ __forceinline__ void store_half(const Params& p, const uint32_t* o, int r0, int rs,
                                            int q4, int rows_valid, int q_start, int kvh,
                                            int split, const Rows2& R, bool save) {
@@ -533,6 +558,8 @@ __device__ __forceinline__ void store_half(const Params& p, const uint32_t* o, i
         const int head = kvh * p.g + row % p.g;
         if (nsp == 1 && !save) {
             const float inv = __fmul_rn(__frcp_rn(R.l[sr]), p.v_scale);
+            if constexpr (STATS)
+                if (q4 == 0) p.lse[int64_t(tok) * p.Hq + head] = row_lse(R.m[sr], R.l[sr], p.c);
             __nv_bfloat16* dst = p.out + (int64_t(tok) * p.Hq + head) * D;
 #pragma unroll
             for (int cc = 0; cc < D / 8; ++cc) {
@@ -610,7 +637,7 @@ struct Fold2 {
 // running result unchanged, as the combine would not fold it. Unless fin, the result goes to
 // tm_p, whose buffer holds the running result from here on; with fin the rows are finished,
 // out = bf16(ACC * (rcp(L) * v_scale)), like every other row of the step.
-template <int D>
+template <int D, bool STATS>
 __device__ __forceinline__ void fold_half(const Params& p, uint32_t tm_a, uint32_t tm_p, int r0,
                                           int rs, int q4, int rows_valid, int q_start, int kvh,
                                           int js, bool fin, const Rows2& R, Fold2& F) {
@@ -629,6 +656,12 @@ __device__ __forceinline__ void fold_half(const Params& p, uint32_t tm_a, uint32
             F.M[sr] = mn;
         }
         inv[sr] = fin ? __fmul_rn(__frcp_rn(F.L[sr]), p.v_scale) : 0.f;
+        if constexpr (STATS) {
+            const int row = r0 + rs + 8 * sr;
+            if (fin && q4 == 0 && row < rows_valid)
+                p.lse[int64_t(q_start + row / p.g) * p.Hq + kvh * p.g + row % p.g] =
+                    row_lse(F.M[sr], F.L[sr], p.c);
+        }
     }
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) {
@@ -693,7 +726,8 @@ __device__ __forceinline__ void zero_v_tail(uint32_t vb, int kb, int ctx, int bs
 
 // F8: the pools hold float8_e4m3fn codes (head_dim 128 only); the loaders expand each tile
 // to f16 in shared memory, Q is rounded to f16, and the MMAs take f16 operands.
-template <int D, bool F8>
+// STATS: the rows' log-sum-exps and, for decode rows, their raw scores are stored as well.
+template <int D, bool F8, bool STATS>
 __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v,
@@ -807,6 +841,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     sl->rows_valid = I.rows_valid;
                     sl->kind = I.kind;
                     sl->tile0 = I.tile0;
+                    sl->decode = I.decode;
                     sl->last = have ? 0 : 1;
                     mbar_arrive(bar(kItemFull + slot));
                 }
@@ -1183,6 +1218,18 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             mbar_arrive(bar(kItemEmpty + (ic & 3)));
             if (last) break;
             const bool on = r0 < I.rows_valid;    // warp-uniform: the warp holds a valid row
+            float* sc[2] = {nullptr, nullptr};
+            if constexpr (STATS) {
+                if (p.scores && I.decode) {
+#pragma unroll
+                    for (int sr = 0; sr < 2; ++sr) {
+                        const int row = r0 + rs + 8 * sr;
+                        if (row < I.rows_valid)
+                            sc[sr] = p.scores + (int64_t(I.seq + row / p.g) * p.Hq +
+                                                 I.kvh * p.g + row % p.g) * p.scores_ld;
+                    }
+                }
+            }
             Rows2 R;
             Fold2 F;
             // a RESUME item starts inside split 0, at tile tile0 (0 for every other item)
@@ -1212,9 +1259,13 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 tc_fence_after();
                 const int kb = I.k_begin + jt * kTileKeys;
                 float alpha[2] = {1.f, 1.f};
+                if constexpr (STATS) {
+                    // a context that outgrew the caller's bound: behind the row's scores
+                    if (kb + kTileKeys > p.scores_ld) sc[0] = sc[1] = nullptr;
+                }
                 if (on)
-                    softmax_half<F8>(tmem + (tc & 1) * 128 + lanes, r0, q4, I.rows_valid, kb, c, R,
-                                     alpha);
+                    softmax_half<F8, STATS>(tmem + (tc & 1) * 128 + lanes, r0, q4, I.rows_valid, kb,
+                                            c, R, alpha, sc);
                 // O belongs to the previous tile's PV until it has finished: rescale only then,
                 // and only in warps where some row's running maximum moved
                 const bool need = alpha[0] != 1.f || alpha[1] != 1.f;
@@ -1258,7 +1309,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     const bool fin = js == I.n_splits - 1;
                     const uint32_t tm_a = tmem + kTmemO + (ob ^ 1) * 128 + lanes;
                     if (on)
-                        fold_half<D>(p, tm_a, tm_o, r0, rs, q4, I.rows_valid, I.q_start, I.kvh,
+                        fold_half<D, STATS>(p, tm_a, tm_o, r0, rs, q4, I.rows_valid, I.q_start, I.kvh,
                                      js, fin, R, F);
                     tc_fence_before();
                     mbar_arrive(bar(kOFree + (ob ^ 1)));     // the previous running result
@@ -1273,7 +1324,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     tmem_wait_ld();
                     tc_fence_before();
                     mbar_arrive(bar(kOFree + ob));       // O is in registers: its buffer is free
-                    store_half<D>(p, o, r0, rs, q4, I.rows_valid, I.q_start, I.kvh, I.split, R,
+                    store_half<D, STATS>(p, o, r0, rs, q4, I.rows_valid, I.q_start, I.kvh, I.split, R,
                                   I.kind == PA_ITEM_GROUP);
                 }
                 if (I.kind == PA_ITEM_GROUP) {
@@ -1314,12 +1365,12 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
 // as a programmatic dependent of the attention kernel (its launch overlaps the attention
 // tail); griddepcontrol.wait holds every thread until that grid has completed and its
 // writes are visible.
-template <int D>
+template <int D, bool STATS>
 __global__ void __launch_bounds__(256)
     combine_kernel(const float* __restrict__ ws_acc, const float* __restrict__ ws_ml,
                    const int32_t* __restrict__ cu, const int32_t* __restrict__ ctx, int32_t B,
                    int32_t T, int32_t Hq, int32_t max_splits, float c, float v_scale,
-                   __nv_bfloat16* __restrict__ out) {
+                   __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
     constexpr int kCols = 4;                  // columns per thread (one float4)
     constexpr int kUnits = D / kCols;         // threads per (row, q head)
     constexpr int kBatch = 8;                 // splits loaded ahead of their fold
@@ -1378,6 +1429,8 @@ __global__ void __launch_bounds__(256)
             M = mn;
         }
     }
+    if constexpr (STATS)
+        if (col == 0) lse[tok * Hq + head] = row_lse(M, Lsum, c);
     const float inv = __fmul_rn(__frcp_rn(Lsum), v_scale);
     __nv_bfloat16* dst = out + (tok * Hq + head) * D + col;
     *reinterpret_cast<uint2*>(dst) =
@@ -1435,24 +1488,25 @@ constexpr int kMaxDevices = 64;
 // Raises the kernel's dynamic shared-memory limit once per device. Several host threads (one
 // per GPU, say) may get here at once: the flags are atomic, and the attribute call is
 // idempotent, so two threads that both find a flag clear both set the same value.
-template <int D, bool F8>
+template <int D, bool F8, bool STATS>
 int32_t ensure_smem_attr(int dev) {
     static std::atomic<bool> raised[kMaxDevices];     // zero-initialised: not raised yet
     if (dev < 0 || dev >= kMaxDevices) return PA_ERR_INVALID;
     if (raised[dev].load(std::memory_order_acquire)) return PA_OK;
     const int32_t st = note_cuda(cudaFuncSetAttribute(
-        paged_attn_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kAlloc));
+        paged_attn_kernel<D, F8, STATS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        Layout<D>::kAlloc));
     if (st) return st;
     raised[dev].store(true, std::memory_order_release);
     return PA_OK;
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool STATS = false>
 int32_t launch(const Maps& maps, const Params& prm, int32_t max_ctx, cudaStream_t stream) {
     int dev = 0;
     int32_t st = note_cuda(cudaGetDevice(&dev));
     if (st) return st;
-    if ((st = ensure_smem_attr<D, F8>(dev))) return st;
+    if ((st = ensure_smem_attr<D, F8, STATS>(dev))) return st;
     const int grid = std::min(prm.n_items, PA_PLAN_CTAS);      // one CTA per list of the plan
     // Both kernels are programmatic dependents of what precedes them on the stream: each
     // launches while its predecessor drains and waits (griddepcontrol.wait) before it reads
@@ -1467,7 +1521,7 @@ int32_t launch(const Maps& maps, const Params& prm, int32_t max_ctx, cudaStream_
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    st = note_cuda(cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, F8>, maps.k, maps.v, maps.q1,
+    st = note_cuda(cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, F8, STATS>, maps.k, maps.v, maps.q1,
                                       maps.qn, prm));
     if (st) return st;
     if (max_ctx > kSplit) {
@@ -1475,9 +1529,10 @@ int32_t launch(const Maps& maps, const Params& prm, int32_t max_ctx, cudaStream_
         cfg.gridDim = dim3(unsigned((threads + 255) / 256));
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
-        st = note_cuda(cudaLaunchKernelEx(&cfg, combine_kernel<D>, (const float*)prm.ws_acc,
+        st = note_cuda(cudaLaunchKernelEx(&cfg, combine_kernel<D, STATS>, (const float*)prm.ws_acc,
                                           (const float*)prm.ws_ml, prm.cu, prm.ctx, prm.B, prm.T,
-                                          prm.Hq, prm.max_splits, prm.c, prm.v_scale, prm.out));
+                                          prm.Hq, prm.max_splits, prm.c, prm.v_scale, prm.out,
+                                          prm.lse));
     }
     return st;
 }
@@ -1522,6 +1577,9 @@ int32_t prepare_step(const void* q, const void* k_pool, const void* v_pool,
     prm->num_blocks = shape->num_blocks;
     prm->c = float(1.4426950408889634 / std::sqrt(double(D)));
     prm->v_scale = 1.f;
+    prm->lse = nullptr;
+    prm->scores = nullptr;
+    prm->scores_ld = 0;
     prm->never_ns = 0;
     return PA_OK;
 }
@@ -1617,6 +1675,73 @@ extern "C" int32_t paged_attention_step_fp8(const void* q, const void* k_pool, c
     prm.v_scale = v_scale;
     point_workspace(&prm, static_cast<float*>(workspace), T, shape->num_q_heads, shape->head_dim);
     return launch<128, true>(maps, prm, max_ctx, stream);
+}
+
+// The step with its rows' log-sum-exps and, where scores is given, the raw scores of its decode
+// rows: row (sequence s, q head h) at scores + (s * Hq + h) * scores_ld, one per key and -infinity
+// behind the row's last key up to the end of its tile. Same arithmetic and output bits as the
+// plain step.
+int32_t pa_detail::attention_step_stats(const void* q, const void* k_pool, const void* v_pool,
+                                        const int32_t* block_table, int32_t max_blocks,
+                                        const int32_t* cu_seqlens_q, const int32_t* ctx_lens,
+                                        int32_t B, int32_t T, int32_t max_ctx,
+                                        const pa_work_item* items, int32_t n_items, bool fp8,
+                                        float k_scale, float v_scale, void* workspace,
+                                        size_t ws_bytes, void* out, float* lse, float* scores,
+                                        int64_t scores_ld, const pa_shape* shape,
+                                        int32_t* err_flag, cudaStream_t stream) {
+    int32_t st = check_shape(shape);
+    if (st) return st;
+    if (fp8 && shape->head_dim != 128) return PA_ERR_SHAPE;
+    if (B < 0 || T < 0 || n_items < 0 || max_ctx < 0 || max_blocks < 0) return PA_ERR_INVALID;
+    if (fp8 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !(k_scale < INFINITY) ||
+                !(v_scale < INFINITY)))
+        return PA_ERR_INVALID;
+    if (T == 0 || n_items == 0) return PA_OK;
+    if (!lse) return PA_ERR_INVALID;
+    if (max_ctx > kSplit && (!workspace || ws_bytes < pa_workspace_bytes(shape, T, max_ctx)))
+        return PA_ERR_WORKSPACE;
+    if (max_ctx > kSplit && (reinterpret_cast<uintptr_t>(workspace) & 15)) return PA_ERR_INVALID;
+    Maps maps;
+    Params prm;
+    if ((st = prepare_step(q, k_pool, v_pool, block_table, max_blocks, cu_seqlens_q, ctx_lens, B,
+                           T, max_ctx, items, n_items, out, shape, err_flag, &maps, &prm, fp8)))
+        return st;
+    if (fp8) {
+        prm.c = prm.c * k_scale;
+        prm.v_scale = v_scale;
+    }
+    prm.lse = lse;
+    prm.scores = scores;
+    prm.scores_ld = scores_ld;
+    point_workspace(&prm, static_cast<float*>(workspace), T, shape->num_q_heads, shape->head_dim);
+    if (fp8) return launch<128, true, true>(maps, prm, max_ctx, stream);
+    if (shape->head_dim == 128) return launch<128, false, true>(maps, prm, max_ctx, stream);
+    return launch<64, false, true>(maps, prm, max_ctx, stream);
+}
+
+extern "C" int32_t paged_attention_step_lse(const void* q, const void* k_pool, const void* v_pool,
+                                            const int32_t* block_table, int32_t max_blocks,
+                                            const int32_t* cu_seqlens_q, const int32_t* ctx_lens,
+                                            int32_t B, int32_t T, int32_t max_ctx,
+                                            const pa_work_item* items, int32_t n_items,
+                                            void* workspace, size_t ws_bytes, void* out,
+                                            float* lse, const pa_shape* shape, int32_t* err_flag,
+                                            pa_stream_t stream) {
+    return attention_step_stats(q, k_pool, v_pool, block_table, max_blocks, cu_seqlens_q, ctx_lens,
+                                B, T, max_ctx, items, n_items, false, 1.f, 1.f, workspace,
+                                ws_bytes, out, lse, nullptr, 0, shape, err_flag, stream);
+}
+
+extern "C" int32_t paged_attention_step_fp8_lse(
+    const void* q, const void* k_pool, const void* v_pool, const int32_t* block_table,
+    int32_t max_blocks, const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t B,
+    int32_t T, int32_t max_ctx, const pa_work_item* items, int32_t n_items, float k_scale,
+    float v_scale, void* workspace, size_t ws_bytes, void* out, float* lse,
+    const pa_shape* shape, int32_t* err_flag, pa_stream_t stream) {
+    return attention_step_stats(q, k_pool, v_pool, block_table, max_blocks, cu_seqlens_q, ctx_lens,
+                                B, T, max_ctx, items, n_items, true, k_scale, v_scale, workspace,
+                                ws_bytes, out, lse, nullptr, 0, shape, err_flag, stream);
 }
 
 // ------------------------------------------- allocation-free variant of the attention step

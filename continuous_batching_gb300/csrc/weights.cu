@@ -96,6 +96,7 @@ struct Params {
     float* weights;              // [n_rows][Hkv][max_len]
     int32_t* err;
     int32_t B, T, max_blocks, Hq, Hkv, g, bs, num_blocks, n_rows, max_len;
+    int32_t skip_decode;         // sequences of one row are another kernel's
     float c;                     // log2(e) / sqrt(D), times the K scale of an fp8 cache
 };
 
@@ -137,7 +138,15 @@ __device__ __forceinline__ int tile_at(const Seq& q, int64_t x, int log2qt) {
     return t;
 }
 
-__device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt) {
+// Another sequence with query rows names sequence s's state row: both would race on it.
+__device__ __noinline__ bool shares_row(const int32_t* rows, const int32_t* cu, int B, int s) {
+    for (int i = 0; i < B; ++i)
+        if (i != s && rows[i] == rows[s] && cu[i + 1] != cu[i]) return true;
+    return false;
+}
+
+// repeated: some row is named twice (the sequences that do are then looked for).
+__device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt, bool repeated) {
     Seq q;
     const int c0 = p.cu[s], c1 = p.cu[s + 1];
     q.row = p.rows ? p.rows[s] : s;
@@ -145,13 +154,13 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt) {
     const int64_t n = int64_t(c1) - c0;
     q.bad = false;
     q.head_cost = 0;
-    if (n == 0 || q.row < 0) return q;
+    if (n == 0 || q.row < 0 || (p.skip_decode && n == 1)) return q;
     q.n_q = int(n);
     q.cu0 = c0;
     q.held = p.held ? p.held[s] : q.ctx - q.n_q;
     if (n < 0 || c0 < 0 || c1 > p.T || q.n_q > q.ctx || q.ctx > p.max_len ||
         (int64_t(q.ctx) + p.bs - 1) / p.bs > p.max_blocks || q.row >= p.n_rows || q.held < 0 ||
-        q.held > q.ctx) {
+        q.held > q.ctx || (repeated && shares_row(p.rows, p.cu, p.B, s))) {
         q.bad = true;
         return q;
     }
@@ -282,10 +291,9 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         }
         __syncthreads();
     }
-    // two sequences over one state row would race on it: the call then does nothing
-    const bool refused = *repeated != 0;
+    const bool twice = *repeated != 0;
     int64_t total = 0;
-    bool bad = refused;
+    bool bad = false;
     // inclusive sums over the sequences of one round of kThreads; returns the thread's own
     const auto round_scan = [&](int64_t x, int64_t& sum) {
 #pragma unroll
@@ -305,11 +313,11 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         return x + before;
     };
     int64_t mine = 0, upto = 0;
-    for (int s0 = 0; s0 < p.B && !refused; s0 += kThreads) {
+    for (int s0 = 0; s0 < p.B; s0 += kThreads) {
         const int s = s0 + int(threadIdx.x);
         mine = 0;
         if (s < p.B) {
-            const Seq q = load_seq(p, s, log2qt);
+            const Seq q = load_seq(p, s, log2qt, twice);
             mine = q.head_cost * p.Hkv;
             bad = bad || q.bad;
         }
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         int64_t run = 0;
         for (int s0 = 0; s0 < p.B && run <= lo; s0 += kThreads) {
             const int s = s0 + int(threadIdx.x);
-            mine = s < p.B ? load_seq(p, s, log2qt).head_cost * p.Hkv : 0;
+            mine = s < p.B ? load_seq(p, s, log2qt, twice).head_cost * p.Hkv : 0;
             int64_t sum;
             upto = round_scan(mine, sum) + run;
             if (mine > 0 && upto - mine <= lo && lo < upto) {
@@ -459,7 +467,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         };
         int64_t base = start_at;
         for (int s = start_s; s < p.B && base < hi && ok; ++s) {
-            const Seq q = load_seq(p, s, log2qt);
+            const Seq q = load_seq(p, s, log2qt, twice);
             if (q.head_cost == 0) continue;
             Item I;
             I.seq = s;
@@ -814,12 +822,71 @@ int32_t launch_weights(const CUtensorMap& k, const CUtensorMap& q1, const CUtens
     return note_cuda(cudaLaunchKernelEx(&cfg, attn_weights_kernel<D, F8>, k, q1, qn, p));
 }
 
+// ------------------------------------------------ decode rows of a step that kept their scores
+// One thread per four keys of a (sequence, KV head): the group's raw scores, stored by the
+// attention kernel, against the rows' log-sum-exps. A decode step so pays 4 g bytes per key and
+// KV head written and read again (in L2, mostly) in place of a second read of K's 2 D.
+constexpr int kDecodeKeys = 1024;      // per block of 256 threads
+__global__ void __launch_bounds__(256)
+    decode_weights_kernel(const float* __restrict__ scores, int64_t scores_ld, const Params p) {
+    __shared__ float nl[16];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int s = int(blockIdx.z), h = int(blockIdx.y);
+    const int c0 = p.cu[s], ctx = p.ctx[s];
+    const int row = p.rows ? p.rows[s] : s;
+    const int j0 = int(blockIdx.x) * kDecodeKeys;
+    if (p.cu[s + 1] - c0 != 1 || row < 0 || (j0 >= ctx && j0 > 0)) return;
+    const int held = p.held ? p.held[s] : ctx - 1;
+    bool bad = c0 < 0 || c0 >= p.T || ctx < 1 || ctx > p.max_len || ctx > scores_ld ||
+               (int64_t(ctx) + p.bs - 1) / p.bs > p.max_blocks || row >= p.n_rows || held < 0 ||
+               held > ctx;
+    if (p.rows)
+        for (int i = threadIdx.x; i < p.B; i += 256)
+            bad = bad || (i != s && p.rows[i] == row && p.cu[i + 1] != p.cu[i]);
+    if (threadIdx.x < p.g)
+        nl[threadIdx.x] = bad ? 0.f
+                              : -1.4426950408889634f *
+                                    p.lse[int64_t(c0) * p.Hq + h * p.g + threadIdx.x];
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0 && j0 == 0 && h == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+        return;
+    }
+    const int j = j0 + 4 * int(threadIdx.x);
+    if (j >= ctx) return;
+    // scores_ld is a multiple of 128: a thread's four lie within the row
+    const float* sc = scores + (int64_t(s) * p.Hq + h * p.g) * scores_ld + j;
+    float* w = p.weights + (int64_t(row) * p.Hkv + h) * p.max_len + j;
+    float sum[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = j + e < held ? w[e] : 0.f;
+    for (int i = 0; i < p.g; ++i) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(sc + int64_t(i) * scores_ld));
+        sum[0] += ex2(fmaf(x.x, p.c, nl[i]));
+        sum[1] += ex2(fmaf(x.y, p.c, nl[i]));
+        sum[2] += ex2(fmaf(x.z, p.c, nl[i]));
+        sum[3] += ex2(fmaf(x.w, p.c, nl[i]));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (j + e < ctx) w[e] = sum[e];
+}
+
+// Scores kept for a step: rows of a whole number of tiles.
+int64_t scores_row(int32_t max_ctx) {
+    return (int64_t(max_ctx) + kTileKeys - 1) / kTileKeys * kTileKeys;
+}
+size_t partials_bytes(const pa_shape* s, int32_t T, int32_t max_ctx) {
+    return (pa_workspace_bytes(s, T, max_ctx) + 255) & ~size_t(255);
+}
+
 int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
                           const int32_t* block_table, int32_t max_blocks, const int32_t* cu,
                           const int32_t* ctx, int32_t B, int32_t T, const int32_t* held,
                           const int32_t* rows, float* weights, int32_t n_rows, int32_t max_len,
                           bool fp8, float k_scale, const pa_shape* s, int32_t* err,
-                          cudaStream_t stream) {
+                          cudaStream_t stream, const float* scores = nullptr,
+                          int32_t max_ctx = 0) {
     int32_t st = check_shape(s);
     if (st) return st;
     if (fp8 && s->head_dim != 128) return PA_ERR_SHAPE;
@@ -860,6 +927,22 @@ int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
     p.n_rows = n_rows;
     p.max_len = max_len;
     p.c = float(1.4426950408889634 / std::sqrt(double(D))) * k_scale;
+    p.skip_decode = scores != nullptr;
+    if (scores) {
+        cudaLaunchAttribute pdl[1];
+        pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        pdl[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned((max_ctx + kDecodeKeys - 1) / kDecodeKeys), unsigned(p.Hkv),
+                           unsigned(B));
+        cfg.blockDim = dim3(256);
+        cfg.stream = stream;
+        cfg.attrs = pdl;
+        cfg.numAttrs = 1;
+        if ((st = note_cuda(cudaLaunchKernelEx(&cfg, decode_weights_kernel, scores,
+                                               scores_row(max_ctx), p))))
+            return st;
+    }
     if (fp8) return launch_weights<128, true>(k, q1, qn, p, stream);
     if (D == 128) return launch_weights<128, false>(k, q1, qn, p, stream);
     return launch_weights<64, false>(k, q1, qn, p, stream);
@@ -887,4 +970,77 @@ extern "C" int32_t paged_attention_weights_fp8(
     return attention_weights(q, k_pool, lse, block_table, max_blocks, cu_seqlens_q, ctx_lens, B, T,
                              held, rows, weights, n_rows, max_len, true, k_scale, shape, err_flag,
                              stream);
+}
+
+// ------------------------------------------------ the step of a bounded cache
+namespace {
+
+int32_t step_weights(const void* q, const void* k_pool, const void* v_pool,
+                     const int32_t* block_table, int32_t max_blocks, const int32_t* cu,
+                     const int32_t* ctx, int32_t B, int32_t T, int32_t max_ctx,
+                     const pa_work_item* items, int32_t n_items, bool fp8, float k_scale,
+                     float v_scale, void* workspace, size_t ws_bytes, void* out, float* lse,
+                     const int32_t* held, const int32_t* rows, float* weights, int32_t n_rows,
+                     int32_t max_len, const pa_shape* s, int32_t* err, cudaStream_t stream) {
+    int32_t st = check_shape(s);
+    if (st) return st;
+    if (B < 0 || T < 0 || n_items < 0 || max_ctx < 0) return PA_ERR_INVALID;
+    if (T == 0 || B == 0 || n_items == 0) return PA_OK;
+    // both halves' checks come before either launches
+    if (!q || !k_pool || !v_pool || !block_table || !cu || !ctx || !items || !out || !lse ||
+        !weights || max_len <= 0 || max_ctx == 0 || n_rows < 0 || (!rows && n_rows < B))
+        return PA_ERR_INVALID;
+    if (B > 65535 || s->num_kv_heads > 65535 || n_rows > kMaxRows ||
+        max_len > INT32_MAX - kTileKeys || max_ctx > INT32_MAX - kTileKeys ||
+        int64_t(s->num_blocks) * s->block_size > INT32_MAX)
+        return PA_ERR_SHAPE;
+    if (!workspace || ws_bytes < pa_step_weights_workspace_bytes(s, B, T, max_ctx))
+        return PA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 15) return PA_ERR_INVALID;
+    float* scores = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                             partials_bytes(s, T, max_ctx));
+    if ((st = attention_step_stats(q, k_pool, v_pool, block_table, max_blocks, cu, ctx, B, T,
+                                   max_ctx, items, n_items, fp8, k_scale, v_scale, workspace,
+                                   ws_bytes, out, lse, scores, scores_row(max_ctx), s, err,
+                                   stream)))
+        return st;
+    return attention_weights(q, k_pool, lse, block_table, max_blocks, cu, ctx, B, T, held, rows,
+                             weights, n_rows, max_len, fp8, k_scale, s, err, stream, scores,
+                             max_ctx);
+}
+
+}  // namespace
+
+extern "C" size_t pa_step_weights_workspace_bytes(const pa_shape* shape, int32_t B, int32_t T,
+                                                  int32_t max_ctx) {
+    if (check_shape(shape) || B < 0 || T < 0 || max_ctx < 0) return 0;
+    return partials_bytes(shape, T, max_ctx) +
+           size_t(B) * shape->num_q_heads * size_t(scores_row(max_ctx)) * sizeof(float);
+}
+
+extern "C" int32_t paged_attention_step_weights(
+    const void* q, const void* k_pool, const void* v_pool, const int32_t* block_table,
+    int32_t max_blocks, const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t B,
+    int32_t T, int32_t max_ctx, const pa_work_item* items, int32_t n_items, void* workspace,
+    size_t ws_bytes, void* out, float* lse, const int32_t* held, const int32_t* rows,
+    float* weights, int32_t n_rows, int32_t max_len, const pa_shape* shape, int32_t* err_flag,
+    pa_stream_t stream) {
+    return step_weights(q, k_pool, v_pool, block_table, max_blocks, cu_seqlens_q, ctx_lens, B, T,
+                        max_ctx, items, n_items, false, 1.f, 1.f, workspace, ws_bytes, out, lse,
+                        held, rows, weights, n_rows, max_len, shape, err_flag, stream);
+}
+
+extern "C" int32_t paged_attention_step_weights_fp8(
+    const void* q, const void* k_pool, const void* v_pool, const int32_t* block_table,
+    int32_t max_blocks, const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t B,
+    int32_t T, int32_t max_ctx, const pa_work_item* items, int32_t n_items, float k_scale,
+    float v_scale, void* workspace, size_t ws_bytes, void* out, float* lse, const int32_t* held,
+    const int32_t* rows, float* weights, int32_t n_rows, int32_t max_len, const pa_shape* shape,
+    int32_t* err_flag, pa_stream_t stream) {
+    if (!(k_scale > 0.f) || !(v_scale > 0.f) || !(k_scale < INFINITY) || !(v_scale < INFINITY))
+        return PA_ERR_INVALID;
+    if (shape && shape->head_dim != 128) return PA_ERR_SHAPE;
+    return step_weights(q, k_pool, v_pool, block_table, max_blocks, cu_seqlens_q, ctx_lens, B, T,
+                        max_ctx, items, n_items, true, k_scale, v_scale, workspace, ws_bytes, out,
+                        lse, held, rows, weights, n_rows, max_len, shape, err_flag, stream);
 }

@@ -546,9 +546,8 @@ int32_t paged_qk_norm_rope_write_fp8(const void* q, int64_t q_stride, const void
  * Device inputs: q [T, Hq, D] bf16; k_pool as in paged_attention_step; lse [T, Hq] fp32;
  * block_table [B, max_blocks], cu_seqlens_q [B+1], ctx_lens [B], held [B] or NULL, rows [B] or
  * NULL int32. A sequence whose metadata does not fit (n_q > ctx, ctx > max_len or the table, held
- * outside [0, ctx], a row >= n_rows) is skipped and sets PA_DEVERR_META; if two sequences with
- * query rows name one state row, the whole call does nothing and sets it. Weights whose lse or q
- * is NaN are NaN.
+ * outside [0, ctx], a row >= n_rows or named by another sequence with query rows) is skipped and
+ * sets PA_DEVERR_META. Weights whose lse or q is NaN are NaN.
  * Host checks: as paged_attention_step; n_rows <= 2^18; n_rows >= B without rows. One launch, a
  * programmatic dependent of what precedes it, no workspace, nothing planned on the host: a captured
  * call follows its metadata. */
@@ -566,6 +565,55 @@ int32_t paged_attention_weights_fp8(const void* q, const void* k_pool, const flo
                                     const int32_t* rows, float* weights, int32_t n_rows,
                                     int32_t max_len, float k_scale, const pa_shape* shape,
                                     int32_t* err_flag, pa_stream_t stream);
+
+/* The step that also gives every row's log-sum-exp (natural logarithm) of its scaled scores:
+ * paged_attention_step with lse [T, Hq] fp32 (device) behind out; rows not covered by items are
+ * not written. out has the same bits. */
+int32_t paged_attention_step_lse(const void* q, const void* k_pool, const void* v_pool,
+                                 const int32_t* block_table, int32_t max_blocks,
+                                 const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t B,
+                                 int32_t T, int32_t max_ctx, const pa_work_item* items,
+                                 int32_t n_items, void* workspace, size_t ws_bytes, void* out,
+                                 float* lse, const pa_shape* shape, int32_t* err_flag,
+                                 pa_stream_t stream);
+int32_t paged_attention_step_fp8_lse(const void* q, const void* k_pool, const void* v_pool,
+                                     const int32_t* block_table, int32_t max_blocks,
+                                     const int32_t* cu_seqlens_q, const int32_t* ctx_lens,
+                                     int32_t B, int32_t T, int32_t max_ctx,
+                                     const pa_work_item* items, int32_t n_items, float k_scale,
+                                     float v_scale, void* workspace, size_t ws_bytes, void* out,
+                                     float* lse, const pa_shape* shape, int32_t* err_flag,
+                                     pa_stream_t stream);
+
+/* The step of a bounded cache: paged_attention_step_lse, and paged_attention_weights of its rows
+ * in the same call. A decode row's raw scores are kept in the workspace while its keys are in
+ * hand, so that K is read once for both; the keys of longer chunks are read again. Every row of the
+ * step must be covered by items (a plan of pa_plan_step or pa_plan_step_shared covers them).
+ * workspace: at least pa_step_weights_workspace_bytes(shape, B, T, max_ctx) bytes, 16-byte aligned,
+ * always needed; it holds B * Hq * max_ctx scores beside the split partials, and nothing between
+ * calls. max_ctx >= every ctx_lens[s] (a longer decode sequence adds nothing and sets
+ * PA_DEVERR_META). Other arguments, state and errors as in the two. B <= 65535. */
+size_t pa_step_weights_workspace_bytes(const pa_shape* shape, int32_t B, int32_t T,
+                                       int32_t max_ctx);
+int32_t paged_attention_step_weights(const void* q, const void* k_pool, const void* v_pool,
+                                     const int32_t* block_table, int32_t max_blocks,
+                                     const int32_t* cu_seqlens_q, const int32_t* ctx_lens,
+                                     int32_t B, int32_t T, int32_t max_ctx,
+                                     const pa_work_item* items, int32_t n_items, void* workspace,
+                                     size_t ws_bytes, void* out, float* lse, const int32_t* held,
+                                     const int32_t* rows, float* weights, int32_t n_rows,
+                                     int32_t max_len, const pa_shape* shape, int32_t* err_flag,
+                                     pa_stream_t stream);
+int32_t paged_attention_step_weights_fp8(const void* q, const void* k_pool, const void* v_pool,
+                                         const int32_t* block_table, int32_t max_blocks,
+                                         const int32_t* cu_seqlens_q, const int32_t* ctx_lens,
+                                         int32_t B, int32_t T, int32_t max_ctx,
+                                         const pa_work_item* items, int32_t n_items,
+                                         float k_scale, float v_scale, void* workspace,
+                                         size_t ws_bytes, void* out, float* lse,
+                                         const int32_t* held, const int32_t* rows, float* weights,
+                                         int32_t n_rows, int32_t max_len, const pa_shape* shape,
+                                         int32_t* err_flag, pa_stream_t stream);
 
 /* ------------------------------------------------------------------------- eviction
  * Cuts every sequence's cache to a budget, per KV head, by accumulated attention weight

@@ -241,7 +241,7 @@ def test_bad_metadata_is_skipped_and_flagged():
     assert run(ctx=[40, 50, 70], max_len=128) == ([True, True, False], bd.PA_DEVERR_META)  # behind the table
     assert run(cu=[0, 1, 2, 9]) == ([True, True, False], bd.PA_DEVERR_META)         # behind T
     assert run(rows=[0, 3, 2]) == ([True, False, True], bd.PA_DEVERR_META)
-    assert run(rows=[0, 2, 2]) == ([False] * 3, bd.PA_DEVERR_META)                  # one row twice
+    assert run(rows=[1, 2, 2]) == ([False, True, False], bd.PA_DEVERR_META)         # one row twice
     assert run(rows=[0, -5, 2]) == ([True, False, True], 0)
     assert run(held=[40, 51, -1]) == ([True, False, False], bd.PA_DEVERR_META)
     table = st.block_table.copy()
@@ -285,3 +285,124 @@ def test_streams_and_a_graph_that_follows_its_metadata():
     w.zero_()
     graph.replay()
     assert torch.equal(w, direct) and not torch.equal(direct, want)
+
+
+# ------------------------------------------------------------------ the step that keeps them (GPU)
+
+def _step_case(st, fp8=False, shared=False, seed=0):
+    """paged_attention_step_lse and _weights of a step: outputs with the plain step's bits, the
+    definition's log-sum-exps and weights."""
+    rng = np.random.default_rng(seed)
+    B, g = len(st.ctx_lens), st.Hq // st.Hkv
+    shape = bd.Shape.make(st.Hq, st.Hkv, st.D, st.block_size, st.num_blocks)
+    q = pa.bf16_to_f64(st.q)
+    scales = (0.0125, 0.02) if fp8 else ()
+    if fp8:
+        codes = ofp8.quantize(st.k_pool, scales[0])
+        k, kp, vp = ofp8.dequantize(codes, scales[0]), dev(codes), dev(ofp8.quantize(st.v_pool, scales[1]))
+    else:
+        k = pa.bf16_to_f64(st.k_pool)
+        kp, vp = (dev(x.view(np.int16), torch.bfloat16) for x in (st.k_pool, st.v_pool))
+    plan = bd.pa_plan_step_shared(shape, st.cu_seqlens_q, st.ctx_lens, st.block_table) if shared else \
+        bd.pa_plan_step(shape, st.cu_seqlens_q, st.ctx_lens)
+    items = dev(plan.view(np.int32).reshape(-1))
+    max_ctx = int(st.ctx_lens.max())
+    qd, table, cu, ctx = dev(st.q.view(np.int16), torch.bfloat16), dev(st.block_table), dev(st.cu_seqlens_q), dev(st.ctx_lens)
+    nan = lambda *s, dtype=torch.float32: torch.full(s, float("nan"), dtype=dtype, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = nan(bd.pa_workspace_bytes(shape, st.T, max_ctx) // 4 + 1)
+    want_out, out, out2 = (nan(st.T, st.Hq, st.D, dtype=torch.bfloat16) for _ in range(3))
+    pre = (qd, kp, vp, table, cu, ctx, max_ctx, items, *scales)
+    s8 = "_fp8" if fp8 else ""
+    getattr(bd, "paged_attention_step" + s8)(*pre, ws, want_out, shape, err)
+    lse = nan(st.T, st.Hq)
+    getattr(bd, "paged_attention_step" + s8 + "_lse")(*pre, ws, out, lse, shape, err)
+    want_lse, want = lse_and_weights(q, k, st.block_table, st.cu_seqlens_q, st.ctx_lens)
+    got_lse = lse.cpu().numpy()
+    tol = tolerance(q, k, st.D, want_lse, st.T * g) + 16 * 2.0 ** -24
+    # the sum's relative error is the logarithm's absolute one; then two roundings of lse's size
+    assert np.all(np.abs(got_lse - want_lse) <= tol + 2.0 ** -22 * np.maximum(np.abs(want_lse), 1))
+    bits = lambda t: t.view(torch.int16)
+    assert torch.equal(bits(out), bits(want_out))
+    rows = rng.permutation(B + 2)[:B].astype(np.int32)
+    start = rng.random((B + 2, st.Hkv, max_ctx + 5)).astype(np.float32)
+    w = dev(start.copy())
+    ws2 = nan((bd.pa_step_weights_workspace_bytes(shape, B, st.T, max_ctx) + 3) // 4)
+    lse2 = nan(st.T, st.Hq)
+    step = lambda: getattr(bd, "paged_attention_step_weights" + s8)(*pre, ws2, out2, lse2, dev(rows), w, shape, err=err)
+    step()
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert torch.equal(bits(out2), bits(want_out)) and torch.equal(lse2, lse)
+    got = w.cpu().numpy()
+    expect = start.astype(np.float64)
+    for s in range(B):
+        n, c, r = int(st.n_q[s]), int(st.ctx_lens[s]), rows[s]
+        if n == 0:
+            continue
+        expect[r, :, c - n:c] = 0
+        expect[r, :, :c] += want[s]
+        d = np.abs(got[r, :, :c] - expect[r, :, :c])
+        # the kernel's own lse stands in: its error is the weights' as well
+        assert np.all(d <= 3 * tol * want[s] + 2.0 ** -24 * expect[r, :, :c] + 1e-37), s
+        expect[r, :, :c] = got[r, :, :c]
+    assert np.array_equal(got, expect.astype(np.float32))
+    # against paged_attention_weights from the same log-sum-exps
+    w2 = dev(start.copy())
+    getattr(bd, "paged_attention_weights" + s8)(qd, kp, lse, table, cu, ctx, dev(rows), w2, *scales[:1], shape)
+    np.testing.assert_allclose(w2.cpu().numpy(), got, rtol=1e-5, atol=1e-7)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq, Hkv, D, bs", SHAPES)
+@pytest.mark.parametrize("ctx, n_q", [
+    ([1], [1]), ([17, 128, 64, 100], [1, 1, 1, 1]), ([2049, 2048, 4500], [1, 1, 1]),
+    ([140, 300, 2100], [140, 257, 33]), ([700, 20, 129, 64, 2500], [130, 1, 129, 0, 1]),
+])
+def test_step_against_the_definition(Hq, Hkv, D, bs, ctx, n_q):
+    _step_case(wl.make_step(Hq, Hkv, D, bs, ctx, n_q, seed=len(ctx) + D))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq, Hkv, bs", [(32, 8, 16), (8, 8, 32), (16, 1, 128)])
+@pytest.mark.parametrize("ctx, n_q", [([17, 128, 64, 3000], [1, 1, 1, 1]), ([700, 20, 2129], [130, 1, 129])])
+def test_fp8_step_against_the_definition(Hq, Hkv, bs, ctx, n_q):
+    _step_case(wl.make_step(Hq, Hkv, 128, bs, ctx, n_q, seed=5), fp8=True)
+
+
+@pytest.mark.gpu
+def test_step_with_shared_prefixes():
+    """Rows of GROUP and RESUME items keep their scores as well (each under its own sequence)."""
+    for Hq, D in ((8, 64), (32, 128)):
+        _step_case(wl.make_prefix_step(Hq, 8, D, 16, prompts=2, samples=5, prompt_tokens=640, cont_max=900, seed=2),
+                   shared=True)
+    _step_case(wl.make_prefix_step(32, 8, 128, 16, prompts=2, samples=3, prompt_tokens=640, cont_max=2500, seed=3),
+               fp8=True, shared=True)
+
+
+@pytest.mark.gpu
+def test_step_refusals_and_contexts_behind_the_bound():
+    st = wl.make_step(4, 2, 64, 16, [40, 150, 60], [1, 1, 1], seed=8)
+    shape = bd.Shape.make(st.Hq, st.Hkv, st.D, st.block_size, st.num_blocks)
+    q, kp, vp = (dev(x.view(np.int16), torch.bfloat16) for x in (st.q, st.k_pool, st.v_pool))
+    items = dev(bd.pa_plan_step(shape, st.cu_seqlens_q, st.ctx_lens).view(np.int32).reshape(-1))
+    out, lse = torch.empty(3, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 4, device="cuda")
+    need = bd.pa_step_weights_workspace_bytes(shape, 3, 3, 160) // 4
+
+    def run(max_ctx=160, ws=need, max_len=160, rows=(0, 1, 2), n=3):
+        w = torch.full((n, 2, max_len), -1.0, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        bd.paged_attention_step_weights(q, kp, vp, dev(st.block_table), dev(st.cu_seqlens_q), dev(st.ctx_lens), max_ctx,
+                                        items, None if ws is None else torch.empty(ws, device="cuda"), out, lse,
+                                        torch.tensor(rows, dtype=torch.int32, device="cuda"), w, shape, err=err)
+        return [bool((w[s] != -1).any()) for s in range(n)], int(err.item())
+
+    assert run() == ([True] * 3, 0)
+    for bad in (dict(ws=None), dict(ws=need - 1), dict(max_ctx=0)):
+        with pytest.raises(bd.PagedAttnError):
+            run(**bad)
+    # sequence 1 is longer than the bound the caller gave: its scores have no room, it adds nothing
+    assert run(max_ctx=100) == ([True, False, True], bd.PA_DEVERR_META)
+    assert run(max_len=100) == ([True, False, True], bd.PA_DEVERR_META)
+    assert run(rows=(0, 2, 2)) == ([True, False, False], bd.PA_DEVERR_META)
+    assert run(rows=(0, -1, 2)) == ([True, False, True], 0)
