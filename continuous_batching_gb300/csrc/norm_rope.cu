@@ -10,29 +10,33 @@
 // Angles. A pair's frequency is held as turns per position in units of 2^-64 turn
 // (pa_rope_pair.step), so position * step in 64-bit integers, wrapping, IS the phase modulo one
 // turn, exactly, for positions of any size and sign: nothing is lost to range reduction. Its top
-// 32 bits go to fp32 (2^-25 of half a turn) and sincospif. The sines are computed once per token
-// and shared by its heads through shared memory; reading them from a table instead would read
-// 8 bytes a pair and token from memory, against none here.
+// 32 bits go to fp32 (2^-25 of half a turn) and sincospif. Reading the sines from a table instead
+// would read 8 bytes a pair and token from memory, against none here.
 //
 // Bound by memory: (Hq + 2 Hkv) D read and written per token. D / 8 lanes hold a head, each lane
 // the elements of four pairs (two 8-byte pieces r/2 apart, or one of 16 bytes for adjacent
 // pairs), so a pair never crosses lanes and the norm is the only exchange (log2(D / 8) shuffles).
-// A group of lanes loads up to kUnits heads before it waits for the sines.
+// A warp takes some rounds of one token's heads, all of one kind at a time, so its lanes' four sines
+// (each lane computes its share and gets the rest from its neighbours) and the products of weights
+// and sines serve them from registers and nothing is shared between warps. What it costs beyond
+// memory is instructions: per head, 4 shuffles and some 50 others, the arithmetic in packed pairs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.h"
+#include "sm103.h"
 
 using namespace pa_detail;
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;          // heads a lane group has in flight
-constexpr int kMaxTokens = 8;      // tokens per CTA
+constexpr int kUnits = 2;          // heads a lane group has in flight
+constexpr int kMaxRounds = 24;     // heads a lane group takes, where there are tokens enough
 
 struct RopeParams {
     const __nv_bfloat16 *q, *k, *v, *wq, *wk;
@@ -44,17 +48,13 @@ struct RopeParams {
     void *k_pool, *v_pool;
     int64_t num_slots;
     int32_t* err;
-    int32_t T, Hq, Hkv, n_pairs, n_axes, tokens;
+    int32_t T, Hq, Hkv, n_pairs, n_axes;
+    int32_t warps;                             // per token
     float eps, k_scale, v_scale;
 };
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
 
 // Four values -> four codes e4m3(x / s): the same division and rounding as paged_kv_write_fp8,
 // from the fp32 value, so that a K element is rounded once.
@@ -67,180 +67,221 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* x, float s) {
     return uint32_t(a) | (uint32_t(b) << 16);
 }
 
+enum Kind { kQ, kK, kV };
+
 template <int D, bool INTER, bool F8>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeParams p) {
     constexpr int kLanes = D / 8;              // lanes per head
-    constexpr int kGroups = kThreads / kLanes;
-    __shared__ float2 trig[kMaxTokens][D / 2]; // (cos, sin) of a token's pairs
+    constexpr int kHeads = 32 / kLanes;        // heads a warp has at a time: a round
     // the attention kernel that follows waits for this grid before it reads anything; this one
     // in turn waits for what came before it
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    const int heads = p.Hq + 2 * p.Hkv;
-    const int t0 = int(blockIdx.x) * p.tokens;
-    const int nt = min(p.tokens, p.T - t0);
-    const int total = nt * heads;
+    const int64_t wid = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t = wid / p.warps;
+    if (t >= p.T) return;
+    const int part = int(wid - t * p.warps);
+    const int sub = (threadIdx.x & 31) / kLanes;
     const int l = threadIdx.x % kLanes;
-    const int group = threadIdx.x / kLanes;
-    const int n_rot = p.n_pairs / 4;           // lanes whose elements rotate
-    const bool turns = l < n_rot;
+    const bool turns = l < p.n_pairs / 4;      // the lane's elements rotate
     // the lane's two four-element pieces: adjacent pairs lie in one 16-byte piece
     const int a = INTER ? 8 * l : turns ? 4 * l : 8 * l;
     const int b = INTER ? 8 * l + 4 : turns ? p.n_pairs + 4 * l : 8 * l + 4;
 
-    for (int u0 = group; u0 - group < total; u0 += kGroups * kUnits) {
-        uint2 xa[kUnits], xb[kUnits];
-        int tok[kUnits], head[kUnits];
+    const int32_t slot = p.slots[t];
+    const bool writes = slot >= 0 && slot < p.num_slots;
+    if (slot >= p.num_slots && part == 0 && (threadIdx.x & 31) == 0 && p.err)
+        atomicOr(p.err, PA_DEVERR_SLOT);
+
+    float co[4], si[4];                        // of the lane's pairs
+    bool have = false;
+    const auto sines = [&]() {
+        have = true;
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int u = u0 + i * kGroups;
-            tok[i] = u < total ? u / heads : -1;
-            head[i] = u - tok[i] * heads;
-            if (tok[i] < 0) continue;
-            const int64_t t = t0 + tok[i];
-            const int h = head[i];
-            const __nv_bfloat16* src =
-                h < p.Hq           ? p.q + t * p.q_stride + h * D
-                : h < p.Hq + p.Hkv ? p.k + t * p.k_stride + (h - p.Hq) * D
-                                   : p.v + t * p.v_stride + (h - p.Hq - p.Hkv) * D;
-            if constexpr (INTER) {
-                const uint4 w = *reinterpret_cast<const uint4*>(src + a);
-                xa[i] = make_uint2(w.x, w.y);
-                xb[i] = make_uint2(w.z, w.w);
-            } else {
-                xa[i] = *reinterpret_cast<const uint2*>(src + a);
-                xb[i] = *reinterpret_cast<const uint2*>(src + b);
-            }
-        }
-        if (u0 == group) {
-            for (int e = threadIdx.x; e < nt * p.n_pairs; e += kThreads) {
-                const int t = e / p.n_pairs, i = e - t * p.n_pairs;
-                const pa_rope_pair f = p.rope[i];
+        for (int e = 0; e < 4; ++e) co[e] = 1.f, si[e] = 0.f;
+        // a pair's lanes in the warp's lane groups share its sines: each computes 4 / kHeads
+#pragma unroll
+        for (int k = 0; k < 4 / kHeads; ++k) {
+            const int e = k * kHeads + sub;
+            float c = 1.f, s = 0.f;
+            if (turns) {
+                const pa_rope_pair f = p.rope[4 * l + e];
                 int axis = f.axis;
                 if (axis < 0 || axis >= p.n_axes) {
                     if (p.err) atomicOr(p.err, PA_DEVERR_META);
                     axis = 0;
                 }
-                const int64_t pos = p.positions[int64_t(axis) * p.T + t0 + t];
+                const int64_t pos = p.positions[int64_t(axis) * p.T + t];
                 const uint64_t phase = uint64_t(pos) * f.step;
-                float s, c;
                 sincospif(float(int32_t(phase >> 32)) * 0x1p-31f, &s, &c);
-                trig[t][i] = make_float2(c, s);
             }
-            __syncthreads();
+#pragma unroll
+            for (int g = 0; g < kHeads; ++g) {
+                co[k * kHeads + g] = __shfl_sync(0xffffffffu, c, g * kLanes + l);
+                si[k * kHeads + g] = __shfl_sync(0xffffffffu, s, g * kLanes + l);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            // a group's lanes agree on the unit, but a warp holds several groups
-            const bool on = tok[i] >= 0;
-            const int h = head[i];
-            const bool is_v = h >= p.Hq + p.Hkv;
-            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (on) {
-                x[0] = lo16(xa[i].x);
-                x[1] = hi16(xa[i].x);
-                x[2] = lo16(xa[i].y);
-                x[3] = hi16(xa[i].y);
-                x[4] = lo16(xb[i].x);
-                x[5] = hi16(xb[i].x);
-                x[6] = lo16(xb[i].y);
-                x[7] = hi16(xb[i].y);
+    };
+
+    // rounds r0 .. r1 - 1 of one kind's heads
+    const auto run = [&](auto kind, const __nv_bfloat16* src, const __nv_bfloat16* weight, int heads,
+                         int r0, int r1) {
+        constexpr Kind K = decltype(kind)::value;
+        if (r0 >= r1 || (K != kQ && !writes)) return;
+        src += sub * D;
+        const auto load = [&](int r, uint2& xa, uint2& xb) {
+            if (r >= r1 || r * kHeads + sub >= heads) return;
+            const __nv_bfloat16* s = src + r * (kHeads * D);
+            if constexpr (INTER) {
+                const uint4 w = *reinterpret_cast<const uint4*>(s + a);
+                xa = make_uint2(w.x, w.y);
+                xb = make_uint2(w.z, w.w);
+            } else {
+                xa = *reinterpret_cast<const uint2*>(s + a);
+                xb = *reinterpret_cast<const uint2*>(s + b);
             }
-            float ss = 0.f;
+        };
+        uint2 xa[kUnits] = {}, xb[kUnits] = {};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+        for (int i = 0; i < kUnits; ++i) load(r0 + i, xa[i], xb[i]);
+        // With weights (wu, wv) of a pair's elements: (u, v) -> r (u wu c - v wv s, u wu s + v wv c),
+        // r the norm's factor (c = 1, s = 0 in lanes that do not turn).
+        uint64_t uc[2], us[2], vc[2], vs[2];
+        const bool norm = K != kV && weight;
+        if constexpr (K != kV) {
+            if (!have) sines();
+            float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+            if (weight) {
+                const uint2 wa = __ldg(reinterpret_cast<const uint2*>(weight + a));
+                const uint2 wb = __ldg(reinterpret_cast<const uint2*>(weight + b));
+                w[0] = lo16(wa.x), w[1] = hi16(wa.x), w[2] = lo16(wa.y), w[3] = hi16(wa.y);
+                w[4] = lo16(wb.x), w[5] = hi16(wb.x), w[6] = lo16(wb.y), w[7] = hi16(wb.y);
+            }
 #pragma unroll
-            for (int m = kLanes / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-            if (!on) continue;
-            if (!is_v) {
-                const __nv_bfloat16* w = h < p.Hq ? p.wq : p.wk;
-                if (w) {
-                    const float r = rsqrtf(ss * (1.f / D) + p.eps);
-                    const uint2 wa = __ldg(reinterpret_cast<const uint2*>(w + a));
-                    const uint2 wb = __ldg(reinterpret_cast<const uint2*>(w + b));
-                    x[0] *= r * lo16(wa.x);
-                    x[1] *= r * hi16(wa.x);
-                    x[2] *= r * lo16(wa.y);
-                    x[3] *= r * hi16(wa.y);
-                    x[4] *= r * lo16(wb.x);
-                    x[5] *= r * hi16(wb.x);
-                    x[6] *= r * lo16(wb.y);
-                    x[7] *= r * hi16(wb.y);
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * e, j = 2 * e + 1;
+                const float wui = INTER ? w[2 * i] : w[i], wvi = INTER ? w[2 * i + 1] : w[4 + i];
+                const float wuj = INTER ? w[2 * j] : w[j], wvj = INTER ? w[2 * j + 1] : w[4 + j];
+                uc[e] = f2(wui * co[i], wuj * co[j]);
+                us[e] = f2(wui * si[i], wuj * si[j]);
+                vc[e] = f2(wvi * co[i], wvj * co[j]);
+                vs[e] = f2(-wvi * si[i], -wvj * si[j]);
+            }
+        }
+        const int64_t row = K == kQ ? t * p.Hq : int64_t(slot) * p.Hkv;
+#pragma unroll 1
+        for (int rb = r0; rb < r1; rb += kUnits) {
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const int r = rb + i;
+                if (r >= r1) break;
+                const int h = r * kHeads + sub;
+                uint2 ya = xa[i], yb = xb[i];
+                load(r + kUnits, xa[i], xb[i]);
+                float x[8];
+                if (K != kV || F8) {
+                    x[0] = lo16(ya.x), x[1] = hi16(ya.x), x[2] = lo16(ya.y), x[3] = hi16(ya.y);
+                    x[4] = lo16(yb.x), x[5] = hi16(yb.x), x[6] = lo16(yb.y), x[7] = hi16(yb.y);
                 }
-                if (turns) {
+                if constexpr (K != kV) {
+                    uint64_t u[2], v[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 cs = trig[tok[i]][4 * l + e];
-                        float& u = INTER ? x[2 * e] : x[e];
-                        float& v = INTER ? x[2 * e + 1] : x[4 + e];
-                        const float nu = u * cs.x - v * cs.y;
-                        v = u * cs.y + v * cs.x;
-                        u = nu;
+                    for (int e = 0; e < 2; ++e) {
+                        u[e] = INTER ? f2(x[4 * e], x[4 * e + 2]) : f2(x[2 * e], x[2 * e + 1]);
+                        v[e] = INTER ? f2(x[4 * e + 1], x[4 * e + 3])
+                                     : f2(x[4 + 2 * e], x[5 + 2 * e]);
+                    }
+                    uint64_t q2 = mul2(u[0], u[0]);
+                    q2 = fma2(u[1], u[1], q2);
+                    q2 = fma2(v[0], v[0], q2);
+                    q2 = fma2(v[1], v[1], q2);
+                    float f = 1.f;
+                    if (norm) {
+                        float s0, s1;
+                        f2_split(q2, s0, s1);
+                        float ss = s0 + s1;
+#pragma unroll
+                        for (int m = kLanes / 2; m; m >>= 1)
+                            ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                        f = rsqrtf(ss * (1.f / D) + p.eps);
+                    }
+                    const uint64_t ff = f2(f, f);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        u[e] = mul2(u[e], ff);
+                        v[e] = mul2(v[e], ff);
+                        uint64_t nu = mul2(u[e], uc[e]), nv = mul2(v[e], vc[e]);
+                        if (turns) {                   // else the other's infinity would leak in
+                            nu = fma2(v[e], vs[e], nu);
+                            nv = fma2(u[e], us[e], nv);
+                        }
+                        float u0, u1, v0, v1;
+                        f2_split(nu, u0, u1);
+                        f2_split(nv, v0, v1);
+                        if constexpr (INTER) {
+                            x[4 * e] = u0, x[4 * e + 1] = v0, x[4 * e + 2] = u1, x[4 * e + 3] = v1;
+                        } else {
+                            x[2 * e] = u0, x[2 * e + 1] = u1, x[4 + 2 * e] = v0, x[5 + 2 * e] = v1;
+                        }
+                    }
+                    if (!F8 || K == kQ) {
+                        ya = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+                        yb = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                    }
+                }
+                if (h >= heads) continue;
+                const int64_t at = (row + h) * D;
+                if constexpr (F8 && K != kQ) {
+                    uint8_t* dst = static_cast<uint8_t*>(K == kV ? p.v_pool : p.k_pool) + at;
+                    const float s = K == kV ? p.v_scale : p.k_scale;
+                    const uint32_t ca = e4m3x4(x, s), cb = e4m3x4(x + 4, s);
+                    if constexpr (INTER) {
+                        *reinterpret_cast<uint2*>(dst + a) = make_uint2(ca, cb);
+                    } else {
+                        *reinterpret_cast<uint32_t*>(dst + a) = ca;
+                        *reinterpret_cast<uint32_t*>(dst + b) = cb;
+                    }
+                } else {
+                    __nv_bfloat16* dst =
+                        (K == kQ ? p.q_out : static_cast<__nv_bfloat16*>(K == kV ? p.v_pool
+                                                                                 : p.k_pool)) + at;
+                    if constexpr (INTER) {
+                        *reinterpret_cast<uint4*>(dst + a) = make_uint4(ya.x, ya.y, yb.x, yb.y);
+                    } else {
+                        *reinterpret_cast<uint2*>(dst + a) = ya;
+                        *reinterpret_cast<uint2*>(dst + b) = yb;
                     }
                 }
             }
-            const int64_t t = t0 + tok[i];
-            if (h < p.Hq) {
-                __nv_bfloat16* dst = p.q_out + (t * p.Hq + h) * D;
-                const uint2 ya = make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
-                const uint2 yb = make_uint2(bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
-                if constexpr (INTER) {
-                    *reinterpret_cast<uint4*>(dst + a) = make_uint4(ya.x, ya.y, yb.x, yb.y);
-                } else {
-                    *reinterpret_cast<uint2*>(dst + a) = ya;
-                    *reinterpret_cast<uint2*>(dst + b) = yb;
-                }
-                continue;
-            }
-            const int32_t slot = p.slots[t];
-            if (slot < 0) continue;                       // "no write" marker
-            if (slot >= p.num_slots) {
-                if (l == 0 && p.err) atomicOr(p.err, PA_DEVERR_SLOT);
-                continue;
-            }
-            const int kvh = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-            const int64_t at = (int64_t(slot) * p.Hkv + kvh) * D;
-            if constexpr (F8) {
-                uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_pool : p.k_pool) + at;
-                const float s = is_v ? p.v_scale : p.k_scale;
-                const uint32_t ya = e4m3x4(x, s), yb = e4m3x4(x + 4, s);
-                if constexpr (INTER) {
-                    *reinterpret_cast<uint2*>(dst + a) = make_uint2(ya, yb);
-                } else {
-                    *reinterpret_cast<uint32_t*>(dst + a) = ya;
-                    *reinterpret_cast<uint32_t*>(dst + b) = yb;
-                }
-            } else {
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.v_pool : p.k_pool) + at;
-                // v goes through unchanged: its bits, not a round trip
-                const uint2 ya = is_v ? xa[i] : make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
-                const uint2 yb = is_v ? xb[i] : make_uint2(bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
-                if constexpr (INTER) {
-                    *reinterpret_cast<uint4*>(dst + a) = make_uint4(ya.x, ya.y, yb.x, yb.y);
-                } else {
-                    *reinterpret_cast<uint2*>(dst + a) = ya;
-                    *reinterpret_cast<uint2*>(dst + b) = yb;
-                }
-            }
         }
-    }
+    };
+    const int rq = (p.Hq + kHeads - 1) / kHeads, rk = (p.Hkv + kHeads - 1) / kHeads;
+    const int rounds = rq + 2 * rk;
+    const int r0 = rounds * part / p.warps, r1 = rounds * (part + 1) / p.warps;
+    run(std::integral_constant<Kind, kQ>(), p.q + t * p.q_stride, p.wq, p.Hq, r0, min(r1, rq));
+    run(std::integral_constant<Kind, kK>(), p.k + t * p.k_stride, p.wk, p.Hkv, max(r0 - rq, 0),
+        min(r1 - rq, rk));
+    run(std::integral_constant<Kind, kV>(), p.v + t * p.v_stride, nullptr, p.Hkv,
+        max(r0 - rq - rk, 0), min(r1 - rq - rk, rk));
 }
 
 template <int D, bool INTER, bool F8>
 int32_t launch_rope(RopeParams& p, cudaStream_t stream) {
-    constexpr int kGroups = kThreads / (D / 8);
-    const int heads = p.Hq + 2 * p.Hkv;
-    // Tokens per CTA: one, unless a token has so few heads that most lane groups would idle and
-    // there are tokens enough to fill the GPU all the same.
-    int tokens = std::min(kMaxTokens, std::max(1, kGroups * kUnits / heads));
-    while (tokens > 1 && (p.T + tokens - 1) / tokens < 4 * PA_PLAN_CTAS) --tokens;
-    p.tokens = tokens;
+    constexpr int kHeads = 256 / D;            // heads a warp has at a time
+    // Warps per token: few, so that each has kMaxRounds rounds of heads to its sines, unless there
+    // are too few tokens to fill the GPU with (16 warps an SM); at most one for every round.
+    const int rounds = (p.Hq + kHeads - 1) / kHeads + 2 * ((p.Hkv + kHeads - 1) / kHeads);
+    const int64_t fill = (16 * int64_t(PA_PLAN_CTAS) + p.T - 1) / p.T;
+    p.warps = int(std::min<int64_t>(rounds, std::max<int64_t>((rounds + kMaxRounds - 1) / kMaxRounds,
+                                                              fill)));
+    const int64_t blocks = (int64_t(p.T) * p.warps * 32 + kThreads - 1) / kThreads;
+    if (blocks > INT32_MAX) return PA_ERR_SHAPE;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned((p.T + tokens - 1) / tokens));
+    cfg.gridDim = dim3(unsigned(blocks));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cfg.attrs = pdl;
