@@ -25,11 +25,14 @@
 // its 1/G of the total. No plan is made or uploaded, so a captured graph needs nothing renewed but
 // its metadata.
 //
-// Warps: 0-7 two epilogue warpgroups, 8 scheduler and loader of what stays, 9 MMA issuer, 10
-// loader of what streams, 11 log-sum-exps; over an fp8 cache 12-15 turn codes and q to f16.
-// Shared memory: two sets of two 32 KB slots for what stays (an item loads while the one before
-// it runs), three 32 KB stages for what streams. TMEM: two accumulators of 128 columns for each
-// warpgroup. Every wait is bounded.
+// Warps: 0-15 four epilogue warpgroups, 16 scheduler and loader of what stays, 17 MMA issuer, 18
+// loader of what streams, 19 log-sum-exps; over an fp8 cache 20-23 turn codes and q to f16. Each
+// warpgroup has one accumulator of 128 TMEM columns and takes every fourth product (with two
+// warpgroups of two accumulators the epilogue's latencies showed: 36 % of the tensor pipe). A MANY
+// tile's query tiles alternate between two of them, whose sums meet in shared memory.
+// Shared memory: seven 32 KB slots. Two sets of two for what stays (an item loads while the one
+// before it runs) and three stages for what streams; where no sequence is MANY, each set is one
+// slot, and the two others are stages as well (five tiles of K in flight). Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -47,19 +50,18 @@ using namespace pa_detail;
 
 namespace {
 
-constexpr int kBaseThreads = 384;
+constexpr int kBaseThreads = 640;
 template <bool F8>
 constexpr int kThreadsFor = F8 ? kBaseThreads + 128 : kBaseThreads;
 constexpr int kCols = 128;                     // columns of a query tile
 constexpr int kSlot = 32768;                   // one tile, 128 rows of D = 128
 constexpr int kHalf = 16384;                   // its 64-column halves
 constexpr int kStay = 0;                       // 2 sets x 2 slots
-constexpr int kStream = 4 * kSlot;             // stages
-constexpr int kStages = 3;
-constexpr int kCtl = kStream + kStages * kSlot;
+constexpr int kMaxStages = 5;
+constexpr int kCtl = 7 * kSlot;
 constexpr int kBytes = kCtl + 3072;
 static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
-constexpr int kLseSlots = 3;
+constexpr int kLseSlots = 2;
 constexpr int kMaxRows = 1 << 18;              // state rows whose repeats are looked for
 constexpr int64_t kCostFew = 4, kCostMany = 2; // of a key tile; of a key tile and query tile
 
@@ -67,24 +69,32 @@ enum Bar {
     kStayFull = 0,     // + set: TMA -> MMA (or the f16 warps)
     kStayEmpty = 2,    // + set: MMA -> loader
     kStreamFull = 4,   // + stage
-    kStreamEmpty = 7,  // + stage
-    kAccFull = 10,     // + accumulator: MMA -> its warpgroup
-    kAccEmpty = 14,    // + accumulator: 128 arrivals -> MMA
-    kLseFull = 18,     // + slot: 32 arrivals -> both warpgroups
-    kLseEmpty = 21,    // + slot: 256 arrivals
-    kItemFull = 24,    // + slot (4)
-    kItemEmpty = 28,   // + slot: every consumer thread
-    kStayReady = 32,   // + set, fp8 only: 128 arrivals of the f16 warps
-    kStreamReady = 34, // + stage
-    kDrain = 37,
-    kNumBars = 38
+    kStreamEmpty = 9,  // + stage
+    kAccFull = 14,     // + warpgroup: MMA -> its accumulator's warpgroup
+    kAccEmpty = 18,    // + warpgroup: 128 arrivals -> MMA
+    kLseFull = 22,     // + slot: 32 arrivals -> the warpgroups
+    kLseEmpty = 24,    // + slot: 512 arrivals
+    kItemFull = 26,    // + slot (4)
+    kItemEmpty = 30,   // + slot: every consumer thread
+    kPartFull = 34,    // + key tile of a pair: 128 arrivals, its second warpgroup -> its first
+    kPartEmpty = 36,   // + key tile: 128 arrivals
+    kStayReady = 38,   // + set, fp8 only: 128 arrivals of the f16 warps
+    kStreamReady = 40, // + stage
+    kDrain = 45,
+    kNumBars = 46
 };
 constexpr int kHolderOff = 8 * kNumBars;
 constexpr int kAbortOff = kHolderOff + 4;
-constexpr int kRingOff = 320;                  // 4 items of 64 bytes
+constexpr int kRingOff = 384;                  // 4 items of 64 bytes
 constexpr int kLseOff = kRingOff + 4 * 64;     // kLseSlots x 128 floats
+constexpr int kPartOff = kLseOff + kLseSlots * 512;   // 2 x 128 floats
 constexpr int kScanOff = kLseOff;              // before the pipeline starts
-static_assert(kAbortOff + 4 <= kRingOff && kLseOff + kLseSlots * 512 <= 3072, "control area");
+static_assert(kAbortOff + 4 <= kRingOff && kPartOff + 2 * 512 <= 3072, "control area");
+
+// Stage st of the stream: slots 4, 5, 6, and without MANY sequences the sets' second slots 1, 3.
+__device__ __forceinline__ uint32_t stage_at(int st) {
+    return uint32_t(st < 3 ? 4 + st : st == 3 ? 1 : 3) * kSlot;
+}
 
 struct Params {
     const float* lse;            // [T][Hq]
@@ -199,26 +209,47 @@ __device__ __forceinline__ Item read_item(const volatile Item* v) {
     return i;
 }
 
-__device__ __forceinline__ float ld_shared_f32x2(uint32_t a, float& y) {
-    float x;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(a) : "memory");
-    return x;
+// Adds 2^(s c + nl) of 16 columns (nl: minus the columns' log-sum-exp in base 2) to four packed
+// pairs of sums.
+__device__ __forceinline__ void add16(const uint32_t (&s)[16], const float4* nl, uint64_t c2,
+                                      uint64_t (&a)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 n = nl[i];
+        float x0, x1, x2, x3;
+        f2_split(fma2(f2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), c2,
+                      f2(n.x, n.y)), x0, x1);
+        f2_split(fma2(f2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), c2,
+                      f2(n.z, n.w)), x2, x3);
+        a[2 * (i & 1)] = add2(a[2 * (i & 1)], f2(ex2(x0), ex2(x1)));
+        a[2 * (i & 1) + 1] = add2(a[2 * (i & 1) + 1], f2(ex2(x2), ex2(x3)));
+    }
 }
 
-// Adds 2^(s c + nl) of 32 columns (nl: minus the columns' log-sum-exp in base 2, at shared address
-// la) to two packed pairs of sums.
-__device__ __forceinline__ void add32(const uint32_t (&s)[32], uint32_t la, uint64_t c2,
-                                      uint64_t& a0, uint64_t& a1) {
+// A K slot's code rows r0 .. r0 + 31 expanded to f16 by one warp, like expand_codes but with 16 rows
+// read before any is written: the reads' latency is paid twice a tile, not eight times. Rows from
+// `rows` on hold nothing that counts; their (stale) codes are turned as well.
+__device__ __forceinline__ void expand_rows(uint32_t slot, int r0, int rows, int lane) {
+    const uint32_t c = lane & 7, j0 = 2 * (c & 3), hi = c >> 2;
+#pragma unroll 1
+    for (int b = r0; b < min(rows, r0 + 32); b += 16) {
+        uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-        const uint4 n = ld_shared_v4(la + 4 * i);
-        float x0, x1, x2, x3;
-        f2_split(fma2(f2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2,
-                      f2(__uint_as_float(n.x), __uint_as_float(n.y))), x0, x1);
-        f2_split(fma2(f2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c2,
-                      f2(__uint_as_float(n.z), __uint_as_float(n.w))), x2, x3);
-        a0 = add2(a0, f2(ex2(x0), ex2(x1)));
-        a1 = add2(a1, f2(ex2(x2), ex2(x3)));
+        for (int i = 0; i < 4; ++i)
+            v[i] = ld_shared_v4(slot + kHalf + uint32_t(b + 4 * i + (lane >> 3)) * 128 + c * 16);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t R = uint32_t(b + 4 * i + (lane >> 3)), x = R & 7;
+            uint32_t f[8];
+            e4m3x4_to_f16x4(v[i].x, f[0], f[1]);
+            e4m3x4_to_f16x4(v[i].y, f[2], f[3]);
+            e4m3x4_to_f16x4(v[i].z, f[4], f[5]);
+            e4m3x4_to_f16x4(v[i].w, f[6], f[7]);
+            const uint32_t rb = slot + hi * kHalf + R * 128;
+            st_shared_v4(rb + ((j0 ^ x) << 4), f[0], f[1], f[2], f[3]);
+            st_shared_v4(rb + (((j0 + 1) ^ x) << 4), f[4], f[5], f[6], f[7]);
+        }
     }
 }
 
@@ -250,15 +281,15 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         for (int b = 0; b < kNumBars; ++b)
             mbar_init(bar(b), (b >= kAccEmpty && b < kLseFull)        ? 128
                               : (b >= kLseFull && b < kLseEmpty)      ? 32
-                              : (b >= kLseEmpty && b < kItemFull)     ? 256
-                              // MMA 1, stream loader 32, log-sum-exps 32, epilogue 256, f16 128
-                              : (b >= kItemEmpty && b < kStayReady)   ? 1 + 64 + 256 + (F8 ? 128 : 0)
-                              : (b >= kStayReady && b < kDrain)       ? 128
+                              : (b >= kLseEmpty && b < kItemFull)     ? 512
+                              // MMA 1, stream loader 32, log-sum-exps 32, epilogue 512, f16 128
+                              : (b >= kItemEmpty && b < kPartFull)    ? 1 + 64 + 512 + (F8 ? 128 : 0)
+                              : (b >= kPartFull && b < kDrain)        ? 128
                                                                       : 1);
         *abort_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) {
+    if (warp == 17) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          bars + kHolderOff),
                      "r"(512)
@@ -270,9 +301,9 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
 
     // ---- this CTA's share: repeated state rows, the total cost, where the share starts
     uint32_t* once = reinterpret_cast<uint32_t*>(smem + kStay);
-    int64_t* scan = reinterpret_cast<int64_t*>(smem + kCtl + kScanOff);   // [16] warps
-    int64_t* found = scan + 16;                      // start offset of the first sequence
-    int* found_s = reinterpret_cast<int*>(scan + 17);
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + kCtl + kScanOff);   // [32] warps
+    int64_t* found = scan + 32;                      // start offset of the first sequence
+    int* found_s = reinterpret_cast<int*>(scan + 33);
     int* repeated = found_s + 1;
     if (threadIdx.x == 0) {
         *found_s = p.B;
@@ -293,7 +324,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     }
     const bool twice = *repeated != 0;
     int64_t total = 0;
-    bool bad = false;
+    bool bad = false, some_many = false;
     // inclusive sums over the sequences of one round of kThreads; returns the thread's own
     const auto round_scan = [&](int64_t x, int64_t& sum) {
 #pragma unroll
@@ -320,6 +351,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             const Seq q = load_seq(p, s, log2qt, twice);
             mine = q.head_cost * p.Hkv;
             bad = bad || q.bad;
+            some_many = some_many || (q.head_cost > 0 && !q.few);
         }
         int64_t sum;
         upto = round_scan(mine, sum) + total;
@@ -350,7 +382,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     // the rows' bits were written through the generic proxy where TMA writes next
     fence_proxy_async();
     tc_fence_before();
-    __syncthreads();
+    const int n_stages = __syncthreads_or(some_many) ? 3 : kMaxStages;
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kCtl + kHolderOff);
     const int start_s = *reinterpret_cast<volatile int*>(found_s);
@@ -367,26 +399,27 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     };
     // the K tile of key tile t into `slot` (all lanes; lane 0 has waited for the slot): one box per
     // block and 64-column half, or over an fp8 cache one box of codes per block into the second
-    // half, where they are expanded. `id`: the lane's table entry.
-    const auto load_k = [&](uint32_t slot, uint32_t full, const Item& I, int t, int id) {
-        const int nblk = (min(kTileKeys, I.ctx - t * kTileKeys) + p.bs - 1) >> log2bs;
-        if (lane == 0) mbar_expect_tx(full, uint32_t(nblk) * p.bs * (F8 ? 128 : 128 * kChunks));
-        __syncwarp();
-        if (lane < nblk) {
-            if constexpr (F8) {
-                tma_load_3d(slot + kHalf + lane * p.bs * 128, &tm_k, full, 0, I.kvh, id * p.bs);
-            } else {
+    // half, where they are expanded. `id`: the lane's block.
+    const auto blocks_of = [&](const Item& I, int t) {
+        return (min(kTileKeys, I.ctx - t * kTileKeys) + p.bs - 1) >> log2bs;
+    };
+    const auto load_k = [&](uint32_t slot, uint32_t full, const Item& I, int nblk, int id) {
+        if (lane >= nblk) return;
+        const uint32_t dst = slot + lane * p.bs * 128;
+        if constexpr (F8) {
+            tma_load_3d(dst + kHalf, &tm_k, full, 0, I.kvh, id * p.bs);
+        } else {
 #pragma unroll
-                for (int h = 0; h < kChunks; ++h)
-                    tma_load_3d(slot + h * kHalf + lane * p.bs * 128, &tm_k, full, 64 * h, I.kvh,
-                                id * p.bs);
-            }
+            for (int h = 0; h < kChunks; ++h)
+                tma_load_3d(dst + h * kHalf, &tm_k, full, 64 * h, I.kvh, id * p.bs);
         }
     };
-    // the lane's block id of key tile t; one outside the pool reads zeros
-    const auto block_id = [&](const Item& I, int t) {
+    const auto k_bytes = [&](int nblk) { return uint32_t(nblk) * p.bs * (F8 ? 128 : 128 * kChunks); };
+    // the block in the lane's entry of the table, counted from key tile t's first, up to key tile
+    // `end`; one outside the pool reads zeros
+    const auto block_id = [&](const Item& I, int t, int end) {
         const int e = (t << (7 - log2bs)) + lane;
-        if (lane >= (kTileKeys >> log2bs) || e << log2bs >= I.ctx) return -1;
+        if (e << log2bs >= min(I.ctx, end * kTileKeys)) return -1;
         const int b = __ldg(p.block_table + int64_t(I.seq) * p.max_blocks + e);
         if (b >= 0 && b < p.num_blocks) return b;
         if (p.err) atomicOr(p.err, PA_DEVERR_BLOCK);
@@ -401,7 +434,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                         I.cu0 + (qt << log2qt));
     };
 
-    if (warp == 8) {
+    if (warp == 16) {
         // ------------------------------------------------ scheduler, loader of what stays
         int ic = 0, ok = 1;
         // publishes an item and loads its query tile or key tiles
@@ -432,7 +465,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             const int set = ic & 1;
             int id[2] = {-1, -1};
             if (!few)
-                for (int r = 0; r < I.nt; ++r) id[r] = block_id(I, I.t0 + r);
+                for (int r = 0; r < I.nt; ++r) id[r] = block_id(I, I.t0 + r, I.t0 + r + 1);
             if (lane == 0 && ic >= 2)
                 ok = wait_bounded(bar(kStayEmpty + set), ((ic >> 1) - 1) & 1, abort_word);
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -442,26 +475,11 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 if (lane == 0) load_q(slot, bar(kStayFull + set), I, 0);
             } else {
                 // one barrier for both tiles: its one arrival carries the bytes of both
-                const int n0 = (min(kTileKeys, I.ctx - I.t0 * kTileKeys) + p.bs - 1) >> log2bs;
-                const int n1 = I.nt == 2
-                    ? (min(kTileKeys, I.ctx - (I.t0 + 1) * kTileKeys) + p.bs - 1) >> log2bs : 0;
-                if (lane == 0)
-                    mbar_expect_tx(bar(kStayFull + set),
-                                   uint32_t(n0 + n1) * p.bs * (F8 ? 128 : 128 * kChunks));
+                const int n0 = blocks_of(I, I.t0), n1 = I.nt == 2 ? blocks_of(I, I.t0 + 1) : 0;
+                if (lane == 0) mbar_expect_tx(bar(kStayFull + set), k_bytes(n0 + n1));
                 __syncwarp();
-                for (int r = 0; r < I.nt; ++r) {
-                    if (lane >= (r ? n1 : n0)) continue;
-                    const uint32_t dst = slot + r * kSlot + lane * p.bs * 128;
-                    if constexpr (F8) {
-                        tma_load_3d(dst + kHalf, &tm_k, bar(kStayFull + set), 0, I.kvh,
-                                    id[r] * p.bs);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < kChunks; ++h)
-                            tma_load_3d(dst + h * kHalf, &tm_k, bar(kStayFull + set), 64 * h,
-                                        I.kvh, id[r] * p.bs);
-                    }
-                }
+                load_k(slot, bar(kStayFull + set), I, n0, id[0]);
+                load_k(slot + kSlot, bar(kStayFull + set), I, n1, id[1]);
             }
             ++ic;
         };
@@ -512,25 +530,25 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             for (int i = max(0, ic - 2); i < ic; ++i)
                 wait_drain(bar(kStayFull + (i & 1)), (i >> 1) & 1);
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ------------------------------------------------ MMA issuer
         if (lane == 0) {
             int st = 0, ph = 0;              // stream stage and its phase
-            int m[2] = {0, 0};               // products of each warpgroup
+            uint32_t used = 0, phase = 0;    // per warpgroup: its accumulator has been used; parity
             int turn = 0;                    // the warpgroup of the next FEW tile
             bool ok = true;
-            // accumulator of the next product of warpgroup w: columns 128 (2 w + (m & 1))
+            // the next product of warpgroup w, into its accumulator
             const auto product = [&](int w, uint32_t a, uint32_t b, int cols) {
-                const int acc = 2 * w + (m[w] & 1);
-                if (m[w] >= 2 &&
-                    !(ok = wait_bounded(bar(kAccEmpty + acc), ((m[w] >> 1) - 1) & 1, abort_word)))
+                if ((used >> w & 1) &&
+                    !(ok = wait_bounded(bar(kAccEmpty + w), phase >> w & 1, abort_word)))
                     return;
+                phase ^= (used >> w & 1) << w;
+                used |= 1u << w;
                 tc_fence_after();
-                issue_s_group<D>(1u, tmem + acc * 128, make_sdesc(a, 16, 1024),
+                issue_s_group<D>(1u, tmem + w * kCols, make_sdesc(a, 16, 1024),
                                  make_sdesc(b, 16, 1024),
                                  make_idesc(128, (cols + 15) & ~15, false, F8));
-                tc_commit_if(1u, bar(kAccFull + acc));
-                ++m[w];
+                tc_commit_if(1u, bar(kAccFull + w));
             };
             for (int ic = 0;; ++ic) {
                 Item I;
@@ -542,17 +560,17 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 const int n = few ? I.nt : I.n_qt - I.qt0;
                 for (int i = 0; i < n && ok; ++i) {
                     if (!(ok = wait_bounded(bar(kStreamUse + st), ph, abort_word))) break;
-                    const uint32_t stage = sb + kStream + st * kSlot;
+                    const uint32_t stage = sb + stage_at(st);
                     if (few) {
                         product(turn, stage, stay, I.n_q * p.g);
-                        turn ^= 1;
+                        turn = (turn + 1) & 3;
                     } else {
                         const int cols = min(kCols, (I.n_q - ((I.qt0 + i) << log2qt)) * p.g);
                         for (int r = 0; r < I.nt && ok; ++r)
-                            product(r, stay + r * kSlot, stage, cols);
+                            product(r + 2 * (i & 1), stay + r * kSlot, stage, cols);
                     }
                     tc_commit_if(1u, bar(kStreamEmpty + st));
-                    if (++st == kStages) {
+                    if (++st == n_stages) {
                         st = 0;
                         ph ^= 1;
                     }
@@ -564,36 +582,50 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             tc_commit_if(1u, bar(kDrain));
             wait_drain(bar(kDrain), 0);
         }
-    } else if (warp == 10) {
+    } else if (warp == 18) {
         // ------------------------------------------------ loader of what streams
-        int n_done = 0, ok = 1;
+        int st = 0, ph = 1, n_done = 0, ok = 1;      // a fresh barrier's phase 1 counts as past
+        const int per_tile = kTileKeys >> log2bs, per_load = 32 / per_tile;   // blocks; tiles
         for (int ic = 0; ok; ++ic) {
             Item I;
             ok = next_item(ic, I);
             if (!__all_sync(0xffffffffu, ok)) break;
             const bool few = I.n_qt == 1;
-            const int n = few ? I.nt : I.n_qt - I.qt0;
-            int id = few ? block_id(I, I.t0) : -1;
+            const int n = few ? I.nt : I.n_qt - I.qt0, end = I.t0 + I.nt;
+            // the lanes hold the blocks of per_load tiles, and those of the next ones on their way
+            int ids = -1, next = few ? block_id(I, I.t0, end) : -1;
             for (int i = 0; i < n; ++i) {
-                const int st = n_done % kStages;
-                const int id_next = few && i + 1 < n ? block_id(I, I.t0 + i + 1) : -1;
-                if (lane == 0 && n_done >= kStages)
-                    ok = wait_bounded(bar(kStreamEmpty + st), (n_done / kStages - 1) & 1,
-                                      abort_word);
+                const int at = i & (per_load - 1);
+                if (few && at == 0) {
+                    ids = next;
+                    next = i + per_load < n ? block_id(I, I.t0 + i + per_load, end) : -1;
+                }
+                if (lane == 0) ok = wait_bounded(bar(kStreamEmpty + st), ph, abort_word);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
-                const uint32_t slot = sb + kStream + st * kSlot;
-                if (few) load_k(slot, bar(kStreamFull + st), I, I.t0 + i, id);
-                else if (lane == 0) load_q(slot, bar(kStreamFull + st), I, I.qt0 + i);
-                id = id_next;
+                const uint32_t slot = sb + stage_at(st), full = bar(kStreamFull + st);
+                if (few) {
+                    const int nblk = blocks_of(I, I.t0 + i);
+                    const int id = __shfl_sync(0xffffffffu, ids, (at * per_tile + lane) & 31);
+                    if (lane == 0) mbar_expect_tx(full, k_bytes(nblk));
+                    __syncwarp();
+                    load_k(slot, full, I, nblk, id);
+                } else if (lane == 0) {
+                    load_q(slot, full, I, I.qt0 + i);
+                }
                 ++n_done;
+                if (++st == n_stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
         }
         if (lane == 0) {
-            for (int i = max(0, n_done - kStages); i < n_done; ++i)
-                wait_drain(bar(kStreamFull + i % kStages), (i / kStages) & 1);
+            // never leave with copies in flight into this CTA's shared memory
+            for (int i = 0; i < min(n_done, n_stages); ++i)
+                wait_drain(bar(kStreamFull + i), ((n_done - 1 - i) / n_stages) & 1);
         }
-    } else if (warp == 11) {
+    } else if (warp == 19) {
         // ------------------------------------------------ log-sum-exps, negated, in base 2
         int n_done = 0, ok = 1;
         for (int ic = 0; ok; ++ic) {
@@ -628,16 +660,16 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 mbar_arrive(bar(kLseFull + slot));
             }
         }
-    } else if (warp >= 12) {
+    } else if (warp >= 20) {
         // ------------------------------------------------ codes and q to f16 (fp8 cache)
         if constexpr (F8) {
-            const int w = warp - 12;
+            const int w = warp - 20;
             // the MMAs take f16 operands: 32 rows a warp of a K tile's codes are expanded, or of a
             // query tile rounded in place (a 16-byte chunk keeps its place, so the swizzle holds)
             const auto turn_k = [&](uint32_t slot, const Item& I, int t) {
                 const int rows =
                     ((min(kTileKeys, I.ctx - t * kTileKeys) + p.bs - 1) >> log2bs) << log2bs;
-                expand_codes<false>(slot, 32 * w, min(rows, 32 * w + 32), p.bs, log2bs, lane);
+                expand_rows(slot, 32 * w, rows, lane);
             };
             const auto turn_q = [&](uint32_t slot, int rows) {
                 for (int i = threadIdx.x - kBaseThreads; i < rows * 16; i += 128) {
@@ -647,7 +679,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                                  bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
                 }
             };
-            int n_done = 0;
+            int st = 0, ph = 0;
             bool ok = true;
             for (int ic = 0; ok; ++ic) {
                 Item I;
@@ -662,75 +694,83 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 fence_proxy_async();
                 mbar_arrive(bar(kStayReady + set));
                 const int n = few ? I.nt : I.n_qt - I.qt0;
-                for (int i = 0; i < n; ++i, ++n_done) {
-                    const int st = n_done % kStages;
-                    if (!(ok = wait_bounded(bar(kStreamFull + st), (n_done / kStages) & 1,
-                                            abort_word)))
-                        break;
-                    const uint32_t slot = sb + kStream + st * kSlot;
+                for (int i = 0; i < n; ++i) {
+                    if (!(ok = wait_bounded(bar(kStreamFull + st), ph, abort_word))) break;
+                    const uint32_t slot = sb + stage_at(st);
                     if (few) turn_k(slot, I, I.t0 + i);
                     else turn_q(slot, kCols);
                     fence_proxy_async();
                     mbar_arrive(bar(kStreamReady + st));
+                    if (++st == n_stages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
                 }
             }
         }
     } else {
         // ------------------------------------------------ epilogue warpgroups
         const int w = warp >> 2;
-        const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+        const uint32_t tm = tmem + w * kCols + (uint32_t(32 * (warp & 3)) << 16);
         const int key_in_tile = 32 * (warp & 3) + lane;
         const uint64_t c2 = f2(p.c, p.c);
-        int m = 0, turn = 0, n_lse = 0;
+        int acc_ph = 0, turn = 0, n_lse = 0, n_part = 0;
         bool ok = true;
+        const float4* lse_smem = reinterpret_cast<const float4*>(smem + kCtl + kLseOff);
+        float* part = reinterpret_cast<float*>(smem + kCtl + kPartOff) + (w & 1) * 128;
         // the sum over the columns of this warpgroup's next product: query rows from position
         // `at` on, `cols` columns, key j
-        const auto column_sum = [&](uint32_t la, int cols, int at, int j, int tile_end, float& sum) {
-            const int acc = 2 * w + (m & 1);
-            if (!(ok = wait_bounded(bar(kAccFull + acc), (m >> 1) & 1, abort_word))) return;
+        const auto column_sum = [&](const float4* nl, int cols, int at, int j, int tile_end,
+                                    float& sum) {
+            if (!(ok = wait_bounded(bar(kAccFull + w), acc_ph, abort_word))) return;
+            acc_ph ^= 1;
             tc_fence_after();
-            ++m;
-            const uint32_t tm = tmem + acc * 128 + lanes;
-            uint64_t a0 = f2(0.f, 0.f), a1 = a0;
+            uint64_t a[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = f2(0.f, 0.f);
             if (cols == kCols && tile_end <= at + 1) {
-                uint32_t s0[32], s1[32];
-                tmem_ld_32x32b_x32(tm, s0);
-                tmem_wait_ld();
-                tmem_ld_32x32b_x32(tm + 32, s1);
-                add32(s0, la, c2, a0, a1);
-                tmem_wait_ld();
-                tmem_ld_32x32b_x32(tm + 64, s0);
-                add32(s1, la + 128, c2, a0, a1);
-                tmem_wait_ld();
-                tmem_ld_32x32b_x32(tm + 96, s1);
-                add32(s0, la + 256, c2, a0, a1);
-                tmem_wait_ld();
-                tc_fence_before();
-                mbar_arrive(bar(kAccEmpty + acc));
-                add32(s1, la + 384, c2, a0, a1);
+                uint32_t s0[16], s1[16];
+                tmem_ld_32x32b_x16(tm, s0);
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) {
+                    tmem_wait_ld();
+                    tmem_ld_32x32b_x16(tm + c + 16, s1);
+                    add16(s0, nl + c / 4, c2, a);
+                    tmem_wait_ld();
+                    if (c + 32 < kCols) {
+                        tmem_ld_32x32b_x16(tm + c + 32, s0);
+                    } else {
+                        tc_fence_before();
+                        mbar_arrive(bar(kAccEmpty + w));
+                    }
+                    add16(s1, nl + c / 4 + 4, c2, a);
+                }
             } else {
                 // the first column whose row comes at or after the key
                 const int from = max(0, j - at) << (7 - log2qt);
-                for (int c0 = 0; c0 < cols; c0 += 16) {
+                for (int c = 0; c < cols; c += 16) {
                     uint32_t s[16];
-                    tmem_ld_32x32b_x16(tm + c0, s);
+                    tmem_ld_32x32b_x16(tm + c, s);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        float n1;
-                        const float n0 = ld_shared_f32x2(la + 4 * (c0 + i), n1);
-                        const int col = c0 + i;
-                        const float e0 = ex2(fmaf(__uint_as_float(s[i]), p.c, n0));
-                        const float e1 = ex2(fmaf(__uint_as_float(s[i + 1]), p.c, n1));
-                        a0 = add2(a0, f2(col >= from && col < cols ? e0 : 0.f,
-                                         col + 1 >= from && col + 1 < cols ? e1 : 0.f));
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 n = nl[(c + i) / 4];
+                        const float v[4] = {n.x, n.y, n.z, n.w};
+                        float e[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float x = ex2(fmaf(__uint_as_float(s[i + k]), p.c, v[k]));
+                            e[k] = c + i + k >= from && c + i + k < cols ? x : 0.f;
+                        }
+                        a[0] = add2(a[0], f2(e[0], e[1]));
+                        a[1] = add2(a[1], f2(e[2], e[3]));
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(bar(kAccEmpty + acc));
+                mbar_arrive(bar(kAccEmpty + w));
             }
             float x0, x1;
-            f2_split(add2(a0, a1), x0, x1);
+            f2_split(add2(add2(a[0], a[1]), add2(a[2], a[3])), x0, x1);
             sum += x0 + x1;
         };
         for (int ic = 0; ok; ++ic) {
@@ -743,45 +783,60 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             const auto done_lse = [&]() { mbar_arrive(bar(kLseEmpty + n_lse++ % kLseSlots)); };
             if (I.n_qt == 1) {
                 if (!wait_lse()) break;
-                const uint32_t la = sb + kCtl + kLseOff + (n_lse % kLseSlots) * 512;
+                const float4* nl = lse_smem + (n_lse % kLseSlots) * 32;
                 for (int i = 0; i < I.nt; ++i) {
                     const bool my = turn == w;
-                    turn ^= 1;
+                    turn = (turn + 1) & 3;
                     if (!my) continue;
                     const int kb = (I.t0 + i) * kTileKeys, j = kb + key_in_tile;
                     float* dst = p.weights + I.state + j;
                     const float old = j < I.held ? *dst : 0.f;
                     float sum = 0.f;
-                    column_sum(la, I.n_q * p.g, I.pos0, j, kb + kTileKeys, sum);
+                    column_sum(nl, I.n_q * p.g, I.pos0, j, kb + kTileKeys, sum);
                     if (!ok) break;
                     if (j < I.ctx) *dst = old + sum;
                 }
                 if (!ok) break;
                 done_lse();
-            } else {
-                const bool my = w < I.nt;
-                const int kb = (I.t0 + w) * kTileKeys, j = kb + key_in_tile;
-                float* dst = p.weights + I.state + j;
-                const float old = my && j < I.held ? *dst : 0.f;
-                float sum = 0.f;
-                for (int qt = I.qt0; qt < I.n_qt; ++qt) {
-                    if (!wait_lse()) break;
-                    if (my)
-                        column_sum(sb + kCtl + kLseOff + (n_lse % kLseSlots) * 512,
-                                   min(kCols, (I.n_q - (qt << log2qt)) * p.g),
-                                   I.pos0 + (qt << log2qt), j, kb + kTileKeys, sum);
-                    if (!ok) break;
-                    done_lse();
-                }
-                if (!ok) break;
-                if (my && j < I.ctx) *dst = old + sum;
+                continue;
             }
+            // the tile w & 1 of the pair; its query tiles alternate between warpgroups w and w ^ 2
+            const int r = w & 1;
+            const bool my = r < I.nt;
+            const int kb = (I.t0 + r) * kTileKeys, j = kb + key_in_tile;
+            float* dst = p.weights + I.state + j;
+            const float old = my && w < 2 && j < I.held ? *dst : 0.f;
+            float sum = 0.f;
+            for (int qt = I.qt0; qt < I.n_qt; ++qt) {
+                if (!wait_lse()) break;
+                if (my && ((qt - I.qt0) & 1) == w >> 1)
+                    column_sum(lse_smem + (n_lse % kLseSlots) * 32,
+                               min(kCols, (I.n_q - (qt << log2qt)) * p.g),
+                               I.pos0 + (qt << log2qt), j, kb + kTileKeys, sum);
+                if (!ok) break;
+                done_lse();
+            }
+            if (!ok) break;
+            if (!my) continue;
+            if (w >= 2) {
+                if (n_part > 0 &&
+                    !(ok = wait_bounded(bar(kPartEmpty + r), (n_part - 1) & 1, abort_word)))
+                    break;
+                part[key_in_tile] = sum;
+                mbar_arrive(bar(kPartFull + r));
+            } else {
+                if (!(ok = wait_bounded(bar(kPartFull + r), n_part & 1, abort_word))) break;
+                sum += part[key_in_tile];
+                mbar_arrive(bar(kPartEmpty + r));
+                if (j < I.ctx) *dst = old + sum;
+            }
+            ++n_part;
         }
     }
     if (*abort_word && threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
