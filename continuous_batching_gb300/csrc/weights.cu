@@ -25,11 +25,14 @@
 // its 1/G of the total. No plan is made or uploaded, so a captured graph needs nothing renewed but
 // its metadata.
 //
-// Warps: 0-15 four epilogue warpgroups, 16 scheduler and loader of what stays, 17 MMA issuer, 18
-// loader of what streams, 19 log-sum-exps; over an fp8 cache 20-23 turn codes and q to f16. Each
-// warpgroup has one accumulator of 128 TMEM columns and takes every fourth product (with two
-// warpgroups of two accumulators the epilogue's latencies showed: 36 % of the tensor pipe). A MANY
-// tile's query tiles alternate between two of them, whose sums meet in shared memory.
+// Warps: 0-15 four epilogue warpgroups, 16 scheduler and loader of what stays, 17 and 20 MMA issuers,
+// 18 loader of what streams, 19 log-sum-exps; over an fp8 cache 24-27 turn codes and q to f16. The
+// stream's tiles alternate between the two issuers, each with two of the four accumulators (128
+// TMEM columns each): an issuer's waits, commits and address arithmetic, made slow by the warps it
+// shares its scheduler with, run while the other's MMAs keep the tensor pipe busy (one issuer left
+// it idle for more than half of the time). FEW: each tile has one accumulator and one warpgroup.
+// MANY: a query tile has an accumulator for each of its two key tiles, and each of these is read by
+// two warpgroups, 64 columns each, whose sums meet in shared memory at the item's end.
 // Shared memory: seven 32 KB slots. Two sets of two for what stays (an item loads while the one
 // before it runs) and three stages for what streams; where no sequence is MANY, each set is one
 // slot, and the two others are stages as well (five tiles of K in flight). Every wait is bounded.
@@ -50,9 +53,10 @@ using namespace pa_detail;
 
 namespace {
 
-constexpr int kBaseThreads = 640;
+constexpr int kBaseThreads = 672;
 template <bool F8>
 constexpr int kThreadsFor = F8 ? kBaseThreads + 128 : kBaseThreads;
+constexpr int kTurners = kBaseThreads / 32;    // the first f16 warp of an fp8 cache
 constexpr int kCols = 128;                     // columns of a query tile
 constexpr int kSlot = 32768;                   // one tile, 128 rows of D = 128
 constexpr int kHalf = 16384;                   // its 64-column halves
@@ -65,27 +69,32 @@ constexpr int kLseSlots = 2;
 constexpr int kMaxRows = 1 << 18;              // state rows whose repeats are looked for
 constexpr int64_t kCostFew = 4, kCostMany = 2; // of a key tile; of a key tile and query tile
 
+// Stream tile n (counted over all items) has stage n % n_stages and issuer n % 2. The barriers that
+// issuers wait on for it are numbered n % (2 n_stages), n_stages being odd: each is only ever waited
+// on by one of them, which keeps its parity's meaning sound.
 enum Bar {
-    kStayFull = 0,     // + set: TMA -> MMA (or the f16 warps)
-    kStayEmpty = 2,    // + set: MMA -> loader
-    kStreamFull = 4,   // + stage
-    kStreamEmpty = 9,  // + stage
-    kAccFull = 14,     // + warpgroup: MMA -> its accumulator's warpgroup
-    kAccEmpty = 18,    // + warpgroup: 128 arrivals -> MMA
-    kLseFull = 22,     // + slot: 32 arrivals -> the warpgroups
-    kLseEmpty = 24,    // + slot: 512 arrivals
-    kItemFull = 26,    // + slot (4)
-    kItemEmpty = 30,   // + slot: every consumer thread
-    kPartFull = 34,    // + key tile of a pair: 128 arrivals, its second warpgroup -> its first
-    kPartEmpty = 36,   // + key tile: 128 arrivals
-    kStayReady = 38,   // + set, fp8 only: 128 arrivals of the f16 warps
-    kStreamReady = 40, // + stage
-    kDrain = 45,
-    kNumBars = 46
+    kStayFull = 0,     // + set: TMA -> issuers (or the f16 warps)
+    kStayEmpty = 2,    // + set: both issuers -> loader
+    kStreamFull = 4,   // + n % (2 n_stages)
+    kStreamEmpty = 14, // + stage: its issuer -> loader
+    kAccFull = 19,     // + accumulator, FEW: issuer -> its warpgroup
+    kAccEmpty = 23,    // + accumulator, FEW: 128 arrivals -> issuer
+    kPairFull = 27,    // + n % 2, MANY: issuer -> the warpgroups (one for both key tiles)
+    kPairEmpty = 29,   // + n % 2, MANY: 512 arrivals -> issuer
+    kLseFull = 31,     // + slot: 32 arrivals -> the warpgroups
+    kLseEmpty = 33,    // + slot: 512 arrivals
+    kItemFull = 35,    // + slot (4)
+    kItemEmpty = 39,   // + slot: every consumer thread
+    kPartFull = 43,    // + key tile of a pair: 128 arrivals, its second warpgroup -> its first
+    kPartEmpty = 45,   // + key tile: 128 arrivals
+    kDrain = 47,       // + issuer
+    kStayReady = 49,   // + set, fp8 only: 128 arrivals of the f16 warps
+    kStreamReady = 51, // + n % (2 n_stages)
+    kNumBars = 61
 };
 constexpr int kHolderOff = 8 * kNumBars;
 constexpr int kAbortOff = kHolderOff + 4;
-constexpr int kRingOff = 384;                  // 4 items of 64 bytes
+constexpr int kRingOff = 512;                  // 4 items of 64 bytes
 constexpr int kLseOff = kRingOff + 4 * 64;     // kLseSlots x 128 floats
 constexpr int kPartOff = kLseOff + kLseSlots * 512;   // 2 x 128 floats
 constexpr int kScanOff = kLseOff;              // before the pipeline starts
@@ -191,38 +200,38 @@ struct Item {
 };
 static_assert(sizeof(Item) == 64, "item slot size");
 
-__device__ __forceinline__ Item read_item(const volatile Item* v) {
-    Item i;
-    i.seq = v->seq;
-    i.kvh = v->kvh;
-    i.t0 = v->t0;
-    i.nt = v->nt;
-    i.qt0 = v->qt0;
-    i.n_qt = v->n_qt;
-    i.cu0 = v->cu0;
-    i.n_q = v->n_q;
-    i.pos0 = v->pos0;
-    i.ctx = v->ctx;
-    i.held = v->held;
-    i.last = v->last;
-    i.state = v->state;
-    return i;
+__device__ __forceinline__ Item read_item(uint32_t at) {
+    union {
+        uint4 v[4];
+        Item i;
+    } u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u.v[k] = ld_shared_v4(at + 16 * k);
+    return u.i;
 }
 
-// Adds 2^(s c + nl) of 16 columns (nl: minus the columns' log-sum-exp in base 2) to four packed
-// pairs of sums.
-__device__ __forceinline__ void add16(const uint32_t (&s)[16], const float4* nl, uint64_t c2,
-                                      uint64_t (&a)[4]) {
+// Where column col's log-sum-exp lies in its slot: the order in which add16 takes them.
+__device__ __forceinline__ int lse_place(int col) {
+    return (col & ~15) + ((col & 7) >> 1) * 4 + ((col >> 3) & 1) * 2 + (col & 1);
+}
+
+// A thread's share of 16 columns for the 32 keys of its warp (tcgen05.ld 16x256b, the lower and
+// the upper 16 lanes): keys rs + 8 k (rs = lane / 4, k = 0 .. 3) and columns 8 cc + 2 q4 + {0, 1}
+// (q4 = lane % 4, cc = 0, 1). One 16-byte read of log-sum-exps so serves 16 elements: with a lane
+// per key it served four, and those reads took a quarter of the shared-memory bandwidth that the
+// MMAs' operands need. Adds 2^(s c + n) to the packed sum of each of the four keys.
+__device__ __forceinline__ void add16(const uint32_t (&lo)[8], const uint32_t (&hi)[8], float4 n,
+                                      uint64_t c2, uint64_t (&a)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 n = nl[i];
-        float x0, x1, x2, x3;
-        f2_split(fma2(f2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), c2,
-                      f2(n.x, n.y)), x0, x1);
-        f2_split(fma2(f2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), c2,
-                      f2(n.z, n.w)), x2, x3);
-        a[2 * (i & 1)] = add2(a[2 * (i & 1)], f2(ex2(x0), ex2(x1)));
-        a[2 * (i & 1) + 1] = add2(a[2 * (i & 1) + 1], f2(ex2(x2), ex2(x3)));
+    for (int cc = 0; cc < 2; ++cc) {
+        const uint64_t n2 = cc ? f2(n.z, n.w) : f2(n.x, n.y);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t* s = (k < 2 ? lo : hi) + 4 * cc + 2 * (k & 1);
+            float x0, x1;
+            f2_split(fma2(f2(__uint_as_float(s[0]), __uint_as_float(s[1])), c2, n2), x0, x1);
+            a[k] = add2(a[k], f2(ex2(x0), ex2(x1)));
+        }
     }
 }
 
@@ -279,12 +288,18 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < kNumBars; ++b)
-            mbar_init(bar(b), (b >= kAccEmpty && b < kLseFull)        ? 128
-                              : (b >= kLseFull && b < kLseEmpty)      ? 32
-                              : (b >= kLseEmpty && b < kItemFull)     ? 512
-                              // MMA 1, stream loader 32, log-sum-exps 32, epilogue 512, f16 128
-                              : (b >= kItemEmpty && b < kPartFull)    ? 1 + 64 + 512 + (F8 ? 128 : 0)
-                              : (b >= kPartFull && b < kDrain)        ? 128
+            mbar_init(bar(b), b >= kStayReady                         ? 128
+                              : b >= kDrain                           ? 1
+                              : b >= kPartFull                        ? 128
+                              // issuers 2, stream loader and log-sum-exps 64, epilogue 512, f16 128
+                              : b >= kItemEmpty                       ? 2 + 64 + 512 + (F8 ? 128 : 0)
+                              : b >= kItemFull                        ? 1
+                              : b >= kLseEmpty                        ? 512
+                              : b >= kLseFull                         ? 32
+                              : b >= kPairEmpty                       ? 512
+                              : b >= kPairFull                        ? 1
+                              : b >= kAccEmpty                        ? 128
+                              : b >= kStayEmpty && b < kStreamFull    ? 2
                                                                       : 1);
         *abort_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -312,6 +327,12 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     }
     if (p.rows)
         for (int i = threadIdx.x; i < (p.n_rows + 31) / 32; i += kThreads) once[i] = 0;
+    // the first round's metadata, read before the barriers
+    Seq mine_seq;
+    mine_seq.head_cost = 0;
+    mine_seq.bad = false;
+    mine_seq.few = true;
+    if (int(threadIdx.x) < p.B) mine_seq = load_seq(p, int(threadIdx.x), log2qt, false);
     __syncthreads();
     if (p.rows) {
         for (int s = threadIdx.x; s < p.B; s += kThreads) {
@@ -348,7 +369,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         const int s = s0 + int(threadIdx.x);
         mine = 0;
         if (s < p.B) {
-            const Seq q = load_seq(p, s, log2qt, twice);
+            const Seq q = s0 == 0 && !twice ? mine_seq : load_seq(p, s, log2qt, twice);
             mine = q.head_cost * p.Hkv;
             bad = bad || q.bad;
             some_many = some_many || (q.head_cost > 0 && !q.few);
@@ -393,7 +414,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     // takes the next item: every consumer thread (or the one lane that stands for a warp) calls it
     const auto next_item = [&](int ic, Item& I) {
         if (!wait_bounded(bar(kItemFull + (ic & 3)), (ic >> 2) & 1, abort_word)) return false;
-        I = read_item(ring + (ic & 3));
+        I = read_item(sb + kCtl + kRingOff + (ic & 3) * 64);
         mbar_arrive(bar(kItemEmpty + (ic & 3)));
         return I.last == 0;
     };
@@ -530,48 +551,71 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             for (int i = max(0, ic - 2); i < ic; ++i)
                 wait_drain(bar(kStayFull + (i & 1)), (i >> 1) & 1);
         }
-    } else if (warp == 17) {
-        // ------------------------------------------------ MMA issuer
+    } else if (warp == 17 || warp == 20) {
+        // ------------------------------------------------ MMA issuers
         if (lane == 0) {
-            int st = 0, ph = 0;              // stream stage and its phase
-            uint32_t used = 0, phase = 0;    // per warpgroup: its accumulator has been used; parity
-            int turn = 0;                    // the warpgroup of the next FEW tile
+            const int me = warp == 20;           // takes the stream tiles n with n % 2 == me
+            int n = 0, st = 0, fb = 0;           // stream tile, its stage and full barrier
+            uint32_t ph = 0;                     // parity of the barriers of this turn of fb
+            // accumulators me, me + 2 (FEW) or both (MANY) handed to the epilogue and not seen back,
+            // and the parity of their next return
+            uint32_t few_out = 0, few_ph = 0, pair_out = 0, pair_ph = 0;
             bool ok = true;
-            // the next product of warpgroup w, into its accumulator
-            const auto product = [&](int w, uint32_t a, uint32_t b, int cols) {
-                if ((used >> w & 1) &&
-                    !(ok = wait_bounded(bar(kAccEmpty + w), phase >> w & 1, abort_word)))
-                    return;
-                phase ^= (used >> w & 1) << w;
-                used |= 1u << w;
-                tc_fence_after();
-                issue_s_group<D>(1u, tmem + w * kCols, make_sdesc(a, 16, 1024),
-                                 make_sdesc(b, 16, 1024),
-                                 make_idesc(128, (cols + 15) & ~15, false, F8));
-                tc_commit_if(1u, bar(kAccFull + w));
+            const auto few_back = [&](int h) {
+                if (!(few_out >> h & 1)) return;
+                ok = ok && wait_bounded(bar(kAccEmpty + me + 2 * h), few_ph >> h & 1, abort_word);
+                few_out &= ~(1u << h);
+                few_ph ^= 1u << h;
             };
+            const auto pair_back = [&]() {
+                if (!pair_out) return;
+                ok = ok && wait_bounded(bar(kPairEmpty + me), pair_ph, abort_word);
+                pair_out = 0;
+                pair_ph ^= 1;
+            };
+            const uint32_t idesc_full = make_idesc(128, kCols, false, F8);
             for (int ic = 0;; ++ic) {
                 Item I;
                 if (!next_item(ic, I)) break;
                 const int set = ic & 1;
                 const bool few = I.n_qt == 1;
-                const uint32_t stay = sb + kStay + set * 2 * kSlot;
+                const uint64_t stay = make_sdesc(sb + kStay + set * 2 * kSlot, 16, 1024);
                 if (!(ok = wait_bounded(bar(kStayUse + set), (ic >> 1) & 1, abort_word))) break;
-                const int n = few ? I.nt : I.n_qt - I.qt0;
-                for (int i = 0; i < n && ok; ++i) {
-                    if (!(ok = wait_bounded(bar(kStreamUse + st), ph, abort_word))) break;
-                    const uint32_t stage = sb + stage_at(st);
-                    if (few) {
-                        product(turn, stage, stay, I.n_q * p.g);
-                        turn = (turn + 1) & 3;
-                    } else {
-                        const int cols = min(kCols, (I.n_q - ((I.qt0 + i) << log2qt)) * p.g);
-                        for (int r = 0; r < I.nt && ok; ++r)
-                            product(r + 2 * (i & 1), stay + r * kSlot, stage, cols);
+                const int end = n + (few ? I.nt : I.n_qt - I.qt0);
+                const int last_cols = (I.n_q - ((I.n_qt - 1) << log2qt)) * p.g;
+                const uint32_t idesc_last = make_idesc(128, (last_cols + 15) & ~15, false, F8);
+                for (; n < end; ++n) {
+                    if ((n & 1) == me) {
+                        const uint64_t stage = make_sdesc(sb + stage_at(st), 16, 1024);
+                        pair_back();
+                        if (few) {
+                            const int h = n >> 1 & 1, acc = n & 3;
+                            few_back(h);
+                            if (!ok || !(ok = wait_bounded(bar(kStreamUse + fb), ph, abort_word)))
+                                break;
+                            tc_fence_after();
+                            issue_s_group<D>(1u, tmem + acc * kCols, stage, stay, idesc_last);
+                            tc_commit_if(1u, bar(kAccFull + acc));
+                            few_out |= 1u << h;
+                        } else {
+                            const uint32_t idesc = n + 1 == end ? idesc_last : idesc_full;
+                            few_back(0);
+                            few_back(1);
+                            if (!ok || !(ok = wait_bounded(bar(kStreamUse + fb), ph, abort_word)))
+                                break;
+                            tc_fence_after();
+                            issue_s_group<D>(1u, tmem + me * kCols, stay, stage, idesc);
+                            if (I.nt == 2)
+                                issue_s_group<D>(1u, tmem + (me + 2) * kCols, stay + (kSlot >> 4),
+                                                 stage, idesc);
+                            tc_commit_if(1u, bar(kPairFull + me));
+                            pair_out = 1;
+                        }
+                        tc_commit_if(1u, bar(kStreamEmpty + st));
                     }
-                    tc_commit_if(1u, bar(kStreamEmpty + st));
-                    if (++st == n_stages) {
-                        st = 0;
+                    if (++st == n_stages) st = 0;
+                    if (++fb == 2 * n_stages) {
+                        fb = 0;
                         ph ^= 1;
                     }
                 }
@@ -579,12 +623,12 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 tc_commit_if(1u, bar(kStayEmpty + set));
             }
             // every MMA has finished before TMEM is released
-            tc_commit_if(1u, bar(kDrain));
-            wait_drain(bar(kDrain), 0);
+            tc_commit_if(1u, bar(kDrain + me));
+            wait_drain(bar(kDrain + me), 0);
         }
     } else if (warp == 18) {
         // ------------------------------------------------ loader of what streams
-        int st = 0, ph = 1, n_done = 0, ok = 1;      // a fresh barrier's phase 1 counts as past
+        int st = 0, fb = 0, ph = 1, n_done = 0, ok = 1;   // a fresh barrier's phase 1 counts as past
         const int per_tile = kTileKeys >> log2bs, per_load = 32 / per_tile;   // blocks; tiles
         for (int ic = 0; ok; ++ic) {
             Item I;
@@ -603,7 +647,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 if (lane == 0) ok = wait_bounded(bar(kStreamEmpty + st), ph, abort_word);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
-                const uint32_t slot = sb + stage_at(st), full = bar(kStreamFull + st);
+                const uint32_t slot = sb + stage_at(st), full = bar(kStreamFull + fb);
                 if (few) {
                     const int nblk = blocks_of(I, I.t0 + i);
                     const int id = __shfl_sync(0xffffffffu, ids, (at * per_tile + lane) & 31);
@@ -614,6 +658,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     load_q(slot, full, I, I.qt0 + i);
                 }
                 ++n_done;
+                if (++fb == 2 * n_stages) fb = 0;
                 if (++st == n_stages) {
                     st = 0;
                     ph ^= 1;
@@ -622,8 +667,8 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         }
         if (lane == 0) {
             // never leave with copies in flight into this CTA's shared memory
-            for (int i = 0; i < min(n_done, n_stages); ++i)
-                wait_drain(bar(kStreamFull + i), ((n_done - 1 - i) / n_stages) & 1);
+            for (int i = max(0, n_done - n_stages); i < n_done; ++i)
+                wait_drain(bar(kStreamFull + i % (2 * n_stages)), (i / (2 * n_stages)) & 1);
         }
     } else if (warp == 19) {
         // ------------------------------------------------ log-sum-exps, negated, in base 2
@@ -656,14 +701,16 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                                       abort_word);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
-                *reinterpret_cast<float4*>(smem + kCtl + kLseOff + slot * 512 + lane * 16) = v;
+                float* to = reinterpret_cast<float*>(smem + kCtl + kLseOff) + slot * 128;
+                *reinterpret_cast<float2*>(to + lse_place(4 * lane)) = make_float2(v.x, v.y);
+                *reinterpret_cast<float2*>(to + lse_place(4 * lane + 2)) = make_float2(v.z, v.w);
                 mbar_arrive(bar(kLseFull + slot));
             }
         }
-    } else if (warp >= 20) {
+    } else if (warp >= kTurners) {
         // ------------------------------------------------ codes and q to f16 (fp8 cache)
         if constexpr (F8) {
-            const int w = warp - 20;
+            const int w = warp - kTurners;
             // the MMAs take f16 operands: 32 rows a warp of a K tile's codes are expanded, or of a
             // query tile rounded in place (a 16-byte chunk keeps its place, so the swizzle holds)
             const auto turn_k = [&](uint32_t slot, const Item& I, int t) {
@@ -679,7 +726,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                                  bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
                 }
             };
-            int st = 0, ph = 0;
+            int st = 0, fb = 0, ph = 0;
             bool ok = true;
             for (int ic = 0; ok; ++ic) {
                 Item I;
@@ -695,14 +742,15 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 mbar_arrive(bar(kStayReady + set));
                 const int n = few ? I.nt : I.n_qt - I.qt0;
                 for (int i = 0; i < n; ++i) {
-                    if (!(ok = wait_bounded(bar(kStreamFull + st), ph, abort_word))) break;
+                    if (!(ok = wait_bounded(bar(kStreamFull + fb), ph, abort_word))) break;
                     const uint32_t slot = sb + stage_at(st);
                     if (few) turn_k(slot, I, I.t0 + i);
                     else turn_q(slot, kCols);
                     fence_proxy_async();
-                    mbar_arrive(bar(kStreamReady + st));
-                    if (++st == n_stages) {
-                        st = 0;
+                    mbar_arrive(bar(kStreamReady + fb));
+                    if (++st == n_stages) st = 0;
+                    if (++fb == 2 * n_stages) {
+                        fb = 0;
                         ph ^= 1;
                     }
                 }
@@ -710,68 +758,92 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         }
     } else {
         // ------------------------------------------------ epilogue warpgroups
-        const int w = warp >> 2;
-        const uint32_t tm = tmem + w * kCols + (uint32_t(32 * (warp & 3)) << 16);
-        const int key_in_tile = 32 * (warp & 3) + lane;
+        const int w = warp >> 2;             // FEW: accumulator w; MANY: the pair's key tile w >> 1,
+                                             // columns 64 (w & 1) .. + 63
+        const uint32_t tm = tmem + (uint32_t(32 * (warp & 3)) << 16);
+        const int q4 = lane & 3, rs = lane >> 2;
+        // after the sums over the four threads of a key have met, thread q4 has key rs + 8 q4
+        const int key_in_tile = 32 * (warp & 3) + rs + 8 * q4;
         const uint64_t c2 = f2(p.c, p.c);
-        int acc_ph = 0, turn = 0, n_lse = 0, n_part = 0;
+        int n = 0, few_ph = 0, pair_ph = 0, n_lse = 0, n_part = 0;
         bool ok = true;
-        const float4* lse_smem = reinterpret_cast<const float4*>(smem + kCtl + kLseOff);
-        float* part = reinterpret_cast<float*>(smem + kCtl + kPartOff) + (w & 1) * 128;
-        // the sum over the columns of this warpgroup's next product: query rows from position
-        // `at` on, `cols` columns, key j
-        const auto column_sum = [&](const float4* nl, int cols, int at, int j, int tile_end,
-                                    float& sum) {
-            if (!(ok = wait_bounded(bar(kAccFull + w), acc_ph, abort_word))) return;
-            acc_ph ^= 1;
+        const float4* lse_smem = reinterpret_cast<const float4*>(smem + kCtl + kLseOff) + q4;
+        float* part = reinterpret_cast<float*>(smem + kCtl + kPartOff) + (w >> 1) * 128;
+        uint64_t a[4];                       // the thread's part of its four keys' sums
+        const auto clear = [&]() {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a[k] = f2(0.f, 0.f);
+        };
+        // adds columns c0 .. c1 - 1 of the accumulator at ta: query rows from position `at` on, the
+        // warp's keys from `kw` on; `empty` takes the accumulator back
+        const auto add_columns = [&](uint32_t ta, const float4* nl, int c0, int c1, int at, int kw,
+                                     uint32_t empty) {
             tc_fence_after();
-            uint64_t a[4];
+            if (c1 - c0 == 64 && kw + 31 <= at) {
+                ta += c0;
+                nl += c0 / 4;
+                uint32_t lo0[8], hi0[8], lo1[8], hi1[8];
+                tmem_ld_16x256b_x2(ta, lo0);
+                tmem_ld_16x256b_x2(ta + (16u << 16), hi0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = f2(0.f, 0.f);
-            if (cols == kCols && tile_end <= at + 1) {
-                uint32_t s0[16], s1[16];
-                tmem_ld_32x32b_x16(tm, s0);
-#pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
+                for (int c = 0; c < 64; c += 32) {
                     tmem_wait_ld();
-                    tmem_ld_32x32b_x16(tm + c + 16, s1);
-                    add16(s0, nl + c / 4, c2, a);
+                    tmem_ld_16x256b_x2(ta + c + 16, lo1);
+                    tmem_ld_16x256b_x2(ta + c + 16 + (16u << 16), hi1);
+                    add16(lo0, hi0, nl[c / 4], c2, a);
                     tmem_wait_ld();
-                    if (c + 32 < kCols) {
-                        tmem_ld_32x32b_x16(tm + c + 32, s0);
+                    if (c + 32 < 64) {
+                        tmem_ld_16x256b_x2(ta + c + 32, lo0);
+                        tmem_ld_16x256b_x2(ta + c + 32 + (16u << 16), hi0);
                     } else {
                         tc_fence_before();
-                        mbar_arrive(bar(kAccEmpty + w));
+                        mbar_arrive(empty);
                     }
-                    add16(s1, nl + c / 4 + 4, c2, a);
+                    add16(lo1, hi1, nl[c / 4 + 4], c2, a);
                 }
-            } else {
-                // the first column whose row comes at or after the key
-                const int from = max(0, j - at) << (7 - log2qt);
-                for (int c = 0; c < cols; c += 16) {
-                    uint32_t s[16];
-                    tmem_ld_32x32b_x16(tm + c, s);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 n = nl[(c + i) / 4];
-                        const float v[4] = {n.x, n.y, n.z, n.w};
-                        float e[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float x = ex2(fmaf(__uint_as_float(s[i + k]), p.c, v[k]));
-                            e[k] = c + i + k >= from && c + i + k < cols ? x : 0.f;
-                        }
-                        a[0] = add2(a[0], f2(e[0], e[1]));
-                        a[1] = add2(a[1], f2(e[2], e[3]));
-                    }
-                }
-                tc_fence_before();
-                mbar_arrive(bar(kAccEmpty + w));
+                return;
             }
-            float x0, x1;
-            f2_split(add2(add2(a[0], a[1]), add2(a[2], a[3])), x0, x1);
-            sum += x0 + x1;
+            for (int c = c0; c < c1; c += 16) {
+                uint32_t lo[8], hi[8];
+                tmem_ld_16x256b_x2(ta + c, lo);
+                tmem_ld_16x256b_x2(ta + c + (16u << 16), hi);
+                const float4 l = nl[c / 4];
+                const float nv[4] = {l.x, l.y, l.z, l.w};
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // the first column whose row comes at or after the key
+                    const int from = max(0, kw + rs + 8 * k - at) << (7 - log2qt);
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) {
+                        const uint32_t* s = (k < 2 ? lo : hi) + 4 * cc + 2 * (k & 1);
+                        float e[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int col = c + 8 * cc + 2 * q4 + i;
+                            const float x = ex2(fmaf(__uint_as_float(s[i]), p.c, nv[2 * cc + i]));
+                            e[i] = col >= from && col < c1 ? x : 0.f;
+                        }
+                        a[k] = add2(a[k], f2(e[0], e[1]));
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(empty);
+        };
+        // the sum of key key_in_tile
+        const auto total_of_key = [&]() {
+            float mine = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float x0, x1;
+                f2_split(a[k], x0, x1);
+                float x = x0 + x1;
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                if (q4 == k) mine = x;
+            }
+            return mine;
         };
         for (int ic = 0; ok; ++ic) {
             Item I;
@@ -784,41 +856,49 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             if (I.n_qt == 1) {
                 if (!wait_lse()) break;
                 const float4* nl = lse_smem + (n_lse % kLseSlots) * 32;
-                for (int i = 0; i < I.nt; ++i) {
-                    const bool my = turn == w;
-                    turn = (turn + 1) & 3;
-                    if (!my) continue;
+                // the item's first tile of this warpgroup, then every fourth
+                for (int i = (w - n) & 3; i < I.nt; i += 4) {
                     const int kb = (I.t0 + i) * kTileKeys, j = kb + key_in_tile;
                     float* dst = p.weights + I.state + j;
                     const float old = j < I.held ? *dst : 0.f;
-                    float sum = 0.f;
-                    column_sum(nl, I.n_q * p.g, I.pos0, j, kb + kTileKeys, sum);
-                    if (!ok) break;
+                    if (!(ok = wait_bounded(bar(kAccFull + w), few_ph, abort_word))) break;
+                    few_ph ^= 1;
+                    clear();
+                    add_columns(tm + w * kCols, nl, 0, I.n_q * p.g, I.pos0, kb + 32 * (warp & 3),
+                                bar(kAccEmpty + w));
+                    const float sum = total_of_key();
                     if (j < I.ctx) *dst = old + sum;
                 }
                 if (!ok) break;
+                n += I.nt;
                 done_lse();
                 continue;
             }
-            // the tile w & 1 of the pair; its query tiles alternate between warpgroups w and w ^ 2
-            const int r = w & 1;
+            const int r = w >> 1, c0 = 64 * (w & 1);
             const bool my = r < I.nt;
             const int kb = (I.t0 + r) * kTileKeys, j = kb + key_in_tile;
             float* dst = p.weights + I.state + j;
-            const float old = my && w < 2 && j < I.held ? *dst : 0.f;
-            float sum = 0.f;
-            for (int qt = I.qt0; qt < I.n_qt; ++qt) {
+            const float old = my && !(w & 1) && j < I.held ? *dst : 0.f;
+            clear();
+            for (int qt = I.qt0; qt < I.n_qt; ++qt, ++n) {
                 if (!wait_lse()) break;
-                if (my && ((qt - I.qt0) & 1) == w >> 1)
-                    column_sum(lse_smem + (n_lse % kLseSlots) * 32,
-                               min(kCols, (I.n_q - (qt << log2qt)) * p.g),
-                               I.pos0 + (qt << log2qt), j, kb + kTileKeys, sum);
-                if (!ok) break;
+                const int pair = n & 1;
+                if (!(ok = wait_bounded(bar(kPairFull + pair), pair_ph >> pair & 1, abort_word)))
+                    break;
+                pair_ph ^= 1 << pair;
+                const int c1 = min(c0 + 64, (I.n_q - (qt << log2qt)) * p.g);
+                if (my && c0 < c1)
+                    add_columns(tm + (pair + 2 * r) * kCols, lse_smem + (n_lse % kLseSlots) * 32, c0,
+                                c1, I.pos0 + (qt << log2qt), kb + 32 * (warp & 3),
+                                bar(kPairEmpty + pair));
+                else
+                    mbar_arrive(bar(kPairEmpty + pair));
                 done_lse();
             }
             if (!ok) break;
             if (!my) continue;
-            if (w >= 2) {
+            const float sum = total_of_key();
+            if (w & 1) {
                 if (n_part > 0 &&
                     !(ok = wait_bounded(bar(kPartEmpty + r), (n_part - 1) & 1, abort_word)))
                     break;
@@ -826,9 +906,9 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 mbar_arrive(bar(kPartFull + r));
             } else {
                 if (!(ok = wait_bounded(bar(kPartFull + r), n_part & 1, abort_word))) break;
-                sum += part[key_in_tile];
+                const float all = sum + part[key_in_tile];
                 mbar_arrive(bar(kPartEmpty + r));
-                if (j < I.ctx) *dst = old + sum;
+                if (j < I.ctx) *dst = old + all;
             }
             ++n_part;
         }
