@@ -17,25 +17,24 @@
 //   FEW   all its columns fit one query tile (n_q * g <= 128; a decode row among them): the query
 //         tile stays, key tiles stream past it. Bound by the read of K (a 32 KB tile per 128 keys
 //         against 16 .. 128 MMA columns); K is read once, no other pass touches it.
-//   MANY  a prefill chunk: one or two key tiles stay, query tiles (128 columns) stream past them
-//         from L2. Bound by the tensor pipe and the exponentials (per element one fused
-//         multiply-add and one addition, packed in pairs, and one ex2).
+//   MANY  a prefill chunk: up to four key tiles stay, query tiles (128 columns) stream past them from
+//         L2. Bound by the tensor pipe and the exponentials (per element one fused multiply-add and
+//         one addition, packed in pairs, and one ex2). With two key tiles staying, the 32 KB a query
+//         tile takes out of L2 for each of their products was what bound it.
 // Work is dealt by cost, on the device: every (sequence, KV head, key tile) in order has a cost
-// (4 for a FEW tile, 2 for each query tile a MANY tile meets), CTA c takes the tiles that start in
-// its 1/G of the total. No plan is made or uploaded, so a captured graph needs nothing renewed but
-// its metadata.
+// (kCostFew for a FEW tile, kCostMany for each query tile a MANY tile meets), CTA c takes the tiles
+// that start in its 1/G of the total. No plan is made or uploaded, so a captured graph needs nothing
+// renewed but its metadata.
 //
-// Warps: 0-15 four epilogue warpgroups, 16 scheduler and loader of what stays, 17 and 20 MMA issuers,
-// 18 loader of what streams, 19 log-sum-exps; over an fp8 cache 24-27 turn codes and q to f16. The
-// stream's tiles alternate between the two issuers, each with two of the four accumulators (128
-// TMEM columns each): an issuer's waits, commits and address arithmetic, made slow by the warps it
-// shares its scheduler with, run while the other's MMAs keep the tensor pipe busy (one issuer left
-// it idle for more than half of the time). FEW: each tile has one accumulator and one warpgroup.
-// MANY: a query tile has an accumulator for each of its two key tiles, and each of these is read by
-// two warpgroups, 64 columns each, whose sums meet in shared memory at the item's end.
-// Shared memory: seven 32 KB slots. Two sets of two for what stays (an item loads while the one
-// before it runs) and three stages for what streams; where no sequence is MANY, each set is one
-// slot, and the two others are stages as well (five tiles of K in flight). Every wait is bounded.
+// Warps: 0-15 four epilogue warpgroups, 16 scheduler and loader of what stays, 17 and 19 MMA issuers,
+// 18 loader of what streams; over an fp8 cache 20-23 turn codes and q to f16. There are four
+// accumulators of 128 TMEM columns, warpgroup w reads accumulator w: FEW's stream tiles take them in
+// turn, a MANY item's key tile r has accumulator r. Issuer i fills accumulators i and i + 2: its
+// waits, commits and address arithmetic, made slow by the warps it shares its scheduler with, run
+// while the other's MMAs keep the tensor pipe busy.
+// Shared memory: seven 32 KB slots. Four in a ring for what stays (the next item's tiles load as this
+// one's are done with) and three stages for what streams; where no sequence is MANY, two for what
+// stays and five stages (five tiles of K in flight). Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -53,56 +52,55 @@ using namespace pa_detail;
 
 namespace {
 
-constexpr int kBaseThreads = 672;
+constexpr int kBaseThreads = 640;
 template <bool F8>
 constexpr int kThreadsFor = F8 ? kBaseThreads + 128 : kBaseThreads;
 constexpr int kTurners = kBaseThreads / 32;    // the first f16 warp of an fp8 cache
 constexpr int kCols = 128;                     // columns of a query tile
 constexpr int kSlot = 32768;                   // one tile, 128 rows of D = 128
 constexpr int kHalf = 16384;                   // its 64-column halves
-constexpr int kStay = 0;                       // 2 sets x 2 slots
 constexpr int kMaxStages = 5;
 constexpr int kCtl = 7 * kSlot;
 constexpr int kBytes = kCtl + 3072;
 static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
-constexpr int kLseSlots = 2;
 constexpr int kMaxRows = 1 << 18;              // state rows whose repeats are looked for
-constexpr int64_t kCostFew = 4, kCostMany = 2; // of a key tile; of a key tile and query tile
+constexpr int kMaxSeqs = 8192;                 // sequences whose costs are held while they are dealt
+// before the pipeline starts: a bit per state row in slots 0 and 1, a cost per sequence from slot 4
+constexpr int kCosts = 4 * kSlot;
+static_assert(kMaxRows / 8 <= 2 * kSlot && kMaxSeqs * 8 <= 3 * kSlot, "scratch of the deal");
+constexpr int64_t kCostFew = 5, kCostMany = 2; // of a key tile; of a key tile and query tile
 
-// Stream tile n (counted over all items) has stage n % n_stages and issuer n % 2. The barriers that
-// issuers wait on for it are numbered n % (2 n_stages), n_stages being odd: each is only ever waited
-// on by one of them, which keeps its parity's meaning sound.
+// A role that waits on a barrier waits for each of its phases in turn: parity tells only neighbours
+// apart. Warps arrive once, not 32 times.
 enum Bar {
-    kStayFull = 0,     // + set: TMA -> issuers (or the f16 warps)
-    kStayEmpty = 2,    // + set: both issuers -> loader
-    kStreamFull = 4,   // + n % (2 n_stages)
-    kStreamEmpty = 14, // + stage: its issuer -> loader
-    kAccFull = 19,     // + accumulator, FEW: issuer -> its warpgroup
-    kAccEmpty = 23,    // + accumulator, FEW: 128 arrivals -> issuer
-    kPairFull = 27,    // + n % 2, MANY: issuer -> the warpgroups (one for both key tiles)
-    kPairEmpty = 29,   // + n % 2, MANY: 512 arrivals -> issuer
-    kLseFull = 31,     // + slot: 32 arrivals -> the warpgroups
-    kLseEmpty = 33,    // + slot: 512 arrivals
-    kItemFull = 35,    // + slot (4)
-    kItemEmpty = 39,   // + slot: every consumer thread
-    kPartFull = 43,    // + key tile of a pair: 128 arrivals, its second warpgroup -> its first
-    kPartEmpty = 45,   // + key tile: 128 arrivals
-    kDrain = 47,       // + issuer
-    kStayReady = 49,   // + set, fp8 only: 128 arrivals of the f16 warps
-    kStreamReady = 51, // + n % (2 n_stages)
-    kNumBars = 61
+    kStayFull = 0,     // + slot: TMA -> issuers (or the f16 warps)
+    kStayEmpty = 4,    // + slot: both issuers -> loader
+    kStreamFull = 8,   // + stage: TMA -> issuers (or the f16 warps)
+    kStreamEmpty = 13, // + stage: both issuers -> loader
+    kAccFull = 18,     // + accumulator: its issuer -> its warpgroup
+    kAccEmpty = 22,    // + accumulator: 4 arrivals -> its issuer
+    kLseFull = 26,     // + slot (4), MANY: the stream's loader -> the warpgroups
+    kLseEmpty = 30,    // + slot, MANY: 16 arrivals
+    kItemFull = 34,    // + slot (4)
+    kItemEmpty = 38,   // + slot: every consumer warp
+    kDrain = 42,       // + issuer
+    kStayReady = 44,   // + slot, fp8 only: 4 arrivals of the f16 warps
+    kStreamReady = 48, // + stage
+    kNumBars = 53
 };
 constexpr int kHolderOff = 8 * kNumBars;
 constexpr int kAbortOff = kHolderOff + 4;
-constexpr int kRingOff = 512;                  // 4 items of 64 bytes
-constexpr int kLseOff = kRingOff + 4 * 64;     // kLseSlots x 128 floats
-constexpr int kPartOff = kLseOff + kLseSlots * 512;   // 2 x 128 floats
-constexpr int kScanOff = kLseOff;              // before the pipeline starts
-static_assert(kAbortOff + 4 <= kRingOff && kPartOff + 2 * 512 <= 3072, "control area");
+constexpr int kRingOff = 448;                  // 4 items of 64 bytes
+constexpr int kLseOff = kRingOff + 4 * 64;     // MANY: 4 x 128 log-sum-exps
+constexpr int kTwiceOff = kLseOff + 4 * 512;   // whether some state row is named twice
+static_assert(kAbortOff + 4 <= kRingOff && kTwiceOff + 4 <= 3072, "control area");
 
-// Stage st of the stream: slots 4, 5, 6, and without MANY sequences the sets' second slots 1, 3.
+// Slots of stage st of the stream, and of tile k of what stays.
 __device__ __forceinline__ uint32_t stage_at(int st) {
     return uint32_t(st < 3 ? 4 + st : st == 3 ? 1 : 3) * kSlot;
+}
+__device__ __forceinline__ uint32_t stay_at(int s, int n_stay) {
+    return uint32_t(n_stay == 4 ? s : 2 * s) * kSlot;
 }
 
 struct Params {
@@ -123,6 +121,7 @@ struct Params {
 // metadata that does not fit, which sets bad).
 struct Seq {
     int n_q, ctx, pos0, cu0, row, held;
+    bool any;                    // it has query rows
     int n_tiles, n_qt;           // key tiles; query tiles
     bool few, bad;
     int64_t head_cost;
@@ -143,14 +142,19 @@ __device__ __forceinline__ int64_t cost_before(const Seq& q, int t, int log2qt) 
     return kCostMany * f;
 }
 
+// Quotients of costs: nearly always of 32 bits.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 // The first tile whose start is at or behind x.
 __device__ __forceinline__ int tile_at(const Seq& q, int64_t x, int log2qt) {
     if (x <= 0) return 0;
     if (x >= q.head_cost) return q.n_tiles;
-    if (q.few) return int((x + kCostFew - 1) / kCostFew);
+    if (q.few) return int(quot(x + kCostFew - 1, kCostFew));
     const int u = min(q.n_tiles, (q.pos0 + (1 << log2qt) - 1) / kTileKeys + 1);
     const int64_t per = kCostMany * q.n_qt;
-    if (x <= per * u) return int((x + per - 1) / per);
+    if (x <= per * u) return int(quot(x + per - 1, per));
     int64_t f = per * u;
     int t = u;
     for (; t < q.n_tiles && f < x; ++t) f += kCostMany * (q.n_qt - first_qt(q, t, log2qt));
@@ -172,7 +176,9 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt, bool
     q.ctx = p.ctx[s];
     const int64_t n = int64_t(c1) - c0;
     q.bad = false;
+    q.few = true;
     q.head_cost = 0;
+    q.any = n != 0;
     if (n == 0 || q.row < 0 || (p.skip_decode && n == 1)) return q;
     q.n_q = int(n);
     q.cu0 = c0;
@@ -192,7 +198,7 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt, bool
 }
 
 // One unit of work, published by the scheduler: FEW: query tile 0 against key tiles t0 .. t0 + nt
-// - 1; MANY: key tiles t0 (and t0 + 1 with nt 2) against query tiles qt0 .. n_qt - 1.
+// - 1; MANY: key tiles t0 .. t0 + nt - 1 (nt <= 4) against query tiles qt0 .. n_qt - 1.
 struct Item {
     int seq, kvh, t0, nt, qt0, n_qt, cu0, n_q, pos0, ctx, held, last;
     int64_t state;               // index of entry 0 in weights
@@ -217,10 +223,11 @@ __device__ __forceinline__ int lse_place(int col) {
 
 // A thread's share of 16 columns for the 32 keys of its warp (tcgen05.ld 16x256b, the lower and
 // the upper 16 lanes): keys rs + 8 k (rs = lane / 4, k = 0 .. 3) and columns 8 cc + 2 q4 + {0, 1}
-// (q4 = lane % 4, cc = 0, 1). One 16-byte read of log-sum-exps so serves 16 elements: with a lane
-// per key it served four, and those reads took a quarter of the shared-memory bandwidth that the
-// MMAs' operands need. Adds 2^(s c + n) to the packed sum of each of the four keys.
-__device__ __forceinline__ void add16(const uint32_t (&lo)[8], const uint32_t (&hi)[8], float4 n,
+// (q4 = lane % 4, cc = 0, 1). One 16-byte read of log-sum-exps (n, negated, in base 2) so serves 16
+// elements: with a lane per key it served four, and those reads took a quarter of the shared-memory
+// bandwidth that the MMAs' operands need. Adds 2^(s c + n) to the packed sum of each of the four
+// keys.
+__device__ __forceinline__ void add16(const uint32_t* lo, const uint32_t* hi, float4 n,
                                       uint64_t c2, uint64_t (&a)[4]) {
 #pragma unroll
     for (int cc = 0; cc < 2; ++cc) {
@@ -288,19 +295,19 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < kNumBars; ++b)
-            mbar_init(bar(b), b >= kStayReady                         ? 128
-                              : b >= kDrain                           ? 1
-                              : b >= kPartFull                        ? 128
-                              // issuers 2, stream loader and log-sum-exps 64, epilogue 512, f16 128
-                              : b >= kItemEmpty                       ? 2 + 64 + 512 + (F8 ? 128 : 0)
-                              : b >= kItemFull                        ? 1
-                              : b >= kLseEmpty                        ? 512
-                              : b >= kLseFull                         ? 32
-                              : b >= kPairEmpty                       ? 512
-                              : b >= kPairFull                        ? 1
-                              : b >= kAccEmpty                        ? 128
-                              : b >= kStayEmpty && b < kStreamFull    ? 2
-                                                                      : 1);
+            mbar_init(bar(b), b >= kStayReady                             ? 4
+                              : b >= kDrain                               ? 1
+                              // issuers 2, stream loader 1, epilogue 16, f16 4
+                              : b >= kItemEmpty                           ? 2 + 1 + 16 + (F8 ? 4 : 0)
+                              : b >= kItemFull                            ? 1
+                              : b >= kLseEmpty                            ? 16
+                              : b >= kLseFull                             ? 1
+                              : b >= kAccEmpty                            ? 4
+                              : b >= kAccFull                             ? 1
+                              : b >= kStreamEmpty                         ? 2
+                              : b >= kStreamFull                          ? 1
+                              : b >= kStayEmpty                           ? 2
+                                                                          : 1);
         *abort_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -311,111 +318,56 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    uint32_t* once = reinterpret_cast<uint32_t*>(smem);
+    int64_t* costs = reinterpret_cast<int64_t*>(smem + kCosts);
+    volatile int* repeated = reinterpret_cast<volatile int*>(smem + kCtl + kTwiceOff);
+    if (p.rows)
+        for (int i = threadIdx.x; i < (p.n_rows + 31) / 32; i += kThreads) once[i] = 0;
+    if (threadIdx.x == 0) *repeated = 0;
+    if (warp == 18 && lane < 3)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(
+                         lane == 0 ? &tm_k : lane == 1 ? &tm_q1 : &tm_qn))
+                     : "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kCtl + kHolderOff);
     // a programmatic dependent: nothing the kernel before it wrote is read before this point
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---- this CTA's share: repeated state rows, the total cost, where the share starts
-    uint32_t* once = reinterpret_cast<uint32_t*>(smem + kStay);
-    int64_t* scan = reinterpret_cast<int64_t*>(smem + kCtl + kScanOff);   // [32] warps
-    int64_t* found = scan + 32;                      // start offset of the first sequence
-    int* found_s = reinterpret_cast<int*>(scan + 33);
-    int* repeated = found_s + 1;
-    if (threadIdx.x == 0) {
-        *found_s = p.B;
-        *found = 0;
-        *repeated = 0;
-    }
-    if (p.rows)
-        for (int i = threadIdx.x; i < (p.n_rows + 31) / 32; i += kThreads) once[i] = 0;
-    // the first round's metadata, read before the barriers
-    Seq mine_seq;
-    mine_seq.head_cost = 0;
-    mine_seq.bad = false;
-    mine_seq.few = true;
-    if (int(threadIdx.x) < p.B) mine_seq = load_seq(p, int(threadIdx.x), log2qt, false);
-    __syncthreads();
-    if (p.rows) {
+    // ---- every sequence's cost, and whether two name one state row
+    int n_stages;
+    {
+        bool bad = false, some_many = false;
         for (int s = threadIdx.x; s < p.B; s += kThreads) {
-            const int row = p.rows[s];
-            if (row < 0 || row >= p.n_rows || p.cu[s + 1] == p.cu[s]) continue;
-            const uint32_t bit = 1u << (row & 31);
-            if (atomicOr(once + (row >> 5), bit) & bit) *repeated = 1;
-        }
-        __syncthreads();
-    }
-    const bool twice = *repeated != 0;
-    int64_t total = 0;
-    bool bad = false, some_many = false;
-    // inclusive sums over the sequences of one round of kThreads; returns the thread's own
-    const auto round_scan = [&](int64_t x, int64_t& sum) {
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
-        }
-        __syncthreads();
-        if (lane == 31) scan[warp] = x;
-        __syncthreads();
-        sum = 0;
-        int64_t before = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w == warp) before = sum;
-            sum += scan[w];
-        }
-        return x + before;
-    };
-    int64_t mine = 0, upto = 0;
-    for (int s0 = 0; s0 < p.B; s0 += kThreads) {
-        const int s = s0 + int(threadIdx.x);
-        mine = 0;
-        if (s < p.B) {
-            const Seq q = s0 == 0 && !twice ? mine_seq : load_seq(p, s, log2qt, twice);
-            mine = q.head_cost * p.Hkv;
+            const Seq q = load_seq(p, s, log2qt, false);
+            if (p.rows && q.row >= 0 && q.row < p.n_rows && q.any) {
+                const uint32_t bit = 1u << (q.row & 31);
+                if (atomicOr(once + (q.row >> 5), bit) & bit) *repeated = 1;
+            }
+            costs[s] = q.head_cost;
             bad = bad || q.bad;
             some_many = some_many || (q.head_cost > 0 && !q.few);
         }
-        int64_t sum;
-        upto = round_scan(mine, sum) + total;
-        total += sum;
+        if (bad && blockIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+        // these words were written through the generic proxy where TMA writes next
+        fence_proxy_async();
+        n_stages = __syncthreads_or(some_many) ? 3 : kMaxStages;
     }
-    if (bad && blockIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
-    const int64_t lo = total * int64_t(blockIdx.x) / int64_t(gridDim.x);
-    const int64_t hi = total * (int64_t(blockIdx.x) + 1) / int64_t(gridDim.x);
-    if (p.B <= kThreads) {
-        if (mine > 0 && upto - mine <= lo && lo < upto) {
-            *found_s = int(threadIdx.x);
-            *found = upto - mine;
-        }
-    } else if (lo < hi) {
-        int64_t run = 0;
-        for (int s0 = 0; s0 < p.B && run <= lo; s0 += kThreads) {
-            const int s = s0 + int(threadIdx.x);
-            mine = s < p.B ? load_seq(p, s, log2qt, twice).head_cost * p.Hkv : 0;
-            int64_t sum;
-            upto = round_scan(mine, sum) + run;
-            if (mine > 0 && upto - mine <= lo && lo < upto) {
-                *found_s = s;
-                *found = upto - mine;
-            }
-            run += sum;
-        }
-    }
-    // the rows' bits were written through the generic proxy where TMA writes next
-    fence_proxy_async();
-    tc_fence_before();
-    const int n_stages = __syncthreads_or(some_many) ? 3 : kMaxStages;
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kCtl + kHolderOff);
-    const int start_s = *reinterpret_cast<volatile int*>(found_s);
-    const int64_t start_at = *reinterpret_cast<volatile int64_t*>(found);
-    __syncthreads();                                 // the scan's words belong to the ring now
+    const int n_stay = n_stages == 3 ? 4 : 2;
 
     volatile Item* ring = reinterpret_cast<volatile Item*>(smem + kCtl + kRingOff);
-    // takes the next item: every consumer thread (or the one lane that stands for a warp) calls it
-    const auto next_item = [&](int ic, Item& I) {
+    // a whole warp's arrival, after what its lanes have read or written
+    const auto warp_arrive = [&](uint32_t b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b);
+    };
+    // takes the next item; called by whole warps, or by the one lane that stands for an issuer's
+    const auto next_item = [&](int ic, Item& I, bool alone = false) {
         if (!wait_bounded(bar(kItemFull + (ic & 3)), (ic >> 2) & 1, abort_word)) return false;
         I = read_item(sb + kCtl + kRingOff + (ic & 3) * 64);
-        mbar_arrive(bar(kItemEmpty + (ic & 3)));
+        if (alone) mbar_arrive(bar(kItemEmpty + (ic & 3)));
+        else warp_arrive(bar(kItemEmpty + (ic & 3)));
         return I.last == 0;
     };
     // the K tile of key tile t into `slot` (all lanes; lane 0 has waited for the slot): one box per
@@ -458,6 +410,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     if (warp == 16) {
         // ------------------------------------------------ scheduler, loader of what stays
         int ic = 0, ok = 1;
+        int ks = 0, kph = 1, n_loaded = 0;               // next slot of what stays, parity, tiles so far
         // publishes an item and loads its query tile or key tiles
         const auto emit = [&](Item& I, bool few) {
             if (lane == 0) {
@@ -483,29 +436,60 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok || I.last) return;
-            const int set = ic & 1;
-            int id[2] = {-1, -1};
-            if (!few)
-                for (int r = 0; r < I.nt; ++r) id[r] = block_id(I, I.t0 + r, I.t0 + r + 1);
-            if (lane == 0 && ic >= 2)
-                ok = wait_bounded(bar(kStayEmpty + set), ((ic >> 1) - 1) & 1, abort_word);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) return;
-            const uint32_t slot = sb + kStay + set * 2 * kSlot;
-            if (few) {
-                if (lane == 0) load_q(slot, bar(kStayFull + set), I, 0);
-            } else {
-                // one barrier for both tiles: its one arrival carries the bytes of both
-                const int n0 = blocks_of(I, I.t0), n1 = I.nt == 2 ? blocks_of(I, I.t0 + 1) : 0;
-                if (lane == 0) mbar_expect_tx(bar(kStayFull + set), k_bytes(n0 + n1));
-                __syncwarp();
-                load_k(slot, bar(kStayFull + set), I, n0, id[0]);
-                load_k(slot + kSlot, bar(kStayFull + set), I, n1, id[1]);
-            }
             ++ic;
+            for (int r = 0; r < (few ? 1 : I.nt); ++r) {
+                const int id = few ? -1 : block_id(I, I.t0 + r, I.t0 + r + 1);
+                if (lane == 0) ok = wait_bounded(bar(kStayEmpty + ks), kph, abort_word);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) return;
+                const uint32_t slot = sb + stay_at(ks, n_stay), full = bar(kStayFull + ks);
+                if (few) {
+                    if (lane == 0) load_q(slot, full, I, 0);
+                } else {
+                    const int nblk = blocks_of(I, I.t0 + r);
+                    if (lane == 0) mbar_expect_tx(full, k_bytes(nblk));
+                    __syncwarp();
+                    load_k(slot, full, I, nblk, id);
+                }
+                ++n_loaded;
+                if (++ks == n_stay) {
+                    ks = 0;
+                    kph ^= 1;
+                }
+            }
         };
-        int64_t base = start_at;
-        for (int s = start_s; s < p.B && base < hi && ok; ++s) {
+        // ---- the share: this CTA's range of the total cost, and the sequence it starts in
+        const bool twice = *repeated != 0;
+        if (twice) {                                 // rare: those that share a row drop out
+            for (int s = lane; s < p.B; s += 32) {
+                const Seq q = load_seq(p, s, log2qt, true);
+                costs[s] = q.head_cost;
+                if (q.bad && blockIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+            }
+            fence_proxy_async();
+            __syncwarp();
+        }
+        const int per = (p.B + 31) / 32;             // sequences a lane adds up
+        int64_t mine = 0;
+        for (int i = 0, s = lane * per; i < per && s < p.B; ++i, ++s) mine += costs[s];
+        int64_t upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += y;
+        }
+        const int64_t total = __shfl_sync(0xffffffffu, upto, 31) * p.Hkv;
+        const int64_t each = quot(total, gridDim.x), rest = total - each * gridDim.x;
+        const auto bound = [&](int c) { return each * c + int64_t(uint32_t(rest) * c / gridDim.x); };
+        const int64_t lo = bound(int(blockIdx.x)), hi = bound(int(blockIdx.x) + 1);
+        // the last lane whose sequences start at or before lo
+        const uint32_t before = __ballot_sync(0xffffffffu, (upto - mine) * p.Hkv <= lo);
+        const int from = 31 - __clz(before);
+        int64_t base = __shfl_sync(0xffffffffu, upto - mine, from) * p.Hkv;
+        int first_s = from * per;
+        while (first_s < p.B && base + costs[first_s] * p.Hkv <= lo) base += costs[first_s++] * p.Hkv;
+        __syncwarp();                                // the costs make room for what streams
+        for (int s = first_s; s < p.B && base < hi && ok; ++s) {
             const Seq q = load_seq(p, s, log2qt, twice);
             if (q.head_cost == 0) continue;
             Item I;
@@ -517,7 +501,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             I.held = q.held;
             I.last = 0;
             I.n_qt = q.n_qt;
-            for (int h = base < lo ? int((lo - base) / q.head_cost) : 0; h < p.Hkv && ok; ++h) {
+            for (int h = base < lo ? int(quot(lo - base, q.head_cost)) : 0; h < p.Hkv && ok; ++h) {
                 const int64_t hb = base + h * q.head_cost;
                 if (hb >= hi) break;
                 const int ta = tile_at(q, lo - hb, log2qt), tb = tile_at(q, hi - hb, log2qt);
@@ -530,9 +514,11 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     I.qt0 = 0;
                     emit(I, true);
                 } else {
-                    for (int t = ta; t < tb && ok; t += 2) {
+                    // as few items as hold the tiles, of even sizes
+                    int items = (tb - ta + 3) / 4;
+                    for (int t = ta; t < tb && ok; t += I.nt, --items) {
                         I.t0 = t;
-                        I.nt = min(2, tb - t);
+                        I.nt = (tb - t + items - 1) / items;
                         I.qt0 = first_qt(q, t, log2qt);
                         emit(I, false);
                     }
@@ -548,79 +534,85 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         }
         if (lane == 0) {
             // never leave with copies in flight into this CTA's shared memory
-            for (int i = max(0, ic - 2); i < ic; ++i)
-                wait_drain(bar(kStayFull + (i & 1)), (i >> 1) & 1);
+            for (int i = max(0, n_loaded - n_stay); i < n_loaded; ++i)
+                wait_drain(bar(kStayFull + i % n_stay), (i / n_stay) & 1);
         }
-    } else if (warp == 17 || warp == 20) {
+    } else if (warp == 17 || warp == 19) {
         // ------------------------------------------------ MMA issuers
         if (lane == 0) {
-            const int me = warp == 20;           // takes the stream tiles n with n % 2 == me
-            int n = 0, st = 0, fb = 0;           // stream tile, its stage and full barrier
-            uint32_t ph = 0;                     // parity of the barriers of this turn of fb
-            // accumulators me, me + 2 (FEW) or both (MANY) handed to the epilogue and not seen back,
-            // and the parity of their next return
-            uint32_t few_out = 0, few_ph = 0, pair_out = 0, pair_ph = 0;
+            const int me = warp == 19;           // fills accumulators me and me + 2
+            int n = 0, st = 0, ph = 0;           // stream tile, its stage and the stage's parity
+            int ks = 0, kph = 0;                 // next slot of what stays and its parity
+            uint32_t out = 0, eph = 0;           // the two accumulators: handed to the epilogue and
+                                                 // not seen back; parity of their next return
             bool ok = true;
-            const auto few_back = [&](int h) {
-                if (!(few_out >> h & 1)) return;
-                ok = ok && wait_bounded(bar(kAccEmpty + me + 2 * h), few_ph >> h & 1, abort_word);
-                few_out &= ~(1u << h);
-                few_ph ^= 1u << h;
-            };
-            const auto pair_back = [&]() {
-                if (!pair_out) return;
-                ok = ok && wait_bounded(bar(kPairEmpty + me), pair_ph, abort_word);
-                pair_out = 0;
-                pair_ph ^= 1;
+            const auto take_back = [&](int h) {
+                if (out >> h & 1) {
+                    ok = wait_bounded(bar(kAccEmpty + me + 2 * h), eph >> h & 1, abort_word);
+                    eph ^= 1u << h;
+                }
+                out |= 1u << h;
+                return ok;
             };
             const uint32_t idesc_full = make_idesc(128, kCols, false, F8);
             for (int ic = 0;; ++ic) {
                 Item I;
-                if (!next_item(ic, I)) break;
-                const int set = ic & 1;
+                if (!next_item(ic, I, true)) break;
                 const bool few = I.n_qt == 1;
-                const uint64_t stay = make_sdesc(sb + kStay + set * 2 * kSlot, 16, 1024);
-                if (!(ok = wait_bounded(bar(kStayUse + set), (ic >> 1) & 1, abort_word))) break;
+                const int n_tiles = few ? 1 : I.nt, first = ks;
+                for (int r = 0; r < n_tiles && ok; ++r) {
+                    ok = wait_bounded(bar(kStayUse + ks), kph, abort_word);
+                    if (++ks == n_stay) {
+                        ks = 0;
+                        kph ^= 1;
+                    }
+                }
+                if (!ok) break;
+                const auto stay = [&](int r) {
+                    return make_sdesc(sb + stay_at((first + r) & (n_stay - 1), n_stay), 16, 1024);
+                };
+                const uint64_t stay0 = stay(few ? 0 : me), stay1 = stay(few ? 0 : me + 2);
                 const int end = n + (few ? I.nt : I.n_qt - I.qt0);
                 const int last_cols = (I.n_q - ((I.n_qt - 1) << log2qt)) * p.g;
                 const uint32_t idesc_last = make_idesc(128, (last_cols + 15) & ~15, false, F8);
                 for (; n < end; ++n) {
-                    if ((n & 1) == me) {
-                        const uint64_t stage = make_sdesc(sb + stage_at(st), 16, 1024);
-                        pair_back();
-                        if (few) {
-                            const int h = n >> 1 & 1, acc = n & 3;
-                            few_back(h);
-                            if (!ok || !(ok = wait_bounded(bar(kStreamUse + fb), ph, abort_word)))
-                                break;
+                    if (!(ok = wait_bounded(bar(kStreamUse + st), ph, abort_word))) break;
+                    const uint64_t stage = make_sdesc(sb + stage_at(st), 16, 1024);
+                    if (few) {
+                        const int acc = n & 3;
+                        if ((acc & 1) == me) {
+                            if (!take_back(acc >> 1)) break;
                             tc_fence_after();
-                            issue_s_group<D>(1u, tmem + acc * kCols, stage, stay, idesc_last);
+                            issue_s_group<D>(1u, tmem + acc * kCols, stage, stay0, idesc_last);
                             tc_commit_if(1u, bar(kAccFull + acc));
-                            few_out |= 1u << h;
+                            tc_commit_if(1u, bar(kStreamEmpty + st));
                         } else {
-                            const uint32_t idesc = n + 1 == end ? idesc_last : idesc_full;
-                            few_back(0);
-                            few_back(1);
-                            if (!ok || !(ok = wait_bounded(bar(kStreamUse + fb), ph, abort_word)))
-                                break;
+                            mbar_arrive(bar(kStreamEmpty + st));
+                        }
+                    } else {
+                        const uint32_t idesc = n + 1 == end ? idesc_last : idesc_full;
+                        if (me < I.nt) {
+                            if (!take_back(0)) break;
                             tc_fence_after();
-                            issue_s_group<D>(1u, tmem + me * kCols, stay, stage, idesc);
-                            if (I.nt == 2)
-                                issue_s_group<D>(1u, tmem + (me + 2) * kCols, stay + (kSlot >> 4),
-                                                 stage, idesc);
-                            tc_commit_if(1u, bar(kPairFull + me));
-                            pair_out = 1;
+                            issue_s_group<D>(1u, tmem + me * kCols, stay0, stage, idesc);
+                            tc_commit_if(1u, bar(kAccFull + me));
+                        }
+                        if (me + 2 < I.nt) {
+                            if (!take_back(1)) break;
+                            tc_fence_after();
+                            issue_s_group<D>(1u, tmem + (me + 2) * kCols, stay1, stage, idesc);
+                            tc_commit_if(1u, bar(kAccFull + me + 2));
                         }
                         tc_commit_if(1u, bar(kStreamEmpty + st));
                     }
-                    if (++st == n_stages) st = 0;
-                    if (++fb == 2 * n_stages) {
-                        fb = 0;
+                    if (++st == n_stages) {
+                        st = 0;
                         ph ^= 1;
                     }
                 }
                 if (!ok) break;
-                tc_commit_if(1u, bar(kStayEmpty + set));
+                for (int r = 0; r < n_tiles; ++r)
+                    tc_commit_if(1u, bar(kStayEmpty + ((first + r) & (n_stay - 1))));
             }
             // every MMA has finished before TMEM is released
             tc_commit_if(1u, bar(kDrain + me));
@@ -628,7 +620,8 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         }
     } else if (warp == 18) {
         // ------------------------------------------------ loader of what streams
-        int st = 0, fb = 0, ph = 1, n_done = 0, ok = 1;   // a fresh barrier's phase 1 counts as past
+        int n_lse = 0;                                    // MANY tiles so far
+        int st = 0, ph = 1, n_done = 0, ok = 1;   // a fresh barrier's phase 1 counts as past
         const int per_tile = kTileKeys >> log2bs, per_load = 32 / per_tile;   // blocks; tiles
         for (int ic = 0; ok; ++ic) {
             Item I;
@@ -638,6 +631,21 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             const int n = few ? I.nt : I.n_qt - I.qt0, end = I.t0 + I.nt;
             // the lanes hold the blocks of per_load tiles, and those of the next ones on their way
             int ids = -1, next = few ? block_id(I, I.t0, end) : -1;
+            // the lane's four log-sum-exps of a query tile, negated, in base 2
+            const auto fetch_lse = [&](int qt) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int col = 4 * lane + e, tok = (qt << log2qt) + (col >> (7 - log2qt));
+                    v[e] = 0.f;
+                    if (tok < I.n_q)
+                        v[e] = -1.4426950408889634f *
+                               __ldg(p.lse + int64_t(I.cu0 + tok) * p.Hq + I.kvh * p.g +
+                                     (col & (p.g - 1)));
+                }
+                return make_float4(v[0], v[1], v[2], v[3]);
+            };
+            float4 l_next = few ? make_float4(0.f, 0.f, 0.f, 0.f) : fetch_lse(I.qt0);
             for (int i = 0; i < n; ++i) {
                 const int at = i & (per_load - 1);
                 if (few && at == 0) {
@@ -647,65 +655,46 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 if (lane == 0) ok = wait_bounded(bar(kStreamEmpty + st), ph, abort_word);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
-                const uint32_t slot = sb + stage_at(st), full = bar(kStreamFull + fb);
+                const uint32_t slot = sb + stage_at(st), full = bar(kStreamFull + st);
                 if (few) {
                     const int nblk = blocks_of(I, I.t0 + i);
                     const int id = __shfl_sync(0xffffffffu, ids, (at * per_tile + lane) & 31);
                     if (lane == 0) mbar_expect_tx(full, k_bytes(nblk));
                     __syncwarp();
                     load_k(slot, full, I, nblk, id);
-                } else if (lane == 0) {
-                    load_q(slot, full, I, I.qt0 + i);
+                } else {
+                    const int lse_slot = n_lse & 3;
+                    if (lane == 0) {
+                        load_q(slot, full, I, I.qt0 + i);
+                        ok = wait_bounded(bar(kLseEmpty + lse_slot), (n_lse >> 2 & 1) ^ 1,
+                                          abort_word);
+                    }
+                    const float4 v = l_next;
+                    if (i + 1 < n) l_next = fetch_lse(I.qt0 + i + 1);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (ok) {
+                        float* to = reinterpret_cast<float*>(smem + kCtl + kLseOff) +
+                                    lse_slot * 128;
+                        *reinterpret_cast<float2*>(to + lse_place(4 * lane)) =
+                            make_float2(v.x, v.y);
+                        *reinterpret_cast<float2*>(to + lse_place(4 * lane + 2)) =
+                            make_float2(v.z, v.w);
+                        warp_arrive(bar(kLseFull + lse_slot));
+                        ++n_lse;
+                    }
                 }
                 ++n_done;
-                if (++fb == 2 * n_stages) fb = 0;
                 if (++st == n_stages) {
                     st = 0;
                     ph ^= 1;
                 }
+                if (!ok) break;
             }
         }
         if (lane == 0) {
             // never leave with copies in flight into this CTA's shared memory
             for (int i = max(0, n_done - n_stages); i < n_done; ++i)
-                wait_drain(bar(kStreamFull + i % (2 * n_stages)), (i / (2 * n_stages)) & 1);
-        }
-    } else if (warp == 19) {
-        // ------------------------------------------------ log-sum-exps, negated, in base 2
-        int n_done = 0, ok = 1;
-        for (int ic = 0; ok; ++ic) {
-            Item I;
-            ok = next_item(ic, I);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            const auto fetch = [&](int qt) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int col = 4 * lane + e;
-                    const int tok = (qt << log2qt) + (col >> (7 - log2qt));
-                    v[e] = 0.f;
-                    if (tok < I.n_q)
-                        v[e] = -1.4426950408889634f *
-                               __ldg(p.lse + int64_t(I.cu0 + tok) * p.Hq + I.kvh * p.g +
-                                     (col & (p.g - 1)));
-                }
-                return make_float4(v[0], v[1], v[2], v[3]);
-            };
-            float4 next = fetch(I.qt0);
-            for (int qt = I.qt0; qt < I.n_qt; ++qt, ++n_done) {
-                const float4 v = next;
-                if (qt + 1 < I.n_qt) next = fetch(qt + 1);
-                const int slot = n_done % kLseSlots;
-                if (lane == 0 && n_done >= kLseSlots)
-                    ok = wait_bounded(bar(kLseEmpty + slot), (n_done / kLseSlots - 1) & 1,
-                                      abort_word);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                float* to = reinterpret_cast<float*>(smem + kCtl + kLseOff) + slot * 128;
-                *reinterpret_cast<float2*>(to + lse_place(4 * lane)) = make_float2(v.x, v.y);
-                *reinterpret_cast<float2*>(to + lse_place(4 * lane + 2)) = make_float2(v.z, v.w);
-                mbar_arrive(bar(kLseFull + slot));
-            }
+                wait_drain(bar(kStreamFull + i % n_stages), (i / n_stages) & 1);
         }
     } else if (warp >= kTurners) {
         // ------------------------------------------------ codes and q to f16 (fp8 cache)
@@ -726,31 +715,34 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                                  bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
                 }
             };
-            int st = 0, fb = 0, ph = 0;
+            int st = 0, ph = 0, ks = 0, kph = 0;
             bool ok = true;
             for (int ic = 0; ok; ++ic) {
                 Item I;
                 if (!next_item(ic, I)) break;
                 const bool few = I.n_qt == 1;
-                const int set = ic & 1;
-                const uint32_t stay = sb + kStay + set * 2 * kSlot;
-                if (!(ok = wait_bounded(bar(kStayFull + set), (ic >> 1) & 1, abort_word))) break;
-                if (few) turn_q(stay, I.n_q == 1 ? p.g : kCols);
-                else
-                    for (int r = 0; r < I.nt; ++r) turn_k(stay + r * kSlot, I, I.t0 + r);
-                fence_proxy_async();
-                mbar_arrive(bar(kStayReady + set));
+                for (int r = 0; r < (few ? 1 : I.nt); ++r) {
+                    if (!(ok = wait_bounded(bar(kStayFull + ks), kph, abort_word))) break;
+                    const uint32_t slot = sb + stay_at(ks, n_stay);
+                    if (few) turn_q(slot, I.n_q == 1 ? p.g : kCols);
+                    else turn_k(slot, I, I.t0 + r);
+                    fence_proxy_async();
+                    warp_arrive(bar(kStayReady + ks));
+                    if (++ks == n_stay) {
+                        ks = 0;
+                        kph ^= 1;
+                    }
+                }
                 const int n = few ? I.nt : I.n_qt - I.qt0;
-                for (int i = 0; i < n; ++i) {
-                    if (!(ok = wait_bounded(bar(kStreamFull + fb), ph, abort_word))) break;
+                for (int i = 0; i < n && ok; ++i) {
+                    if (!(ok = wait_bounded(bar(kStreamFull + st), ph, abort_word))) break;
                     const uint32_t slot = sb + stage_at(st);
                     if (few) turn_k(slot, I, I.t0 + i);
                     else turn_q(slot, kCols);
                     fence_proxy_async();
-                    mbar_arrive(bar(kStreamReady + fb));
-                    if (++st == n_stages) st = 0;
-                    if (++fb == 2 * n_stages) {
-                        fb = 0;
+                    warp_arrive(bar(kStreamReady + st));
+                    if (++st == n_stages) {
+                        st = 0;
                         ph ^= 1;
                     }
                 }
@@ -758,62 +750,62 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         }
     } else {
         // ------------------------------------------------ epilogue warpgroups
-        const int w = warp >> 2;             // FEW: accumulator w; MANY: the pair's key tile w >> 1,
-                                             // columns 64 (w & 1) .. + 63
-        const uint32_t tm = tmem + (uint32_t(32 * (warp & 3)) << 16);
+        const int w = warp >> 2;             // reads accumulator w
+        const uint32_t tm = tmem + w * kCols + (uint32_t(32 * (warp & 3)) << 16);
         const int q4 = lane & 3, rs = lane >> 2;
         // after the sums over the four threads of a key have met, thread q4 has key rs + 8 q4
         const int key_in_tile = 32 * (warp & 3) + rs + 8 * q4;
         const uint64_t c2 = f2(p.c, p.c);
-        int n = 0, few_ph = 0, pair_ph = 0, n_lse = 0, n_part = 0;
-        bool ok = true;
+        int n = 0, acc_ph = 0, n_lse = 0;
+        const uint32_t full = bar(kAccFull + w), empty = bar(kAccEmpty + w);
         const float4* lse_smem = reinterpret_cast<const float4*>(smem + kCtl + kLseOff) + q4;
-        float* part = reinterpret_cast<float*>(smem + kCtl + kPartOff) + (w >> 1) * 128;
+        bool ok = true;
+        const int log2g = 7 - log2qt;
         uint64_t a[4];                       // the thread's part of its four keys' sums
         const auto clear = [&]() {
 #pragma unroll
             for (int k = 0; k < 4; ++k) a[k] = f2(0.f, 0.f);
         };
-        // adds columns c0 .. c1 - 1 of the accumulator at ta: query rows from position `at` on, the
-        // warp's keys from `kw` on; `empty` takes the accumulator back
-        const auto add_columns = [&](uint32_t ta, const float4* nl, int c0, int c1, int at, int kw,
-                                     uint32_t empty) {
-            tc_fence_after();
-            if (c1 - c0 == 64 && kw + 31 <= at) {
-                ta += c0;
-                nl += c0 / 4;
-                uint32_t lo0[8], hi0[8], lo1[8], hi1[8];
-                tmem_ld_16x256b_x2(ta, lo0);
-                tmem_ld_16x256b_x2(ta + (16u << 16), hi0);
-#pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    tmem_wait_ld();
-                    tmem_ld_16x256b_x2(ta + c + 16, lo1);
-                    tmem_ld_16x256b_x2(ta + c + 16 + (16u << 16), hi1);
-                    add16(lo0, hi0, nl[c / 4], c2, a);
-                    tmem_wait_ld();
-                    if (c + 32 < 64) {
-                        tmem_ld_16x256b_x2(ta + c + 32, lo0);
-                        tmem_ld_16x256b_x2(ta + c + 32 + (16u << 16), hi0);
-                    } else {
-                        tc_fence_before();
-                        mbar_arrive(empty);
-                    }
-                    add16(lo1, hi1, nl[c / 4 + 4], c2, a);
+        // log-sum-exps of columns col, col + 1 (col even) of the query tile from token `tok` on,
+        // negated, in base 2; columns behind the sequence's rows read nothing
+        const auto lse_pair = [&](const Item& I, int tok, int col) {
+            const int i = tok + (col >> log2g);
+            const float* l = p.lse + int64_t(I.cu0 + i) * p.Hq + I.kvh * p.g;
+            float x = 0.f, y = 0.f;
+            if (log2g > 0) {
+                if (i < I.n_q) {
+                    const float2 v = __ldg(reinterpret_cast<const float2*>(l + (col & (p.g - 1))));
+                    x = v.x;
+                    y = v.y;
                 }
-                return;
+            } else {
+                if (i < I.n_q) x = __ldg(l);
+                if (i + 1 < I.n_q) y = __ldg(l + p.Hq);
             }
-            for (int c = c0; c < c1; c += 16) {
+            return mul2(f2(x, y), f2(-1.4426950408889634f, -1.4426950408889634f));
+        };
+        // adds the first `cols` columns of the accumulator (query tile from token tok on), masked by
+        // causality, and hands it back; the warp's keys are those from kw on. nl: the log-sum-exps
+        // in shared memory, or NULL
+        const auto add_masked = [&](const Item& I, int tok, int cols, int kw, const float4* nl) {
+            const int at = I.pos0 + tok;
+            for (int c = 0; c < cols; c += 16) {
                 uint32_t lo[8], hi[8];
-                tmem_ld_16x256b_x2(ta + c, lo);
-                tmem_ld_16x256b_x2(ta + c + (16u << 16), hi);
-                const float4 l = nl[c / 4];
-                const float nv[4] = {l.x, l.y, l.z, l.w};
+                tmem_ld_16x256b_x2(tm + c, lo);
+                tmem_ld_16x256b_x2(tm + c + (16u << 16), hi);
+                float nv[4];
+                if (nl) {
+                    const float4 v = nl[c / 4];
+                    nv[0] = v.x, nv[1] = v.y, nv[2] = v.z, nv[3] = v.w;
+                } else {
+                    f2_split(lse_pair(I, tok, c + 2 * q4), nv[0], nv[1]);
+                    f2_split(lse_pair(I, tok, c + 8 + 2 * q4), nv[2], nv[3]);
+                }
                 tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     // the first column whose row comes at or after the key
-                    const int from = max(0, kw + rs + 8 * k - at) << (7 - log2qt);
+                    const int from = max(0, kw + rs + 8 * k - at) << log2g;
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
                         const uint32_t* s = (k < 2 ? lo : hi) + 4 * cc + 2 * (k & 1);
@@ -822,14 +814,48 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                         for (int i = 0; i < 2; ++i) {
                             const int col = c + 8 * cc + 2 * q4 + i;
                             const float x = ex2(fmaf(__uint_as_float(s[i]), p.c, nv[2 * cc + i]));
-                            e[i] = col >= from && col < c1 ? x : 0.f;
+                            e[i] = col >= from && col < cols ? x : 0.f;
                         }
                         a[k] = add2(a[k], f2(e[0], e[1]));
                     }
                 }
             }
             tc_fence_before();
-            mbar_arrive(empty);
+            warp_arrive(empty);
+        };
+        // the same for a whole query tile that every key of the warp comes before
+        const auto add_all = [&](const float4* nl) {
+            if constexpr (F8) {                        // fewer registers a thread
+                uint32_t lo[8], hi[8];
+#pragma unroll 2
+                for (int c = 0; c < kCols; c += 16) {
+                    tmem_ld_16x256b_x2(tm + c, lo);
+                    tmem_ld_16x256b_x2(tm + c + (16u << 16), hi);
+                    tmem_wait_ld();
+                    if (c == kCols - 16) {
+                        tc_fence_before();
+                        warp_arrive(empty);
+                    }
+                    add16(lo, hi, nl[c / 4], c2, a);
+                }
+            } else {
+                // half of it into registers at a time: the accumulator is free again before the
+                // second half's exponentials
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t lo[32], hi[32];
+                    tmem_ld_16x256b_x8(tm + 64 * h, lo);
+                    tmem_ld_16x256b_x8(tm + 64 * h + (16u << 16), hi);
+                    tmem_wait_ld();
+                    if (h) {
+                        tc_fence_before();
+                        warp_arrive(empty);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        add16(lo + 8 * c, hi + 8 * c, nl[16 * h + 4 * c], c2, a);
+                }
+            }
         };
         // the sum of key key_in_tile
         const auto total_of_key = [&]() {
@@ -848,69 +874,48 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         for (int ic = 0; ok; ++ic) {
             Item I;
             if (!next_item(ic, I)) break;
-            const auto wait_lse = [&]() {
-                return ok = wait_bounded(bar(kLseFull + n_lse % kLseSlots), (n_lse / kLseSlots) & 1,
-                                         abort_word);
-            };
-            const auto done_lse = [&]() { mbar_arrive(bar(kLseEmpty + n_lse++ % kLseSlots)); };
             if (I.n_qt == 1) {
-                if (!wait_lse()) break;
-                const float4* nl = lse_smem + (n_lse % kLseSlots) * 32;
                 // the item's first tile of this warpgroup, then every fourth
                 for (int i = (w - n) & 3; i < I.nt; i += 4) {
                     const int kb = (I.t0 + i) * kTileKeys, j = kb + key_in_tile;
                     float* dst = p.weights + I.state + j;
                     const float old = j < I.held ? *dst : 0.f;
-                    if (!(ok = wait_bounded(bar(kAccFull + w), few_ph, abort_word))) break;
-                    few_ph ^= 1;
+                    if (!(ok = wait_bounded(full, acc_ph, abort_word))) break;
+                    acc_ph ^= 1;
                     clear();
-                    add_columns(tm + w * kCols, nl, 0, I.n_q * p.g, I.pos0, kb + 32 * (warp & 3),
-                                bar(kAccEmpty + w));
+                    tc_fence_after();
+                    add_masked(I, 0, I.n_q * p.g, kb + 32 * (warp & 3), nullptr);
                     const float sum = total_of_key();
                     if (j < I.ctx) *dst = old + sum;
                 }
-                if (!ok) break;
                 n += I.nt;
-                done_lse();
                 continue;
             }
-            const int r = w >> 1, c0 = 64 * (w & 1);
-            const bool my = r < I.nt;
-            const int kb = (I.t0 + r) * kTileKeys, j = kb + key_in_tile;
+            const bool my = w < I.nt;
+            const int kb = (I.t0 + w) * kTileKeys, j = kb + key_in_tile, kw = kb + 32 * (warp & 3);
             float* dst = p.weights + I.state + j;
-            const float old = my && !(w & 1) && j < I.held ? *dst : 0.f;
+            const float old = my && j < I.held ? *dst : 0.f;
             clear();
-            for (int qt = I.qt0; qt < I.n_qt; ++qt, ++n) {
-                if (!wait_lse()) break;
-                const int pair = n & 1;
-                if (!(ok = wait_bounded(bar(kPairFull + pair), pair_ph >> pair & 1, abort_word)))
+            for (int qt = I.qt0; qt < I.n_qt; ++qt, ++n_lse) {
+                const int tok = qt << log2qt, cols = min(kCols, (I.n_q - tok) * p.g);
+                const int at = I.pos0 + tok;             // the tile's first row
+                const float4* nl = lse_smem + (n_lse & 3) * 32;
+                if (!(ok = wait_bounded(bar(kLseFull + (n_lse & 3)), n_lse >> 2 & 1, abort_word)))
                     break;
-                pair_ph ^= 1 << pair;
-                const int c1 = min(c0 + 64, (I.n_q - (qt << log2qt)) * p.g);
-                if (my && c0 < c1)
-                    add_columns(tm + (pair + 2 * r) * kCols, lse_smem + (n_lse % kLseSlots) * 32, c0,
-                                c1, I.pos0 + (qt << log2qt), kb + 32 * (warp & 3),
-                                bar(kPairEmpty + pair));
-                else
-                    mbar_arrive(bar(kPairEmpty + pair));
-                done_lse();
+                if (my) {
+                    if (!(ok = wait_bounded(full, acc_ph, abort_word))) break;
+                    acc_ph ^= 1;
+                    tc_fence_after();
+                    if (kw > at + ((cols - 1) >> log2g)) warp_arrive(empty);   // all rows come before
+                    else if (cols == kCols && kw + 31 <= at) add_all(nl);
+                    else add_masked(I, tok, cols, kw, nl);
+                }
+                warp_arrive(bar(kLseEmpty + (n_lse & 3)));
             }
+            n += I.n_qt - I.qt0;
             if (!ok) break;
-            if (!my) continue;
             const float sum = total_of_key();
-            if (w & 1) {
-                if (n_part > 0 &&
-                    !(ok = wait_bounded(bar(kPartEmpty + r), (n_part - 1) & 1, abort_word)))
-                    break;
-                part[key_in_tile] = sum;
-                mbar_arrive(bar(kPartFull + r));
-            } else {
-                if (!(ok = wait_bounded(bar(kPartFull + r), n_part & 1, abort_word))) break;
-                const float all = sum + part[key_in_tile];
-                mbar_arrive(bar(kPartEmpty + r));
-                if (j < I.ctx) *dst = old + all;
-            }
-            ++n_part;
+            if (my && j < I.ctx) *dst = old + sum;
         }
     }
     if (*abort_word && threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_TIMEOUT);
@@ -1027,12 +1032,14 @@ int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
     if (fp8 && s->head_dim != 128) return PA_ERR_SHAPE;
     if (B < 0 || T < 0 || max_blocks < 0 || n_rows < 0 || max_len < 0) return PA_ERR_INVALID;
     if (T == 0 || B == 0) return PA_OK;
+    if (B > kMaxSeqs) return PA_ERR_SHAPE;
     if (!q || !k_pool || !lse || !block_table || !cu || !ctx || !weights) return PA_ERR_INVALID;
     if (max_len == 0 || (!rows && n_rows < B)) return PA_ERR_INVALID;
     if (n_rows > kMaxRows || int64_t(s->num_blocks) * s->block_size > INT32_MAX ||
         max_len > INT32_MAX - kTileKeys)
         return PA_ERR_SHAPE;
-    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pool)) & 15)
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pool)) & 15 ||
+        reinterpret_cast<uintptr_t>(lse) & 7)
         return PA_ERR_INVALID;
     const int D = s->head_dim, g = s->num_q_heads / s->num_kv_heads;
     const int64_t slots = int64_t(s->num_blocks) * s->block_size;
@@ -1125,7 +1132,7 @@ int32_t step_weights(const void* q, const void* k_pool, const void* v_pool,
     if (!q || !k_pool || !v_pool || !block_table || !cu || !ctx || !items || !out || !lse ||
         !weights || max_len <= 0 || max_ctx == 0 || n_rows < 0 || (!rows && n_rows < B))
         return PA_ERR_INVALID;
-    if (B > 65535 || s->num_kv_heads > 65535 || n_rows > kMaxRows ||
+    if (B > kMaxSeqs || s->num_kv_heads > 65535 || n_rows > kMaxRows ||
         max_len > INT32_MAX - kTileKeys || max_ctx > INT32_MAX - kTileKeys ||
         int64_t(s->num_blocks) * s->block_size > INT32_MAX)
         return PA_ERR_SHAPE;

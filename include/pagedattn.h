@@ -548,7 +548,8 @@ int32_t paged_qk_norm_rope_write_fp8(const void* q, int64_t q_stride, const void
  * NULL int32. A sequence whose metadata does not fit (n_q > ctx, ctx > max_len or the table, held
  * outside [0, ctx], a row >= n_rows or named by another sequence with query rows) is skipped and
  * sets PA_DEVERR_META. Weights whose lse or q is NaN are NaN.
- * Host checks: as paged_attention_step; n_rows <= 2^18; n_rows >= B without rows. One launch, a
+ * Host checks: as paged_attention_step; lse 8-byte aligned; B <= 8192 and n_rows <= 2^18 (PA_ERR_SHAPE); n_rows >= B
+ * without rows. One launch, a
  * programmatic dependent of what precedes it, no workspace, nothing planned on the host: a captured
  * call follows its metadata. */
 int32_t paged_attention_weights(const void* q, const void* k_pool, const float* lse,
@@ -592,7 +593,7 @@ int32_t paged_attention_step_fp8_lse(const void* q, const void* k_pool, const vo
  * workspace: at least pa_step_weights_workspace_bytes(shape, B, T, max_ctx) bytes, 16-byte aligned,
  * always needed; it holds B * Hq * max_ctx scores beside the split partials, and nothing between
  * calls. max_ctx >= every ctx_lens[s] (a longer decode sequence adds nothing and sets
- * PA_DEVERR_META). Other arguments, state and errors as in the two. B <= 65535. */
+ * PA_DEVERR_META). Other arguments, state and errors as in the two. */
 size_t pa_step_weights_workspace_bytes(const pa_shape* shape, int32_t B, int32_t T,
                                        int32_t max_ctx);
 int32_t paged_attention_step_weights(const void* q, const void* k_pool, const void* v_pool,
