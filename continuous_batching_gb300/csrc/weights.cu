@@ -29,7 +29,8 @@
 // Warps: 0-15 four epilogue warpgroups, 16 scheduler and loader of what stays, 17 and 19 MMA issuers,
 // 18 loader of what streams; over an fp8 cache 20-23 turn codes and q to f16. There are four
 // accumulators of 128 TMEM columns, warpgroup w reads accumulator w: FEW's stream tiles take them in
-// turn, a MANY item's key tile r has accumulator r. Issuer i fills accumulators i and i + 2: its
+// turn, a MANY item's key tile r has accumulator r, and of one or two key tiles the query tiles
+// alternate between accumulators r and r + 2, whose sums meet in memory at the item's end. Issuer i fills accumulators i and i + 2: its
 // waits, commits and address arithmetic, made slow by the warps it shares its scheduler with, run
 // while the other's MMAs keep the tensor pipe busy.
 // Shared memory: seven 32 KB slots. Four in a ring for what stays (the next item's tiles load as this
@@ -83,14 +84,16 @@ enum Bar {
     kLseEmpty = 30,    // + slot, MANY: 16 arrivals
     kItemFull = 34,    // + slot (4)
     kItemEmpty = 38,   // + slot: every consumer warp
-    kDrain = 42,       // + issuer
-    kStayReady = 44,   // + slot, fp8 only: 4 arrivals of the f16 warps
-    kStreamReady = 48, // + stage
-    kNumBars = 53
+    kPartDone = 42,    // + key tile of two: 4 arrivals, warpgroup r + 2 -> r
+    kPartSeen = 44,    // + key tile of two: 4 arrivals, warpgroup r -> r + 2
+    kDrain = 46,       // + issuer
+    kStayReady = 48,   // + slot, fp8 only: 4 arrivals of the f16 warps
+    kStreamReady = 52, // + stage
+    kNumBars = 57
 };
 constexpr int kHolderOff = 8 * kNumBars;
 constexpr int kAbortOff = kHolderOff + 4;
-constexpr int kRingOff = 448;                  // 4 items of 64 bytes
+constexpr int kRingOff = 512;                  // 4 items of 64 bytes
 constexpr int kLseOff = kRingOff + 4 * 64;     // MANY: 4 x 128 log-sum-exps
 constexpr int kTwiceOff = kLseOff + 4 * 512;   // whether some state row is named twice
 static_assert(kAbortOff + 4 <= kRingOff && kTwiceOff + 4 <= 3072, "control area");
@@ -297,6 +300,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         for (int b = 0; b < kNumBars; ++b)
             mbar_init(bar(b), b >= kStayReady                             ? 4
                               : b >= kDrain                               ? 1
+                              : b >= kPartDone                            ? 4
                               // issuers 2, stream loader 1, epilogue 16, f16 4
                               : b >= kItemEmpty                           ? 2 + 1 + 16 + (F8 ? 4 : 0)
                               : b >= kItemFull                            ? 1
@@ -437,8 +441,12 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok || I.last) return;
             ++ic;
+            int ids[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                ids[r] = !few && r < I.nt ? block_id(I, I.t0 + r, I.t0 + r + 1) : -1;
             for (int r = 0; r < (few ? 1 : I.nt); ++r) {
-                const int id = few ? -1 : block_id(I, I.t0 + r, I.t0 + r + 1);
+                const int id = r == 0 ? ids[0] : r == 1 ? ids[1] : r == 2 ? ids[2] : ids[3];
                 if (lane == 0) ok = wait_bounded(bar(kStayEmpty + ks), kph, abort_word);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) return;
@@ -514,11 +522,9 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     I.qt0 = 0;
                     emit(I, true);
                 } else {
-                    // as few items as hold the tiles, of even sizes
-                    int items = (tb - ta + 3) / 4;
-                    for (int t = ta; t < tb && ok; t += I.nt, --items) {
+                    for (int t = ta; t < tb && ok; t += I.nt) {
                         I.t0 = t;
-                        I.nt = (tb - t + items - 1) / items;
+                        I.nt = min(4, tb - t);
                         I.qt0 = first_qt(q, t, log2qt);
                         emit(I, false);
                     }
@@ -568,8 +574,9 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     }
                 }
                 if (!ok) break;
+                const auto first_slot = [&](int r) { return (first + r) & (n_stay - 1); };
                 const auto stay = [&](int r) {
-                    return make_sdesc(sb + stay_at((first + r) & (n_stay - 1), n_stay), 16, 1024);
+                    return make_sdesc(sb + stay_at(first_slot(r), n_stay), 16, 1024);
                 };
                 const uint64_t stay0 = stay(few ? 0 : me), stay1 = stay(few ? 0 : me + 2);
                 const int end = n + (few ? I.nt : I.n_qt - I.qt0);
@@ -592,12 +599,16 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     } else {
                         const uint32_t idesc = n + 1 == end ? idesc_last : idesc_full;
                         if (me < I.nt) {
-                            if (!take_back(0)) break;
+                            const int h = I.nt <= 2 ? n & 1 : 0;
+                            if (!take_back(h)) break;
                             tc_fence_after();
-                            issue_s_group<D>(1u, tmem + me * kCols, stay0, stage, idesc);
-                            tc_commit_if(1u, bar(kAccFull + me));
+                            issue_s_group<D>(1u, tmem + (me + 2 * h) * kCols, stay0, stage, idesc);
+                            tc_commit_if(1u, bar(kAccFull + me + 2 * h));
                         }
                         if (me + 2 < I.nt) {
+                            // (the first tile's slot is not needed any more once the last query
+                            // tile's product is in the pipe)
+                            if (n + 1 == end) tc_commit_if(1u, bar(kStayEmpty + first_slot(me)));
                             if (!take_back(1)) break;
                             tc_fence_after();
                             issue_s_group<D>(1u, tmem + (me + 2) * kCols, stay1, stage, idesc);
@@ -612,7 +623,8 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 }
                 if (!ok) break;
                 for (int r = 0; r < n_tiles; ++r)
-                    tc_commit_if(1u, bar(kStayEmpty + ((first + r) & (n_stay - 1))));
+                    if (few || r != me || me + 2 >= I.nt)
+                        tc_commit_if(1u, bar(kStayEmpty + first_slot(r)));
             }
             // every MMA has finished before TMEM is released
             tc_commit_if(1u, bar(kDrain + me));
@@ -756,7 +768,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         // after the sums over the four threads of a key have met, thread q4 has key rs + 8 q4
         const int key_in_tile = 32 * (warp & 3) + rs + 8 * q4;
         const uint64_t c2 = f2(p.c, p.c);
-        int n = 0, acc_ph = 0, n_lse = 0;
+        int n = 0, acc_ph = 0, n_lse = 0, n_part = 0;
         const uint32_t full = bar(kAccFull + w), empty = bar(kAccEmpty + w);
         const float4* lse_smem = reinterpret_cast<const float4*>(smem + kCtl + kLseOff) + q4;
         bool ok = true;
@@ -825,36 +837,26 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         };
         // the same for a whole query tile that every key of the warp comes before
         const auto add_all = [&](const float4* nl) {
-            if constexpr (F8) {                        // fewer registers a thread
-                uint32_t lo[8], hi[8];
-#pragma unroll 2
-                for (int c = 0; c < kCols; c += 16) {
-                    tmem_ld_16x256b_x2(tm + c, lo);
-                    tmem_ld_16x256b_x2(tm + c + (16u << 16), hi);
-                    tmem_wait_ld();
-                    if (c == kCols - 16) {
-                        tc_fence_before();
-                        warp_arrive(empty);
-                    }
-                    add16(lo, hi, nl[c / 4], c2, a);
-                }
-            } else {
-                // half of it into registers at a time: the accumulator is free again before the
-                // second half's exponentials
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t lo[32], hi[32];
-                    tmem_ld_16x256b_x8(tm + 64 * h, lo);
-                    tmem_ld_16x256b_x8(tm + 64 * h + (16u << 16), hi);
-                    tmem_wait_ld();
-                    if (h) {
-                        tc_fence_before();
-                        warp_arrive(empty);
-                    }
+            // 16 columns at a time, the next ones on their way (half or all of the accumulator in
+            // registers first, to hand it back earlier, made the whole kernel a fourth slower)
+            uint32_t lo0[8], hi0[8], lo1[8], hi1[8];
+            tmem_ld_16x256b_x2(tm, lo0);
+            tmem_ld_16x256b_x2(tm + (16u << 16), hi0);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        add16(lo + 8 * c, hi + 8 * c, nl[16 * h + 4 * c], c2, a);
+            for (int c = 0; c < kCols; c += 32) {
+                tmem_wait_ld();
+                tmem_ld_16x256b_x2(tm + c + 16, lo1);
+                tmem_ld_16x256b_x2(tm + c + 16 + (16u << 16), hi1);
+                add16(lo0, hi0, nl[c / 4], c2, a);
+                tmem_wait_ld();
+                if (c + 32 < kCols) {
+                    tmem_ld_16x256b_x2(tm + c + 32, lo0);
+                    tmem_ld_16x256b_x2(tm + c + 32 + (16u << 16), hi0);
+                } else {
+                    tc_fence_before();
+                    warp_arrive(empty);
                 }
+                add16(lo1, hi1, nl[c / 4 + 4], c2, a);
             }
         };
         // the sum of key key_in_tile
@@ -891,18 +893,21 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 n += I.nt;
                 continue;
             }
-            const bool my = w < I.nt;
-            const int kb = (I.t0 + w) * kTileKeys, j = kb + key_in_tile, kw = kb + 32 * (warp & 3);
+            // one key tile, all query tiles; or of one or two key tiles every second query tile
+            const bool half = I.nt <= 2;
+            const int r = half ? w & 1 : w;
+            const bool my = r < I.nt;
+            const int kb = (I.t0 + r) * kTileKeys, j = kb + key_in_tile, kw = kb + 32 * (warp & 3);
             float* dst = p.weights + I.state + j;
-            const float old = my && j < I.held ? *dst : 0.f;
+            const float old = my && (!half || w >= 2) && j < I.held ? *dst : 0.f;
             clear();
-            for (int qt = I.qt0; qt < I.n_qt; ++qt, ++n_lse) {
+            for (int qt = I.qt0; qt < I.n_qt; ++qt, ++n, ++n_lse) {
                 const int tok = qt << log2qt, cols = min(kCols, (I.n_q - tok) * p.g);
                 const int at = I.pos0 + tok;             // the tile's first row
                 const float4* nl = lse_smem + (n_lse & 3) * 32;
                 if (!(ok = wait_bounded(bar(kLseFull + (n_lse & 3)), n_lse >> 2 & 1, abort_word)))
                     break;
-                if (my) {
+                if (my && (!half || (n & 1) == w >> 1)) {
                     if (!(ok = wait_bounded(full, acc_ph, abort_word))) break;
                     acc_ph ^= 1;
                     tc_fence_after();
@@ -912,10 +917,25 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 }
                 warp_arrive(bar(kLseEmpty + (n_lse & 3)));
             }
-            n += I.n_qt - I.qt0;
             if (!ok) break;
+            if (!my) continue;
             const float sum = total_of_key();
-            if (my && j < I.ctx) *dst = old + sum;
+            if (!half) {
+                if (j < I.ctx) *dst = old + sum;
+                continue;
+            }
+            if (w >= 2) {
+                if (j < I.ctx) *dst = old + sum;
+                if (n_part > 0 &&
+                    !(ok = wait_bounded(bar(kPartSeen + r), (n_part - 1) & 1, abort_word)))
+                    break;
+                warp_arrive(bar(kPartDone + r));
+            } else {
+                if (!(ok = wait_bounded(bar(kPartDone + r), n_part & 1, abort_word))) break;
+                warp_arrive(bar(kPartSeen + r));
+                if (j < I.ctx) *dst += sum;
+            }
+            ++n_part;
         }
     }
     if (*abort_word && threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_TIMEOUT);
