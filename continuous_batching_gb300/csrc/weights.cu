@@ -54,8 +54,9 @@ using namespace pa_detail;
 namespace {
 
 constexpr int kBaseThreads = 640;
+constexpr int kTurnWarps = 4;                  // turn an fp8 cache's codes, 32 rows of a tile each
 template <bool F8>
-constexpr int kThreadsFor = F8 ? kBaseThreads + 128 : kBaseThreads;
+constexpr int kThreadsFor = F8 ? kBaseThreads + 32 * kTurnWarps : kBaseThreads;
 constexpr int kTurners = kBaseThreads / 32;    // the first f16 warp of an fp8 cache
 constexpr int kCols = 128;                     // columns of a query tile
 constexpr int kSlot = 32768;                   // one tile, 128 rows of D = 128
@@ -87,7 +88,7 @@ enum Bar {
     kPartDone = 42,    // + key tile of two: 4 arrivals, warpgroup r + 2 -> r
     kPartSeen = 44,    // + key tile of two: 4 arrivals, warpgroup r -> r + 2
     kDrain = 46,       // + issuer
-    kStayReady = 48,   // + slot, fp8 only: 4 arrivals of the f16 warps
+    kStayReady = 48,   // + slot, fp8 only: the f16 warps
     kStreamReady = 52, // + stage
     kNumBars = 57
 };
@@ -146,8 +147,9 @@ __device__ __forceinline__ int64_t cost_before(const Seq& q, int t, int log2qt) 
 }
 
 // Quotients of costs: nearly always of 32 bits.
+__device__ __noinline__ int64_t quot_64(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+    return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : quot_64(a, b);
 }
 
 // The first tile whose start is at or behind x.
@@ -245,30 +247,27 @@ __device__ __forceinline__ void add16(const uint32_t* lo, const uint32_t* hi, fl
     }
 }
 
-// A K slot's code rows r0 .. r0 + 31 expanded to f16 by one warp, like expand_codes but with 16 rows
-// read before any is written: the reads' latency is paid twice a tile, not eight times. Rows from
-// `rows` on hold nothing that counts; their (stale) codes are turned as well.
-__device__ __forceinline__ void expand_rows(uint32_t slot, int r0, int rows, int lane) {
+// A K slot's code rows r0 .. r0 + 15 expanded to f16 by one warp, like expand_codes but with all of
+// them read before any is written, so that the reads' latency is paid once. Rows behind the tile's
+// keys hold nothing that counts; their (stale) codes are turned as well.
+__device__ __forceinline__ void expand_rows(uint32_t slot, int r0, int lane) {
     const uint32_t c = lane & 7, j0 = 2 * (c & 3), hi = c >> 2;
-#pragma unroll 1
-    for (int b = r0; b < min(rows, r0 + 32); b += 16) {
-        uint4 v[4];
+    uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = ld_shared_v4(slot + kHalf + uint32_t(b + 4 * i + (lane >> 3)) * 128 + c * 16);
-        __syncwarp();
+    for (int i = 0; i < 4; ++i)
+        v[i] = ld_shared_v4(slot + kHalf + uint32_t(r0 + 4 * i + (lane >> 3)) * 128 + c * 16);
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t R = uint32_t(b + 4 * i + (lane >> 3)), x = R & 7;
-            uint32_t f[8];
-            e4m3x4_to_f16x4(v[i].x, f[0], f[1]);
-            e4m3x4_to_f16x4(v[i].y, f[2], f[3]);
-            e4m3x4_to_f16x4(v[i].z, f[4], f[5]);
-            e4m3x4_to_f16x4(v[i].w, f[6], f[7]);
-            const uint32_t rb = slot + hi * kHalf + R * 128;
-            st_shared_v4(rb + ((j0 ^ x) << 4), f[0], f[1], f[2], f[3]);
-            st_shared_v4(rb + (((j0 + 1) ^ x) << 4), f[4], f[5], f[6], f[7]);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t R = uint32_t(r0 + 4 * i + (lane >> 3)), x = R & 7;
+        uint32_t f[8];
+        e4m3x4_to_f16x4(v[i].x, f[0], f[1]);
+        e4m3x4_to_f16x4(v[i].y, f[2], f[3]);
+        e4m3x4_to_f16x4(v[i].z, f[4], f[5]);
+        e4m3x4_to_f16x4(v[i].w, f[6], f[7]);
+        const uint32_t rb = slot + hi * kHalf + R * 128;
+        st_shared_v4(rb + ((j0 ^ x) << 4), f[0], f[1], f[2], f[3]);
+        st_shared_v4(rb + (((j0 + 1) ^ x) << 4), f[4], f[5], f[6], f[7]);
     }
 }
 
@@ -296,13 +295,27 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         return;
     }
 
+    // the metadata's and the tables' lines on their way into L2, dealt over the grid's CTAs (up to 8 a
+    // lane; a prefetch reads nothing that the kernel before might still write)
+    if (warp == 18) {
+        const int64_t l_b = (int64_t(p.B) + 31) / 32;
+        const int64_t all = 3 * l_b + (int64_t(p.B) * p.max_blocks + 31) / 32;
+        int64_t l = int64_t(blockIdx.x) * 32 + lane;
+        for (int k = 0; k < 8 && l < all; ++k, l += int64_t(gridDim.x) * 32) {
+            const int32_t* at = l < l_b ? p.cu + l * 32
+                                : l < 2 * l_b ? p.ctx + (l - l_b) * 32
+                                : l < 3 * l_b ? (p.rows ? p.rows + (l - 2 * l_b) * 32 : nullptr)
+                                              : p.block_table + (l - 3 * l_b) * 32;
+            if (at) prefetch_l2(at);
+        }
+    }
     if (threadIdx.x == 0) {
         for (int b = 0; b < kNumBars; ++b)
-            mbar_init(bar(b), b >= kStayReady                             ? 4
+            mbar_init(bar(b), b >= kStayReady                             ? kTurnWarps
                               : b >= kDrain                               ? 1
                               : b >= kPartDone                            ? 4
-                              // issuers 2, stream loader 1, epilogue 16, f16 4
-                              : b >= kItemEmpty                           ? 2 + 1 + 16 + (F8 ? 4 : 0)
+                              // issuers 2, stream loader 1, epilogue 16, f16 warps
+                              : b >= kItemEmpty                           ? 2 + 1 + 16 + (F8 ? kTurnWarps : 0)
                               : b >= kItemFull                            ? 1
                               : b >= kLseEmpty                            ? 16
                               : b >= kLseFull                             ? 1
@@ -712,15 +725,15 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         // ------------------------------------------------ codes and q to f16 (fp8 cache)
         if constexpr (F8) {
             const int w = warp - kTurners;
-            // the MMAs take f16 operands: 32 rows a warp of a K tile's codes are expanded, or of a
-            // query tile rounded in place (a 16-byte chunk keeps its place, so the swizzle holds)
+            // the MMAs take f16 operands: 32 rows a warp of a K tile's codes are expanded, or a
+            // query tile is rounded in place (a 16-byte chunk keeps its place, so the swizzle holds)
             const auto turn_k = [&](uint32_t slot, const Item& I, int t) {
-                const int rows =
-                    ((min(kTileKeys, I.ctx - t * kTileKeys) + p.bs - 1) >> log2bs) << log2bs;
-                expand_rows(slot, 32 * w, rows, lane);
+                const int rows = I.ctx - t * kTileKeys;
+                if (32 * w < rows) expand_rows(slot, 32 * w, lane);
+                if (32 * w + 16 < rows) expand_rows(slot, 32 * w + 16, lane);
             };
             const auto turn_q = [&](uint32_t slot, int rows) {
-                for (int i = threadIdx.x - kBaseThreads; i < rows * 16; i += 128) {
+                for (int i = threadIdx.x - kBaseThreads; i < rows * 16; i += 32 * kTurnWarps) {
                     const uint32_t a = slot + ((i >> 3) & 1) * kHalf + (i >> 4) * 128 + (i & 7) * 16;
                     const uint4 v = ld_shared_v4(a);
                     st_shared_v4(a, bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y),
