@@ -308,26 +308,30 @@ __global__ void __launch_bounds__(kThreads, 4) evict_kernel(const EvictParams p)
     }
 
     // ---- holes and strays, this CTA's share of the moves a window at a time
-    const int per = (words + kThreads - 1) / kThreads;
-    const int wa = min(words, tid * per), wb = min(words, wa + per);
     const auto bits_of = [&](int w, bool holes) {
         const int below = len - 32 * w;                // entries of the word that lie before len
         const uint32_t in = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1;
         return holes ? ~keep[w] & in : keep[w] & ~in;
     };
-    int n_hole = 0, n_stray = 0, moves, strays;
-    for (int w = wa; w < wb; ++w) {
-        n_hole += __popc(bits_of(w, true));
-        n_stray += __popc(bits_of(w, false));
+    // Both kinds' ranks, a word per thread and kThreads words at a time (neighbouring words are
+    // dense in holes: a thread with several of them would list them alone): the number before the
+    // thread's word and in the whole round, holes in the lower 16 bits, strays in the upper ones
+    static_assert(32 * kThreads < 1 << 16, "a round's counts fit 16 bits");
+    const auto round_scan = [&](int w, int& all) {
+        const int n = w < words ? __popc(bits_of(w, true)) | __popc(bits_of(w, false)) << 16 : 0;
+        return block_scan(n, sh.warp_sum, all) - n;
+    };
+    int moves = 0;
+    for (int r = 0; r < words; r += kThreads) {
+        int all;
+        round_scan(r + tid, all);
+        moves += all & 0xffff;
     }
-    const int hole0 = block_scan(n_hole, sh.warp_sum, moves) - n_hole;
-    const int stray0 = block_scan(n_stray, sh.warp_sum, strays) - n_stray;
     const int m0 = int(int64_t(moves) * rank / C), m1 = int(int64_t(moves) * (rank + 1) / C);
-    const auto list = [&](int32_t* to, int at, int n, bool holes, int first, int end) {
-        if (at >= end || at + n <= first) return;
-        for (int w = wa; w < wb; ++w)
-            for (uint32_t m = bits_of(w, holes); m; m &= m - 1, ++at)
-                if (at >= first && at < end) to[at - first] = 32 * w + __ffs(m) - 1;
+    const auto list = [&](int32_t* to, int at, int w, bool holes, int first, int end) {
+        if (at >= end || at + 32 <= first) return;
+        for (uint32_t m = bits_of(w, holes); m; m &= m - 1, ++at)
+            if (at >= first && at < end) to[at - first] = 32 * w + __ffs(m) - 1;
     };
     const int32_t* table = p.table + int64_t(s) * p.max_blocks;
     // the slot of entry j, -1 where the table leads outside the pool
@@ -341,8 +345,17 @@ __global__ void __launch_bounds__(kThreads, 4) evict_kernel(const EvictParams p)
     for (int first = m0; first < m1; first += kWindow) {
         const int end = min(m1, first + kWindow);
         __syncthreads();
-        list(sh.hole, hole0, n_hole, true, first, end);
-        list(sh.stray, stray0, n_stray, false, first, end);
+        for (int r = 0, holes = 0, strays = 0; r < words; r += kThreads) {
+            const int w = r + tid;
+            int all;
+            const int before = round_scan(w, all);
+            if (w < words) {
+                list(sh.hole, holes + (before & 0xffff), w, true, first, end);
+                list(sh.stray, strays + (before >> 16), w, false, first, end);
+            }
+            holes += all & 0xffff;
+            strays += all >> 16;
+        }
         __syncthreads();
         for (int e = tid; e < end - first; e += kThreads) {
             const int to = sh.hole[e], from = sh.stray[e];
