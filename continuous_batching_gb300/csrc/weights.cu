@@ -67,9 +67,11 @@ constexpr int kBytes = kCtl + 3072;
 static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr int kMaxRows = 1 << 18;              // state rows whose repeats are looked for
 constexpr int kMaxSeqs = 8192;                 // sequences whose costs are held while they are dealt
-// before the pipeline starts: a bit per state row in slots 0 and 1, a cost per sequence from slot 4
-constexpr int kCosts = 4 * kSlot;
-static_assert(kMaxRows / 8 <= 2 * kSlot && kMaxSeqs * 8 <= 3 * kSlot, "scratch of the deal");
+// before the pipeline starts: a bit per state row in slot 0, the first sequences' metadata from slot
+// 1, a cost per sequence from slot 4
+constexpr int kMeta = kSlot, kCosts = 4 * kSlot;
+constexpr int kMetaSeqs = 3 * kSlot / 32;
+static_assert(kMaxRows / 8 <= kSlot && kMaxSeqs * 8 <= 3 * kSlot, "scratch of the deal");
 constexpr int64_t kCostFew = 5, kCostMany = 2; // of a key tile; of a key tile and query tile
 
 // A role that waits on a barrier waits for each of its phases in turn: parity tells only neighbours
@@ -166,6 +168,15 @@ __device__ __forceinline__ int tile_at(const Seq& q, int64_t x, int log2qt) {
     return t;
 }
 
+// What follows from n_q and ctx.
+__device__ __forceinline__ void derive(Seq& q, int log2qt) {
+    q.pos0 = q.ctx - q.n_q;
+    q.n_tiles = (q.ctx + kTileKeys - 1) / kTileKeys;
+    q.n_qt = (q.n_q + (1 << log2qt) - 1) >> log2qt;
+    q.few = q.n_qt == 1;
+    q.head_cost = cost_before(q, q.n_tiles, log2qt);
+}
+
 // Another sequence with query rows names sequence s's state row: both would race on it.
 __device__ __noinline__ bool shares_row(const int32_t* rows, const int32_t* cu, int B, int s) {
     for (int i = 0; i < B; ++i)
@@ -194,11 +205,7 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt, bool
         q.bad = true;
         return q;
     }
-    q.pos0 = q.ctx - q.n_q;
-    q.n_tiles = (q.ctx + kTileKeys - 1) / kTileKeys;
-    q.n_qt = (q.n_q + (1 << log2qt) - 1) >> log2qt;
-    q.few = q.n_qt == 1;
-    q.head_cost = cost_before(q, q.n_tiles, log2qt);
+    derive(q, log2qt);
     return q;
 }
 
@@ -309,23 +316,23 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             if (at) prefetch_l2(at);
         }
     }
-    if (threadIdx.x == 0) {
-        for (int b = 0; b < kNumBars; ++b)
-            mbar_init(bar(b), b >= kStayReady                             ? kTurnWarps
-                              : b >= kDrain                               ? 1
-                              : b >= kPartDone                            ? 4
-                              // issuers 2, stream loader 1, epilogue 16, f16 warps
-                              : b >= kItemEmpty                           ? 2 + 1 + 16 + (F8 ? kTurnWarps : 0)
-                              : b >= kItemFull                            ? 1
-                              : b >= kLseEmpty                            ? 16
-                              : b >= kLseFull                             ? 1
-                              : b >= kAccEmpty                            ? 4
-                              : b >= kAccFull                             ? 1
-                              : b >= kStreamEmpty                         ? 2
-                              : b >= kStreamFull                          ? 1
-                              : b >= kStayEmpty                           ? 2
-                                                                          : 1);
-        *abort_word = 0;
+    if (threadIdx.x < kNumBars) {
+        const int b = threadIdx.x;
+        mbar_init(bar(b), b >= kStayReady                             ? kTurnWarps
+                          : b >= kDrain                               ? 1
+                          : b >= kPartDone                            ? 4
+                          // issuers 2, stream loader 1, epilogue 16, f16 warps
+                          : b >= kItemEmpty                           ? 2 + 1 + 16 + (F8 ? kTurnWarps : 0)
+                          : b >= kItemFull                            ? 1
+                          : b >= kLseEmpty                            ? 16
+                          : b >= kLseFull                             ? 1
+                          : b >= kAccEmpty                            ? 4
+                          : b >= kAccFull                             ? 1
+                          : b >= kStreamEmpty                         ? 2
+                          : b >= kStreamFull                          ? 1
+                          : b >= kStayEmpty                           ? 2
+                                                                      : 1);
+        if (b == 0) *abort_word = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 17) {
@@ -363,6 +370,11 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 if (atomicOr(once + (q.row >> 5), bit) & bit) *repeated = 1;
             }
             costs[s] = q.head_cost;
+            if (s < kMetaSeqs) {
+                int4* m = reinterpret_cast<int4*>(smem + kMeta) + 2 * s;
+                m[0] = make_int4(q.n_q, q.ctx, q.cu0, q.row);
+                m[1].x = q.held;
+            }
             bad = bad || q.bad;
             some_many = some_many || (q.head_cost > 0 && !q.few);
         }
@@ -509,9 +521,23 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         int64_t base = __shfl_sync(0xffffffffu, upto - mine, from) * p.Hkv;
         int first_s = from * per;
         while (first_s < p.B && base + costs[first_s] * p.Hkv <= lo) base += costs[first_s++] * p.Hkv;
-        __syncwarp();                                // the costs make room for what streams
+        // the first sequence's metadata is still at hand; the next ones are read again
+        Seq q;
+        if (first_s < min(p.B, kMetaSeqs)) {
+            const int4* m = reinterpret_cast<const int4*>(smem + kMeta) + 2 * first_s;
+            const int4 v = m[0];
+            q.n_q = v.x;
+            q.ctx = v.y;
+            q.cu0 = v.z;
+            q.row = v.w;
+            q.held = m[1].x;
+            derive(q, log2qt);
+        } else if (first_s < p.B) {
+            q = load_seq(p, first_s, log2qt, twice);
+        }
+        __syncwarp();                                // costs and metadata make room for the tiles
         for (int s = first_s; s < p.B && base < hi && ok; ++s) {
-            const Seq q = load_seq(p, s, log2qt, twice);
+            if (s > first_s) q = load_seq(p, s, log2qt, twice);
             if (q.head_cost == 0) continue;
             Item I;
             I.seq = s;
@@ -655,7 +681,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             const bool few = I.n_qt == 1;
             const int n = few ? I.nt : I.n_qt - I.qt0, end = I.t0 + I.nt;
             // the lanes hold the blocks of per_load tiles, and those of the next ones on their way
-            int ids = -1, next = few ? block_id(I, I.t0, end) : -1;
+            int ids = few ? block_id(I, I.t0, end) : -1, next = -1;
             // the lane's four log-sum-exps of a query tile, negated, in base 2
             const auto fetch_lse = [&](int qt) {
                 float v[4];
@@ -673,10 +699,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             float4 l_next = few ? make_float4(0.f, 0.f, 0.f, 0.f) : fetch_lse(I.qt0);
             for (int i = 0; i < n; ++i) {
                 const int at = i & (per_load - 1);
-                if (few && at == 0) {
-                    ids = next;
-                    next = i + per_load < n ? block_id(I, I.t0 + i + per_load, end) : -1;
-                }
+                if (few && at == 0 && i > 0) ids = next;
                 if (lane == 0) ok = wait_bounded(bar(kStreamEmpty + st), ph, abort_word);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
@@ -687,6 +710,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     if (lane == 0) mbar_expect_tx(full, k_bytes(nblk));
                     __syncwarp();
                     load_k(slot, full, I, nblk, id);
+                    if (at == 0 && i + per_load < n) next = block_id(I, I.t0 + i + per_load, end);
                 } else {
                     const int lse_slot = n_lse & 3;
                     if (lane == 0) {
