@@ -21,10 +21,11 @@
 //         L2. Bound by the tensor pipe and the exponentials (per element one fused multiply-add and
 //         one addition, packed in pairs, and one ex2). With two key tiles staying, the 32 KB a query
 //         tile takes out of L2 for each of their products was what bound it.
-// Work is dealt by cost, on the device: every (sequence, KV head, key tile) in order has a cost
-// (kCostFew for a FEW tile, kCostMany for each query tile a MANY tile meets), CTA c takes the tiles
-// that start in its 1/G of the total. No plan is made or uploaded, so a captured graph needs nothing
-// renewed but its metadata.
+// Work is dealt by cost, on the device, to groups of CTAs, one for each of 8 (4, 2, 1) neighbouring KV
+// heads: every (sequence, heads, key tile) in order has a cost (kCostFew for a FEW tile, kCostMany for
+// each query tile a MANY tile meets), a group takes the tiles that start in its share of the total.
+// The heads of a token lie side by side in memory; read at about the same time, whole rows of DRAM
+// are used. No plan is made or uploaded, so a captured graph needs nothing renewed but its metadata.
 //
 // Warps: 0-15 four epilogue warpgroups, 16 scheduler and loader of what stays, 17 and 19 MMA issuers,
 // 18 loader of what streams; over an fp8 cache 20-23 turn codes and q to f16. There are four
@@ -119,6 +120,7 @@ struct Params {
     float* weights;              // [n_rows][Hkv][max_len]
     int32_t* err;
     int32_t B, T, max_blocks, Hq, Hkv, g, bs, num_blocks, n_rows, max_len;
+    int32_t heads;               // CTAs of a group: neighbouring KV heads
     int32_t skip_decode;         // sequences of one row are another kernel's
     float c;                     // log2(e) / sqrt(D), times the K scale of an fp8 cache
 };
@@ -511,16 +513,18 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
             if (lane >= d) upto += y;
         }
-        const int64_t total = __shfl_sync(0xffffffffu, upto, 31) * p.Hkv;
-        const int64_t each = quot(total, gridDim.x), rest = total - each * gridDim.x;
-        const auto bound = [&](int c) { return each * c + int64_t(uint32_t(rest) * c / gridDim.x); };
-        const int64_t lo = bound(int(blockIdx.x)), hi = bound(int(blockIdx.x) + 1);
+        const int blocks = p.Hkv / p.heads, groups = int(gridDim.x) / p.heads;
+        const int group = int(blockIdx.x) / p.heads, member = int(blockIdx.x) - group * p.heads;
+        const int64_t total = __shfl_sync(0xffffffffu, upto, 31) * blocks;
+        const int64_t each = quot(total, groups), rest = total - each * groups;
+        const auto bound = [&](int c) { return each * c + int64_t(uint32_t(rest) * c / groups); };
+        const int64_t lo = bound(group), hi = bound(group + 1);
         // the last lane whose sequences start at or before lo
-        const uint32_t before = __ballot_sync(0xffffffffu, (upto - mine) * p.Hkv <= lo);
+        const uint32_t before = __ballot_sync(0xffffffffu, (upto - mine) * blocks <= lo);
         const int from = 31 - __clz(before);
-        int64_t base = __shfl_sync(0xffffffffu, upto - mine, from) * p.Hkv;
+        int64_t base = __shfl_sync(0xffffffffu, upto - mine, from) * blocks;
         int first_s = from * per;
-        while (first_s < p.B && base + costs[first_s] * p.Hkv <= lo) base += costs[first_s++] * p.Hkv;
+        while (first_s < p.B && base + costs[first_s] * blocks <= lo) base += costs[first_s++] * blocks;
         // the first sequence's metadata is still at hand; the next ones are read again
         Seq q;
         if (first_s < min(p.B, kMetaSeqs)) {
@@ -548,12 +552,12 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             I.held = q.held;
             I.last = 0;
             I.n_qt = q.n_qt;
-            for (int h = base < lo ? int(quot(lo - base, q.head_cost)) : 0; h < p.Hkv && ok; ++h) {
+            for (int h = base < lo ? int(quot(lo - base, q.head_cost)) : 0; h < blocks && ok; ++h) {
                 const int64_t hb = base + h * q.head_cost;
                 if (hb >= hi) break;
                 const int ta = tile_at(q, lo - hb, log2qt), tb = tile_at(q, hi - hb, log2qt);
-                I.kvh = h;
-                I.state = (int64_t(q.row) * p.Hkv + h) * p.max_len;
+                I.kvh = h * p.heads + member;
+                I.state = (int64_t(q.row) * p.Hkv + I.kvh) * p.max_len;
                 if (q.few) {
                     if (ta >= tb) continue;
                     I.t0 = ta;
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     }
                 }
             }
-            base += q.head_cost * p.Hkv;
+            base += q.head_cost * blocks;
         }
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (ok) {
@@ -1004,8 +1008,10 @@ int32_t launch_weights(const CUtensorMap& k, const CUtensorMap& q1, const CUtens
             return st;
         raised[dev].store(true, std::memory_order_release);
     }
-    const int64_t tiles =
-        int64_t(p.B) * p.Hkv * ((int64_t(p.max_len) + kTileKeys - 1) / kTileKeys);
+    // whole groups: 152 is a multiple of 8
+    const int64_t tiles = int64_t(p.B) * (p.Hkv / p.heads) *
+                          ((int64_t(p.max_len) + kTileKeys - 1) / kTileKeys) * p.heads;
+    static_assert(PA_PLAN_CTAS % 8 == 0, "groups of up to 8 CTAs");
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1121,6 +1127,7 @@ int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
     p.Hq = s->num_q_heads;
     p.Hkv = s->num_kv_heads;
     p.g = g;
+    p.heads = p.Hkv % 8 == 0 ? 8 : p.Hkv % 4 == 0 ? 4 : p.Hkv % 2 == 0 ? 2 : 1;
     p.bs = s->block_size;
     p.num_blocks = s->num_blocks;
     p.n_rows = n_rows;
