@@ -30,8 +30,9 @@
 // Warps: 0-15 four epilogue warpgroups, 16 scheduler and loader of what stays, 17 and 19 MMA issuers,
 // 18 loader of what streams; over an fp8 cache 20-23 turn codes and q to f16. There are four
 // accumulators of 128 TMEM columns, warpgroup w reads accumulator w: FEW's stream tiles take them in
-// turn, a MANY item's key tile r has accumulator r, and of one or two key tiles the query tiles
-// alternate between accumulators r and r + 2, whose sums meet in memory at the item's end. Issuer i fills accumulators i and i + 2: its
+// turn, a MANY item's key tile r has accumulator r; with two key tiles the query tiles alternate
+// between accumulators r and r + 2, with one they take all four in turn, and the sums meet in memory
+// at the item's end, in a fixed order. Issuer i fills accumulators i and i + 2: its
 // waits, commits and address arithmetic, made slow by the warps it shares its scheduler with, run
 // while the other's MMAs keep the tensor pipe busy.
 // Shared memory: seven 32 KB slots. Four in a ring for what stays (the next item's tiles load as this
@@ -90,10 +91,12 @@ enum Bar {
     kItemEmpty = 38,   // + slot: every consumer warp
     kPartDone = 42,    // + key tile of two: 4 arrivals, warpgroup r + 2 -> r
     kPartSeen = 44,    // + key tile of two: 4 arrivals, warpgroup r -> r + 2
-    kDrain = 46,       // + issuer
-    kStayReady = 48,   // + slot, fp8 only: the f16 warps
-    kStreamReady = 52, // + stage
-    kNumBars = 57
+    kChainDone = 46,   // + w, one key tile: 4 arrivals, warpgroup w + 1 -> w
+    kChainSeen = 49,   // + w, one key tile: 4 arrivals, warpgroup w -> w + 1
+    kDrain = 52,       // + issuer
+    kStayReady = 54,   // + slot, fp8 only: the f16 warps
+    kStreamReady = 58, // + stage
+    kNumBars = 63
 };
 constexpr int kHolderOff = 8 * kNumBars;
 constexpr int kAbortOff = kHolderOff + 4;
@@ -140,13 +143,14 @@ __device__ __forceinline__ int first_qt(const Seq& q, int t, int log2qt) {
     return max(0, t * kTileKeys - q.pos0) >> log2qt;
 }
 
-// Cost of a head's key tiles before tile t.
+// Cost of a head's key tiles before tile t: a tile costs the query tiles that the first of its four
+// meets (an item passes all of them by its four tiles).
 __device__ __forceinline__ int64_t cost_before(const Seq& q, int t, int log2qt) {
     if (q.few) return kCostFew * t;
     // tiles up to u meet every query tile
-    const int u = min(t, (q.pos0 + (1 << log2qt) - 1) / kTileKeys + 1);
+    const int u = min(t, ((q.pos0 + (1 << log2qt) - 1) / kTileKeys + 4) & ~3);
     int64_t f = int64_t(u) * q.n_qt;
-    for (int i = u; i < t; ++i) f += q.n_qt - first_qt(q, i, log2qt);
+    for (int i = u; i < t; ++i) f += q.n_qt - first_qt(q, i & ~3, log2qt);
     return kCostMany * f;
 }
 
@@ -161,12 +165,12 @@ __device__ __forceinline__ int tile_at(const Seq& q, int64_t x, int log2qt) {
     if (x <= 0) return 0;
     if (x >= q.head_cost) return q.n_tiles;
     if (q.few) return int(quot(x + kCostFew - 1, kCostFew));
-    const int u = min(q.n_tiles, (q.pos0 + (1 << log2qt) - 1) / kTileKeys + 1);
+    const int u = min(q.n_tiles, ((q.pos0 + (1 << log2qt) - 1) / kTileKeys + 4) & ~3);
     const int64_t per = kCostMany * q.n_qt;
     if (x <= per * u) return int(quot(x + per - 1, per));
     int64_t f = per * u;
     int t = u;
-    for (; t < q.n_tiles && f < x; ++t) f += kCostMany * (q.n_qt - first_qt(q, t, log2qt));
+    for (; t < q.n_tiles && f < x; ++t) f += kCostMany * (q.n_qt - first_qt(q, t & ~3, log2qt));
     return t;
 }
 
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 const auto stay = [&](int r) {
                     return make_sdesc(sb + stay_at(first_slot(r), n_stay), 16, 1024);
                 };
-                const uint64_t stay0 = stay(few ? 0 : me), stay1 = stay(few ? 0 : me + 2);
+                const uint64_t stay0 = stay(few || I.nt == 1 ? 0 : me), stay1 = stay(few ? 0 : me + 2);
                 const int end = n + (few ? I.nt : I.n_qt - I.qt0);
                 const int last_cols = (I.n_q - ((I.n_qt - 1) << log2qt)) * p.g;
                 const uint32_t idesc_last = make_idesc(128, (last_cols + 15) & ~15, false, F8);
@@ -641,8 +645,9 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                         }
                     } else {
                         const uint32_t idesc = n + 1 == end ? idesc_last : idesc_full;
-                        if (me < I.nt) {
-                            const int h = I.nt <= 2 ? n & 1 : 0;
+                        const bool mine = I.nt == 1 ? (n & 1) == me : me < I.nt;
+                        if (mine) {
+                            const int h = I.nt == 1 ? n >> 1 & 1 : I.nt == 2 ? n & 1 : 0;
                             if (!take_back(h)) break;
                             tc_fence_after();
                             issue_s_group<D>(1u, tmem + (me + 2 * h) * kCols, stay0, stage, idesc);
@@ -809,7 +814,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         // after the sums over the four threads of a key have met, thread q4 has key rs + 8 q4
         const int key_in_tile = 32 * (warp & 3) + rs + 8 * q4;
         const uint64_t c2 = f2(p.c, p.c);
-        int n = 0, acc_ph = 0, n_lse = 0, n_part = 0;
+        int n = 0, acc_ph = 0, n_lse = 0, n_part = 0, n_chain = 0;
         const uint32_t full = bar(kAccFull + w), empty = bar(kAccEmpty + w);
         const float4* lse_smem = reinterpret_cast<const float4*>(smem + kCtl + kLseOff) + q4;
         bool ok = true;
@@ -934,13 +939,16 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 n += I.nt;
                 continue;
             }
-            // one key tile, all query tiles; or of one or two key tiles every second query tile
-            const bool half = I.nt <= 2;
-            const int r = half ? w & 1 : w;
+            // key tile r: all query tiles, or with one or two key tiles those n with n & mod == w's
+            const int mod = I.nt == 1 ? 3 : I.nt == 2 ? 1 : 0;
+            const int r = I.nt == 1 ? 0 : I.nt == 2 ? w & 1 : w;
+            const int turn = I.nt == 1 ? w : w >> 1;
             const bool my = r < I.nt;
             const int kb = (I.t0 + r) * kTileKeys, j = kb + key_in_tile, kw = kb + 32 * (warp & 3);
             float* dst = p.weights + I.state + j;
-            const float old = my && (!half || w >= 2) && j < I.held ? *dst : 0.f;
+            // the sums meet in the order of falling w: the first to add has the old one
+            const bool opens = mod == 0 || w == 3 || (mod == 1 && w == 2);
+            const float old = my && opens && j < I.held ? *dst : 0.f;
             clear();
             for (int qt = I.qt0; qt < I.n_qt; ++qt, ++n, ++n_lse) {
                 const int tok = qt << log2qt, cols = min(kCols, (I.n_q - tok) * p.g);
@@ -948,7 +956,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 const float4* nl = lse_smem + (n_lse & 3) * 32;
                 if (!(ok = wait_bounded(bar(kLseFull + (n_lse & 3)), n_lse >> 2 & 1, abort_word)))
                     break;
-                if (my && (!half || (n & 1) == w >> 1)) {
+                if (my && (n & mod) == (turn & mod)) {
                     if (!(ok = wait_bounded(full, acc_ph, abort_word))) break;
                     acc_ph ^= 1;
                     tc_fence_after();
@@ -961,22 +969,28 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             if (!ok) break;
             if (!my) continue;
             const float sum = total_of_key();
-            if (!half) {
+            if (mod == 0) {
                 if (j < I.ctx) *dst = old + sum;
                 continue;
             }
-            if (w >= 2) {
+            // from the warpgroup before in the order, to the one after
+            const int hop = mod == 1 ? 2 : 1;
+            int& n_hops = mod == 1 ? n_part : n_chain;
+            const int done = mod == 1 ? kPartDone : kChainDone, seen = mod == 1 ? kPartSeen : kChainSeen;
+            if (opens) {
                 if (j < I.ctx) *dst = old + sum;
-                if (n_part > 0 &&
-                    !(ok = wait_bounded(bar(kPartSeen + r), (n_part - 1) & 1, abort_word)))
-                    break;
-                warp_arrive(bar(kPartDone + r));
             } else {
-                if (!(ok = wait_bounded(bar(kPartDone + r), n_part & 1, abort_word))) break;
-                warp_arrive(bar(kPartSeen + r));
+                if (!(ok = wait_bounded(bar(done + w), n_hops & 1, abort_word))) break;
+                warp_arrive(bar(seen + w));
                 if (j < I.ctx) *dst += sum;
             }
-            ++n_part;
+            if (w >= hop) {
+                if (n_hops > 0 &&
+                    !(ok = wait_bounded(bar(seen + w - hop), (n_hops - 1) & 1, abort_word)))
+                    break;
+                warp_arrive(bar(done + w - hop));
+            }
+            ++n_hops;
         }
     }
     if (*abort_word && threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_TIMEOUT);
