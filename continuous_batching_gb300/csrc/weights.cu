@@ -32,7 +32,8 @@
 // accumulators of 128 TMEM columns, warpgroup w reads accumulator w: FEW's stream tiles take them in
 // turn, a MANY item's key tile r has accumulator r; with two key tiles the query tiles alternate
 // between accumulators r and r + 2, with one they take all four in turn, and the sums meet in memory
-// at the item's end, in a fixed order. Issuer i fills accumulators i and i + 2: its
+// at the item's end. A key's sum is the same whichever way its tile came to be taken: query tiles are
+// summed in four classes (qt % 4), and these are added to the old sum in the order 0, 2, 1, 3. Issuer i fills accumulators i and i + 2: its
 // waits, commits and address arithmetic, made slow by the warps it shares its scheduler with, run
 // while the other's MMAs keep the tensor pipe busy.
 // Shared memory: seven 32 KB slots. Four in a ring for what stays (the next item's tiles load as this
@@ -89,10 +90,10 @@ enum Bar {
     kLseEmpty = 30,    // + slot, MANY: 16 arrivals
     kItemFull = 34,    // + slot (4)
     kItemEmpty = 38,   // + slot: every consumer warp
-    kPartDone = 42,    // + key tile of two: 4 arrivals, warpgroup r + 2 -> r
-    kPartSeen = 44,    // + key tile of two: 4 arrivals, warpgroup r -> r + 2
-    kChainDone = 46,   // + w, one key tile: 4 arrivals, warpgroup w + 1 -> w
-    kChainSeen = 49,   // + w, one key tile: 4 arrivals, warpgroup w -> w + 1
+    kPartDone = 42,    // + key tile of two: 4 arrivals, warpgroup r -> r + 2
+    kPartSeen = 44,    // + key tile of two: 4 arrivals, warpgroup r + 2 -> r
+    kChainDone = 46,   // + place, one key tile: 4 arrivals, a warpgroup -> the next
+    kChainSeen = 49,   // + place, one key tile: 4 arrivals, and back
     kDrain = 52,       // + issuer
     kStayReady = 54,   // + slot, fp8 only: the f16 warps
     kStreamReady = 58, // + stage
@@ -172,6 +173,39 @@ __device__ __forceinline__ int tile_at(const Seq& q, int64_t x, int log2qt) {
     int t = u;
     for (; t < q.n_tiles && f < x; ++t) f += kCostMany * (q.n_qt - first_qt(q, t & ~3, log2qt));
     return t;
+}
+
+// The order in which an item's query tiles qt0 .. n_qt - 1 stream: class by class with three or four
+// key tiles (each accumulator's warpgroup sums one class after the other), classes 0 and 1 before 2 and
+// 3 with two (a warpgroup takes the even or the odd ones), as they come with one (a warpgroup each).
+__device__ __forceinline__ int first_in_class(int c, int qt0) { return qt0 + ((c - qt0) & 3); }
+__device__ __forceinline__ int first_in_half(int h, int qt0) {          // >= qt0, qt & 2 == h
+    return (qt0 & 2) == h ? qt0 : (qt0 | 1) + 1;
+}
+__device__ __forceinline__ int next_class(int c) { return 0x3132 >> (4 * c) & 3; }   // 0, 2, 1, 3
+__device__ __forceinline__ int stream_first(int qt0, int n_qt, int nt) {
+    if (nt == 1) return qt0;
+    if (nt == 2) {
+        const int qt = first_in_half(0, qt0);
+        return qt < n_qt ? qt : first_in_half(2, qt0);
+    }
+    int c = 0, qt = first_in_class(0, qt0);
+    while (qt >= n_qt) {
+        c = next_class(c);
+        qt = first_in_class(c, qt0);
+    }
+    return qt;
+}
+// The one behind qt (there is one).
+__device__ __forceinline__ int stream_next(int qt, int qt0, int n_qt, int nt) {
+    if (nt == 1) return qt + 1;
+    if (nt == 2) {
+        const int next = qt & 1 ? qt + 3 : qt + 1;
+        return next < n_qt || (qt & 2) ? next : first_in_half(2, qt0);
+    }
+    int c = qt & 3;
+    for (qt += 4; qt >= n_qt; qt = first_in_class(c, qt0)) c = next_class(c);
+    return qt;
 }
 
 // What follows from n_q and ctx.
@@ -627,6 +661,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 };
                 const uint64_t stay0 = stay(few || I.nt == 1 ? 0 : me), stay1 = stay(few ? 0 : me + 2);
                 const int end = n + (few ? I.nt : I.n_qt - I.qt0);
+                int qt = few ? 0 : stream_first(I.qt0, I.n_qt, I.nt);
                 const int last_cols = (I.n_q - ((I.n_qt - 1) << log2qt)) * p.g;
                 const uint32_t idesc_last = make_idesc(128, (last_cols + 15) & ~15, false, F8);
                 for (; n < end; ++n) {
@@ -644,10 +679,10 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                             mbar_arrive(bar(kStreamEmpty + st));
                         }
                     } else {
-                        const uint32_t idesc = n + 1 == end ? idesc_last : idesc_full;
-                        const bool mine = I.nt == 1 ? (n & 1) == me : me < I.nt;
+                        const uint32_t idesc = qt + 1 == I.n_qt ? idesc_last : idesc_full;
+                        const bool mine = I.nt == 1 ? (qt & 1) == me : me < I.nt;
                         if (mine) {
-                            const int h = I.nt == 1 ? n >> 1 & 1 : I.nt == 2 ? n & 1 : 0;
+                            const int h = I.nt == 1 ? qt >> 1 & 1 : I.nt == 2 ? qt & 1 : 0;
                             if (!take_back(h)) break;
                             tc_fence_after();
                             issue_s_group<D>(1u, tmem + (me + 2 * h) * kCols, stay0, stage, idesc);
@@ -663,6 +698,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                             tc_commit_if(1u, bar(kAccFull + me + 2));
                         }
                         tc_commit_if(1u, bar(kStreamEmpty + st));
+                        if (n + 1 < end) qt = stream_next(qt, I.qt0, I.n_qt, I.nt);
                     }
                     if (++st == n_stages) {
                         st = 0;
@@ -705,7 +741,8 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 }
                 return make_float4(v[0], v[1], v[2], v[3]);
             };
-            float4 l_next = few ? make_float4(0.f, 0.f, 0.f, 0.f) : fetch_lse(I.qt0);
+            int qt = few ? 0 : stream_first(I.qt0, I.n_qt, I.nt);
+            float4 l_next = few ? make_float4(0.f, 0.f, 0.f, 0.f) : fetch_lse(qt);
             for (int i = 0; i < n; ++i) {
                 const int at = i & (per_load - 1);
                 if (few && at == 0 && i > 0) ids = next;
@@ -723,12 +760,15 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 } else {
                     const int lse_slot = n_lse & 3;
                     if (lane == 0) {
-                        load_q(slot, full, I, I.qt0 + i);
+                        load_q(slot, full, I, qt);
                         ok = wait_bounded(bar(kLseEmpty + lse_slot), (n_lse >> 2 & 1) ^ 1,
                                           abort_word);
                     }
                     const float4 v = l_next;
-                    if (i + 1 < n) l_next = fetch_lse(I.qt0 + i + 1);
+                    if (i + 1 < n) {
+                        qt = stream_next(qt, I.qt0, I.n_qt, I.nt);
+                        l_next = fetch_lse(qt);
+                    }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (ok) {
                         float* to = reinterpret_cast<float*>(smem + kCtl + kLseOff) +
@@ -939,24 +979,36 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 n += I.nt;
                 continue;
             }
-            // key tile r: all query tiles, or with one or two key tiles those n with n & mod == w's
+            // key tile r: all query tiles, or with one or two key tiles those with qt & mod == w's
             const int mod = I.nt == 1 ? 3 : I.nt == 2 ? 1 : 0;
             const int r = I.nt == 1 ? 0 : I.nt == 2 ? w & 1 : w;
             const int turn = I.nt == 1 ? w : w >> 1;
             const bool my = r < I.nt;
             const int kb = (I.t0 + r) * kTileKeys, j = kb + key_in_tile, kw = kb + 32 * (warp & 3);
             float* dst = p.weights + I.state + j;
-            // the sums meet in the order of falling w: the first to add has the old one
-            const bool opens = mod == 0 || w == 3 || (mod == 1 && w == 2);
+            // the one that has class 0 begins with the old sum; the classes are added in the order
+            // 0, 2, 1, 3, those of another warpgroup once they are there (at most two: kept apart)
+            const bool opens = mod == 0 || turn == 0;
             const float old = my && opens && j < I.held ? *dst : 0.f;
+            float sum = old, later = 0.f;
+            int qt = stream_first(I.qt0, I.n_qt, I.nt), now = -1;
+            const auto close = [&]() {                   // the class that was being summed
+                const float s = total_of_key();
+                if (opens) sum += s;
+                else if (mod == 1 && now >= 2) later = s;
+                else sum = s;
+                clear();
+            };
             clear();
-            for (int qt = I.qt0; qt < I.n_qt; ++qt, ++n, ++n_lse) {
+            for (int i = I.qt0; i < I.n_qt; ++i, ++n, ++n_lse) {
                 const int tok = qt << log2qt, cols = min(kCols, (I.n_q - tok) * p.g);
                 const int at = I.pos0 + tok;             // the tile's first row
                 const float4* nl = lse_smem + (n_lse & 3) * 32;
                 if (!(ok = wait_bounded(bar(kLseFull + (n_lse & 3)), n_lse >> 2 & 1, abort_word)))
                     break;
-                if (my && (n & mod) == (turn & mod)) {
+                if (my && (qt & mod) == (turn & mod)) {
+                    if (now >= 0 && now != (qt & 3)) close();
+                    now = qt & 3;
                     if (!(ok = wait_bounded(full, acc_ph, abort_word))) break;
                     acc_ph ^= 1;
                     tc_fence_after();
@@ -965,30 +1017,33 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     else add_masked(I, tok, cols, kw, nl);
                 }
                 warp_arrive(bar(kLseEmpty + (n_lse & 3)));
+                if (i + 1 < I.n_qt) qt = stream_next(qt, I.qt0, I.n_qt, I.nt);
             }
             if (!ok) break;
             if (!my) continue;
-            const float sum = total_of_key();
+            if (now >= 0) close();
             if (mod == 0) {
-                if (j < I.ctx) *dst = old + sum;
+                if (j < I.ctx) *dst = sum;
                 continue;
             }
-            // from the warpgroup before in the order, to the one after
-            const int hop = mod == 1 ? 2 : 1;
+            // the warpgroups' order: 0, 2, 1, 3 with one key tile, r, r + 2 with two
+            const int place = mod == 1 ? w >> 1 : w == 0 ? 0 : w == 2 ? 1 : w == 1 ? 2 : 3;
+            const int hops = mod == 1 ? 1 : 3, of = mod == 1 ? r : place;
             int& n_hops = mod == 1 ? n_part : n_chain;
             const int done = mod == 1 ? kPartDone : kChainDone, seen = mod == 1 ? kPartSeen : kChainSeen;
             if (opens) {
-                if (j < I.ctx) *dst = old + sum;
+                if (j < I.ctx) *dst = sum;
             } else {
-                if (!(ok = wait_bounded(bar(done + w), n_hops & 1, abort_word))) break;
-                warp_arrive(bar(seen + w));
-                if (j < I.ctx) *dst += sum;
+                const int from = mod == 1 ? of : of - 1;
+                if (!(ok = wait_bounded(bar(done + from), n_hops & 1, abort_word))) break;
+                warp_arrive(bar(seen + from));
+                if (j < I.ctx) *dst = (*dst + sum) + later;
             }
-            if (w >= hop) {
+            if (place < hops) {
                 if (n_hops > 0 &&
-                    !(ok = wait_bounded(bar(seen + w - hop), (n_hops - 1) & 1, abort_word)))
+                    !(ok = wait_bounded(bar(seen + of), (n_hops - 1) & 1, abort_word)))
                     break;
-                warp_arrive(bar(done + w - hop));
+                warp_arrive(bar(done + of));
             }
             ++n_hops;
         }

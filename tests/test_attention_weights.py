@@ -186,6 +186,39 @@ def test_rows_held_and_windows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq, Hkv, D, fp8", [(8, 2, 128, False), (8, 8, 64, False), (16, 2, 128, True)])
+def test_a_sequences_bits_do_not_depend_on_the_batch(Hq, Hkv, D, fp8):
+    """However the key tiles are dealt (four, three, two or one to an item), a sum has the same bits."""
+    ctx, n_q = [1500, 700, 2048, 130, 90, 901], [700, 1, 300, 130, 20, 515]
+    st = wl.make_step(Hq, Hkv, D, 16, ctx, n_q, seed=12)
+    shape = bd.Shape.make(st.Hq, st.Hkv, st.D, st.block_size, st.num_blocks)
+    q = dev(st.q.view(np.int16), torch.bfloat16)
+    kp = dev(ofp8.quantize(st.k_pool, 0.0125)) if fp8 else dev(st.k_pool.view(np.int16), torch.bfloat16)
+    gen = torch.Generator("cuda").manual_seed(3)
+    lse = 4 + torch.rand(st.T, Hq, device="cuda", generator=gen)
+    start = torch.rand(len(ctx), Hkv, 2100, device="cuda", generator=gen)
+
+    def run(seqs):
+        w = start.clone()
+        at = [slice(int(st.cu_seqlens_q[s]), int(st.cu_seqlens_q[s + 1])) for s in seqs]
+        cu = np.concatenate([[0], np.cumsum([n_q[s] for s in seqs])]).astype(np.int32)
+        i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+        args = (torch.cat([q[a] for a in at]), kp, torch.cat([lse[a] for a in at]), dev(st.block_table[list(seqs)]),
+                dev(cu), i32([ctx[s] for s in seqs]), i32(list(seqs)), w)
+        if fp8:
+            bd.paged_attention_weights_fp8(*args, 0.0125, shape)
+        else:
+            bd.paged_attention_weights(*args, shape)
+        return w
+
+    whole = run(range(len(ctx)))
+    for seqs in [[s] for s in range(len(ctx))] + [[4, 0], [2, 5, 1], [5, 4, 3, 2, 1, 0], [0] + [1, 3, 4]]:
+        part = run(seqs)
+        for s in range(len(ctx)):
+            assert torch.equal(part[s], whole[s] if s in seqs else start[s]), (seqs, s)
+
+
+@pytest.mark.gpu
 def test_stale_keys_and_values_outside_leave_no_trace():
     """NaN and infinity in the rows behind ctx, in blocks of nobody and in the q rows of another
     sequence reach only what they belong to."""
