@@ -66,9 +66,11 @@ constexpr int kSlot = 32768;                   // one tile, 128 rows of D = 128
 constexpr int kHalf = 16384;                   // its 64-column halves
 constexpr int kMaxStages = 5;
 constexpr int kCtl = 7 * kSlot;
-constexpr int kBytes = kCtl + 3072;
+constexpr int kCtlBytes = 3 * 1024;            // barriers, items, log-sum-exps
+constexpr int kBytes = kCtl + kCtlBytes;
 static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr int kMaxRows = 1 << 18;              // state rows whose repeats are looked for
+constexpr int kMaxLen = INT32_MAX - 32 * 128;  // keys: a warp's 32 blocks more are counted in 32 bits
 constexpr int kMaxSeqs = 8192;                 // sequences whose costs are held while they are dealt
 // before the pipeline starts: a bit per state row in slot 0, the first sequences' metadata from slot
 // 1, a cost per sequence from slot 4
@@ -104,7 +106,7 @@ constexpr int kAbortOff = kHolderOff + 4;
 constexpr int kRingOff = 512;                  // 4 items of 64 bytes
 constexpr int kLseOff = kRingOff + 4 * 64;     // MANY: 4 x 128 log-sum-exps
 constexpr int kTwiceOff = kLseOff + 4 * 512;   // whether some state row is named twice
-static_assert(kAbortOff + 4 <= kRingOff && kTwiceOff + 4 <= 3072, "control area");
+static_assert(kAbortOff + 4 <= kRingOff && kTwiceOff + 4 <= kCtlBytes, "control area");
 
 // Slots of stage st of the stream, and of tile k of what stays.
 __device__ __forceinline__ uint32_t stage_at(int st) {
@@ -1095,12 +1097,17 @@ int32_t launch_weights(const CUtensorMap& k, const CUtensorMap& q1, const CUtens
 }
 
 // ------------------------------------------------ decode rows of a step that kept their scores
+// Scores kept for a step: rows of a whole number of tiles.
+__host__ __device__ int64_t scores_row(int32_t max_ctx) {
+    return (int64_t(max_ctx) + kTileKeys - 1) / kTileKeys * kTileKeys;
+}
+
 // One thread per four keys of a (sequence, KV head): the group's raw scores, stored by the
 // attention kernel, against the rows' log-sum-exps. A decode step so pays 4 g bytes per key and
 // KV head written and read again (in L2, mostly) in place of a second read of K's 2 D.
 constexpr int kDecodeKeys = 1024;      // per block of 256 threads
 __global__ void __launch_bounds__(256)
-    decode_weights_kernel(const float* __restrict__ scores, int64_t scores_ld, const Params p) {
+    decode_weights_kernel(const float* __restrict__ scores, int32_t max_ctx, const Params p) {
     __shared__ float nl[16];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1110,7 +1117,7 @@ __global__ void __launch_bounds__(256)
     const int j0 = int(blockIdx.x) * kDecodeKeys;
     if (p.cu[s + 1] - c0 != 1 || row < 0 || (j0 >= ctx && j0 > 0)) return;
     const int held = p.held ? p.held[s] : ctx - 1;
-    bool bad = c0 < 0 || c0 >= p.T || ctx < 1 || ctx > p.max_len || ctx > scores_ld ||
+    bool bad = c0 < 0 || c0 >= p.T || ctx < 1 || ctx > p.max_len || ctx > max_ctx ||
                (int64_t(ctx) + p.bs - 1) / p.bs > p.max_blocks || row >= p.n_rows || held < 0 ||
                held > ctx;
     if (p.rows)
@@ -1126,7 +1133,8 @@ __global__ void __launch_bounds__(256)
     }
     const int j = j0 + 4 * int(threadIdx.x);
     if (j >= ctx) return;
-    // scores_ld is a multiple of 128: a thread's four lie within the row
+    // a row of scores is a whole number of tiles: a thread's four lie within it
+    const int64_t scores_ld = scores_row(max_ctx);
     const float* sc = scores + (int64_t(s) * p.Hq + h * p.g) * scores_ld + j;
     float* w = p.weights + (int64_t(row) * p.Hkv + h) * p.max_len + j;
     float sum[4];
@@ -1144,10 +1152,6 @@ __global__ void __launch_bounds__(256)
         if (j + e < ctx) w[e] = sum[e];
 }
 
-// Scores kept for a step: rows of a whole number of tiles.
-int64_t scores_row(int32_t max_ctx) {
-    return (int64_t(max_ctx) + kTileKeys - 1) / kTileKeys * kTileKeys;
-}
 size_t partials_bytes(const pa_shape* s, int32_t T, int32_t max_ctx) {
     return (pa_workspace_bytes(s, T, max_ctx) + 255) & ~size_t(255);
 }
@@ -1168,7 +1172,7 @@ int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
     if (!q || !k_pool || !lse || !block_table || !cu || !ctx || !weights) return PA_ERR_INVALID;
     if (max_len == 0 || (!rows && n_rows < B)) return PA_ERR_INVALID;
     if (n_rows > kMaxRows || int64_t(s->num_blocks) * s->block_size > INT32_MAX ||
-        max_len > INT32_MAX - kTileKeys)
+        max_len > kMaxLen)
         return PA_ERR_SHAPE;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pool)) & 15 ||
         reinterpret_cast<uintptr_t>(lse) & 7)
@@ -1215,7 +1219,7 @@ int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
         cfg.attrs = pdl;
         cfg.numAttrs = 1;
         if ((st = note_cuda(cudaLaunchKernelEx(&cfg, decode_weights_kernel, scores,
-                                               scores_row(max_ctx), p))))
+                                               max_ctx, p))))
             return st;
     }
     if (fp8) return launch_weights<128, true>(k, q1, qn, p, stream);
@@ -1266,12 +1270,13 @@ int32_t step_weights(const void* q, const void* k_pool, const void* v_pool,
         !weights || max_len <= 0 || max_ctx == 0 || n_rows < 0 || (!rows && n_rows < B))
         return PA_ERR_INVALID;
     if (B > kMaxSeqs || s->num_kv_heads > 65535 || n_rows > kMaxRows ||
-        max_len > INT32_MAX - kTileKeys || max_ctx > INT32_MAX - kTileKeys ||
+        max_len > kMaxLen || max_ctx > kMaxLen ||
         int64_t(s->num_blocks) * s->block_size > INT32_MAX)
         return PA_ERR_SHAPE;
     if (!workspace || ws_bytes < pa_step_weights_workspace_bytes(s, B, T, max_ctx))
         return PA_ERR_WORKSPACE;
-    if (reinterpret_cast<uintptr_t>(workspace) & 15) return PA_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 15) || (reinterpret_cast<uintptr_t>(lse) & 7))
+        return PA_ERR_INVALID;
     float* scores = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                              partials_bytes(s, T, max_ctx));
     if ((st = attention_step_stats(q, k_pool, v_pool, block_table, max_blocks, cu, ctx, B, T,

@@ -549,10 +549,10 @@ int32_t paged_qk_norm_rope_write_fp8(const void* q, int64_t q_stride, const void
  * NULL int32. A sequence whose metadata does not fit (n_q > ctx, ctx > max_len or the table, held
  * outside [0, ctx], a row >= n_rows or named by another sequence with query rows) is skipped and
  * sets PA_DEVERR_META. Weights whose lse or q is NaN are NaN.
- * Host checks: as paged_attention_step; lse 8-byte aligned; B <= 8192 and n_rows <= 2^18 (PA_ERR_SHAPE); n_rows >= B
- * without rows. One launch, a
- * programmatic dependent of what precedes it, no workspace, nothing planned on the host: a captured
- * call follows its metadata. */
+ * Host checks: as paged_attention_step; lse 8-byte aligned; B <= 8192, n_rows <= 2^18 and
+ * max_len < 2^31 - 4096 (PA_ERR_SHAPE); n_rows >= B without rows. One launch, a programmatic
+ * dependent of what precedes it, no workspace, nothing planned on the host: a captured call follows
+ * its metadata. */
 int32_t paged_attention_weights(const void* q, const void* k_pool, const float* lse,
                                 const int32_t* block_table, int32_t max_blocks,
                                 const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t B,

@@ -53,7 +53,8 @@ def _call(**kw):
     (dict(cu=None), bd.PA_ERR_INVALID), (dict(ctx=None), bd.PA_ERR_INVALID),
     (dict(w=None), bd.PA_ERR_INVALID), (dict(m=0), bd.PA_ERR_INVALID), (dict(m=-1), bd.PA_ERR_INVALID),
     (dict(rows=None, n=1), bd.PA_ERR_INVALID), (dict(n=(1 << 18) + 1), bd.PA_ERR_SHAPE),
-    (dict(m=2 ** 31 - 1), bd.PA_ERR_SHAPE), (dict(q=24), bd.PA_ERR_INVALID),
+    (dict(m=2 ** 31 - 1), bd.PA_ERR_SHAPE), (dict(m=2 ** 31 - 4096), bd.PA_ERR_SHAPE),
+    (dict(lse=20), bd.PA_ERR_INVALID), (dict(q=24), bd.PA_ERR_INVALID),
     (dict(kp=8), bd.PA_ERR_INVALID), (dict(shape=bd.Shape.make(4, 2, 32, 16, 8)), bd.PA_ERR_SHAPE),
     (dict(shape=bd.Shape.make(6, 2, 128, 16, 8)), bd.PA_ERR_SHAPE),
     (dict(shape=bd.Shape.make(4, 2, 64, 16, 8), scale=1.0), bd.PA_ERR_SHAPE),
@@ -61,6 +62,29 @@ def _call(**kw):
 ])
 def test_refusals(kw, want):
     assert _call(**kw) == want
+
+
+def _step_call(**kw):
+    a = dict(q=16, kp=16, vp=16, tb=16, mb=4, cu=16, ctx=16, B=2, T=2, mc=64, items=16, n_items=2, ws=16,
+             wb=None, out=16, lse=16, held=None, rows=16, w=16, n=4, m=64)
+    shape = bd.Shape.make(4, 2, 128, 16, 8)
+    a.update(kw)
+    if a["wb"] is None:
+        a["wb"] = bd.pa_step_weights_workspace_bytes(shape, max(a["B"], 0), max(a["T"], 0), max(a["mc"], 0))
+    return bd.load().paged_attention_step_weights(*a.values(), shape, None, None)
+
+
+# Every refusal comes before the attention step's launch (it would fail here, without a device).
+@pytest.mark.parametrize("kw, want", [
+    (dict(T=0), bd.PA_OK), (dict(B=0), bd.PA_OK), (dict(n_items=0), bd.PA_OK), (dict(B=-1), bd.PA_ERR_INVALID),
+    (dict(mc=0), bd.PA_ERR_INVALID), (dict(mc=2 ** 31 - 4096), bd.PA_ERR_SHAPE),
+    (dict(m=2 ** 31 - 4096), bd.PA_ERR_SHAPE), (dict(m=0), bd.PA_ERR_INVALID), (dict(w=None), bd.PA_ERR_INVALID),
+    (dict(lse=None), bd.PA_ERR_INVALID), (dict(lse=20), bd.PA_ERR_INVALID), (dict(ws=None), bd.PA_ERR_WORKSPACE),
+    (dict(wb=64), bd.PA_ERR_WORKSPACE), (dict(ws=24), bd.PA_ERR_INVALID), (dict(rows=None, n=1), bd.PA_ERR_INVALID),
+    (dict(B=8193, n=8193), bd.PA_ERR_SHAPE), (dict(n=(1 << 18) + 1), bd.PA_ERR_SHAPE),
+])
+def test_step_refusals(kw, want):
+    assert _step_call(**kw) == want
 
 
 # ------------------------------------------------------------------ the kernels (GPU)
@@ -436,6 +460,8 @@ def test_step_refusals_and_contexts_behind_the_bound():
             run(**bad)
     # sequence 1 is longer than the bound the caller gave: its scores have no room, it adds nothing
     assert run(max_ctx=100) == ([True, False, True], bd.PA_DEVERR_META)
+    assert run(max_ctx=149) == ([True, False, True], bd.PA_DEVERR_META)   # one key, within the same tile
+    assert run(max_ctx=150) == ([True] * 3, 0)
     assert run(max_len=100) == ([True, False, True], bd.PA_DEVERR_META)
     assert run(rows=(0, 2, 2)) == ([True, False, False], bd.PA_DEVERR_META)
     assert run(rows=(0, -1, 2)) == ([True, False, True], 0)
