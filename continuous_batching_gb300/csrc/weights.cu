@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     // ---- every sequence's cost, and whether two name one state row
     int n_stages;
     {
-        bool bad = false, some_many = false;
+        bool bad = false, some = false, some_many = false;
         for (int s = threadIdx.x; s < p.B; s += kThreads) {
             const Seq q = load_seq(p, s, log2qt, false);
             if (p.rows && q.row >= 0 && q.row < p.n_rows && q.any) {
@@ -418,12 +418,21 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 m[1].x = q.held;
             }
             bad = bad || q.bad;
+            some = some || q.head_cost > 0;
             some_many = some_many || (q.head_cost > 0 && !q.few);
         }
         if (bad && blockIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
         // these words were written through the generic proxy where TMA writes next
         fence_proxy_async();
         n_stages = __syncthreads_or(some_many) ? 3 : kMaxStages;
+        // behind a step of decode rows alone there is nothing left: 1.3 us earlier out
+        if (p.skip_decode && !__syncthreads_or(some)) {
+            if (warp == 17)
+                asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                             "r"(512)
+                             : "memory");
+            return;
+        }
     }
     const int n_stay = n_stages == 3 ? 4 : 2;
 
