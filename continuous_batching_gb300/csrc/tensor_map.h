@@ -40,9 +40,9 @@ inline int32_t make_map(CUtensorMap* m, const void* base, int D, int heads, int6
 }
 
 // An fp8 pool as {D, heads, rows} bytes: one box is one block of one KV head, bs rows of D
-// code bytes, unswizzled (the loader expands it in shared memory).
+// code bytes (the loader expands it in shared memory), swizzled for D = 128 if asked for.
 inline int32_t make_map_codes(CUtensorMap* m, const void* base, int D, int heads, int64_t rows,
-                       int box_rows) {
+                       int box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
     auto fn = encode_fn();
     if (!fn) return PA_ERR_CUDA;
     const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(rows)};
@@ -51,7 +51,7 @@ inline int32_t make_map_codes(CUtensorMap* m, const void* base, int D, int heads
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims,
                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
 }

@@ -296,19 +296,28 @@ __device__ __forceinline__ void add16(const uint32_t* lo, const uint32_t* hi, fl
     }
 }
 
-// A K slot's code rows r0 .. r0 + 15 expanded to f16 by one warp, like expand_codes but with all of
-// them read before any is written, so that the reads' latency is paid once. Rows behind the tile's
-// keys hold nothing that counts; their (stale) codes are turned as well.
+// A K slot's code rows r0 .. r0 + 15 (128-byte swizzled, like what they become) expanded to f16 by one
+// warp, all of them read before any is written, so that the reads' latency is paid once. Eight lanes
+// take one half of the code rows x and x ^ 5 of a swizzle's eight: their reads, and each of their
+// two writes, so meet all the banks once (a row of codes to eight lanes met half of them twice when it
+// was written). Rows behind the tile's keys hold nothing that counts; their (stale) codes are turned
+// as well.
 __device__ __forceinline__ void expand_rows(uint32_t slot, int r0, int lane) {
-    const uint32_t c = lane & 7, j0 = 2 * (c & 3), hi = c >> 2;
+    const uint32_t cc = lane & 3, hi = (lane >> 3) & 1, j0 = 2 * cc;
+    const auto row = [&](int i) {                        // pair 2 i + lane / 16
+        const uint32_t pair = 2 * i + (lane >> 4), x = pair & 3;
+        return uint32_t(r0) + 8 * (pair >> 2) + (lane & 4 ? x ^ 5 : x);
+    };
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v[i] = ld_shared_v4(slot + kHalf + uint32_t(r0 + 4 * i + (lane >> 3)) * 128 + c * 16);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t R = row(i);
+        v[i] = ld_shared_v4(slot + kHalf + R * 128 + (((4 * hi + cc) ^ (R & 7)) << 4));
+    }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t R = uint32_t(r0 + 4 * i + (lane >> 3)), x = R & 7;
+        const uint32_t R = row(i), x = R & 7;
         uint32_t f[8];
         e4m3x4_to_f16x4(v[i].x, f[0], f[1]);
         e4m3x4_to_f16x4(v[i].y, f[2], f[3]);
@@ -1189,7 +1198,8 @@ int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
     const int D = s->head_dim, g = s->num_q_heads / s->num_kv_heads;
     const int64_t slots = int64_t(s->num_blocks) * s->block_size;
     CUtensorMap k, q1, qn;
-    st = fp8 ? make_map_codes(&k, k_pool, D, s->num_kv_heads, slots, s->block_size)
+    st = fp8 ? make_map_codes(&k, k_pool, D, s->num_kv_heads, slots, s->block_size,
+                              CU_TENSOR_MAP_SWIZZLE_128B)
              : make_map(&k, k_pool, D, s->num_kv_heads, slots, 1, s->block_size);
     if (st) return st;
     if ((st = make_map(&q1, q, D, s->num_q_heads, T, g, 1))) return st;
