@@ -78,13 +78,16 @@ __device__ __forceinline__ unsigned long long global_ns() {
 }
 
 // Waits for the phase of `bar` with the given parity. Gives up when another role has set
-// the CTA's abort word or after limit_ns; then sets the abort word and returns false.
+// the CTA's abort word or after limit_ns; then sets the abort word and returns false. Between two
+// looks at the abort word and the clock, which leave the other warps' work in peace for a while, it
+// polls POLLS times.
+template <int POLLS = 32>
 __device__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_word,
                              unsigned long long limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
     for (;;) {
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < POLLS; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (*abort_word) return false;
         if (global_ns() - t0 > limit_ns) {
