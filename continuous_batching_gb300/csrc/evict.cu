@@ -199,10 +199,11 @@ __global__ void __launch_bounds__(kThreads, 4) evict_kernel(const EvictParams p)
 
     // ---- the key of rank `len`, and how many of its equals stay
     uint32_t prefix = 0;
-    int need = len, count = ctx;
+    int need = len, count = ctx, shift = 32;
+    // (where all of a bin stay its lower bits need not be looked at: mostly the third pass)
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    for (int pass = 0; pass < 3 && need < count; ++pass) {
+        shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const int bits = pass == 2 ? 10 : 11;
         if (pass > 0)
             for (int j = j0 + tid; j < j1; j += kThreads) {
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 4) evict_kernel(const EvictParams p)
     const bool ties = need < count;
     for (int w = w0 + warp; w < w1; w += kWarps) {
         const int j = 32 * w + lane;
-        const uint32_t k = j < j1 ? key_of(j) : 0u;
+        const uint32_t k = j < j1 ? key_of(j) >> shift : 0u;
         const uint32_t gt = __ballot_sync(0xffffffffu, j < j1 && k > prefix);
         const uint32_t eq = __ballot_sync(0xffffffffu, j < j1 && k == prefix);
         if (lane == 0) {

@@ -137,3 +137,44 @@ def test_prompts_then_tokens_under_a_budget(fp8):
     # tokens behind the budget move, per head: sequence 0 8 (of 64 entries), 6 (of 54), then one in
     # each of 14 steps; sequence 2 one in each of 15
     assert ctx == [budget, 41, budget] and evicted >= Hkv * (8 + 6 + 14 + 15)
+
+
+@pytest.mark.gpu
+def test_offsets_that_pass_32_bits():
+    """Blocks at the end of a pool of more than 2^31 elements, and a state row behind as many: the bits
+    of the same calls at the start of small ones."""
+    Hq, Hkv, D, bs, n, budget, max_len = 16, 8, 128, 128, 300, 130, 1 << 19
+    torch.manual_seed(3)
+    q, k, v = (torch.randn(n, h, D, device="cuda").bfloat16() for h in (Hq, Hkv, Hkv))
+    w = torch.rand(D, device="cuda").bfloat16()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    cu, ctx = np.array([0, n], np.int32), np.array([n], np.int32)
+
+    def run(num_blocks, blocks, n_rows, row):
+        shape = bd.Shape.make(Hq, Hkv, D, bs, num_blocks)
+        kp, vp = (torch.empty(num_blocks, bs, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        weights = torch.empty(n_rows, Hkv, max_len, device="cuda")
+        places = torch.empty(n_rows, Hkv, max_len, dtype=torch.int32, device="cuda")
+        q_out, out, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(n, Hq, device="cuda")
+        table, err = i32(*blocks)[None], i32(0)
+        at = torch.arange(n, dtype=torch.int32, device="cuda")
+        slots = (table[0][(at // bs).long()] * bs + at % bs).int()
+        rope = bd.pa_rope_pairs(1e4 ** (-np.arange(D // 2) / (D // 2)), device="cuda")
+        bd.paged_qk_norm_rope_write(q, k, v, w, w, 1e-6, rope, at, slots, q_out, kp, vp, shape, err=err)
+        items = torch.from_numpy(bd.pa_plan_step(shape, cu, ctx).view(np.int32).reshape(-1)).cuda()
+        ws = torch.empty(bd.pa_step_weights_workspace_bytes(shape, 1, n, n) // 4 + 4, device="cuda")
+        bd.paged_attention_step_weights(q_out, kp, vp, table, i32(0, n), i32(n), n, items, ws, out, lse, i32(row),
+                                        weights, shape, err=err)
+        before = weights[row, :, :n].clone()
+        bd.paged_evict(kp, vp, table, i32(n), i32(budget), i32(n), None, i32(row), 8, 2, weights, weights, places,
+                       places, shape, err=err)
+        assert int(err.item()) == 0
+        rows = table[0].long()
+        return [x.cpu() for x in (q_out, out, lse, before, kp[rows][:, :40], vp[rows][:, :40],
+                                  weights[row, :, :budget], places[row, :, :budget])]
+
+    far_blocks, far_rows = 2 ** 31 // (bs * Hkv * D) + 64, 2 ** 31 // (Hkv * max_len) + 8
+    near = run(8, (7, 0, 5), 1, 0)
+    far = run(far_blocks, (far_blocks - 1, far_blocks - 8, far_blocks - 3), far_rows, far_rows - 1)
+    for a, b in zip(near, far):
+        assert torch.equal(a, b)
