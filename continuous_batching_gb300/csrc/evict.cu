@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, 4) evict_kernel(const EvictParams p)
         const int n = w < words ? __popc(bits_of(w, true)) | __popc(bits_of(w, false)) << 16 : 0;
         return block_scan(n, sh.warp_sum, all) - n;
     };
-    int moves = 0;
-    for (int r = 0; r < words; r += kThreads) {
+    int moves = 0;                                     // as many as there are holes
+    for (int r = 0; 32 * r < len; r += kThreads) {
         int all;
         round_scan(r + tid, all);
         moves += all & 0xffff;
