@@ -11,12 +11,16 @@
 //
 // A cluster of C CTAs takes one (sequence, head): each reads its slice of the weights once (held
 // as ordered 32-bit keys in shared memory; entries before the budget are copied to the output on
-// the way), three radix passes (11, 11, 10 bits) over histograms find the key of rank `budget`,
+// the way), up to three radix passes (11, 11, 10 bits) over histograms find the key of rank `budget`,
 // and two bitmaps (above it, equal to it) give the holes and strays. A pass's non-empty bins are
 // added up in the first CTA's shared memory, which finds the bin and tells the others: tens of
 // bins (pulling whole histograms from each other took 25 us a pass). Nothing depends on the order
 // of atomics: they count. Then the CTAs share the moves. Bound by latency when few rows move (the
 // passes' barriers), by the strays' K and V rows otherwise.
+//
+// Measured (8 KV heads of 128): 64 full caches of 2,049 entries, 10.5 us in a graph; eight prompts of
+// 4,000 .. 40,000 cut to 2,048 (123 MB) 42 us, of a CTA's time on average 5 up to the first histogram, 9
+// in the passes and bitmaps, 6 to list the moves and 10 in them (where memory is at its limit).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -20,6 +20,10 @@
 // (each lane computes its share and gets the rest from its neighbours) and the products of weights
 // and sines serve them from registers and nothing is shared between warps. What it costs beyond
 // memory is instructions: per head, 4 shuffles and some 50 others, the arithmetic in packed pairs.
+//
+// Measured: 16,384 tokens of 32 + 2 x 8 heads of 128 (403 MB) in 75 us, 5.4 TB/s, 79 % of the measured
+// copy rate; replayed in a graph, one token 2.5 us, 128 tokens of 64 + 2 x 8 heads 3.4 us, 2,096
+// tokens into an fp8 pool (47 MB) 14.3 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -270,7 +274,8 @@ template <int D, bool INTER, bool F8>
 int32_t launch_rope(RopeParams& p, cudaStream_t stream) {
     constexpr int kHeads = 256 / D;            // heads a warp has at a time
     // Warps per token: few, so that each has kMaxRounds rounds of heads to its sines, unless there
-    // are too few tokens to fill the GPU with (16 warps an SM); at most one for every round.
+    // are too few tokens to fill the GPU with (16 warps an SM); at most one for every round. 128 and
+    // 2,096 tokens: 3.4 and 14.3 us, with 8 warps an SM 4.6 and 22.5, with 32 3.7 and 17.6.
     const int rounds = (p.Hq + kHeads - 1) / kHeads + 2 * ((p.Hkv + kHeads - 1) / kHeads);
     const int64_t fill = (16 * int64_t(PA_PLAN_CTAS) + p.T - 1) / p.T;
     p.warps = int(std::min<int64_t>(rounds, std::max<int64_t>((rounds + kMaxRounds - 1) / kMaxRounds,
