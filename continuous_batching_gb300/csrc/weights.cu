@@ -666,15 +666,15 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             const int me = warp == 19;           // fills accumulators me and me + 2
             int n = 0, st = 0, ph = 0;           // stream tile, its stage and the stage's parity
             int ks = 0, kph = 0;                 // next slot of what stays and its parity
-            uint32_t out = 0, eph = 0;           // the two accumulators: handed to the epilogue and
-                                                 // not seen back; parity of their next return
+            uint32_t eph = 3;                    // parities of the two accumulators' next return
             bool ok = true;
+            // (the first look in line: mostly the phase is past, and the issuer's own time counts)
+            const auto wait = [&](int b, uint32_t parity) {
+                return mbar_try_wait(bar(b), parity) || await(bar(b), parity, abort_word);
+            };
             const auto take_back = [&](int h) {
-                if (out >> h & 1) {
-                    ok = await(bar(kAccEmpty + me + 2 * h), eph >> h & 1, abort_word);
-                    eph ^= 1u << h;
-                }
-                out |= 1u << h;
+                ok = wait(kAccEmpty + me + 2 * h, eph >> h & 1);
+                eph ^= 1u << h;
                 return ok;
             };
             const uint32_t idesc_full = make_idesc(128, kCols, false, F8);
@@ -696,35 +696,49 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     return make_sdesc(sb + stay_at(first_slot(r), n_stay), 16, 1024);
                 };
                 const uint64_t stay0 = stay(few || I.nt == 1 ? 0 : me), stay1 = stay(few ? 0 : me + 2);
-                const int end = n + (few ? I.nt : I.n_qt - I.qt0);
-                int qt = few ? 0 : stream_first(I.qt0, I.n_qt, I.nt);
                 const int last_cols = (I.n_q - ((I.n_qt - 1) << log2qt)) * p.g;
                 const uint32_t idesc_last = make_idesc(128, (last_cols + 15) & ~15, false, F8);
-                for (; n < end; ++n) {
-                    if (!(ok = await(bar(kStreamUse + st), ph, abort_word))) break;
-                    const uint64_t stage = make_sdesc(sb + stage_at(st), 16, 1024);
-                    if (few) {
+                const auto next_stage = [&]() {
+                    if (++st == n_stages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                };
+                if (few) {
+                    for (const int end = n + I.nt; n < end; ++n) {
+                        if (!(ok = wait(kStreamUse + st, ph))) break;
                         const int acc = n & 3;
                         if ((acc & 1) == me) {
                             if (!take_back(acc >> 1)) break;
                             tc_fence_after();
-                            issue_s_group<D>(1u, tmem + acc * kCols, stage, stay0, idesc_last);
+                            issue_s_group<D>(1u, tmem + acc * kCols,
+                                             make_sdesc(sb + stage_at(st), 16, 1024), stay0,
+                                             idesc_last);
                             tc_commit_if(1u, bar(kAccFull + acc));
                             tc_commit_if(1u, bar(kStreamEmpty + st));
                         } else {
                             mbar_arrive(bar(kStreamEmpty + st));
                         }
-                    } else {
+                        next_stage();
+                    }
+                } else {
+                    const uint64_t stage0 = make_sdesc(sb + stage_at(0), 16, 1024);
+                    const bool two = me + 2 < I.nt;
+                    const int end = n + I.n_qt - I.qt0;
+                    int qt = stream_first(I.qt0, I.n_qt, I.nt);
+                    for (; n < end; ++n) {
+                        // (three stages, side by side)
+                        const uint64_t stage = stage0 + uint32_t(st) * (kSlot / 16);
                         const uint32_t idesc = qt + 1 == I.n_qt ? idesc_last : idesc_full;
-                        const bool mine = I.nt == 1 ? (qt & 1) == me : me < I.nt;
-                        if (mine) {
+                        if (!(ok = wait(kStreamUse + st, ph))) break;
+                        if (I.nt == 1 ? (qt & 1) == me : me < I.nt) {
                             const int h = I.nt == 1 ? qt >> 1 & 1 : I.nt == 2 ? qt & 1 : 0;
                             if (!take_back(h)) break;
                             tc_fence_after();
                             issue_s_group<D>(1u, tmem + (me + 2 * h) * kCols, stay0, stage, idesc);
                             tc_commit_if(1u, bar(kAccFull + me + 2 * h));
                         }
-                        if (me + 2 < I.nt) {
+                        if (two) {
                             // (the first tile's slot is not needed any more once the last query
                             // tile's product is in the pipe)
                             if (n + 1 == end) tc_commit_if(1u, bar(kStayEmpty + first_slot(me)));
@@ -735,10 +749,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                         }
                         tc_commit_if(1u, bar(kStreamEmpty + st));
                         if (n + 1 < end) qt = stream_next(qt, I.qt0, I.n_qt, I.nt);
-                    }
-                    if (++st == n_stages) {
-                        st = 0;
-                        ph ^= 1;
+                        next_stage();
                     }
                 }
                 if (!ok) break;
