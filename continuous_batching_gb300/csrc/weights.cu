@@ -38,16 +38,16 @@
 // summed in four classes (qt % 4), and these are added to the old sum in the order 0, 2, 1, 3.
 // Issuer i fills accumulators i and i + 2: its waits, commits and address arithmetic, made slow by the
 // warps it shares its scheduler with, run while the other's MMAs keep the tensor pipe busy (strict
-// turns of the two, 0, 1, 2, 3, were slower: 92 us against 87 for the chunks below).
+// turns of the two, 0, 1, 2, 3, were slower: 92 us where the chunks below then took 87).
 // Shared memory: seven 32 KB slots. Four in a ring for what stays (the next item's tiles load as this
 // one's are done with) and three stages for what streams; where no sequence is MANY, two for what
 // stays and five stages (five tiles of K in flight). Every wait is bounded.
 //
 // Measured (8 KV heads of 128, group 4): 64 decode rows at 2k .. 16k keys 93 us, 5.6 TB/s, 82 % of the
 // measured copy rate; one at 16,001 keys 11.7 us (some 7 of them up to the first tile: launch,
-// metadata, deal, first loads); four chunks of 512 rows at up to 9,512 keys 87 us, 995 TFLOP/s, 52 % of the
-// measured matrix rate; 32 decode rows at up to 40,000 keys over an fp8 cache (group 8) 51 us, 4.0
-// TB/s, 59 % (its 16 KB tiles leave half the bytes in flight; with no expansion at all it took 46.6).
+// metadata, deal, first loads); four chunks of 512 rows at up to 9,512 keys 84 us, 1.03 PFLOP/s, 54 %
+// of the measured matrix rate; 32 decode rows at up to 40,000 keys over an fp8 cache (group 8) 50 us, 4.05
+// TB/s, 60 % (its 16 KB tiles leave half the bytes in flight; with no expansion at all it took 46.6).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
