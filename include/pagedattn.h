@@ -504,8 +504,9 @@ int32_t pa_rope_pairs(const double* inv_freq, const int32_t* axes, int32_t n_pai
  * Device: q [T, Hq, D], k, v [T, Hkv, D] bf16, each with its own stride in elements between tokens
  * (heads and columns dense), so the three may be parts of one projection; q_weight, k_weight [D]
  * bf16 or NULL; rope [n_pairs]; positions [n_axes, T] int32; slot_mapping [T]; q_out [T, Hq, D]
- * dense (q itself if that is dense, else no overlap with q, k or v). Tokens with the same slot >= 0
- * leave one of them there. An axis outside [0, n_axes) turns by axis 0 and sets PA_DEVERR_META.
+ * dense (q itself if that is dense, else no overlap with q, k or v). A slot >= 0 belongs to one
+ * token: named by two it is left with a mixture of theirs. An axis outside [0, n_axes) turns by axis
+ * 0 and sets PA_DEVERR_META.
  * Host checks: n_pairs a multiple of 4, at most D / 2, or 0 for no rotation (PA_ERR_SHAPE; rope and
  * positions may then be NULL); eps finite and >= 0; pointers 16-byte aligned, strides multiples of
  * 8 elements and at least a token long. Launched as a programmatic dependent of what precedes it on
@@ -593,8 +594,9 @@ int32_t paged_attention_step_fp8_lse(const void* q, const void* k_pool, const vo
  * step must be covered by items (a plan of pa_plan_step or pa_plan_step_shared covers them).
  * workspace: at least pa_step_weights_workspace_bytes(shape, B, T, max_ctx) bytes, 16-byte aligned,
  * always needed; it holds B * Hq * max_ctx scores beside the split partials, and nothing between
- * calls. max_ctx >= every ctx_lens[s] (a longer decode sequence adds nothing and sets
- * PA_DEVERR_META). Other arguments, state and errors as in the two. */
+ * calls (calls or graphs that may overlap need one each). max_ctx >= every ctx_lens[s] (a longer
+ * decode sequence adds nothing and sets PA_DEVERR_META). Other arguments, state and errors as in
+ * the two. */
 size_t pa_step_weights_workspace_bytes(const pa_shape* shape, int32_t B, int32_t T,
                                        int32_t max_ctx);
 int32_t paged_attention_step_weights(const void* q, const void* k_pool, const void* v_pool,
