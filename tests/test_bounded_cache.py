@@ -178,3 +178,88 @@ def test_offsets_that_pass_32_bits():
     far = run(far_blocks, (far_blocks - 1, far_blocks - 8, far_blocks - 3), far_rows, far_rows - 1)
     for a, b in zip(near, far):
         assert torch.equal(a, b)
+
+
+class _Cache:
+    """Four sequences with their pools, state and buffers; run queues a step and an eviction."""
+    Hq, Hkv, D, bs, nb, max_len = 16, 8, 128, 16, 600, 4000
+    ctx, n_q = np.array([3001, 1700, 40, 3333], np.int32), np.array([1, 300, 40, 1], np.int32)
+    shape = bd.Shape.make(Hq, Hkv, D, bs, nb)
+
+    def __init__(self, seed):
+        torch.manual_seed(seed)
+        B, cu = len(self.ctx), np.concatenate([[0], np.cumsum(self.n_q)]).astype(np.int32)
+        T, self.longest = int(cu[-1]), int(self.ctx.max())
+        i32 = lambda x: torch.as_tensor(np.asarray(x, np.int32)).cuda()
+        half = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+        self.q, self.k, self.v = half(T, self.Hq, self.D), half(T, self.Hkv, self.D), half(T, self.Hkv, self.D)
+        blocks, table, slots = torch.randperm(self.nb).numpy(), np.zeros((B, -(-self.longest // self.bs)), np.int32), []
+        for s, c in enumerate(self.ctx):
+            n = -(-int(c) // self.bs)
+            table[s, :n], blocks = blocks[:n], blocks[n:]
+            new = np.arange(c - self.n_q[s], c)
+            slots.append(table[s, new // self.bs] * self.bs + new % self.bs)
+        self.table, self.slots, self.cu = i32(table), i32(np.concatenate(slots)), i32(cu)
+        self.pos = i32(np.concatenate([np.arange(c - n, c) for c, n in zip(self.ctx, self.n_q)]))
+        self.ctx_d, self.rows, self.budget, self.err = i32(self.ctx), i32([2, 0, 3, 1]), i32([1500] * B), i32([0])
+        self.rope = bd.pa_rope_pairs(1e4 ** (-np.arange(self.D // 2) / (self.D // 2)), device="cuda")
+        self.items = torch.from_numpy(bd.pa_plan_step(self.shape, cu, self.ctx).view(np.int32).reshape(-1)).cuda()
+        need = bd.pa_step_weights_workspace_bytes(self.shape, B, T, self.longest)
+        self.ws = torch.empty(need // 4 + 4, device="cuda")
+        pool, state = (self.nb, self.bs, self.Hkv, self.D), (B, self.Hkv, self.max_len)
+        self.first = [half(*pool), half(*pool), torch.rand(*state, device="cuda"),
+                      torch.zeros(state, dtype=torch.int32, device="cuda"), torch.zeros_like(self.q),
+                      torch.zeros_like(self.q), torch.zeros(T, self.Hq, device="cuda")]
+        self.now = [x.clone() for x in self.first]
+
+    def reset(self):
+        for x, y in zip(self.now, self.first):
+            x.copy_(y)
+
+    def run(self, stream=None):
+        kp, vp, weights, places, q_out, out, lse = self.now
+        bd.paged_qk_norm_rope_write(self.q, self.k, self.v, None, None, 1e-6, self.rope, self.pos, self.slots, q_out,
+                                    kp, vp, self.shape, err=self.err, stream=stream)
+        bd.paged_attention_step_weights(q_out, kp, vp, self.table, self.cu, self.ctx_d, self.longest, self.items,
+                                        self.ws, out, lse, self.rows, weights, self.shape, err=self.err, stream=stream)
+        bd.paged_evict(kp, vp, self.table, self.ctx_d, self.budget, self.ctx_d, None, self.rows, 16, 2, weights,
+                       weights, places, places, self.shape, err=self.err, stream=stream)
+
+
+@pytest.mark.gpu
+def test_two_caches_at_once():
+    """Calls of two caches queued in turn on two streams, by themselves and as replayed graphs: the bits
+    of each cache alone."""
+    caches, streams = [_Cache(1), _Cache(2)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = []
+    for c in caches:
+        c.run()
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in c.now])
+
+    def check():
+        torch.cuda.synchronize()
+        for c, w in zip(caches, want):
+            assert int(c.err.item()) == 0
+            for x, y in zip(c.now, w):
+                assert torch.equal(x, y)
+            c.reset()
+        torch.cuda.synchronize()
+
+    for c in caches:
+        c.reset()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for c, s in zip(caches, streams):
+            c.run(s)
+        check()
+    graphs = []
+    for c, s in zip(caches, streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            c.run()
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        check()
