@@ -144,6 +144,7 @@ struct Params {
     int32_t B, T, max_blocks, Hq, Hkv, g, bs, num_blocks, n_rows, max_len;
     int32_t heads;               // CTAs of a group: neighbouring KV heads
     int32_t skip_decode;         // sequences of one row are another kernel's
+    int32_t max_ctx;             // a step's bound: rows of longer contexts may have no lse
     float c;                     // log2(e) / sqrt(D), times the K scale of an fp8 cache
 };
 
@@ -257,7 +258,7 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt, bool
     q.n_q = int(n);
     q.cu0 = c0;
     q.held = p.held ? p.held[s] : q.ctx - q.n_q;
-    if (n < 0 || c0 < 0 || c1 > p.T || q.n_q > q.ctx || q.ctx > p.max_len ||
+    if (n < 0 || c0 < 0 || c1 > p.T || q.n_q > q.ctx || q.ctx > min(p.max_len, p.max_ctx) ||
         (int64_t(q.ctx) + p.bs - 1) / p.bs > p.max_blocks || q.row >= p.n_rows || q.held < 0 ||
         q.held > q.ctx || (repeated && shares_row(p.rows, p.cu, p.B, s))) {
         q.bad = true;
@@ -1155,7 +1156,7 @@ __host__ __device__ int64_t scores_row(int32_t max_ctx) {
 // four tiles at a time) 265 to 271.
 constexpr int kDecodeKeys = 1024;      // per block of 256 threads
 __global__ void __launch_bounds__(256)
-    decode_weights_kernel(const float* __restrict__ scores, int32_t max_ctx, const Params p) {
+    decode_weights_kernel(const float* __restrict__ scores, const Params p) {
     __shared__ float nl[16];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1165,7 +1166,7 @@ __global__ void __launch_bounds__(256)
     const int j0 = int(blockIdx.x) * kDecodeKeys;
     if (p.cu[s + 1] - c0 != 1 || row < 0 || (j0 >= ctx && j0 > 0)) return;
     const int held = p.held ? p.held[s] : ctx - 1;
-    bool bad = c0 < 0 || c0 >= p.T || ctx < 1 || ctx > p.max_len || ctx > max_ctx ||
+    bool bad = c0 < 0 || c0 >= p.T || ctx < 1 || ctx > p.max_len || ctx > p.max_ctx ||
                (int64_t(ctx) + p.bs - 1) / p.bs > p.max_blocks || row >= p.n_rows || held < 0 ||
                held > ctx;
     if (p.rows)
@@ -1182,7 +1183,7 @@ __global__ void __launch_bounds__(256)
     const int j = j0 + 4 * int(threadIdx.x);
     if (j >= ctx) return;
     // a row of scores is a whole number of tiles: a thread's four lie within it
-    const int64_t scores_ld = scores_row(max_ctx);
+    const int64_t scores_ld = scores_row(p.max_ctx);
     const float* sc = scores + (int64_t(s) * p.Hq + h * p.g) * scores_ld + j;
     float* w = p.weights + (int64_t(row) * p.Hkv + h) * p.max_len + j;
     float sum[4];
@@ -1210,7 +1211,7 @@ int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
                           const int32_t* rows, float* weights, int32_t n_rows, int32_t max_len,
                           bool fp8, float k_scale, const pa_shape* s, int32_t* err,
                           cudaStream_t stream, const float* scores = nullptr,
-                          int32_t max_ctx = 0) {
+                          int32_t max_ctx = INT32_MAX) {
     int32_t st = check_shape(s);
     if (st) return st;
     if (fp8 && s->head_dim != 128) return PA_ERR_SHAPE;
@@ -1256,6 +1257,7 @@ int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
     p.max_len = max_len;
     p.c = float(1.4426950408889634 / std::sqrt(double(D))) * k_scale;
     p.skip_decode = scores != nullptr;
+    p.max_ctx = max_ctx;
     if (scores) {
         cudaLaunchAttribute pdl[1];
         pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1267,8 +1269,7 @@ int32_t attention_weights(const void* q, const void* k_pool, const float* lse,
         cfg.stream = stream;
         cfg.attrs = pdl;
         cfg.numAttrs = 1;
-        if ((st = note_cuda(cudaLaunchKernelEx(&cfg, decode_weights_kernel, scores,
-                                               max_ctx, p))))
+        if ((st = note_cuda(cudaLaunchKernelEx(&cfg, decode_weights_kernel, scores, p))))
             return st;
     }
     if (fp8) return launch_weights<128, true>(k, q1, qn, p, stream);

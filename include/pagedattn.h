@@ -595,8 +595,8 @@ int32_t paged_attention_step_fp8_lse(const void* q, const void* k_pool, const vo
  * workspace: at least pa_step_weights_workspace_bytes(shape, B, T, max_ctx) bytes, 16-byte aligned,
  * always needed; it holds B * Hq * max_ctx scores beside the split partials, and nothing between
  * calls (calls or graphs that may overlap need one each). max_ctx >= every ctx_lens[s] (a longer
- * decode sequence adds nothing and sets PA_DEVERR_META). Other arguments, state and errors as in
- * the two. */
+ * sequence, decode row or chunk, gives no weight and sets PA_DEVERR_META: its state stays as it
+ * was). Other arguments, state and errors as in the two. */
 size_t pa_step_weights_workspace_bytes(const pa_shape* shape, int32_t B, int32_t T,
                                        int32_t max_ctx);
 int32_t paged_attention_step_weights(const void* q, const void* k_pool, const void* v_pool,

@@ -465,3 +465,35 @@ def test_step_refusals_and_contexts_behind_the_bound():
     assert run(max_len=100) == ([True, False, True], bd.PA_DEVERR_META)
     assert run(rows=(0, 2, 2)) == ([True, False, False], bd.PA_DEVERR_META)
     assert run(rows=(0, -1, 2)) == ([True, False, True], 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ctx, max_ctx", [(2200, 2048), (2200, 2199), (400, 399)])
+def test_step_chunk_behind_the_bound_takes_no_part(ctx, max_ctx, fp8):
+    """A chunk longer than max_ctx: rows that reach a split behind the bound are refused by the step and
+    have no log-sum-exp (here NaN is left in the buffer). Its state row stays as it was."""
+    st = wl.make_step(8, 2, 128, 16, [40, ctx, 60], [1, 300, 20], seed=8)
+    shape = bd.Shape.make(st.Hq, st.Hkv, st.D, st.block_size, st.num_blocks)
+    scales, s8 = ((0.0125, 0.02), "_fp8") if fp8 else ((), "")
+    pools = [dev(ofp8.quantize(x, s)) for x, s in zip((st.k_pool, st.v_pool), scales)] if fp8 else \
+        [dev(x.view(np.int16), torch.bfloat16) for x in (st.k_pool, st.v_pool)]
+    q, table, cu, lens = dev(st.q.view(np.int16), torch.bfloat16), dev(st.block_table), dev(st.cu_seqlens_q), dev(st.ctx_lens)
+    items = dev(bd.pa_plan_step(shape, st.cu_seqlens_q, st.ctx_lens).view(np.int32).reshape(-1))
+    step = getattr(bd, "paged_attention_step_weights" + s8)
+
+    def run(bound):
+        ws = torch.empty((bd.pa_step_weights_workspace_bytes(shape, 3, st.T, bound) + 3) // 4, device="cuda")
+        out = torch.empty(st.T, st.Hq, st.D, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((st.T, st.Hq), float("nan"), device="cuda")
+        w = torch.full((3, st.Hkv, ctx + 9), 0.25, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        step(q, *pools, table, cu, lens, bound, items, *scales, ws, out, lse, None, w, shape, err=err)
+        return w, int(err.item())
+
+    want, err = run(ctx)
+    assert err == 0 and bool((want[1] != 0.25).any()) and bool(torch.isfinite(want).all())
+    got, err = run(max_ctx)
+    assert err == bd.PA_DEVERR_META
+    assert bool((got[1] == 0.25).all())
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
