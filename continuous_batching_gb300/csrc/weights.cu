@@ -1186,9 +1186,13 @@ __global__ void __launch_bounds__(256)
     const int64_t scores_ld = scores_row(p.max_ctx);
     const float* sc = scores + (int64_t(s) * p.Hq + h * p.g) * scores_ld + j;
     float* w = p.weights + (int64_t(row) * p.Hkv + h) * p.max_len + j;
-    float sum[4];
+    // the old sum joins once, rounded once: a head's weight may be below half a step of it
+    float old[4], sum[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = j + e < held ? w[e] : 0.f;
+    for (int e = 0; e < 4; ++e) {
+        old[e] = j + e < held ? w[e] : 0.f;
+        sum[e] = 0.f;
+    }
     for (int i = 0; i < p.g; ++i) {
         const float4 x = __ldcs(reinterpret_cast<const float4*>(sc + int64_t(i) * scores_ld));
         sum[0] += ex2(fmaf(x.x, p.c, nl[i]));
@@ -1198,7 +1202,7 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (j + e < ctx) w[e] = sum[e];
+        if (j + e < ctx) w[e] = old[e] + sum[e];
 }
 
 size_t partials_bytes(const pa_shape* s, int32_t T, int32_t max_ctx) {

@@ -497,3 +497,49 @@ def test_step_chunk_behind_the_bound_takes_no_part(ctx, max_ctx, fp8):
     assert err == bd.PA_DEVERR_META
     assert bool((got[1] == 0.25).all())
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+
+
+# A state much larger than what a step adds: the bound is one rounding of the total (half a step,
+# 2^-24 of it at most) on top of the increment's own tolerance. The starting states are such that a
+# part of the increment (a head's weight) is below half a step of theirs.
+def _large_state(st, start, step, fp8=False):
+    shape = bd.Shape.make(st.Hq, st.Hkv, st.D, st.block_size, st.num_blocks)
+    q = pa.bf16_to_f64(st.q)
+    scales, s8 = ((0.0125, 0.02), "_fp8") if fp8 else ((), "")
+    if fp8:
+        k = ofp8.dequantize(ofp8.quantize(st.k_pool, scales[0]), scales[0])
+        kp, vp = (dev(ofp8.quantize(x, s)) for x, s in zip((st.k_pool, st.v_pool), scales))
+    else:
+        k = pa.bf16_to_f64(st.k_pool)
+        kp, vp = (dev(x.view(np.int16), torch.bfloat16) for x in (st.k_pool, st.v_pool))
+    lse64, want = lse_and_weights(q, k, st.block_table, st.cu_seqlens_q, st.ctx_lens)
+    B, max_ctx = len(st.ctx_lens), int(st.ctx_lens.max())
+    state = (start * (1 + np.random.default_rng(1).random((B, st.Hkv, max_ctx)))).astype(np.float32)
+    w, held, err = dev(state.copy()), dev(st.ctx_lens), torch.zeros(1, dtype=torch.int32, device="cuda")
+    qd, table, cu, ctx = dev(st.q.view(np.int16), torch.bfloat16), dev(st.block_table), dev(st.cu_seqlens_q), dev(st.ctx_lens)
+    if step:
+        items = dev(bd.pa_plan_step(shape, st.cu_seqlens_q, st.ctx_lens).view(np.int32).reshape(-1))
+        ws = torch.empty((bd.pa_step_weights_workspace_bytes(shape, B, st.T, max_ctx) + 3) // 4, device="cuda")
+        out = torch.empty(st.T, st.Hq, st.D, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(st.T, st.Hq, device="cuda")
+        getattr(bd, "paged_attention_step_weights" + s8)(qd, kp, vp, table, cu, ctx, max_ctx, items, *scales, ws, out,
+                                                         lse, None, w, shape, held=held, err=err)
+    else:
+        getattr(bd, "paged_attention_weights" + s8)(qd, kp, dev(lse64.astype(np.float32)), table, cu, ctx, None, w,
+                                                    *scales[:1], shape, held=held, err=err)
+    got = w.cpu().numpy()
+    assert int(err.item()) == 0
+    tol = 3 * (tolerance(q, k, st.D, lse64, st.T * st.Hq // st.Hkv) + 16 * 2.0 ** -24)
+    for s in range(B):
+        c = int(st.ctx_lens[s])
+        total = state[s, :, :c].astype(np.float64) + want[s]
+        d = np.abs(got[s, :, :c] - total)
+        assert np.all(d <= tol * want[s] + 2.0 ** -24 * total), (s, float((d / (2.0 ** -24 * total)).max()))
+        assert np.array_equal(got[s, :, c:], state[s, :, c:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("step", [True, False])
+@pytest.mark.parametrize("Hq, Hkv, D, fp8", [(16, 1, 128, False), (16, 2, 64, False), (32, 2, 128, True)])
+def test_decode_rows_into_a_large_state_round_once(Hq, Hkv, D, fp8, step):
+    _large_state(wl.make_step(Hq, Hkv, D, 16, [300, 2100, 129], [1, 1, 1], seed=3), 1e5, step, fp8)
