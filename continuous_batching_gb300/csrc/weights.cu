@@ -35,7 +35,8 @@
 // turn, a MANY item's key tile r has accumulator r; with two key tiles the query tiles alternate
 // between accumulators r and r + 2, with one they take all four in turn, and the sums meet in memory
 // at the item's end. A key's sum is the same whichever way its tile came to be taken: query tiles are
-// summed in four classes (qt % 4), and these are added to the old sum in the order 0, 2, 1, 3.
+// summed in four classes (qt % 4), these are added up in the order 0, 2, 1, 3, and the old sum joins
+// last, in one rounding (a class may be below half a step of a large old sum).
 // Issuer i fills accumulators i and i + 2: its waits, commits and address arithmetic, made slow by the
 // warps it shares its scheduler with, run while the other's MMAs keep the tensor pipe busy (strict
 // turns of the two, 0, 1, 2, 3, were slower: 92 us where the chunks below then took 87).
@@ -102,13 +103,13 @@ enum Bar {
     kItemFull = 34,    // + slot (4)
     kItemEmpty = 38,   // + slot: every consumer warp
     kPartDone = 42,    // + key tile of two: 4 arrivals, warpgroup r -> r + 2
-    kPartSeen = 44,    // + key tile of two: 4 arrivals, warpgroup r + 2 -> r
+    kPartSeen = 44,    // + key tile of two: 4 arrivals, r + 2 -> r: it has read the old sum
     kChainDone = 46,   // + place, one key tile: 4 arrivals, a warpgroup -> the next
-    kChainSeen = 49,   // + place, one key tile: 4 arrivals, and back
-    kDrain = 52,       // + issuer
-    kStayReady = 54,   // + slot, fp8 only: the f16 warps
-    kStreamReady = 58, // + stage
-    kNumBars = 63
+    kChainSeen = 49,   // one key tile: 4 arrivals, the last -> the first: it has read the old sum
+    kDrain = 50,       // + issuer
+    kStayReady = 52,   // + slot, fp8 only: the f16 warps
+    kStreamReady = 56, // + stage
+    kNumBars = 61
 };
 constexpr int kHolderOff = 8 * kNumBars;
 constexpr int kAbortOff = kHolderOff + 4;
@@ -1034,11 +1035,17 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             const bool my = r < I.nt;
             const int kb = (I.t0 + r) * kTileKeys, j = kb + key_in_tile, kw = kb + 32 * (warp & 3);
             float* dst = p.weights + I.state + j;
-            // the one that has class 0 begins with the old sum; the classes are added in the order
-            // 0, 2, 1, 3, those of another warpgroup once they are there (at most two: kept apart)
-            const bool opens = mod == 0 || turn == 0;
-            const float old = my && opens && j < I.held ? *dst : 0.f;
-            float sum = old, later = 0.f;
+            // the warpgroups' order: 0, 2, 1, 3 with one key tile, r, r + 2 with two
+            const int place = mod == 0 ? 0 : mod == 1 ? w >> 1 : w == 0 ? 0 : w == 2 ? 1 : w == 1 ? 2 : 3;
+            const int hops = mod == 0 ? 0 : mod == 1 ? 1 : 3;
+            // the one that has class 0 begins; the classes are added in the order 0, 2, 1, 3, those of
+            // another warpgroup once they are there (at most two: kept apart). The last one adds the
+            // old sum: it reads it here, before the first may write the entry
+            const bool opens = place == 0, ends = place == hops;
+            const float old = my && ends && j < I.held ? *dst : 0.f;
+            const int seen = bar(mod == 1 ? kPartSeen + r : kChainSeen);
+            if (mod != 0 && ends) warp_arrive(seen);
+            float sum = 0.f, later = 0.f;
             int qt = stream_first(I.qt0, I.n_qt, I.nt), now = -1;
             const auto close = [&]() {                   // the class that was being summed
                 const float s = total_of_key();
@@ -1071,28 +1078,24 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             if (!my) continue;
             if (now >= 0) close();
             if (mod == 0) {
-                if (j < I.ctx) *dst = sum;
+                if (j < I.ctx) *dst = old + sum;
                 continue;
             }
-            // the warpgroups' order: 0, 2, 1, 3 with one key tile, r, r + 2 with two
-            const int place = mod == 1 ? w >> 1 : w == 0 ? 0 : w == 2 ? 1 : w == 1 ? 2 : 3;
-            const int hops = mod == 1 ? 1 : 3, of = mod == 1 ? r : place;
             int& n_hops = mod == 1 ? n_part : n_chain;
-            const int done = mod == 1 ? kPartDone : kChainDone, seen = mod == 1 ? kPartSeen : kChainSeen;
+            // from place to place; the next item's first hand-over waits for the last one's look at
+            // its entries, and so for the end of this item's
+            const int done = bar(mod == 1 ? kPartDone + r : kChainDone + place);
             if (opens) {
+                if (!(ok = await(seen, n_hops & 1, abort_word))) break;
                 if (j < I.ctx) *dst = sum;
             } else {
-                const int from = mod == 1 ? of : of - 1;
-                if (!(ok = await(bar(done + from), n_hops & 1, abort_word))) break;
-                warp_arrive(bar(seen + from));
-                if (j < I.ctx) *dst = (*dst + sum) + later;
+                if (!(ok = await(mod == 1 ? done : done - 8, n_hops & 1, abort_word))) break;
+                if (j < I.ctx) {
+                    const float all = (*dst + sum) + later;
+                    *dst = ends ? old + all : all;
+                }
             }
-            if (place < hops) {
-                if (n_hops > 0 &&
-                    !(ok = await(bar(seen + of), (n_hops - 1) & 1, abort_word)))
-                    break;
-                warp_arrive(bar(done + of));
-            }
+            if (!ends) warp_arrive(done);
             ++n_hops;
         }
     }

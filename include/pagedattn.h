@@ -544,7 +544,8 @@ int32_t paged_qk_norm_rope_write_fp8(const void* q, int64_t q_stride, const void
  * entries (NULL: ctx - n_q, the entries that steps before this one have seen) are added to; those
  * from held[s] to ctx are set, whatever they held; the others are left as they were.
  * Sums are fp32, one writer per entry, in an order that depends on the sequence's own n_q and ctx
- * alone: its bits do not depend on what else is in the batch.
+ * alone: its bits do not depend on what else is in the batch. A call's weights are added up first;
+ * an entry's old sum joins them last, in one rounding.
  * Device inputs: q [T, Hq, D] bf16; k_pool as in paged_attention_step; lse [T, Hq] fp32;
  * block_table [B, max_blocks], cu_seqlens_q [B+1], ctx_lens [B], held [B] or NULL, rows [B] or
  * NULL int32. A sequence whose metadata does not fit (n_q > ctx, ctx > max_len or the table, held

@@ -543,3 +543,18 @@ def _large_state(st, start, step, fp8=False):
 @pytest.mark.parametrize("Hq, Hkv, D, fp8", [(16, 1, 128, False), (16, 2, 64, False), (32, 2, 128, True)])
 def test_decode_rows_into_a_large_state_round_once(Hq, Hkv, D, fp8, step):
     _large_state(wl.make_step(Hq, Hkv, D, 16, [300, 2100, 129], [1, 1, 1], seed=3), 1e5, step, fp8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("step", [True, False])
+@pytest.mark.parametrize("seqs", [1, 5, 14])
+def test_chunks_into_a_large_state_round_once(seqs, step):
+    """Four query tiles to a chunk, its key tiles dealt one, two and up to four to an item: the step's
+    weights are added up before the old sum joins them."""
+    ctx = [1000 - 37 * s for s in range(seqs)]
+    _large_state(wl.make_step(64, 8, 64, 16, ctx, [60] * seqs, seed=seqs), 5e6, step)
+
+
+@pytest.mark.gpu
+def test_fp8_chunks_into_a_large_state_round_once():
+    _large_state(wl.make_step(64, 8, 128, 16, [1000, 700, 300], [60, 100, 17], seed=2), 5e6, True, fp8=True)
