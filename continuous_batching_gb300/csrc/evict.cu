@@ -365,10 +365,15 @@ __global__ void __launch_bounds__(kThreads, 4) evict_kernel(const EvictParams p)
         for (int e = tid; e < end - first; e += kThreads) {
             const int to = sh.hole[e], from = sh.stray[e];
             const int dst = slot_of(to), src = slot_of(from);
-            w_out[to] = w_in[from];
-            pos_out[to] = position(from);
-            if ((dst < 0 || src < 0) && p.err) atomicOr(p.err, PA_DEVERR_BLOCK);
-            sh.hole[e] = src < 0 ? -1 : dst;           // the lists hold slots from here on
+            const bool inside = dst >= 0 && src >= 0;
+            if (inside) {
+                w_out[to] = w_in[from];
+                pos_out[to] = position(from);
+            } else if (p.err) {
+                // the hole keeps its own entry whole: weight and position are in the output already
+                atomicOr(p.err, PA_DEVERR_BLOCK);
+            }
+            sh.hole[e] = inside ? dst : -1;            // the lists hold slots from here on
             sh.stray[e] = src;
         }
         __syncthreads();

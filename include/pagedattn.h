@@ -643,8 +643,9 @@ int32_t paged_attention_step_weights_fp8(const void* q, const void* k_pool, cons
  * Device: k_pool, v_pool of elem_bytes 2 (bf16) or 1 (fp8 codes); block_table, ctx_lens, budget,
  * n_tokens, kept, rows int32 per sequence. A sequence whose metadata does not fit (budget < 1,
  * ctx > n_tokens, max_len or the table, kept > ctx, a row >= n_rows or named by two sequences) is
- * skipped and sets PA_DEVERR_META; rows[s] < 0 takes no part; a row of a block outside the pool is
- * not moved and sets PA_DEVERR_BLOCK. The first min(ctx, budget) entries are written: blocks that
+ * skipped and sets PA_DEVERR_META; rows[s] < 0 takes no part; where either end of a move lies in a
+ * block outside the pool, nothing of it moves (the place keeps its own entry, K, V, weight and
+ * position) and PA_DEVERR_BLOCK is set. The first min(ctx, budget) entries are written: blocks that
  * hold them and are shared have to be made private first (pa_alloc_slots over them answers
  * PA_ERR_READONLY if there are any, pa_alloc_cow replaces them), and no two sequences of a call may
  * share one.

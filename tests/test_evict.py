@@ -238,3 +238,53 @@ def test_binding_refusals_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(state(), want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("ctx, budget, max_len", [(60, 20, 64), (3000, 1000, 3000)])
+def test_an_entry_that_cannot_move_leaves_the_hole_its_own(ctx, budget, max_len, in_place):
+    """Blocks outside the pool among the strays' and among the holes': K, V, weight and position of such a
+    move stay together, in both places."""
+    rng = np.random.default_rng(ctx)
+    bs, Hkv, D = 16, 2, 64
+    n = -(-ctx // bs)
+    shape = bd.Shape.make(Hkv, Hkv, D, bs, n)
+    table = rng.permutation(n).astype(np.int32)[None]
+    bad = [0, n - 2, n // 2] if n > 10 else [0, n - 2]
+    table[0, bad] = [n, -1, n + 5][:len(bad)]
+    flat = [rng.integers(0, 120, (n * bs, Hkv, D)).astype(np.int16) for _ in "kv"]
+    w = rng.lognormal(0, 2, (1, Hkv, max_len)).astype(np.float32)
+    kept, n_tokens = ctx // 3, 2 * ctx
+    pos = np.stack([[rng.permutation(n_tokens - ctx)[:max_len] if n_tokens - ctx >= max_len else
+                     rng.permutation(max_len) for _ in range(Hkv)]]).astype(np.int32)
+    d = lambda a: torch.from_numpy(a.copy()).cuda()
+    kp, vp = (d(x.reshape(n, bs, Hkv, D)).view(torch.bfloat16) for x in flat)
+    wi, pi = d(w), d(pos)
+    wo, po = (wi, pi) if in_place else (torch.full_like(wi, -5), torch.full_like(pi, -5))
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    err = i(0)
+    bd.paged_evict(kp, vp, d(table), i(ctx), i(budget), i(n_tokens), i(kept), None, 4, 1, wi, wo, pi, po, shape, err=err)
+    assert int(err.item()) == bd.PA_DEVERR_BLOCK
+    got_w, got_p = wo.cpu().numpy()[0], po.cpu().numpy()[0]
+    got = [x.view(torch.int16).cpu().numpy().reshape(n * bs, Hkv, D) for x in (kp, vp)]
+    want = [x.copy() for x in flat]
+    slot = [int(table[0, j // bs]) * bs + j % bs if 0 <= table[0, j // bs] < n else -1 for j in range(ctx)]
+    stayed = 0
+    for h in range(Hkv):
+        j = np.arange(ctx)
+        p = np.where(j < kept, pos[0, h, :ctx], n_tokens - ctx + j)
+        src = evict(w[0, h, :ctx].astype(np.float64), p, n_tokens, budget, 4, 1)
+        for to, f in enumerate(src):
+            if f == to:
+                continue
+            if slot[f] < 0 or slot[to] < 0:
+                src[to] = to
+                stayed += 1
+            else:
+                for a, b in zip(want, flat):
+                    a[slot[to], h] = b[slot[f], h]
+        np.testing.assert_array_equal(got_w[h, :budget], w[0, h, src])
+        np.testing.assert_array_equal(got_p[h, :budget], p[src])
+    assert stayed > 4
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
