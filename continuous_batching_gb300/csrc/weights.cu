@@ -82,11 +82,12 @@ static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr int kMaxRows = 1 << 18;              // state rows whose repeats are looked for
 constexpr int kMaxLen = INT32_MAX - 32 * 128;  // keys: a warp's 32 blocks more are counted in 32 bits
 constexpr int kMaxSeqs = 8192;                 // sequences whose costs are held while they are dealt
-// before the pipeline starts: a bit per state row in slot 0, the first sequences' metadata from slot
-// 1, a cost per sequence from slot 4
-constexpr int kMeta = kSlot, kCosts = 4 * kSlot;
+// before the pipeline starts: a bit per state row in slot 0 (named) and in slot 6 (named again), the
+// first sequences' metadata from slot 1, a cost per sequence from slot 4
+constexpr int kMeta = kSlot, kCosts = 4 * kSlot, kAgain = 6 * kSlot;
 constexpr int kMetaSeqs = 3 * kSlot / 32;
-static_assert(kMaxRows / 8 <= kSlot && kMaxSeqs * 8 <= 3 * kSlot, "scratch of the deal");
+static_assert(kMaxRows / 8 <= kSlot && kMaxSeqs * 8 <= 2 * kSlot, "scratch of the deal");
+constexpr int64_t kShared = -1;                // cost of a sequence whose state row another one names
 constexpr int64_t kCostFew = 5, kCostMany = 2; // of a key tile; of a key tile and query tile
 
 // A role that waits on a barrier waits for each of its phases in turn: parity tells only neighbours
@@ -237,15 +238,8 @@ __device__ __forceinline__ void derive(Seq& q, int log2qt) {
     q.head_cost = cost_before(q, q.n_tiles, log2qt);
 }
 
-// Another sequence with query rows names sequence s's state row: both would race on it.
-__device__ __noinline__ bool shares_row(const int32_t* rows, const int32_t* cu, int B, int s) {
-    for (int i = 0; i < B; ++i)
-        if (i != s && rows[i] == rows[s] && cu[i + 1] != cu[i]) return true;
-    return false;
-}
-
-// repeated: some row is named twice (the sequences that do are then looked for).
-__device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt, bool repeated) {
+// shared: another sequence with query rows names s's state row (both would race on it).
+__device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt, bool shared) {
     Seq q;
     const int c0 = p.cu[s], c1 = p.cu[s + 1];
     q.row = p.rows ? p.rows[s] : s;
@@ -261,7 +255,7 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int s, int log2qt, bool
     q.held = p.held ? p.held[s] : q.ctx - q.n_q;
     if (n < 0 || c0 < 0 || c1 > p.T || q.n_q > q.ctx || q.ctx > min(p.max_len, p.max_ctx) ||
         (int64_t(q.ctx) + p.bs - 1) / p.bs > p.max_blocks || q.row >= p.n_rows || q.held < 0 ||
-        q.held > q.ctx || (repeated && shares_row(p.rows, p.cu, p.B, s))) {
+        q.held > q.ctx || shared) {
         q.bad = true;
         return q;
     }
@@ -412,10 +406,11 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     uint32_t* once = reinterpret_cast<uint32_t*>(smem);
+    uint32_t* again = reinterpret_cast<uint32_t*>(smem + kAgain);
     int64_t* costs = reinterpret_cast<int64_t*>(smem + kCosts);
     volatile int* repeated = reinterpret_cast<volatile int*>(smem + kCtl + kTwiceOff);
     if (p.rows)
-        for (int i = threadIdx.x; i < (p.n_rows + 31) / 32; i += kThreads) once[i] = 0;
+        for (int i = threadIdx.x; i < (p.n_rows + 31) / 32; i += kThreads) once[i] = again[i] = 0;
     if (threadIdx.x == 0) *repeated = 0;
     if (warp == 18 && lane < 3)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(
@@ -436,7 +431,10 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             const Seq q = load_seq(p, s, log2qt, false);
             if (p.rows && q.row >= 0 && q.row < p.n_rows && q.any) {
                 const uint32_t bit = 1u << (q.row & 31);
-                if (atomicOr(once + (q.row >> 5), bit) & bit) *repeated = 1;
+                if (atomicOr(once + (q.row >> 5), bit) & bit) {
+                    atomicOr(again + (q.row >> 5), bit);
+                    *repeated = 1;
+                }
             }
             costs[s] = q.head_cost;
             if (s < kMetaSeqs) {
@@ -452,6 +450,18 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         // these words were written through the generic proxy where TMA writes next
         fence_proxy_async();
         n_stages = __syncthreads_or(some_many) ? 3 : kMaxStages;
+        if (*repeated) {                             // rare: those that share a row drop out
+            for (int s = threadIdx.x; s < p.B; s += kThreads) {
+                const int row = p.rows[s];
+                if (row < 0 || row >= p.n_rows || p.cu[s + 1] == p.cu[s] ||
+                    !(again[row >> 5] >> (row & 31) & 1))
+                    continue;
+                costs[s] = kShared;
+                if (blockIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+            }
+            fence_proxy_async();
+            __syncthreads();
+        }
         // behind a step of decode rows alone there is nothing left: 1.3 us earlier out
         if (p.skip_decode && !__syncthreads_or(some)) {
             if (warp == 17)
@@ -570,16 +580,24 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             }
         };
         // ---- the share: this CTA's range of the total cost, and the sequence it starts in
+        // (the tiles take the costs' place while later sequences are read: which of them share a row is
+        // kept as bits, those of sequences 1024 k + 32 l .. + 31 in lane l's word k)
         const bool twice = *repeated != 0;
-        if (twice) {                                 // rare: those that share a row drop out
-            for (int s = lane; s < p.B; s += 32) {
-                const Seq q = load_seq(p, s, log2qt, true);
-                costs[s] = q.head_cost;
-                if (q.bad && blockIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+        uint32_t shared[kMaxSeqs / 1024];
+        if (twice) {
+            for (int s0 = 0; s0 < p.B; s0 += 32) {
+                const bool out = s0 + lane < p.B && costs[s0 + lane] == kShared;
+                const uint32_t word = __ballot_sync(0xffffffffu, out);
+                if (lane == (s0 >> 5 & 31)) shared[s0 >> 10] = word;
+                if (out) costs[s0 + lane] = 0;
             }
             fence_proxy_async();
             __syncwarp();
         }
+        const auto is_shared = [&](int s) {          // s the same for the whole warp
+            if (!twice) return false;
+            return (__shfl_sync(0xffffffffu, shared[s >> 10], s >> 5 & 31) >> (s & 31) & 1) != 0;
+        };
         const int per = (p.B + 31) / 32;             // sequences a lane adds up
         int64_t mine = 0;
         for (int i = 0, s = lane * per; i < per && s < p.B; ++i, ++s) mine += costs[s];
@@ -613,11 +631,11 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             q.held = m[1].x;
             derive(q, log2qt);
         } else if (first_s < p.B) {
-            q = load_seq(p, first_s, log2qt, twice);
+            q = load_seq(p, first_s, log2qt, false);
         }
         __syncwarp();                                // costs and metadata make room for the tiles
         for (int s = first_s; s < p.B && base < hi && ok; ++s) {
-            if (s > first_s) q = load_seq(p, s, log2qt, twice);
+            if (s > first_s) q = load_seq(p, s, log2qt, is_shared(s));
             if (q.head_cost == 0) continue;
             Item I;
             I.seq = s;

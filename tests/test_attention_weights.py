@@ -558,3 +558,56 @@ def test_chunks_into_a_large_state_round_once(seqs, step):
 @pytest.mark.gpu
 def test_fp8_chunks_into_a_large_state_round_once():
     _large_state(wl.make_step(64, 8, 128, 16, [1000, 700, 300], [60, 100, 17], seed=2), 5e6, True, fp8=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("chunks", [False, True])
+def test_rows_named_twice_among_thousands(chunks):
+    """Those that share a state row drop out, wherever they lie in the deal; the others are as without
+    them, and the call stays one of microseconds."""
+    B, Hkv = 6001, 2
+    rng = np.random.default_rng(B)
+    ctx = rng.integers(1, 60, B)
+    n_q = np.minimum(ctx, rng.integers(0, 50, B)) if chunks else np.ones(B, int)
+    st = wl.make_step(8, Hkv, 64, 8, ctx, n_q, seed=9)
+    shape = bd.Shape.make(st.Hq, st.Hkv, st.D, st.block_size, st.num_blocks)
+    q, kp = dev(st.q.view(np.int16), torch.bfloat16), dev(st.k_pool.view(np.int16), torch.bfloat16)
+    lse = torch.full((st.T, st.Hq), 3.0, device="cuda")
+    table, cu, lens = dev(st.block_table), dev(st.cu_seqlens_q), dev(st.ctx_lens)
+    plain = rng.permutation(B + 40)[:B].astype(np.int32)
+    start = torch.rand(B + 40, Hkv, 64, device="cuda")
+
+    def run(rows):
+        w, err, r = start.clone(), torch.zeros(1, dtype=torch.int32, device="cuda"), dev(rows)
+        call = lambda: bd.paged_attention_weights(q, kp, lse, table, cu, lens, r, w, shape, err=err)
+        call()
+        got = w.clone(), int(err.item())
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        times = []
+        for _ in range(3):
+            a.record()
+            call()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return *got, min(times)
+
+    whole, err, t_plain = run(plain)
+    assert err == 0
+    active = np.flatnonzero(n_q > 0)
+    rows = plain.copy()
+    groups = [active[[3, -2]], active[[1000, 1001, 4000]], active[[0, 2500]]]
+    out = set()
+    for g in groups:
+        rows[g] = plain[g[0]]
+        out |= set(g.tolist())
+    idle = np.flatnonzero(n_q == 0)
+    if len(idle):
+        rows[idle[0]] = plain[active[70]]           # a sequence without query rows shares nothing
+    got, err, t = run(rows)
+    assert err == bd.PA_DEVERR_META
+    want = start.clone()
+    live = torch.from_numpy(plain[[s for s in active.tolist() if s not in out]].astype(np.int64)).cuda()
+    want[live] = whole[live]
+    assert torch.equal(got, want)
+    assert t < 3 * t_plain + 0.3, (t, t_plain)      # milliseconds; a scan of all pairs takes tens of them
