@@ -7,9 +7,10 @@
 // with the pairs (i, i + r/2) or (2i, 2i+1) of the first r of D columns; the others pass through.
 // Everything between the bf16 input and the single rounding of the output is fp32.
 //
-// Angles. A pair's frequency is held as turns per position in units of 2^-64 turn
-// (pa_rope_pair.step), so position * step in 64-bit integers, wrapping, IS the phase modulo one
-// turn, exactly, for positions of any size and sign: nothing is lost to range reduction. Its top
+// Angles. A pair's frequency is held as turns per position, rounded to units of 2^-64 turn
+// (pa_rope_pair.step). position * step in 64-bit integers, wrapping, is that step's phase modulo one
+// turn exactly, for positions of any size and sign: nothing is lost to range reduction, and what the
+// step's rounding makes of it is 2^-65 turn a position (2^-34 turn at 2^31). The phase's top
 // 32 bits go to fp32 (2^-25 of half a turn) and sincospif. Reading the sines from a table instead
 // would read 8 bytes a pair and token from memory, against none here.
 //
@@ -359,6 +360,27 @@ int32_t norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stri
 
 }  // namespace
 
+namespace {
+
+// f / 2 pi turns modulo one turn, rounded to the nearest 2^-64 of a turn. The quotient is carried in
+// two doubles (quotient and what it leaves of f, 2 pi in two doubles itself; their 2^-100 is enough for
+// |f| < 2^30): one double's 53 bits would be off by 2^10 units for a frequency of a turn, which a far
+// position multiplies.
+uint64_t turn_step(double f) {
+    constexpr double kTwoPi = 0x1.921fb54442d18p+2, kTwoPiLow = 0x1.1a62633145c07p-52;
+    const double turns = std::fabs(f) / kTwoPi;
+    const double left = std::fma(-turns, kTwoPi, std::fabs(f)) - turns * kTwoPiLow;
+    double low = left / kTwoPi;
+    low -= std::nearbyint(low);                     // (not zero for frequencies of 2^53 turns or more)
+    // the fraction of `turns` in units, exactly; its whole units apart from the rest
+    const double units = std::ldexp(turns - std::floor(turns), 64), whole = std::floor(units);
+    const double rest = std::nearbyint((units - whole) + std::ldexp(low, 64));   // |rest| <= 2^63 + 1
+    const uint64_t step = uint64_t(whole) + (rest < 0 ? ~uint64_t(-rest) + 1 : uint64_t(rest));
+    return f < 0 ? ~step + 1 : step;
+}
+
+}  // namespace
+
 extern "C" int32_t pa_rope_pairs(const double* inv_freq, const int32_t* axes, int32_t n_pairs,
                                  int32_t n_axes, pa_rope_pair* out) {
     if (n_pairs < 0 || n_axes < 1) return PA_ERR_INVALID;
@@ -369,11 +391,7 @@ extern "C" int32_t pa_rope_pairs(const double* inv_freq, const int32_t* axes, in
         if (axes && (axes[i] < 0 || axes[i] >= n_axes)) return PA_ERR_BOUNDS;
     }
     for (int32_t i = 0; i < n_pairs; ++i) {
-        const double turns = inv_freq[i] / 6.283185307179586477;
-        // the fraction of a turn, in [0, 1); a tiny negative one would round up to a whole turn
-        double frac = turns - std::floor(turns);
-        if (frac >= 1.0) frac = 0.0;
-        out[i].step = uint64_t(std::ldexp(frac, 64));
+        out[i].step = turn_step(inv_freq[i]);
         out[i].axis = axes ? axes[i] : 0;
         out[i].reserved = 0;
     }

@@ -486,7 +486,8 @@ typedef struct pa_rope_pair {
 } pa_rope_pair;
 
 /* Fills out[n_pairs] (host) from frequencies in radians per position (host doubles; any finite
- * value: scaled or interpolated frequencies are passed as they come out). axes (host, may be NULL:
+ * value: scaled or interpolated frequencies are passed as they come out). A step is the nearest
+ * 2^-64 turn for |f| < 2^30; faster ones lose a bit for each doubling. axes (host, may be NULL:
  * all 0) says which row of positions turns each pair, in any arrangement: sections, interleaved.
  * PA_ERR_BOUNDS for an axis outside [0, n_axes). Upload it once; a model's layers share it. */
 int32_t pa_rope_pairs(const double* inv_freq, const int32_t* axes, int32_t n_pairs,
@@ -499,8 +500,9 @@ int32_t pa_rope_pairs(const double* inv_freq, const int32_t* axes, int32_t n_pai
  * from 2 n_pairs on pass through. q goes to q_out[t], k to k_pool[slot_mapping[t]], v unchanged to
  * v_pool[slot_mapping[t]]; a slot < 0 writes no K and V, one outside the pool is skipped and sets
  * PA_DEVERR_SLOT. fp32 in between, one rounding to bf16 (k over an fp8 pool: to e4m3(y / k_scale),
- * v as paged_kv_write_fp8). The phase is kept modulo a turn in 64-bit integers: positions of any
- * size (negative ones too) turn exactly.
+ * v as paged_kv_write_fp8). The phase is position * step modulo a turn in 64-bit integers, exact for
+ * positions of any size (negative ones too); against f itself it is off by the step's rounding, at
+ * most |position| * 2^-65 turn.
  * Device: q [T, Hq, D], k, v [T, Hkv, D] bf16, each with its own stride in elements between tokens
  * (heads and columns dense), so the three may be parts of one projection; q_weight, k_weight [D]
  * bf16 or NULL; rope [n_pairs]; positions [n_axes, T] int32; slot_mapping [T]; q_out [T, Hq, D]

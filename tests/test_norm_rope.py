@@ -271,3 +271,36 @@ def test_binding_refusals_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want * 2) and torch.equal(kp, want_k)
+
+
+def _turn_digits(bits):
+    """2 pi in units of 2^-bits, from Machin's formula."""
+    one = 1 << (bits + 32)
+
+    def arctan_of_inverse(n):
+        total, term, k = 0, one // n, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+
+    return 2 * (16 * arctan_of_inverse(5) - 4 * arctan_of_inverse(239)) >> 32
+
+
+def test_pairs_are_the_nearest_of_their_unit():
+    """A step is f / 2 pi turns, rounded once to units of 2^-64 turn: the quotient is known to more bits
+    than a double's, so a far position's phase is off by the step's half unit times the position."""
+    rng = np.random.default_rng(0)
+    f = np.concatenate([10000.0 ** (-np.arange(64) / 64), [1.0, -1.0, 0.5, 2 * np.pi, -2 * np.pi, 6.25, 100.0, 1e6, 1e-19,
+                                                           -1e-19, 0.0, 5e-324, -5e-324], rng.standard_normal(200)])
+    bits = 1200
+    turn = _turn_digits(bits)
+    got = bd.pa_rope_pairs(f)["step"]
+    for x, step in zip(f.tolist(), got.tolist()):
+        m, d = x.as_integer_ratio()
+        want = (m << (bits + 64 + 20)) // (d * turn)             # turns in units of 2^-84
+        off = ((step << 20) - want) % (1 << 84)
+        off = min(off, (1 << 84) - off)
+        # half a unit, and what a double-double quotient leaves of it (2^-100 of the turns)
+        assert off <= (1 << 19) + 2 + abs(want) // (1 << 100), (x, off / 2 ** 20)
