@@ -611,3 +611,28 @@ def test_rows_named_twice_among_thousands(chunks):
     want[live] = whole[live]
     assert torch.equal(got, want)
     assert t < 3 * t_plain + 0.3, (t, t_plain)      # milliseconds; a scan of all pairs takes tens of them
+
+
+@pytest.mark.gpu
+def test_step_of_a_decode_row_and_a_chunk_that_name_one_state_row():
+    """Decode rows and chunks are summed by different kernels: both drop out, whichever else is there."""
+    st = wl.make_step(8, 2, 64, 16, [40, 350, 60, 500, 90], [1, 300, 1, 120, 7], seed=8)
+    shape = bd.Shape.make(st.Hq, st.Hkv, st.D, st.block_size, st.num_blocks)
+    q, kp, vp = (dev(x.view(np.int16), torch.bfloat16) for x in (st.q, st.k_pool, st.v_pool))
+    items = dev(bd.pa_plan_step(shape, st.cu_seqlens_q, st.ctx_lens).view(np.int32).reshape(-1))
+    out, lse = torch.empty(st.T, 8, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(st.T, 8, device="cuda")
+    ws = torch.empty(bd.pa_step_weights_workspace_bytes(shape, 5, st.T, 500) // 4, device="cuda")
+
+    def run(rows):
+        w, err = torch.full((6, 2, 512), 0.5, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        bd.paged_attention_step_weights(q, kp, vp, dev(st.block_table), dev(st.cu_seqlens_q), dev(st.ctx_lens), 500, items,
+                                        ws, out, lse, dev(np.asarray(rows, np.int32)), w, shape, err=err)
+        return w, int(err.item())
+
+    want, err = run([0, 1, 2, 3, 4])
+    assert err == 0
+    for rows, alone in (([0, 0, 2, 3, 4], [2, 3, 4]), ([0, 1, 2, 2, 2], [0, 1]), ([5, 1, 2, 1, 5], [2])):
+        got, err = run(rows)
+        assert err == bd.PA_DEVERR_META
+        for r in range(6):
+            assert torch.equal(got[r], want[r]) if r in alone else bool((got[r] == 0.5).all()), (rows, r)
