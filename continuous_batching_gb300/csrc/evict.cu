@@ -18,7 +18,11 @@
 // of atomics: they count. Then the CTAs share the moves. Bound by latency when few rows move (the
 // passes' barriers), by the strays' K and V rows otherwise.
 //
-// Measured (8 KV heads of 128): 64 full caches of 2,049 entries, 10.5 us in a graph; eight prompts of
+// Shared memory and the cluster's size follow max_len: the contexts are the device's to know.
+//
+// Measured (8 KV heads of 128): 64 full caches of 2,049 entries in a graph, 10.1 us with state rows of
+// 2,054 entries (one wave of CTAs), 14.2 with rows of 8,192 to 131,072 (two waves, for the bitmaps and
+// keys that longer contexts would need), 24.1 with 524,288; eight prompts of
 // 4,000 .. 40,000 cut to 2,048 (123 MB) 42 us, of a CTA's time on average 5 up to the first histogram, 9
 // in the passes and bitmaps, 6 to list the moves and 10 in them (where memory is at its limit).
 #include <cooperative_groups.h>

@@ -88,7 +88,11 @@ constexpr int kMeta = kSlot, kCosts = 4 * kSlot, kAgain = 6 * kSlot;
 constexpr int kMetaSeqs = 3 * kSlot / 32;
 static_assert(kMaxRows / 8 <= kSlot && kMaxSeqs * 8 <= 2 * kSlot, "scratch of the deal");
 constexpr int64_t kShared = -1;                // cost of a sequence whose state row another one names
-constexpr int64_t kCostFew = 5, kCostMany = 2; // of a key tile; of a key tile and query tile
+// Cost of a key tile, and of a key tile and query tile. Their ratio counts in a batch with both kinds
+// alone, and it weighs streamed keys too heavily there: 48 decode rows at 2k .. 16k keys beside four
+// 512-row chunks (32 / 8 heads of 128) take 261 us, the two kinds by themselves 151 and 87; with 5 : 3
+// 231, 5 : 4 246, 5 : 1 443. Over an e4m3 cache 288 (5 : 3 236, 5 : 4 241), head_dim 64 244 (192, 180).
+constexpr int64_t kCostFew = 5, kCostMany = 2;
 
 // A role that waits on a barrier waits for each of its phases in turn: parity tells only neighbours
 // apart. Warps arrive once, not 32 times.
@@ -1171,10 +1175,13 @@ __host__ __device__ int64_t scores_row(int32_t max_ctx) {
 
 // One thread per four keys of a (sequence, KV head): the group's raw scores, stored by the
 // attention kernel, against the rows' log-sum-exps. A decode step so pays 4 g bytes per key and
-// KV head written and read again in place of a second read of K's 2 D: 32 rows at 4k .. 16k keys (8 KV
-// heads of 128, group 4) take 261 us, 230 of them the plain step, 15 this kernel (56 MB read); the step
-// followed by a pass over K 360. As a part of the kernel above (a warp per key tile, one, two or
-// four tiles at a time) 265 to 271.
+// KV head written and read again in place of a second read of K's 2 D (D over an e4m3 cache): 32 rows at
+// 4k .. 16k keys (8 KV heads of 128, group 4) take 261 us, 230 of them the plain step, 15 this kernel (56
+// MB read); the step followed by a pass over K 360. Larger groups gain less, but gain: 32 rows at 8,000
+// keys, kept scores against a second pass, group 8 202 / 271 us, group 16 (4 KV heads) 132 / 158, over
+// e4m3 149 / 171, head_dim 64 101 / 120. As a part of the kernel above (a warp per key tile, one, two or
+// four tiles at a time) 265 to 271. The grid covers max_ctx, whose idle blocks leave at once: 32 rows of
+// 2,000 keys 79 us at a bound of 2,000 or 10,000, 85 at 40,000.
 constexpr int kDecodeKeys = 1024;      // per block of 256 threads
 __global__ void __launch_bounds__(256)
     decode_weights_kernel(const float* __restrict__ scores, const Params p) {
