@@ -66,7 +66,17 @@ class WorkItem(C.Structure):
 
 WORK_ITEM_DTYPE = np.dtype([(n, np.int32) for n, _ in WorkItem._fields_])
 ITEM_INTS = len(WorkItem._fields_)          # int32 words per pa_work_item
-PA_ITEM_PLAIN, PA_ITEM_GROUP, PA_ITEM_RESUME = 0, 1, 2
+PA_ITEM_PLAIN, PA_ITEM_GROUP, PA_ITEM_RESUME, PA_ITEM_DIRECT = 0, 1, 2, 3
+
+
+class Q4Sizes(C.Structure):
+    """pa_q4_plan: the sizes of a 4-bit step's plan."""
+    _fields_ = [(n, C.c_int32) for n in ("B", "T", "max_ctx", "direct_rows", "n_direct", "n_fold",
+                                         "n_chunk", "n_expand", "expand_cols", "words")]
+
+
+class Pages(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("page_bytes", C.c_int64)]
 
 _lib = None
 _lock = threading.Lock()
@@ -185,6 +195,21 @@ def load() -> C.CDLL:
         _sig(lib, "pa_step_weights_workspace_bytes", C.c_size_t, [sp, i32, i32, i32])
         _sig(lib, "paged_attention_step_weights", i32, step + lse + state + end)
         _sig(lib, "paged_attention_step_weights_fp8", i32, step + f8 + lse + state + end)
+        _sig(lib, "pa_alloc_compact", i32, [ap, _i32p, i32, _i32p])
+        _sig(lib, "pa_alloc_resize", i32, [ap, i32])
+        _sig(lib, "paged_copy_pages", i32, [_vp, i32, C.POINTER(Pages), i32, i32, _vp, _vp])
+        i64, qp = C.c_int64, C.POINTER(Q4Sizes)
+        _sig(lib, "paged_kv_write_q4", i32, [_vp, i64, _vp, i64, _vp, i32, _vp, _vp] + end)
+        _sig(lib, "paged_kv_read_q4", i32, [_vp, i32, _vp, _vp, _vp, _vp] + end)
+        _sig(lib, "paged_qk_norm_rope_write_q4", i32, norm_rope + end)
+        _sig(lib, "pa_q4_max_direct_rows", i32, [])
+        _sig(lib, "pa_q4_direct_rows", i32, [sp, i32])
+        _sig(lib, "pa_q4_plan_size", i32, [sp, i32, _i32p, _i32p, i32, qp])
+        _sig(lib, "pa_q4_plan_limits", i32, [sp, i32, i32, i32, i32, i32, qp])
+        _sig(lib, "pa_plan_step_q4", i32, [sp, i32, _i32p, _i32p, qp, _i32p])
+        _sig(lib, "pa_q4_workspace_bytes", C.c_size_t, [sp, qp])
+        _sig(lib, "paged_attention_step_q4", i32,
+             [_vp, _vp, _vp, _vp, i32, _vp, _vp, qp, _vp, _vp, C.c_size_t, _vp] + end)
         _sig(lib, "paged_evict", C.c_int32,
              [_vp, _vp, C.c_int32, _vp, C.c_int32, _vp, _vp, _vp, _vp, _vp, C.c_int32, C.c_int32,
               C.c_int32, _vp, _vp, _vp, _vp, C.c_int32, C.c_int32, sp, _vp, _vp])
@@ -333,6 +358,19 @@ class Allocator:
         _check(self._lib.pa_alloc_cow(self._h, int(seq), int(start), int(n), _p32(pairs), cap,
                                       C.byref(k)), "pa_alloc_cow")
         return [(int(pairs[2 * i]), int(pairs[2 * i + 1])) for i in range(k.value)]
+
+    def compact(self) -> list:
+        """Moves the live blocks to the lowest ids; returns the [(old, new)] page copies to make."""
+        k = C.c_int32()
+        cap = max(self.num_blocks, 1)
+        pairs = np.empty(2 * cap, np.int32)
+        _check(self._lib.pa_alloc_compact(self._h, _p32(pairs), cap, C.byref(k)), "pa_alloc_compact")
+        return [(int(pairs[2 * i]), int(pairs[2 * i + 1])) for i in range(k.value)]
+
+    def resize(self, num_blocks: int) -> None:
+        """Gives up the blocks from num_blocks on (none may be live), or adds blocks."""
+        _check(self._lib.pa_alloc_resize(self._h, int(num_blocks)), "pa_alloc_resize")
+        self.num_blocks = int(num_blocks)
 
     def build_step(self, seqs, ctx_lens, n_new, max_blocks: int):
         """Returns (cu_seqlens_q, slot_mapping, block_table) host arrays for one step."""
@@ -622,7 +660,8 @@ def _norm_rope(q, k_new, v_new, q_weight, k_weight, eps, rope, positions, slot_m
         one = positions.dim() == 1
         n_axes = 1 if one else positions.shape[0]
         pp = _arg(positions, i32, dev, (T,) if one else (n_axes, T), "positions")
-    pool = (shape.num_blocks, shape.block_size, Hkv, D)
+    q4 = scales == "q4"
+    pool = pa_q4_pool_shape(shape) if q4 else (shape.num_blocks, shape.block_size, Hkv, D)
     e = bf16 if scales is None else rt.u8
     args = (qp, qs, kp, ks, vp, vs,
             None if q_weight is None else _arg(q_weight, bf16, dev, (D,), "q_weight"),
@@ -635,6 +674,9 @@ def _norm_rope(q, k_new, v_new, q_weight, k_weight, eps, rope, positions, slot_m
     if scales is None:
         _check(rt.lib.paged_qk_norm_rope_write(*args, C.byref(shape), ep, rt.stream(stream, dev)),
                "paged_qk_norm_rope_write")
+    elif q4:
+        _check(rt.lib.paged_qk_norm_rope_write_q4(*args, C.byref(shape), ep, rt.stream(stream, dev)),
+               "paged_qk_norm_rope_write_q4")
     else:
         _check(rt.lib.paged_qk_norm_rope_write_fp8(*args, *scales, C.byref(shape), ep,
                                                    rt.stream(stream, dev)),
@@ -817,6 +859,155 @@ def paged_evict(k_pool, v_pool, block_table, ctx_lens, budget, n_tokens, kept, r
         _arg(positions_out, i32, dev, state, "positions_out"), n_rows, max_len, C.byref(shape),
         None if err is None else _arg(err, i32, dev, (1,), "err"), rt.stream(stream, dev)),
         "paged_evict")
+
+
+# ------------------------------------------------------------------------- 4-bit cache
+
+def pa_q4_pool_shape(shape: Shape) -> tuple:
+    """Shape of a 4-bit pool (uint8): per block and KV head the tokens' codes, then their parameters."""
+    D = shape.head_dim
+    return (shape.num_blocks, shape.num_kv_heads, shape.block_size * (D // 2 + D // 8))
+
+
+def paged_kv_write_q4(k_new, v_new, slot_mapping, k_pool, v_pool, shape: Shape, err=None,
+                      stream=None) -> None:
+    """bf16 k_new / v_new [T, Hkv, D] (strided between tokens) quantised into 4-bit pools
+    (pa_q4_pool_shape): per 32 columns a scale and a minimum in bf16."""
+    rt = _rt()
+    dev, T = rt.device(), slot_mapping.shape[0]
+    Hkv, D = shape.num_kv_heads, shape.head_dim
+    pool = pa_q4_pool_shape(shape)
+    kp, ks = _token_rows(k_new, rt.bf16, Hkv, D, T, dev, "k_new")
+    vp, vs = _token_rows(v_new, rt.bf16, Hkv, D, T, dev, "v_new")
+    _check(rt.lib.paged_kv_write_q4(
+        kp, ks, vp, vs, _arg(slot_mapping, rt.i32, dev, (T,), "slot_mapping"), T,
+        _arg(k_pool, rt.u8, dev, pool, "k_pool"), _arg(v_pool, rt.u8, dev, pool, "v_pool"),
+        C.byref(shape), None if err is None else _arg(err, rt.i32, dev, (1,), "err"),
+        rt.stream(stream, dev)), "paged_kv_write_q4")
+
+
+def paged_qk_norm_rope_write_q4(q, k_new, v_new, q_weight, k_weight, eps: float, rope, positions,
+                                slot_mapping, q_out, k_pool, v_pool, shape: Shape,
+                                interleaved: bool = False, err=None, stream=None) -> None:
+    """paged_qk_norm_rope_write into 4-bit pools (pa_q4_pool_shape)."""
+    _norm_rope(q, k_new, v_new, q_weight, k_weight, eps, rope, positions, slot_mapping, q_out,
+               k_pool, v_pool, shape, interleaved, err, stream, "q4")
+
+
+def paged_kv_read_q4(slot_mapping, k_pool, v_pool, k_out, v_out, shape: Shape, err=None,
+                     stream=None) -> None:
+    """The rows at slot_mapping of 4-bit pools, to bf16 k_out / v_out [T, Hkv, D]."""
+    rt = _rt()
+    dev, T = rt.device(), slot_mapping.shape[0]
+    rows = (T, shape.num_kv_heads, shape.head_dim)
+    pool = pa_q4_pool_shape(shape)
+    _check(rt.lib.paged_kv_read_q4(
+        _arg(slot_mapping, rt.i32, dev, (T,), "slot_mapping"), T,
+        _arg(k_pool, rt.u8, dev, pool, "k_pool"), _arg(v_pool, rt.u8, dev, pool, "v_pool"),
+        _arg(k_out, rt.bf16, dev, rows, "k_out"), _arg(v_out, rt.bf16, dev, rows, "v_out"),
+        C.byref(shape), None if err is None else _arg(err, rt.i32, dev, (1,), "err"),
+        rt.stream(stream, dev)), "paged_kv_read_q4")
+
+
+class Q4Plan:
+    """The plan of a 4-bit step: its sizes and its words (int32, numpy or on the device)."""
+
+    def __init__(self, sizes: Q4Sizes, words):
+        self.sizes, self.words = sizes, words
+
+
+def pa_q4_direct_rows(shape: Shape, max_new: int = 1) -> int:
+    return int(load().pa_q4_direct_rows(C.byref(shape), int(max_new)))
+
+
+def pa_q4_plan_limits(shape: Shape, B: int, T: int, max_ctx: int, direct_rows: int,
+                      max_expand: int = 0) -> Q4Sizes:
+    """Sizes for every step within these bounds (max_expand: 128-token blocks of expanded contexts)."""
+    s = Q4Sizes()
+    _check(load().pa_q4_plan_limits(C.byref(shape), int(B), int(T), int(max_ctx), int(direct_rows),
+                                    int(max_expand), C.byref(s)), "pa_q4_plan_limits")
+    return s
+
+
+def pa_plan_step_q4(shape: Shape, cu_seqlens_q: np.ndarray, ctx_lens: np.ndarray,
+                    direct_rows: Optional[int] = None, limits: Optional[Q4Sizes] = None,
+                    device=None) -> Q4Plan:
+    """The plan of one 4-bit step: of exactly its sizes, or padded to `limits`. direct_rows: sequences
+    of up to so many query rows (tokens times heads of a group) are read from the codes (None: what is
+    fast; 0: none, so that single rows and chunks get the same bits)."""
+    lib = load()
+    cu, ctx = _i32(cu_seqlens_q), _i32(ctx_lens)
+    B = len(ctx)
+    if limits is not None:
+        sizes = limits
+    else:
+        if direct_rows is None:
+            g = shape.num_q_heads // max(shape.num_kv_heads, 1)
+            most = int(load().pa_q4_max_direct_rows()) // max(g, 1)
+            n = np.diff(cu)
+            few = n[(n > 0) & (n <= max(most, 1))]
+            direct_rows = pa_q4_direct_rows(shape, int(few.max()) if len(few) else 1)
+        sizes = Q4Sizes()
+        _check(lib.pa_q4_plan_size(C.byref(shape), B, _p32(cu), _p32(ctx), int(direct_rows),
+                                   C.byref(sizes)), "pa_q4_plan_size")
+    words = np.empty(max(sizes.words, 1), np.int32)
+    _check(lib.pa_plan_step_q4(C.byref(shape), B, _p32(cu), _p32(ctx), C.byref(sizes), _p32(words)),
+           "pa_plan_step_q4")
+    if device is not None:
+        import torch
+        words = torch.from_numpy(words).to(device)
+    return Q4Plan(sizes, words)
+
+
+def pa_q4_workspace_bytes(shape: Shape, plan) -> int:
+    """Bytes of workspace for a step under a Q4Plan (or Q4Sizes)."""
+    return int(load().pa_q4_workspace_bytes(C.byref(shape), C.byref(getattr(plan, "sizes", plan))))
+
+
+def paged_attention_step_q4(q, k_pool, v_pool, block_table, cu_seqlens_q, ctx_lens, plan: Q4Plan,
+                            workspace, out, shape: Shape, err=None, stream=None) -> None:
+    """paged_attention_step over 4-bit pools (pa_q4_pool_shape). plan: from pa_plan_step_q4, its words
+    on the device; workspace: a flat fp32 tensor of pa_q4_workspace_bytes (or None if that is 0)."""
+    rt = _rt()
+    dev, i32, sizes = rt.device(), rt.i32, plan.sizes
+    B, T, mb = sizes.B, sizes.T, block_table.shape[1]
+    rows = (T, shape.num_q_heads, shape.head_dim)
+    pool = pa_q4_pool_shape(shape)
+    ws, n = None, 0
+    if workspace is not None:
+        n = workspace.shape[0]
+        ws = _arg(workspace, rt.f32, dev, (n,), "workspace")
+    _check(rt.lib.paged_attention_step_q4(
+        _arg(q, rt.bf16, dev, rows, "q"), _arg(k_pool, rt.u8, dev, pool, "k_pool"),
+        _arg(v_pool, rt.u8, dev, pool, "v_pool"), _arg(block_table, i32, dev, (B, mb), "block_table"),
+        mb, _arg(cu_seqlens_q, i32, dev, (B + 1,), "cu_seqlens_q"),
+        _arg(ctx_lens, i32, dev, (B,), "ctx_lens"), C.byref(sizes),
+        _arg(plan.words, i32, dev, (max(sizes.words, 1),), "plan"), ws, 4 * n,
+        _arg(out, rt.bf16, dev, rows, "out"), C.byref(shape),
+        None if err is None else _arg(err, i32, dev, (1,), "err"), rt.stream(stream, dev)),
+        "paged_attention_step_q4")
+
+
+# ------------------------------------------------------------------------- pages
+
+def paged_copy_pages(pairs, pools, err=None, stream=None) -> None:
+    """Copies pages in every pool: pairs int32 [n, 2] (device) of (from, to) block ids, from
+    Allocator.cow or Allocator.compact; pools: tensors of any type whose first dimension is the blocks
+    (of all layers, K and V), all with the same number of blocks."""
+    rt = _rt()
+    dev = rt.device()
+    n = pairs.shape[0]
+    blocks = pools[0].shape[0] if len(pools) else 0
+    a = (Pages * max(len(pools), 1))()
+    for i, t in enumerate(pools):
+        if t.shape[0] != blocks or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"pools[{i}]: expected a contiguous tensor of {blocks} blocks on the "
+                             f"current CUDA device ({dev})")
+        a[i].pool = t.data_ptr()
+        a[i].page_bytes = t.numel() // max(blocks, 1) * t.element_size()
+    _check(rt.lib.paged_copy_pages(_arg(pairs, rt.i32, dev, (n, 2), "pairs"), n, a, len(pools), blocks,
+                                   None if err is None else _arg(err, rt.i32, dev, (1,), "err"),
+                                   rt.stream(stream, dev)), "paged_copy_pages")
 
 
 class StepLimits:

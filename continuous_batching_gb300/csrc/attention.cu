@@ -1722,6 +1722,27 @@ int32_t pa_detail::attention_step_stats(const void* q, const void* k_pool, const
     return launch<64, false, true>(maps, prm, max_ctx, stream);
 }
 
+// Without partials no row of one token may have several splits (they would have no place): a sequence of
+// one query row then has a context of 0 (q4_expand_kernel), which its items are refused by, and the combine
+// is not launched.
+int32_t pa_detail::attention_step_expanded(const void* q, const void* k_pool, const void* v_pool,
+                                           const int32_t* block_table, int32_t max_blocks,
+                                           const int32_t* cu_seqlens_q, const int32_t* ctx_lens,
+                                           int32_t B, int32_t T, int32_t max_ctx,
+                                           const pa_work_item* items, int32_t n_items,
+                                           void* partials, void* out, const pa_shape* shape,
+                                           int32_t* err_flag, cudaStream_t stream) {
+    Maps maps;
+    Params prm;
+    const int32_t st = prepare_step(q, k_pool, v_pool, block_table, max_blocks, cu_seqlens_q, ctx_lens,
+                                    B, T, max_ctx, items, n_items, out, shape, err_flag, &maps, &prm);
+    if (st) return st;
+    point_workspace(&prm, static_cast<float*>(partials), T, shape->num_q_heads, shape->head_dim);
+    const int32_t combined = partials ? max_ctx : std::min(max_ctx, kSplit);
+    if (shape->head_dim == 128) return launch<128, false>(maps, prm, combined, stream);
+    return launch<64, false>(maps, prm, combined, stream);
+}
+
 extern "C" int32_t paged_attention_step_lse(const void* q, const void* k_pool, const void* v_pool,
                                             const int32_t* block_table, int32_t max_blocks,
                                             const int32_t* cu_seqlens_q, const int32_t* ctx_lens,

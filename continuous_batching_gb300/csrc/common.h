@@ -9,7 +9,50 @@
 // Rows of every tile-routine MMA (M): (query token, head-in-group) pairs of one KV head.
 #define PA_ROWS 128
 
+// The 4-bit cache's rows that are read from the codes (q4.cu): warps of a CTA, and CTAs (so lists of the
+// plan) with up to 8 and up to 16 rows an item, three and two a multiprocessor.
+#define PA_Q4_WARPS 4
+// Most rows (query tokens times heads of a group) of a sequence that are faster read from the codes.
+#define PA_Q4_DIRECT_ROWS 64
+#define PA_Q4_LISTS_8 (3 * PA_PLAN_CTAS)
+#define PA_Q4_LISTS_16 (2 * PA_PLAN_CTAS)
+
 namespace pa_detail {
+
+// Keys of a split of a row read from the codes, by its sequence's context alone: short ones where there
+// are few, so that a single sequence spreads over the GPU, and longer ones where the parts' own
+// bytes (a split's result is written and read once more) would add up. A multiple of 128.
+__host__ __device__ constexpr int64_t q4_split_keys(int32_t ctx) {
+    return ctx <= 4096 ? 512 : ctx <= 32768 ? 1024 : 2048;
+}
+// The longest context of one split.
+constexpr int64_t q4_one_split() { return 512; }
+// Most splits of any context up to max_ctx.
+inline int64_t q4_max_splits(int64_t max_ctx) {
+    const auto n = [](int64_t c) { return c <= 0 ? 1 : (c + q4_split_keys(int32_t(c)) - 1) / q4_split_keys(int32_t(c)); };
+    int64_t most = n(max_ctx);
+    if (max_ctx > 4096 && n(4096) > most) most = n(4096);
+    if (max_ctx > 32768 && n(32768) > most) most = n(32768);
+    return most;
+}
+
+// Where the parts of a plan's words begin (see pa_q4_plan).
+struct Q4Words {
+    int64_t direct, fold, chunk, expand, table, total;
+};
+inline Q4Words q4_words(const pa_q4_plan& p) {
+    constexpr int64_t item = sizeof(pa_work_item) / 4;
+    Q4Words w;
+    w.direct = 0;
+    w.fold = w.direct + item * p.n_direct;
+    w.chunk = w.fold + p.n_fold;
+    w.expand = w.chunk + item * p.n_chunk;
+    w.table = w.expand + 2 * int64_t(p.n_expand);
+    w.total = w.table + int64_t(p.n_chunk > 0 ? p.B : 0) * p.expand_cols;
+    return w;
+}
+// PA_OK, or what is wrong with a plan's sizes.
+int32_t check_q4_plan(const pa_shape* shape, const pa_q4_plan& p);
 
 // Records a failed CUDA call for pa_last_cuda_error(); returns PA_OK or PA_ERR_CUDA.
 int32_t note_cuda(cudaError_t e);
@@ -27,5 +70,14 @@ int32_t attention_step_stats(const void* q, const void* k_pool, const void* v_po
                              void* workspace, size_t ws_bytes, void* out, float* lse,
                              float* scores, int64_t scores_ld, const pa_shape* shape,
                              int32_t* err_flag, cudaStream_t stream);
+
+// paged_attention_step over the contexts that a 4-bit step has expanded (attention.cu). partials: as the
+// workspace of paged_attention_step, or NULL where no single token is among the rows.
+int32_t attention_step_expanded(const void* q, const void* k_pool, const void* v_pool,
+                                const int32_t* block_table, int32_t max_blocks,
+                                const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t B,
+                                int32_t T, int32_t max_ctx, const pa_work_item* items,
+                                int32_t n_items, void* partials, void* out, const pa_shape* shape,
+                                int32_t* err_flag, cudaStream_t stream);
 
 }  // namespace pa_detail

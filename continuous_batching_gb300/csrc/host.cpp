@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <new>
 #include <unordered_map>
 #include <vector>
 
@@ -456,11 +457,12 @@ void plain_items(const pa_shape* shape, int32_t s, int32_t q0, int32_t n, int32_
 // items (n_q == 0) take indices G .. PA_PLAN_CTAS - 1, so that the CTAs past the lists find
 // no work.
 int32_t deal(const std::vector<pa_work_item>& out, const std::vector<Unit>& units,
-             pa_work_item* items, int32_t max_items, int32_t* n_items) {
+             pa_work_item* items, int32_t max_items, int32_t* n_items,
+             int32_t lists = PA_PLAN_CTAS) {
     const int32_t n = int32_t(out.size());
     const int32_t nu = int32_t(units.size());
-    const int32_t G = std::min<int32_t>(nu, PA_PLAN_CTAS);
-    const int32_t pad = G < std::min<int32_t>(n, PA_PLAN_CTAS) ? PA_PLAN_CTAS - G : 0;
+    const int32_t G = std::min<int32_t>(nu, lists);
+    const int32_t pad = G < std::min<int32_t>(n, lists) ? lists - G : 0;
     if (int64_t(n) + pad > max_items) return PA_ERR_INVALID;
     // by decreasing cost, ties in generation order (a stable counting sort when it is small)
     int64_t max_cost = 0;
@@ -478,20 +480,20 @@ int32_t deal(const std::vector<pa_work_item>& out, const std::vector<Unit>& unit
             return units[size_t(x)].cost > units[size_t(y)].cost;
         });
     }
-    // a binary min-heap of keys cost * 256 + list (G <= 256), so that equal costs order by list
-    static_assert(PA_PLAN_CTAS <= 256, "list index must fit the heap key's low byte");
+    // a binary min-heap of keys cost * 1024 + list (G <= 1024), so that equal costs order by list
+    static_assert(PA_Q4_LISTS_8 <= 1024, "list index must fit the heap key's low bits");
     std::vector<uint64_t> heap(static_cast<size_t>(G));
     for (int32_t c = 0; c < G; ++c) heap[size_t(c)] = uint64_t(c);   // ascending: a heap
     std::vector<int32_t> owner(static_cast<size_t>(n)), rank(static_cast<size_t>(n));
     std::vector<int32_t> len(static_cast<size_t>(G), 0);
     for (int32_t j = 0; j < nu && G > 0; ++j) {
         const Unit& u = units[size_t(by_cost[size_t(j)])];
-        const int32_t c = int32_t(heap[0] & 255u);
+        const int32_t c = int32_t(heap[0] & 1023u);
         for (int32_t k = 0; k < u.count; ++k) {
             owner[size_t(u.first + k)] = c;
             rank[size_t(u.first + k)] = len[size_t(c)]++;
         }
-        uint64_t key = heap[0] + uint64_t(u.cost) * 256u;
+        uint64_t key = heap[0] + uint64_t(u.cost) * 1024u;
         size_t k = 0;                                                // sift the root down
         for (;;) {
             size_t m = 2 * k + 1;
@@ -669,6 +671,272 @@ int32_t pa_upload_block_table(const pa_shape* shape, const int32_t* host, int32_
     if (!dev) return PA_ERR_INVALID;
     return note_cuda(cudaMemcpyAsync(dev, host, size_t(n) * sizeof(int32_t),
                                      cudaMemcpyHostToDevice, stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------- the plan of a step over a 4-bit cache
+
+namespace {
+
+// What a step needs of a plan; fills it where items is given.
+struct Q4Parts {
+    std::vector<pa_work_item> direct, chunk;
+    std::vector<Unit> direct_units, chunk_units;
+    std::vector<int32_t> list;              // (sequence, 128-token block) of the expanded contexts
+    int32_t tiles_folded = 0;
+};
+
+int32_t q4_tile_rows(int32_t direct_rows) { return direct_rows > 8 ? 16 : 8; }
+
+int32_t q4_parts(const pa_shape* shape, int32_t B, const int32_t* cu, const int32_t* ctx,
+                 int32_t direct_rows, Q4Parts& out) {
+    const int32_t g = shape->num_q_heads / shape->num_kv_heads;
+    const int32_t tokens = q4_tile_rows(direct_rows) / g;       // of a tile read from the codes
+    for (int32_t s = 0; s < B; ++s) {
+        const int32_t n = cu[s + 1] - cu[s];
+        if (n == 0) continue;
+        if (int64_t(n) * g > direct_rows) {
+            const int32_t rpt = PA_ROWS / g;
+            for (int32_t t0 = 0; t0 < n; t0 += rpt)
+                plain_items(shape, s, cu[s], n, t0, std::min(rpt, n - t0), ctx, 0, out.chunk,
+                            out.chunk_units);
+            for (int64_t b = 0; b < blocks_for(ctx[s], 128); ++b) {
+                out.list.push_back(s);
+                out.list.push_back(int32_t(b));
+            }
+            continue;
+        }
+        const int64_t len = q4_split_keys(ctx[s]);
+        for (int32_t t0 = 0; t0 < n; t0 += tokens) {
+            const int32_t nt = std::min(tokens, n - t0);
+            const int64_t keys = int64_t(ctx[s]) - n + t0 + nt;
+            const int32_t splits = int32_t((keys + len - 1) / len);
+            out.tiles_folded += splits > 1;
+            if (int64_t(out.direct.size()) + int64_t(splits) * shape->num_kv_heads > (int64_t(1) << 26))
+                return PA_ERR_SHAPE;
+            for (int32_t h = 0; h < shape->num_kv_heads; ++h) {
+                const int32_t base = int32_t(out.direct.size());
+                for (int32_t sp = 0; sp < splits; ++sp) {
+                    const int64_t k = std::min(keys - sp * len, len);
+                    pa_work_item it{};
+                    it.seq = s;
+                    it.q_start = cu[s] + t0;
+                    it.n_q = nt;
+                    it.kv_head = h;
+                    it.split = sp;
+                    it.n_tiles = int32_t((k + PA_TILE_KEYS - 1) / PA_TILE_KEYS);
+                    it.n_splits = splits;
+                    it.kind = PA_ITEM_DIRECT;
+                    it.tile0 = base;
+                    // 128 keys are one tile of each warp; an item's start and join cost about two
+                    out.direct_units.push_back({base + sp, 1, int64_t(it.n_tiles) + 2});
+                    out.direct.push_back(it);
+                }
+            }
+        }
+    }
+    if (out.list.size() / 2 > size_t(INT32_MAX) / 128) return PA_ERR_SHAPE;
+    return PA_OK;
+}
+
+// The host memory of a plan or a table may run out: an error, never an exception through a C entry.
+template <class F>
+int32_t guarded(F f) {
+    try {
+        return f();
+    } catch (const std::bad_alloc&) {
+        return PA_ERR_OOM;
+    }
+}
+
+int32_t q4_finish(pa_q4_plan* p) {
+    const int64_t words = q4_words(*p).total;
+    if (words > INT32_MAX) return PA_ERR_SHAPE;
+    p->words = int32_t(words);
+    return PA_OK;
+}
+
+}  // namespace
+
+int32_t pa_detail::check_q4_plan(const pa_shape* shape, const pa_q4_plan& p) {
+    const int32_t g = shape->num_q_heads / shape->num_kv_heads;
+    if (p.B < 0 || p.T < 0 || p.max_ctx < 0 || p.direct_rows < 0 || p.n_direct < 0 || p.n_fold < 0 ||
+        p.n_chunk < 0 || p.n_expand < 0 || p.expand_cols < 0)
+        return PA_ERR_INVALID;
+    if (p.n_direct > 0 && p.direct_rows < g) return PA_ERR_INVALID;
+    if (p.n_fold > p.n_direct || (p.n_chunk > 0) != (p.n_expand > 0) ||
+        (p.n_chunk > 0 && p.expand_cols == 0))
+        return PA_ERR_INVALID;
+    if (int64_t(p.n_expand) * 128 > INT32_MAX) return PA_ERR_SHAPE;
+    return q4_words(p).total == p.words ? PA_OK : PA_ERR_INVALID;
+}
+
+extern "C" {
+
+int32_t pa_q4_max_direct_rows(void) { return PA_Q4_DIRECT_ROWS; }
+
+int32_t pa_q4_direct_rows(const pa_shape* shape, int32_t max_new) {
+    if (check_shape(shape) || max_new < 1) return 0;
+    const int64_t g = shape->num_q_heads / shape->num_kv_heads, rows = max_new * g;
+    return rows <= 8 ? 8 : rows <= PA_Q4_DIRECT_ROWS ? PA_Q4_DIRECT_ROWS : g <= 8 ? 8 : 16;
+}
+
+int32_t pa_q4_plan_size(const pa_shape* shape, int32_t B, const int32_t* cu, const int32_t* ctx,
+                        int32_t direct_rows, pa_q4_plan* plan) {
+    return guarded([&]() -> int32_t {
+    int32_t st = check_shape(shape);
+    if (st) return st;
+    if ((st = check_step_meta(B, cu, ctx))) return st;
+    if (!plan || direct_rows < 0) return PA_ERR_INVALID;
+    Q4Parts parts;
+    if ((st = q4_parts(shape, B, cu, ctx, direct_rows, parts))) return st;
+    pa_q4_plan p{};
+    p.B = B;
+    p.T = B > 0 ? cu[B] : 0;
+    for (int32_t s = 0; s < B; ++s) p.max_ctx = std::max(p.max_ctx, ctx[s]);
+    p.direct_rows = direct_rows;
+    p.n_direct = int32_t(parts.direct.size());
+    p.n_fold = parts.tiles_folded * shape->num_kv_heads;
+    p.n_chunk = int32_t(parts.chunk.size());
+    p.n_expand = int32_t(parts.list.size() / 2);
+    p.expand_cols = p.n_chunk > 0 ? int32_t(blocks_for(p.max_ctx, 128)) : 0;
+    if ((st = q4_finish(&p))) return st;
+    *plan = p;
+    return PA_OK;
+    });
+}
+
+int32_t pa_q4_plan_limits(const pa_shape* shape, int32_t B, int32_t T, int32_t max_ctx,
+                          int32_t direct_rows, int32_t max_expand, pa_q4_plan* plan) {
+    int32_t st = check_shape(shape);
+    if (st) return st;
+    if (!plan || B < 0 || T < 0 || max_ctx < 0 || direct_rows < 0 || max_expand < 0) return PA_ERR_INVALID;
+    pa_q4_plan p{};
+    p.B = B;
+    p.T = T;
+    p.max_ctx = max_ctx;
+    p.direct_rows = direct_rows;
+    const int32_t g = shape->num_q_heads / shape->num_kv_heads;
+    const int64_t tokens = q4_tile_rows(direct_rows) / g;
+    if (direct_rows >= g && tokens > 0) {
+        const int64_t per_seq = (direct_rows / g + tokens - 1) / tokens;
+        const int64_t tiles = std::min<int64_t>(T, B * per_seq);
+        const int64_t splits = q4_max_splits(max_ctx), heads = tiles * shape->num_kv_heads;
+        if (heads * splits > (int64_t(1) << 26)) return PA_ERR_SHAPE;
+        p.n_direct = int32_t(heads * splits);
+        p.n_fold = splits > 1 ? int32_t(heads) : 0;
+    }
+    if (max_expand > 0 && T > 0 && max_ctx > 0) {
+        if (max_expand > INT32_MAX / 128) return PA_ERR_SHAPE;
+        const int64_t items = pa_plan_max_items(shape, B, T, max_ctx);
+        if (items > (int64_t(1) << 26)) return PA_ERR_SHAPE;
+        p.n_chunk = int32_t(items);
+        p.n_expand = max_expand;
+        p.expand_cols = int32_t(blocks_for(max_ctx, 128));
+    }
+    if ((st = q4_finish(&p))) return st;
+    *plan = p;
+    return PA_OK;
+}
+
+int32_t pa_plan_step_q4(const pa_shape* shape, int32_t B, const int32_t* cu, const int32_t* ctx,
+                        const pa_q4_plan* plan, int32_t* words) {
+    return guarded([&]() -> int32_t {
+    int32_t st = check_shape(shape);
+    if (st) return st;
+    if ((st = check_step_meta(B, cu, ctx))) return st;
+    if (!plan) return PA_ERR_INVALID;
+    if ((st = check_q4_plan(shape, *plan))) return st;
+    if (plan->words > 0 && !words) return PA_ERR_INVALID;
+    if (B != plan->B || (B > 0 ? cu[B] : 0) != plan->T) return PA_ERR_INVALID;
+    for (int32_t s = 0; s < B; ++s)
+        if (ctx[s] > plan->max_ctx) return PA_ERR_INVALID;
+    Q4Parts parts;
+    if ((st = q4_parts(shape, B, cu, ctx, plan->direct_rows, parts))) return st;
+    if (int64_t(parts.direct.size()) > plan->n_direct || int64_t(parts.chunk.size()) > plan->n_chunk ||
+        int64_t(parts.list.size() / 2) > plan->n_expand ||
+        int64_t(parts.tiles_folded) * shape->num_kv_heads > plan->n_fold)
+        return PA_ERR_INVALID;
+    if (plan->words == 0) return PA_OK;
+    std::memset(words, 0, size_t(plan->words) * 4);             // items with n_q == 0: padding
+    const Q4Words at = q4_words(*plan);
+    auto* direct = reinterpret_cast<pa_work_item*>(words + at.direct);
+    auto* chunk = reinterpret_cast<pa_work_item*>(words + at.chunk);
+    int32_t n = 0;
+    if ((st = deal(parts.direct, parts.direct_units, direct, plan->n_direct, &n,
+                   plan->direct_rows > 8 ? PA_Q4_LISTS_16 : PA_Q4_LISTS_8)))
+        return st;
+    int32_t k = 0;
+    for (int32_t i = 0; i < n; ++i)
+        if (direct[i].split == 0 && direct[i].n_splits > 1) words[at.fold + k++] = i;
+    while (k < plan->n_fold) words[at.fold + k++] = -1;
+    if ((st = deal(parts.chunk, parts.chunk_units, chunk, plan->n_chunk, &n))) return st;
+    if (plan->n_chunk == 0) return PA_OK;
+    const int32_t used = int32_t(parts.list.size() / 2);
+    for (int32_t i = 0; i < 2 * plan->n_expand; ++i)
+        words[at.expand + i] = i < 2 * used ? parts.list[size_t(i)] : -1;
+    for (int64_t i = at.table; i < at.total; ++i) words[i] = -1;
+    for (int32_t i = 0; i < used; ++i)
+        words[at.table + int64_t(parts.list[size_t(2 * i)]) * plan->expand_cols +
+              parts.list[size_t(2 * i + 1)]] = i;
+    return PA_OK;
+    });
+}
+
+// ------------------------------------------------------------- compaction and size of a pool
+
+int32_t pa_alloc_compact(pa_allocator* a, int32_t* pairs, int32_t max_pairs, int32_t* n_pairs) {
+    return guarded([&]() -> int32_t {
+    if (!a || !n_pairs || max_pairs < 0) return PA_ERR_INVALID;
+    const int32_t live = a->num_blocks - int32_t(a->free_stack.size());
+    std::vector<int32_t> from, to, place(size_t(a->num_blocks), -1);
+    for (int32_t b = 0; b < a->num_blocks; ++b) {
+        if (b < live && a->ref[b] == 0) to.push_back(b);
+        if (b >= live && a->ref[b] > 0) from.push_back(b);
+    }
+    if (from.size() != to.size()) return PA_ERR_INCONSISTENT;
+    const int32_t n = int32_t(from.size());
+    // a block that something other than a table refers to cannot be renamed behind its back
+    std::vector<int32_t> refs(size_t(a->num_blocks), 0);
+    for (const auto& kv : a->tables)
+        for (int32_t b : kv.second) ++refs[size_t(b)];
+    for (int32_t b : from)
+        if (refs[size_t(b)] != a->ref[b]) return PA_ERR_STATE;
+    *n_pairs = n;
+    if (n > max_pairs || (n > 0 && !pairs)) return PA_ERR_INVALID;
+    for (int32_t i = 0; i < n; ++i) {
+        pairs[2 * i] = from[size_t(i)];
+        pairs[2 * i + 1] = to[size_t(i)];
+        place[size_t(from[size_t(i)])] = to[size_t(i)];
+        a->ref[to[size_t(i)]] = a->ref[from[size_t(i)]];
+        a->ref[from[size_t(i)]] = 0;
+    }
+    for (auto& kv : a->tables)
+        for (int32_t& b : kv.second)
+            if (place[size_t(b)] >= 0) b = place[size_t(b)];
+    a->free_stack.clear();
+    for (int32_t b = a->num_blocks - 1; b >= live; --b) a->free_stack.push_back(b);
+    return PA_OK;
+    });
+}
+
+int32_t pa_alloc_resize(pa_allocator* a, int32_t num_blocks) {
+    return guarded([&]() -> int32_t {
+    if (!a || num_blocks < 0) return PA_ERR_INVALID;
+    for (int32_t b = num_blocks; b < a->num_blocks; ++b)
+        if (a->ref[b] > 0) return PA_ERR_STATE;
+    std::vector<int32_t> stack;
+    stack.reserve(size_t(num_blocks));
+    a->ref.reserve(size_t(num_blocks));
+    for (int32_t b = num_blocks - 1; b >= a->num_blocks; --b) stack.push_back(b);   // below the others
+    for (int32_t b : a->free_stack)
+        if (b < num_blocks) stack.push_back(b);
+    a->free_stack.swap(stack);
+    a->ref.resize(size_t(num_blocks), 0);
+    a->num_blocks = num_blocks;
+    return PA_OK;
+    });
 }
 
 }  // extern "C"

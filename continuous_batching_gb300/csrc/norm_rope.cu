@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "q4.h"
 #include "sm103.h"
 
 using namespace pa_detail;
@@ -55,6 +56,7 @@ struct RopeParams {
     int32_t* err;
     int32_t T, Hq, Hkv, n_pairs, n_axes;
     int32_t warps;                             // per token
+    int32_t bs;                                // tokens a block (4-bit pools)
     float eps, k_scale, v_scale;
 };
 
@@ -73,9 +75,11 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* x, float s) {
 }
 
 enum Kind { kQ, kK, kV };
+enum Cache { kBf16, kFp8, kQ4 };               // what the pools hold
 
-template <int D, bool INTER, bool F8>
+template <int D, bool INTER, Cache C>
 __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeParams p) {
+    constexpr bool F8 = C == kFp8;
     constexpr int kLanes = D / 8;              // lanes per head
     constexpr int kHeads = 32 / kLanes;        // heads a warp has at a time: a round
     // the attention kernel that follows waits for this grid before it reads anything; this one
@@ -235,6 +239,38 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeParams
                         yb = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
                     }
                 }
+                if constexpr (C == kQ4 && K != kQ) {
+                    // The row goes to the lanes in column order, lane l columns 8 l .. 8 l + 7: of the
+                    // rotated columns the first halves lie in the lanes' first pieces and the second
+                    // ones in their second pieces.
+                    uint32_t w[4] = {ya.x, ya.y, yb.x, yb.y};
+                    if constexpr (!INTER) {
+                        const int half = p.n_pairs / 4;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int piece = 2 * l + i;
+                            const bool second = piece < half ? false
+                                                : piece < 2 * half ? true : i == 1;
+                            const int from = piece < half ? piece
+                                             : piece < 2 * half ? piece - half : l;
+                            const uint32_t x0 = __shfl_sync(0xffffffffu, ya.x, from, kLanes);
+                            const uint32_t x1 = __shfl_sync(0xffffffffu, ya.y, from, kLanes);
+                            const uint32_t y0 = __shfl_sync(0xffffffffu, yb.x, from, kLanes);
+                            const uint32_t y1 = __shfl_sync(0xffffffffu, yb.y, from, kLanes);
+                            w[2 * i] = second ? y0 : x0;
+                            w[2 * i + 1] = second ? y1 : x1;
+                        }
+                    }
+                    uint32_t codes, params;
+                    q4_quantise8(w, codes, params);
+                    if constexpr (K == kV) codes = q4_pair_groups(codes, l);
+                    if (h >= heads) continue;
+                    const int block = slot / p.bs;
+                    q4_store_row<D, K == kV>(static_cast<uint8_t*>(K == kV ? p.v_pool : p.k_pool),
+                                             q4_base<D>(block, p.Hkv, h, p.bs), p.bs,
+                                             slot - block * p.bs, l, codes, params);
+                    continue;
+                }
                 if (h >= heads) continue;
                 const int64_t at = (row + h) * D;
                 if constexpr (F8 && K != kQ) {
@@ -271,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeParams
         max(r0 - rq - rk, 0), min(r1 - rq - rk, rk));
 }
 
-template <int D, bool INTER, bool F8>
+template <int D, bool INTER, Cache C>
 int32_t launch_rope(RopeParams& p, cudaStream_t stream) {
     constexpr int kHeads = 256 / D;            // heads a warp has at a time
     // Warps per token: few, so that each has kMaxRounds rounds of heads to its sines, unless there
@@ -292,7 +328,7 @@ int32_t launch_rope(RopeParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return note_cuda(cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, INTER, F8>, p));
+    return note_cuda(cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, INTER, C>, p));
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -301,7 +337,7 @@ int32_t norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stri
                   int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
                   const pa_rope_pair* rope, int32_t n_pairs, int32_t interleaved,
                   const int32_t* positions, int32_t n_axes, const int32_t* slot_mapping, int32_t T,
-                  void* q_out, void* k_pool, void* v_pool, bool fp8, float k_scale, float v_scale,
+                  void* q_out, void* k_pool, void* v_pool, Cache cache, float k_scale, float v_scale,
                   const pa_shape* shape, int32_t* err_flag, cudaStream_t stream) {
     int32_t st = check_shape(shape);
     if (st) return st;
@@ -345,17 +381,16 @@ int32_t norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stri
     p.eps = eps;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    const bool inter = interleaved != 0;
-    if (D == 128) {
-        if (fp8) return inter ? launch_rope<128, true, true>(p, stream)
-                              : launch_rope<128, false, true>(p, stream);
-        return inter ? launch_rope<128, true, false>(p, stream)
-                     : launch_rope<128, false, false>(p, stream);
-    }
-    if (fp8) return inter ? launch_rope<64, true, true>(p, stream)
-                          : launch_rope<64, false, true>(p, stream);
-    return inter ? launch_rope<64, true, false>(p, stream)
-                 : launch_rope<64, false, false>(p, stream);
+    p.bs = shape->block_size;
+    const auto launch = [&](auto held) {
+        constexpr Cache C = decltype(held)::value;
+        if (D == 128)
+            return interleaved ? launch_rope<128, true, C>(p, stream) : launch_rope<128, false, C>(p, stream);
+        return interleaved ? launch_rope<64, true, C>(p, stream) : launch_rope<64, false, C>(p, stream);
+    };
+    if (cache == kFp8) return launch(std::integral_constant<Cache, kFp8>());
+    if (cache == kQ4) return launch(std::integral_constant<Cache, kQ4>());
+    return launch(std::integral_constant<Cache, kBf16>());
 }
 
 }  // namespace
@@ -405,7 +440,7 @@ extern "C" int32_t paged_qk_norm_rope_write(
     int32_t n_axes, const int32_t* slot_mapping, int32_t T, void* q_out, void* k_pool,
     void* v_pool, const pa_shape* shape, int32_t* err_flag, pa_stream_t stream) {
     return norm_rope(q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, rope, n_pairs,
-                     interleaved, positions, n_axes, slot_mapping, T, q_out, k_pool, v_pool, false,
+                     interleaved, positions, n_axes, slot_mapping, T, q_out, k_pool, v_pool, kBf16,
                      1.f, 1.f, shape, err_flag, stream);
 }
 
@@ -419,6 +454,17 @@ extern "C" int32_t paged_qk_norm_rope_write_fp8(
     if (!(k_scale > 0.f) || !(v_scale > 0.f) || !(k_scale < INFINITY) || !(v_scale < INFINITY))
         return PA_ERR_INVALID;
     return norm_rope(q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, rope, n_pairs,
-                     interleaved, positions, n_axes, slot_mapping, T, q_out, k_pool, v_pool, true,
+                     interleaved, positions, n_axes, slot_mapping, T, q_out, k_pool, v_pool, kFp8,
                      k_scale, v_scale, shape, err_flag, stream);
+}
+
+extern "C" int32_t paged_qk_norm_rope_write_q4(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+    const pa_rope_pair* rope, int32_t n_pairs, int32_t interleaved, const int32_t* positions,
+    int32_t n_axes, const int32_t* slot_mapping, int32_t T, void* q_out, void* k_pool,
+    void* v_pool, const pa_shape* shape, int32_t* err_flag, pa_stream_t stream) {
+    return norm_rope(q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, rope, n_pairs,
+                     interleaved, positions, n_axes, slot_mapping, T, q_out, k_pool, v_pool, kQ4,
+                     1.f, 1.f, shape, err_flag, stream);
 }

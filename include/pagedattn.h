@@ -123,6 +123,9 @@ typedef struct pa_work_item {
 #define PA_ITEM_PLAIN 0
 #define PA_ITEM_GROUP 1
 #define PA_ITEM_RESUME 2
+/* Of a 4-bit step (pa_plan_step_q4): a tile of query rows read from the codes, one split of a length
+ * of its own; n_splits counts the tile's splits, tile0 is the item's place among their results. */
+#define PA_ITEM_DIRECT 3
 
 /* ---------------------------------------------------------------- library ---------- */
 
@@ -191,6 +194,20 @@ int32_t pa_alloc_fork(pa_allocator* a, int32_t src, int32_t dst);
  * nothing changes then. */
 int32_t pa_alloc_cow(pa_allocator* a, int32_t seq, int32_t start, int32_t n, int32_t* pairs,
                      int32_t max_pairs, int32_t* n_pairs);
+
+/* Compaction: the live blocks with ids past the number of live blocks move, in ascending order, to
+ * the free ids below it, every table follows, and the (old, new) pairs are returned in pairs[2 k],
+ * pairs[2 k + 1] (host, up to max_pairs, count in *n_pairs). Afterwards the live blocks are
+ * 0 .. n_live - 1 and the lowest free id is the next one handed out. The caller copies the pages of every
+ * layer (paged_copy_pages) before anything that uses the new tables, and builds metadata afresh: what was built
+ * before names the old ids. No page is source and destination at once. Nothing changes on an error:
+ * PA_ERR_INVALID if max_pairs is too small (*n_pairs then holds the count needed), PA_ERR_STATE if
+ * a block that would move is referenced by something other than tables (pa_alloc_block,
+ * pa_alloc_incref), PA_ERR_OOM without host memory. */
+int32_t pa_alloc_compact(pa_allocator* a, int32_t* pairs, int32_t max_pairs, int32_t* n_pairs);
+/* Changes the number of blocks: a pool's tail is given up (PA_ERR_STATE if a block in it is live:
+ * nothing changes), or new blocks are added, handed out after those that are free now. */
+int32_t pa_alloc_resize(pa_allocator* a, int32_t num_blocks);
 
 /* PA_OK if free + referenced == total, the free list has no duplicates and every refcount
  * equals the references held by live tables; PA_ERR_INCONSISTENT otherwise. */
@@ -347,6 +364,23 @@ int32_t paged_kv_write(const void* k_new, const void* v_new, const int32_t* slot
  * launches nothing. Order it before the step's paged_kv_write on the same stream. */
 int32_t paged_copy_blocks(const int32_t* pairs, int32_t n_pairs, void* k_pool, void* v_pool,
                           const pa_shape* shape, int32_t* err_flag, pa_stream_t stream);
+
+/* One pool of pages: page_bytes bytes for each of its blocks, block b at pool + b * page_bytes. */
+typedef struct pa_pages {
+    void* pool;             /* device, 16-byte aligned */
+    int64_t page_bytes;     /* > 0, a multiple of 16 */
+} pa_pages;
+
+/* Copies pages in every pool given, of any element type: for k in [0, n_pairs) and each of the
+ * n_pools pools, the bytes of page pairs[2k] to page pairs[2k + 1]. One launch for up to 128 pools (the K and V
+ * of 64 layers). Order: as paged_copy_blocks; for pairs of pa_alloc_cow and pa_alloc_compact.
+ * Device: pairs [2 * n_pairs] int32. Host: pools [n_pools] (read before the call returns). Pages are
+ * copied at the same time: destinations are distinct and none is a source of the call (a page that breaks this
+ * is left with a mixture). A pair with an id outside [0, num_blocks) or equal ids is skipped and
+ * sets PA_DEVERR_BLOCK. */
+int32_t paged_copy_pages(const int32_t* pairs, int32_t n_pairs, const pa_pages* pools,
+                         int32_t n_pools, int32_t num_blocks, int32_t* err_flag,
+                         pa_stream_t stream);
 
 /* Attention for one flat ragged step over an already-written pool (call paged_kv_write
  * first: ctx_lens count this step's tokens, P3 page "write new K/V, return [T, H, D]").
@@ -660,6 +694,101 @@ int32_t paged_evict(void* k_pool, void* v_pool, int32_t elem_bytes, const int32_
                     const int32_t* positions, int32_t* positions_out, int32_t n_rows,
                     int32_t max_len, const pa_shape* shape, int32_t* err_flag,
                     pa_stream_t stream);
+
+/* ------------------------------------------------------------------ 4-bit KV cache
+ * K and V held as 4-bit codes with a scale and a minimum (bf16) for every 32 columns of a token and
+ * head: 5 bits an element, 3.2 times the tokens of a bf16 pool. No counterpart on the pages (their
+ * "Review" names an fp8 cache only). A code u stands for scale * u + minimum.
+ *
+ * Pools: uint8 [num_blocks, Hkv, block_size * (D/2 + D/8)], 16-byte aligned. Per block and head, the
+ * code rows of the block's tokens (D/2 bytes each), then their parameter rows (D/8 bytes: per group of
+ * 32 columns scale, minimum). With G = D / 32, column 32 g + 8 c + n of a K row is nibble n of
+ * 32-bit word c G + g of its code row, column 32 g + 4 r + n of a V row nibble n of 16-bit word
+ * r G + g (little endian, nibble 0 lowest): the order of the tensor-core operands that the codes become.
+ * A token's bytes are its own.
+ *
+ * Write: minimum = min x, scale = bf16((max x - min x) / 15), u = clamp(rint((x - minimum) / scale), 0, 15)
+ * with fp32 subtractions and divisions (all u 0 where the scale is 0), so that a value is off by at most
+ * 0.54 of a scale. A group that holds a NaN or an infinity, or whose range passes fp32, reads as 32 NaNs.
+ * Arguments as paged_kv_write, plus strides: k_new, v_new [T, Hkv, D] bf16 with k_stride, v_stride
+ * elements between tokens (multiples of 8, at least Hkv * D; heads and columns dense). */
+int32_t paged_kv_write_q4(const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                          const int32_t* slot_mapping, int32_t T, void* k_pool, void* v_pool,
+                          const pa_shape* shape, int32_t* err_flag, pa_stream_t stream);
+/* paged_qk_norm_rope_write into 4-bit pools: the bytes of paged_kv_write_q4 of the bf16 k it would have
+ * written, and of v. */
+int32_t paged_qk_norm_rope_write_q4(const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride,
+                                    const void* q_weight, const void* k_weight, float eps,
+                                    const pa_rope_pair* rope, int32_t n_pairs,
+                                    int32_t interleaved, const int32_t* positions, int32_t n_axes,
+                                    const int32_t* slot_mapping, int32_t T, void* q_out,
+                                    void* k_pool, void* v_pool, const pa_shape* shape,
+                                    int32_t* err_flag, pa_stream_t stream);
+/* The rows that a slot mapping names, in bf16 (scale * u + minimum, one rounding): k_out, v_out
+ * [T, Hkv, D] dense. A row whose slot is < 0 is left as it was; a slot outside the pool too, and sets
+ * PA_DEVERR_SLOT. */
+int32_t paged_kv_read_q4(const int32_t* slot_mapping, int32_t T, const void* k_pool,
+                         const void* v_pool, void* k_out, void* v_out, const pa_shape* shape,
+                         int32_t* err_flag, pa_stream_t stream);
+
+/* Sizes of a 4-bit step's plan. The plan itself is one array of `words` int32, made on the host by
+ * pa_plan_step_q4 and copied to the device by the caller. direct_rows parts the sequences: one whose
+ * n_q * group is at most direct_rows has its rows computed from the codes as they are (tiles of up to 8 rows
+ * where direct_rows <= 8, else 16); the context of any other is expanded to bf16 once, 128-token block by
+ * block, in the workspace, and its rows go through the kernel of paged_attention_step. pa_q4_direct_rows gives a fast choice. */
+typedef struct pa_q4_plan {
+    int32_t B, T, max_ctx;      /* sequences, query rows, bound of every context */
+    int32_t direct_rows;
+    int32_t n_direct;           /* items read from the codes */
+    int32_t n_fold;             /* (tile of rows, KV head) pairs of several splits among them */
+    int32_t n_chunk;            /* items over expanded contexts */
+    int32_t n_expand;           /* 128-token blocks expanded */
+    int32_t expand_cols;        /* columns of the table of expanded blocks */
+    int32_t words;
+} pa_q4_plan;
+
+/* The direct_rows that is fast for the largest number of query tokens, max_new, that the sequences of few
+ * tokens bring (1: decoding). Returns the number, 0 on bad arguments. */
+int32_t pa_q4_direct_rows(const pa_shape* shape, int32_t max_new);
+/* The most rows of a sequence for which that choice reads the codes (returns the number). */
+int32_t pa_q4_max_direct_rows(void);
+/* The sizes of one step's plan, exactly. */
+int32_t pa_q4_plan_size(const pa_shape* shape, int32_t B, const int32_t* cu_seqlens_q,
+                        const int32_t* ctx_lens, int32_t direct_rows, pa_q4_plan* plan);
+/* Sizes for every step of B sequences, T query rows, contexts up to max_ctx and at most max_expand
+ * expanded blocks of 128 tokens (0: no chunks): for a captured step, whose later plans are written over the
+ * first one's words. */
+int32_t pa_q4_plan_limits(const pa_shape* shape, int32_t B, int32_t T, int32_t max_ctx,
+                          int32_t direct_rows, int32_t max_expand, pa_q4_plan* plan);
+/* The plan of a step (host in, host out: words [plan->words]) under sizes from either call; what it
+ * does not use is padded. PA_ERR_INVALID if the step does not fit them. */
+int32_t pa_plan_step_q4(const pa_shape* shape, int32_t B, const int32_t* cu_seqlens_q,
+                        const int32_t* ctx_lens, const pa_q4_plan* plan, int32_t* words);
+/* Bytes of workspace of a step under these sizes (0 if it needs none). It holds nothing between calls;
+ * calls or graphs that may overlap need one each. */
+size_t pa_q4_workspace_bytes(const pa_shape* shape, const pa_q4_plan* plan);
+
+/* paged_attention_step over 4-bit pools. Rows read from the codes: exact products of q and the codes, fp32
+ * sums, the scales applied in fp32 (K is not rounded beyond its code), p * scale rounded to bf16, splits
+ * whose length depends on the sequence's context alone, joined in a fixed order. Rows over expanded
+ * contexts: K and V values rounded to bf16, otherwise as paged_attention_step (a NaN or infinity among the
+ * V of a later key of the chunk reaches the rows before it, as there; not so for rows read from the
+ * codes). A row's bits depend on its own query, keys, position and context, and on which of the two ways its
+ * sequence takes: with direct_rows 0 every row takes the second, and a token has the same bits as a
+ * single row and within a chunk.
+ * Device: words, the plan's; q, out [T, Hq, D] bf16; block_table [B, max_blocks], cu_seqlens_q, ctx_lens
+ * as planned (items that they contradict are skipped and set PA_DEVERR_META, their rows not written);
+ * keys of a block outside the pool read as 0 and set PA_DEVERR_BLOCK; workspace 16-byte aligned.
+ * Host checks: as paged_attention_step. Launches (programmatic dependents of what precedes them): the rows read
+ * from the codes, the join of their splits; the expansion, the attention over it and its combine; each only
+ * where the plan has sizes for it. */
+int32_t paged_attention_step_q4(const void* q, const void* k_pool, const void* v_pool,
+                                const int32_t* block_table, int32_t max_blocks,
+                                const int32_t* cu_seqlens_q, const int32_t* ctx_lens,
+                                const pa_q4_plan* plan, const int32_t* words, void* workspace,
+                                size_t ws_bytes, void* out, const pa_shape* shape,
+                                int32_t* err_flag, pa_stream_t stream);
 
 /* Allocation-free variant of paged_attention_step (no counterpart on the pages: it is a
  * deployment convenience of this library). Same arguments, meaning and result as

@@ -1,0 +1,526 @@
+"""The attention step over a 4-bit cache: the plan and the refusals on the CPU; on the GPU its outputs
+against the definition in 64 bits, bit for bit invariances, graphs, bad pages and metadata."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+import oracle.paged_attention as pa
+import oracle.q4 as q4
+from continuous_batching_gb300 import binding as bd
+from continuous_batching_gb300 import workloads as wl
+
+torch = pytest.importorskip("torch")
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def bf16(bits):
+    return dev(bits.view(np.int16)).view(torch.bfloat16)
+
+
+def bits_of(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+class Case:
+    """A step over pools whose unwritten bytes are NaN parameters: lens is [(rows, context)]."""
+
+    def __init__(self, lens, Hq=8, Hkv=2, D=128, bs=16, seed=0, spare=2, offset=0.0):
+        rng = np.random.default_rng(seed)
+        self.lens, self.Hq, self.Hkv, self.D, self.bs = lens, Hq, Hkv, D, bs
+        ctx = np.array([c for _, c in lens], np.int32)
+        self.ctx, self.cu = ctx, np.concatenate([[0], np.cumsum([n for n, _ in lens])]).astype(np.int32)
+        need = [-(-int(c) // bs) for c in ctx]
+        self.nb = sum(need) + spare
+        self.table = np.full((len(lens), max(max(need), 1) + 1), -1, np.int32)
+        order = rng.permutation(self.nb)
+        at = 0
+        for s, n in enumerate(need):
+            self.table[s, :n] = order[at:at + n]
+            at += n
+        self.shape = bd.Shape.make(Hq, Hkv, D, bs, self.nb)
+        self.T = int(self.cu[-1])
+        self.q = wl.random_bf16(rng, (self.T, Hq, D))
+        self.pools = []
+        for is_v in (False, True):
+            pool = np.full((self.nb, Hkv, bs * (D // 2 + D // 8)), 0xFF, np.uint8)
+            x = pa.bf16_to_f64(wl.random_bf16(rng, (int(ctx.sum()), Hkv, D)))
+            x = wl.f32_to_bf16_bits((x + offset * rng.standard_normal((1, Hkv, D))).astype(np.float32))
+            slots = np.concatenate([self.table[s][np.arange(c) // bs] * bs + np.arange(c) % bs for s, c in enumerate(ctx) if c] or [np.zeros(0, int)])
+            self.pools.append(q4.write(pool, x, slots, bs, is_v))
+
+    def rounded(self):
+        """K and V as bf16 (what a step over expanded contexts computes on), NaN bytes as 0."""
+        return [np.nan_to_num(pa.bf16_to_f64(q4._to_bf16_bits(q4.values(p, self.bs, self.D, i == 1)))) for i, p in enumerate(self.pools)]
+
+    def exact(self, k=None, v=None):
+        if k is None:
+            k, v = (np.nan_to_num(q4.values(p, self.bs, self.D, i == 1).astype(np.float64)) for i, p in enumerate(self.pools))
+        return pa.attention(pa.bf16_to_f64(self.q), k, v, self.table, self.cu, self.ctx, self.Hq)
+
+    def bound(self):
+        """How far an output of rows read from the codes may be off, per value. Three parts:
+        the output's rounding, 2^-8 of it; the rounding of p * scale to bf16, 2^-8 of each term p s |u - 8|;
+        and what fp32 does to a score: products and sums of a group stay below 144 sum |q| (codes as
+        128 + u), of which 2^-20 covers the sums of 32 products and four groups at 2^-23 each (a tensor core
+        may truncate), times the scale. A score off by e moves a weight by exp(e) - 1, and so the result by at most that
+        of twice the magnitudes (numerator and denominator)."""
+        k, v = self.pools
+        D, g = self.D, self.Hq // self.Hkv
+        out = np.abs(self.exact()) * 2.0 ** -8
+        q = pa.bf16_to_f64(self.q)
+        vals, cent, mag = (np.zeros((self.nb, self.bs, self.Hkv, D)) for _ in range(3))
+        ks = np.zeros((self.nb, self.bs, self.Hkv, D // 32))
+        for b in range(self.nb):
+            for h in range(self.Hkv):
+                pv = v[b, h, self.bs * (D // 2):].view("<u2").reshape(self.bs, D // 32, 2)
+                s, m = (np.nan_to_num(np.repeat(pa.bf16_to_f64(pv[..., i]), 32, -1)) for i in (0, 1))
+                c = v[b, h, :self.bs * (D // 2)].reshape(self.bs, D // 2)
+                u = np.stack([c & 15, c >> 4], -1).reshape(self.bs, D)[:, q4.column_nibble(D, True)].astype(float)
+                cent[b, :, h] = s * np.abs(u - 8)
+                mag[b, :, h] = cent[b, :, h] + np.abs(m + 8 * s)
+                ks[b, :, h] = np.nan_to_num(pa.bf16_to_f64(k[b, h, self.bs * (D // 2):].view("<u2").reshape(self.bs, D // 32, 2)[..., 0]))
+        kv = np.nan_to_num(q4.values(k, self.bs, D, False).astype(np.float64))
+        out += pa.attention(q, kv, cent, self.table, self.cu, self.ctx, self.Hq) * 2.0 ** -8
+        big = pa.attention(q, kv, mag, self.table, self.cu, self.ctx, self.Hq)
+        e = np.abs(q).reshape(self.T, self.Hq, D // 32, 32).sum(-1) @ np.full(D // 32, ks.max()) * 144 * 2.0 ** -20 / np.sqrt(D)
+        return out + 2 * np.expm1(2 * e)[..., None] * big + 2.0 ** -18 * big
+
+    def plan(self, direct_rows=None, limits=None):
+        return bd.pa_plan_step_q4(self.shape, self.cu, self.ctx, direct_rows, limits, device="cuda")
+
+    def run(self, direct_rows=None, plan=None, pools=None, table=None, cu=None, ctx=None, expect=0):
+        plan = plan or self.plan(direct_rows)
+        ws = torch.empty(bd.pa_q4_workspace_bytes(self.shape, plan) // 4 + 1, device="cuda")
+        ws.fill_(float("nan"))
+        out = torch.full((self.T, self.Hq, self.D), 9.0, dtype=torch.bfloat16, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        k, v = pools or [dev(p) for p in self.pools]
+        bd.paged_attention_step_q4(bf16(self.q), k, v, dev(self.table if table is None else table), dev(self.cu if cu is None else cu),
+                                   dev(self.ctx if ctx is None else ctx), plan, ws, out, self.shape, err=err)
+        assert int(err.item()) == expect
+        return bits_of(out)
+
+    def check_direct(self, direct_rows):
+        got = pa.bf16_to_f64(self.run(direct_rows))
+        far, most = np.abs(got - self.exact()), self.bound()
+        assert np.isfinite(got).all() and (far <= most).all(), float((far / np.maximum(most, 1e-30)).max())
+
+
+# ------------------------------------------------------------------------------------ plan
+
+def _items(words, at, n):
+    return words[at:at + n * bd.ITEM_INTS].view(bd.WORK_ITEM_DTYPE)
+
+
+def _split(ctx):
+    return 512 if ctx <= 4096 else 1024 if ctx <= 32768 else 2048
+
+
+@pytest.mark.parametrize("direct_rows", [0, 8, 16, 64])
+@pytest.mark.parametrize("Hq, Hkv", [(8, 8), (8, 2), (32, 2)])
+def test_plan_covers_every_row_once(direct_rows, Hq, Hkv):
+    rng = np.random.default_rng(direct_rows + Hq)
+    n_q = rng.integers(0, 40, 30)
+    n_q[:10] = 1
+    ctx = np.maximum(n_q, rng.integers(1, 9000, 30)).astype(np.int32)
+    ctx[3], ctx[4] = 33000, 0
+    n_q[4] = 0
+    cu = np.concatenate([[0], np.cumsum(n_q)]).astype(np.int32)
+    shape = bd.Shape.make(Hq, Hkv, 128, 16, 4)
+    g = Hq // Hkv
+    exact = bd.pa_plan_step_q4(shape, cu, ctx, direct_rows)
+    limits = bd.pa_q4_plan_limits(shape, 30, int(cu[-1]), 33000, direct_rows, 3000)
+    for plan in (exact, bd.pa_plan_step_q4(shape, cu, ctx, limits=limits)):
+        s, w = plan.sizes, plan.words
+        at = 0
+        direct = _items(w, 0, s.n_direct)
+        fold = w[s.n_direct * bd.ITEM_INTS:][:s.n_fold]
+        at = s.n_direct * bd.ITEM_INTS + s.n_fold
+        chunk = _items(w, at, s.n_chunk)
+        at += s.n_chunk * bd.ITEM_INTS
+        blocks = w[at:at + 2 * s.n_expand].reshape(-1, 2)
+        table = w[at + 2 * s.n_expand:s.words].reshape(30 if s.n_chunk else 0, s.expand_cols)
+        seen, places = {}, set()
+        lists = 3 * 152 if direct_rows <= 8 else 2 * 152
+        n_real = int((direct["n_q"] > 0).sum())
+        walked = set()
+        for c in range(min(lists, n_real)):
+            i = c
+            while True:
+                assert i not in walked and direct[i]["n_q"] > 0
+                walked.add(i)
+                if direct[i]["next"] <= 0:
+                    break
+                assert direct[i]["next"] > i
+                i = int(direct[i]["next"])
+        assert len(walked) == n_real and (direct[n_real:]["n_q"] == 0).all()
+        for i in range(n_real):
+            it = direct[i]
+            q = int(it["seq"])
+            keys = int(ctx[q] - cu[q + 1] + it["q_start"] + it["n_q"])
+            assert n_q[q] * g <= direct_rows and it["kind"] == bd.PA_ITEM_DIRECT and it["n_q"] * g <= (16 if direct_rows > 8 else 8)
+            assert it["n_splits"] == -(-keys // _split(ctx[q])) and 0 <= it["split"] < it["n_splits"]
+            place = int(it["tile0"] + it["split"])
+            assert place not in places and place < s.n_direct
+            places.add(place)
+            for t in range(it["q_start"], it["q_start"] + it["n_q"]):
+                seen.setdefault((t, int(it["kv_head"])), []).append(int(it["split"]))
+            assert (i in fold) == (it["split"] == 0 and it["n_splits"] > 1)
+        wide = [q for q in range(30) if n_q[q] * g > direct_rows]
+        for q in range(30):
+            nb = -(-int(ctx[q]) // 128)
+            if q in wide:
+                mine = [i for i in range(len(blocks)) if blocks[i, 0] == q]
+                assert blocks[mine, 1].tolist() == list(range(nb)) and table[q, :nb].tolist() == mine and (table[q, nb:] == -1).all()
+            else:
+                assert len(table) == 0 or (table[q] == -1).all()
+                for t in range(cu[q], cu[q + 1]):
+                    for h in range(Hkv):
+                        assert len(seen[t, h]) == max(seen[t, h]) + 1 == len(set(seen[t, h]))
+        assert {int(i["seq"]) for i in chunk if i["n_q"] > 0} == set(wide)
+
+
+def test_plan_refuses():
+    shape = bd.Shape.make(8, 2, 128, 16, 64)
+    cu, ctx = np.array([0, 1, 31], np.int32), np.array([700, 90], np.int32)
+    lim = lambda **kw: bd.pa_q4_plan_limits(shape, **{**dict(B=2, T=31, max_ctx=700, direct_rows=8, max_expand=2), **kw})
+    bd.pa_plan_step_q4(shape, cu, ctx, limits=lim())
+    for bad in (dict(B=3), dict(T=32), dict(max_ctx=699), dict(max_expand=0)):
+        with pytest.raises(bd.PagedAttnError) as e:
+            bd.pa_plan_step_q4(shape, cu, ctx, limits=lim(**bad))
+        assert e.value.status == bd.PA_ERR_INVALID, bad
+    for bad in (dict(B=-1), dict(T=-1), dict(direct_rows=-1), dict(max_expand=-1)):
+        with pytest.raises(bd.PagedAttnError):
+            lim(**bad)
+    with pytest.raises(bd.PagedAttnError):
+        bd.pa_plan_step_q4(shape, np.array([0, 1, 100], np.int32), ctx, 8)      # more rows than context
+    s = lim()
+    s.words += 1                                          # sizes that are not one plan's
+    with pytest.raises(bd.PagedAttnError):
+        bd.pa_plan_step_q4(shape, cu, ctx, limits=s)
+
+
+def test_step_refuses():
+    lib, shape = bd.load(), bd.Shape.make(8, 2, 128, 16, 64)
+    sizes = bd.pa_plan_step_q4(shape, np.array([0, 1], np.int32), np.array([700], np.int32), 8).sizes
+    need = bd.pa_q4_workspace_bytes(shape, sizes)
+    assert need > 0
+
+    def call(q=4096, kp=4096, vp=4096, table=4096, mb=44, cu=4096, ctx=4096, sz=sizes, words=4096, ws=4096, n=need, out=4096, sh=shape):
+        return lib.paged_attention_step_q4(q, kp, vp, table, mb, cu, ctx, None if sz is None else C.byref(sz), words, ws, n, out, C.byref(sh), None, None)
+
+    for kw in (dict(q=None), dict(q=4104), dict(kp=None), dict(vp=4100), dict(table=None), dict(mb=-1), dict(cu=None), dict(ctx=None), dict(sz=None), dict(words=None), dict(out=None),
+               dict(out=4098), dict(ws=4100)):
+        assert call(**kw) == bd.PA_ERR_INVALID, kw
+    assert call(ws=None) == bd.PA_ERR_WORKSPACE and call(n=need - 1) == bd.PA_ERR_WORKSPACE
+    assert call(sh=bd.Shape.make(24, 2, 128, 16, 64)) == bd.PA_ERR_SHAPE
+    assert call(sh=bd.Shape.make(32, 2, 128, 16, 64)) == bd.PA_ERR_INVALID       # groups of 16 in tiles of 8
+    empty = bd.pa_plan_step_q4(shape, np.array([0, 0], np.int32), np.array([5], np.int32), 8).sizes
+    assert call(sz=empty, q=None, words=None) == bd.PA_OK
+    bad = bd.Q4Sizes.from_buffer_copy(sizes)
+    bad.n_direct = -1
+    assert call(sz=bad) == bd.PA_ERR_INVALID
+
+
+# ------------------------------------------------------------------------------------- GPU
+
+SHAPES = [(8, 8, 128, 16), (8, 4, 64, 8), (8, 2, 128, 32), (16, 2, 128, 128), (8, 1, 64, 64), (32, 2, 128, 16), (16, 1, 64, 16)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq, Hkv, D, bs", SHAPES)
+def test_single_rows_read_from_the_codes(Hq, Hkv, D, bs):
+    """Contexts around tiles, warps, splits and the places where the split's length changes."""
+    ctx = [1, 2, 8, 31, 32, 33, 127, 128, 129, 160, 511, 512, 513, 640, 1025, 4095, 4096, 4097, 5200]
+    Case([(1, c) for c in ctx], Hq, Hkv, D, bs, seed=Hq + D).check_direct(16)
+
+
+@pytest.mark.gpu
+def test_a_long_context():
+    Case([(1, 33000), (1, 32768), (3, 32769)], 8, 1, 128, 16, seed=5).check_direct(24)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq, Hkv, D, bs", SHAPES)
+def test_few_rows_read_from_the_codes(Hq, Hkv, D, bs):
+    """Several tokens per sequence: prompts of a few tokens, tiles with a part of the rows, a split that
+    begins between the rows' positions, sequences without rows among them."""
+    lens = [(2, 2), (3, 3), (5, 700), (1, 90), (0, 40), (4, 514), (7, 515), (0, 0), (2, 33), (6, 130), (8, 1027)]
+    Case(lens, Hq, Hkv, D, bs, seed=Hkv).check_direct(8 * max(Hq // Hkv, 2))
+
+
+@pytest.mark.gpu
+def test_keys_with_a_common_offset():
+    """Columns whose keys share a large offset: the minimum carries it, the codes the rest."""
+    Case([(1, 300), (2, 77)], seed=11, offset=6.0).check_direct(16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq, Hkv, D, bs", SHAPES)
+@pytest.mark.parametrize("direct_rows", [0, 16])
+def test_chunks_over_expanded_contexts(Hq, Hkv, D, bs, direct_rows):
+    """Chunks, and with direct_rows 0 single rows, against the definition on K and V rounded to bf16, as the bf16 step is tested."""
+    from tests.gpu_util import assert_close
+    c = Case([(70, 70), (1, 2500), (129, 700), (33, 2300), (0, 5), (1, 3), (40, 41)], Hq, Hkv, D, bs, seed=bs)
+    assert_close(c.run(direct_rows), c.exact(*c.rounded()), f"q4 chunks {Hq}/{Hkv}/{D} rows {direct_rows}")
+
+
+@pytest.mark.gpu
+def test_bits_do_not_depend_on_the_batch():
+    """A sequence alone, among others and in another place of pool and step; single tokens and the same rows
+    as drafted tokens (contexts whose splits have one length); tiles of 8 and of 16 rows."""
+    lens = [(1, 700), (4, 2500), (1, 5000), (2, 40), (3, 1500)]
+    a = Case(lens, seed=3)
+    for rows in (8, 16):
+        whole = a.run(rows)
+        assert np.array_equal(whole, a.run(rows))
+        for s, (n, c) in enumerate(lens):
+            if n * 4 > rows:
+                continue
+            b = Case([(n, c)], seed=17)
+            b.q = a.q[a.cu[s]:a.cu[s + 1]]
+            nb = -(-c // 16)
+            for pool, src in zip(b.pools, a.pools):
+                pool[b.table[0, :nb]] = src[a.table[s, :nb]]
+            assert np.array_equal(b.run(rows), whole[a.cu[s]:a.cu[s + 1]])
+    wide, narrow = a.run(16), a.run(8)
+    for s, (n, c) in enumerate(lens):
+        if n <= 2:
+            assert np.array_equal(wide[a.cu[s]:a.cu[s + 1]], narrow[a.cu[s]:a.cu[s + 1]])
+    # row i of sequence 1 by itself: context shorter by what follows it
+    for i in range(4):
+        one = Case([(1, 2500 - 3 + i)], seed=19)
+        one.q = a.q[a.cu[1] + i:a.cu[1] + i + 1]
+        nb = -(-int(one.ctx[0]) // 16)
+        for pool, src in zip(one.pools, a.pools):
+            pool[one.table[0, :nb]] = src[a.table[1, :nb]]
+        assert np.array_equal(one.run(8)[0], wide[a.cu[1] + i])
+
+
+@pytest.mark.gpu
+def test_one_way_for_all_rows():
+    """direct_rows 0: a token has the same bits as a single row and within a chunk."""
+    a = Case([(60, 2100)], seed=23)
+    chunk = a.run(0)
+    for i in (0, 17, 59):
+        one = Case([(1, 2100 - 59 + i), (1, 9)], seed=29)
+        one.q[0] = a.q[i]
+        nb = -(-int(one.ctx[0]) // 16)
+        for pool, src in zip(one.pools, a.pools):
+            pool[one.table[0, :nb]] = src[a.table[0, :nb]]
+        assert np.array_equal(one.run(0)[0], chunk[i])
+
+
+@pytest.mark.gpu
+def test_numbers_that_are_none_stay_with_the_rows_that_see_them():
+    """A NaN or infinity in K or V of a later token does not reach earlier rows, heads or groups."""
+    c = Case([(4, 300), (1, 300)], seed=31)
+    clean = c.run(16)
+    slot = lambda s, p: int(c.table[s, p // 16]) * 16 + p % 16
+    for is_v in (False, True):
+        for p in (297, 298, 299):
+            pools = [x.copy() for x in c.pools]
+            x = np.full((1, 2, 128), 0x3F80, np.uint16)
+            x[0, 1, 70] = 0x7F80 if p == 298 else 0x7FC0  # head 1, group 2
+            other = q4.write(pools[is_v], x, [slot(0, p)], 16, is_v)
+            b, o = divmod(slot(0, p), 16)
+            pools[is_v][b, 1] = other[b, 1]
+            got = c.run(16, pools=[dev(x) for x in pools])
+            val = pa.bf16_to_f64(got)
+            assert np.array_equal(got[:, :4], clean[:, :4]) and np.array_equal(got[4:], clean[4:])
+            for i in range(4):
+                if 296 + i < p:
+                    assert np.array_equal(got[i], clean[i])
+                elif is_v:
+                    assert np.isnan(val[i, 4:, 64:96]).all() and np.isfinite(val[i, 4:, :64]).all() and np.isfinite(val[i, 4:, 96:]).all()
+                else:
+                    assert np.isnan(val[i, 4:]).all()
+    c.q[2, 3, 9] = 0x7FC0                                 # a NaN in one row's q
+    got = c.run(16)
+    keep = np.ones((5, 8), bool)
+    keep[2, 3] = False
+    assert np.array_equal(got[keep], clean[keep]) and np.isnan(pa.bf16_to_f64(got[2, 3])).all()
+
+
+@pytest.mark.gpu
+def test_bad_pages_and_metadata():
+    c = Case([(1, 600), (2, 300), (40, 200)], seed=37)
+    clean = c.run(8)
+    table = c.table.copy()
+    table[0, 5], table[2, 1] = c.nb, -1                   # outside the pool: keys of value 0
+    got = c.run(8, table=table, expect=bd.PA_DEVERR_BLOCK)
+    k, v = (np.nan_to_num(q4.values(p, 16, 128, i == 1).astype(np.float64)) for i, p in enumerate(c.pools))
+    k, v = (np.concatenate([x, np.zeros((1, *x.shape[1:]))]) for x in (k, v))
+    zero = np.where((table < 0) | (table >= c.nb), c.nb, table)
+    want = pa.attention(pa.bf16_to_f64(c.q), k, v, zero, c.cu, c.ctx, 8)
+    np.testing.assert_allclose(pa.bf16_to_f64(got), want, atol=2e-2)
+    assert np.array_equal(got[1:3], clean[1:3])
+    nine = wl.f32_to_bf16_bits(np.float32(9))
+    # contexts and rows other than the planned ones: those sequences are left out, the rest is as it was
+    for s, ctx, cu in ((0, 1300, None), (0, 0, None), (1, 1, None), (2, 39, None), (2, 300, None), (0, -4, None), (0, 2 ** 31 - 1, None),
+                       (1, None, [0, 1, 2, 43]), (2, None, [0, 1, 3, 4])):
+        x, y = c.ctx.copy(), c.cu if cu is None else np.array(cu, np.int32)
+        if ctx is not None:
+            x[s] = ctx
+        # (a longer chunk's context runs into the table's -1 entries as well)
+        got = c.run(8, ctx=x, cu=y, expect=bd.PA_DEVERR_META | (bd.PA_DEVERR_BLOCK if ctx == 300 else 0))
+        for t in range(3):
+            rows = slice(c.cu[t], c.cu[t + 1])
+            if t == s:
+                assert (got[rows] == nine).all(), (s, ctx, cu)
+            elif cu is None:
+                assert np.array_equal(got[rows], clean[rows])
+    # a context that the table does not cover
+    short = c.table[:, :20].copy()
+    got = c.run(8, table=short, expect=bd.PA_DEVERR_META)
+    assert (got[0] == nine).all() and np.array_equal(got[1:], clean[1:])
+    # words that are no plan: nothing is written
+    plan = c.plan(8)
+    plan.words.fill_(2 ** 31 - 1)
+    assert (c.run(plan=plan, expect=bd.PA_DEVERR_META) == nine).all()
+
+
+@pytest.mark.gpu
+def test_a_captured_step_follows_its_plan():
+    """One graph under limits replays steps of other contexts, with and without chunks; two graphs with a
+    workspace each on two streams at once."""
+    steps = [Case([(1, 700), (1, 90), (30, 2200)], seed=41), Case([(4, 4), (1, 5100), (27, 27)], seed=43), Case([(2, 1000), (1, 513), (29, 129)], seed=47)]
+    nb = max(c.nb for c in steps)
+    shape = bd.Shape.make(8, 2, 128, 16, nb)
+    lim = bd.pa_q4_plan_limits(shape, 3, 32, 5200, 16, 60)
+
+    class Slot:
+        def __init__(self):
+            self.k, self.v = (torch.zeros(bd.pa_q4_pool_shape(shape), dtype=torch.uint8, device="cuda") for _ in "kv")
+            self.q, self.out = (torch.zeros(32, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in "qo")
+            self.table = torch.full((3, 330), -1, dtype=torch.int32, device="cuda")
+            self.cu, self.ctx = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (4, 3))
+            self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            self.ws = torch.empty(bd.pa_q4_workspace_bytes(shape, lim) // 4 + 1, device="cuda")
+            self.plan = None
+            self.stream = torch.cuda.Stream()
+
+        def load(self, c):
+            for to, x in ((self.k, c.pools[0]), (self.v, c.pools[1])):
+                to[:c.nb].copy_(dev(x))
+            self.q.copy_(bf16(c.q))
+            self.out.fill_(9.0)
+            self.table.fill_(-1)
+            self.table[:, :c.table.shape[1]].copy_(dev(c.table))
+            self.cu.copy_(dev(c.cu))
+            self.ctx.copy_(dev(c.ctx))
+            p = bd.pa_plan_step_q4(shape, c.cu, c.ctx, limits=lim, device="cuda")
+            if self.plan is None:
+                self.plan = p
+            else:
+                self.plan.words.copy_(p.words)
+
+        def call(self):
+            bd.paged_attention_step_q4(self.q, self.k, self.v, self.table, self.cu, self.ctx, self.plan, self.ws, self.out, shape, err=self.err)
+
+    slots = [Slot(), Slot()]
+    graphs = []
+    for s in slots:
+        s.load(steps[0])
+        s.call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.call()
+        graphs.append(g)
+    want = [c.run(16) for c in steps]
+    for a, b in ((0, 1), (1, 2), (2, 0)):
+        slots[0].load(steps[a])
+        slots[1].load(steps[b])
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for s, g in zip(slots, graphs):
+                with torch.cuda.stream(s.stream):
+                    g.replay()
+        torch.cuda.synchronize()
+        for s, i in zip(slots, (a, b)):
+            assert int(s.err.item()) == 0 and np.array_equal(bits_of(s.out), want[i])
+
+
+@pytest.mark.gpu
+def test_pools_behind_two_gigabytes():
+    """Pages at the end of pools of more than 2^31 bytes give the bits of the same pages in small ones."""
+    a = Case([(1, 900), (3, 140), (50, 310)], 16, 8, 128, 128, seed=53)
+    small = a.run(16)
+    per = 8 * 128 * 80
+    nb = 2 ** 31 // per + 40
+    shape = bd.Shape.make(16, 8, 128, 128, nb)
+    pools = [torch.empty(bd.pa_q4_pool_shape(shape), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    shift = nb - a.nb
+    for p, x in zip(pools, a.pools):
+        p[shift:].copy_(dev(x))
+    table = np.where(a.table >= 0, a.table + shift, -1).astype(np.int32)
+    a.shape = shape
+    assert np.array_equal(a.run(16, pools=pools, table=table), small)
+
+
+@pytest.mark.gpu
+def test_a_run_as_it_is_used():
+    """Prompts in chunks, then single and drafted tokens: norm + rotation + write, step; a fork whose first
+    write copies its page, and a compaction between steps, the pages of K and V together."""
+    rng = np.random.default_rng(61)
+    Hq, Hkv, D, bs, nb = 8, 2, 128, 16, 64
+    shape = bd.Shape.make(Hq, Hkv, D, bs, nb)
+    f = 1e4 ** (-np.arange(D // 2) / (D // 2))
+    rope = bd.pa_rope_pairs(f, device="cuda")
+    w = dev((1 + 0.1 * rng.standard_normal(D)).astype(np.float32)).bfloat16()
+    kp, vp = (torch.full(bd.pa_q4_pool_shape(shape), 255, dtype=torch.uint8, device="cuda") for _ in "kv")
+    alloc = bd.Allocator(nb, bs)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ctx = {}
+
+    def copy(pairs):
+        if pairs:
+            bd.paged_copy_pages(dev(np.array(pairs, np.int32)), [kp, vp], err=err)
+
+    def step(new, rows=None):
+        seqs = list(new)
+        for s in seqs:
+            if s not in ctx:
+                alloc.admit(s, new[s])
+                ctx[s] = 0
+            ctx[s] += new[s]
+            alloc.ensure_capacity(s, ctx[s])
+            copy(alloc.cow(s, ctx[s] - new[s], new[s]))
+        lens = np.array([ctx[s] for s in seqs], np.int32)
+        cu, slots, table = alloc.build_step(seqs, lens, [new[s] for s in seqs], max_blocks=24)
+        T = int(cu[-1])
+        x = bf16(wl.random_bf16(rng, (T, Hq + 2 * Hkv, D)))
+        q = torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+        pos = np.concatenate([np.arange(ctx[s] - new[s], ctx[s]) for s in seqs]).astype(np.int32)
+        bd.paged_qk_norm_rope_write_q4(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], w, w, 1e-6, rope, dev(pos), dev(slots), q, kp, vp, shape, err=err)
+        plan = bd.pa_plan_step_q4(shape, cu, lens, rows, device="cuda")
+        ws = torch.empty(bd.pa_q4_workspace_bytes(shape, plan) // 4 + 1, device="cuda")
+        out = torch.empty_like(q)
+        bd.paged_attention_step_q4(q, kp, vp, dev(table), dev(cu), dev(lens), plan, ws, out, shape, err=err)
+        k, v = (np.nan_to_num(q4.values(p.cpu().numpy(), bs, D, i == 1).astype(np.float64)) for i, p in enumerate((kp, vp)))
+        want = pa.attention(pa.bf16_to_f64(bits_of(q)), k, v, table, cu, lens, Hq)
+        got = pa.bf16_to_f64(bits_of(out))
+        # the rounding of K, V, p and the output to bf16, as of the bf16 step
+        assert np.all(np.abs(got - want) <= 2.0 ** -5 * np.sqrt((want ** 2).mean(-1, keepdims=True)) + 1e-3)
+
+    step({0: 90, 1: 33, 2: 64})
+    step({0: 1, 1: 1, 2: 40})
+    alloc.fork(0, 7)
+    ctx[7] = ctx[0]
+    step({0: 1, 7: 4, 1: 1, 2: 1})
+    alloc.free_seq(1)
+    del ctx[1]
+    alloc.trim(2, 50)
+    ctx[2] = 50
+    pairs = alloc.compact()
+    assert pairs
+    copy(pairs)
+    alloc.check_consistent()
+    step({0: 2, 7: 1, 2: 1, 9: 20})
+    step({0: 1, 7: 1, 2: 1, 9: 1}, rows=0)
+    assert int(err.item()) == 0
