@@ -9,9 +9,6 @@
 // Rows of every tile-routine MMA (M): (query token, head-in-group) pairs of one KV head.
 #define PA_ROWS 128
 
-// The 4-bit cache's rows that are read from the codes (q4.cu): warps of a CTA, and CTAs (so lists of the
-// plan) with up to 8 and up to 16 rows an item, three and two a multiprocessor.
-#define PA_Q4_WARPS 4
 // Most rows (query tokens times heads of a group) of a sequence that are faster read from the codes.
 #define PA_Q4_DIRECT_ROWS 64
 #define PA_Q4_LISTS_8 (3 * PA_PLAN_CTAS)
@@ -19,14 +16,15 @@
 
 namespace pa_detail {
 
-// Keys of a split of a row read from the codes, by its sequence's context alone: short ones where there
-// are few, so that a single sequence spreads over the GPU, and longer ones where the parts' own
-// bytes (a split's result is written and read once more) would add up. A multiple of 128.
+// Keys of a split of a row read from the codes, by its sequence's context alone. A split is a warp's work:
+// short ones where there are few, so that a single sequence spreads over the GPU, and longer ones where
+// what a split costs beyond its keys (its start, its result written and read once more) would add up. A
+// multiple of 32.
 __host__ __device__ constexpr int64_t q4_split_keys(int32_t ctx) {
-    return ctx <= 4096 ? 512 : ctx <= 32768 ? 1024 : 2048;
+    return ctx <= 4096 ? 256 : ctx <= 32768 ? 512 : 1024;
 }
 // The longest context of one split.
-constexpr int64_t q4_one_split() { return 512; }
+constexpr int64_t q4_one_split() { return 256; }
 // Most splits of any context up to max_ctx.
 inline int64_t q4_max_splits(int64_t max_ctx) {
     const auto n = [](int64_t c) { return c <= 0 ? 1 : (c + q4_split_keys(int32_t(c)) - 1) / q4_split_keys(int32_t(c)); };
@@ -38,13 +36,14 @@ inline int64_t q4_max_splits(int64_t max_ctx) {
 
 // Where the parts of a plan's words begin (see pa_q4_plan).
 struct Q4Words {
-    int64_t direct, fold, chunk, expand, table, total;
+    int64_t direct, lists, fold, chunk, expand, table, total;
 };
 inline Q4Words q4_words(const pa_q4_plan& p) {
     constexpr int64_t item = sizeof(pa_work_item) / 4;
     Q4Words w;
     w.direct = 0;
-    w.fold = w.direct + item * p.n_direct;
+    w.lists = w.direct + item * p.n_direct;
+    w.fold = w.lists + (p.n_direct > 0 ? PA_PLAN_CTAS + 1 : 0);
     w.chunk = w.fold + p.n_fold;
     w.expand = w.chunk + item * p.n_chunk;
     w.table = w.expand + 2 * int64_t(p.n_expand);

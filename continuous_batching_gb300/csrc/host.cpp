@@ -449,21 +449,15 @@ void plain_items(const pa_shape* shape, int32_t s, int32_t q0, int32_t n, int32_
 }
 
 // Deals the units longest processing time first: each unit, by decreasing cost (ties in
-// generation order), joins the list (one per CTA) with the least cost so far, the lower list on
-// a tie; its items take consecutive places in that list. The output holds the first item of
-// every list (list c at index c), then the second item of every list that has one, in list
-// order, and so on, with `next` linking each list. The kernel runs min(output items,
-// PA_PLAN_CTAS) CTAs, CTA c from index c: when units make fewer lists G than that, padding
-// items (n_q == 0) take indices G .. PA_PLAN_CTAS - 1, so that the CTAs past the lists find
-// no work.
-int32_t deal(const std::vector<pa_work_item>& out, const std::vector<Unit>& units,
-             pa_work_item* items, int32_t max_items, int32_t* n_items,
-             int32_t lists = PA_PLAN_CTAS) {
-    const int32_t n = int32_t(out.size());
+// generation order), joins the list (one per CTA, G of them) with the least cost so far, the lower
+// list on a tie; its items take consecutive places in that list. owner and rank are the items' list
+// and place in it, len the lists' items.
+struct Deal {
+    std::vector<int32_t> owner, rank, len;
+};
+
+void assign(int32_t n, const std::vector<Unit>& units, int32_t G, Deal& out) {
     const int32_t nu = int32_t(units.size());
-    const int32_t G = std::min<int32_t>(nu, lists);
-    const int32_t pad = G < std::min<int32_t>(n, lists) ? lists - G : 0;
-    if (int64_t(n) + pad > max_items) return PA_ERR_INVALID;
     // by decreasing cost, ties in generation order (a stable counting sort when it is small)
     int64_t max_cost = 0;
     for (const Unit& u : units) max_cost = std::max(max_cost, u.cost);
@@ -480,20 +474,21 @@ int32_t deal(const std::vector<pa_work_item>& out, const std::vector<Unit>& unit
             return units[size_t(x)].cost > units[size_t(y)].cost;
         });
     }
-    // a binary min-heap of keys cost * 1024 + list (G <= 1024), so that equal costs order by list
-    static_assert(PA_Q4_LISTS_8 <= 1024, "list index must fit the heap key's low bits");
+    // a binary min-heap of keys cost * 256 + list (G <= 256), so that equal costs order by list
+    static_assert(PA_PLAN_CTAS <= 256, "list index must fit the heap key's low byte");
     std::vector<uint64_t> heap(static_cast<size_t>(G));
     for (int32_t c = 0; c < G; ++c) heap[size_t(c)] = uint64_t(c);   // ascending: a heap
-    std::vector<int32_t> owner(static_cast<size_t>(n)), rank(static_cast<size_t>(n));
-    std::vector<int32_t> len(static_cast<size_t>(G), 0);
+    out.owner.resize(static_cast<size_t>(n));
+    out.rank.resize(static_cast<size_t>(n));
+    out.len.assign(static_cast<size_t>(G), 0);
     for (int32_t j = 0; j < nu && G > 0; ++j) {
         const Unit& u = units[size_t(by_cost[size_t(j)])];
-        const int32_t c = int32_t(heap[0] & 1023u);
+        const int32_t c = int32_t(heap[0] & 255u);
         for (int32_t k = 0; k < u.count; ++k) {
-            owner[size_t(u.first + k)] = c;
-            rank[size_t(u.first + k)] = len[size_t(c)]++;
+            out.owner[size_t(u.first + k)] = c;
+            out.rank[size_t(u.first + k)] = out.len[size_t(c)]++;
         }
-        uint64_t key = heap[0] + uint64_t(u.cost) * 1024u;
+        uint64_t key = heap[0] + uint64_t(u.cost) * 256u;
         size_t k = 0;                                                // sift the root down
         for (;;) {
             size_t m = 2 * k + 1;
@@ -505,6 +500,24 @@ int32_t deal(const std::vector<pa_work_item>& out, const std::vector<Unit>& unit
         }
         heap[k] = key;
     }
+}
+
+// The deal as paged_attention_step takes it: the output holds the first item of
+// every list (list c at index c), then the second item of every list that has one, in list
+// order, and so on, with `next` linking each list. The kernel runs min(output items,
+// PA_PLAN_CTAS) CTAs, CTA c from index c: when units make fewer lists G than that, padding
+// items (n_q == 0) take indices G .. PA_PLAN_CTAS - 1, so that the CTAs past the lists find
+// no work.
+int32_t deal(const std::vector<pa_work_item>& out, const std::vector<Unit>& units,
+             pa_work_item* items, int32_t max_items, int32_t* n_items) {
+    const int32_t n = int32_t(out.size());
+    const int32_t nu = int32_t(units.size());
+    const int32_t G = std::min<int32_t>(nu, PA_PLAN_CTAS);
+    const int32_t pad = G < std::min<int32_t>(n, PA_PLAN_CTAS) ? PA_PLAN_CTAS - G : 0;
+    if (int64_t(n) + pad > max_items) return PA_ERR_INVALID;
+    Deal d;
+    assign(n, units, G, d);
+    const std::vector<int32_t>&owner = d.owner, &rank = d.rank, &len = d.len;
     // stored position by position: so list c starts at index c and a successor has a higher
     // index
     std::vector<int32_t> off(size_t(G) + 1, 0);
@@ -533,6 +546,17 @@ int32_t deal(const std::vector<pa_work_item>& out, const std::vector<Unit>& unit
     }
     *n_items = n + pad;
     return PA_OK;
+}
+
+// The deal with every list's items side by side, by decreasing cost: list c is
+// items[first[c]] .. items[first[c + 1] - 1].
+void deal_lists(const std::vector<pa_work_item>& out, const std::vector<Unit>& units, int32_t lists,
+                pa_work_item* items, int32_t* first) {
+    Deal d;
+    assign(int32_t(out.size()), units, lists, d);
+    first[0] = 0;
+    for (int32_t c = 0; c < lists; ++c) first[c + 1] = first[c] + d.len[size_t(c)];
+    for (size_t i = 0; i < out.size(); ++i) items[first[d.owner[i]] + d.rank[i]] = out[i];
 }
 
 int32_t plan(const pa_shape* shape, int32_t B, const int32_t* cu, const int32_t* ctx,
@@ -729,8 +753,9 @@ int32_t q4_parts(const pa_shape* shape, int32_t B, const int32_t* cu, const int3
                     it.n_splits = splits;
                     it.kind = PA_ITEM_DIRECT;
                     it.tile0 = base;
-                    // 128 keys are one tile of each warp; an item's start and join cost about two
-                    out.direct_units.push_back({base + sp, 1, int64_t(it.n_tiles) + 2});
+                    it.next = ctx[s];
+                    // in tiles of 32 keys; an item's start and end cost about two
+                    out.direct_units.push_back({base + sp, 1, (k + 31) / 32 + 2});
                     out.direct.push_back(it);
                 }
             }
@@ -863,10 +888,9 @@ int32_t pa_plan_step_q4(const pa_shape* shape, int32_t B, const int32_t* cu, con
     const Q4Words at = q4_words(*plan);
     auto* direct = reinterpret_cast<pa_work_item*>(words + at.direct);
     auto* chunk = reinterpret_cast<pa_work_item*>(words + at.chunk);
-    int32_t n = 0;
-    if ((st = deal(parts.direct, parts.direct_units, direct, plan->n_direct, &n,
-                   plan->direct_rows > 8 ? PA_Q4_LISTS_16 : PA_Q4_LISTS_8)))
-        return st;
+    if (plan->n_direct > 0)
+        deal_lists(parts.direct, parts.direct_units, PA_PLAN_CTAS, direct, words + at.lists);
+    int32_t n = int32_t(parts.direct.size());
     int32_t k = 0;
     for (int32_t i = 0; i < n; ++i)
         if (direct[i].split == 0 && direct[i].n_splits > 1) words[at.fold + k++] = i;

@@ -228,10 +228,11 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
 // ------------------------------------------------------------------- rows read from the codes
 //
 // An item is one KV head, one tile of query rows (tokens x heads of its group, at most 8 NT of them)
-// and one split of the sequence's keys. Each of the CTA's four warps takes every fourth tile of 32 keys and keeps its own
-// online softmax; the warps' results are joined in a fixed order at the item's end, the splits' by
-// q4_fold_kernel. A split's length depends on the sequence's context alone (q4_split_keys), so a row's
-// bits do not depend on the batch.
+// and one split of the sequence's keys: the work of one warp, which takes the split's tiles of 32 keys in turn and keeps
+// their online softmax. A CTA's warps draw items from its list (one CTA and list a
+// multiprocessor, dealt by cost on the host), so nothing waits for anything but its own loads. A row's splits are
+// joined in a fixed order by q4_fold_kernel. A split's length depends on the sequence's context alone
+// (q4_split_keys), so a row's bits do not depend on the batch.
 //
 // Why mma.sync and not tcgen05: the contraction's free dimension is at most 8 NT columns, so the tensor
 // rate is no concern; what is, is the way of the codes to the tensor core. tcgen05 would take them expanded to
@@ -239,61 +240,61 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
 // attention.cu, which does this, takes 2.5 T elements/s). mma.sync takes them from
 // the registers that unpacked them. So (keys x columns) is the A operand, and with the row order of q4.h
 // a lane's 16-byte piece of a row is its fragments:
-//   S^T = K Q^T     A = K codes as 128 + u (bf16: the code in the mantissa, no conversion), B = Q^T
-//   S = sum_g s_g (q . (128 + u))_g + (m_g - 128 s_g) sum(q_g)
-// exact products and fp32 sums: K is never rounded beyond its code.
-//   O^T = V^T P^T   A = V codes as u - 8 (exact), B = P^T with the group's scale in it, rounded to bf16
-//   O = sum_j bf16(p_j s_jg) (u_j - 8) + sum_j p_j (m_jg + 8 s_jg)        (the second sum in fp32)
-// The tensor core turns P^T's layout by movmatrix. u - 8 instead of u: a rounding of p s then weighs as
-// much as that of p against a bf16 V; u alone would double it.
+//   S^T = K Q^T     A = K codes as f16 subnormals, u 2^-24 and 16 u 2^-24 (no conversion: a mask), B = Q^T and
+//                   Q^T / 16 in f16, each row of q times a power of two
+//   S = sum_g s_g (q . codes)_g + sum_g m_g sum(q_g)
+// with exact products and fp32 sums: K is never rounded beyond its code. The second sum is a product too, of the
+// minima and sum(q_g) in three bf16 parts.
+//   O^T = V^T P^T   A = V codes as u - 8 (bf16: the code in the mantissa, less 136), B = w = bf16(p s_g), p
+//                   rounded to bf16
+//   O = sum_j w_j (u_j - 8) + sum_j p_j bf16(m_jg + 8 s_jg)
+// u - 8 and not u: the roundings of w then weigh as much as that of p, u alone would double them.
+// P^T's layout is turned by movmatrix, once for all groups.
+// A masked key's parameters may be anything (it may not have been written yet), and 0 times them too: its w
+// are cleared for the rows that do not see it, its centre is clamped to numbers. What is not finite still
+// reaches the rows that see it, through w.
 //
-// Loads: cp.async into a ring of kStages tiles per warp (codes and parameters; keys behind the context
-// and blocks outside the pool are filled with zeros), no barrier but the warp's own.
+// Loads: cp.async into a ring of kStages tiles per warp (codes and parameters; blocks outside the pool are
+// filled with zeros, keys of a block behind the last row may hold anything and are masked), no barrier
+// but the warp's own.
 struct DirectParams {
     const __nv_bfloat16* q;
     const uint8_t *k_pool, *v_pool;
     const int32_t *table, *cu, *ctx;
     const pa_work_item* items;
+    const int32_t* lists;               // [PA_PLAN_CTAS + 1]: the first item of every CTA's
     float* part;                        // [n_items][8 NT][D + 2]: splits' (acc, m, l)
     __nv_bfloat16* out;
     int32_t* err;
     int32_t n_items, B, T, max_blocks, num_blocks, Hq, Hkv, log2g, log2bs, max_ctx;
     float c;                            // log2(e) / sqrt(D)
+    uint32_t bits;                      // 0x43004300
 };
 
-constexpr int kWarps = PA_Q4_WARPS;
+// warps of a CTA (one a multiprocessor): what the registers hold
+template <int NT>
+constexpr int kWarps = NT == 1 ? 12 : 8;
+constexpr uint32_t kEights = 0x41004100u;   // two bf16
 constexpr int kKeys = 32;               // keys of a warp's tile
+constexpr int kHeld = 128;              // items of a list that a CTA keeps in shared memory
+constexpr float kNone = 3e38f;          // minus a maximum that every score passes
 
 template <int D>
 struct Ring {
-    static constexpr int kStages = 3;
+    static constexpr int kStages = 2;
     static constexpr int kCodes = kKeys * kQ4Codes<D>;
     static constexpr int kParams = kKeys * kQ4Params<D>;
     static constexpr int kStage = 2 * (kCodes + kParams);       // K codes, V codes, K, V parameters
     static constexpr int kWarp = kStages * kStage;
-    static constexpr int kBytes = kWarps * kWarp;
 };
-
-// What the warps leave for the join at an item's end, over the ring: rows of D + 4 floats (so that a
-// quarter warp's 16-byte stores meet every bank once), then (m, l).
-template <int D, int NT>
-struct Join {
-    static constexpr int kRow = D + 4;
-    static constexpr int kMl = kWarps * 8 * NT * kRow;          // floats
-    static constexpr int kBytes = (kMl + kWarps * 8 * NT * 2) * 4;
-};
-
-template <int D, int NT>
-constexpr int kDirectSmem = Ring<D>::kBytes > Join<D, NT>::kBytes ? Ring<D>::kBytes
-                                                                  : Join<D, NT>::kBytes;
 
 template <int D>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[D / kQ4Group]) {
     if constexpr (D == 128) {
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
     } else {
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
     }
 }
 
@@ -301,10 +302,16 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[D / kQ4Gr
 template <int D>
 __device__ __forceinline__ void lds_halves(uint32_t addr, uint32_t (&w)[D / kQ4Group / 2]) {
     if constexpr (D == 128) {
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
     } else {
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
     }
+}
+
+__device__ __forceinline__ uint32_t lds_word(uint32_t addr) {
+    uint32_t w;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(addr));
+    return w;
 }
 
 template <int BYTES>
@@ -319,31 +326,55 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// D (+)= A B, A 16 x 16 and B 16 x 8 bf16, fp32 accumulator.
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                    uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-                 "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// D = A B and D += A B, A 16 x 16 and B 16 x 8 bf16 (or f16), fp32 accumulator.
+#define PA_Q4_MMA(NAME, SHAPE, TYPE)                                                                          \
+    __device__ __forceinline__ void NAME(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,         \
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {                      \
+        asm("mma.sync.aligned." SHAPE ".row.col.f32." TYPE "." TYPE ".f32 {%0, %1, %2, %3}, "           \
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"                                            \
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                           \
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                                   \
+    }                                                                                                  \
+    __device__ __forceinline__ void NAME##0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,      \
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {                   \
+        asm("mma.sync.aligned." SHAPE ".row.col.f32." TYPE "." TYPE ".f32 {%0, %1, %2, %3}, "           \
+            "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"                                        \
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                           \
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));                         \
+    }
+PA_Q4_MMA(mma, "m16n8k16", "bf16")
+PA_Q4_MMA(mma_f16_, "m16n8k16", "f16")
+#undef PA_Q4_MMA
+
+__device__ __forceinline__ uint32_t mul_bf16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+// NaN and infinities become large numbers, numbers stay.
+__device__ __forceinline__ uint32_t finite_bf16(uint32_t a) {
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(0xFF00FF00u));
+    asm("min.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(0x7F007F00u));
+    return a;
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t w) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
     return r;
 }
 
-// Nibble K of both 16-bit halves as bf16 128 + u.
+// Nibble K of both 16-bit halves as bf16 u - 8. bits: 128 twice, in a register that the compiler does not know
+// the value of (with two constants it makes two instructions of mask and exponent).
 template <int K>
-__device__ __forceinline__ uint32_t biased(uint32_t w) {
-    return ((w >> (4 * K)) & 0x000F000Fu) | 0x43004300u;
-}
-// ... as bf16 u - 8.
-template <int K>
-__device__ __forceinline__ uint32_t centred(uint32_t w) {
+__device__ __forceinline__ uint32_t centred(uint32_t w, uint32_t bits) {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(biased<K>(w)), "r"(0x43084308u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(((w >> (4 * K)) & 0x000F000Fu) | bits), "r"(0x43084308u));
     return r;
 }
 
@@ -358,83 +389,136 @@ template <int D, int NT>
 struct Rows {
     static constexpr int G = D / kQ4Group;
     uint32_t qb[NT][G][4];              // Q^T fragments of the group's two steps
-    uint64_t qs[NT][G];                 // sums of q over the group, rows 2 c and 2 c + 1
+    uint32_t qm[NT][2];                 // ... of the minima's product
     float o[NT][2 * G][4];
-    uint64_t z[NT][G];                  // sum of p (m + 8 s), this lane's keys
+    float z[NT][4];                     // sums of p (m + 8 s): lane row r holds group r % G
     uint64_t l[NT];                     // sum of p, this lane's keys
-    float m[NT][2];                     // reference maximum, in raw scores
-    int pos[NT][2];                     // position of the row
+    float c[NT][2];                     // scores to base 2: log2(e) / sqrt(D) and q's power of two
+    float nm[NT][2];                    // minus the reference maximum, in base 2; kNone: no key yet
+    int pos0, rows, log2g;              // position of the first row, rows, heads of a token
+
+    // Position of a row; those behind the last one see what the last one sees.
+    __device__ __forceinline__ int pos(int row) const { return pos0 + (min(row, rows - 1) >> log2g); }
+    uint32_t bits;                      // of 128, twice (see centred)
 };
 
-// Two keys' weights for two rows: p * scale as bf16 pairs, p (m + 8 s) onto z.
-__device__ __forceinline__ void q4_weigh(uint64_t p0, uint64_t p1, uint64_t s0, uint64_t s1, uint64_t m0,
-                                         uint64_t m1, uint32_t& w0, uint32_t& w1, uint64_t& z) {
-    float a, b;
-    f2_split(mul2(p0, s0), a, b);
-    w0 = pack_bf16(a, b);
-    f2_split(mul2(p1, s1), a, b);
-    w1 = pack_bf16(a, b);
-    z = fma2(p0, m0, z);
-    z = fma2(p1, m1, z);
+// The rows of column tile j from q (w: columns 32 g + 8 c .. + 7 of row 8 j + r), and their state at the start.
+template <int D, int NT>
+__device__ __forceinline__ void q4_take_q(Rows<D, NT>& R, const uint4 (&w)[D / kQ4Group], int j, float c_plain,
+                                          int lane) {
+    constexpr int G = D / kQ4Group;
+    const int cc = lane & 3;
+    float v[G][8], big = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        v[g][0] = scale_of(w[g].x), v[g][1] = min_of(w[g].x), v[g][2] = scale_of(w[g].y), v[g][3] = min_of(w[g].y);
+        v[g][4] = scale_of(w[g].z), v[g][5] = min_of(w[g].z), v[g][6] = scale_of(w[g].w), v[g][7] = min_of(w[g].w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(v[g][i]));
+    }
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    // q 2^e, its largest element below 2^15: a bf16's 8 bits are kept down to 2^-29 of it (in the halves
+    // divided by 16, 2^-25). Exponent 255, an infinity, is taken like the largest number's: infinities and NaN
+    // stay what they are.
+    const int e = 14 + 127 - int(max(__float_as_uint(big) >> 23, 24u));     // 2^e and 2^-e are fp32 numbers
+    const float up = __uint_as_float(uint32_t(127 + e) << 23);
+    const float c = c_plain * __uint_as_float(uint32_t(127 - e) << 23) * 0x1p24f;
+    R.c[j][0] = __shfl_sync(0xffffffffu, c, 8 * cc);
+    R.c[j][1] = __shfl_sync(0xffffffffu, c, 8 * cc + 4);
+    float sum[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[g][i] *= up;
+        // nibbles 0, 4 | 1, 5 | 2, 6 | 3, 7 are the steps' operands
+        R.qb[j][g][0] = pack_f16(v[g][0], v[g][4]);
+        R.qb[j][g][1] = pack_f16(v[g][1] * 0.0625f, v[g][5] * 0.0625f);
+        R.qb[j][g][2] = pack_f16(v[g][2], v[g][6]);
+        R.qb[j][g][3] = pack_f16(v[g][3] * 0.0625f, v[g][7] * 0.0625f);
+        float t = ((v[g][0] + v[g][1]) + (v[g][2] + v[g][3])) + ((v[g][4] + v[g][5]) + (v[g][6] + v[g][7]));
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        sum[g] = t * 0x1p-24f;
+    }
+    // The minima's product. Every lane of a row holds all its minima, groups 0 and 1 in the first half of the
+    // step and 2 and 3 in the second; against them stand part c of sum(q_g) (lanes c < 3) or nothing.
+    uint32_t part[2] = {0, 0};
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float t = sum[g];
+        const __nv_bfloat16 p0 = __float2bfloat16_rn(t);
+        t -= __bfloat162float(p0);
+        const __nv_bfloat16 p1 = __float2bfloat16_rn(t);
+        t -= __bfloat162float(p1);
+        const __nv_bfloat16 p2 = __float2bfloat16_rn(t);
+        const uint32_t b = __bfloat16_as_ushort(cc == 0 ? p0 : cc == 1 ? p1 : p2);
+        part[g / 2] |= b << (16 * (g & 1));
+    }
+    R.qm[j][0] = cc < 3 ? part[0] : 0;
+    R.qm[j][1] = cc < 3 ? part[1] : 0;              // (two groups: nothing)
+#pragma unroll
+    for (int t = 0; t < 2 * G; ++t) R.o[j][t][0] = R.o[j][t][1] = R.o[j][t][2] = R.o[j][t][3] = 0.f;
+    R.z[j][0] = R.z[j][1] = R.z[j][2] = R.z[j][3] = 0.f;
+    R.l[j] = 0;
+    R.nm[j][0] = R.nm[j][1] = kNone;
 }
 
-// One tile of 32 keys, from key0 on. MASK: some key lies behind some row.
-template <int D, int NT, bool MASK>
-__device__ __forceinline__ void q4_tile(uint32_t stage, Rows<D, NT>& R, float c, int key0, int lane) {
+// Scores of 16 keys of a tile (h: which half) from its stage, in units of 1 / R.c.
+template <int D, int NT>
+__device__ __forceinline__ void q4_scores(uint32_t stage, const Rows<D, NT>& R, int h, int lane,
+                                          float (&x)[NT][2][4]) {
     constexpr int G = D / kQ4Group;
     using L = Ring<D>;
     const int r = lane >> 2, cc = lane & 3;
-    float x[NT][2][4];                  // [column tile][16 keys][key r: rows 2c, 2c + 1; key r + 8]
+    uint32_t ka[G], kb[G], pa[G], pb[G];
+    const uint32_t row = stage + (16 * h + r) * kQ4Codes<D> + cc * (4 * G);
+    lds_words<D>(row, ka);
+    lds_words<D>(row + 8 * kQ4Codes<D>, kb);
+    const uint32_t par = stage + 2 * L::kCodes + (16 * h + r) * kQ4Params<D>;
+    lds_words<D>(par, pa);
+    lds_words<D>(par + 8 * kQ4Params<D>, pb);
+    const uint32_t m0 = __byte_perm(pa[0], pa[1], 0x7632), m1 = __byte_perm(pb[0], pb[1], 0x7632);
+    const uint32_t m2 = __byte_perm(pa[G - 2], pa[G - 1], 0x7632), m3 = __byte_perm(pb[G - 2], pb[G - 1], 0x7632);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t ka[G], kb[G], pa[G], pb[G];
-        const uint32_t row = stage + (16 * h + r) * kQ4Codes<D> + cc * (4 * G);
-        lds_words<D>(row, ka);
-        lds_words<D>(row + 8 * kQ4Codes<D>, kb);
-        const uint32_t par = stage + 2 * L::kCodes + (16 * h + r) * kQ4Params<D>;
-        lds_words<D>(par, pa);
-        lds_words<D>(par + 8 * kQ4Params<D>, pb);
-        uint64_t sa[NT], sb[NT];
+    for (int j = 0; j < NT; ++j) mma0(x[j][h], m0, m1, m2, m3, R.qm[j][0], R.qm[j][1]);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            float raw[NT][4];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                raw[j][0] = raw[j][1] = raw[j][2] = raw[j][3] = 0.f;
-                mma(raw[j], biased<0>(ka[g]), biased<0>(kb[g]), biased<1>(ka[g]), biased<1>(kb[g]),
-                    R.qb[j][g][0], R.qb[j][g][1]);
-                mma(raw[j], biased<2>(ka[g]), biased<2>(kb[g]), biased<3>(ka[g]), biased<3>(kb[g]),
-                    R.qb[j][g][2], R.qb[j][g][3]);
-            }
-            const float s0 = scale_of(pa[g]), s1 = scale_of(pb[g]);
-            const float m0 = fmaf(-128.f, s0, min_of(pa[g])), m1 = fmaf(-128.f, s1, min_of(pb[g]));
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const uint64_t ra = f2(raw[j][0], raw[j][1]), rb = f2(raw[j][2], raw[j][3]);
-                sa[j] = g ? fma2(ra, f2(s0, s0), sa[j]) : mul2(ra, f2(s0, s0));
-                sb[j] = g ? fma2(rb, f2(s1, s1), sb[j]) : mul2(rb, f2(s1, s1));
-                sa[j] = fma2(R.qs[j][g], f2(m0, m0), sa[j]);
-                sb[j] = fma2(R.qs[j][g], f2(m1, m1), sb[j]);
-            }
-        }
+    for (int g = 0; g < G; ++g) {
+        const float s0 = scale_of(pa[g]), s1 = scale_of(pb[g]);
+        const uint32_t ha = ka[g] >> 8, hb = kb[g] >> 8;
+        constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            f2_split(sa[j], x[j][h][0], x[j][h][1]);
-            f2_split(sb[j], x[j][h][2], x[j][h][3]);
+            float t[4];
+            mma_f16_0(t, ka[g] & kLow, kb[g] & kLow, ka[g] & kHigh, kb[g] & kHigh, R.qb[j][g][0], R.qb[j][g][1]);
+            mma_f16_(t, ha & kLow, hb & kLow, ha & kHigh, hb & kHigh, R.qb[j][g][2], R.qb[j][g][3]);
+            x[j][h][0] = fmaf(t[0], s0, x[j][h][0]);
+            x[j][h][1] = fmaf(t[1], s0, x[j][h][1]);
+            x[j][h][2] = fmaf(t[2], s1, x[j][h][2]);
+            x[j][h][3] = fmaf(t[3], s1, x[j][h][3]);
         }
     }
-    // online softmax; the reference maximum moves when the rows' maximum outgrows it by 2^8
+}
+
+// Online softmax of a tile of 32 keys from key0 on: p as bf16 pairs of keys 2 c, 2 c + 1 (and 8 behind them) of
+// row r. masked: some key lies behind some row. The reference maximum moves when the rows' maximum outgrows it
+// by 2^8.
+template <int D, int NT>
+__device__ __forceinline__ void q4_softmax(Rows<D, NT>& R, float (&x)[NT][2][4], bool masked, int key0,
+                                           int lane, uint32_t (&p)[NT][2][2]) {
+    constexpr int G = D / kQ4Group;
+    const int r = lane >> 2;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         float mx[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            if constexpr (MASK) {
+            if (masked) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
-                        if (key0 + 16 * h + 8 * b + r > R.pos[j][e]) x[j][h][2 * b + e] = -INFINITY;
+                        if (key0 + 16 * h + 8 * b + r > R.pos(8 * j + 2 * (lane & 3) + e)) x[j][h][2 * b + e] = -INFINITY;
             }
             mx[e] = fmaxf(fmaxf(x[j][0][e], x[j][0][2 + e]), fmaxf(x[j][1][e], x[j][1][2 + e]));
         }
@@ -443,30 +527,31 @@ __device__ __forceinline__ void q4_tile(uint32_t stage, Rows<D, NT>& R, float c,
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], d));
             mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], d));
         }
-        float a[2], nmc[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float old = R.m[j][e], now = fmaxf(old, mx[e]);
-            const bool move = old == -INFINITY ? now != -INFINITY : (now - old) * c > 8.f;
-            R.m[j][e] = move ? now : old;
-            const float use = R.m[j][e] == -INFINITY ? 0.f : R.m[j][e];
-            a[e] = !move || old == -INFINITY ? 1.f : ex2((old - use) * c);
-            nmc[e] = -use * c;
-        }
-        if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+        // in base 2 above the reference
+        const float up0 = fmaf(mx[0], R.c[j][0], R.nm[j][0]), up1 = fmaf(mx[1], R.c[j][1], R.nm[j][1]);
+        if (__any_sync(0xffffffffu, up0 > 8.f || up1 > 8.f)) {
+            // the result's factors, 1 for a row that stays
+            float a[2] = {1.f, 1.f};
+            if (up0 > 8.f) {
+                const float now = -mx[0] * R.c[j][0];
+                a[0] = ex2(now - R.nm[j][0]);
+                R.nm[j][0] = now;
+            }
+            if (up1 > 8.f) {
+                const float now = -mx[1] * R.c[j][1];
+                a[1] = ex2(now - R.nm[j][1]);
+                R.nm[j][1] = now;
+            }
             const uint64_t a2 = f2(a[0], a[1]);
             R.l[j] = mul2(R.l[j], a2);
+            R.z[j][0] *= a[0];
+            R.z[j][1] *= a[1];
 #pragma unroll
-            for (int g = 0; g < G; ++g) R.z[j][g] = mul2(R.z[j][g], a2);
+            for (int t = 0; t < 2 * G; ++t)
 #pragma unroll
-            for (int t = 0; t < 2 * G; ++t) {
-                R.o[j][t][0] *= a[0];
-                R.o[j][t][1] *= a[1];
-                R.o[j][t][2] *= a[0];
-                R.o[j][t][3] *= a[1];
-            }
+                for (int e = 0; e < 4; ++e) R.o[j][t][e] *= a[e & 1];
         }
-        const uint64_t n2 = f2(nmc[0], nmc[1]), c2 = f2(c, c);
+        const uint64_t n2 = f2(R.nm[j][0], R.nm[j][1]), c2 = f2(R.c[j][0], R.c[j][1]);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -478,195 +563,230 @@ __device__ __forceinline__ void q4_tile(uint32_t stage, Rows<D, NT>& R, float c,
                 v = ex2(v);
                 R.l[j] = add2(R.l[j], f2(u, v));
             }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            p[j][h][0] = transpose8(pack_bf16(x[j][h][0], x[j][h][1]));
+            p[j][h][1] = transpose8(pack_bf16(x[j][h][2], x[j][h][3]));
+        }
+    }
+}
+
+// O of 16 keys of a tile (h: which half) from its stage and p. MASK: some key lies behind some row.
+template <int D, int NT, bool MASK>
+__device__ __forceinline__ void q4_values(uint32_t stage, Rows<D, NT>& R, const uint32_t (&p)[NT][2][2],
+                                          int h, int key0, int lane) {
+    constexpr int G = D / kQ4Group;
+    using L = Ring<D>;
+    const int r = lane >> 2, cc = lane & 3;
+    // Keys 2 c, 2 c + 1 and those 8 behind them. Of eight keys the even ones lie before the odd ones, and (D = 128) of
+    // four such rows the first halves before the second, so that what half a warp reads is contiguous.
+    const uint32_t row = stage + L::kCodes + 16 * h * kQ4Codes<D> + cc * 32 + (D == 128 ? (r >> 2) * 128 + (r & 3) * 8 : r * 4);
+    const uint32_t par = stage + 2 * L::kCodes + L::kParams + (16 * h + 2 * cc) * kQ4Params<D>;
+    uint32_t v[4][G / 2], zp[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        lds_halves<D>(row + 4 * k * kQ4Codes<D>, v[k]);
+        zp[k] = lds_word(par + ((k >> 1) * 8 + (k & 1)) * kQ4Params<D> + 4 * (r % G));
+    }
+    uint32_t keep0[NT], keep1[NT];
+    uint32_t z0 = fma_bf16(__byte_perm(zp[0], zp[1], 0x5410), kEights, __byte_perm(zp[0], zp[1], 0x7632));
+    uint32_t z1 = fma_bf16(__byte_perm(zp[2], zp[3], 0x5410), kEights, __byte_perm(zp[2], zp[3], 0x7632));
+    if constexpr (MASK) {
+        z0 = finite_bf16(z0);
+        z1 = finite_bf16(z1);
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        // keys 2 c, 2 c + 1 and those 8 behind them: even keys of eight lie before odd ones
-        uint32_t v[4][G / 2], pa[G], pb[G];
-        const uint32_t row = stage + L::kCodes + (16 * h + cc) * kQ4Codes<D> + r * (2 * G);
+    for (int j = 0; j < NT; ++j) {
+        mma(R.z[j], z0, 0u, z1, 0u, p[j][h][0], p[j][h][1]);
+        if constexpr (MASK) {
+            const int seen = R.pos(8 * j + r) - (key0 + 16 * h + 2 * cc);     // >= 0: key 2 c, and so on
+            keep0[j] = (seen >= 0 ? 0xFFFFu : 0u) | (seen >= 1 ? 0xFFFF0000u : 0u);
+            keep1[j] = (seen >= 8 ? 0xFFFFu : 0u) | (seen >= 9 ? 0xFFFF0000u : 0u);
+        }
+    }
+    uint32_t pv[4][G];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) lds_halves<D>(row + 4 * k * kQ4Codes<D>, v[k]);
-        const uint32_t par = stage + 2 * L::kCodes + L::kParams + (16 * h + r) * kQ4Params<D>;
-        lds_words<D>(par, pa);
-        lds_words<D>(par + 8 * kQ4Params<D>, pb);
+    for (int k = 0; k < 4; ++k) lds_words<D>(par + ((k >> 1) * 8 + (k & 1)) * kQ4Params<D>, pv[k]);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const float s0 = scale_of(pa[g]), s1 = scale_of(pb[g]);
-            const float m0 = fmaf(8.f, s0, min_of(pa[g])), m1 = fmaf(8.f, s1, min_of(pb[g]));
-            const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
-            const uint32_t lo = __byte_perm(v[0][g / 2], v[1][g / 2], sel);
-            const uint32_t hi = __byte_perm(v[2][g / 2], v[3][g / 2], sel);
-            const uint32_t a0 = centred<0>(lo), a1 = centred<1>(lo), a2 = centred<2>(lo), a3 = centred<3>(lo);
-            const uint32_t b0 = centred<0>(hi), b1 = centred<1>(hi), b2 = centred<2>(hi), b3 = centred<3>(hi);
+    for (int g = 0; g < G; ++g) {
+        const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
+        const uint32_t lo = __byte_perm(v[0][g / 2], v[1][g / 2], sel), hi = __byte_perm(v[2][g / 2], v[3][g / 2], sel);
+        const uint32_t s0 = __byte_perm(pv[0][g], pv[1][g], 0x5410), s1 = __byte_perm(pv[2][g], pv[3][g], 0x5410);
+        const uint32_t a0 = centred<0>(lo, R.bits), a1 = centred<1>(lo, R.bits);
+        const uint32_t a2 = centred<2>(lo, R.bits), a3 = centred<3>(lo, R.bits);
+        const uint32_t b0 = centred<0>(hi, R.bits), b1 = centred<1>(hi, R.bits);
+        const uint32_t b2 = centred<2>(hi, R.bits), b3 = centred<3>(hi, R.bits);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                uint32_t w0, w1;
-                if constexpr (MASK) {
-                    // a masked key's parameters may be anything (its p is 0): they are taken as 0, with the
-                    // arithmetic of the other branch, so that a row's bits do not depend on its tile's others
-                    const bool on0 = key0 + 16 * h + r <= R.pos[j][0], on1 = key0 + 16 * h + r <= R.pos[j][1];
-                    const bool on2 = key0 + 16 * h + 8 + r <= R.pos[j][0], on3 = key0 + 16 * h + 8 + r <= R.pos[j][1];
-                    q4_weigh(f2(x[j][h][0], x[j][h][1]), f2(x[j][h][2], x[j][h][3]),
-                             f2(on0 ? s0 : 0.f, on1 ? s0 : 0.f), f2(on2 ? s1 : 0.f, on3 ? s1 : 0.f),
-                             f2(on0 ? m0 : 0.f, on1 ? m0 : 0.f), f2(on2 ? m1 : 0.f, on3 ? m1 : 0.f), w0, w1,
-                             R.z[j][g]);
-                } else {
-                    q4_weigh(f2(x[j][h][0], x[j][h][1]), f2(x[j][h][2], x[j][h][3]), f2(s0, s0), f2(s1, s1),
-                             f2(m0, m0), f2(m1, m1), w0, w1, R.z[j][g]);
-                }
-                w0 = transpose8(w0);
-                w1 = transpose8(w1);
-                mma(R.o[j][2 * g], a0, a1, b0, b1, w0, w1);
-                mma(R.o[j][2 * g + 1], a2, a3, b2, b3, w0, w1);
+        for (int j = 0; j < NT; ++j) {
+            uint32_t w0 = mul_bf16(p[j][h][0], s0), w1 = mul_bf16(p[j][h][1], s1);
+            if constexpr (MASK) {
+                w0 &= keep0[j];
+                w1 &= keep1[j];
             }
+            mma(R.o[j][2 * g], a0, a1, b0, b1, w0, w1);
+            mma(R.o[j][2 * g + 1], a2, a3, b2, b3, w0, w1);
         }
     }
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) q4_direct_kernel(const DirectParams p) {
+__global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const DirectParams p) {
     constexpr int G = D / kQ4Group;
     constexpr int kCols = 8 * NT;
     using L = Ring<D>;
-    using J = Join<D, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ pa_work_item held[kHeld];
+    __shared__ int next_item;
     dependent_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, cc = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
-    float* const join = reinterpret_cast<float*>(smem);
     const int bs = 1 << p.log2bs, gq = 1 << p.log2g;
+    int first = p.lists[blockIdx.x], last = p.lists[blockIdx.x + 1];
+    if (first < 0 || last < first || last > p.n_items) {
+        if (threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+        first = last = 0;               // (n_items is far from where the counter would wrap)
+    }
+    if (threadIdx.x == 0) next_item = first;
+    // the list's first items, so that a warp that draws one has it at once
+    constexpr int kWords = sizeof(pa_work_item) / 4;
+    for (int i = threadIdx.x; i < min(last - first, kHeld) * kWords; i += 32 * kWarps<NT>)
+        reinterpret_cast<int32_t*>(held)[i] = reinterpret_cast<const int32_t*>(p.items + first)[i];
+    __syncthreads();
 
-    for (int idx = blockIdx.x; idx < p.n_items;) {
-        const pa_work_item it = p.items[idx];
-        if (it.n_q == 0) break;                                 // padding: no more work
-        // ---- the item against the metadata it points at
+    for (;;) {
+        int idx = 0;
+        if (lane == 0) idx = atomicAdd(&next_item, 1);
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+        if (idx < 0 || idx >= last) break;
+        const pa_work_item* const at_item = idx - first < kHeld ? held + (idx - first) : p.items + idx;
+        const pa_work_item it = *at_item;
+        // ---- The item by itself, then against the metadata it points at: what the loads of q, of the first blocks and
+        // of the metadata need is in the item (next: the context it was planned for), so that they
+        // are all on the way at once.
+        const int ctx = it.next;
         bool good = it.kind == PA_ITEM_DIRECT && it.seq >= 0 && it.seq < p.B && it.kv_head >= 0 &&
                     it.kv_head < p.Hkv && it.n_q > 0 && it.n_q <= (kCols >> p.log2g) && it.q_start >= 0 &&
                     it.q_start <= p.T - it.n_q && it.split >= 0 && it.n_splits > it.split &&
-                    it.tile0 >= 0 && it.tile0 <= p.n_items - it.n_splits;
-        int ctx = 0, pos0 = 0, k_begin = 0, k_end = 0;
-        if (good) {
-            ctx = p.ctx[it.seq];
-            const int cu0 = p.cu[it.seq], cu1 = p.cu[it.seq + 1];
-            good = ctx > 0 && ctx <= p.max_ctx && cu0 <= it.q_start && it.q_start + it.n_q <= cu1 &&
-                   int64_t(cu1) - cu0 <= ctx && (int64_t(ctx) + bs - 1) / bs <= p.max_blocks;
-            pos0 = ctx - cu1 + it.q_start;                      // position of the first row
-            const int keys = pos0 + it.n_q;                     // up to the last row
-            const int64_t len = good ? q4_split_keys(ctx) : 1;
-            good = good && (keys + len - 1) / len == it.n_splits;
-            k_begin = int(it.split * len);
-            k_end = int(min(int64_t(keys), k_begin + len));
+                    it.tile0 >= 0 && it.tile0 <= p.n_items - it.n_splits && ctx > 0 && ctx <= p.max_ctx &&
+                    (int64_t(ctx) + bs - 1) / bs <= p.max_blocks && it.split * q4_split_keys(ctx) < ctx;
+        if (!good) {
+            if (lane == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+            continue;
         }
-        if (!good && threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
-        if (good) {
+        {
+            const int ctx_now = __ldg(p.ctx + it.seq), cu0 = __ldg(p.cu + it.seq), cu1 = __ldg(p.cu + it.seq + 1);
+            const int len = int(q4_split_keys(ctx)), k_begin = it.split * len, k_last = min(ctx, k_begin + len);
+            const int32_t* table = p.table + int64_t(it.seq) * p.max_blocks;
+            // (the split's keys up to the context: the last row may lie before it)
+            const auto block_of = [&](int tile) {
+                const int key = k_begin + (tile + (lane >> 2)) * kKeys + 8 * (lane & 3);
+                return key < k_last ? max(__ldg(table + (key >> p.log2bs)), -1) : -2;
+            };
+            int block = block_of(0);
             const int rows = it.n_q << p.log2g;
-            Rows<D, NT> R;
+            uint4 qw[NT][G];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const int row = 8 * j + r;
-                const bool on = row < rows;
-                const __nv_bfloat16* src =
-                    p.q + (int64_t(it.q_start + (on ? row >> p.log2g : 0)) * p.Hq + it.kv_head * gq +
-                           (on ? row & (gq - 1) : 0)) * D;
+                const __nv_bfloat16* src = p.q + (int64_t(it.q_start + (row >> p.log2g)) * p.Hq + it.kv_head * gq +
+                                                  (row & (gq - 1))) * D + 8 * cc;
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (on) w = __ldg(reinterpret_cast<const uint4*>(src + 32 * g + 8 * cc));
-                    R.qb[j][g][0] = __byte_perm(w.x, w.z, 0x5410);      // columns 0, 4
-                    R.qb[j][g][1] = __byte_perm(w.x, w.z, 0x7632);      // 1, 5
-                    R.qb[j][g][2] = __byte_perm(w.y, w.w, 0x5410);      // 2, 6
-                    R.qb[j][g][3] = __byte_perm(w.y, w.w, 0x7632);      // 3, 7
-                    float s = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        s += scale_of(R.qb[j][g][i]) + min_of(R.qb[j][g][i]);
-                    s += __shfl_xor_sync(0xffffffffu, s, 1);
-                    s += __shfl_xor_sync(0xffffffffu, s, 2);
-                    R.qs[j][g] = f2(__shfl_sync(0xffffffffu, s, 8 * cc),
-                                    __shfl_sync(0xffffffffu, s, 8 * cc + 4));
-                    R.z[j][g] = 0;
-                }
-#pragma unroll
-                for (int t = 0; t < 2 * G; ++t)
-                    R.o[j][t][0] = R.o[j][t][1] = R.o[j][t][2] = R.o[j][t][3] = 0.f;
-                R.l[j] = 0;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    R.m[j][e] = -INFINITY;
-                    // rows behind the last one see what the last one sees
-                    R.pos[j][e] = pos0 + (min(8 * j + 2 * cc + e, rows - 1) >> p.log2g);
-                }
+                for (int g = 0; g < G; ++g)
+                    qw[j][g] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + 32 * g)) : make_uint4(0, 0, 0, 0);
             }
-            // ---- the warp's tiles: keys k_begin + 32 (warp + kWarps n)
-            const int n_keys = k_end - k_begin;
-            const int tiles = (n_keys + kKeys - 1) / kKeys;
-            const int n = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-            const int32_t* table = p.table + int64_t(it.seq) * p.max_blocks;
-            // lane i holds the block of eight keys i % 4 of tile i / 4 of the next eight tiles
-            const auto blocks_from = [&](int tile) {
-                const int key = k_begin + (warp + kWarps * (tile + (lane >> 2))) * kKeys + 8 * (lane & 3);
-                int b = -1;
-                if (tile + (lane >> 2) < n && key < k_end) {
-                    b = __ldg(table + (key >> p.log2bs));
-                    if (b < 0 || b >= p.num_blocks) {
-                        if (p.err) atomicOr(p.err, PA_DEVERR_BLOCK);
-                        b = -1;                                 // its keys read as 0
-                    }
-                }
-                return b;
+            const int pos0 = ctx - (cu1 - it.q_start);              // position of the first row
+            const int keys = pos0 + it.n_q;                         // up to the last row
+            good = ctx_now == ctx && cu0 <= it.q_start && it.q_start + it.n_q <= cu1 &&
+                   int64_t(cu1) - cu0 <= ctx && (keys + len - 1) / len == it.n_splits;
+            if (!good) {
+                if (lane == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+                continue;
+            }
+            const int k_end = min(keys, k_begin + len);
+            const int n = (k_end - k_begin + kKeys - 1) / kKeys;    // tiles of 32 keys
+            // Lane i looks after the eight keys i % 4 of tile i / 4 of eight tiles: where their code rows and their
+            // parameter rows begin, in units of 16 bytes, and (a bit of `there`) whether their block is there.
+            constexpr int kRow16 = kQ4Codes<D> / 16, kPar8 = 8 * kQ4Params<D> / 16;
+            uint32_t codes_at = 0, params_at = 0, there = 0;
+            const auto turn_to = [&](int tile) {                // the eight tiles from `tile` on
+                const int key = k_begin + (tile + (lane >> 2)) * kKeys + 8 * (lane & 3);
+                const bool on = block >= 0 && block < p.num_blocks;
+                if (!on && block != -2 && p.err) atomicOr(p.err, PA_DEVERR_BLOCK);   // its keys read as 0
+                there = __ballot_sync(0xffffffffu, on);
+                const int o = key & (bs - 1);
+                const uint32_t at = (uint32_t(on ? block : 0) * p.Hkv + it.kv_head) * (bs * kQ4Row<D> / 16);
+                codes_at = at + o * kRow16;
+                params_at = at + bs * kRow16 + (o >> 3) * kPar8;
+                block = block_of(tile + 8);
             };
-            int blocks = blocks_from(0), blocks_next = blocks_from(8);
+            constexpr int kPieces = kRow16;                     // 16-byte pieces of a code row
+            constexpr int kAtOnce = 32 / kPieces;               // keys the warp's lanes cover
+            // the lane's piece of a unit's eight code rows, in 16 bytes: K as it lies, V as q4_values reads it
+            const uint32_t k_lane = lane % (8 * kPieces);
+            const uint32_t v_lane = D == 128 ? ((lane & 6) + (lane >> 4)) * kPieces + ((lane >> 2) & 2) + (lane & 1)
+                                             : (lane & 6) * kPieces + ((lane >> 3) & 1) * kPieces + (lane & 1);
+            uint32_t stage_in = ring;
             const auto issue = [&](int tile) {
                 if (tile < n) {
-                    if (tile && (tile & 7) == 0) {
-                        blocks = blocks_next;
-                        blocks_next = blocks_from(tile + 8);
-                    }
-                    const int key0 = k_begin + (warp + kWarps * tile) * kKeys;
-                    const uint32_t stage = ring + (tile % L::kStages) * L::kStage;
-                    constexpr int kPieces = kQ4Codes<D> / 16;           // of a code row
-                    constexpr int kAtOnce = 32 / kPieces;               // keys the warp's lanes cover
-                    const int piece = lane % kPieces;
+                    if ((tile & 7) == 0) turn_to(tile);
+                    const int u0 = (tile & 7) * 4;
+                    const bool all = ((there >> u0) & 15u) == 15u;
 #pragma unroll
                     for (int i = 0; i < kKeys / kAtOnce; ++i) {
-                        const int place = i * kAtOnce + lane / kPieces;     // row in the stage
-                        const int b = __shfl_sync(0xffffffffu, blocks, (tile & 7) * 4 + place / 8);
-                        const int w = place & 7;
-                        // V: even keys of eight first (see q4_tile)
-                        const int v_key = (place & ~7) + (w < 4 ? 2 * w : 2 * w - 7);
-                        const int64_t at = q4_base<D>(b < 0 ? 0 : b, p.Hkv, it.kv_head, bs) + 16 * piece;
-                        cp_async<16>(stage + place * kQ4Codes<D> + 16 * piece,
-                                     p.k_pool + at + ((key0 + place) & (bs - 1)) * kQ4Codes<D>,
-                                     b >= 0 && key0 + place < k_end);
-                        cp_async<16>(stage + L::kCodes + place * kQ4Codes<D> + 16 * piece,
-                                     p.v_pool + at + ((key0 + v_key) & (bs - 1)) * kQ4Codes<D>,
-                                     b >= 0 && key0 + v_key < k_end);
+                        const int unit = u0 + (i * kAtOnce + lane / kPieces) / 8;
+                        const uint32_t at = __shfl_sync(0xffffffffu, codes_at, unit);
+                        const bool on = all || ((there >> unit) & 1u);
+                        const uint32_t to = stage_in + i * (kAtOnce * kQ4Codes<D>) + 16 * lane;
+                        cp_async<16>(to, p.k_pool + uint64_t(at + k_lane) * 16, on);
+                        cp_async<16>(to + L::kCodes, p.v_pool + uint64_t(at + v_lane) * 16, on);
                     }
-                    const int b = __shfl_sync(0xffffffffu, blocks, (tile & 7) * 4 + lane / 8);
-                    const int64_t at = q4_base<D>(b < 0 ? 0 : b, p.Hkv, it.kv_head, bs) +
-                                       bs * kQ4Codes<D> + ((key0 + lane) & (bs - 1)) * kQ4Params<D>;
-                    const uint32_t to = stage + 2 * L::kCodes + lane * kQ4Params<D>;
-                    const bool on = b >= 0 && key0 + lane < k_end;
-                    cp_async<kQ4Params<D>>(to, p.k_pool + at, on);
-                    cp_async<kQ4Params<D>>(to + L::kParams, p.v_pool + at, on);
+                    const uint32_t at = __shfl_sync(0xffffffffu, params_at, u0 + lane / 8);
+                    const bool on = all || ((there >> (u0 + lane / 8)) & 1u);
+                    const uint32_t to = stage_in + 2 * L::kCodes + lane * kQ4Params<D>;
+                    const int64_t par = int64_t(uint64_t(at) * 16) + (lane & 7) * kQ4Params<D>;
+                    cp_async<kQ4Params<D>>(to, p.k_pool + par, on);
+                    cp_async<kQ4Params<D>>(to + L::kParams, p.v_pool + par, on);
+                    stage_in = stage_in == ring + (L::kStages - 1) * L::kStage ? ring : stage_in + L::kStage;
                 }
                 cp_commit();
             };
 #pragma unroll
-            for (int i = 0; i < L::kStages - 1; ++i) issue(i);
-            for (int i = 0; i < n; ++i) {
-                cp_wait<L::kStages - 2>();
-                __syncwarp();                                   // every lane's copies, every lane done
-                issue(i + L::kStages - 1);
-                const int key0 = k_begin + (warp + kWarps * i) * kKeys;
-                const uint32_t stage = ring + (i % L::kStages) * L::kStage;
-                if (key0 + kKeys - 1 <= pos0) q4_tile<D, NT, false>(stage, R, p.c, key0, lane);
-                else q4_tile<D, NT, true>(stage, R, p.c, key0, lane);
+            for (int i = 0; i < L::kStages; ++i) issue(i);
+            // ---- Q, while the first tiles are on their way
+            Rows<D, NT> R;
+            R.bits = __shfl_sync(0xffffffffu, p.bits, 0);
+            R.pos0 = pos0;
+            R.rows = rows;
+            R.log2g = p.log2g;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) q4_take_q<D, NT>(R, qw[j], j, p.c, lane);
+            uint32_t stage = ring;
+            for (int i = 0, key0 = k_begin; i < n; ++i, key0 += kKeys) {
+                cp_wait<L::kStages - 1>();
+                __syncwarp();                                   // every lane's copies
+                float x[NT][2][4];
+                uint32_t prob[NT][2][2];
+                const bool masked = key0 + kKeys - 1 > pos0;
+                q4_scores<D, NT>(stage, R, 0, lane, x);
+                q4_scores<D, NT>(stage, R, 1, lane, x);
+                q4_softmax<D, NT>(R, x, masked, key0, lane, prob);
+                if (masked) {
+                    q4_values<D, NT, true>(stage, R, prob, 0, key0, lane);
+                    q4_values<D, NT, true>(stage, R, prob, 1, key0, lane);
+                } else {
+                    q4_values<D, NT, false>(stage, R, prob, 0, key0, lane);
+                    q4_values<D, NT, false>(stage, R, prob, 1, key0, lane);
+                }
+                __syncwarp();                                   // every lane has read the stage
+                issue(i + L::kStages);
+                stage = stage == ring + (L::kStages - 1) * L::kStage ? ring : stage + L::kStage;
             }
             cp_wait<0>();
-            // ---- join the warps: rows in shared memory, over the ring
-            __syncthreads();
+            // ---- the rows' results: finished where they have one split, else left for the fold
+            const pa_work_item done = *at_item;                     // (again: not kept in registers meanwhile)
+            const bool whole = done.n_splits == 1;
+            float* const part = p.part + int64_t(done.tile0 + done.split) * (kCols * (D + 2));
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 float l[2];
@@ -676,77 +796,40 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) q4_direct_kernel
                     l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
                     l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
                 }
-                float* to = join + (warp * kCols + 8 * j + 2 * cc) * J::kRow + 4 * r;
+                const float f[2] = {whole ? __frcp_rn(l[0]) : 1.f, whole ? __frcp_rn(l[1]) : 1.f};
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    float z[2];
-                    f2_split(R.z[j][g], z[0], z[1]);
 #pragma unroll
-                    for (int d = 4; d <= 16; d <<= 1) {
-                        z[0] += __shfl_xor_sync(0xffffffffu, z[0], d);
-                        z[1] += __shfl_xor_sync(0xffffffffu, z[1], d);
+                    for (int e = 0; e < 2; ++e) {
+                        const float z = __shfl_sync(0xffffffffu, R.z[j][e], 4 * g + cc);
+                        const int row = 8 * j + 2 * cc + e;
+                        if (row >= rows) continue;
+                        const float y[4] = {(R.o[j][2 * g][e] + z) * f[e], (R.o[j][2 * g][2 + e] + z) * f[e],
+                                            (R.o[j][2 * g + 1][e] + z) * f[e], (R.o[j][2 * g + 1][2 + e] + z) * f[e]};
+                        const int col = 32 * g + 4 * r;
+                        if (whole) {
+                            const int64_t at = (int64_t(done.q_start + (row >> p.log2g)) * p.Hq + done.kv_head * gq +
+                                                (row & (gq - 1))) * D + col;
+                            *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                        } else {
+                            *reinterpret_cast<float4*>(part + row * D + col) = make_float4(y[0], y[1], y[2], y[3]);
+                        }
                     }
+                }
+                if (r == 0 && !whole) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float4*>(to + e * J::kRow + 32 * g) =
-                            make_float4(R.o[j][2 * g][e] + z[e], R.o[j][2 * g][2 + e] + z[e],
-                                        R.o[j][2 * g + 1][e] + z[e], R.o[j][2 * g + 1][2 + e] + z[e]);
-                }
-                if (r == 0) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float2*>(join + J::kMl + (warp * kCols + 8 * j + 2 * cc + e) * 2) =
-                            make_float2(R.m[j][e], l[e]);
+                        *reinterpret_cast<float2*>(part + kCols * D + 2 * (8 * j + 2 * cc + e)) = make_float2(-R.nm[j][e], l[e]);
                 }
             }
-            __syncthreads();
-            constexpr int kPer = D / 4;                         // threads of a row
-            for (int u = threadIdx.x; u < rows * kPer; u += 32 * kWarps) {
-                const int row = u / kPer, col = (u % kPer) * 4;
-                float M = -INFINITY, Lsum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-                float2 ml[kWarps];
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    ml[w] = *reinterpret_cast<const float2*>(join + J::kMl + (w * kCols + row) * 2);
-                    M = fmaxf(M, ml[w].x);
-                }
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f = ml[w].x == -INFINITY ? 0.f : ex2((ml[w].x - M) * p.c);
-                    const float4 a = *reinterpret_cast<const float4*>(join + (w * kCols + row) * J::kRow + col);
-                    Lsum = fmaf(ml[w].y, f, Lsum);
-                    acc[0] = fmaf(a.x, f, acc[0]);
-                    acc[1] = fmaf(a.y, f, acc[1]);
-                    acc[2] = fmaf(a.z, f, acc[2]);
-                    acc[3] = fmaf(a.w, f, acc[3]);
-                }
-                if (it.n_splits == 1) {
-                    const float inv = __frcp_rn(Lsum);
-                    const int64_t at = (int64_t(it.q_start + (row >> p.log2g)) * p.Hq + it.kv_head * gq +
-                                        (row & (gq - 1))) * D + col;
-                    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(
-                        pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-                } else {
-                    float* part = p.part + int64_t(it.tile0 + it.split) * (kCols * (D + 2));
-                    *reinterpret_cast<float4*>(part + row * D + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    if (col == 0)
-                        *reinterpret_cast<float2*>(part + kCols * D + 2 * row) = make_float2(M, Lsum);
-                }
-            }
-            __syncthreads();                                    // the ring is free again
+            __syncwarp();                                       // the ring is free again
         }
-        if (it.next <= 0) break;
-        if (it.next <= idx || it.next >= p.n_items) {
-            if (threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
-            break;
-        }
-        idx = it.next;
     }
 }
 
 // Joins the splits of a tile of rows and head, in ascending order: one CTA per entry of the plan's fold
-// list (items of split 0 with more splits behind them), a warp per row at a time. A part whose row has no
-// key in its split holds m = -infinity and l = 0.
+// list (items of split 0 with more splits behind them), a warp per row at a time. Maxima are in base 2; a part
+// whose row has no key in its split holds -kNone and l = 0.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) q4_fold_kernel(const DirectParams p, const int32_t* fold) {
     constexpr int kCols = 8 * NT;
@@ -780,7 +863,7 @@ __global__ void __launch_bounds__(128) q4_fold_kernel(const DirectParams p, cons
     for (int u = threadIdx.x; u < rows * kPer; u += 128) {
         const int row = u / kPer, col = (u % kPer) * 4;
         const float* part = p.part + int64_t(it.tile0) * kPart;
-        float M = -INFINITY, Lsum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float M = -kNone, Lsum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
         for (int s0 = 0; s0 < it.n_splits; s0 += kBatch) {
             float2 ml[kBatch];
             float4 a[kBatch];
@@ -795,8 +878,7 @@ __global__ void __launch_bounds__(128) q4_fold_kernel(const DirectParams p, cons
             for (int i = 0; i < kBatch; ++i) {
                 if (s0 + i >= it.n_splits) break;
                 const float now = fmaxf(M, ml[i].x);
-                const float fa = M == -INFINITY ? 0.f : ex2((M - now) * p.c);
-                const float fb = ml[i].x == -INFINITY ? 0.f : ex2((ml[i].x - now) * p.c);
+                const float fa = ex2(M - now), fb = ex2(ml[i].x - now);
                 Lsum = Lsum * fa + ml[i].y * fb;
                 acc[0] = acc[0] * fa + a[i].x * fb;
                 acc[1] = acc[1] * fa + a[i].y * fb;
@@ -822,7 +904,7 @@ int32_t launch_direct(const DirectParams& p, const int32_t* fold, int32_t n_fold
     int32_t st = note_cuda(cudaGetDevice(&dev));
     if (st) return st;
     if (dev < 0 || dev >= kMaxDevices) return PA_ERR_INVALID;
-    constexpr int smem = kDirectSmem<D, NT>;
+    constexpr int smem = kWarps<NT> * Ring<D>::kWarp;
     if (!raised[dev].load(std::memory_order_acquire)) {
         st = note_cuda(cudaFuncSetAttribute(q4_direct_kernel<D, NT>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
@@ -830,8 +912,7 @@ int32_t launch_direct(const DirectParams& p, const int32_t* fold, int32_t n_fold
         raised[dev].store(true, std::memory_order_release);
     }
     cudaLaunchAttribute pdl;
-    const int lists = NT == 1 ? PA_Q4_LISTS_8 : PA_Q4_LISTS_16;
-    auto cfg = dependent_launch(&pdl, dim3(unsigned(std::min(p.n_items, lists))), 32 * kWarps, smem, stream);
+    auto cfg = dependent_launch(&pdl, dim3(PA_PLAN_CTAS), 32 * kWarps<NT>, smem, stream);
     st = note_cuda(cudaLaunchKernelEx(&cfg, q4_direct_kernel<D, NT>, p));
     if (st || n_fold == 0) return st;
     cfg = dependent_launch(&pdl, dim3(unsigned(n_fold)), 128, 0, stream);
@@ -957,6 +1038,10 @@ extern "C" int32_t paged_attention_step_q4(const void* q, const void* k_pool, co
         return PA_ERR_INVALID;
     if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return PA_ERR_INVALID;
     if (int64_t(shape->num_blocks) * shape->block_size > INT32_MAX) return PA_ERR_SHAPE;
+    // places in a pool are counted in 16 bytes, in 32 bits
+    if (int64_t(shape->num_blocks) * shape->num_kv_heads * (shape->block_size * (shape->head_dim / 8) * 5 / 16) >
+        int64_t(UINT32_MAX))
+        return PA_ERR_SHAPE;
     const Space w = space_of(shape, plan);
     if (w.total > 0 && (!workspace || ws_bytes < w.total)) return PA_ERR_WORKSPACE;
     if (w.total > 0 && !aligned16(workspace)) return PA_ERR_INVALID;
@@ -972,6 +1057,7 @@ extern "C" int32_t paged_attention_step_q4(const void* q, const void* k_pool, co
         p.cu = cu_seqlens_q;
         p.ctx = ctx_lens;
         p.items = reinterpret_cast<const pa_work_item*>(words + f.direct);
+        p.lists = words + f.lists;
         p.part = reinterpret_cast<float*>(at);
         p.out = static_cast<__nv_bfloat16*>(out);
         p.err = err_flag;
@@ -987,6 +1073,7 @@ extern "C" int32_t paged_attention_step_q4(const void* q, const void* k_pool, co
         // without a fold no row may have a second split: its part would have no place
         p.max_ctx = P.n_fold > 0 ? P.max_ctx : int32_t(std::min<int64_t>(P.max_ctx, q4_one_split()));
         p.c = float(1.4426950408889634 / std::sqrt(double(D)));
+        p.bits = 0x43004300u;
         const int32_t* fold = words + f.fold;
         const bool wide = P.direct_rows > 8;
         st = D == 128 ? (wide ? launch_direct<128, 2>(p, fold, P.n_fold, stream)

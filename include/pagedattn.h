@@ -124,7 +124,7 @@ typedef struct pa_work_item {
 #define PA_ITEM_GROUP 1
 #define PA_ITEM_RESUME 2
 /* Of a 4-bit step (pa_plan_step_q4): a tile of query rows read from the codes, one split of a length
- * of its own; n_splits counts the tile's splits, tile0 is the item's place among their results. */
+ * of its own; n_splits counts the tile's splits, tile0 is the place of its results among all items', next the context. */
 #define PA_ITEM_DIRECT 3
 
 /* ---------------------------------------------------------------- library ---------- */
