@@ -9,7 +9,10 @@ The library is loaded on first use from this package's directory; a missing libr
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
+import itertools
+import operator
 import os
 import threading
 from typing import Optional
@@ -572,6 +575,7 @@ class _Runtime:
         self.lib = load()
         self.bf16, self.u8, self.i32 = torch.bfloat16, torch.uint8, torch.int32
         self.i64, self.f32 = torch.int64, torch.float32
+        self.Tensor, self.nbytes = torch.Tensor, operator.attrgetter("nbytes")
         self.device = torch.cuda.current_device
         # the raw handle of the current stream, without a Stream object around it
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -996,16 +1000,22 @@ def paged_copy_pages(pairs, pools, err=None, stream=None) -> None:
     (of all layers, K and V), all with the same number of blocks."""
     rt = _rt()
     dev = rt.device()
-    n = pairs.shape[0]
-    blocks = pools[0].shape[0] if len(pools) else 0
-    a = (Pages * max(len(pools), 1))()
-    for i, t in enumerate(pools):
-        if t.shape[0] != blocks or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"pools[{i}]: expected a contiguous tensor of {blocks} blocks on the "
-                             f"current CUDA device ({dev})")
-        a[i].pool = t.data_ptr()
-        a[i].page_bytes = t.numel() // max(blocks, 1) * t.element_size()
-    _check(rt.lib.paged_copy_pages(_arg(pairs, rt.i32, dev, (n, 2), "pairs"), n, a, len(pools), blocks,
+    n, m = pairs.shape[0], len(pools)
+    # one pass of a method over all pools at a time: a fork's few pages take less than a loop over them would
+    T = rt.Tensor
+    blocks = set(map(T.size, pools, itertools.repeat(0))) or {0}
+    if len(blocks) > 1 or not all(map(T.is_contiguous, pools)) or set(map(T.get_device, pools)) - {dev}:
+        raise ValueError(f"pools: expected contiguous tensors of the same number of blocks on the current "
+                         f"CUDA device ({dev})")
+    blocks, = blocks
+    words = array.array("q", bytes(16 * max(m, 1)))
+    if m:
+        words[0::2] = array.array("q", map(T.data_ptr, pools))
+        per, sizes = max(blocks, 1), list(map(rt.nbytes, pools))
+        same = min(sizes) == max(sizes)
+        words[1::2] = array.array("q", [sizes[0] // per]) * m if same else array.array("q", [x // per for x in sizes])
+    a = (Pages * max(m, 1)).from_buffer(words)
+    _check(rt.lib.paged_copy_pages(_arg(pairs, rt.i32, dev, (n, 2), "pairs"), n, a, m, blocks,
                                    None if err is None else _arg(err, rt.i32, dev, (1,), "err"),
                                    rt.stream(stream, dev)), "paged_copy_pages")
 

@@ -56,7 +56,7 @@ struct RopeParams {
     int32_t* err;
     int32_t T, Hq, Hkv, n_pairs, n_axes;
     int32_t warps;                             // per token
-    int32_t bs;                                // tokens a block (4-bit pools)
+    int32_t log2bs;                            // of the tokens a block (4-bit pools)
     float eps, k_scale, v_scale;
 };
 
@@ -265,10 +265,10 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeParams
                     q4_quantise8(w, codes, params);
                     if constexpr (K == kV) codes = q4_pair_groups(codes, l);
                     if (h >= heads) continue;
-                    const int block = slot / p.bs;
+                    const int block = slot >> p.log2bs;
                     q4_store_row<D, K == kV>(static_cast<uint8_t*>(K == kV ? p.v_pool : p.k_pool),
-                                             q4_base<D>(block, p.Hkv, h, p.bs), p.bs,
-                                             slot - block * p.bs, l, codes, params);
+                                             q4_base<D>(block, p.Hkv, h, 1 << p.log2bs), 1 << p.log2bs,
+                                             slot - (block << p.log2bs), l, codes, params);
                     continue;
                 }
                 if (h >= heads) continue;
@@ -381,7 +381,8 @@ int32_t norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stri
     p.eps = eps;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    p.bs = shape->block_size;
+    p.log2bs = 0;
+    while ((1 << p.log2bs) < shape->block_size) ++p.log2bs;
     const auto launch = [&](auto held) {
         constexpr Cache C = decltype(held)::value;
         if (D == 128)

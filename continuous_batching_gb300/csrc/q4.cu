@@ -23,6 +23,12 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
+int ilog2(int x) {
+    int n = 0;
+    while ((1 << n) < x) ++n;
+    return n;
+}
+
 cudaLaunchConfig_t dependent_launch(cudaLaunchAttribute* pdl, dim3 grid, int threads, size_t smem,
                                     cudaStream_t stream) {
     pdl->id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -50,8 +56,9 @@ struct RowsParams {
     int64_t k_stride, v_stride;         // elements between tokens
     const int32_t* slots;
     uint8_t *k_pool, *v_pool;
-    int64_t num_slots, rows;            // rows: T * Hkv
-    int32_t Hkv, bs;
+    int64_t num_slots;
+    uint32_t rows;                      // T * Hkv
+    int32_t Hkv, log2bs;
     int32_t* err;
 };
 
@@ -65,21 +72,21 @@ __global__ void __launch_bounds__(kRowsThreads) q4_write_kernel(const RowsParams
     constexpr int kLanes = D / 8;
     constexpr int kGroups = kRowsThreads / kLanes;
     dependent_start();
-    const int l = threadIdx.x % kLanes;
-    const int64_t row0 = int64_t(blockIdx.x) * (kGroups * kRowsPer) + threadIdx.x / kLanes;
+    const int l = threadIdx.x % kLanes, bs = 1 << p.log2bs;
+    const uint32_t row0 = blockIdx.x * uint32_t(kGroups * kRowsPer) + threadIdx.x / kLanes;
     uint4 k[kRowsPer], v[kRowsPer];
     int32_t slot[kRowsPer];
     int head[kRowsPer];
 #pragma unroll
     for (int i = 0; i < kRowsPer; ++i) {
-        const int64_t row = row0 + i * kGroups;
+        const uint32_t row = row0 + i * kGroups;
         slot[i] = -1;
         if (row < p.rows) {
-            const int64_t t = row / p.Hkv;
-            head[i] = int(row - t * p.Hkv);
+            const uint32_t t = row / uint32_t(p.Hkv);
+            head[i] = int(row - t * uint32_t(p.Hkv));
             slot[i] = p.slots[t];
-            k[i] = *reinterpret_cast<const uint4*>(p.k + t * p.k_stride + head[i] * D + 8 * l);
-            v[i] = *reinterpret_cast<const uint4*>(p.v + t * p.v_stride + head[i] * D + 8 * l);
+            k[i] = *reinterpret_cast<const uint4*>(p.k + int64_t(t) * p.k_stride + head[i] * D + 8 * l);
+            v[i] = *reinterpret_cast<const uint4*>(p.v + int64_t(t) * p.v_stride + head[i] * D + 8 * l);
             if (slot[i] >= p.num_slots) {
                 if (l == 0 && p.err) atomicOr(p.err, PA_DEVERR_SLOT);
                 slot[i] = -1;
@@ -95,10 +102,10 @@ __global__ void __launch_bounds__(kRowsThreads) q4_write_kernel(const RowsParams
         q4_quantise8({v[i].x, v[i].y, v[i].z, v[i].w}, vc, vp);
         vc = q4_pair_groups(vc, l);
         if (slot[i] < 0) continue;
-        const int block = slot[i] / p.bs, o = slot[i] - block * p.bs;
-        const int64_t at = q4_base<D>(block, p.Hkv, head[i], p.bs);
-        q4_store_row<D, false>(p.k_pool, at, p.bs, o, l, kc, kp);
-        q4_store_row<D, true>(p.v_pool, at, p.bs, o, l, vc, vp);
+        const int block = slot[i] >> p.log2bs, o = slot[i] & (bs - 1);
+        const int64_t at = q4_base<D>(block, p.Hkv, head[i], bs);
+        q4_store_row<D, false>(p.k_pool, at, bs, o, l, kc, kp);
+        q4_store_row<D, true>(p.v_pool, at, bs, o, l, vc, vp);
     }
 }
 
@@ -116,18 +123,18 @@ __global__ void __launch_bounds__(kRowsThreads) q4_read_kernel(const RowsParams 
     constexpr int kLanes = D / 8;
     constexpr int kGroups = kRowsThreads / kLanes;
     dependent_start();
-    const int l = threadIdx.x % kLanes;
-    const int64_t row0 = int64_t(blockIdx.x) * (kGroups * kRowsPer) + threadIdx.x / kLanes;
+    const int l = threadIdx.x % kLanes, bs = 1 << p.log2bs;
+    const uint32_t row0 = blockIdx.x * uint32_t(kGroups * kRowsPer) + threadIdx.x / kLanes;
     uint32_t kc[kRowsPer], kp[kRowsPer], vc[kRowsPer], vp[kRowsPer];
     bool on[kRowsPer];
 #pragma unroll
     for (int i = 0; i < kRowsPer; ++i) {
-        const int64_t row = row0 + i * kGroups;
+        const uint32_t row = row0 + i * kGroups;
         kc[i] = kp[i] = vc[i] = vp[i] = 0;
         on[i] = false;
         if (row >= p.rows) continue;
-        const int64_t t = row / p.Hkv;
-        const int head = int(row - t * p.Hkv);
+        const uint32_t t = row / uint32_t(p.Hkv);
+        const int head = int(row - t * uint32_t(p.Hkv));
         const int32_t slot = p.slots[t];
         if (slot < 0) continue;
         if (slot >= p.num_slots) {
@@ -135,10 +142,10 @@ __global__ void __launch_bounds__(kRowsThreads) q4_read_kernel(const RowsParams 
             continue;
         }
         on[i] = true;
-        const int block = slot / p.bs, o = slot - block * p.bs;
-        const int64_t at = q4_base<D>(block, p.Hkv, head, p.bs);
+        const int block = slot >> p.log2bs, o = slot & (bs - 1);
+        const int64_t at = q4_base<D>(block, p.Hkv, head, bs);
         const int64_t codes = at + o * kQ4Codes<D>;
-        const int64_t params = at + p.bs * kQ4Codes<D> + o * kQ4Params<D>;
+        const int64_t params = at + bs * kQ4Codes<D> + o * kQ4Params<D>;
         kc[i] = reinterpret_cast<const uint32_t*>(p.k_pool + codes)[q4_word<D, false>(l)];
         vc[i] = reinterpret_cast<const uint32_t*>(p.v_pool + codes)[q4_word<D, true>(l)];
         kp[i] = reinterpret_cast<const uint32_t*>(p.k_pool + params)[l >> 2];
@@ -148,7 +155,7 @@ __global__ void __launch_bounds__(kRowsThreads) q4_read_kernel(const RowsParams 
     for (int i = 0; i < kRowsPer; ++i) {
         const uint32_t v = q4_pair_groups(vc[i], l);
         if (!on[i]) continue;
-        const int64_t to = (row0 + i * kGroups) * D + 8 * l;
+        const int64_t to = int64_t(row0 + i * kGroups) * D + 8 * l;
         *reinterpret_cast<uint4*>(p.k_out + to) = q4_expand8(kc[i], kp[i]);
         *reinterpret_cast<uint4*>(p.v_out + to) = q4_expand8(v, vp[i]);
     }
@@ -164,7 +171,7 @@ struct ExpandParams {
     int32_t* ex_ctx;                    // [B]: the context of the sequences that are expanded, else 0
     __nv_bfloat16 *k_out, *v_out;       // [n][128][Hkv][D]
     int32_t* err;
-    int32_t n, B, cols, max_blocks, num_blocks, Hkv, g, bs, direct_rows;
+    int32_t n, B, cols, max_blocks, num_blocks, Hkv, g, log2bs, direct_rows;
 };
 
 // CTA (i, h): block i of the plan's list, head h: 128 tokens of K and V to bf16, one rounding each.
@@ -176,6 +183,7 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
     constexpr int kLanes = D / 8;
     constexpr int kGroups = 256 / kLanes;
     dependent_start();
+    const int bs = 1 << p.log2bs;
     const int64_t id = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
     for (int64_t s = id; s < p.B; s += int64_t(gridDim.x) * gridDim.y * 256) {
         const int64_t n_q = int64_t(p.cu[s + 1]) - p.cu[s];
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
     const int head = blockIdx.y;
     const int ctx = seq < p.B ? p.ctx[seq] : 0;
     if (seq >= p.B || first < 0 || int64_t(first) * 128 >= ctx ||
-        (int64_t(ctx) + p.bs - 1) / p.bs > p.max_blocks) {
+        (int64_t(ctx) + bs - 1) / bs > p.max_blocks) {
         if (threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
         return;
     }
@@ -203,12 +211,12 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
         uint32_t kc = 0, vc = 0, kp = 0, vp = 0;
         bool on = key < ctx;
         if (on) {
-            const int32_t block = table[key / p.bs];
+            const int32_t block = table[key >> p.log2bs];
             if (block >= 0 && block < p.num_blocks) {
-                const int o = key % p.bs;
-                const int64_t at = q4_base<D>(block, p.Hkv, head, p.bs);
+                const int o = key & (bs - 1);
+                const int64_t at = q4_base<D>(block, p.Hkv, head, bs);
                 const int64_t codes = at + o * kQ4Codes<D>;
-                const int64_t params = at + p.bs * kQ4Codes<D> + o * kQ4Params<D>;
+                const int64_t params = at + bs * kQ4Codes<D> + o * kQ4Params<D>;
                 kc = reinterpret_cast<const uint32_t*>(p.k_pool + codes)[q4_word<D, false>(l)];
                 vc = reinterpret_cast<const uint32_t*>(p.v_pool + codes)[q4_word<D, true>(l)];
                 kp = reinterpret_cast<const uint32_t*>(p.k_pool + params)[l >> 2];
@@ -919,12 +927,6 @@ int32_t launch_direct(const DirectParams& p, const int32_t* fold, int32_t n_fold
     return note_cuda(cudaLaunchKernelEx(&cfg, q4_fold_kernel<D, NT>, p, fold));
 }
 
-int ilog2(int x) {
-    int n = 0;
-    while ((1 << n) < x) ++n;
-    return n;
-}
-
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int32_t check_rows(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -944,13 +946,14 @@ int32_t launch_rows(RowsParams& p, int32_t T, const int32_t* slots, void* k_pool
     p.k_pool = static_cast<uint8_t*>(k_pool);
     p.v_pool = static_cast<uint8_t*>(v_pool);
     p.num_slots = int64_t(shape->num_blocks) * shape->block_size;
-    p.rows = int64_t(T) * shape->num_kv_heads;
+    const int64_t rows = int64_t(T) * shape->num_kv_heads;
+    if (rows > INT32_MAX) return PA_ERR_SHAPE;
+    p.rows = uint32_t(rows);
     p.Hkv = shape->num_kv_heads;
-    p.bs = shape->block_size;
+    p.log2bs = ilog2(shape->block_size);
     p.err = err;
     const int per = kRowsThreads / (shape->head_dim / 8) * kRowsPer;
-    const int64_t blocks = (p.rows + per - 1) / per;
-    if (blocks > INT32_MAX) return PA_ERR_SHAPE;
+    const int64_t blocks = (rows + per - 1) / per;
     cudaLaunchAttribute pdl;
     auto cfg = dependent_launch(&pdl, dim3(unsigned(blocks)), kRowsThreads, 0, stream);
     if (shape->head_dim == 128)
@@ -1102,7 +1105,7 @@ extern "C" int32_t paged_attention_step_q4(const void* q, const void* k_pool, co
     e.num_blocks = shape->num_blocks;
     e.Hkv = Hkv;
     e.g = g;
-    e.bs = shape->block_size;
+    e.log2bs = ilog2(shape->block_size);
     e.direct_rows = P.direct_rows;
     cudaLaunchAttribute pdl;
     auto cfg = dependent_launch(&pdl, dim3(unsigned(P.n_expand), unsigned(Hkv)), 256, 0, stream);

@@ -176,3 +176,23 @@ def test_norm_rotation_and_write_is_the_bf16_form_quantised(D, rot, inter, norm,
     rows = [bits_of(p).reshape(nb * bs, Hkv, D)[slots] for p in plain]
     assert np.array_equal(kp.cpu().numpy(), q4.write(k0, rows[0], slots, bs, False))
     assert np.array_equal(vp.cpu().numpy(), q4.write(v0, rows[1], slots, bs, True))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -60, 2.0 ** -92, 2.0 ** -126, 2.0 ** -131, 2.0 ** 60, 2.0 ** 89, 2.0 ** 122])
+def test_codes_at_every_magnitude(scale):
+    """Values of a few bits (their quotients fall on ties often), groups whose scale is subnormal or large,
+    and groups around an offset."""
+    rng = np.random.default_rng(17)
+    T, Hkv, D, bs = 512, 4, 128, 16
+    x = rng.integers(-24, 25, (T, Hkv, D)).astype(np.float64)
+    x[::3] = rng.integers(-7, 8, x[::3].shape) * 0.5 + 3.0
+    x[1::3] = rng.standard_normal(x[1::3].shape) * 4
+    bits = wl.f32_to_bf16_bits((x * scale).astype(np.float32))
+    sh = bd.Shape.make(Hkv, Hkv, D, bs, T // bs)
+    kp, vp = pools(rng, T // bs, Hkv, bs, D)
+    slots = np.arange(T, dtype=np.int32)
+    bd.paged_kv_write_q4(bf16(bits), bf16(bits), dev(slots), kp, vp, sh)
+    for pool, is_v in ((kp, False), (vp, True)):
+        want = q4.write(q4.empty_pool(T // bs, Hkv, bs, D), bits, slots, bs, is_v)
+        assert np.array_equal(pool.cpu().numpy(), want)
