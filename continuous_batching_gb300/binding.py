@@ -74,7 +74,7 @@ PA_ITEM_PLAIN, PA_ITEM_GROUP, PA_ITEM_RESUME, PA_ITEM_DIRECT = 0, 1, 2, 3
 
 class Q4Sizes(C.Structure):
     """pa_q4_plan: the sizes of a 4-bit step's plan."""
-    _fields_ = [(n, C.c_int32) for n in ("B", "T", "max_ctx", "direct_rows", "n_direct", "n_fold",
+    _fields_ = [(n, C.c_int32) for n in ("B", "T", "max_ctx", "direct_rows", "n_direct", "n_fold", "fold_rows",
                                          "n_chunk", "n_expand", "expand_cols", "words")]
 
 

@@ -708,7 +708,7 @@ struct Q4Parts {
     std::vector<pa_work_item> direct, chunk;
     std::vector<Unit> direct_units, chunk_units;
     std::vector<int32_t> list;              // (sequence, 128-token block) of the expanded contexts
-    int32_t tiles_folded = 0;
+    int32_t tiles_folded = 0, fold_rows = 0;
 };
 
 int32_t q4_tile_rows(int32_t direct_rows) { return direct_rows > 8 ? 16 : 8; }
@@ -737,6 +737,7 @@ int32_t q4_parts(const pa_shape* shape, int32_t B, const int32_t* cu, const int3
             const int64_t keys = int64_t(ctx[s]) - n + t0 + nt;
             const int32_t splits = int32_t((keys + len - 1) / len);
             out.tiles_folded += splits > 1;
+            if (splits > 1) out.fold_rows = std::max(out.fold_rows, nt * g);
             if (int64_t(out.direct.size()) + int64_t(splits) * shape->num_kv_heads > (int64_t(1) << 26))
                 return PA_ERR_SHAPE;
             for (int32_t h = 0; h < shape->num_kv_heads; ++h) {
@@ -790,7 +791,8 @@ int32_t pa_detail::check_q4_plan(const pa_shape* shape, const pa_q4_plan& p) {
         p.n_chunk < 0 || p.n_expand < 0 || p.expand_cols < 0)
         return PA_ERR_INVALID;
     if (p.n_direct > 0 && p.direct_rows < g) return PA_ERR_INVALID;
-    if (p.n_fold > p.n_direct || (p.n_chunk > 0) != (p.n_expand > 0) ||
+    if (p.n_fold > p.n_direct || p.fold_rows < 0 || p.fold_rows > q4_tile_rows(p.direct_rows) ||
+        (p.n_fold > 0) != (p.fold_rows > 0) || (p.n_chunk > 0) != (p.n_expand > 0) ||
         (p.n_chunk > 0 && p.expand_cols == 0))
         return PA_ERR_INVALID;
     if (int64_t(p.n_expand) * 128 > INT32_MAX) return PA_ERR_SHAPE;
@@ -823,6 +825,7 @@ int32_t pa_q4_plan_size(const pa_shape* shape, int32_t B, const int32_t* cu, con
     p.direct_rows = direct_rows;
     p.n_direct = int32_t(parts.direct.size());
     p.n_fold = parts.tiles_folded * shape->num_kv_heads;
+    p.fold_rows = parts.fold_rows;
     p.n_chunk = int32_t(parts.chunk.size());
     p.n_expand = int32_t(parts.list.size() / 2);
     p.expand_cols = p.n_chunk > 0 ? int32_t(blocks_for(p.max_ctx, 128)) : 0;
@@ -851,6 +854,7 @@ int32_t pa_q4_plan_limits(const pa_shape* shape, int32_t B, int32_t T, int32_t m
         if (heads * splits > (int64_t(1) << 26)) return PA_ERR_SHAPE;
         p.n_direct = int32_t(heads * splits);
         p.n_fold = splits > 1 ? int32_t(heads) : 0;
+        p.fold_rows = splits > 1 ? int32_t(std::min<int64_t>(tokens, direct_rows / g) * g) : 0;
     }
     if (max_expand > 0 && T > 0 && max_ctx > 0) {
         if (max_expand > INT32_MAX / 128) return PA_ERR_SHAPE;
@@ -881,7 +885,7 @@ int32_t pa_plan_step_q4(const pa_shape* shape, int32_t B, const int32_t* cu, con
     if ((st = q4_parts(shape, B, cu, ctx, plan->direct_rows, parts))) return st;
     if (int64_t(parts.direct.size()) > plan->n_direct || int64_t(parts.chunk.size()) > plan->n_chunk ||
         int64_t(parts.list.size() / 2) > plan->n_expand ||
-        int64_t(parts.tiles_folded) * shape->num_kv_heads > plan->n_fold)
+        int64_t(parts.tiles_folded) * shape->num_kv_heads > plan->n_fold || parts.fold_rows > plan->fold_rows)
         return PA_ERR_INVALID;
     if (plan->words == 0) return PA_OK;
     std::memset(words, 0, size_t(plan->words) * 4);             // items with n_q == 0: padding

@@ -645,7 +645,9 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ pa_work_item held[kHeld];
     __shared__ int next_item;
-    dependent_start();
+    // (in this order: q4_fold_kernel reads the metadata before it waits for this kernel)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, cc = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
@@ -835,78 +837,106 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
     }
 }
 
-// Joins the splits of a tile of rows and head, in ascending order: one CTA per entry of the plan's fold
-// list (items of split 0 with more splits behind them), a warp per row at a time. Maxima are in base 2; a part
-// whose row has no key in its split holds -kNone and l = 0.
+// Joins the splits of the rows of a tile and head: a warp per row, CTAs of the plan's fold list (items of split 0 with
+// more splits behind them). Eight splits are joined in ascending order, then the eights, likewise: an order that
+// the number of splits alone decides. Maxima are in base 2; a part whose row has no key in its split holds -kNone
+// and l = 0.
+//
+// Bound by latency: the way to the parts (list, item, metadata) lies before the wait for the direct kernel, the loads
+// of the next eight are on their way while one is joined, and the CTAs are few (a CTA per row, or per tile and eight,
+// took twice as long; the last warp of a tile doing this inside the direct kernel 20 to 40 us, row after row).
+constexpr int kFoldWarps = 4, kEight = 8;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(128) q4_fold_kernel(const DirectParams p, const int32_t* fold) {
-    constexpr int kCols = 8 * NT;
-    constexpr int kPart = kCols * (D + 2);
-    constexpr int kBatch = 8;
-    dependent_start();
+__global__ void __launch_bounds__(32 * kFoldWarps) q4_fold_kernel(const DirectParams p, const int32_t* fold) {
+    constexpr int kCols = 8 * NT, kPart = kCols * (D + 2), kLane = D / 32;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // (what precedes the direct kernel has completed before this one starts, and that one writes none of these)
     const int idx = fold[blockIdx.x];
     if (idx < 0) return;                                        // padding
-    if (idx >= p.n_items) {
-        if (threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+    const pa_work_item it = p.items[min(idx, p.n_items - 1)];
+    const int row = blockIdx.y * kFoldWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const bool good = idx < p.n_items && it.kind == PA_ITEM_DIRECT && it.split == 0 && it.n_splits >= 2 && it.tile0 >= 0 &&
+                      it.tile0 <= p.n_items - it.n_splits && it.n_q >= 1 && it.n_q <= (kCols >> p.log2g) &&
+                      it.q_start >= 0 && it.q_start <= p.T - it.n_q && it.kv_head >= 0 && it.kv_head < p.Hkv &&
+                      it.seq >= 0 && it.seq < p.B;
+    if (!good) {
+        if (row == 0 && lane == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
         return;
     }
-    const pa_work_item it = p.items[idx];
-    if (it.kind != PA_ITEM_DIRECT || it.split != 0 || it.n_splits < 2 || it.tile0 < 0 ||
-        it.tile0 > p.n_items - it.n_splits || it.n_q < 1 || it.n_q > (kCols >> p.log2g) ||
-        it.q_start < 0 || it.q_start > p.T - it.n_q || it.kv_head < 0 || it.kv_head >= p.Hkv ||
-        it.seq < 0 || it.seq >= p.B) {
-        if (threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
-        return;
-    }
+    if (row >= it.n_q << p.log2g) return;
     // an item that the direct kernel refused has left no parts
     const int ctx = p.ctx[it.seq], cu0 = p.cu[it.seq], cu1 = p.cu[it.seq + 1];
-    if (ctx <= 0 || ctx > p.max_ctx || cu0 > it.q_start || it.q_start + it.n_q > cu1 ||
+    if (ctx <= 0 || ctx != it.next || ctx > p.max_ctx || cu0 > it.q_start || it.q_start + it.n_q > cu1 ||
         int64_t(cu1) - cu0 > ctx)
         return;
-    const int64_t keys = ctx - cu1 + it.q_start + it.n_q, len = q4_split_keys(ctx);
+    const int64_t keys = ctx - (cu1 - it.q_start) + it.n_q, len = q4_split_keys(ctx);
     if ((keys + len - 1) / len != it.n_splits || (int64_t(ctx) + (1 << p.log2bs) - 1) >> p.log2bs > p.max_blocks)
         return;
-    const int gq = 1 << p.log2g, rows = it.n_q << p.log2g;
-    constexpr int kPer = D / 4;
-    for (int u = threadIdx.x; u < rows * kPer; u += 128) {
-        const int row = u / kPer, col = (u % kPer) * 4;
-        const float* part = p.part + int64_t(it.tile0) * kPart;
-        float M = -kNone, Lsum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int s0 = 0; s0 < it.n_splits; s0 += kBatch) {
-            float2 ml[kBatch];
-            float4 a[kBatch];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int n_splits = it.n_splits;
+    const float* const part = p.part + int64_t(it.tile0) * kPart + row * D + kLane * lane;
+    const float* const stat = p.part + int64_t(it.tile0) * kPart + kCols * D + 2 * row;
+    float a[2][kEight][kLane];
+    float2 ml[2];
+    // lane i has (m, l) of the eight's split i; those behind the last weigh nothing
+    const auto load = [&](int s0, float (&a)[kEight][kLane], float2& ml) {
+        ml = make_float2(-kNone, 0.f);
+        if (s0 + lane < n_splits && lane < kEight) ml = *reinterpret_cast<const float2*>(stat + int64_t(s0 + lane) * kPart);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (s0 + i < it.n_splits) {
-                    const float* from = part + int64_t(s0 + i) * kPart;
-                    a[i] = *reinterpret_cast<const float4*>(from + row * D + col);
-                    ml[i] = *reinterpret_cast<const float2*>(from + kCols * D + 2 * row);
-                }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (s0 + i >= it.n_splits) break;
-                const float now = fmaxf(M, ml[i].x);
-                const float fa = ex2(M - now), fb = ex2(ml[i].x - now);
-                Lsum = Lsum * fa + ml[i].y * fb;
-                acc[0] = acc[0] * fa + a[i].x * fb;
-                acc[1] = acc[1] * fa + a[i].y * fb;
-                acc[2] = acc[2] * fa + a[i].z * fb;
-                acc[3] = acc[3] * fa + a[i].w * fb;
-                M = now;
+        for (int i = 0; i < kEight; ++i) {
+            if (s0 + i >= n_splits) continue;
+            if constexpr (kLane == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(part + int64_t(s0 + i) * kPart);
+                a[i][0] = v.x, a[i][1] = v.y, a[i][2] = v.z, a[i][3] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(part + int64_t(s0 + i) * kPart);
+                a[i][0] = v.x, a[i][1] = v.y;
             }
         }
-        const float inv = __frcp_rn(Lsum);
-        const int64_t at = (int64_t(it.q_start + (row >> p.log2g)) * p.Hq + it.kv_head * gq +
-                            (row & (gq - 1))) * D + col;
-        *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
-                                                           pack_bf16(acc[2] * inv, acc[3] * inv));
+    };
+    float M = -kNone, Lsum = 0.f, sum[kLane] = {};
+    const auto join = [&](int s0, const float (&a)[kEight][kLane], float2 ml) {
+        float m = ml.x;
+#pragma unroll
+        for (int d = 1; d < kEight; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        m = __shfl_sync(0xffffffffu, m, 0);
+        const float f = ex2(ml.x - m), fl = f * ml.y;
+        float l = 0.f, out[kLane] = {};
+#pragma unroll
+        for (int i = 0; i < kEight; ++i) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            l += __shfl_sync(0xffffffffu, fl, i);
+            if (s0 + i >= n_splits) continue;
+#pragma unroll
+            for (int c = 0; c < kLane; ++c) out[c] = fmaf(a[i][c], fi, out[c]);
+        }
+        const float now = fmaxf(M, m), fa = ex2(M - now), fb = ex2(m - now);
+        Lsum = Lsum * fa + l * fb;
+#pragma unroll
+        for (int c = 0; c < kLane; ++c) sum[c] = sum[c] * fa + out[c] * fb;
+        M = now;
+    };
+    load(0, a[0], ml[0]);
+    for (int s0 = 0; s0 < n_splits; s0 += 2 * kEight) {
+        load(s0 + kEight, a[1], ml[1]);
+        join(s0, a[0], ml[0]);
+        load(s0 + 2 * kEight, a[0], ml[0]);
+        if (s0 + kEight < n_splits) join(s0 + kEight, a[1], ml[1]);
     }
+    const float inv = __frcp_rn(Lsum);
+    __nv_bfloat16* const out = p.out + (int64_t(it.q_start + (row >> p.log2g)) * p.Hq + (it.kv_head << p.log2g) +
+                                        (row & ((1 << p.log2g) - 1))) * D + kLane * lane;
+#pragma unroll
+    for (int c = 0; c < kLane; c += 2)
+        *reinterpret_cast<uint32_t*>(out + c) = pack_bf16(sum[c] * inv, sum[c + 1] * inv);
 }
 
 // ------------------------------------------------------------------------------- host side
 
 template <int D, int NT>
-int32_t launch_direct(const DirectParams& p, const int32_t* fold, int32_t n_fold, cudaStream_t stream) {
+int32_t launch_direct(const DirectParams& p, const int32_t* fold, int32_t n_fold, int32_t fold_rows,
+                      cudaStream_t stream) {
     static std::atomic<bool> raised[kMaxDevices];               // zero-initialised: not raised yet
     int dev = 0;
     int32_t st = note_cuda(cudaGetDevice(&dev));
@@ -923,7 +953,7 @@ int32_t launch_direct(const DirectParams& p, const int32_t* fold, int32_t n_fold
     auto cfg = dependent_launch(&pdl, dim3(PA_PLAN_CTAS), 32 * kWarps<NT>, smem, stream);
     st = note_cuda(cudaLaunchKernelEx(&cfg, q4_direct_kernel<D, NT>, p));
     if (st || n_fold == 0) return st;
-    cfg = dependent_launch(&pdl, dim3(unsigned(n_fold)), 128, 0, stream);
+    cfg = dependent_launch(&pdl, dim3(unsigned(n_fold), unsigned((fold_rows + kFoldWarps - 1) / kFoldWarps)), 32 * kFoldWarps, 0, stream);
     return note_cuda(cudaLaunchKernelEx(&cfg, q4_fold_kernel<D, NT>, p, fold));
 }
 
@@ -1079,10 +1109,10 @@ extern "C" int32_t paged_attention_step_q4(const void* q, const void* k_pool, co
         p.bits = 0x43004300u;
         const int32_t* fold = words + f.fold;
         const bool wide = P.direct_rows > 8;
-        st = D == 128 ? (wide ? launch_direct<128, 2>(p, fold, P.n_fold, stream)
-                              : launch_direct<128, 1>(p, fold, P.n_fold, stream))
-                      : (wide ? launch_direct<64, 2>(p, fold, P.n_fold, stream)
-                              : launch_direct<64, 1>(p, fold, P.n_fold, stream));
+        st = D == 128 ? (wide ? launch_direct<128, 2>(p, fold, P.n_fold, P.fold_rows, stream)
+                              : launch_direct<128, 1>(p, fold, P.n_fold, P.fold_rows, stream))
+                      : (wide ? launch_direct<64, 2>(p, fold, P.n_fold, P.fold_rows, stream)
+                              : launch_direct<64, 1>(p, fold, P.n_fold, P.fold_rows, stream));
         if (st) return st;
     }
     if (P.n_chunk == 0) return PA_OK;

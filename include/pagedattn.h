@@ -742,6 +742,7 @@ typedef struct pa_q4_plan {
     int32_t direct_rows;
     int32_t n_direct;           /* items read from the codes */
     int32_t n_fold;             /* (tile of rows, KV head) pairs of several splits among them */
+    int32_t fold_rows;          /* rows of the largest of these tiles */
     int32_t n_chunk;            /* items over expanded contexts */
     int32_t n_expand;           /* 128-token blocks expanded */
     int32_t expand_cols;        /* columns of the table of expanded blocks */
