@@ -18,10 +18,11 @@ namespace pa_detail {
 
 // Keys of a split of a row read from the codes, by its sequence's context alone. A split is a warp's work:
 // short ones where there are few, so that a single sequence spreads over the GPU, and longer ones where
-// what a split costs beyond its keys (its start, its result written and read once more) would add up. A
-// multiple of 32.
+// what a split costs beyond its keys (its start, its result written and read once more) would add up.
+// Multiples of 32. (64 sequences of median 2,048 keys / 12 of 700 to 6,000 / one of 16,001: 73 / 14 / 21 us; with 256
+// keys everywhere 80 / 14.6 / 17, with 1,024 from 4,096 on 70 / 33 / 34.)
 __host__ __device__ constexpr int64_t q4_split_keys(int32_t ctx) {
-    return ctx <= 4096 ? 256 : ctx <= 32768 ? 512 : 1024;
+    return ctx <= 6144 ? 256 : ctx <= 12288 ? 384 : ctx <= 32768 ? 512 : 1024;
 }
 // The longest context of one split.
 constexpr int64_t q4_one_split() { return 256; }
@@ -29,8 +30,8 @@ constexpr int64_t q4_one_split() { return 256; }
 inline int64_t q4_max_splits(int64_t max_ctx) {
     const auto n = [](int64_t c) { return c <= 0 ? 1 : (c + q4_split_keys(int32_t(c)) - 1) / q4_split_keys(int32_t(c)); };
     int64_t most = n(max_ctx);
-    if (max_ctx > 4096 && n(4096) > most) most = n(4096);
-    if (max_ctx > 32768 && n(32768) > most) most = n(32768);
+    for (const int64_t c : {6144, 12288, 32768})                // the last context of every length
+        if (max_ctx > c && n(c) > most) most = n(c);
     return most;
 }
 

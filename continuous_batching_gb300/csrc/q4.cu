@@ -109,55 +109,33 @@ __global__ void __launch_bounds__(kRowsThreads) q4_write_kernel(const RowsParams
     }
 }
 
-// Eight columns of a row from its code word and the group's parameters, as bf16.
-__device__ __forceinline__ uint4 q4_expand8(uint32_t codes, uint32_t params) {
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = q4_value((codes >> (4 * i)) & 15u, params);
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                      pack_bf16(x[6], x[7]));
-}
-
+// Four lanes take a (token, head) of K and of V, all of their loads in flight. Bound by memory (672 bytes a token and
+// head for D = 128, in and out).
 template <int D>
 __global__ void __launch_bounds__(kRowsThreads) q4_read_kernel(const RowsParams p) {
-    constexpr int kLanes = D / 8;
-    constexpr int kGroups = kRowsThreads / kLanes;
+    constexpr int G = D / kQ4Group;
     dependent_start();
-    const int l = threadIdx.x % kLanes, bs = 1 << p.log2bs;
-    const uint32_t row0 = blockIdx.x * uint32_t(kGroups * kRowsPer) + threadIdx.x / kLanes;
-    uint32_t kc[kRowsPer], kp[kRowsPer], vc[kRowsPer], vp[kRowsPer];
-    bool on[kRowsPer];
-#pragma unroll
-    for (int i = 0; i < kRowsPer; ++i) {
-        const uint32_t row = row0 + i * kGroups;
-        kc[i] = kp[i] = vc[i] = vp[i] = 0;
-        on[i] = false;
-        if (row >= p.rows) continue;
-        const uint32_t t = row / uint32_t(p.Hkv);
-        const int head = int(row - t * uint32_t(p.Hkv));
-        const int32_t slot = p.slots[t];
-        if (slot < 0) continue;
-        if (slot >= p.num_slots) {
-            if (l == 0 && p.err) atomicOr(p.err, PA_DEVERR_SLOT);
-            continue;
-        }
-        on[i] = true;
-        const int block = slot >> p.log2bs, o = slot & (bs - 1);
-        const int64_t at = q4_base<D>(block, p.Hkv, head, bs);
-        const int64_t codes = at + o * kQ4Codes<D>;
-        const int64_t params = at + bs * kQ4Codes<D> + o * kQ4Params<D>;
-        kc[i] = reinterpret_cast<const uint32_t*>(p.k_pool + codes)[q4_word<D, false>(l)];
-        vc[i] = reinterpret_cast<const uint32_t*>(p.v_pool + codes)[q4_word<D, true>(l)];
-        kp[i] = reinterpret_cast<const uint32_t*>(p.k_pool + params)[l >> 2];
-        vp[i] = reinterpret_cast<const uint32_t*>(p.v_pool + params)[l >> 2];
+    const int c = threadIdx.x & 3, bs = 1 << p.log2bs;
+    const uint32_t row = blockIdx.x * uint32_t(kRowsThreads / 4) + threadIdx.x / 4;
+    if (row >= p.rows) return;
+    const uint32_t t = row / uint32_t(p.Hkv);
+    const int head = int(row - t * uint32_t(p.Hkv));
+    const int32_t slot = p.slots[t];
+    if (slot < 0) return;
+    if (slot >= p.num_slots) {
+        if (c == 0 && p.err) atomicOr(p.err, PA_DEVERR_SLOT);
+        return;
     }
+    const int o = slot & (bs - 1);
+    const int64_t at = q4_base<D>(slot >> p.log2bs, p.Hkv, head, bs);
+    uint32_t kw[G], kp[G], vw[G], vp[G];
+    q4_load_row<D>(p.k_pool, at, bs, o, c, kw, kp);
+    q4_load_row<D>(p.v_pool, at, bs, o, c, vw, vp);
+    const int64_t to = int64_t(row) * D + 8 * c;
 #pragma unroll
-    for (int i = 0; i < kRowsPer; ++i) {
-        const uint32_t v = q4_pair_groups(vc[i], l);
-        if (!on[i]) continue;
-        const int64_t to = int64_t(row0 + i * kGroups) * D + 8 * l;
-        *reinterpret_cast<uint4*>(p.k_out + to) = q4_expand8(kc[i], kp[i]);
-        *reinterpret_cast<uint4*>(p.v_out + to) = q4_expand8(v, vp[i]);
+    for (int g = 0; g < G; ++g) {
+        *reinterpret_cast<uint4*>(p.k_out + to + 32 * g) = q4_columns<D, false>(kw, kp, g);
+        *reinterpret_cast<uint4*>(p.v_out + to + 32 * g) = q4_columns<D, true>(vw, vp, g);
     }
 }
 
@@ -180,8 +158,7 @@ struct ExpandParams {
 // are read directly, metadata that the plan was not made for) have a context of 0 there.
 template <int D>
 __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
-    constexpr int kLanes = D / 8;
-    constexpr int kGroups = 256 / kLanes;
+    constexpr int G = D / kQ4Group, kGroups = 256 / 4;          // rows at a time
     dependent_start();
     const int bs = 1 << p.log2bs;
     const int64_t id = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
@@ -202,34 +179,28 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
         if (threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
         return;
     }
-    const int l = threadIdx.x % kLanes;
+    const int c = threadIdx.x & 3;
     const int32_t* table = p.table + int64_t(seq) * p.max_blocks;
-#pragma unroll 2
+#pragma unroll
     for (int i = 0; i < 128 / kGroups; ++i) {
-        const int tok = i * kGroups + threadIdx.x / kLanes;
+        const int tok = i * kGroups + threadIdx.x / 4;
         const int key = first * 128 + tok;                      // < ctx + 128
-        uint32_t kc = 0, vc = 0, kp = 0, vp = 0;
-        bool on = key < ctx;
-        if (on) {
-            const int32_t block = table[key >> p.log2bs];
-            if (block >= 0 && block < p.num_blocks) {
-                const int o = key & (bs - 1);
-                const int64_t at = q4_base<D>(block, p.Hkv, head, bs);
-                const int64_t codes = at + o * kQ4Codes<D>;
-                const int64_t params = at + bs * kQ4Codes<D> + o * kQ4Params<D>;
-                kc = reinterpret_cast<const uint32_t*>(p.k_pool + codes)[q4_word<D, false>(l)];
-                vc = reinterpret_cast<const uint32_t*>(p.v_pool + codes)[q4_word<D, true>(l)];
-                kp = reinterpret_cast<const uint32_t*>(p.k_pool + params)[l >> 2];
-                vp = reinterpret_cast<const uint32_t*>(p.v_pool + params)[l >> 2];
-            } else if (p.err) {
-                atomicOr(p.err, PA_DEVERR_BLOCK);               // its keys read as 0
-            }
+        if (key >= ctx) break;
+        uint32_t kw[G] = {}, kp[G] = {}, vw[G] = {}, vp[G] = {};
+        const int32_t block = table[key >> p.log2bs];
+        if (block >= 0 && block < p.num_blocks) {
+            const int64_t at = q4_base<D>(block, p.Hkv, head, bs);
+            q4_load_row<D>(p.k_pool, at, bs, key & (bs - 1), c, kw, kp);
+            q4_load_row<D>(p.v_pool, at, bs, key & (bs - 1), c, vw, vp);
+        } else if (p.err) {
+            atomicOr(p.err, PA_DEVERR_BLOCK);                   // its keys read as 0
         }
-        const uint32_t v = q4_pair_groups(vc, l);
-        if (!on) continue;
-        const int64_t to = ((int64_t(blockIdx.x) * 128 + tok) * p.Hkv + head) * D + 8 * l;
-        *reinterpret_cast<uint4*>(p.k_out + to) = q4_expand8(kc, kp);
-        *reinterpret_cast<uint4*>(p.v_out + to) = q4_expand8(v, vp);
+        const int64_t to = ((int64_t(blockIdx.x) * 128 + tok) * p.Hkv + head) * D + 8 * c;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            *reinterpret_cast<uint4*>(p.k_out + to + 32 * g) = q4_columns<D, false>(kw, kp, g);
+            *reinterpret_cast<uint4*>(p.v_out + to + 32 * g) = q4_columns<D, true>(vw, vp, g);
+        }
     }
 }
 
@@ -982,7 +953,7 @@ int32_t launch_rows(RowsParams& p, int32_t T, const int32_t* slots, void* k_pool
     p.Hkv = shape->num_kv_heads;
     p.log2bs = ilog2(shape->block_size);
     p.err = err;
-    const int per = kRowsThreads / (shape->head_dim / 8) * kRowsPer;
+    const int per = WRITE ? kRowsThreads / (shape->head_dim / 8) * kRowsPer : kRowsThreads / 4;
     const int64_t blocks = (rows + per - 1) / per;
     cudaLaunchAttribute pdl;
     auto cfg = dependent_launch(&pdl, dim3(unsigned(blocks)), kRowsThreads, 0, stream);

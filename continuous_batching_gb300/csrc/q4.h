@@ -135,7 +135,7 @@ __device__ __forceinline__ void q4_quantise8(const uint32_t (&w)[4], uint32_t& c
 
 // A V row's 16-bit words pair the groups g and g + 1 (g even) of one r. Lanes (g, c) hold r = 2 c in
 // their low and r = 2 c + 1 in their high half; the even lane takes the pair of r = 2 c, the odd one that of
-// r = 2 c + 1. The exchange is its own inverse (a reader's words become the lane's eight codes).
+// r = 2 c + 1.
 __device__ __forceinline__ uint32_t q4_pair_groups(uint32_t codes, int l) {
     const bool odd = (l >> 2) & 1;
     const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? codes & 0xFFFFu : codes >> 16, 4);
@@ -160,9 +160,42 @@ __device__ __forceinline__ void q4_store_row(uint8_t* pool, int64_t at, int bs, 
         reinterpret_cast<uint32_t*>(pool + at + bs * kQ4Codes<D> + o * kQ4Params<D>)[l >> 2] = params;
 }
 
-// The value a code stands for: scale * code + minimum in one rounding to fp32 (the product is exact).
-__device__ __forceinline__ float q4_value(uint32_t code, uint32_t params) {
-    return fmaf(__uint_as_float(params << 16), float(code), __uint_as_float(params & 0xFFFF0000u));
+// What reads the cache back takes a row by four lanes: lane c its D / 8 bytes of codes from c D / 8 on (w: G words)
+// and all of the row's parameters (p), and gives columns 32 g + 8 c .. + 7 of every group g. In a V row these bytes are
+// the halves r = 2 c and r = 2 c + 1.
+template <int D, bool IS_V>
+__device__ __forceinline__ uint4 q4_columns(const uint32_t (&w)[D / kQ4Group],
+                                            const uint32_t (&p)[D / kQ4Group], int g) {
+    constexpr int G = D / kQ4Group;
+    const uint32_t x = IS_V ? __byte_perm(w[g / 2], w[G / 2 + g / 2], g & 1 ? 0x7632 : 0x5410) : w[g];
+    const uint32_t scale = __byte_perm(p[g], 0, 0x1010), low = __byte_perm(p[g], 0, 0x3232);
+    // the value scale * u + minimum in one rounding, two columns n and n + 4 at a time: u as bf16 128 + u, less 128
+    uint32_t y[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        uint32_t u = ((x >> (4 * n)) & 0x000F000Fu) | 0x43004300u;
+        asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(u) : "r"(0x43004300u));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y[n]) : "r"(u), "r"(scale), "r"(low));
+    }
+    return make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
+                      __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632));
+}
+
+// A lane's codes and its row's parameters; `at` is q4_base of the block and head, o the token in it.
+template <int D>
+__device__ __forceinline__ void q4_load_row(const uint8_t* pool, int64_t at, int bs, int o, int c,
+                                            uint32_t (&w)[D / kQ4Group], uint32_t (&p)[D / kQ4Group]) {
+    const uint8_t* codes = pool + at + o * kQ4Codes<D> + c * (D / 8);
+    const uint8_t* params = pool + at + bs * kQ4Codes<D> + o * kQ4Params<D>;
+    if constexpr (D == 128) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(codes)), b = __ldg(reinterpret_cast<const uint4*>(params));
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        p[0] = b.x, p[1] = b.y, p[2] = b.z, p[3] = b.w;
+    } else {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(codes)), b = __ldg(reinterpret_cast<const uint2*>(params));
+        w[0] = a.x, w[1] = a.y;
+        p[0] = b.x, p[1] = b.y;
+    }
 }
 
 }  // namespace

@@ -116,7 +116,7 @@ def _items(words, at, n):
 
 
 def _split(ctx):
-    return 256 if ctx <= 4096 else 512 if ctx <= 32768 else 1024
+    return 256 if ctx <= 6144 else 384 if ctx <= 12288 else 512 if ctx <= 32768 else 1024
 
 
 @pytest.mark.parametrize("direct_rows", [0, 8, 16, 64])
@@ -227,13 +227,13 @@ SHAPES = [(8, 8, 128, 16), (8, 4, 64, 8), (8, 2, 128, 32), (16, 2, 128, 128), (8
 @pytest.mark.parametrize("Hq, Hkv, D, bs", SHAPES)
 def test_single_rows_read_from_the_codes(Hq, Hkv, D, bs):
     """Contexts around tiles, warps, splits and the places where the split's length changes."""
-    ctx = [1, 2, 8, 31, 32, 33, 127, 128, 129, 160, 511, 512, 513, 640, 1025, 4095, 4096, 4097, 5200]
+    ctx = [1, 2, 8, 31, 32, 33, 127, 128, 129, 160, 511, 512, 513, 640, 1025, 4095, 4096, 4097, 6144, 6145]
     Case([(1, c) for c in ctx], Hq, Hkv, D, bs, seed=Hq + D).check_direct(16)
 
 
 @pytest.mark.gpu
 def test_a_long_context():
-    Case([(1, 33000), (1, 32768), (3, 32769)], 8, 1, 128, 16, seed=5).check_direct(24)
+    Case([(1, 33000), (1, 32768), (3, 32769), (2, 12289), (1, 12288)], 8, 1, 128, 16, seed=5).check_direct(24)
 
 
 @pytest.mark.gpu
