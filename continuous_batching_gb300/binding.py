@@ -1041,14 +1041,21 @@ class StepRunner:
     Those buffers are views of one device array, filled from one pinned host array by a single
     asynchronous copy on the current stream; the next prepare() first waits for that copy.
     With kv_scales = (k_scale, v_scale) the pools are uint8 float8_e4m3fn caches and the fp8
-    write and read entry points run instead.
+    write and read entry points run instead; with kv_bits = 4 they are 4-bit pools (pa_q4_pool_shape)
+    and the q4 ones do, sequences of up to direct_rows rows read from the codes (see pa_plan_step_q4; None:
+    what is fast, with limits for single tokens).
     """
 
     def __init__(self, shape: Shape, device="cuda", limits: Optional[StepLimits] = None,
-                 kv_scales: Optional[tuple] = None):
+                 kv_scales: Optional[tuple] = None, kv_bits: Optional[int] = None,
+                 direct_rows: Optional[int] = None):
         import torch
+        if kv_bits not in (None, 4) or (kv_bits is not None and kv_scales is not None):
+            raise ValueError("kv_bits: 4, without kv_scales")
         self.torch = torch
         self.shape = shape
+        self.q4 = kv_bits == 4
+        self.direct_rows = direct_rows
         self.kv_scales = None if kv_scales is None else (float(kv_scales[0]), float(kv_scales[1]))
         self.device = torch.device(device)
         self.limits = limits
@@ -1058,9 +1065,18 @@ class StepRunner:
         if limits is not None:
             L = limits
             d = self.device
-            cap = int(load().pa_plan_max_items_shared(C.byref(shape), L.B, L.T, L.max_ctx))
-            self.n_items_cap = max(cap, 1)
-            parts = (("items", self.n_items_cap * ITEM_INTS), ("cu", L.B + 1), ("ctx", L.B),
+            if self.q4:
+                rows = pa_q4_direct_rows(shape) if direct_rows is None else int(direct_rows)
+                # chunks: sequences of more rows than that
+                chunks = min(L.B, L.T // (rows // (shape.num_q_heads // shape.num_kv_heads) + 1))
+                self.q4_sizes = pa_q4_plan_limits(shape, L.B, L.T, L.max_ctx, rows,
+                                                  chunks * (-(-L.max_ctx // 128)))
+                n_words = max(self.q4_sizes.words, 1)
+            else:
+                cap = int(load().pa_plan_max_items_shared(C.byref(shape), L.B, L.T, L.max_ctx))
+                self.n_items_cap = max(cap, 1)
+                n_words = self.n_items_cap * ITEM_INTS
+            parts = (("items", n_words), ("cu", L.B + 1), ("ctx", L.B),
                      ("table", L.B * L.max_blocks), ("slots", L.T))
             total = sum(n for _, n in parts)
             self._meta = torch.empty(max(total, 1), dtype=torch.int32, device=d)
@@ -1083,7 +1099,11 @@ class StepRunner:
             self._n_planned = 0                           # real items of the last plan
             self.max_ctx = L.max_ctx
             self.T = L.T
-            need = pa_workspace_bytes(shape, L.T, L.max_ctx)
+            if self.q4:
+                self.plan = Q4Plan(self.q4_sizes, self.items)
+                need = pa_q4_workspace_bytes(shape, self.q4_sizes)
+            else:
+                need = pa_workspace_bytes(shape, L.T, L.max_ctx)
             self.ws = torch.empty((need + 3) // 4, dtype=torch.float32, device=d)
 
     def prepare(self, cu_seqlens_q: np.ndarray, ctx_lens: np.ndarray, block_table: np.ndarray,
@@ -1092,18 +1112,23 @@ class StepRunner:
         cu, ctx = _i32(cu_seqlens_q), _i32(ctx_lens)
         if self.limits is not None:
             return self._prepare_fixed(cu, ctx, _i32(block_table), slot_mapping)
-        items = pa_plan_step_shared(self.shape, cu, ctx, block_table)
+        d = self.device
+        if self.q4:
+            self.plan = pa_plan_step_q4(self.shape, cu, ctx, self.direct_rows, device=d)
+        else:
+            items = pa_plan_step_shared(self.shape, cu, ctx, block_table)
         if slot_mapping is None:
             slot_mapping = pa_compute_slots(self.shape, block_table, cu, ctx)
-        d = self.device
         self.max_ctx = int(ctx.max()) if len(ctx) else 0
         self.T = int(cu[-1]) if len(ctx) else 0
-        self.items = torch.from_numpy(items.view(np.int32).reshape(-1).copy()).to(d)
+        self.items = self.plan.words if self.q4 else \
+            torch.from_numpy(items.view(np.int32).reshape(-1).copy()).to(d)
         self.cu = torch.from_numpy(cu.copy()).to(d)
         self.ctx = torch.from_numpy(ctx.copy()).to(d)
         self.table = torch.from_numpy(_i32(block_table).copy()).to(d)
         self.slots = torch.from_numpy(_i32(slot_mapping).copy()).to(d)
-        need = pa_workspace_bytes(self.shape, self.T, self.max_ctx)
+        need = pa_q4_workspace_bytes(self.shape, self.plan) if self.q4 else \
+            pa_workspace_bytes(self.shape, self.T, self.max_ctx)
         if self.ws is None or self.ws.numel() * 4 < need:
             self.ws = torch.empty((need + 3) // 4, dtype=torch.float32, device=d)
         return self
@@ -1122,6 +1147,10 @@ class StepRunner:
         lib = load()
         hi = self._h["items"]
         n = C.c_int32()
+        if self.q4:
+            _check(lib.pa_plan_step_q4(C.byref(self.shape), B, _p32(cu), _p32(ctx),
+                                       C.byref(self.q4_sizes), _p32(hi)), "pa_plan_step_q4")
+            return self._upload_fixed(cu, ctx, table, slot_mapping)
         _check(lib.pa_plan_step_shared(C.byref(self.shape), B, _p32(cu), _p32(ctx), _p32(table),
                                        table.shape[1], hi.ctypes.data_as(C.POINTER(WorkItem)),
                                        self.n_items_cap, C.byref(n)), "pa_plan_step_shared")
@@ -1129,6 +1158,10 @@ class StepRunner:
         if self._n_planned > n.value:
             hs[n.value:self._n_planned] = 0               # n_q == 0: padding
         self._n_planned = n.value
+        return self._upload_fixed(cu, ctx, table, slot_mapping)
+
+    def _upload_fixed(self, cu, ctx, table, slot_mapping):
+        L, lib, (B, T) = self.limits, load(), (self.limits.B, self.limits.T)
         self._h["cu"][:] = cu
         self._h["ctx"][:] = ctx
         ht = self._h["table"]
@@ -1183,6 +1216,9 @@ class StepRunner:
         self.graph.replay()
 
     def write(self, k_new, v_new, k_pool, v_pool, stream=None):
+        if self.q4:
+            paged_kv_write_q4(k_new, v_new, self.slots, k_pool, v_pool, self.shape, self.err, stream)
+            return
         if self.kv_scales is not None:
             paged_kv_write_fp8(k_new, v_new, self.slots, k_pool, v_pool, *self.kv_scales,
                                self.shape, self.err, stream)
@@ -1190,6 +1226,10 @@ class StepRunner:
         paged_kv_write(k_new, v_new, self.slots, k_pool, v_pool, self.shape, self.err, stream)
 
     def attend(self, q, k_pool, v_pool, out, stream=None):
+        if self.q4:
+            paged_attention_step_q4(q, k_pool, v_pool, self.table, self.cu, self.ctx, self.plan,
+                                    self.ws, out, self.shape, self.err, stream)
+            return
         if self.kv_scales is not None:
             paged_attention_step_fp8(q, k_pool, v_pool, self.table, self.cu, self.ctx,
                                      self.max_ctx, self.items, *self.kv_scales, self.ws, out,

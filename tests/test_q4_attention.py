@@ -516,3 +516,46 @@ def test_a_run_as_it_is_used():
     step({0: 2, 7: 1, 2: 1, 9: 20})
     step({0: 1, 7: 1, 2: 1, 9: 1}, rows=0)
     assert int(err.item()) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fixed", [False, True])
+def test_step_runner(fixed):
+    """StepRunner over 4-bit pools: write and step of its own plans, with limits as a captured graph."""
+    lens = [[(1, 500), (1, 33), (20, 260)], [(1, 501), (20, 53), (1, 261)]]
+    a = Case(lens[0], seed=71)
+    if not fixed:
+        runner = bd.StepRunner(a.shape, kv_bits=4).prepare(a.cu, a.ctx, a.table)
+        k, v = (dev(p) for p in a.pools)
+        kn, vn = (wl.random_bf16(np.random.default_rng(s), (a.T, 2, 128)) for s in (1, 2))
+        out = torch.empty(a.T, 8, 128, dtype=torch.bfloat16, device="cuda")
+        runner.run(bf16(a.q), bf16(kn), bf16(vn), k, v, out)
+        slots = bd.pa_compute_slots(a.shape, a.table, a.cu, a.ctx)
+        a.pools = [q4.write(p, x, slots, 16, i == 1) for i, (p, x) in enumerate(zip(a.pools, (kn, vn)))]
+        assert np.array_equal(k.cpu().numpy(), a.pools[0]) and np.array_equal(v.cpu().numpy(), a.pools[1])
+        assert runner.device_error() == 0 and np.array_equal(bits_of(out), a.run())
+        return
+    runner = bd.StepRunner(a.shape, limits=bd.StepLimits(3, 22, 40, 520), kv_bits=4)
+    k, v = (dev(p) for p in a.pools)
+    q, out = (torch.empty(a.T, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in "qo")
+    for i, l in enumerate(lens):
+        c = Case(l, seed=71 + i, spare=2)
+        if c.nb > a.nb:
+            continue
+        runner.prepare(c.cu, c.ctx, c.table)
+        k.zero_(), v.zero_()
+        k[:c.nb].copy_(dev(c.pools[0])), v[:c.nb].copy_(dev(c.pools[1]))
+        q.copy_(bf16(c.q))
+        if i == 0:
+            runner.capture(q, None, None, k, v, out, write=False)
+        out.zero_()
+        runner.replay()
+        torch.cuda.synchronize()
+        assert runner.device_error() == 0 and np.array_equal(bits_of(out), c.run(8))
+
+
+def test_runner_refuses():
+    with pytest.raises(ValueError):
+        bd.StepRunner(bd.Shape.make(8, 2, 128, 16, 4), device="cpu", kv_bits=8)
+    with pytest.raises(ValueError):
+        bd.StepRunner(bd.Shape.make(8, 2, 128, 16, 4), device="cpu", kv_bits=4, kv_scales=(1.0, 1.0))
