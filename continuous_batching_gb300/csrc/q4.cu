@@ -2,10 +2,10 @@
 //
 // Layout and quantisation: q4.h. A value is scale * code + minimum per group of 32 columns.
 //
-// Rows of few tokens (direct_rows or fewer per sequence and KV head: single tokens, drafted tokens) are computed from the codes
-// themselves, never expanded to memory; see q4_direct_kernel. Sequences with more rows (chunks) have
-// their context expanded once to bf16 in the workspace and go through the tcgen05 step of the bf16
-// cache: the products are then the cost, and an expansion of a few us serves every row tile.
+// Sequences of few rows (tokens x heads of a group, direct_rows or fewer: single tokens, drafted tokens) are
+// computed from the codes themselves, never expanded to memory; see q4_direct_kernel. Sequences with more rows
+// (chunks) have their context expanded once to bf16 in the workspace and go through the tcgen05 step of
+// the bf16 cache: the products are then the cost, and an expansion of a few us serves every row tile.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -224,11 +224,12 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
 //   S = sum_g s_g (q . codes)_g + sum_g m_g sum(q_g)
 // with exact products and fp32 sums: K is never rounded beyond its code. The second sum is a product too, of the
 // minima and sum(q_g) in three bf16 parts.
-//   O^T = V^T P^T   A = V codes as u - 8 (bf16: the code in the mantissa, less 136), B = w = bf16(p s_g), p
-//                   rounded to bf16
+//   O^T = V^T P^T   A = V codes as u - 8 (bf16: the code in the mantissa, less 136), B = w = bf16(p s_g)
 //   O = sum_j w_j (u_j - 8) + sum_j p_j bf16(m_jg + 8 s_jg)
-// u - 8 and not u: the roundings of w then weigh as much as that of p, u alone would double them.
-// P^T's layout is turned by movmatrix, once for all groups.
+// u - 8 and not u: |u - 8| s is the size of the value's distance from its group's middle, u s twice that, and so
+// would the roundings of w be. p is a sum of two bf16 (16 bits: p itself rounded to one would add an error
+// as large as that of w; against 64 bits the output's was 0.0028 so and is 0.0022, 73.1 -> 74.5 us for the decode
+// batch below); w = fma(p_hi, s, p_lo s) rounds once. P^T's layout is turned by movmatrix, once for all groups.
 // A masked key's parameters may be anything (it may not have been written yet), and 0 times them too: its w
 // are cleared for the rows that do not see it, its centre is clamped to numbers. What is not finite still
 // reaches the rows that see it, through w.
@@ -480,11 +481,11 @@ __device__ __forceinline__ void q4_scores(uint32_t stage, const Rows<D, NT>& R, 
 }
 
 // Online softmax of a tile of 32 keys from key0 on: p as bf16 pairs of keys 2 c, 2 c + 1 (and 8 behind them) of
-// row r. masked: some key lies behind some row. The reference maximum moves when the rows' maximum outgrows it
-// by 2^8.
+// row r, and what that rounding leaves. masked: some key lies behind some row. The reference maximum moves when
+// the rows' maximum outgrows it by 2^8.
 template <int D, int NT>
 __device__ __forceinline__ void q4_softmax(Rows<D, NT>& R, float (&x)[NT][2][4], bool masked, int key0,
-                                           int lane, uint32_t (&p)[NT][2][2]) {
+                                           int lane, uint32_t (&p)[NT][2][2], uint32_t (&rest)[NT][2][2]) {
     constexpr int G = D / kQ4Group;
     const int r = lane >> 2;
 #pragma unroll
@@ -544,8 +545,14 @@ __device__ __forceinline__ void q4_softmax(Rows<D, NT>& R, float (&x)[NT][2][4],
             }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            p[j][h][0] = transpose8(pack_bf16(x[j][h][0], x[j][h][1]));
-            p[j][h][1] = transpose8(pack_bf16(x[j][h][2], x[j][h][3]));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint32_t hi = pack_bf16(x[j][h][2 * b], x[j][h][2 * b + 1]);
+                float u, v;
+                f2_split(fma2(f2(scale_of(hi), min_of(hi)), f2(-1.f, -1.f), f2(x[j][h][2 * b], x[j][h][2 * b + 1])), u, v);
+                p[j][h][b] = transpose8(hi);
+                rest[j][h][b] = transpose8(pack_bf16(u, v));
+            }
         }
     }
 }
@@ -553,7 +560,7 @@ __device__ __forceinline__ void q4_softmax(Rows<D, NT>& R, float (&x)[NT][2][4],
 // O of 16 keys of a tile (h: which half) from its stage and p. MASK: some key lies behind some row.
 template <int D, int NT, bool MASK>
 __device__ __forceinline__ void q4_values(uint32_t stage, Rows<D, NT>& R, const uint32_t (&p)[NT][2][2],
-                                          int h, int key0, int lane) {
+                                          const uint32_t (&rest)[NT][2][2], int h, int key0, int lane) {
     constexpr int G = D / kQ4Group;
     using L = Ring<D>;
     const int r = lane >> 2, cc = lane & 3;
@@ -577,6 +584,7 @@ __device__ __forceinline__ void q4_values(uint32_t stage, Rows<D, NT>& R, const 
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         mma(R.z[j], z0, 0u, z1, 0u, p[j][h][0], p[j][h][1]);
+        mma(R.z[j], z0, 0u, z1, 0u, rest[j][h][0], rest[j][h][1]);
         if constexpr (MASK) {
             const int seen = R.pos(8 * j + r) - (key0 + 16 * h + 2 * cc);     // >= 0: key 2 c, and so on
             keep0[j] = (seen >= 0 ? 0xFFFFu : 0u) | (seen >= 1 ? 0xFFFF0000u : 0u);
@@ -597,7 +605,8 @@ __device__ __forceinline__ void q4_values(uint32_t stage, Rows<D, NT>& R, const 
         const uint32_t b2 = centred<2>(hi, R.bits), b3 = centred<3>(hi, R.bits);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            uint32_t w0 = mul_bf16(p[j][h][0], s0), w1 = mul_bf16(p[j][h][1], s1);
+            uint32_t w0 = fma_bf16(p[j][h][0], s0, mul_bf16(rest[j][h][0], s0));
+            uint32_t w1 = fma_bf16(p[j][h][1], s1, mul_bf16(rest[j][h][1], s1));
             if constexpr (MASK) {
                 w0 &= keep0[j];
                 w1 &= keep1[j];
@@ -655,156 +664,154 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
             if (lane == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
             continue;
         }
-        {
-            const int ctx_now = __ldg(p.ctx + it.seq), cu0 = __ldg(p.cu + it.seq), cu1 = __ldg(p.cu + it.seq + 1);
-            const int len = int(q4_split_keys(ctx)), k_begin = it.split * len, k_last = min(ctx, k_begin + len);
-            const int32_t* table = p.table + int64_t(it.seq) * p.max_blocks;
-            // (the split's keys up to the context: the last row may lie before it)
-            const auto block_of = [&](int tile) {
-                const int key = k_begin + (tile + (lane >> 2)) * kKeys + 8 * (lane & 3);
-                return key < k_last ? max(__ldg(table + (key >> p.log2bs)), -1) : -2;
-            };
-            int block = block_of(0);
-            const int rows = it.n_q << p.log2g;
-            uint4 qw[NT][G];
+        const int ctx_now = __ldg(p.ctx + it.seq), cu0 = __ldg(p.cu + it.seq), cu1 = __ldg(p.cu + it.seq + 1);
+        const int len = int(q4_split_keys(ctx)), k_begin = it.split * len, k_last = min(ctx, k_begin + len);
+        const int32_t* table = p.table + int64_t(it.seq) * p.max_blocks;
+        // (the split's keys up to the context: the last row may lie before it)
+        const auto block_of = [&](int tile) {
+            const int key = k_begin + (tile + (lane >> 2)) * kKeys + 8 * (lane & 3);
+            return key < k_last ? max(__ldg(table + (key >> p.log2bs)), -1) : -2;
+        };
+        int block = block_of(0);
+        const int rows = it.n_q << p.log2g;
+        uint4 qw[NT][G];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int row = 8 * j + r;
-                const __nv_bfloat16* src = p.q + (int64_t(it.q_start + (row >> p.log2g)) * p.Hq + it.kv_head * gq +
-                                                  (row & (gq - 1))) * D + 8 * cc;
+        for (int j = 0; j < NT; ++j) {
+            const int row = 8 * j + r;
+            const __nv_bfloat16* src = p.q + (int64_t(it.q_start + (row >> p.log2g)) * p.Hq + it.kv_head * gq +
+                                              (row & (gq - 1))) * D + 8 * cc;
 #pragma unroll
-                for (int g = 0; g < G; ++g)
-                    qw[j][g] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + 32 * g)) : make_uint4(0, 0, 0, 0);
-            }
-            const int pos0 = ctx - (cu1 - it.q_start);              // position of the first row
-            const int keys = pos0 + it.n_q;                         // up to the last row
-            good = ctx_now == ctx && cu0 <= it.q_start && it.q_start + it.n_q <= cu1 &&
-                   int64_t(cu1) - cu0 <= ctx && (keys + len - 1) / len == it.n_splits;
-            if (!good) {
-                if (lane == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
-                continue;
-            }
-            const int k_end = min(keys, k_begin + len);
-            const int n = (k_end - k_begin + kKeys - 1) / kKeys;    // tiles of 32 keys
-            // Lane i looks after the eight keys i % 4 of tile i / 4 of eight tiles: where their code rows and their
-            // parameter rows begin, in units of 16 bytes, and (a bit of `there`) whether their block is there.
-            constexpr int kRow16 = kQ4Codes<D> / 16, kPar8 = 8 * kQ4Params<D> / 16;
-            uint32_t codes_at = 0, params_at = 0, there = 0;
-            const auto turn_to = [&](int tile) {                // the eight tiles from `tile` on
-                const int key = k_begin + (tile + (lane >> 2)) * kKeys + 8 * (lane & 3);
-                const bool on = block >= 0 && block < p.num_blocks;
-                if (!on && block != -2 && p.err) atomicOr(p.err, PA_DEVERR_BLOCK);   // its keys read as 0
-                there = __ballot_sync(0xffffffffu, on);
-                const int o = key & (bs - 1);
-                const uint32_t at = (uint32_t(on ? block : 0) * p.Hkv + it.kv_head) * (bs * kQ4Row<D> / 16);
-                codes_at = at + o * kRow16;
-                params_at = at + bs * kRow16 + (o >> 3) * kPar8;
-                block = block_of(tile + 8);
-            };
-            constexpr int kPieces = kRow16;                     // 16-byte pieces of a code row
-            constexpr int kAtOnce = 32 / kPieces;               // keys the warp's lanes cover
-            // the lane's piece of a unit's eight code rows, in 16 bytes: K as it lies, V as q4_values reads it
-            const uint32_t k_lane = lane % (8 * kPieces);
-            const uint32_t v_lane = D == 128 ? ((lane & 6) + (lane >> 4)) * kPieces + ((lane >> 2) & 2) + (lane & 1)
-                                             : (lane & 6) * kPieces + ((lane >> 3) & 1) * kPieces + (lane & 1);
-            uint32_t stage_in = ring;
-            const auto issue = [&](int tile) {
-                if (tile < n) {
-                    if ((tile & 7) == 0) turn_to(tile);
-                    const int u0 = (tile & 7) * 4;
-                    const bool all = ((there >> u0) & 15u) == 15u;
-#pragma unroll
-                    for (int i = 0; i < kKeys / kAtOnce; ++i) {
-                        const int unit = u0 + (i * kAtOnce + lane / kPieces) / 8;
-                        const uint32_t at = __shfl_sync(0xffffffffu, codes_at, unit);
-                        const bool on = all || ((there >> unit) & 1u);
-                        const uint32_t to = stage_in + i * (kAtOnce * kQ4Codes<D>) + 16 * lane;
-                        cp_async<16>(to, p.k_pool + uint64_t(at + k_lane) * 16, on);
-                        cp_async<16>(to + L::kCodes, p.v_pool + uint64_t(at + v_lane) * 16, on);
-                    }
-                    const uint32_t at = __shfl_sync(0xffffffffu, params_at, u0 + lane / 8);
-                    const bool on = all || ((there >> (u0 + lane / 8)) & 1u);
-                    const uint32_t to = stage_in + 2 * L::kCodes + lane * kQ4Params<D>;
-                    const int64_t par = int64_t(uint64_t(at) * 16) + (lane & 7) * kQ4Params<D>;
-                    cp_async<kQ4Params<D>>(to, p.k_pool + par, on);
-                    cp_async<kQ4Params<D>>(to + L::kParams, p.v_pool + par, on);
-                    stage_in = stage_in == ring + (L::kStages - 1) * L::kStage ? ring : stage_in + L::kStage;
-                }
-                cp_commit();
-            };
-#pragma unroll
-            for (int i = 0; i < L::kStages; ++i) issue(i);
-            // ---- Q, while the first tiles are on their way
-            Rows<D, NT> R;
-            R.bits = __shfl_sync(0xffffffffu, p.bits, 0);
-            R.pos0 = pos0;
-            R.rows = rows;
-            R.log2g = p.log2g;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) q4_take_q<D, NT>(R, qw[j], j, p.c, lane);
-            uint32_t stage = ring;
-            for (int i = 0, key0 = k_begin; i < n; ++i, key0 += kKeys) {
-                cp_wait<L::kStages - 1>();
-                __syncwarp();                                   // every lane's copies
-                float x[NT][2][4];
-                uint32_t prob[NT][2][2];
-                const bool masked = key0 + kKeys - 1 > pos0;
-                q4_scores<D, NT>(stage, R, 0, lane, x);
-                q4_scores<D, NT>(stage, R, 1, lane, x);
-                q4_softmax<D, NT>(R, x, masked, key0, lane, prob);
-                if (masked) {
-                    q4_values<D, NT, true>(stage, R, prob, 0, key0, lane);
-                    q4_values<D, NT, true>(stage, R, prob, 1, key0, lane);
-                } else {
-                    q4_values<D, NT, false>(stage, R, prob, 0, key0, lane);
-                    q4_values<D, NT, false>(stage, R, prob, 1, key0, lane);
-                }
-                __syncwarp();                                   // every lane has read the stage
-                issue(i + L::kStages);
-                stage = stage == ring + (L::kStages - 1) * L::kStage ? ring : stage + L::kStage;
-            }
-            cp_wait<0>();
-            // ---- the rows' results: finished where they have one split, else left for the fold
-            const pa_work_item done = *at_item;                     // (again: not kept in registers meanwhile)
-            const bool whole = done.n_splits == 1;
-            float* const part = p.part + int64_t(done.tile0 + done.split) * (kCols * (D + 2));
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                float l[2];
-                f2_split(R.l[j], l[0], l[1]);
-#pragma unroll
-                for (int d = 4; d <= 16; d <<= 1) {
-                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
-                    l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
-                }
-                const float f[2] = {whole ? __frcp_rn(l[0]) : 1.f, whole ? __frcp_rn(l[1]) : 1.f};
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float z = __shfl_sync(0xffffffffu, R.z[j][e], 4 * g + cc);
-                        const int row = 8 * j + 2 * cc + e;
-                        if (row >= rows) continue;
-                        const float y[4] = {(R.o[j][2 * g][e] + z) * f[e], (R.o[j][2 * g][2 + e] + z) * f[e],
-                                            (R.o[j][2 * g + 1][e] + z) * f[e], (R.o[j][2 * g + 1][2 + e] + z) * f[e]};
-                        const int col = 32 * g + 4 * r;
-                        if (whole) {
-                            const int64_t at = (int64_t(done.q_start + (row >> p.log2g)) * p.Hq + done.kv_head * gq +
-                                                (row & (gq - 1))) * D + col;
-                            *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-                        } else {
-                            *reinterpret_cast<float4*>(part + row * D + col) = make_float4(y[0], y[1], y[2], y[3]);
-                        }
-                    }
-                }
-                if (r == 0 && !whole) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float2*>(part + kCols * D + 2 * (8 * j + 2 * cc + e)) = make_float2(-R.nm[j][e], l[e]);
-                }
-            }
-            __syncwarp();                                       // the ring is free again
+            for (int g = 0; g < G; ++g)
+                qw[j][g] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + 32 * g)) : make_uint4(0, 0, 0, 0);
         }
+        const int pos0 = ctx - (cu1 - it.q_start);              // position of the first row
+        const int keys = pos0 + it.n_q;                         // up to the last row
+        good = ctx_now == ctx && cu0 <= it.q_start && it.q_start + it.n_q <= cu1 &&
+               int64_t(cu1) - cu0 <= ctx && (keys + len - 1) / len == it.n_splits;
+        if (!good) {
+            if (lane == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+            continue;
+        }
+        const int k_end = min(keys, k_begin + len);
+        const int n = (k_end - k_begin + kKeys - 1) / kKeys;    // tiles of 32 keys
+        // Lane i looks after the eight keys i % 4 of tile i / 4 of eight tiles: where their code rows and their
+        // parameter rows begin, in units of 16 bytes, and (a bit of `there`) whether their block is there.
+        constexpr int kRow16 = kQ4Codes<D> / 16, kPar8 = 8 * kQ4Params<D> / 16;
+        uint32_t codes_at = 0, params_at = 0, there = 0;
+        const auto turn_to = [&](int tile) {                // the eight tiles from `tile` on
+            const int key = k_begin + (tile + (lane >> 2)) * kKeys + 8 * (lane & 3);
+            const bool on = block >= 0 && block < p.num_blocks;
+            if (!on && block != -2 && p.err) atomicOr(p.err, PA_DEVERR_BLOCK);   // its keys read as 0
+            there = __ballot_sync(0xffffffffu, on);
+            const int o = key & (bs - 1);
+            const uint32_t at = (uint32_t(on ? block : 0) * p.Hkv + it.kv_head) * (bs * kQ4Row<D> / 16);
+            codes_at = at + o * kRow16;
+            params_at = at + bs * kRow16 + (o >> 3) * kPar8;
+            block = block_of(tile + 8);
+        };
+        constexpr int kPieces = kRow16;                     // 16-byte pieces of a code row
+        constexpr int kAtOnce = 32 / kPieces;               // keys the warp's lanes cover
+        // the lane's piece of a unit's eight code rows, in 16 bytes: K as it lies, V as q4_values reads it
+        const uint32_t k_lane = lane % (8 * kPieces);
+        const uint32_t v_lane = D == 128 ? ((lane & 6) + (lane >> 4)) * kPieces + ((lane >> 2) & 2) + (lane & 1)
+                                         : (lane & 6) * kPieces + ((lane >> 3) & 1) * kPieces + (lane & 1);
+        uint32_t stage_in = ring;
+        const auto issue = [&](int tile) {
+            if (tile < n) {
+                if ((tile & 7) == 0) turn_to(tile);
+                const int u0 = (tile & 7) * 4;
+                const bool all = ((there >> u0) & 15u) == 15u;
+#pragma unroll
+                for (int i = 0; i < kKeys / kAtOnce; ++i) {
+                    const int unit = u0 + (i * kAtOnce + lane / kPieces) / 8;
+                    const uint32_t at = __shfl_sync(0xffffffffu, codes_at, unit);
+                    const bool on = all || ((there >> unit) & 1u);
+                    const uint32_t to = stage_in + i * (kAtOnce * kQ4Codes<D>) + 16 * lane;
+                    cp_async<16>(to, p.k_pool + uint64_t(at + k_lane) * 16, on);
+                    cp_async<16>(to + L::kCodes, p.v_pool + uint64_t(at + v_lane) * 16, on);
+                }
+                const uint32_t at = __shfl_sync(0xffffffffu, params_at, u0 + lane / 8);
+                const bool on = all || ((there >> (u0 + lane / 8)) & 1u);
+                const uint32_t to = stage_in + 2 * L::kCodes + lane * kQ4Params<D>;
+                const int64_t par = int64_t(uint64_t(at) * 16) + (lane & 7) * kQ4Params<D>;
+                cp_async<kQ4Params<D>>(to, p.k_pool + par, on);
+                cp_async<kQ4Params<D>>(to + L::kParams, p.v_pool + par, on);
+                stage_in = stage_in == ring + (L::kStages - 1) * L::kStage ? ring : stage_in + L::kStage;
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < L::kStages; ++i) issue(i);
+        // ---- Q, while the first tiles are on their way
+        Rows<D, NT> R;
+        R.bits = __shfl_sync(0xffffffffu, p.bits, 0);
+        R.pos0 = pos0;
+        R.rows = rows;
+        R.log2g = p.log2g;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) q4_take_q<D, NT>(R, qw[j], j, p.c, lane);
+        uint32_t stage = ring;
+        for (int i = 0, key0 = k_begin; i < n; ++i, key0 += kKeys) {
+            cp_wait<L::kStages - 1>();
+            __syncwarp();                                   // every lane's copies
+            float x[NT][2][4];
+            uint32_t prob[NT][2][2], rest[NT][2][2];
+            const bool masked = key0 + kKeys - 1 > pos0;
+            q4_scores<D, NT>(stage, R, 0, lane, x);
+            q4_scores<D, NT>(stage, R, 1, lane, x);
+            q4_softmax<D, NT>(R, x, masked, key0, lane, prob, rest);
+            if (masked) {
+                q4_values<D, NT, true>(stage, R, prob, rest, 0, key0, lane);
+                q4_values<D, NT, true>(stage, R, prob, rest, 1, key0, lane);
+            } else {
+                q4_values<D, NT, false>(stage, R, prob, rest, 0, key0, lane);
+                q4_values<D, NT, false>(stage, R, prob, rest, 1, key0, lane);
+            }
+            __syncwarp();                                   // every lane has read the stage
+            issue(i + L::kStages);
+            stage = stage == ring + (L::kStages - 1) * L::kStage ? ring : stage + L::kStage;
+        }
+        cp_wait<0>();
+        // ---- the rows' results: finished where they have one split, else left for the fold
+        const pa_work_item done = *at_item;                     // (again: not kept in registers meanwhile)
+        const bool whole = done.n_splits == 1;
+        float* const part = p.part + int64_t(done.tile0 + done.split) * (kCols * (D + 2));
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float l[2];
+            f2_split(R.l[j], l[0], l[1]);
+#pragma unroll
+            for (int d = 4; d <= 16; d <<= 1) {
+                l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
+                l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
+            }
+            const float f[2] = {whole ? __frcp_rn(l[0]) : 1.f, whole ? __frcp_rn(l[1]) : 1.f};
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float z = __shfl_sync(0xffffffffu, R.z[j][e], 4 * g + cc);
+                    const int row = 8 * j + 2 * cc + e;
+                    if (row >= rows) continue;
+                    const float y[4] = {(R.o[j][2 * g][e] + z) * f[e], (R.o[j][2 * g][2 + e] + z) * f[e],
+                                        (R.o[j][2 * g + 1][e] + z) * f[e], (R.o[j][2 * g + 1][2 + e] + z) * f[e]};
+                    const int col = 32 * g + 4 * r;
+                    if (whole) {
+                        const int64_t at = (int64_t(done.q_start + (row >> p.log2g)) * p.Hq + done.kv_head * gq +
+                                            (row & (gq - 1))) * D + col;
+                        *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                    } else {
+                        *reinterpret_cast<float4*>(part + row * D + col) = make_float4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+            if (r == 0 && !whole) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *reinterpret_cast<float2*>(part + kCols * D + 2 * (8 * j + 2 * cc + e)) = make_float2(-R.nm[j][e], l[e]);
+            }
+        }
+        __syncwarp();                                       // the ring is free again
     }
 }
 

@@ -63,8 +63,9 @@ class Case:
 
     def bound(self):
         """How far an output of rows read from the codes may be off, per value. Three parts:
-        the output's rounding, 2^-8 of it; the roundings of a term p (s (u - 8) + (m + 8 s)) to bf16: p (2^-8 of
-        both summands), the product p s (of the first) and the centre m + 8 s (of the second), so twice 2^-8
+        the output's rounding, 2^-8 of it; the roundings of a term p (s (u - 8) + (m + 8 s)): p to two bf16
+        (2^-8 of what the first leaves, 2^-16), the product of the second part and s (2^-8 of 2^-8), and to one bf16 the
+        whole product p s (2^-8 of the first summand) or the centre m + 8 s (2^-8 of the second), so 2^-8 + 2^-15
         of p (|s (u - 8)| + |m + 8 s|); and what fp32 does to a score: products and sums of a group stay
         below 144 sum |q| (codes as 128 + u), of which 2^-20 covers the sums of 32 products and four groups at 2^-23
         each (a tensor core may truncate), times the scale. A score off by e moves a weight by exp(e) - 1, and so the
@@ -86,7 +87,7 @@ class Case:
         kv = np.nan_to_num(q4.values(k, self.bs, D, False).astype(np.float64))
         big = pa.attention(q, kv, mag, self.table, self.cu, self.ctx, self.Hq)
         e = np.abs(q).reshape(self.T, self.Hq, D // 32, 32).sum(-1) @ np.full(D // 32, ks.max()) * 144 * 2.0 ** -20 / np.sqrt(D)
-        return out + (2 * 2.0 ** -8 + 2 * np.expm1(2 * e)[..., None] + 2.0 ** -18) * big
+        return out + (2.0 ** -8 + 2.0 ** -15 + 2 * np.expm1(2 * e)[..., None] + 2.0 ** -18) * big
 
     def plan(self, direct_rows=None, limits=None):
         return bd.pa_plan_step_q4(self.shape, self.cu, self.ctx, direct_rows, limits, device="cuda")
