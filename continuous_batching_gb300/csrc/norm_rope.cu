@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeParams
             if (r >= r1 || r * kHeads + sub >= heads) return;
             const __nv_bfloat16* s = src + r * (kHeads * D);
             if constexpr (INTER) {
-                const uint4 w = *reinterpret_cast<const uint4*>(s + a);
+                const uint4 w = *reinterpret_cast<const uint4*>(s + 8 * l);
                 xa = make_uint2(w.x, w.y);
                 xb = make_uint2(w.z, w.w);
             } else {
@@ -177,6 +177,20 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeParams
                 vc[e] = f2(wvi * co[i], wvj * co[j]);
                 vs[e] = f2(-wvi * si[i], -wvj * si[j]);
             }
+        }
+        // Rows in column order (4-bit pools): piece i of four columns, of half = n_pairs / 4 in either half of the
+        // rotated ones, is the first piece of lane i or the second of lane i - half, and behind those lane i / 2's own. In
+        // the first of two exchanges even lanes give their first piece and odd ones their second, in the other the
+        // rest, and every lane takes one of its two pieces from each.
+        int from_a = l, from_b = l;
+        bool a_second = l & 1;
+        if constexpr (C == kQ4 && !INTER && K != kQ) {
+            const int half = p.n_pairs / 4;
+            const auto from = [&](int i) { return i < half ? i : i < 2 * half ? i - half : l; };
+            const auto in_a = [&](int i) { return ((from(i) & 1) != 0) == (i < half ? false : i < 2 * half ? true : (i & 1) != 0); };
+            a_second = !in_a(2 * l);
+            from_a = from(2 * l + a_second);
+            from_b = from(2 * l + !a_second);
         }
         const int64_t row = K == kQ ? t * p.Hq : int64_t(slot) * p.Hkv;
 #pragma unroll 1
@@ -240,35 +254,27 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeParams
                     }
                 }
                 if constexpr (C == kQ4 && K != kQ) {
-                    // The row goes to the lanes in column order, lane l columns 8 l .. 8 l + 7: of the
-                    // rotated columns the first halves lie in the lanes' first pieces and the second
-                    // ones in their second pieces.
+                    // The row in column order, lane l columns 8 l .. 8 l + 7
                     uint32_t w[4] = {ya.x, ya.y, yb.x, yb.y};
                     if constexpr (!INTER) {
-                        const int half = p.n_pairs / 4;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int piece = 2 * l + i;
-                            const bool second = piece < half ? false
-                                                : piece < 2 * half ? true : i == 1;
-                            const int from = piece < half ? piece
-                                             : piece < 2 * half ? piece - half : l;
-                            const uint32_t x0 = __shfl_sync(0xffffffffu, ya.x, from, kLanes);
-                            const uint32_t x1 = __shfl_sync(0xffffffffu, ya.y, from, kLanes);
-                            const uint32_t y0 = __shfl_sync(0xffffffffu, yb.x, from, kLanes);
-                            const uint32_t y1 = __shfl_sync(0xffffffffu, yb.y, from, kLanes);
-                            w[2 * i] = second ? y0 : x0;
-                            w[2 * i + 1] = second ? y1 : x1;
-                        }
+                        const bool odd = l & 1;
+                        const uint32_t p0 = odd ? yb.x : ya.x, p1 = odd ? yb.y : ya.y;
+                        const uint32_t q0 = odd ? ya.x : yb.x, q1 = odd ? ya.y : yb.y;
+                        const uint32_t x0 = __shfl_sync(0xffffffffu, p0, from_a, kLanes);
+                        const uint32_t x1 = __shfl_sync(0xffffffffu, p1, from_a, kLanes);
+                        const uint32_t y0 = __shfl_sync(0xffffffffu, q0, from_b, kLanes);
+                        const uint32_t y1 = __shfl_sync(0xffffffffu, q1, from_b, kLanes);
+                        w[0] = a_second ? y0 : x0, w[1] = a_second ? y1 : x1;
+                        w[2] = a_second ? x0 : y0, w[3] = a_second ? x1 : y1;
                     }
-                    uint32_t codes, params;
-                    q4_quantise8(w, codes, params);
-                    if constexpr (K == kV) codes = q4_pair_groups(codes, l);
+                    uint32_t codes[1], params;
+                    q4_quantise<4>(w, codes, params);
+                    if constexpr (K == kV) codes[0] = q4_pair_groups(codes[0], l);
                     if (h >= heads) continue;
                     const int block = slot >> p.log2bs;
                     q4_store_row<D, K == kV>(static_cast<uint8_t*>(K == kV ? p.v_pool : p.k_pool),
                                              q4_base<D>(block, p.Hkv, h, 1 << p.log2bs), 1 << p.log2bs,
-                                             slot - (block << p.log2bs), l, codes, params);
+                                             slot - (block << p.log2bs), l, codes[0], params);
                     continue;
                 }
                 if (h >= heads) continue;

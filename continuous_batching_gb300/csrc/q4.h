@@ -35,20 +35,21 @@ __device__ __forceinline__ int64_t q4_base(int64_t block, int Hkv, int head, int
     return (block * Hkv + head) * (int64_t(bs) * kQ4Row<D>);
 }
 
-__device__ __forceinline__ float q4_min3(float a, float b, float c) {
-    float r;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+// Two bf16 at a time; NaN where one of a pair is.
+__device__ __forceinline__ uint32_t q4_max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float q4_max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+__device__ __forceinline__ uint32_t q4_min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// Lane l of a row's D / 8 lanes (consecutive lanes of a warp, all of them active) holds columns
-// 8 l .. 8 l + 7 as bf16 pairs w[0 .. 3]; its group is l / 4. Gives the lane's eight codes (column
-// 8 l + n in nibble n) and its group's (scale | minimum << 16):
+// Lane l of a row's D / (2 W) lanes (consecutive lanes of a warp, all of them active) holds columns
+// 2 W l .. 2 W l + 2 W - 1 as bf16 pairs w[0 .. W - 1], W 4 or 8; 16 / W lanes hold a group. Gives the lane's codes
+// (column 2 W l + 8 i + n in nibble n of word i) and its group's (scale | minimum << 16):
 //   minimum = min x;  scale = bf16((max x - min x) / 15);  code = clamp(rint((x - minimum) / scale), 0, 15)
 // with fp32 subtractions and divisions rounded to nearest (the minimum is a bf16 value itself, so
 // storing it loses nothing). All codes are 0 where the scale is 0. A group that holds a NaN or an
@@ -59,38 +60,27 @@ __device__ __forceinline__ float q4_max3(float a, float b, float c) {
 // nearest: before its rounding it is off by at most 2^-46 of itself (the remainder is exact and y is
 // off by 2^-24), while d / s, d of 24 bits and s of 8, is at least 2^-33 of itself away from every point half way
 // between two fp32 numbers (such a point has 25 bits, and no multiple of s by it has 24). The division by 15
-// likewise. Ranges so small or so large that a step could leave fp32's normal numbers divide as usual. (With a division per element the
-// write took 60 us for 16,384 tokens of 8 heads of 128, bound by instructions.)
-__device__ __forceinline__ void q4_quantise8(const uint32_t (&w)[4], uint32_t& codes,
-                                             uint32_t& params) {
-    float x[8];
-    uint64_t odd = 0;
+// likewise. Ranges so small or so large that a step could leave fp32's normal numbers divide as usual. (16,384
+// tokens of 8 heads of 128: 60 us with a division per element and fp32 extremes, bound by instructions, 23 with
+// this one, 15.1 with packed extremes and 16 columns a lane in the write.)
+template <int W>
+__device__ __forceinline__ void q4_quantise(const uint32_t (&w)[W], uint32_t (&codes)[W / 4], uint32_t& params) {
+    uint32_t top = w[0], low = w[0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 1; i < W; ++i) {
+        top = q4_max2(top, w[i]);
+        low = q4_min2(low, w[i]);
     }
-    float lo = x[0], hi = x[0];
+    // (max, -min), so that one maximum serves both
+    constexpr uint32_t kSign = 0x80000000u;
+    top = q4_max2(__byte_perm(top, low, 0x5410) ^ kSign, __byte_perm(top, low, 0x7632) ^ kSign);
 #pragma unroll
-    for (int i = 1; i < 7; i += 2) {
-        lo = q4_min3(lo, x[i], x[i + 1]);
-        hi = q4_max3(hi, x[i], x[i + 1]);
-    }
-    lo = fminf(lo, x[7]);
-    hi = fmaxf(hi, x[7]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) odd = fma2(f2(x[2 * i], x[2 * i + 1]), 0ull, odd);      // NaN where x is none
-    float odd0, odd1;
-    f2_split(odd, odd0, odd1);
-    if (!(odd0 + odd1 == 0.f)) hi = INFINITY;       // NaN or infinite
-#pragma unroll
-    for (int m = 1; m <= 2; m <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-    }
+    for (int m = 1; m < 16 / W; m <<= 1) top = q4_max2(top, __shfl_xor_sync(0xffffffffu, top, m));
+    const float hi = __uint_as_float(top << 16), lo = __uint_as_float((top & 0xFFFF0000u) ^ kSign);
     const float range = __fsub_rn(hi, lo);
-    codes = 0;
-    if (!(range < INFINITY)) {
+#pragma unroll
+    for (int k = 0; k < W / 4; ++k) codes[k] = 0;
+    if (!(range < INFINITY)) {                      // (NaN, too)
         params = 0x7FC07FC0u;
         return;
     }
@@ -113,24 +103,28 @@ __device__ __forceinline__ void q4_quantise8(const uint32_t (&w)[4], uint32_t& c
         const float y = __frcp_rn(sf);
         const uint64_t y2 = f2(y, y), n2 = f2(-sf, -sf), lo2 = f2(-lo, -lo), round2 = f2(kRound, kRound);
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {              // two elements at a time
-            const uint64_t d = add2(f2(x[2 * i], x[2 * i + 1]), lo2);
+        for (int i = W - 1; i >= 0; --i) {          // two elements at a time
+            const uint64_t d = add2(f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), lo2);
             uint64_t q = mul2(d, y2);
             q = fma2(fma2(q, n2, d), y2, q);        // (at most 15.06: no code but 0 .. 15)
             float u, v;
             f2_split(add2(q, round2), u, v);
-            codes = (codes * 16u + __float_as_uint(v)) * 16u + __float_as_uint(u);
+            codes[i / 4] = (codes[i / 4] * 16u + __float_as_uint(v)) * 16u + __float_as_uint(u);
         }
     } else {
         if (!(sf > 0.f)) return;
+#pragma unroll
+        for (int k = 0; k < W / 4; ++k) {
 #pragma unroll 1
-        for (int i = 7; i >= 0; --i) {
-            const uint32_t h = i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16;
-            const float q = __fdiv_rn(__fsub_rn(__uint_as_float(h), lo), sf);
-            codes = codes * 16u + __float_as_uint(fminf(q, 15.f) + kRound);
+            for (int i = 7; i >= 0; --i) {
+                const uint32_t x = i < 4 ? (i < 2 ? w[4 * k] : w[4 * k + 1]) : (i < 6 ? w[4 * k + 2] : w[4 * k + 3]);
+                const float q = __fdiv_rn(__fsub_rn(__uint_as_float(i & 1 ? x & 0xFFFF0000u : x << 16), lo), sf);
+                codes[k] = codes[k] * 16u + __float_as_uint(fminf(q, 15.f) + kRound);
+            }
         }
     }
-    codes -= kUpper;
+#pragma unroll
+    for (int k = 0; k < W / 4; ++k) codes[k] -= kUpper;
 }
 
 // A V row's 16-bit words pair the groups g and g + 1 (g even) of one r. Lanes (g, c) hold r = 2 c in
@@ -158,6 +152,34 @@ __device__ __forceinline__ void q4_store_row(uint8_t* pool, int64_t at, int bs, 
     reinterpret_cast<uint32_t*>(row)[q4_word<D, IS_V>(l)] = codes;
     if ((l & 3) == 0)
         reinterpret_cast<uint32_t*>(pool + at + bs * kQ4Codes<D> + o * kQ4Params<D>)[l >> 2] = params;
+}
+
+// The same of lanes with 16 columns, g = l / 2 and c = 2 (l % 2) and the next, codes[0] and codes[1].
+__device__ __forceinline__ void q4_pair_groups2(uint32_t (&codes)[2], int l) {
+    // the even group's lane takes r = 4 (l % 2) and the next, the odd one's the two behind them
+    const bool odd = (l >> 1) & 1;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? codes[0] : codes[1], 2);
+    const uint32_t even_half = odd ? other : codes[0], odd_half = odd ? codes[1] : other;
+    codes[0] = __byte_perm(even_half, odd_half, 0x5410);
+    codes[1] = __byte_perm(even_half, odd_half, 0x7632);
+}
+
+template <int D, bool IS_V>
+__device__ __forceinline__ void q4_store_row2(uint8_t* pool, int64_t at, int bs, int o, int l,
+                                              const uint32_t (&codes)[2], uint32_t params) {
+    constexpr int G = D / kQ4Group;
+    const int g = l >> 1, c = l & 1;
+    uint32_t* const row = reinterpret_cast<uint32_t*>(pool + at + o * kQ4Codes<D>);
+    if constexpr (IS_V) {
+        uint32_t* const to = row + (4 * c + 2 * (g & 1)) * (G / 2) + (g >> 1);
+        to[0] = codes[0];
+        to[G / 2] = codes[1];
+    } else {
+        uint32_t* const to = row + 2 * c * G + g;
+        to[0] = codes[0];
+        to[G] = codes[1];
+    }
+    if (c == 0) reinterpret_cast<uint32_t*>(pool + at + bs * kQ4Codes<D> + o * kQ4Params<D>)[g] = params;
 }
 
 // What reads the cache back takes a row by four lanes: lane c its D / 8 bytes of codes from c D / 8 on (w: G words)
