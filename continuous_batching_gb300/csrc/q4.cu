@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kRowsThreads) q4_write_kernel(const RowsParams
     constexpr int kLanes = D / 16;
     dependent_start();
     const int l = threadIdx.x % kLanes, bs = 1 << p.log2bs;
-    const uint32_t row = (blockIdx.x * uint32_t(kRowsThreads) + threadIdx.x) / kLanes;
+    const uint32_t row = blockIdx.x * uint32_t(kRowsThreads / kLanes) + threadIdx.x / kLanes;
     uint32_t k[8] = {}, v[8] = {};
     int32_t slot = -1;
     int head = 0;
@@ -823,9 +823,12 @@ template <int D, int NT>
 __global__ void __launch_bounds__(32 * kFoldWarps) q4_fold_kernel(const DirectParams p, const int32_t* fold) {
     constexpr int kCols = 8 * NT, kPart = kCols * (D + 2), kLane = D / 32;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // Every thread waits for the direct kernel, also one that has nothing to do: were this grid to end before that one,
+    // the next kernel, which waits for this grid alone, would start too early.
+    const auto wait = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
     // (what precedes the direct kernel has completed before this one starts, and that one writes none of these)
     const int idx = fold[blockIdx.x];
-    if (idx < 0) return;                                        // padding
+    if (idx < 0) return wait();                                 // padding
     const pa_work_item it = p.items[min(idx, p.n_items - 1)];
     const int row = blockIdx.y * kFoldWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const bool good = idx < p.n_items && it.kind == PA_ITEM_DIRECT && it.split == 0 && it.n_splits >= 2 && it.tile0 >= 0 &&
@@ -834,18 +837,18 @@ __global__ void __launch_bounds__(32 * kFoldWarps) q4_fold_kernel(const DirectPa
                       it.seq >= 0 && it.seq < p.B;
     if (!good) {
         if (row == 0 && lane == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
-        return;
+        return wait();
     }
-    if (row >= it.n_q << p.log2g) return;
+    if (row >= it.n_q << p.log2g) return wait();
     // an item that the direct kernel refused has left no parts
     const int ctx = p.ctx[it.seq], cu0 = p.cu[it.seq], cu1 = p.cu[it.seq + 1];
     if (ctx <= 0 || ctx != it.next || ctx > p.max_ctx || cu0 > it.q_start || it.q_start + it.n_q > cu1 ||
         int64_t(cu1) - cu0 > ctx)
-        return;
+        return wait();
     const int64_t keys = ctx - (cu1 - it.q_start) + it.n_q, len = q4_split_keys(ctx);
     if ((keys + len - 1) / len != it.n_splits || (int64_t(ctx) + (1 << p.log2bs) - 1) >> p.log2bs > p.max_blocks)
-        return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+        return wait();
+    wait();
     const int n_splits = it.n_splits;
     const float* const part = p.part + int64_t(it.tile0) * kPart + row * D + kLane * lane;
     const float* const stat = p.part + int64_t(it.tile0) * kPart + kCols * D + 2 * row;

@@ -440,6 +440,85 @@ def test_a_captured_step_follows_its_plan():
 
 
 @pytest.mark.gpu
+def test_a_chain_of_captured_steps_without_splits():
+    # room for splits that no context of these steps has: each step still ends after its rows are written, and the
+    # next one reads them as its q
+    case = Case([(1, 1 + s % 256) for s in range(600)], Hq=8, Hkv=8, D=64, bs=16, seed=41)
+    limits = bd.pa_q4_plan_limits(case.shape, 600, 600, 5000, 8, 0)
+    assert limits.n_fold > 0
+    plan = bd.pa_plan_step_q4(case.shape, case.cu, case.ctx, limits=limits, device="cuda")
+    k, v, table, cu, ctx = (dev(x) for x in (*case.pools, case.table, case.cu, case.ctx))
+    ws = torch.empty(bd.pa_q4_workspace_bytes(case.shape, plan) // 4, device="cuda")
+    rows = [bf16(case.q)] + [torch.zeros(600, 8, 64, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+
+    def step(i):
+        bd.paged_attention_step_q4(rows[i], k, v, table, cu, ctx, plan, ws, rows[i + 1], case.shape)
+
+    for i in range(8):
+        step(i)
+        torch.cuda.synchronize()
+    want = [bits_of(r) for r in rows]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(8):
+            step(i)
+    for _ in range(3):
+        for r in rows[1:]:
+            r.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for r, w in zip(rows, want):
+            np.testing.assert_array_equal(bits_of(r), w)
+
+
+@pytest.mark.gpu
+def test_lists_longer_than_a_cta_holds():
+    # 2,600 sequences of 8 heads over 152 lists: 136 or 137 items a list, 128 of which are held on chip
+    rng = np.random.default_rng(42)
+    case = Case([(1, int(c)) for c in rng.integers(1, 41, 2600)], Hq=8, Hkv=8, D=64, bs=8, seed=42)
+    first = np.diff(case.plan(8).words.cpu().numpy()[case.plan(8).sizes.n_direct * bd.ITEM_INTS:][:153])
+    assert first.max() > 128
+    case.check_direct(8)
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    cases = [Case([(1, 900 + 37 * s) for s in range(20)], seed=43), Case([(3, 5000 - 91 * s) for s in range(9)], seed=44)]
+    want = [c.run(16) for c in cases]
+    plans = [c.plan(16) for c in cases]
+    held = []
+    for c, p in zip(cases, plans):
+        held.append([bf16(c.q), *(dev(x) for x in (*c.pools, c.table, c.cu, c.ctx)), p,
+                     torch.empty(bd.pa_q4_workspace_bytes(c.shape, p) // 4, device="cuda"),
+                     torch.zeros(c.T, c.Hq, c.D, dtype=torch.bfloat16, device="cuda"), c.shape])
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, h in zip(streams, held):
+            with torch.cuda.stream(s):
+                bd.paged_attention_step_q4(*h)
+    torch.cuda.synchronize()
+    for h, w in zip(held, want):
+        np.testing.assert_array_equal(bits_of(h[-2]), w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [-100, -20, 20, 100])
+@pytest.mark.parametrize("direct_rows", [8, 16])
+def test_queries_of_every_magnitude(power, direct_rows):
+    # q 2^n over K 2^-n: the same scores, bit for bit, since every scaling on the way is by a power of two
+    case = Case([(1, 300), (1, 7), (2, 1000)], Hq=8, Hkv=2, seed=45)
+    want = case.run(direct_rows)
+    case.q = wl.f32_to_bf16_bits((pa.bf16_to_f64(case.q) * 2.0 ** power).astype(np.float32))
+    rows = case.pools[0].reshape(case.nb, case.Hkv, -1)
+    params = np.ascontiguousarray(rows[..., case.bs * (case.D // 2):]).view("<u2")
+    with np.errstate(invalid="ignore"):
+        scaled = wl.f32_to_bf16_bits((pa.bf16_to_f64(params) * 2.0 ** -power).astype(np.float32))
+    rows[..., case.bs * (case.D // 2):] = np.where(params == 0xFFFF, params, scaled).astype("<u2").view(np.uint8)
+    np.testing.assert_array_equal(case.run(direct_rows), want)
+
+
+@pytest.mark.gpu
 def test_pools_behind_two_gigabytes():
     """Pages at the end of pools of more than 2^31 bytes give the bits of the same pages in small ones."""
     a = Case([(1, 900), (3, 140), (50, 310)], 16, 8, 128, 128, seed=53)
