@@ -141,13 +141,15 @@ struct ExpandParams {
     const int32_t* list;                // [n][2]: sequence, 128-token block of it
     const int32_t* ex_table;            // [B][cols]: place of every block in the expanded pools, -1
     int32_t* ex_ctx;                    // [B]: the context of the sequences that are expanded, else 0
+    int32_t* queue;                     // of the rows read from the codes (see DirectParams): back to 0
     __nv_bfloat16 *k_out, *v_out;       // [n][128][Hkv][D]
     int32_t* err;
     int32_t n, B, cols, max_blocks, num_blocks, Hkv, g, log2bs, direct_rows;
 };
 
 // CTA (i, h): block i of the plan's list, head h: 128 tokens of K and V to bf16, one rounding each.
-// The values are those of paged_kv_read_q4. Bound by its writes (512 bytes a token and head, 160 read).
+// The values are those of paged_kv_read_q4. Bound by memory (512 bytes a token and head written, 160 read): 21,900
+// tokens of 8 heads take 14 us ahead of the attention that reads them.
 // The sequences whose context is expanded whole are told to the attention by ex_ctx; the others (rows that
 // are read directly, metadata that the plan was not made for) have a context of 0 there.
 template <int D>
@@ -156,6 +158,7 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
     dependent_start();
     const int bs = 1 << p.log2bs;
     const int64_t id = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+    if (id == 0) *p.queue = 0;
     for (int64_t s = id; s < p.B; s += int64_t(gridDim.x) * gridDim.y * 256) {
         const int64_t n_q = int64_t(p.cu[s + 1]) - p.cu[s];
         const int c = p.ctx[s];
@@ -231,12 +234,21 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
 // Loads: cp.async into a ring of kStages tiles per warp (codes and parameters; blocks outside the pool are
 // filled with zeros, keys of a block behind the last row may hold anything and are masked), no barrier
 // but the warp's own.
+//
+// Measured, with the join, replayed in a graph: 64 sequences of median 2,048 (up to 16,384) keys, 32 / 8 heads of 128
+// (314 MB of cache): 74.5 us, 4.2 TB/s; 32 of 1,000 to 40,000 keys, 64 / 8 heads: 57.8; 12 of 4 rows, 16 / 4
+// heads of 64: 14.1; one of 16,001 keys: 21.3. 32 single rows beside a chunk of 257: 84.6, 98.5 when they waited for
+// the chunk's 72 CTAs (or these for them). The copies alone take 63 us of the first: what the rest is bound by is
+// a tile's chain of products and softmax, 1,036 cycles with three warps a scheduler, of which the memory's rate
+// leaves 871. Tried without gain: 16 warps of 128 registers, a third stage, the next tile's scores between the
+// values' products, K as e4m3 (its mma.sync is emulated), splits joined inside this kernel (20 to 40 us more).
 struct DirectParams {
     const __nv_bfloat16* q;
     const uint8_t *k_pool, *v_pool;
     const int32_t *table, *cu, *ctx;
     const pa_work_item* items;
     const int32_t* lists;               // [PA_PLAN_CTAS + 1]: the first item of every CTA's
+    int32_t* queue;                     // behind an attention over chunks: the next item, for all CTAs; else null
     float* part;                        // [n_items][8 NT][D + 2]: splits' (acc, m, l)
     __nv_bfloat16* out;
     int32_t* err;
@@ -619,31 +631,40 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ pa_work_item held[kHeld];
     __shared__ int next_item;
-    // (in this order: q4_fold_kernel reads the metadata before it waits for this kernel)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Behind the attention over the step's chunks this kernel starts while that one ends: it reads nothing of it (what
+    // came before that one has completed, or it would not have let this one start), and waits for it at its end, for
+    // the sake of the next one. (In this order: q4_fold_kernel reads the metadata before it waits for this kernel.)
+    if (!p.queue) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, cc = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
     const int bs = 1 << p.log2bs, gq = 1 << p.log2g;
-    int first = p.lists[blockIdx.x], last = p.lists[blockIdx.x + 1];
+    // by itself: the CTA's list; else the whole plan, since CTAs start when the chunks leave them a multiprocessor
+    int first = p.queue ? 0 : p.lists[blockIdx.x], last = p.lists[p.queue ? PA_PLAN_CTAS : blockIdx.x + 1];
     if (first < 0 || last < first || last > p.n_items) {
         if (threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
         first = last = 0;               // (n_items is far from where the counter would wrap)
     }
+    const int n_held = p.queue ? 0 : min(last - first, kHeld);
     if (threadIdx.x == 0) next_item = first;
     // the list's first items, so that a warp that draws one has it at once
     constexpr int kWords = sizeof(pa_work_item) / 4;
-    for (int i = threadIdx.x; i < min(last - first, kHeld) * kWords; i += 32 * kWarps<NT>)
+    for (int i = threadIdx.x; i < n_held * kWords; i += 32 * kWarps<NT>)
         reinterpret_cast<int32_t*>(held)[i] = reinterpret_cast<const int32_t*>(p.items + first)[i];
     __syncthreads();
 
     for (;;) {
         int idx = 0;
-        if (lane == 0) idx = atomicAdd(&next_item, 1);
+        if (lane == 0) {
+            if (p.queue)
+                idx = atomicAdd(p.queue, 1);
+            else
+                idx = atomicAdd(&next_item, 1);
+        }
         idx = __shfl_sync(0xffffffffu, idx, 0);
         if (idx < 0 || idx >= last) break;
-        const pa_work_item* const at_item = idx - first < kHeld ? held + (idx - first) : p.items + idx;
+        const pa_work_item* const at_item = !p.queue && idx - first < kHeld ? held + (idx - first) : p.items + idx;
         const pa_work_item it = *at_item;
         // ---- The item by itself, then against the metadata it points at: what the loads of q, of the first blocks and
         // of the metadata need is in the item (next: the context it was planned for), so that they
@@ -807,6 +828,7 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
         }
         __syncwarp();                                       // the ring is free again
     }
+    if (p.queue) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Joins the splits of the rows of a tile and head: a warp per row, CTAs of the plan's fold list (items of split 0 with
@@ -972,7 +994,7 @@ int32_t launch_rows(RowsParams& p, int32_t T, const int32_t* slots, void* k_pool
 
 // Parts of the workspace, each a multiple of 256 bytes.
 struct Space {
-    size_t parts, partials, expanded, ctx, total;   // sizes: split parts, decode partials, one pool, contexts
+    size_t parts, partials, expanded, ctx, total;   // sizes: split parts, decode partials, one pool, contexts and queue
 };
 
 Space space_of(const pa_shape* s, const pa_q4_plan* p) {
@@ -986,7 +1008,7 @@ Space space_of(const pa_shape* s, const pa_q4_plan* p) {
         if (p->direct_rows < g && p->max_ctx > PA_SPLIT_TOKENS)
             w.partials = up(pa_workspace_bytes(s, p->T, p->max_ctx));
         w.expanded = up(size_t(p->n_expand) * 128 * s->num_kv_heads * D * 2);
-        w.ctx = up(size_t(p->B) * 4);
+        w.ctx = up((size_t(p->B) + 1) * 4);
     }
     w.total = w.parts + w.partials + 2 * w.expanded + w.ctx;
     return w;
@@ -1060,72 +1082,75 @@ extern "C" int32_t paged_attention_step_q4(const void* q, const void* k_pool, co
     uint8_t* at = static_cast<uint8_t*>(workspace);
     const int D = shape->head_dim, Hq = shape->num_q_heads, Hkv = shape->num_kv_heads, g = Hq / Hkv;
     const Q4Words f = q4_words(P);
-    if (P.n_direct > 0) {
-        DirectParams p{};
-        p.q = static_cast<const __nv_bfloat16*>(q);
-        p.k_pool = static_cast<const uint8_t*>(k_pool);
-        p.v_pool = static_cast<const uint8_t*>(v_pool);
-        p.table = block_table;
-        p.cu = cu_seqlens_q;
-        p.ctx = ctx_lens;
-        p.items = reinterpret_cast<const pa_work_item*>(words + f.direct);
-        p.lists = words + f.lists;
-        p.part = reinterpret_cast<float*>(at);
-        p.out = static_cast<__nv_bfloat16*>(out);
-        p.err = err_flag;
-        p.n_items = P.n_direct;
-        p.B = P.B;
-        p.T = P.T;
-        p.max_blocks = max_blocks;
-        p.num_blocks = shape->num_blocks;
-        p.Hq = Hq;
-        p.Hkv = Hkv;
-        p.log2g = ilog2(g);
-        p.log2bs = ilog2(shape->block_size);
-        // without a fold no row may have a second split: its part would have no place
-        p.max_ctx = P.n_fold > 0 ? P.max_ctx : int32_t(std::min<int64_t>(P.max_ctx, q4_one_split()));
-        p.c = float(1.4426950408889634 / std::sqrt(double(D)));
-        p.bits = 0x43004300u;
-        const int32_t* fold = words + f.fold;
-        const bool wide = P.direct_rows > 8;
-        st = D == 128 ? (wide ? launch_direct<128, 2>(p, fold, P.n_fold, P.fold_rows, stream)
-                              : launch_direct<128, 1>(p, fold, P.n_fold, P.fold_rows, stream))
-                      : (wide ? launch_direct<64, 2>(p, fold, P.n_fold, P.fold_rows, stream)
-                              : launch_direct<64, 1>(p, fold, P.n_fold, P.fold_rows, stream));
+    int32_t* queue = nullptr;
+    if (P.n_chunk > 0) {
+        ExpandParams e{};
+        e.k_pool = static_cast<const uint8_t*>(k_pool);
+        e.v_pool = static_cast<const uint8_t*>(v_pool);
+        e.table = block_table;
+        e.cu = cu_seqlens_q;
+        e.ctx = ctx_lens;
+        e.list = words + f.expand;
+        e.ex_table = words + f.table;
+        e.k_out = reinterpret_cast<__nv_bfloat16*>(at + w.parts + w.partials);
+        e.v_out = reinterpret_cast<__nv_bfloat16*>(at + w.parts + w.partials + w.expanded);
+        e.ex_ctx = reinterpret_cast<int32_t*>(at + w.parts + w.partials + 2 * w.expanded);
+        e.queue = queue = e.ex_ctx + P.B;
+        e.err = err_flag;
+        e.n = P.n_expand;
+        e.B = P.B;
+        e.cols = P.expand_cols;
+        e.max_blocks = max_blocks;
+        e.num_blocks = shape->num_blocks;
+        e.Hkv = Hkv;
+        e.g = g;
+        e.log2bs = ilog2(shape->block_size);
+        e.direct_rows = P.direct_rows;
+        cudaLaunchAttribute pdl;
+        auto cfg = dependent_launch(&pdl, dim3(unsigned(P.n_expand), unsigned(Hkv)), 256, 0, stream);
+        st = note_cuda(D == 128 ? cudaLaunchKernelEx(&cfg, q4_expand_kernel<128>, e)
+                                : cudaLaunchKernelEx(&cfg, q4_expand_kernel<64>, e));
+        if (st) return st;
+        pa_shape ex = *shape;
+        ex.block_size = 128;
+        ex.num_blocks = P.n_expand;
+        st = attention_step_expanded(q, e.k_out, e.v_out, e.ex_table, e.cols, cu_seqlens_q, e.ex_ctx, P.B,
+                                     P.T, P.max_ctx,
+                                     reinterpret_cast<const pa_work_item*>(words + f.chunk), P.n_chunk,
+                                     w.partials ? at + w.parts : nullptr, out, &ex, err_flag, stream);
         if (st) return st;
     }
-    if (P.n_chunk == 0) return PA_OK;
-    ExpandParams e{};
-    e.k_pool = static_cast<const uint8_t*>(k_pool);
-    e.v_pool = static_cast<const uint8_t*>(v_pool);
-    e.table = block_table;
-    e.cu = cu_seqlens_q;
-    e.ctx = ctx_lens;
-    e.list = words + f.expand;
-    e.ex_table = words + f.table;
-    e.k_out = reinterpret_cast<__nv_bfloat16*>(at + w.parts + w.partials);
-    e.v_out = reinterpret_cast<__nv_bfloat16*>(at + w.parts + w.partials + w.expanded);
-    e.ex_ctx = reinterpret_cast<int32_t*>(at + w.parts + w.partials + 2 * w.expanded);
-    e.err = err_flag;
-    e.n = P.n_expand;
-    e.B = P.B;
-    e.cols = P.expand_cols;
-    e.max_blocks = max_blocks;
-    e.num_blocks = shape->num_blocks;
-    e.Hkv = Hkv;
-    e.g = g;
-    e.log2bs = ilog2(shape->block_size);
-    e.direct_rows = P.direct_rows;
-    cudaLaunchAttribute pdl;
-    auto cfg = dependent_launch(&pdl, dim3(unsigned(P.n_expand), unsigned(Hkv)), 256, 0, stream);
-    st = note_cuda(D == 128 ? cudaLaunchKernelEx(&cfg, q4_expand_kernel<128>, e)
-                            : cudaLaunchKernelEx(&cfg, q4_expand_kernel<64>, e));
-    if (st) return st;
-    pa_shape ex = *shape;
-    ex.block_size = 128;
-    ex.num_blocks = P.n_expand;
-    return attention_step_expanded(q, e.k_out, e.v_out, e.ex_table, e.cols, cu_seqlens_q, e.ex_ctx, P.B,
-                                   P.T, P.max_ctx,
-                                   reinterpret_cast<const pa_work_item*>(words + f.chunk), P.n_chunk,
-                                   w.partials ? at + w.parts : nullptr, out, &ex, err_flag, stream);
+    if (P.n_direct == 0) return PA_OK;
+    DirectParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k_pool = static_cast<const uint8_t*>(k_pool);
+    p.v_pool = static_cast<const uint8_t*>(v_pool);
+    p.table = block_table;
+    p.cu = cu_seqlens_q;
+    p.ctx = ctx_lens;
+    p.items = reinterpret_cast<const pa_work_item*>(words + f.direct);
+    p.lists = words + f.lists;
+    p.queue = queue;
+    p.part = reinterpret_cast<float*>(at);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.err = err_flag;
+    p.n_items = P.n_direct;
+    p.B = P.B;
+    p.T = P.T;
+    p.max_blocks = max_blocks;
+    p.num_blocks = shape->num_blocks;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.log2g = ilog2(g);
+    p.log2bs = ilog2(shape->block_size);
+    // without a fold no row may have a second split: its part would have no place
+    p.max_ctx = P.n_fold > 0 ? P.max_ctx : int32_t(std::min<int64_t>(P.max_ctx, q4_one_split()));
+    p.c = float(1.4426950408889634 / std::sqrt(double(D)));
+    p.bits = 0x43004300u;
+    const int32_t* fold = words + f.fold;
+    const bool wide = P.direct_rows > 8;
+    return D == 128 ? (wide ? launch_direct<128, 2>(p, fold, P.n_fold, P.fold_rows, stream)
+                            : launch_direct<128, 1>(p, fold, P.n_fold, P.fold_rows, stream))
+                    : (wide ? launch_direct<64, 2>(p, fold, P.n_fold, P.fold_rows, stream)
+                            : launch_direct<64, 1>(p, fold, P.n_fold, P.fold_rows, stream));
 }

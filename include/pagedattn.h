@@ -770,10 +770,13 @@ int32_t pa_plan_step_q4(const pa_shape* shape, int32_t B, const int32_t* cu_seql
  * calls or graphs that may overlap need one each. */
 size_t pa_q4_workspace_bytes(const pa_shape* shape, const pa_q4_plan* plan);
 
-/* paged_attention_step over 4-bit pools. Rows read from the codes: exact products of q and the codes, fp32
- * sums, the scales applied in fp32 (K is not rounded beyond its code), p * scale rounded to bf16, splits
- * whose length depends on the sequence's context alone, joined in a fixed order. Rows over expanded
- * contexts: K and V values rounded to bf16, otherwise as paged_attention_step (a NaN or infinity among the
+/* paged_attention_step over 4-bit pools. Rows read from the codes: exact products of q and the codes (of a row of q,
+ * elements below 2^-25 of its largest may lose bits; elements of 2^120 and more may overflow), fp32 sums, the
+ * scales applied in fp32 (K is not rounded beyond its code), p in 16 bits, p * scale and the middle of a group
+ * (minimum + 8 scale) each rounded once to bf16, splits whose length depends on the sequence's context alone, joined
+ * in a fixed order. Rows over expanded contexts: K and V values rounded to bf16 and p as paged_attention_step
+ * rounds it (against 64 bits an output is off by 0.0032 of its size where the other way leaves 0.0024 and its
+ * own rounding to bf16 alone 0.0017), otherwise as that step (a NaN or infinity among the
  * V of a later key of the chunk reaches the rows before it, as there; not so for rows read from the
  * codes). A row's bits depend on its own query, keys, position and context, and on which of the two ways its
  * sequence takes: with direct_rows 0 every row takes the second, and a token has the same bits as a
@@ -781,8 +784,8 @@ size_t pa_q4_workspace_bytes(const pa_shape* shape, const pa_q4_plan* plan);
  * Device: words, the plan's; q, out [T, Hq, D] bf16; block_table [B, max_blocks], cu_seqlens_q, ctx_lens
  * as planned (items that they contradict are skipped and set PA_DEVERR_META, their rows not written);
  * keys of a block outside the pool read as 0 and set PA_DEVERR_BLOCK; workspace 16-byte aligned.
- * Host checks: as paged_attention_step. Launches (programmatic dependents of what precedes them): the rows read
- * from the codes, the join of their splits; the expansion, the attention over it and its combine; each only
+ * Host checks: as paged_attention_step. Launches (programmatic dependents of what precedes them): the expansion,
+ * the attention over it and its combine; the rows read from the codes, the join of their splits; each only
  * where the plan has sizes for it. */
 int32_t paged_attention_step_q4(const void* q, const void* k_pool, const void* v_pool,
                                 const int32_t* block_table, int32_t max_blocks,

@@ -439,36 +439,51 @@ def test_a_captured_step_follows_its_plan():
             assert int(s.err.item()) == 0 and np.array_equal(bits_of(s.out), want[i])
 
 
-@pytest.mark.gpu
-def test_a_chain_of_captured_steps_without_splits():
-    # room for splits that no context of these steps has: each step still ends after its rows are written, and the
-    # next one reads them as its q
-    case = Case([(1, 1 + s % 256) for s in range(600)], Hq=8, Hkv=8, D=64, bs=16, seed=41)
-    limits = bd.pa_q4_plan_limits(case.shape, 600, 600, 5000, 8, 0)
-    assert limits.n_fold > 0
-    plan = bd.pa_plan_step_q4(case.shape, case.cu, case.ctx, limits=limits, device="cuda")
+def _chain(case, plan, n=8):
+    """n steps whose outputs are the next one's q, captured, against the same steps one by one."""
     k, v, table, cu, ctx = (dev(x) for x in (*case.pools, case.table, case.cu, case.ctx))
     ws = torch.empty(bd.pa_q4_workspace_bytes(case.shape, plan) // 4, device="cuda")
-    rows = [bf16(case.q)] + [torch.zeros(600, 8, 64, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    rows = [bf16(case.q)] + [torch.zeros(case.T, case.Hq, case.D, dtype=torch.bfloat16, device="cuda") for _ in range(n)]
 
     def step(i):
         bd.paged_attention_step_q4(rows[i], k, v, table, cu, ctx, plan, ws, rows[i + 1], case.shape)
 
-    for i in range(8):
+    for i in range(n):
         step(i)
         torch.cuda.synchronize()
     want = [bits_of(r) for r in rows]
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        for i in range(8):
+        for i in range(n):
             step(i)
     for _ in range(3):
         for r in rows[1:]:
             r.zero_()
+        ws.fill_(float("nan"))
         graph.replay()
         torch.cuda.synchronize()
         for r, w in zip(rows, want):
             np.testing.assert_array_equal(bits_of(r), w)
+
+
+@pytest.mark.gpu
+def test_a_chain_of_captured_steps_without_splits():
+    # room for splits that no context of these steps has: each step still ends after its rows are written
+    case = Case([(1, 1 + s % 256) for s in range(600)], Hq=8, Hkv=8, D=64, bs=16, seed=41)
+    limits = bd.pa_q4_plan_limits(case.shape, 600, 600, 5000, 8, 0)
+    assert limits.n_fold > 0
+    _chain(case, bd.pa_plan_step_q4(case.shape, case.cu, case.ctx, limits=limits, device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("chunks, rows", [(1, 250), (6, 3), (40, 2)])
+def test_a_chain_of_captured_steps_with_chunks(chunks, rows):
+    # the rows read from the codes start while the chunks' attention ends: whichever of them is last, the next step
+    # waits for it
+    case = Case([(100, 900 - 3 * s) for s in range(chunks)] + [(1, 31 + 13 * s) for s in range(rows)], seed=46)
+    plan = case.plan(16)
+    assert plan.sizes.n_direct > 0 and plan.sizes.n_chunk > 0
+    _chain(case, plan)
 
 
 @pytest.mark.gpu
