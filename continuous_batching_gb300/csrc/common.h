@@ -17,16 +17,16 @@
 
 namespace pa_detail {
 
-// Keys of a split of a row read from the codes, by its sequence's context alone. A split is a warp's work:
+// Keys of a split of a row read from the codes, by its sequence's context alone. A split is the work of two warps:
 // short ones where there are few, so that a single sequence spreads over the GPU, and longer ones where
 // what a split costs beyond its keys (its start, its result written and read once more) would add up.
-// Multiples of 32. (64 sequences of median 2,048 keys / 12 of 700 to 6,000 / one of 16,001: 73 / 14 / 21 us; with 256
-// keys everywhere 80 / 14.6 / 17, with 1,024 from 4,096 on 70 / 33 / 34.)
+// Multiples of 32. (64 sequences of median 2,048 keys / 12 of 700 to 6,000 / one of 16,001: 72.8 / 13.7 / 20.5 us; with 512
+// keys up to 32,768 78.4 / 13.7 / 15.2, half of each length 80.9 / 12.7 / 15.2, 640 up to 6,144 71.0 / 15.4 / 20.5.)
 __host__ __device__ constexpr int64_t q4_split_keys(int32_t ctx) {
-    return ctx <= 6144 ? 256 : ctx <= 12288 ? 384 : ctx <= 32768 ? 512 : 1024;
+    return ctx <= 6144 ? 512 : ctx <= 12288 ? 768 : ctx <= 32768 ? 1024 : 2048;
 }
 // The longest context of one split.
-constexpr int64_t q4_one_split() { return 256; }
+constexpr int64_t q4_one_split() { return 512; }
 // Most splits of any context up to max_ctx.
 inline int64_t q4_max_splits(int64_t max_ctx) {
     const auto n = [](int64_t c) { return c <= 0 ? 1 : (c + q4_split_keys(int32_t(c)) - 1) / q4_split_keys(int32_t(c)); };

@@ -204,11 +204,15 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
 // ------------------------------------------------------------------- rows read from the codes
 //
 // An item is one KV head, one tile of query rows (tokens x heads of its group, at most 8 NT of them)
-// and one split of the sequence's keys: the work of one warp, which takes the split's tiles of 32 keys in turn and keeps
-// their online softmax. A CTA's warps draw items from its list (one CTA and list a
-// multiprocessor, dealt by cost on the host), so nothing waits for anything but its own loads. A row's splits are
-// joined in a fixed order by q4_fold_kernel. A split's length depends on the sequence's context alone
-// (q4_split_keys), so a row's bits do not depend on the batch.
+// and one split of the sequence's keys: the work of two warps, which take every second one of the split's tiles of 32
+// keys, keep their online softmax, and join at its end. A CTA's pairs draw items from its list (one CTA and list a
+// multiprocessor, dealt by cost on the host), so that a warp waits for nothing but its own loads, and the first one of
+// a pair for the second's part. A row's splits are joined in a fixed order by q4_fold_kernel. A split's length
+// depends on the sequence's context alone (q4_split_keys), so a row's bits do not depend on the batch.
+// A pair and not a warp: an item costs a warp about as much beside its tiles as a tile and a half does (q, state,
+// results), so its tiles should be many, and splits few; but a sequence by itself wants short chains. One warp a split,
+// of half the length: decode batch 74.5 us, long tail 59, one sequence 21.3, four drafted tokens 14.1, where pairs take
+// 72.8 / 57 / 20.5 / 13.7; four warps a split of 1,024 keys or more 77.5 / 61 / 14.2 / 13.7.
 //
 // Why mma.sync and not tcgen05: the contraction's free dimension is at most 8 NT columns, so the tensor
 // rate is no concern; what is, is the way of the codes to the tensor core. tcgen05 would take them expanded to
@@ -236,12 +240,13 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
 // but the warp's own.
 //
 // Measured, with the join, replayed in a graph: 64 sequences of median 2,048 (up to 16,384) keys, 32 / 8 heads of 128
-// (314 MB of cache): 74.5 us, 4.2 TB/s; 32 of 1,000 to 40,000 keys, 64 / 8 heads: 57.8; 12 of 4 rows, 16 / 4
-// heads of 64: 14.1; one of 16,001 keys: 21.3. 32 single rows beside a chunk of 257: 84.6, 98.5 when they waited for
+// (314 MB of cache): 72.8 us, 4.3 TB/s; 32 of 1,000 to 40,000 keys, 64 / 8 heads: 57; 12 of 4 rows, 16 / 4
+// heads of 64: 13.7; one of 16,001 keys: 20.5. 32 single rows beside a chunk of 257: 82, 14 more when they waited for
 // the chunk's 72 CTAs (or these for them). The copies alone take 63 us of the first: what the rest is bound by is
 // a tile's chain of products and softmax, 1,036 cycles with three warps a scheduler, of which the memory's rate
 // leaves 871. Tried without gain: 16 warps of 128 registers, a third stage, the next tile's scores between the
-// values' products, K as e4m3 (its mma.sync is emulated), splits joined inside this kernel (20 to 40 us more).
+// values' products, K as e4m3 (its mma.sync is emulated), splits joined inside this kernel (20 to 40 us more), the
+// next item's first tiles or its L2 lines asked for ahead (3 to 6 us more).
 struct DirectParams {
     const __nv_bfloat16* q;
     const uint8_t *k_pool, *v_pool;
@@ -273,6 +278,19 @@ struct Ring {
     static constexpr int kStage = 2 * (kCodes + kParams);       // K codes, V codes, K, V parameters
     static constexpr int kWarp = kStages * kStage;
 };
+
+// what a pair's second warp hands to the first: a float4 of each lane for every product tile, (l, maxima) and z
+template <int D, int NT>
+constexpr int kHanded = NT * (2 * (D / kQ4Group) + 2) * 512;
+
+// barriers of two warps
+__device__ __forceinline__ void pair_sync(int id) {
+    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void pair_arrive(int id) {
+    __syncwarp();
+    asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
+}
 
 template <int D>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[D / kQ4Group]) {
@@ -630,7 +648,7 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
     using L = Ring<D>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ pa_work_item held[kHeld];
-    __shared__ int next_item;
+    __shared__ int next_item, drawn[kWarps<NT> / 2][2];
     // Behind the attention over the step's chunks this kernel starts while that one ends: it reads nothing of it (what
     // came before that one has completed, or it would not have let this one start), and waits for it at its end, for
     // the sake of the next one. (In this order: q4_fold_kernel reads the metadata before it waits for this kernel.)
@@ -638,7 +656,9 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, cc = lane & 3;
+    const int pair = warp >> 1, half = warp & 1;
     const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
+    float4* const handed = reinterpret_cast<float4*>(smem + kWarps<NT> * L::kWarp + pair * kHanded<D, NT>) + lane;
     const int bs = 1 << p.log2bs, gq = 1 << p.log2g;
     // by itself: the CTA's list; else the whole plan, since CTAs start when the chunks leave them a multiprocessor
     int first = p.queue ? 0 : p.lists[blockIdx.x], last = p.lists[p.queue ? PA_PLAN_CTAS : blockIdx.x + 1];
@@ -654,16 +674,47 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
         reinterpret_cast<int32_t*>(held)[i] = reinterpret_cast<const int32_t*>(p.items + first)[i];
     __syncthreads();
 
-    for (;;) {
+    // The pair's second warp draws its items, one ahead of the first warp: what it arrives with at the barrier `ready` is
+    // its part of an item and the next item's index. It may hand over another part once the first warp has arrived at
+    // `taken`. Both pass them once for every index drawn, whatever they find there.
+    const auto draw = [&](int turn) {
         int idx = 0;
         if (lane == 0) {
             if (p.queue)
                 idx = atomicAdd(p.queue, 1);
             else
                 idx = atomicAdd(&next_item, 1);
+            drawn[pair][turn & 1] = idx;
         }
-        idx = __shfl_sync(0xffffffffu, idx, 0);
-        if (idx < 0 || idx >= last) break;
+        return __shfl_sync(0xffffffffu, idx, 0);
+    };
+    const int ready = 1 + 2 * pair, taken = 2 + 2 * pair;
+    int idx;
+    if (half) {
+        idx = draw(0);
+        __syncwarp();
+        pair_sync(ready);
+    } else {
+        pair_sync(ready);
+        idx = drawn[pair][0];
+    }
+    // an item that is not worked on
+    const auto pass = [&](int turn) {
+        if (half) {
+            if (turn > 0) pair_sync(taken);
+            idx = draw(turn + 1);
+            pair_arrive(ready);
+        } else {
+            pair_sync(ready);
+            idx = drawn[pair][(turn + 1) & 1];
+            pair_arrive(taken);
+        }
+    };
+    for (int turn = 0;; ++turn) {
+        if (idx < 0 || idx >= last) {
+            if (half && turn > 0) pair_sync(taken);
+            break;
+        }
         const pa_work_item* const at_item = !p.queue && idx - first < kHeld ? held + (idx - first) : p.items + idx;
         const pa_work_item it = *at_item;
         // ---- The item by itself, then against the metadata it points at: what the loads of q, of the first blocks and
@@ -677,6 +728,7 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
                     (int64_t(ctx) + bs - 1) / bs <= p.max_blocks && it.split * q4_split_keys(ctx) < ctx;
         if (!good) {
             if (lane == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+            pass(turn);
             continue;
         }
         const int ctx_now = __ldg(p.ctx + it.seq), cu0 = __ldg(p.cu + it.seq), cu1 = __ldg(p.cu + it.seq + 1);
@@ -684,7 +736,7 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
         const int32_t* table = p.table + int64_t(it.seq) * p.max_blocks;
         // (the split's keys up to the context: the last row may lie before it)
         const auto block_of = [&](int tile) {
-            const int key = k_begin + (tile + (lane >> 2)) * kKeys + 8 * (lane & 3);
+            const int key = k_begin + (2 * (tile + (lane >> 2)) + half) * kKeys + 8 * (lane & 3);
             return key < k_last ? max(__ldg(table + (key >> p.log2bs)), -1) : -2;
         };
         int block = block_of(0);
@@ -705,16 +757,18 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
                int64_t(cu1) - cu0 <= ctx && (keys + len - 1) / len == it.n_splits;
         if (!good) {
             if (lane == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
+            pass(turn);
             continue;
         }
         const int k_end = min(keys, k_begin + len);
-        const int n = (k_end - k_begin + kKeys - 1) / kKeys;    // tiles of 32 keys
+        // tiles of 32 keys: the pair's warps take every second one
+        const int n = ((k_end - k_begin + kKeys - 1) / kKeys + 1 - half) / 2;
         // Lane i looks after the eight keys i % 4 of tile i / 4 of eight tiles: where their code rows and their
         // parameter rows begin, in units of 16 bytes, and (a bit of `there`) whether their block is there.
         constexpr int kRow16 = kQ4Codes<D> / 16, kPar8 = 8 * kQ4Params<D> / 16;
         uint32_t codes_at = 0, params_at = 0, there = 0;
         const auto turn_to = [&](int tile) {                // the eight tiles from `tile` on
-            const int key = k_begin + (tile + (lane >> 2)) * kKeys + 8 * (lane & 3);
+            const int key = k_begin + (2 * (tile + (lane >> 2)) + half) * kKeys + 8 * (lane & 3);
             const bool on = block >= 0 && block < p.num_blocks;
             if (!on && block != -2 && p.err) atomicOr(p.err, PA_DEVERR_BLOCK);   // its keys read as 0
             there = __ballot_sync(0xffffffffu, on);
@@ -766,7 +820,7 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
 #pragma unroll
         for (int j = 0; j < NT; ++j) q4_take_q<D, NT>(R, qw[j], j, p.c, lane);
         uint32_t stage = ring;
-        for (int i = 0, key0 = k_begin; i < n; ++i, key0 += kKeys) {
+        for (int i = 0, key0 = k_begin + half * kKeys; i < n; ++i, key0 += 2 * kKeys) {
             cp_wait<L::kStages - 1>();
             __syncwarp();                                   // every lane's copies
             float x[NT][2][4];
@@ -787,6 +841,48 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
             stage = stage == ring + (L::kStages - 1) * L::kStage ? ring : stage + L::kStage;
         }
         cp_wait<0>();
+        // ---- the second warp's part goes to the first
+        if (half) {
+            if (turn > 0) pair_sync(taken);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float4* const to = handed + j * (2 * G + 2) * 32;
+#pragma unroll
+                for (int t = 0; t < 2 * G; ++t) to[32 * t] = make_float4(R.o[j][t][0], R.o[j][t][1], R.o[j][t][2], R.o[j][t][3]);
+                float l0, l1;
+                f2_split(R.l[j], l0, l1);
+                to[32 * 2 * G] = make_float4(l0, l1, R.nm[j][0], R.nm[j][1]);
+                to[32 * (2 * G + 1)] = make_float4(R.z[j][0], R.z[j][1], R.z[j][2], R.z[j][3]);
+            }
+            idx = draw(turn + 1);
+            pair_arrive(ready);
+            continue;
+        }
+        pair_sync(ready);
+        idx = drawn[pair][(turn + 1) & 1];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const float4* const from = handed + j * (2 * G + 2) * 32;
+            const float4 s = from[32 * 2 * G], z = from[32 * (2 * G + 1)];
+            const float m0 = fminf(R.nm[j][0], s.z), m1 = fminf(R.nm[j][1], s.w);    // minus the maxima
+            const float a0 = ex2(m0 - R.nm[j][0]), a1 = ex2(m1 - R.nm[j][1]), b0 = ex2(m0 - s.z), b1 = ex2(m1 - s.w);
+            float l0, l1;
+            f2_split(R.l[j], l0, l1);
+            R.l[j] = f2(l0 * a0 + s.x * b0, l1 * a1 + s.y * b1);
+            R.z[j][0] = R.z[j][0] * a0 + z.x * b0;
+            R.z[j][1] = R.z[j][1] * a1 + z.y * b1;
+            R.nm[j][0] = m0;
+            R.nm[j][1] = m1;
+#pragma unroll
+            for (int t = 0; t < 2 * G; ++t) {
+                const float4 o = from[32 * t];
+                R.o[j][t][0] = R.o[j][t][0] * a0 + o.x * b0;
+                R.o[j][t][1] = R.o[j][t][1] * a1 + o.y * b1;
+                R.o[j][t][2] = R.o[j][t][2] * a0 + o.z * b0;
+                R.o[j][t][3] = R.o[j][t][3] * a1 + o.w * b1;
+            }
+        }
+        pair_arrive(taken);
         // ---- the rows' results: finished where they have one split, else left for the fold
         const pa_work_item done = *at_item;                     // (again: not kept in registers meanwhile)
         const bool whole = done.n_splits == 1;
@@ -939,7 +1035,7 @@ int32_t launch_direct(const DirectParams& p, const int32_t* fold, int32_t n_fold
     int32_t st = note_cuda(cudaGetDevice(&dev));
     if (st) return st;
     if (dev < 0 || dev >= kMaxDevices) return PA_ERR_INVALID;
-    constexpr int smem = kWarps<NT> * Ring<D>::kWarp;
+    constexpr int smem = kWarps<NT> * Ring<D>::kWarp + kWarps<NT> / 2 * kHanded<D, NT>;
     if (!raised[dev].load(std::memory_order_acquire)) {
         st = note_cuda(cudaFuncSetAttribute(q4_direct_kernel<D, NT>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem));

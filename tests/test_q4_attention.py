@@ -117,7 +117,7 @@ def _items(words, at, n):
 
 
 def _split(ctx):
-    return 256 if ctx <= 6144 else 384 if ctx <= 12288 else 512 if ctx <= 32768 else 1024
+    return 512 if ctx <= 6144 else 768 if ctx <= 12288 else 1024 if ctx <= 32768 else 2048
 
 
 @pytest.mark.parametrize("direct_rows", [0, 8, 16, 64])
@@ -150,7 +150,8 @@ def test_plan_covers_every_row_once(direct_rows, Hq, Hkv):
         n_real = int((direct["n_q"] > 0).sum())
         assert first[0] == 0 and (np.diff(first) >= 0).all() and first[-1] == n_real and (direct[n_real:]["n_q"] == 0).all()
         cost = [int((direct["n_tiles"][a:b] + 1).sum()) for a, b in zip(first, first[1:])]
-        assert not cost or max(cost) - min(cost) <= 10
+        # every item goes to the list of the least cost, so no two differ by more than an item's (here rounded up)
+        assert not cost or max(cost) - min(cost) <= direct["n_tiles"].max() + 2
         for i in range(n_real):
             it = direct[i]
             q = int(it["seq"])
