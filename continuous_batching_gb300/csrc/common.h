@@ -10,8 +10,8 @@
 #define PA_ROWS 128
 
 // Most rows (query tokens times heads of a group) of a sequence that the default reads from the codes. Where the
-// GPU is full the two ways meet at about 60 rows (8 sequences of 4,000 keys, 32 / 8 heads of 128: 37 us against
-// 68 with 32 rows, 72 against 70 with 64; 32 of 3,000 keys, 8 / 8 heads: 101 against 158, 191 against 159); a
+// GPU is full the two ways meet at about 60 rows (8 sequences of 4,000 keys, 32 / 8 heads of 128: 40 us against
+// 69 with 32 rows, 77 against 70 with 64; 32 of 3,000 keys, 8 / 8 heads: 110 against 159, 206 against 160); a
 // single sequence is faster read from the codes up to 250 rows, but the choice may not depend on the batch.
 #define PA_Q4_DIRECT_ROWS 48
 

@@ -283,6 +283,11 @@ struct Ring {
 template <int D, int NT>
 constexpr int kHanded = NT * (2 * (D / kQ4Group) + 2) * 512;
 
+// n is the number of splits of `len` keys that `keys` take
+__device__ __forceinline__ bool split_in(int64_t keys, int64_t len, int n) {
+    return n * len >= keys && (n - 1) * len < keys;
+}
+
 // barriers of two warps
 __device__ __forceinline__ void pair_sync(int id) {
     asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
@@ -754,7 +759,7 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
         const int pos0 = ctx - (cu1 - it.q_start);              // position of the first row
         const int keys = pos0 + it.n_q;                         // up to the last row
         good = ctx_now == ctx && cu0 <= it.q_start && it.q_start + it.n_q <= cu1 &&
-               int64_t(cu1) - cu0 <= ctx && (keys + len - 1) / len == it.n_splits;
+               int64_t(cu1) - cu0 <= ctx && split_in(keys, len, it.n_splits);
         if (!good) {
             if (lane == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
             pass(turn);
@@ -964,7 +969,7 @@ __global__ void __launch_bounds__(32 * kFoldWarps) q4_fold_kernel(const DirectPa
         int64_t(cu1) - cu0 > ctx)
         return wait();
     const int64_t keys = ctx - (cu1 - it.q_start) + it.n_q, len = q4_split_keys(ctx);
-    if ((keys + len - 1) / len != it.n_splits || (int64_t(ctx) + (1 << p.log2bs) - 1) >> p.log2bs > p.max_blocks)
+    if (!split_in(keys, len, it.n_splits) || (int64_t(ctx) + (1 << p.log2bs) - 1) >> p.log2bs > p.max_blocks)
         return wait();
     wait();
     const int n_splits = it.n_splits;
