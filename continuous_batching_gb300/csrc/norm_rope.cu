@@ -187,7 +187,10 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeParams
         if constexpr (C == kQ4 && !INTER && K != kQ) {
             const int half = p.n_pairs / 4;
             const auto from = [&](int i) { return i < half ? i : i < 2 * half ? i - half : l; };
-            const auto in_a = [&](int i) { return ((from(i) & 1) != 0) == (i < half ? false : i < 2 * half ? true : (i & 1) != 0); };
+            const auto in_a = [&](int i) {
+                const bool second = i < half ? false : i < 2 * half ? true : (i & 1) != 0;
+                return ((from(i) & 1) != 0) == second;
+            };
             a_second = !in_a(2 * l);
             from_a = from(2 * l + a_second);
             from_b = from(2 * l + !a_second);

@@ -578,7 +578,8 @@ __device__ __forceinline__ void q4_softmax(Rows<D, NT>& R, float (&x)[NT][2][4],
             for (int b = 0; b < 2; ++b) {
                 const uint32_t hi = pack_bf16(x[j][h][2 * b], x[j][h][2 * b + 1]);
                 float u, v;
-                f2_split(fma2(f2(scale_of(hi), min_of(hi)), f2(-1.f, -1.f), f2(x[j][h][2 * b], x[j][h][2 * b + 1])), u, v);
+                const uint64_t both = f2(x[j][h][2 * b], x[j][h][2 * b + 1]);
+                f2_split(fma2(f2(scale_of(hi), min_of(hi)), f2(-1.f, -1.f), both), u, v);
                 p[j][h][b] = transpose8(hi);
                 rest[j][h][b] = transpose8(pack_bf16(u, v));
             }
@@ -595,7 +596,8 @@ __device__ __forceinline__ void q4_values(uint32_t stage, Rows<D, NT>& R, const 
     const int r = lane >> 2, cc = lane & 3;
     // Keys 2 c, 2 c + 1 and those 8 behind them. Of eight keys the even ones lie before the odd ones, and (D = 128) of
     // four such rows the first halves before the second, so that what half a warp reads is contiguous.
-    const uint32_t row = stage + L::kCodes + 16 * h * kQ4Codes<D> + cc * 32 + (D == 128 ? (r >> 2) * 128 + (r & 3) * 8 : r * 4);
+    const uint32_t row = stage + L::kCodes + 16 * h * kQ4Codes<D> + cc * 32 +
+                         (D == 128 ? (r >> 2) * 128 + (r & 3) * 8 : r * 4);
     const uint32_t par = stage + 2 * L::kCodes + L::kParams + (16 * h + 2 * cc) * kQ4Params<D>;
     uint32_t v[4][G / 2], zp[4];
 #pragma unroll
@@ -853,7 +855,8 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
             for (int j = 0; j < NT; ++j) {
                 float4* const to = handed + j * (2 * G + 2) * 32;
 #pragma unroll
-                for (int t = 0; t < 2 * G; ++t) to[32 * t] = make_float4(R.o[j][t][0], R.o[j][t][1], R.o[j][t][2], R.o[j][t][3]);
+                for (int t = 0; t < 2 * G; ++t)
+                    to[32 * t] = make_float4(R.o[j][t][0], R.o[j][t][1], R.o[j][t][2], R.o[j][t][3]);
                 float l0, l1;
                 f2_split(R.l[j], l0, l1);
                 to[32 * 2 * G] = make_float4(l0, l1, R.nm[j][0], R.nm[j][1]);
@@ -924,7 +927,8 @@ __global__ void __launch_bounds__(32 * kWarps<NT>, 1) q4_direct_kernel(const Dir
             if (r == 0 && !whole) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<float2*>(part + kCols * D + 2 * (8 * j + 2 * cc + e)) = make_float2(-R.nm[j][e], l[e]);
+                    *reinterpret_cast<float2*>(part + kCols * D + 2 * (8 * j + 2 * cc + e)) =
+                        make_float2(-R.nm[j][e], l[e]);
             }
         }
         __syncwarp();                                       // the ring is free again
@@ -980,7 +984,8 @@ __global__ void __launch_bounds__(32 * kFoldWarps) q4_fold_kernel(const DirectPa
     // lane i has (m, l) of the eight's split i; those behind the last weigh nothing
     const auto load = [&](int s0, float (&a)[kEight][kLane], float2& ml) {
         ml = make_float2(-kNone, 0.f);
-        if (s0 + lane < n_splits && lane < kEight) ml = *reinterpret_cast<const float2*>(stat + int64_t(s0 + lane) * kPart);
+        if (s0 + lane < n_splits && lane < kEight)
+            ml = *reinterpret_cast<const float2*>(stat + int64_t(s0 + lane) * kPart);
 #pragma unroll
         for (int i = 0; i < kEight; ++i) {
             if (s0 + i >= n_splits) continue;
@@ -1051,7 +1056,8 @@ int32_t launch_direct(const DirectParams& p, const int32_t* fold, int32_t n_fold
     auto cfg = dependent_launch(&pdl, dim3(PA_PLAN_CTAS), 32 * kWarps<NT>, smem, stream);
     st = note_cuda(cudaLaunchKernelEx(&cfg, q4_direct_kernel<D, NT>, p));
     if (st || n_fold == 0) return st;
-    cfg = dependent_launch(&pdl, dim3(unsigned(n_fold), unsigned((fold_rows + kFoldWarps - 1) / kFoldWarps)), 32 * kFoldWarps, 0, stream);
+    const dim3 grid{unsigned(n_fold), unsigned((fold_rows + kFoldWarps - 1) / kFoldWarps)};
+    cfg = dependent_launch(&pdl, grid, 32 * kFoldWarps, 0, stream);
     return note_cuda(cudaLaunchKernelEx(&cfg, q4_fold_kernel<D, NT>, p, fold));
 }
 

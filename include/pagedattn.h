@@ -736,7 +736,8 @@ int32_t paged_kv_read_q4(const int32_t* slot_mapping, int32_t T, const void* k_p
  * pa_plan_step_q4 and copied to the device by the caller. direct_rows parts the sequences: one whose
  * n_q * group is at most direct_rows has its rows computed from the codes as they are (tiles of up to 8 rows
  * where direct_rows <= 8, else 16); the context of any other is expanded to bf16 once, 128-token block by
- * block, in the workspace, and its rows go through the kernel of paged_attention_step. pa_q4_direct_rows gives a fast choice. */
+ * block, in the workspace, and its rows go through the kernel of paged_attention_step.
+ * pa_q4_direct_rows gives a fast choice. */
 typedef struct pa_q4_plan {
     int32_t B, T, max_ctx;      /* sequences, query rows, bound of every context */
     int32_t direct_rows;
@@ -784,7 +785,8 @@ size_t pa_q4_workspace_bytes(const pa_shape* shape, const pa_q4_plan* plan);
  * Device: words, the plan's; q, out [T, Hq, D] bf16; block_table [B, max_blocks], cu_seqlens_q, ctx_lens
  * as planned (items that they contradict are skipped and set PA_DEVERR_META, their rows not written);
  * keys of a block outside the pool read as 0 and set PA_DEVERR_BLOCK; workspace 16-byte aligned.
- * Host checks: as paged_attention_step. Launches (programmatic dependents of what precedes them): the expansion,
+ * Host checks: as paged_attention_step; a pool of 64 GB or more is PA_ERR_SHAPE. Launches (programmatic
+ * dependents of what precedes them): the expansion,
  * the attention over it and its combine; the rows read from the codes, the join of their splits; each only
  * where the plan has sizes for it. */
 int32_t paged_attention_step_q4(const void* q, const void* k_pool, const void* v_pool,
