@@ -11,7 +11,6 @@ from __future__ import annotations
 
 import array
 import ctypes as C
-import itertools
 import operator
 import os
 import threading
@@ -575,7 +574,7 @@ class _Runtime:
         self.lib = load()
         self.bf16, self.u8, self.i32 = torch.bfloat16, torch.uint8, torch.int32
         self.i64, self.f32 = torch.int64, torch.float32
-        self.Tensor, self.nbytes = torch.Tensor, operator.attrgetter("nbytes")
+        self.Tensor, self.shape = torch.Tensor, operator.attrgetter("shape")
         self.device = torch.cuda.current_device
         # the raw handle of the current stream, without a Stream object around it
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -1005,7 +1004,8 @@ def paged_copy_pages(pairs, pools, err=None, stream=None) -> None:
     n, m = pairs.shape[0], len(pools)
     # one pass of a method over all pools at a time: a fork's few pages take less than a loop over them would
     T = rt.Tensor
-    blocks = set(map(T.size, pools, itertools.repeat(0))) or {0}
+    shapes = set(map(rt.shape, pools))
+    blocks = {x[0] for x in shapes} or {0}
     if len(blocks) > 1 or not all(map(T.is_contiguous, pools)) or set(map(T.get_device, pools)) - {dev}:
         raise ValueError(f"pools: expected contiguous tensors of the same number of blocks on the current "
                          f"CUDA device ({dev})")
@@ -1013,9 +1013,11 @@ def paged_copy_pages(pairs, pools, err=None, stream=None) -> None:
     words = array.array("q", bytes(16 * max(m, 1)))
     if m:
         words[0::2] = array.array("q", map(T.data_ptr, pools))
-        per, sizes = max(blocks, 1), list(map(rt.nbytes, pools))
-        same = min(sizes) == max(sizes)
-        words[1::2] = array.array("q", [sizes[0] // per]) * m if same else array.array("q", [x // per for x in sizes])
+        per = max(blocks, 1)
+        if len(shapes) == 1 and len(set(map(T.element_size, pools))) == 1:
+            words[1::2] = array.array("q", [pools[0].nbytes // per]) * m
+        else:
+            words[1::2] = array.array("q", [x.nbytes // per for x in pools])
     a = (Pages * max(m, 1)).from_buffer(words)
     _check(rt.lib.paged_copy_pages(_arg(pairs, rt.i32, dev, (n, 2), "pairs"), n, a, m, blocks,
                                    None if err is None else _arg(err, rt.i32, dev, (1,), "err"),
