@@ -941,7 +941,7 @@ def pa_plan_step_q4(shape: Shape, cu_seqlens_q: np.ndarray, ctx_lens: np.ndarray
     lib = load()
     cu, ctx = _i32(cu_seqlens_q), _i32(ctx_lens)
     B = len(ctx)
-    if B and len(cu) != B + 1:
+    if len(cu) != B + 1:
         raise ValueError(f"cu_seqlens_q: expected {B + 1} entries, got {len(cu)}")
     if limits is not None:
         sizes = limits

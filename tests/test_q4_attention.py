@@ -198,6 +198,18 @@ def test_plan_refuses():
         bd.pa_plan_step_q4(shape, cu, ctx, limits=s)
 
 
+@pytest.mark.parametrize("cu, ctx", [([0], []), ([0, 0], [0]), ([0, 0, 0], [5, 900])])
+def test_plans_of_no_rows(cu, ctx):
+    shape = bd.Shape.make(8, 2, 128, 16, 64)
+    cu, ctx = np.array(cu, np.int32), np.array(ctx, np.int32)
+    plan = bd.pa_plan_step_q4(shape, cu, ctx)
+    assert plan.sizes.words == 0 and bd.pa_q4_workspace_bytes(shape, plan) == 0
+    limits = bd.pa_q4_plan_limits(shape, len(ctx), 0, 900, 8, 0)
+    assert bd.pa_plan_step_q4(shape, cu, ctx, limits=limits).sizes.T == 0
+    with pytest.raises(ValueError):
+        bd.pa_plan_step_q4(shape, cu[1:], ctx)
+
+
 def test_step_refuses():
     lib, shape = bd.load(), bd.Shape.make(8, 2, 128, 16, 64)
     sizes = bd.pa_plan_step_q4(shape, np.array([0, 1], np.int32), np.array([700], np.int32), 8).sizes
