@@ -854,7 +854,7 @@ int32_t pa_q4_plan_limits(const pa_shape* shape, int32_t B, int32_t T, int32_t m
         if (heads * splits > (int64_t(1) << 26)) return PA_ERR_SHAPE;
         p.n_direct = int32_t(heads * splits);
         p.n_fold = splits > 1 ? int32_t(heads) : 0;
-        p.fold_rows = splits > 1 ? int32_t(std::min<int64_t>(tokens, direct_rows / g) * g) : 0;
+        p.fold_rows = p.n_fold > 0 ? int32_t(std::min<int64_t>(tokens, direct_rows / g) * g) : 0;
     }
     if (max_expand > 0 && T > 0 && max_ctx > 0) {
         if (max_expand > INT32_MAX / 128) return PA_ERR_SHAPE;
