@@ -24,7 +24,9 @@
 //
 // Measured: 16,384 tokens of 32 + 2 x 8 heads of 128 (403 MB) in 75 us, 5.4 TB/s, 79 % of the measured
 // copy rate; replayed in a graph, one token 2.5 us, 128 tokens of 64 + 2 x 8 heads 3.4 us, 2,096
-// tokens into an fp8 pool (47 MB) 14.3 us.
+// tokens into an fp8 pool (47 MB) 14.3 us; 8,192 tokens of 32 + 2 x 8 heads into 4-bit pools (178 MB) 44.7 us, 4.0 TB/s
+// (bf16 pools, 201 MB, 40.7), bound by the latency of a head's load, norm and exchange: 1, 3 or 4 heads in flight 50
+// to 51 us, 3 or 5 CTAs a multiprocessor 57 and 53.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
