@@ -5,7 +5,7 @@
 // kChunk bytes of one page of one pool at a time, all of its loads in flight before its first store, so an SM
 // has about 128 KB on the way; consecutive warps take consecutive chunks of a page. Bound by memory: each byte
 // is read and written once (701 pages of 32 KB in 16 pools: 109.9 us, 6.7 TB/s, 98 % of a copy's rate; 6 in 64 pools 3.9 us
-// in a graph, and 32 as a call of the Python binding, which looks at 64 tensors).
+// in a graph, and 32 to 35 as a call of the Python binding, which looks at 64 tensors).
 #include <cuda_runtime.h>
 
 #include <algorithm>
