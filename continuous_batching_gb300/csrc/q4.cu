@@ -151,7 +151,8 @@ struct ExpandParams {
 // The values are those of paged_kv_read_q4. Bound by memory (512 bytes a token and head written, 160 read): 21,900
 // tokens of 8 heads take 14 us ahead of the attention that reads them.
 // The sequences whose context is expanded whole are told to the attention by ex_ctx; the others (rows that
-// are read directly, metadata that the plan was not made for) have a context of 0 there.
+// are read directly, metadata that the plan was not made for, a context that the block table does not cover) have a
+// context of 0 there, by which the attention refuses their items.
 template <int D>
 __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
     constexpr int G = D / kQ4Group, kGroups = 256 / 4;          // rows at a time
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
         const int c = p.ctx[s];
         const int64_t blocks = (int64_t(c) + 127) / 128;
         const bool whole = n_q * p.g > p.direct_rows && c > 0 && blocks <= p.cols &&
-                           p.ex_table[s * p.cols + blocks - 1] >= 0;
+                           (int64_t(c) + bs - 1) / bs <= p.max_blocks && p.ex_table[s * p.cols + blocks - 1] >= 0;
         p.ex_ctx[s] = whole ? c : 0;
     }
     const int seq = p.list[2 * blockIdx.x], first = p.list[2 * blockIdx.x + 1];

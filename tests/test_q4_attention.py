@@ -667,3 +667,16 @@ def test_runner_refuses():
         bd.StepRunner(bd.Shape.make(8, 2, 128, 16, 4), device="cpu", kv_bits=8)
     with pytest.raises(ValueError):
         bd.StepRunner(bd.Shape.make(8, 2, 128, 16, 4), device="cpu", kv_bits=4, kv_scales=(1.0, 1.0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("direct_rows", [0, 8])
+def test_a_table_too_narrow_for_a_chunk(direct_rows):
+    """A chunk, and with direct_rows 0 a single row, whose context the block table does not cover: its rows are not
+    written (the workspace holds nothing of that context), the others are as they were."""
+    c = Case([(1, 600), (40, 700), (2, 300), (1, 2500)], seed=73)
+    clean = c.run(direct_rows)
+    got = c.run(direct_rows, table=c.table[:, :40].copy(), expect=bd.PA_DEVERR_META)
+    nine = wl.f32_to_bf16_bits(np.float32(9))
+    assert (got[1:41] == nine).all() and (got[43] == nine).all()
+    assert np.array_equal(got[[0, 41, 42]], clean[[0, 41, 42]])
