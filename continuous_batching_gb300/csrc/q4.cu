@@ -366,10 +366,10 @@ __device__ __forceinline__ uint32_t fma_bf16(uint32_t a, uint32_t b, uint32_t c)
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
-// NaN and infinities become large numbers, numbers stay.
+// NaN and infinities become the largest numbers, numbers stay.
 __device__ __forceinline__ uint32_t finite_bf16(uint32_t a) {
-    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(0xFF00FF00u));
-    asm("min.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(0x7F007F00u));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(0xFF7FFF7Fu));
+    asm("min.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(0x7F7F7F7Fu));
     return a;
 }
 

@@ -779,7 +779,10 @@ size_t pa_q4_workspace_bytes(const pa_shape* shape, const pa_q4_plan* plan);
  * rounds it (against 64 bits an output is off by 0.0032 of its size where the other way leaves 0.0024 and its
  * own rounding to bf16 alone 0.0017), otherwise as that step (a NaN or infinity among the
  * V of a later key of the chunk reaches the rows before it, as there; not so for rows read from the
- * codes). A row's bits depend on its own query, keys, position and context, and on which of the two ways its
+ * codes). Either way, as in paged_attention_step, p is relative to a reference that a score may pass by 8 in base 2, and
+ * the sum of p is divided out at the end: where p |V| summed over the keys passes fp32 (values of 2^120 and more with
+ * one key of that p, or smaller ones with more), an output may overflow.
+ * A row's bits depend on its own query, keys, position and context, and on which of the two ways its
  * sequence takes: with direct_rows 0 every row takes the second, and a token has the same bits as a
  * single row and within a chunk.
  * Device: words, the plan's; q, out [T, Hq, D] bf16; block_table [B, max_blocks], cu_seqlens_q, ctx_lens

@@ -680,3 +680,28 @@ def test_a_table_too_narrow_for_a_chunk(direct_rows):
     nine = wl.f32_to_bf16_bits(np.float32(9))
     assert (got[1:41] == nine).all() and (got[43] == nine).all()
     assert np.array_equal(got[[0, 41, 42]], clean[[0, 41, 42]])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("direct_rows", [0, 16])
+def test_the_largest_values(direct_rows):
+    """Values up to the largest bf16 number, where one key has all of a row's weight: the middle of their group
+    (minimum + 8 scale) enters as it is, also in tiles that hold later keys, unwritten ones and NaN."""
+    c = Case([(1, 1), (3, 3), (1, 40)], seed=79)
+    k, v = np.zeros((44, 2, 128), np.uint16), np.zeros((44, 2, 128), np.uint16)
+    ramp = wl.f32_to_bf16_bits(np.linspace(2.0, 3.3, 128, dtype=np.float32) * np.float32(1e38))
+    v[0, 0], v[0, 1] = 0x7F7F, 0xFF7F                     # constant groups: scale 0
+    v[1] = ramp                                           # all that the first of three rows sees
+    if direct_rows:
+        v[3] = 0x7FC0                                     # the last row's
+    at = 4 + 35
+    v[at] = ramp
+    k[at] = wl.f32_to_bf16_bits(np.float32(4))            # a score 181 above the others'
+    c.q = wl.f32_to_bf16_bits(np.full((5, 8, 128), 4, np.float32))
+    slots = [int(c.table[s, p // 16]) * 16 + p % 16 for s, n in ((0, 1), (1, 3), (2, 40)) for p in range(n)]
+    c.pools = [q4.write(p, x, slots, 16, i == 1) for i, (p, x) in enumerate(zip(c.pools, (k, v)))]
+    got = pa.bf16_to_f64(c.run(direct_rows))[[0, 1, 4]]
+    want = np.repeat(q4.values(c.pools[1], 16, 128, True).astype(np.float64).reshape(-1, 2, 128)[slots][[0, 1, at]], 4, 1)
+    # Roundings to bf16, 2^-8 of what is rounded each: the output's and the middle's (s (u - 8) has p = 1 and is exact);
+    # the middle is at most 1.1 of the value. Expanded, the value's alone.
+    assert (np.abs(got - want) <= (2.1 * 2.0 ** -8 + 2.0 ** -15) * np.abs(want)).all()
