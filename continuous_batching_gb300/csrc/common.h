@@ -27,6 +27,9 @@ __host__ __device__ constexpr int64_t q4_split_keys(int32_t ctx) {
 }
 // The longest context of one split.
 constexpr int64_t q4_one_split() { return 512; }
+// The longest context: the keys that a warp looks up ahead of a split's, up to 3,000 behind its first, are counted
+// in 32 bits.
+constexpr int32_t kQ4MaxCtx = INT32_MAX - 4096;
 // Most splits of any context up to max_ctx.
 inline int64_t q4_max_splits(int64_t max_ctx) {
     const auto n = [](int64_t c) { return c <= 0 ? 1 : (c + q4_split_keys(int32_t(c)) - 1) / q4_split_keys(int32_t(c)); };

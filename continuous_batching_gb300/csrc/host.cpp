@@ -790,6 +790,7 @@ int32_t pa_detail::check_q4_plan(const pa_shape* shape, const pa_q4_plan& p) {
     if (p.B < 0 || p.T < 0 || p.max_ctx < 0 || p.direct_rows < 0 || p.n_direct < 0 || p.n_fold < 0 ||
         p.n_chunk < 0 || p.n_expand < 0 || p.expand_cols < 0)
         return PA_ERR_INVALID;
+    if (p.max_ctx > kQ4MaxCtx) return PA_ERR_SHAPE;
     if (p.n_direct > 0 && p.direct_rows < g) return PA_ERR_INVALID;
     if (p.n_fold > p.n_direct || p.fold_rows < 0 || p.fold_rows > q4_tile_rows(p.direct_rows) ||
         (p.n_fold > 0) != (p.fold_rows > 0) || (p.n_chunk > 0) != (p.n_expand > 0) ||
@@ -816,6 +817,8 @@ int32_t pa_q4_plan_size(const pa_shape* shape, int32_t B, const int32_t* cu, con
     if (st) return st;
     if ((st = check_step_meta(B, cu, ctx))) return st;
     if (!plan || direct_rows < 0) return PA_ERR_INVALID;
+    for (int32_t s = 0; s < B; ++s)
+        if (ctx[s] > kQ4MaxCtx) return PA_ERR_SHAPE;
     Q4Parts parts;
     if ((st = q4_parts(shape, B, cu, ctx, direct_rows, parts))) return st;
     pa_q4_plan p{};
@@ -840,6 +843,7 @@ int32_t pa_q4_plan_limits(const pa_shape* shape, int32_t B, int32_t T, int32_t m
     int32_t st = check_shape(shape);
     if (st) return st;
     if (!plan || B < 0 || T < 0 || max_ctx < 0 || direct_rows < 0 || max_expand < 0) return PA_ERR_INVALID;
+    if (max_ctx > kQ4MaxCtx) return PA_ERR_SHAPE;
     pa_q4_plan p{};
     p.B = B;
     p.T = T;

@@ -788,8 +788,8 @@ size_t pa_q4_workspace_bytes(const pa_shape* shape, const pa_q4_plan* plan);
  * Device: words, the plan's; q, out [T, Hq, D] bf16; block_table [B, max_blocks], cu_seqlens_q, ctx_lens
  * as planned (items that they contradict are skipped and set PA_DEVERR_META, their rows not written);
  * keys of a block outside the pool read as 0 and set PA_DEVERR_BLOCK; workspace 16-byte aligned.
- * Host checks: as paged_attention_step; a pool of 64 GB or more is PA_ERR_SHAPE. Launches (programmatic
- * dependents of what precedes them): the expansion,
+ * Host checks: as paged_attention_step; a pool of 64 GB or more is PA_ERR_SHAPE, and contexts of 2^31 - 4096 and more
+ * are, here and in the calls that make a plan. Launches (programmatic dependents of what precedes them): the expansion,
  * the attention over it and its combine; the rows read from the codes, the join of their splits; each only
  * where the plan has sizes for it. */
 int32_t paged_attention_step_q4(const void* q, const void* k_pool, const void* v_pool,

@@ -210,6 +210,28 @@ def test_plans_of_no_rows(cu, ctx):
         bd.pa_plan_step_q4(shape, cu[1:], ctx)
 
 
+def test_contexts_near_the_end_of_32_bits_are_refused():
+    shape, most = bd.Shape.make(8, 2, 128, 128, 64), 2 ** 31 - 1 - 4096
+    cu = np.array([0, 1], np.int32)
+    for ctx, rows in ((most + 1, 8), (2 ** 31 - 1, 8), (2 ** 31 - 1, 0)):
+        with pytest.raises(bd.PagedAttnError) as e:
+            bd.pa_plan_step_q4(shape, cu, np.array([ctx], np.int32), rows)
+        assert e.value.status == bd.PA_ERR_SHAPE
+        with pytest.raises(bd.PagedAttnError) as e:
+            bd.pa_q4_plan_limits(shape, 1, 1, ctx, rows)
+        assert e.value.status == bd.PA_ERR_SHAPE
+    sizes = bd.pa_plan_step_q4(shape, cu, np.array([most], np.int32), 8).sizes
+    assert sizes.n_direct == 2 * -(-most // 2048) and bd.pa_q4_plan_limits(shape, 1, 1, most, 8).n_direct >= sizes.n_direct
+    # the largest key that q4_direct_kernel looks up: of the eight tiles, of a pair's 64 keys, after the last eight of a split
+    assert most - 1 + (2 * (-(-2048 // 64) + 14) + 1) * 32 + 24 < 2 ** 31
+    # sizes that no call gave
+    sizes.max_ctx = most + 1
+    lib = bd.load()
+    assert lib.paged_attention_step_q4(4096, 4096, 4096, 4096, 1 << 24, 4096, 4096, C.byref(sizes), 4096, 4096, 1 << 40, 4096, C.byref(shape), None, None) == bd.PA_ERR_SHAPE
+    with pytest.raises(bd.PagedAttnError):
+        bd.pa_plan_step_q4(shape, cu, np.array([most], np.int32), limits=sizes)
+
+
 def test_step_refuses():
     lib, shape = bd.load(), bd.Shape.make(8, 2, 128, 16, 64)
     sizes = bd.pa_plan_step_q4(shape, np.array([0, 1], np.int32), np.array([700], np.int32), 8).sizes
