@@ -1028,10 +1028,18 @@ class StepLimits:
     """Fixed sizes of a step that is captured in a CUDA graph: B sequences, T query rows,
     block-table width max_blocks and a context bound max_ctx. Every step prepared under these
     limits reuses the same device buffers and launches the same kernels with the same
-    arguments, so a graph captured once replays any of them."""
+    arguments, so a graph captured once replays any of them.
 
-    def __init__(self, B: int, T: int, max_blocks: int, max_ctx: int):
+    max_chunks is for runners over 4-bit pools (the others need no such bound): the most sequences of a
+    step that bring more rows than are read from the codes, whose contexts are expanded in the workspace.
+    None: as many as T rows can be. With 0 a step launches no expansion and no attention over it. (64 sequences,
+    contexts up to 16,384, 32 / 8 heads of 128: the workspace takes 34 MB with 0 and 67 MB more for each.)"""
+
+    def __init__(self, B: int, T: int, max_blocks: int, max_ctx: int, max_chunks: Optional[int] = None):
         self.B, self.T, self.max_blocks, self.max_ctx = int(B), int(T), int(max_blocks), int(max_ctx)
+        self.max_chunks = None if max_chunks is None else int(max_chunks)
+        if max_chunks is not None and self.max_chunks < 0:
+            raise ValueError("max_chunks: at least 0")
 
 
 class StepRunner:
@@ -1071,8 +1079,12 @@ class StepRunner:
             d = self.device
             if self.q4:
                 rows = pa_q4_direct_rows(shape) if direct_rows is None else int(direct_rows)
-                # chunks: sequences of more rows than that
-                chunks = min(L.B, L.T // (rows // (shape.num_q_heads // shape.num_kv_heads) + 1))
+                # chunks: sequences of more tokens than that
+                self._few = rows // (shape.num_q_heads // shape.num_kv_heads)
+                chunks = min(L.B, L.T // (self._few + 1))
+                if L.max_chunks is not None:
+                    chunks = min(chunks, L.max_chunks)
+                self.max_chunks = chunks
                 self.q4_sizes = pa_q4_plan_limits(shape, L.B, L.T, L.max_ctx, rows,
                                                   chunks * (-(-L.max_ctx // 128)))
                 n_words = max(self.q4_sizes.words, 1)
@@ -1144,7 +1156,8 @@ class StepRunner:
         B = len(ctx)
         T = int(cu[-1]) if B else 0
         if B != L.B or T != L.T or table.ndim != 2 or table.shape[0] != B or \
-                table.shape[1] > L.max_blocks or (B and int(ctx.max()) > L.max_ctx):
+                table.shape[1] > L.max_blocks or (B and int(ctx.max()) > L.max_ctx) or \
+                (self.q4 and int(np.count_nonzero(np.diff(cu) > self._few)) > self.max_chunks):
             raise ValueError("step exceeds the limits the runner was built for")
         if self._uploaded is not None:
             self._uploaded.synchronize()                  # the pinned array is free again

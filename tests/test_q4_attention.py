@@ -254,6 +254,41 @@ def test_step_refuses():
     assert call(sz=bad) == bd.PA_ERR_INVALID
 
 
+def test_runner_limits_without_chunks():
+    """A runner that only decodes has no room for chunks, in its plan and its workspace; one for a chunk has that
+    chunk's. Contexts of 16,384 and 64 sequences, 32 / 8 heads of 128."""
+    shape = bd.Shape.make(32, 8, 128, 16, 64)
+    runner = lambda T, chunks, rows=None: bd.StepRunner(shape, device="cpu", kv_bits=4, direct_rows=rows,
+                                                        limits=bd.StepLimits(64, T, 1024, 16384, max_chunks=chunks))
+    r = runner(64, 0)
+    assert r.q4_sizes.n_chunk == r.q4_sizes.n_expand == 0
+    # the splits' parts alone: of every row and head, at most 16 splits of 1,024 keys, tiles of 8 rows of 130 numbers
+    assert r.ws.numel() * 4 <= 64 * 8 * 16 * 8 * 130 * 4 + 256
+    table = np.full((64, 1), -1, np.int32)
+    slots = np.full(64, -1, np.int32)
+    ctx = np.full(64, 9000, np.int32)
+    r.prepare(np.arange(65, dtype=np.int32), ctx, table, slots)
+    # the bytes of an expanded context of 16,384: K and V in bf16
+    one = 2 * 16384 * 8 * 128 * 2
+    chunky = runner(576, 1)
+    assert chunky.q4_sizes.n_expand == 128 and chunky.ws.numel() * 4 <= one + 576 * 8 * 16 * 16 * 130 * 4 + 1024
+    n = np.ones(64, np.int32)
+    n[7] = 513
+    cu = lambda n: np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    chunky.prepare(cu(n), ctx, table, np.full(576, -1, np.int32))
+    n[7], n[9] = 257, 257
+    with pytest.raises(ValueError):
+        chunky.prepare(cu(n), ctx, table, np.full(576, -1, np.int32))
+    n = np.ones(64, np.int32)
+    n[:15], n[20] = 0, 16
+    with pytest.raises(ValueError):
+        r.prepare(cu(n), ctx, table, slots)
+    runner(64, None).prepare(cu(n), ctx, table, slots)
+    runner(64, 1).prepare(cu(n), ctx, table, slots)
+    with pytest.raises(ValueError):
+        bd.StepLimits(64, 64, 1024, 16384, max_chunks=-1)
+
+
 # ------------------------------------------------------------------------------------- GPU
 
 SHAPES = [(8, 8, 128, 16), (8, 4, 64, 8), (8, 2, 128, 32), (16, 2, 128, 128), (8, 1, 64, 64), (32, 2, 128, 16), (16, 1, 64, 16)]
