@@ -936,8 +936,8 @@ def pa_plan_step_q4(shape: Shape, cu_seqlens_q: np.ndarray, ctx_lens: np.ndarray
                     direct_rows: Optional[int] = None, limits: Optional[Q4Sizes] = None,
                     device=None) -> Q4Plan:
     """The plan of one 4-bit step: of exactly its sizes, or padded to `limits`. direct_rows: sequences
-    of up to so many query rows (tokens times heads of a group) are read from the codes (None: what is
-    fast; 0: none, so that single rows and chunks get the same bits)."""
+    of up to so many query rows (tokens times heads of a group) are read from the codes (None: up to
+    pa_q4_max_direct_rows; 0: none, so that single rows and chunks get the same bits)."""
     lib = load()
     cu, ctx = _i32(cu_seqlens_q), _i32(ctx_lens)
     B = len(ctx)
@@ -1054,8 +1054,8 @@ class StepRunner:
     asynchronous copy on the current stream; the next prepare() first waits for that copy.
     With kv_scales = (k_scale, v_scale) the pools are uint8 float8_e4m3fn caches and the fp8
     write and read entry points run instead; with kv_bits = 4 they are 4-bit pools (pa_q4_pool_shape)
-    and the q4 ones do, sequences of up to direct_rows rows read from the codes (see pa_plan_step_q4; None:
-    what is fast, with limits for single tokens).
+    and the q4 ones do, sequences of up to direct_rows rows read from the codes (None: up to
+    pa_q4_max_direct_rows, with limits and without, so that a captured step gives an eager one's bits).
     """
 
     def __init__(self, shape: Shape, device="cuda", limits: Optional[StepLimits] = None,
@@ -1078,7 +1078,7 @@ class StepRunner:
             L = limits
             d = self.device
             if self.q4:
-                rows = pa_q4_direct_rows(shape) if direct_rows is None else int(direct_rows)
+                rows = int(load().pa_q4_max_direct_rows() if direct_rows is None else direct_rows)
                 # chunks: sequences of more tokens than that
                 self._few = rows // (shape.num_q_heads // shape.num_kv_heads)
                 chunks = min(L.B, L.T // (self._few + 1))

@@ -39,6 +39,15 @@ inline int64_t q4_max_splits(int64_t max_ctx) {
     return most;
 }
 
+// Rows of a tile read from the codes, 8 or 16, by the plan's sizes. A row's bits do not depend on it. 16 where sequences
+// bring several tokens, so that they share a tile; 8 where a tile would mostly hold one token's rows: where there are
+// no more rows than sequences, and where the step's chunks account for the rest. (32 / 8 heads of 128, contexts of
+// 1,000 to 8,000, caches cold, tiles of 8 / 16 rows: 64 single tokens 91 / 138 us; 32, a prompt's last 5 and a chunk of
+// 512 108 / 136; 32 times 4 drafted tokens and a chunk 136 / 127; 64 / 8 heads, 32 times 2 tokens 261 / 95.)
+inline int32_t q4_tile_rows(int32_t g, const pa_q4_plan& p) {
+    return p.direct_rows > 8 && (g > 8 || (p.T > p.B && p.n_chunk == 0)) ? 16 : 8;
+}
+
 // Where the parts of a plan's words begin (see pa_q4_plan).
 struct Q4Words {
     int64_t direct, lists, fold, chunk, expand, table, total;

@@ -711,12 +711,10 @@ struct Q4Parts {
     int32_t tiles_folded = 0, fold_rows = 0;
 };
 
-int32_t q4_tile_rows(int32_t direct_rows) { return direct_rows > 8 ? 16 : 8; }
-
 int32_t q4_parts(const pa_shape* shape, int32_t B, const int32_t* cu, const int32_t* ctx,
-                 int32_t direct_rows, Q4Parts& out) {
+                 int32_t direct_rows, int32_t tile_rows, Q4Parts& out) {
     const int32_t g = shape->num_q_heads / shape->num_kv_heads;
-    const int32_t tokens = q4_tile_rows(direct_rows) / g;       // of a tile read from the codes
+    const int32_t tokens = tile_rows / g;                       // of a tile read from the codes
     for (int32_t s = 0; s < B; ++s) {
         const int32_t n = cu[s + 1] - cu[s];
         if (n == 0) continue;
@@ -792,7 +790,7 @@ int32_t pa_detail::check_q4_plan(const pa_shape* shape, const pa_q4_plan& p) {
         return PA_ERR_INVALID;
     if (p.max_ctx > kQ4MaxCtx) return PA_ERR_SHAPE;
     if (p.n_direct > 0 && p.direct_rows < g) return PA_ERR_INVALID;
-    if (p.n_fold > p.n_direct || p.fold_rows < 0 || p.fold_rows > q4_tile_rows(p.direct_rows) ||
+    if (p.n_fold > p.n_direct || p.fold_rows < 0 || p.fold_rows > q4_tile_rows(g, p) ||
         (p.n_fold > 0) != (p.fold_rows > 0) || (p.n_chunk > 0) != (p.n_expand > 0) ||
         (p.n_chunk > 0 && p.expand_cols == 0))
         return PA_ERR_INVALID;
@@ -819,13 +817,17 @@ int32_t pa_q4_plan_size(const pa_shape* shape, int32_t B, const int32_t* cu, con
     if (!plan || direct_rows < 0) return PA_ERR_INVALID;
     for (int32_t s = 0; s < B; ++s)
         if (ctx[s] > kQ4MaxCtx) return PA_ERR_SHAPE;
-    Q4Parts parts;
-    if ((st = q4_parts(shape, B, cu, ctx, direct_rows, parts))) return st;
+    const int32_t g = shape->num_q_heads / shape->num_kv_heads;
     pa_q4_plan p{};
     p.B = B;
     p.T = B > 0 ? cu[B] : 0;
-    for (int32_t s = 0; s < B; ++s) p.max_ctx = std::max(p.max_ctx, ctx[s]);
     p.direct_rows = direct_rows;
+    for (int32_t s = 0; s < B; ++s) {
+        p.max_ctx = std::max(p.max_ctx, ctx[s]);
+        if (int64_t(cu[s + 1] - cu[s]) * g > direct_rows) p.n_chunk = 1;    // (the number comes below)
+    }
+    Q4Parts parts;
+    if ((st = q4_parts(shape, B, cu, ctx, direct_rows, q4_tile_rows(g, p), parts))) return st;
     p.n_direct = int32_t(parts.direct.size());
     p.n_fold = parts.tiles_folded * shape->num_kv_heads;
     p.fold_rows = parts.fold_rows;
@@ -850,7 +852,8 @@ int32_t pa_q4_plan_limits(const pa_shape* shape, int32_t B, int32_t T, int32_t m
     p.max_ctx = max_ctx;
     p.direct_rows = direct_rows;
     const int32_t g = shape->num_q_heads / shape->num_kv_heads;
-    const int64_t tokens = q4_tile_rows(direct_rows) / g;
+    p.n_chunk = max_expand > 0 && T > 0 && max_ctx > 0 ? 1 : 0;             // (the number comes below)
+    const int64_t tokens = q4_tile_rows(g, p) / g;
     if (direct_rows >= g && tokens > 0) {
         const int64_t per_seq = (direct_rows / g + tokens - 1) / tokens;
         const int64_t tiles = std::min<int64_t>(T, B * per_seq);
@@ -860,7 +863,7 @@ int32_t pa_q4_plan_limits(const pa_shape* shape, int32_t B, int32_t T, int32_t m
         p.n_fold = splits > 1 ? int32_t(heads) : 0;
         p.fold_rows = p.n_fold > 0 ? int32_t(std::min<int64_t>(tokens, direct_rows / g) * g) : 0;
     }
-    if (max_expand > 0 && T > 0 && max_ctx > 0) {
+    if (p.n_chunk > 0) {
         if (max_expand > INT32_MAX / 128) return PA_ERR_SHAPE;
         const int64_t items = pa_plan_max_items(shape, B, T, max_ctx);
         if (items > (int64_t(1) << 26)) return PA_ERR_SHAPE;
@@ -886,7 +889,8 @@ int32_t pa_plan_step_q4(const pa_shape* shape, int32_t B, const int32_t* cu, con
     for (int32_t s = 0; s < B; ++s)
         if (ctx[s] > plan->max_ctx) return PA_ERR_INVALID;
     Q4Parts parts;
-    if ((st = q4_parts(shape, B, cu, ctx, plan->direct_rows, parts))) return st;
+    const int32_t g = shape->num_q_heads / shape->num_kv_heads;
+    if ((st = q4_parts(shape, B, cu, ctx, plan->direct_rows, q4_tile_rows(g, *plan), parts))) return st;
     if (int64_t(parts.direct.size()) > plan->n_direct || int64_t(parts.chunk.size()) > plan->n_chunk ||
         int64_t(parts.list.size() / 2) > plan->n_expand ||
         int64_t(parts.tiles_folded) * shape->num_kv_heads > plan->n_fold || parts.fold_rows > plan->fold_rows)

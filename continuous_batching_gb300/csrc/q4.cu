@@ -1109,7 +1109,7 @@ Space space_of(const pa_shape* s, const pa_q4_plan* p) {
     const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     Space w{};
     const int D = s->head_dim, g = s->num_q_heads / s->num_kv_heads;
-    const int cols = p->direct_rows > 8 ? 16 : 8;
+    const int cols = q4_tile_rows(g, *p);
     if (p->n_fold > 0) w.parts = up(size_t(p->n_direct) * cols * (D + 2) * 4);
     if (p->n_chunk > 0) {
         // single tokens are among the expanded rows only where a group is larger than direct_rows
@@ -1256,7 +1256,7 @@ extern "C" int32_t paged_attention_step_q4(const void* q, const void* k_pool, co
     p.c = float(1.4426950408889634 / std::sqrt(double(D)));
     p.bits = 0x43004300u;
     const int32_t* fold = words + f.fold;
-    const bool wide = P.direct_rows > 8;
+    const bool wide = q4_tile_rows(g, P) > 8;
     return D == 128 ? (wide ? launch_direct<128, 2>(p, fold, P.n_fold, P.fold_rows, stream)
                             : launch_direct<128, 1>(p, fold, P.n_fold, P.fold_rows, stream))
                     : (wide ? launch_direct<64, 2>(p, fold, P.n_fold, P.fold_rows, stream)

@@ -762,3 +762,80 @@ def test_the_largest_values(direct_rows):
     # Roundings to bf16, 2^-8 of what is rounded each: the output's and the middle's (s (u - 8) has p = 1 and is exact);
     # the middle is at most 1.1 of the value. Expanded, the value's alone.
     assert (np.abs(got - want) <= (2.1 * 2.0 ** -8 + 2.0 ** -15) * np.abs(want)).all()
+
+
+def test_tiles_of_eight_and_sixteen_rows():
+    """What decides the tiles' rows: direct_rows, the group, rows beyond one a sequence, chunks; every plan with the
+    same tokens covered."""
+    def tiles(n_q, Hq, Hkv, rows, ctx=900, limits=None):
+        shape = bd.Shape.make(Hq, Hkv, 128, 16, 4)
+        cu = np.concatenate([[0], np.cumsum(n_q)]).astype(np.int32)
+        if limits is not None:
+            limits = bd.pa_q4_plan_limits(shape, len(n_q), int(cu[-1]), 1000, rows, limits)
+        plan = bd.pa_plan_step_q4(shape, cu, np.full(len(n_q), ctx, np.int32), rows if limits is None else None, limits)
+        it = _items(plan.words, 0, plan.sizes.n_direct)
+        it = it[it["n_q"] > 0]
+        few = [t for s, n in enumerate(n_q) if n * (Hq // Hkv) <= rows for t in range(cu[s], cu[s + 1])]
+        seen = sorted(t for i in it[(it["split"] == 0) & (it["kv_head"] == 0)] for t in range(i["q_start"], i["q_start"] + i["n_q"]))
+        assert seen == few
+        return int(it["n_q"].max()) * (Hq // Hkv)
+
+    for limits in (None, 0):
+        assert tiles([4, 4, 1], 8, 2, 48, limits=limits) == 16 and tiles([4, 1], 8, 2, 16, limits=limits) == 16
+        assert tiles([4, 0, 0, 0], 8, 2, 48, limits=limits) == 8                   # no more rows than sequences
+        assert tiles([1, 1], 32, 2, 48, limits=limits) == 16                       # groups of 16
+        assert tiles([2, 2], 8, 2, 8, limits=limits) == 8
+    for limits in (None, 100):
+        assert tiles([4, 40], 8, 2, 48, limits=limits) == 8                        # a chunk beside them
+        assert tiles([3, 40], 32, 2, 48, limits=limits) == 16
+    assert tiles([4, 4, 1], 8, 2, 48, limits=100) == 8                             # room for chunks
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("max_chunks", [None, 3])
+def test_a_captured_runner_gives_the_eager_ones_bits(max_chunks):
+    """Write and step of a runner with limits, captured once, replayed for steps whose chunks, few tokens and single
+    tokens change places, and for the first one again: the pools' bytes and the outputs' bits of a runner without."""
+    lens = [[(1, 500), (12, 33), (46, 260), (1, 700)], [(46, 300), (1, 501), (1, 53), (12, 261)], [(20, 20), (13, 700), (26, 26), (1, 90)],
+            [(9, 90), (4, 300), (46, 46), (1, 1)]]
+    cases = [Case(l, seed=83 + i) for i, l in enumerate(lens)]
+    shape = bd.Shape.make(8, 2, 128, 16, max(c.nb for c in cases))
+    eager = bd.StepRunner(shape, kv_bits=4)
+    fixed = bd.StepRunner(shape, kv_bits=4, limits=bd.StepLimits(4, 60, 50, 800, max_chunks=max_chunks))
+    pool = lambda: torch.zeros(bd.pa_q4_pool_shape(shape), dtype=torch.uint8, device="cuda")
+    sides = [[torch.zeros(60, 8, 128, dtype=torch.bfloat16, device="cuda"), *(torch.zeros(60, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in "kv"),
+              pool(), pool(), torch.zeros(60, 8, 128, dtype=torch.bfloat16, device="cuda")] for _ in "ab"]
+    for turn, i in enumerate((0, 1, 2, 3, 0)):
+        c, rng = cases[i], np.random.default_rng(i)
+        new = [bf16(wl.random_bf16(rng, (60, 2, 128))) for _ in "kv"]
+        for q, kn, vn, k, v, out in sides:
+            q.copy_(bf16(c.q)), kn.copy_(new[0]), vn.copy_(new[1]), out.zero_()
+            for p, x in ((k, c.pools[0]), (v, c.pools[1])):
+                p.fill_(255)
+                p[:c.nb].copy_(dev(x))
+        for runner in (eager, fixed):
+            runner.prepare(c.cu, c.ctx, c.table)
+        eager.run(*sides[0])
+        if turn == 0:
+            q, kn, vn, k, v, out = sides[1]
+            fixed.capture(q, kn, vn, k, v, out, write=True)
+            out.zero_()
+        fixed.replay()
+        torch.cuda.synchronize()
+        assert eager.device_error() == fixed.device_error() == 0
+        for a, b in zip(sides[0][3:], sides[1][3:]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), turn
+
+
+@pytest.mark.gpu
+def test_bits_do_not_depend_on_the_tiles():
+    """Sequences of several tokens in tiles of 16 rows and, with a chunk beside them, of 8."""
+    lens = [(4, 700), (12, 33), (7, 2500), (1, 5000), (3, 514), (12, 6150)]
+    a = Case(lens, seed=89)
+    b = Case(lens + [(40, 600)], seed=89)
+    b.q[:a.T] = a.q
+    for s, (_, x) in enumerate(lens):
+        n = -(-x // 16)
+        for to, src in zip(b.pools, a.pools):
+            to[b.table[s, :n]] = src[a.table[s, :n]]
+    assert np.array_equal(a.run(48), b.run(48)[:a.T])
