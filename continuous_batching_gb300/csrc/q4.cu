@@ -144,7 +144,7 @@ struct ExpandParams {
     int32_t* queue;                     // of the rows read from the codes (see DirectParams): back to 0
     __nv_bfloat16 *k_out, *v_out;       // [n][128][Hkv][D]
     int32_t* err;
-    int32_t n, B, cols, max_blocks, num_blocks, Hkv, g, log2bs, direct_rows;
+    int32_t B, cols, max_blocks, num_blocks, Hkv, g, log2bs, direct_rows;
 };
 
 // CTA (i, h): block i of the plan's list, head h: 128 tokens of K and V to bf16, one rounding each.
@@ -1205,7 +1205,6 @@ extern "C" int32_t paged_attention_step_q4(const void* q, const void* k_pool, co
         e.ex_ctx = reinterpret_cast<int32_t*>(at + w.parts + w.partials + 2 * w.expanded);
         e.queue = queue = e.ex_ctx + P.B;
         e.err = err_flag;
-        e.n = P.n_expand;
         e.B = P.B;
         e.cols = P.expand_cols;
         e.max_blocks = max_blocks;
