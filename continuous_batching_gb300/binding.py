@@ -945,6 +945,8 @@ def pa_plan_step_q4(shape: Shape, cu_seqlens_q: np.ndarray, ctx_lens: np.ndarray
         raise ValueError(f"cu_seqlens_q: expected {B + 1} entries, got {len(cu)}")
     if limits is not None:
         sizes = limits
+        if direct_rows not in (None, sizes.direct_rows):
+            raise ValueError(f"direct_rows: the limits are for {sizes.direct_rows}, got {direct_rows}")
     else:
         if direct_rows is None:
             g = shape.num_q_heads // max(shape.num_kv_heads, 1)
@@ -1064,6 +1066,8 @@ class StepRunner:
         import torch
         if kv_bits not in (None, 4) or (kv_bits is not None and kv_scales is not None):
             raise ValueError("kv_bits: 4, without kv_scales")
+        if direct_rows is not None and kv_bits != 4:
+            raise ValueError("direct_rows: with kv_bits=4")
         self.torch = torch
         self.shape = shape
         self.q4 = kv_bits == 4

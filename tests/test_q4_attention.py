@@ -839,3 +839,16 @@ def test_bits_do_not_depend_on_the_tiles():
         for to, src in zip(b.pools, a.pools):
             to[b.table[s, :n]] = src[a.table[s, :n]]
     assert np.array_equal(a.run(48), b.run(48)[:a.T])
+
+
+def test_arguments_that_would_have_no_effect_are_refused():
+    shape = bd.Shape.make(8, 2, 128, 16, 4)
+    with pytest.raises(ValueError):
+        bd.StepRunner(shape, device="cpu", direct_rows=8)
+    with pytest.raises(ValueError):
+        bd.StepRunner(shape, device="cpu", direct_rows=8, kv_scales=(1.0, 1.0))
+    cu, ctx = np.array([0, 1], np.int32), np.array([7], np.int32)
+    limits = bd.pa_q4_plan_limits(shape, 1, 1, 100, 8)
+    with pytest.raises(ValueError):
+        bd.pa_plan_step_q4(shape, cu, ctx, 16, limits)
+    assert bd.pa_plan_step_q4(shape, cu, ctx, 8, limits).sizes.direct_rows == 8
