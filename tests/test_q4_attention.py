@@ -852,3 +852,51 @@ def test_arguments_that_would_have_no_effect_are_refused():
     with pytest.raises(ValueError):
         bd.pa_plan_step_q4(shape, cu, ctx, 16, limits)
     assert bd.pa_plan_step_q4(shape, cu, ctx, 8, limits).sizes.direct_rows == 8
+
+
+def _held(pool, bs, D, is_v):
+    """A pool's codes [nb, bs, Hkv, D], and every column's scale and minimum."""
+    nb, H, _ = pool.shape
+    c = pool[:, :, :bs * (D // 2)].reshape(nb, H, bs, D // 2)
+    u = np.stack([c & 15, c >> 4], -1).reshape(nb, H, bs, D)[..., q4.column_nibble(D, is_v)]
+    p = np.ascontiguousarray(pool[:, :, bs * (D // 2):]).view("<u2").reshape(nb, H, bs, D // 32, 2)
+    return [x.transpose(0, 2, 1, 3).astype(np.float64) for x in (u, *(np.repeat(pa.bf16_to_f64(p[..., i]), 32, -1) for i in (0, 1)))]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D, Hq, Hkv", [(128, 8, 2), (64, 16, 2)])
+def test_roundings_of_rows_read_from_the_codes(D, Hq, Hkv):
+    """What the roundings add up to, and how far a score may be off.
+
+    The error against 64 bits is a sum of independent roundings: of the output, of every p scale, of every middle.
+    These are made here, in 64 bits otherwise; were p itself rounded to one bf16 as well, its roundings would come
+    on top. The kernel has to be nearer to the first than to the second (its p is relative to another reference,
+    which changes the roundings but not their size).
+    Per value, an output is off by at most 2^-8 of itself and the roundings' 2^-8 + 2^-15 of p (|s (u - 8)| + |m + 8 s|),
+    as in Case.bound, and by what fp32 does to its scores: a group's 32 products, q (u 2^-24) in fp32, are two sums
+    of 16 and an accumulator, the minima's product three parts of four groups, and a tensor core may cut each of
+    a sum's 17 addends at 2^-23 of the largest: 2 * 17 * 2^-23 < 2^-17 of sum |q| 15 s, and 2^-18 of sum |q| |m| for its 13
+    addends; the products with the scales and their sum over the groups are 2^-24 each of these, 8 of them: 2^-21."""
+    c = Case([(1, 1500), (1, 900), (2, 700), (1, 2100)], Hq, Hkv, D, 16, seed=97)
+    (ku, ks, km), (vu, vs, vm) = (_held(p, 16, D, i == 1) for i, p in enumerate(c.pools))
+    exact, q, g = c.exact(), pa.bf16_to_f64(c.q), Hq // Hkv
+    got = pa.bf16_to_f64(c.run(16))
+    near = lambda x: pa.bf16_to_f64(wl.f32_to_bf16_bits(np.asarray(x, np.float32)))
+    two, one, most = (np.empty_like(exact) for _ in range(3))
+    for s, (n, x) in enumerate(c.lens):
+        block = c.table[s, np.arange(x) // 16]
+        at = lambda a: a[block, np.arange(x) % 16]
+        for i in range(n):
+            t, seen = c.cu[s] + i, x - n + i + 1
+            for h in range(Hq):
+                U, S, M, u, sc, m = (at(a)[:seen, h // g] for a in (ku, ks, km, vu, vs, vm))
+                a = (S * U + M) @ q[t, h] / np.sqrt(D)
+                p = np.exp(a - a.max())
+                for to, r in ((two, p), (one, near(p))):
+                    to[t, h] = near((near(r[:, None] * sc) * (u - 8) + r[:, None] * near(m + 8 * sc)).sum(0) / r.sum())
+                e = ((2.0 ** -17 + 2.0 ** -21) * (15 * S @ np.abs(q[t, h])) + (2.0 ** -18 + 2.0 ** -21) * (np.abs(M) @ np.abs(q[t, h]))).max() / np.sqrt(D)
+                big = (p[:, None] * (np.abs(sc * (u - 8)) + np.abs(m + 8 * sc))).sum(0) / p.sum()
+                most[t, h] = np.abs(exact[t, h]) * 2.0 ** -8 + (2.0 ** -8 + 2.0 ** -15 + 2.0 ** -18 + 2 * np.expm1(2 * e)) * big
+    off = [np.sqrt(((y - exact) ** 2).sum() / (exact ** 2).sum()) for y in (got, two, one)]
+    assert off[1] < off[2] and off[0] < np.sqrt(off[1] * off[2]), off
+    assert (np.abs(got - exact) <= most).all(), float((np.abs(got - exact) / most).max())
