@@ -43,6 +43,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -129,13 +130,14 @@ enum Bar {
 };
 constexpr int kHolderOff = 8 * kNumBars;          // TMEM address written by tcgen05.alloc
 constexpr int kAbortOff = kHolderOff + 4;
+constexpr int kTypeOff = kAbortOff + 4;           // + 4 x tile parity: the tile's P and V are f16 (V16)
 constexpr int kRingOff = 512;                     // 4 item slots of 64 bytes
 constexpr int kTableOff = 768;                    // per loader warp: the item's table entries
 constexpr int kTableKeys = 1024;                  // keys whose table entries a loader holds
 constexpr int kTableTiles = kTableKeys / kTileKeys;
 constexpr int kMaxTableEntries = kTableKeys / 8;  // at the smallest block size, 8 tokens
 static_assert(kSplit % kTableKeys == 0, "a split starts a table window");
-static_assert(kAbortOff + 4 <= kRingOff, "control area");
+static_assert(kTypeOff + 8 <= kRingOff, "control area");
 
 struct Params {
     const __nv_bfloat16* k_pool;
@@ -156,6 +158,7 @@ struct Params {
     float* lse;         // [T][Hq]: log-sum-exp of every row, natural logarithm
     float* scores;      // [B][Hq][scores_ld] raw scores of the decode rows, or NULL
     int64_t scores_ld;
+    const uint8_t* v16; // [num_blocks][Hkv], 16-byte aligned: V of this 128-key block and head is f16 (1) or bf16 (0) (V16)
     unsigned long long never_ns;   // nonzero only in the wait-timeout test: the softmax warps
                                    // first wait this long on kNever, which nothing completes
 };
@@ -360,16 +363,19 @@ __device__ __forceinline__ void rows_init(Rows2& R, int r0, int rs, int rows_val
     }
 }
 
+// The type that P is rounded to, that of V: bf16, f16 (an fp8 cache), or what the tile's V has (V16).
+enum PType { kPBf16, kPF16, kPEither };
+
 // Online softmax step of one 128-key tile (keys kb .. kb + 127) for the thread's first NR rows
 // (sr = 0 .. NR-1), taken in lockstep so that the two rows' dependency chains interleave: the
-// rows' state is updated, their P, rounded to bf16, goes to pk (packed column 4 cc + q4 of row
+// rows' state is updated, their P, rounded, goes to pk (packed column 4 cc + q4 of row
 // sr is pk[2 cc + sr]) and alpha[sr] is the factor the row's O must be scaled by. The
 // arithmetic of a row depends on its own scores only.
 // With STATS the raw scores (masked ones -infinity) of the rows whose sc is not NULL are stored
 // there: what a later kernel needs to turn them into weights once the row's sum is known.
-template <int NR, bool H16, bool STATS>
+template <int NR, int P16, bool STATS>
 __device__ __forceinline__ void softmax_rows(const uint32_t (&r)[64], uint32_t (&pk)[32], int q4,
-                                             int kb, float c, Rows2& R, float alpha[2],
+                                             int kb, float c, bool half, Rows2& R, float alpha[2],
                                              float* const (&sc)[2]) {
     float sv[NR][32];
     float mx[NR];
@@ -476,35 +482,42 @@ __device__ __forceinline__ void softmax_rows(const uint32_t (&r)[64], uint32_t (
         alpha[sr] = a[sr];
     }
     // keys 8cc + 2q4 + {0, 1} -> packed column 4cc + q4 (16x128b layout)
+    if (P16 == kPF16 || (P16 == kPEither && half)) {
 #pragma unroll
-    for (int cc = 0; cc < 16; ++cc)
+        for (int cc = 0; cc < 16; ++cc)
 #pragma unroll
-        for (int sr = 0; sr < NR; ++sr)
-            pk[2 * cc + sr] = H16 ? pack_f16(sv[sr][2 * cc], sv[sr][2 * cc + 1])
-                                  : pack_bf16(sv[sr][2 * cc], sv[sr][2 * cc + 1]);
+            for (int sr = 0; sr < NR; ++sr)
+                pk[2 * cc + sr] = pack_f16(sv[sr][2 * cc], sv[sr][2 * cc + 1]);
+    } else {
+#pragma unroll
+        for (int cc = 0; cc < 16; ++cc)
+#pragma unroll
+            for (int sr = 0; sr < NR; ++sr)
+                pk[2 * cc + sr] = pack_bf16(sv[sr][2 * cc], sv[sr][2 * cc + 1]);
+    }
 }
 
 // Online softmax of one 128-key tile for the half at TMEM address tm_s (lane offset
-// included): S is read, the rows' state is updated and P, rounded to bf16, is stored over the
-// first 64 columns (as f16 when H16, the operand type of an fp8 cache's MMAs, else bf16).
+// included): S is read, the rows' state is updated and P, rounded to the type P16 (half: that of a tile
+// that may have either is f16), is stored over the first 64 columns.
 // alpha[sr] is the factor the row's O must be scaled by. A second 8-row block with no valid
 // row (the tail of a decode or of a ragged tile) needs no softmax: its P is never used for a
 // written output.
-template <bool H16, bool STATS>
+template <int P16, bool STATS>
 __device__ __forceinline__ void softmax_half(uint32_t tm_s, int r0, int q4, int rows_valid,
-                                             int kb, float c, Rows2& R, float alpha[2],
+                                             int kb, float c, bool half, Rows2& R, float alpha[2],
                                              float* const (&sc)[2]) {
     uint32_t r[64];
     tmem_ld_16x256b_x16(tm_s, r);
     tmem_wait_ld();
-    uint32_t pk[32];                 // P rounded to bf16, packed in pairs
+    uint32_t pk[32];                 // P rounded, packed in pairs
     if (r0 + 8 >= rows_valid) {
-        softmax_rows<1, H16, STATS>(r, pk, q4, kb, c, R, alpha, sc);
+        softmax_rows<1, P16, STATS>(r, pk, q4, kb, c, half, R, alpha, sc);
         alpha[1] = 1.f;
 #pragma unroll
         for (int cc = 0; cc < 16; ++cc) pk[2 * cc + 1] = 0u;
     } else {
-        softmax_rows<2, H16, STATS>(r, pk, q4, kb, c, R, alpha, sc);
+        softmax_rows<2, P16, STATS>(r, pk, q4, kb, c, half, R, alpha, sc);
     }
     // P replaces S in the first 64 columns of this tile's S buffer
     tmem_st_16x128b_x16(tm_s, pk);
@@ -729,7 +742,12 @@ __device__ __forceinline__ void zero_v_tail(uint32_t vb, int kb, int ctx, int bs
 // STATS: the rows' log-sum-exps and, for decode rows, their raw scores are stored as well (an
 // instantiation of its own, so that the plain step's registers and time stay what they are: 32 decode
 // rows at 4k .. 16k keys 230 us, with log-sum-exps 231, with 44 MB of scores some 7 more).
-template <int D, bool F8, bool STATS>
+// V16: the contexts are those of a 4-bit cache expanded for this step, blocks of 128 keys, K in bf16 and V in f16
+// where f16 holds it, else in bf16 (p.v16 says which); a tile's P has the type of its V. Beside bf16 for all, two of an output's
+// four roundings have 11 bits in place of 8: against 64 bits 0.0032 -> 0.0023 of its size. Every CTA first sees whether all
+// of the step's blocks are f16, as they mostly are: the MMA warp then has a loop without a choice (four 512-row chunks: 195 us; with
+// the type of each tile looked up there 203, bf16 for all 193).
+template <int D, bool F8, bool STATS, bool V16>
 __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v,
@@ -784,6 +802,19 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     // launched as a programmatic dependent: nothing written by the previous kernel on the
     // stream (the KV write, or whatever produced q) is read before this point
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool all16 = false;
+    if constexpr (V16) {
+        static_assert(kTileKeys == 128, "a tile is a block of the expanded contexts");
+        const int64_t n = int64_t(p.num_blocks) * p.Hkv;
+        uint32_t mine = 0x01010101u;
+#pragma unroll 4
+        for (int64_t i = 16 * int64_t(threadIdx.x); i < n / 16 * 16; i += 16 * kThreadsFor<F8>) {
+            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p.v16 + i));
+            mine &= v.x & v.y & v.z & v.w;
+        }
+        if (threadIdx.x < n % 16 && !__ldcg(p.v16 + n / 16 * 16 + threadIdx.x)) mine = 0;
+        all16 = __syncthreads_and(mine == 0x01010101u);
+    }
 
     if (warp == 8) {
         // ------------------------------------------------------------ producer
@@ -902,7 +933,7 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
         if (lane == 0) {
             const uint32_t leader = 1u;
             constexpr uint32_t idesc_s = make_idesc(kRows, kTileKeys, false, F8);
-            constexpr uint32_t idesc_o = make_idesc(kRows, D, true, F8);
+            constexpr uint32_t idesc_o = make_idesc(kRows, D, true, F8 || V16);
             static_assert(L::kQHalf == L::kKVHalf, "Q and K chunks share the step offsets");
             // This warp shares its scheduler with two softmax warps, and tcgen05.mma issue
             // takes about as long as the tensor work, so every instruction of this loop costs
@@ -935,9 +966,9 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 }
             }
             static_assert(kTileKeys / 16 == 8, "eight PV steps per tile");
-            const auto issue_pv = [&](uint64_t vdesc, uint32_t p_tmem, uint32_t d, bool acc) {
+            const auto issue_pv = [&](uint64_t vdesc, uint32_t p_tmem, uint32_t d, bool acc, uint32_t idesc) {
                 // P of keys 16k .. 16k+15 is 8 packed columns of the S buffer
-                issue_pv_group(leader, d, p_tmem, vdesc, idesc_o, acc ? 1u : 0u, v_off);
+                issue_pv_group(leader, d, p_tmem, vdesc, idesc, acc ? 1u : 0u, v_off);
             };
             // Two cursors walk the same item sequence: one issues S = Q K^T for the next tile
             // as soon as its K has landed (and its S buffer is free), the other issues O += P V
@@ -983,58 +1014,74 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
             Cursor cv{0, 0, 0, 0, 0, 0, false, false, Item{}};
             unsigned idle = 0;
             unsigned long long idle_since = 0;
-            while (!(cs.done && cv.done)) {
-                bool progress = false;
-                fetch(cv);
-                fetch(cs);
-                // O += P V for the oldest tile whose P is ready (P published implies that V
-                // has landed; the first tile of a split starts its O buffer once the epilogue
-                // has released it)
-                // (a RESUME item's first tile continues its split: it accumulates onto the
-                // restored O)
-                const bool cont = ((cv.I.tile0 + cv.jt) & (kSplitTiles - 1)) != 0;
-                if (cv.have && cv.tc < cs.tc &&
-                    mbar_test_wait(bar(kPFull + (cv.tc & 1)), (cv.tc >> 1) & 1) &&
-                    (cont || cv.sg < 2 ||
-                     mbar_test_wait(bar(kOFree + (cv.sg & 1)), ((cv.sg >> 1) - 1) & 1))) {
-                    tc_fence_after();
-                    issue_pv(vd0 + uint32_t(cv.vs) * kBufStep, tmem + (cv.tc & 1) * 128,
-                             tmem + kTmemO + (cv.sg & 1) * 128, cont);
-                    tc_commit_if(leader, bar(kPVDone + cv.vs));
-                    advance(cv);
-                    progress = true;
-                }
-                // S = Q K^T for the next tile: its S buffer last held the P of tile cs.tc - 2,
-                // which must have been read by that tile's PV (finished, not just issued);
-                // that PV's barrier is V slot (tc - 2) % SV, phase ((tc - 2) / SV) & 1
-                const int ks = cs.tc & (SK - 1);
-                const int pv2 = cs.vs >= 2 ? cs.vs - 2 : cs.vs - 2 + SV;
-                const int pv2ph = cs.vs >= 2 ? cs.vph : cs.vph ^ 1;
-                if (cs.have && cs.tc <= cv.tc + 1 &&
-                    (cs.tc < 2 || mbar_test_wait(bar(kPVDone + pv2), pv2ph)) &&
-                    (cs.jt > 0 || mbar_test_wait(bar(kQUse + (cs.ic & 1)), (cs.ic >> 1) & 1)) &&
-                    mbar_test_wait(bar(kKUse + ks), (cs.tc >> kLog2SK) & 1)) {
-                    tc_fence_after();
-                    issue_s(qd0 + uint32_t(cs.ic & 1) * kBufStep, kd0 + uint32_t(ks) * kBufStep,
-                            tmem + (cs.tc & 1) * 128);
-                    tc_commit_if(leader, bar(kSFull + ks));
-                    tc_commit_if(leader && cs.jt == cs.I.n_tiles - 1, bar(kQEmpty + (cs.ic & 1)));
-                    advance(cs);
-                    progress = true;
-                }
-                // the clock is read every 64 idle polls only
-                if (progress) {
-                    idle = 0;
-                } else if ((++idle & 63) == 0) {
-                    if (*abort_word) break;
-                    const unsigned long long now = global_ns();
-                    if (idle == 64) {
-                        idle_since = now;
-                    } else if (now - idle_since > kWaitLimitNs) {
-                        *abort_word = 1;
-                        break;
+            // one_type: every PV has the operand type of idesc_o (V16: f16)
+            const auto run = [&](auto one_type) {
+                while (!(cs.done && cv.done)) {
+                    bool progress = false;
+                    fetch(cv);
+                    fetch(cs);
+                    // O += P V for the oldest tile whose P is ready (P published implies that V
+                    // has landed; the first tile of a split starts its O buffer once the epilogue
+                    // has released it)
+                    // (a RESUME item's first tile continues its split: it accumulates onto the
+                    // restored O)
+                    const bool cont = ((cv.I.tile0 + cv.jt) & (kSplitTiles - 1)) != 0;
+                    if (cv.have && cv.tc < cs.tc &&
+                        mbar_test_wait(bar(kPFull + (cv.tc & 1)), (cv.tc >> 1) & 1) &&
+                        (cont || cv.sg < 2 ||
+                         mbar_test_wait(bar(kOFree + (cv.sg & 1)), ((cv.sg >> 1) - 1) & 1))) {
+                        tc_fence_after();
+                        uint32_t idesc = idesc_o;
+                        if constexpr (!decltype(one_type)::value) {
+                            // (the softmax publishes the word with P, and writes it again once S of the tile after the next
+                            // has finished, which is issued behind this product)
+                            if (!*reinterpret_cast<volatile int*>(smem + L::kBar + kTypeOff + 4 * (cv.tc & 1)))
+                                idesc = make_idesc(kRows, D, true, false);
+                        }
+                        issue_pv(vd0 + uint32_t(cv.vs) * kBufStep, tmem + (cv.tc & 1) * 128,
+                                 tmem + kTmemO + (cv.sg & 1) * 128, cont, idesc);
+                        tc_commit_if(leader, bar(kPVDone + cv.vs));
+                        advance(cv);
+                        progress = true;
+                    }
+                    // S = Q K^T for the next tile: its S buffer last held the P of tile cs.tc - 2,
+                    // which must have been read by that tile's PV (finished, not just issued);
+                    // that PV's barrier is V slot (tc - 2) % SV, phase ((tc - 2) / SV) & 1
+                    const int ks = cs.tc & (SK - 1);
+                    const int pv2 = cs.vs >= 2 ? cs.vs - 2 : cs.vs - 2 + SV;
+                    const int pv2ph = cs.vs >= 2 ? cs.vph : cs.vph ^ 1;
+                    if (cs.have && cs.tc <= cv.tc + 1 &&
+                        (cs.tc < 2 || mbar_test_wait(bar(kPVDone + pv2), pv2ph)) &&
+                        (cs.jt > 0 || mbar_test_wait(bar(kQUse + (cs.ic & 1)), (cs.ic >> 1) & 1)) &&
+                        mbar_test_wait(bar(kKUse + ks), (cs.tc >> kLog2SK) & 1)) {
+                        tc_fence_after();
+                        issue_s(qd0 + uint32_t(cs.ic & 1) * kBufStep, kd0 + uint32_t(ks) * kBufStep,
+                                tmem + (cs.tc & 1) * 128);
+                        tc_commit_if(leader, bar(kSFull + ks));
+                        tc_commit_if(leader && cs.jt == cs.I.n_tiles - 1, bar(kQEmpty + (cs.ic & 1)));
+                        advance(cs);
+                        progress = true;
+                    }
+                    // the clock is read every 64 idle polls only
+                    if (progress) {
+                        idle = 0;
+                    } else if ((++idle & 63) == 0) {
+                        if (*abort_word) break;
+                        const unsigned long long now = global_ns();
+                        if (idle == 64) {
+                            idle_since = now;
+                        } else if (now - idle_since > kWaitLimitNs) {
+                            *abort_word = 1;
+                            break;
+                        }
                     }
                 }
+            };
+            if constexpr (V16) {
+                if (all16) run(std::true_type());
+                else run(std::false_type());
+            } else {
+                run(std::true_type());
             }
             // drain: every MMA lane 0 issued has finished before TMEM is released
             tc_commit_if(leader, bar(kDrain));
@@ -1265,9 +1312,18 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                     // a context that outgrew the caller's bound: behind the row's scores
                     if (kb + kTileKeys > p.scores_ld) sc[0] = sc[1] = nullptr;
                 }
+                bool half = F8;
+                if constexpr (V16) {
+                    half = all16;
+                    if (!all16) {
+                        const int block = p.block_table[int64_t(I.seq) * p.max_blocks + kb / kTileKeys];
+                        half = block >= 0 && block < p.num_blocks && __ldcg(p.v16 + int64_t(block) * p.Hkv + I.kvh);
+                        if (tid == 0) *reinterpret_cast<volatile int*>(smem + L::kBar + kTypeOff + 4 * (tc & 1)) = half;
+                    }
+                }
                 if (on)
-                    softmax_half<F8, STATS>(tmem + (tc & 1) * 128 + lanes, r0, q4, I.rows_valid, kb,
-                                            c, R, alpha, sc);
+                    softmax_half<F8 ? kPF16 : V16 ? kPEither : kPBf16, STATS>(
+                        tmem + (tc & 1) * 128 + lanes, r0, q4, I.rows_valid, kb, c, half, R, alpha, sc);
                 // O belongs to the previous tile's PV until it has finished: rescale only then,
                 // and only in warps where some row's running maximum moved
                 const bool need = alpha[0] != 1.f || alpha[1] != 1.f;
@@ -1490,25 +1546,25 @@ constexpr int kMaxDevices = 64;
 // Raises the kernel's dynamic shared-memory limit once per device. Several host threads (one
 // per GPU, say) may get here at once: the flags are atomic, and the attribute call is
 // idempotent, so two threads that both find a flag clear both set the same value.
-template <int D, bool F8, bool STATS>
+template <int D, bool F8, bool STATS, bool V16>
 int32_t ensure_smem_attr(int dev) {
     static std::atomic<bool> raised[kMaxDevices];     // zero-initialised: not raised yet
     if (dev < 0 || dev >= kMaxDevices) return PA_ERR_INVALID;
     if (raised[dev].load(std::memory_order_acquire)) return PA_OK;
     const int32_t st = note_cuda(cudaFuncSetAttribute(
-        paged_attn_kernel<D, F8, STATS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        paged_attn_kernel<D, F8, STATS, V16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
         Layout<D>::kAlloc));
     if (st) return st;
     raised[dev].store(true, std::memory_order_release);
     return PA_OK;
 }
 
-template <int D, bool F8, bool STATS = false>
+template <int D, bool F8, bool STATS = false, bool V16 = false>
 int32_t launch(const Maps& maps, const Params& prm, int32_t max_ctx, cudaStream_t stream) {
     int dev = 0;
     int32_t st = note_cuda(cudaGetDevice(&dev));
     if (st) return st;
-    if ((st = ensure_smem_attr<D, F8, STATS>(dev))) return st;
+    if ((st = ensure_smem_attr<D, F8, STATS, V16>(dev))) return st;
     const int grid = std::min(prm.n_items, PA_PLAN_CTAS);      // one CTA per list of the plan
     // Both kernels are programmatic dependents of what precedes them on the stream: each
     // launches while its predecessor drains and waits (griddepcontrol.wait) before it reads
@@ -1523,7 +1579,7 @@ int32_t launch(const Maps& maps, const Params& prm, int32_t max_ctx, cudaStream_
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    st = note_cuda(cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, F8, STATS>, maps.k, maps.v, maps.q1,
+    st = note_cuda(cudaLaunchKernelEx(&cfg, paged_attn_kernel<D, F8, STATS, V16>, maps.k, maps.v, maps.q1,
                                       maps.qn, prm));
     if (st) return st;
     if (max_ctx > kSplit) {
@@ -1582,6 +1638,7 @@ int32_t prepare_step(const void* q, const void* k_pool, const void* v_pool,
     prm->lse = nullptr;
     prm->scores = nullptr;
     prm->scores_ld = 0;
+    prm->v16 = nullptr;
     prm->never_ns = 0;
     return PA_OK;
 }
@@ -1728,7 +1785,7 @@ int32_t pa_detail::attention_step_stats(const void* q, const void* k_pool, const
 int32_t pa_detail::attention_step_expanded(const void* q, const void* k_pool, const void* v_pool,
                                            const int32_t* block_table, int32_t max_blocks,
                                            const int32_t* cu_seqlens_q, const int32_t* ctx_lens,
-                                           int32_t B, int32_t T, int32_t max_ctx,
+                                           int32_t B, int32_t T, int32_t max_ctx, const uint8_t* v16,
                                            const pa_work_item* items, int32_t n_items,
                                            void* partials, void* out, const pa_shape* shape,
                                            int32_t* err_flag, cudaStream_t stream) {
@@ -1739,8 +1796,9 @@ int32_t pa_detail::attention_step_expanded(const void* q, const void* k_pool, co
     if (st) return st;
     point_workspace(&prm, static_cast<float*>(partials), T, shape->num_q_heads, shape->head_dim);
     const int32_t combined = partials ? max_ctx : std::min(max_ctx, kSplit);
-    if (shape->head_dim == 128) return launch<128, false>(maps, prm, combined, stream);
-    return launch<64, false>(maps, prm, combined, stream);
+    prm.v16 = v16;
+    if (shape->head_dim == 128) return launch<128, false, false, true>(maps, prm, combined, stream);
+    return launch<64, false, false, true>(maps, prm, combined, stream);
 }
 
 extern "C" int32_t paged_attention_step_lse(const void* q, const void* k_pool, const void* v_pool,

@@ -84,13 +84,14 @@ int32_t attention_step_stats(const void* q, const void* k_pool, const void* v_po
                              float* scores, int64_t scores_ld, const pa_shape* shape,
                              int32_t* err_flag, cudaStream_t stream);
 
-// paged_attention_step over the contexts that a 4-bit step has expanded (attention.cu). partials: as the
-// workspace of paged_attention_step, or NULL where no single token is among the rows.
+// paged_attention_step over the contexts that a 4-bit step has expanded (attention.cu), blocks of 128 keys: K in bf16, V
+// in f16 where v16 [num_blocks][num_kv_heads] is 1, in bf16 where it is 0. partials: as the workspace of
+// paged_attention_step, or NULL where no single token is among the rows.
 int32_t attention_step_expanded(const void* q, const void* k_pool, const void* v_pool,
                                 const int32_t* block_table, int32_t max_blocks,
                                 const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t B,
-                                int32_t T, int32_t max_ctx, const pa_work_item* items,
-                                int32_t n_items, void* partials, void* out, const pa_shape* shape,
+                                int32_t T, int32_t max_ctx, const uint8_t* v16,
+                                const pa_work_item* items, int32_t n_items, void* partials, void* out, const pa_shape* shape,
                                 int32_t* err_flag, cudaStream_t stream);
 
 }  // namespace pa_detail

@@ -142,13 +142,16 @@ struct ExpandParams {
     const int32_t* ex_table;            // [B][cols]: place of every block in the expanded pools, -1
     int32_t* ex_ctx;                    // [B]: the context of the sequences that are expanded, else 0
     int32_t* queue;                     // of the rows read from the codes (see DirectParams): back to 0
-    __nv_bfloat16 *k_out, *v_out;       // [n][128][Hkv][D]
+    __nv_bfloat16 *k_out, *v_out;       // [n][128][Hkv][D]; V in f16 where v16 says so
+    uint8_t* v16;                       // [n][Hkv]
     int32_t* err;
     int32_t B, cols, max_blocks, num_blocks, Hkv, g, log2bs, direct_rows;
 };
 
-// CTA (i, h): block i of the plan's list, head h: 128 tokens of K and V to bf16, one rounding each.
-// The values are those of paged_kv_read_q4. Bound by memory (512 bytes a token and head written, 160 read): 21,900
+// CTA (i, h): block i of the plan's list, head h: 128 tokens of K to bf16, the values of paged_kv_read_q4, and of V to
+// f16, 3 bits more, where the block's largest |V| lies in 2^-12 .. 65,504 or is 0 (groups that are NaN aside), so that
+// what is too small for f16's bits is off by 2^-12 of the largest or less; else V is bf16, too.
+// Bound by memory (512 bytes a token and head written, 160 read): 21,900
 // tokens of 8 heads take 14 us ahead of the attention that reads them.
 // The sequences whose context is expanded whole are told to the attention by ex_ctx; the others (rows that
 // are read directly, metadata that the plan was not made for, a context that the block table does not cover) have a
@@ -169,36 +172,68 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
         p.ex_ctx[s] = whole ? c : 0;
     }
     const int seq = p.list[2 * blockIdx.x], first = p.list[2 * blockIdx.x + 1];
-    if (seq < 0) return;                                        // padding of the plan
     const int head = blockIdx.y;
+    uint8_t* const v16 = p.v16 + int64_t(blockIdx.x) * p.Hkv + head;
+    if (seq < 0) {                                              // padding of the plan
+        if (threadIdx.x == 0) *v16 = 1;
+        return;
+    }
     const int ctx = seq < p.B ? p.ctx[seq] : 0;
     if (seq >= p.B || first < 0 || int64_t(first) * 128 >= ctx ||
         (int64_t(ctx) + bs - 1) / bs > p.max_blocks) {
+        if (threadIdx.x == 0) *v16 = 1;
         if (threadIdx.x == 0 && p.err) atomicOr(p.err, PA_DEVERR_META);
         return;
     }
     const int c = threadIdx.x & 3;
     const int32_t* table = p.table + int64_t(seq) * p.max_blocks;
+    constexpr int kTimes = 128 / kGroups;
+    uint32_t kw[kTimes][G] = {}, kp[kTimes][G] = {}, vw[kTimes][G] = {}, vp[kTimes][G] = {};
+    const int tok = threadIdx.x / 4, key = first * 128 + tok;       // the first row's; key < ctx + 128
 #pragma unroll
-    for (int i = 0; i < 128 / kGroups; ++i) {
-        const int tok = i * kGroups + threadIdx.x / 4;
-        const int key = first * 128 + tok;                      // < ctx + 128
-        if (key >= ctx) break;
-        uint32_t kw[G] = {}, kp[G] = {}, vw[G] = {}, vp[G] = {};
-        const int32_t block = table[key >> p.log2bs];
+    for (int i = 0; i < kTimes; ++i) {
+        if (key + i * kGroups >= ctx) break;
+        const int32_t block = table[(key + i * kGroups) >> p.log2bs];
         if (block >= 0 && block < p.num_blocks) {
             const int64_t at = q4_base<D>(block, p.Hkv, head, bs);
-            q4_load_row<D>(p.k_pool, at, bs, key & (bs - 1), c, kw, kp);
-            q4_load_row<D>(p.v_pool, at, bs, key & (bs - 1), c, vw, vp);
+            q4_load_row<D>(p.v_pool, at, bs, (key + i * kGroups) & (bs - 1), c, vw[i], vp[i]);
+            q4_load_row<D>(p.k_pool, at, bs, (key + i * kGroups) & (bs - 1), c, kw[i], kp[i]);
         } else if (p.err) {
             atomicOr(p.err, PA_DEVERR_BLOCK);                   // its keys read as 0
         }
-        const int64_t to = ((int64_t(blockIdx.x) * 128 + tok) * p.Hkv + head) * D + 8 * c;
+    }
+    float big = 0.f;                                            // (fmaxf passes NaN over)
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i)
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            *reinterpret_cast<uint4*>(p.k_out + to + 32 * g) = q4_columns<D, false>(kw, kp, g);
-            *reinterpret_cast<uint4*>(p.v_out + to + 32 * g) = q4_columns<D, true>(vw, vp, g);
+            const float low = __uint_as_float(vp[i][g] & 0xFFFF0000u);
+            big = fmaxf(big, fmaxf(fabsf(low), fabsf(fmaf(15.f, __uint_as_float(vp[i][g] << 16), low))));
         }
+    // (no negative numbers: they order as whole ones do)
+    __shared__ uint32_t warp_big[256 / 32];
+    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+    if ((threadIdx.x & 31) == 0) warp_big[threadIdx.x >> 5] = most;
+    const auto out = [&](int i, int g) { return ((int64_t(blockIdx.x) * 128 + tok + i * kGroups) * p.Hkv + head) * D + 8 * c + 32 * g; };
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+        if (key + i * kGroups >= ctx) break;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            *reinterpret_cast<uint4*>(p.k_out + out(i, g)) = q4_columns<D, false>(kw[i], kp[i], g);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 256 / 32; ++w) big = fmaxf(big, __uint_as_float(warp_big[w]));
+    const bool half = big <= 65504.f && (big >= 0x1p-12f || big == 0.f);
+    if (threadIdx.x == 0) *v16 = half;
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+        if (key + i * kGroups >= ctx) break;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            *reinterpret_cast<uint4*>(p.v_out + out(i, g)) =
+                half ? q4_columns_f16<D>(vw[i], vp[i], g) : q4_columns<D, true>(vw[i], vp[i], g);
     }
 }
 
@@ -1102,7 +1137,8 @@ int32_t launch_rows(RowsParams& p, int32_t T, const int32_t* slots, void* k_pool
 
 // Parts of the workspace, each a multiple of 256 bytes.
 struct Space {
-    size_t parts, partials, expanded, ctx, total;   // sizes: split parts, decode partials, one pool, contexts and queue
+    // sizes: split parts, decode partials, one pool, contexts and queue, types of V
+    size_t parts, partials, expanded, ctx, types, total;
 };
 
 Space space_of(const pa_shape* s, const pa_q4_plan* p) {
@@ -1117,8 +1153,9 @@ Space space_of(const pa_shape* s, const pa_q4_plan* p) {
             w.partials = up(pa_workspace_bytes(s, p->T, p->max_ctx));
         w.expanded = up(size_t(p->n_expand) * 128 * s->num_kv_heads * D * 2);
         w.ctx = up((size_t(p->B) + 1) * 4);
+        w.types = up(size_t(p->n_expand) * s->num_kv_heads);
     }
-    w.total = w.parts + w.partials + 2 * w.expanded + w.ctx;
+    w.total = w.parts + w.partials + 2 * w.expanded + w.ctx + w.types;
     return w;
 }
 
@@ -1204,6 +1241,7 @@ extern "C" int32_t paged_attention_step_q4(const void* q, const void* k_pool, co
         e.v_out = reinterpret_cast<__nv_bfloat16*>(at + w.parts + w.partials + w.expanded);
         e.ex_ctx = reinterpret_cast<int32_t*>(at + w.parts + w.partials + 2 * w.expanded);
         e.queue = queue = e.ex_ctx + P.B;
+        e.v16 = reinterpret_cast<uint8_t*>(e.ex_ctx) + w.ctx;
         e.err = err_flag;
         e.B = P.B;
         e.cols = P.expand_cols;
@@ -1222,7 +1260,7 @@ extern "C" int32_t paged_attention_step_q4(const void* q, const void* k_pool, co
         ex.block_size = 128;
         ex.num_blocks = P.n_expand;
         st = attention_step_expanded(q, e.k_out, e.v_out, e.ex_table, e.cols, cu_seqlens_q, e.ex_ctx, P.B,
-                                     P.T, P.max_ctx,
+                                     P.T, P.max_ctx, e.v16,
                                      reinterpret_cast<const pa_work_item*>(words + f.chunk), P.n_chunk,
                                      w.partials ? at + w.parts : nullptr, out, &ex, err_flag, stream);
         if (st) return st;

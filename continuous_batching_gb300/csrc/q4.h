@@ -203,21 +203,61 @@ __device__ __forceinline__ uint4 q4_columns(const uint32_t (&w)[D / kQ4Group],
                       __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632));
 }
 
-// A lane's codes and its row's parameters; `at` is q4_base of the block and head, o the token in it.
+// Two values in f16, rounded to odd (cut, the last bit set where bits were cut off): an output that is one value alone
+// is then that value rounded to bf16 once.
+__device__ __forceinline__ uint32_t q4_odd_f16(float lo, float hi) {
+    uint32_t h;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+    // the 13 bits that f16 does not have, plus 2^13 - 1: bit 13 is set where they are not all zeros
+    const uint32_t cut = (__byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410) & 0x1FFF1FFFu) + 0x1FFF1FFFu;
+    return h | ((cut >> 13) & 0x00010001u);
+}
+
+// The columns of a V row in f16: in fp32, where the value is off by 2^-24 at most, then one rounding (below 2^-14 more
+// bits are cut off than are looked at).
+template <int D>
+__device__ __forceinline__ uint4 q4_columns_f16(const uint32_t (&w)[D / kQ4Group], const uint32_t (&p)[D / kQ4Group],
+                                                int g) {
+    constexpr int G = D / kQ4Group;
+    const uint32_t x = __byte_perm(w[g / 2], w[G / 2 + g / 2], g & 1 ? 0x7632 : 0x5410);
+    const float scale = __uint_as_float(p[g] << 16), low = __uint_as_float(p[g] & 0xFFFF0000u);
+    uint32_t y[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        uint32_t u = ((x >> (4 * n)) & 0x000F000Fu) | 0x43004300u;
+        asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(u) : "r"(0x43004300u));
+        y[n] = q4_odd_f16(fmaf(__uint_as_float(u << 16), scale, low), fmaf(__uint_as_float(u & 0xFFFF0000u), scale, low));
+    }
+    return make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
+                      __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632));
+}
+
+// A row's parameters; `at` is q4_base of the block and head, o the token in it.
+template <int D>
+__device__ __forceinline__ void q4_load_params(const uint8_t* pool, int64_t at, int bs, int o, uint32_t (&p)[D / kQ4Group]) {
+    const uint8_t* params = pool + at + bs * kQ4Codes<D> + o * kQ4Params<D>;
+    if constexpr (D == 128) {
+        const uint4 b = __ldg(reinterpret_cast<const uint4*>(params));
+        p[0] = b.x, p[1] = b.y, p[2] = b.z, p[3] = b.w;
+    } else {
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(params));
+        p[0] = b.x, p[1] = b.y;
+    }
+}
+
+// A lane's codes and its row's parameters.
 template <int D>
 __device__ __forceinline__ void q4_load_row(const uint8_t* pool, int64_t at, int bs, int o, int c,
                                             uint32_t (&w)[D / kQ4Group], uint32_t (&p)[D / kQ4Group]) {
     const uint8_t* codes = pool + at + o * kQ4Codes<D> + c * (D / 8);
-    const uint8_t* params = pool + at + bs * kQ4Codes<D> + o * kQ4Params<D>;
     if constexpr (D == 128) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(codes)), b = __ldg(reinterpret_cast<const uint4*>(params));
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(codes));
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-        p[0] = b.x, p[1] = b.y, p[2] = b.z, p[3] = b.w;
     } else {
-        const uint2 a = __ldg(reinterpret_cast<const uint2*>(codes)), b = __ldg(reinterpret_cast<const uint2*>(params));
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(codes));
         w[0] = a.x, w[1] = a.y;
-        p[0] = b.x, p[1] = b.y;
     }
+    q4_load_params<D>(pool, at, bs, o, p);
 }
 
 }  // namespace

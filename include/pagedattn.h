@@ -776,16 +776,17 @@ size_t pa_q4_workspace_bytes(const pa_shape* shape, const pa_q4_plan* plan);
  * elements below 2^-25 of its largest may lose bits; elements of 2^120 and more may overflow), fp32 sums, the
  * scales applied in fp32 (K is not rounded beyond its code), p in 16 bits, p * scale and the middle of a group
  * (minimum + 8 scale) each rounded once to bf16, splits whose length depends on the sequence's context alone, joined
- * in a fixed order. Rows over expanded contexts: K and V values rounded to bf16 and p as paged_attention_step
- * rounds it (against 64 bits an output is off by 0.0032 of its size where the other way leaves 0.0024 and its
- * own rounding to bf16 alone 0.0017), otherwise as that step (a NaN or infinity among the
+ * in a fixed order. Rows over expanded contexts: K rounded to bf16, V and p to f16 where the largest |V| of a block of
+ * 128 keys of the context and head is 0 or lies in 2^-12 .. 65,504, else to bf16. Against 64 bits an output is off by
+ * 0.0023 to 0.0024 of its size either way (0.0032 where V is bf16; its own rounding to bf16 alone is 0.0017).
+ * Otherwise the second way is as paged_attention_step (a NaN or infinity among the
  * V of a later key of the chunk reaches the rows before it, as there; not so for rows read from the
  * codes). Either way, as in paged_attention_step, p is relative to a reference that a score may pass by 8 in base 2, and
  * the sum of p is divided out at the end: where p |V| summed over the keys passes fp32 (values of 2^120 and more with
  * one key of that p, or smaller ones with more), an output may overflow.
  * A row's bits depend on its own query, keys, position and context, and on which of the two ways its
  * sequence takes: with direct_rows 0 every row takes the second, and a token has the same bits as a
- * single row and within a chunk.
+ * single row and within a chunk (unless later keys among the 128 of its last block take that one's V out of f16's part).
  * Device: words, the plan's; q, out [T, Hq, D] bf16; block_table [B, max_blocks], cu_seqlens_q, ctx_lens
  * as planned (items that they contradict are skipped and set PA_DEVERR_META, their rows not written);
  * keys of a block outside the pool read as 0 and set PA_DEVERR_BLOCK; workspace 16-byte aligned.

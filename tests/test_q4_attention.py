@@ -900,3 +900,104 @@ def test_roundings_of_rows_read_from_the_codes(D, Hq, Hkv):
     off = [np.sqrt(((y - exact) ** 2).sum() / (exact ** 2).sum()) for y in (got, two, one)]
     assert off[1] < off[2] and off[0] < np.sqrt(off[1] * off[2]), off
     assert (np.abs(got - exact) <= most).all(), float((np.abs(got - exact) / most).max())
+
+
+def _expanded(c, kinds):
+    """The rows of a case over expanded contexts with the roundings of K, V and p given (bf16 or f16) and the output's,
+    in 64 bits otherwise."""
+    near = {"bf16": lambda x: pa.bf16_to_f64(wl.f32_to_bf16_bits(np.asarray(x, np.float32))), "f16": lambda x: np.asarray(x, np.float16).astype(np.float64)}
+    q, g = pa.bf16_to_f64(c.q), c.Hq // c.Hkv
+    k, v = (q4.values(p, c.bs, c.D, i == 1).astype(np.float64) for i, p in enumerate(c.pools))
+    out = np.empty((c.T, c.Hq, c.D))
+    for s, (n, x) in enumerate(c.lens):
+        at = c.table[s, np.arange(x) // c.bs], np.arange(x) % c.bs
+        ks, vs = near[kinds[0]](k[at]), near[kinds[1]](v[at])
+        a = np.einsum("nhgd,khd->hgnk", q[c.cu[s]:c.cu[s + 1]].reshape(n, c.Hkv, g, c.D), ks) / np.sqrt(c.D)
+        a[..., np.arange(x) > np.arange(x - n, x)[:, None]] = -np.inf
+        p = np.exp(a - a.max(-1, keepdims=True))
+        o = np.einsum("hgnk,khd->nhgd", near[kinds[2]](p), vs) / p.sum(-1).transpose(2, 0, 1)[..., None]
+        out[c.cu[s]:c.cu[s + 1]] = near["bf16"](o.reshape(n, c.Hq, c.D))
+    return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D, Hq, Hkv", [(128, 8, 2), (64, 8, 1)])
+@pytest.mark.parametrize("power", [-60, -18, -12, -8, 0, 8, 13, 16, 100])
+def test_roundings_of_rows_over_expanded_contexts(D, Hq, Hkv, power):
+    """The error against 64 bits is that of K and the output rounded to bf16, V and p to f16 (simulated here), for V of
+    every magnitude that f16 holds, and elsewhere no larger than with bf16 for all. The border between two
+    simulations is their geometric mean; 60,000 outputs leave each uncertain by less than 1 %."""
+    c = Case([(40, 700), (26, 1300)], Hq, Hkv, D, 16, seed=101)
+    params = np.ascontiguousarray(c.pools[1][:, :, c.bs * (D // 2):]).view("<u2")
+    with np.errstate(invalid="ignore"):
+        scaled = wl.f32_to_bf16_bits((pa.bf16_to_f64(params) * 2.0 ** power).astype(np.float32))
+    c.pools[1][:, :, c.bs * (D // 2):] = np.where(params == 0xFFFF, params, scaled).astype("<u2").view(np.uint8)
+    exact = c.exact()
+    far = lambda y: np.sqrt((((y - exact) / 2.0 ** power) ** 2).sum() / ((exact / 2.0 ** power) ** 2).sum())
+    got, low = far(pa.bf16_to_f64(c.run(0))), far(_expanded(c, ("bf16", "bf16", "bf16")))
+    if -12 <= power <= 13:
+        # (every block's largest value lies between 1 and 6: in f16's part of the magnitudes, 2^-12 to 65,504)
+        high = far(_expanded(c, ("bf16", "f16", "f16")))
+        assert high < 0.8 * low and got < np.sqrt(high * low), (got, high, low)
+    else:
+        assert got < 1.05 * low, (got, low)
+
+
+@pytest.mark.gpu
+def test_blocks_of_both_types_of_values():
+    """Blocks of 128 keys whose V is too small for f16, fits, and is too large, one behind the other: every row against
+    64 bits. A row's error is four roundings of at most 2^-8 / sqrt(3) of its size each (0.0045 together);
+    twice that is left for the few keys of a row at a block's begin. A NaN leaves the bits of the other groups' columns."""
+    c = Case([(384, 384), (40, 200)], seed=103)
+    at = np.concatenate([c.table[0][np.arange(384) // 16] * 16 + np.arange(384) % 16, c.table[1][np.arange(200) // 16] * 16 + np.arange(200) % 16])
+    x = pa.bf16_to_f64(wl.random_bf16(np.random.default_rng(5), (584, 2, 128)))
+    x[:384] *= np.repeat(2.0 ** np.array([-30.0, 0.0, 30.0]), 128)[:, None, None]
+    c.pools[1] = q4.write(c.pools[1], wl.f32_to_bf16_bits(x.astype(np.float32)), at, 16, True)
+    got, exact = pa.bf16_to_f64(c.run(8)), c.exact()
+    off = np.sqrt(((got - exact) ** 2).sum((1, 2)) / (exact ** 2).sum((1, 2)))
+    assert off.max() < 0.009, (off.max(), off.argmax())
+    clean = c.run(8)
+    bits = wl.f32_to_bf16_bits(x[-1:].astype(np.float32))
+    bits[0, 1, 40] = 0x7FC0
+    c.pools[1] = q4.write(c.pools[1], bits, at[-1:], 16, True)
+    got = c.run(8)
+    keep = np.ones((8, 128), bool)
+    keep[4:, 32:64] = False
+    assert np.array_equal(got[:, keep], clean[:, keep]) and np.isnan(pa.bf16_to_f64(got[-1, 4:, 32:64])).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("direct_rows", [0, 16])
+def test_a_captured_step_follows_the_values_types(direct_rows):
+    """Replays of one graph while V changes between magnitudes that f16 holds, holds in some blocks, in none: each gives
+    the bits of a step called for those pools."""
+    c = Case([(40, 900), (1, 2100), (129, 300)], seed=107)
+    k, v, table, cu, ctx = (dev(x) for x in (*c.pools, c.table, c.cu, c.ctx))
+    plan = c.plan(direct_rows)
+    ws = torch.empty(bd.pa_q4_workspace_bytes(c.shape, plan) // 4, device="cuda")
+    q, out = bf16(c.q), torch.zeros(c.T, 8, 128, dtype=torch.bfloat16, device="cuda")
+    step = lambda: bd.paged_attention_step_q4(q, k, v, table, cu, ctx, plan, ws, out, c.shape)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    params = np.ascontiguousarray(c.pools[1][:, :, 16 * 64:]).view("<u2")
+    plain = c.pools[1].copy()
+    some = np.zeros(c.nb, bool)
+    some[c.table[0, 20:30]] = some[c.table[1, 3]] = True
+    for power, where in ((0, some), (30, some), (-30, some), (0, some), (40, ~some), (40, some | True), (0, some)):
+        with np.errstate(invalid="ignore"):
+            scaled = wl.f32_to_bf16_bits((pa.bf16_to_f64(params) * 2.0 ** power).astype(np.float32))
+        scaled = np.where((params != 0xFFFF) & where[:, None, None], scaled, params)
+        c.pools[1] = plain.copy()
+        c.pools[1][:, :, 16 * 64:] = scaled.astype("<u2").view(np.uint8)
+        v.copy_(dev(c.pools[1]))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = bits_of(out)
+        assert np.array_equal(got, c.run(plan=plan)) and np.array_equal(got, c.run(direct_rows))
+        exact = c.exact()
+        off = np.sqrt(((pa.bf16_to_f64(got) - exact) ** 2).sum((1, 2)) / (exact ** 2).sum((1, 2)))
+        assert off.max() < 0.009, (power, off.max())          # (as in test_blocks_of_both_types_of_values)
