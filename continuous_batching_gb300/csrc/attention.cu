@@ -743,10 +743,10 @@ __device__ __forceinline__ void zero_v_tail(uint32_t vb, int kb, int ctx, int bs
 // instantiation of its own, so that the plain step's registers and time stay what they are: 32 decode
 // rows at 4k .. 16k keys 230 us, with log-sum-exps 231, with 44 MB of scores some 7 more).
 // V16: the contexts are those of a 4-bit cache expanded for this step, blocks of 128 keys, K in bf16 and V in f16
-// where f16 holds it, else in bf16 (p.v16 says which); a tile's P has the type of its V. Beside bf16 for all, two of an output's
-// four roundings have 11 bits in place of 8: against 64 bits 0.0032 -> 0.0023 of its size. Every CTA first sees whether all
-// of the step's blocks are f16, as they mostly are: the MMA warp then has a loop without a choice (four 512-row chunks: 195 us; with
-// the type of each tile looked up there 203, bf16 for all 193).
+// where f16 holds it, else in bf16 (p.v16 says which); a tile's P has the type of its V. Beside bf16 for all, two of an
+// output's four roundings have 11 bits in place of 8: against 64 bits 0.0032 -> 0.0023 of its size. Every CTA first sees
+// whether all of the step's blocks are f16, as they mostly are: the MMA warp then has a loop without a choice. (Four
+// 512-row chunks with their expansion, in a graph: 216 us, 227 with one bf16 block among them, 210 with bf16 for all.)
 template <int D, bool F8, bool STATS, bool V16>
 __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -1296,6 +1296,22 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                                         tmem + kTmemO + (sg & 1) * 128 + lanes, r0, rs, q4,
                                         I.rows_valid, I.q_start, I.kvh, I.pos0);
             }
+            // V16, blocks of both types: that of the next tile, and the block of the one after it, are asked for a tile
+            // ahead
+            const auto block_of = [&](int jt) {
+                return jt < I.n_tiles ? __ldg(p.block_table + int64_t(I.seq) * p.max_blocks + I.k_begin / kTileKeys + jt) : -1;
+            };
+            const auto type_of = [&](int block) -> uint8_t {
+                return block >= 0 && block < p.num_blocks ? __ldcg(p.v16 + int64_t(block) * p.Hkv + I.kvh) : 0;
+            };
+            int block = -1;
+            uint8_t type = 0;
+            if constexpr (V16) {
+                if (!all16) {
+                    type = type_of(block_of(0));
+                    block = block_of(1);
+                }
+            }
             for (int jt = 0; jt < I.n_tiles; ++jt, ++tc) {
                 // every split starts afresh, exactly as an item of that split alone would
                 const int jin = (jt0 + jt) & (kSplitTiles - 1);
@@ -1314,11 +1330,11 @@ __global__ void __launch_bounds__(kThreadsFor<F8>, 1)
                 }
                 bool half = F8;
                 if constexpr (V16) {
-                    half = all16;
+                    half = all16 || type;
                     if (!all16) {
-                        const int block = p.block_table[int64_t(I.seq) * p.max_blocks + kb / kTileKeys];
-                        half = block >= 0 && block < p.num_blocks && __ldcg(p.v16 + int64_t(block) * p.Hkv + I.kvh);
                         if (tid == 0) *reinterpret_cast<volatile int*>(smem + L::kBar + kTypeOff + 4 * (tc & 1)) = half;
+                        type = type_of(block);
+                        block = block_of(jt + 2);
                     }
                 }
                 if (on)

@@ -21,7 +21,10 @@ namespace pa_detail {
 // short ones where there are few, so that a single sequence spreads over the GPU, and longer ones where
 // what a split costs beyond its keys (its start, its result written and read once more) would add up.
 // Multiples of 32. (64 sequences of median 2,048 keys / 12 of 700 to 6,000 / one of 16,001: 72.8 / 13.7 / 20.5 us; with 512
-// keys up to 32,768 78.4 / 13.7 / 15.2, half of each length 80.9 / 12.7 / 15.2, 640 up to 6,144 71.0 / 15.4 / 20.5.)
+// keys up to 32,768 78.4 / 13.7 / 15.2, half of each length 80.9 / 12.7 / 15.2, 640 up to 6,144 71.0 / 15.4 / 20.5. At the
+// borders, 1 / 8 / 32 sequences of 32 / 8 heads, caches cold, with the shorter split and, a key further, with the longer
+// one: 6,144 keys 20 / 29 / 75 and 24 / 34 / 75 us; 12,288 24 / 50 / 125 and 28 / 42 / 126; 32,768 30 / 95 / 276 and 42 / 106 / 287: a
+// longer split costs the sequences that are few, as said, and gains where one round of items becomes less than one.)
 __host__ __device__ constexpr int64_t q4_split_keys(int32_t ctx) {
     return ctx <= 6144 ? 512 : ctx <= 12288 ? 768 : ctx <= 32768 ? 1024 : 2048;
 }

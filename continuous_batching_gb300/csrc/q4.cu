@@ -5,7 +5,8 @@
 // Sequences of few rows (tokens x heads of a group, direct_rows or fewer: single tokens, drafted tokens) are
 // computed from the codes themselves, never expanded to memory; see q4_direct_kernel. Sequences with more rows
 // (chunks) have their context expanded once to bf16 in the workspace and go through the tcgen05 step of
-// the bf16 cache: the products are then the cost, and an expansion of a few us serves every row tile.
+// the bf16 cache: the products are then the cost, and an expansion of a few us serves every row tile. V and P are
+// f16 there, three bits more than bf16, where V's magnitudes allow.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -151,8 +152,9 @@ struct ExpandParams {
 // CTA (i, h): block i of the plan's list, head h: 128 tokens of K to bf16, the values of paged_kv_read_q4, and of V to
 // f16, 3 bits more, where the block's largest |V| lies in 2^-12 .. 65,504 or is 0 (groups that are NaN aside), so that
 // what is too small for f16's bits is off by 2^-12 of the largest or less; else V is bf16, too.
-// Bound by memory (512 bytes a token and head written, 160 read): 21,900
-// tokens of 8 heads take 14 us ahead of the attention that reads them.
+// Bound by memory (512 bytes a token and head written, 160 read): 21,900 tokens of 8 heads take 18 us ahead of the
+// attention that reads them, 3 of them for V's type: its values wait for all of the block's parameters, while K's are
+// written. (Every warp looking at all of the parameters, without a barrier: 2 us more.)
 // The sequences whose context is expanded whole are told to the attention by ex_ctx; the others (rows that
 // are read directly, metadata that the plan was not made for, a context that the block table does not cover) have a
 // context of 0 there, by which the attention refuses their items.
@@ -265,22 +267,24 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const ExpandParams p) {
 //   O = sum_j w_j (u_j - 8) + sum_j p_j bf16(m_jg + 8 s_jg)
 // u - 8 and not u: |u - 8| s is the size of the value's distance from its group's middle, u s twice that, and so
 // would the roundings of w be. p is a sum of two bf16 (16 bits: p itself rounded to one would add an error
-// as large as that of w; against 64 bits the output's was 0.0028 so and is 0.0022, 73.1 -> 74.5 us for the decode
+// as large as that of w; against 64 bits the output's would be 0.0028 so and is 0.0023 to 0.0024, at 1.4 us of the decode
 // batch below); w = fma(p_hi, s, p_lo s) rounds once. P^T's layout is turned by movmatrix, once for all groups.
 // A masked key's parameters may be anything (it may not have been written yet), and 0 times them too: its w
 // are cleared for the rows that do not see it, its centre is clamped to numbers. What is not finite still
-// reaches the rows that see it, through w.
+// reaches the rows that see it, through w (the write makes such a group's scale NaN, too).
 //
 // Loads: cp.async into a ring of kStages tiles per warp (codes and parameters; blocks outside the pool are
 // filled with zeros, keys of a block behind the last row may hold anything and are masked), no barrier
 // but the warp's own.
 //
-// Measured, with the join, replayed in a graph: 64 sequences of median 2,048 (up to 16,384) keys, 32 / 8 heads of 128
-// (314 MB of cache): 72.8 us, 4.3 TB/s; 32 of 1,000 to 40,000 keys, 64 / 8 heads: 57; 12 of 4 rows, 16 / 4
-// heads of 64: 13.7; one of 16,001 keys: 20.5. 32 single rows beside a chunk of 257: 82, 14 more when they waited for
-// the chunk's 72 CTAs (or these for them). The copies alone take 63 us of the first: what the rest is bound by is
-// a tile's chain of products and softmax, 1,036 cycles with three warps a scheduler, of which the memory's rate
-// leaves 871. Tried without gain: 16 warps of 128 registers, a third stage, the next tile's scores between the
+// Measured, with the join, calls one behind the other: 64 sequences of median 2,048 (up to 16,384) keys, 32 / 8 heads
+// of 128 (314 MB of cache): 73 us, 4.3 TB/s; 32 of 1,000 to 40,000 keys, 64 / 8 heads: 57; 12 of 4 rows, 16 / 4
+// heads of 64: 13.7; one of 16,001 keys: 20.7. 32 single rows beside a chunk of 257: 85, 14 more when they waited for
+// the chunk's 72 CTAs (or these for them). What bounds it: replayed in graphs, where the four take 76, 60, 17 and 24 us,
+// the same kernel without its arithmetic, copies, items and join alone, takes 61, 49, 10 and 12. So of the first's 30 us above
+// its bytes (46) half is the way of the bytes and half the arithmetic beyond it, a tile's chain of products and softmax
+// with three warps a scheduler; a sequence by itself is its 16 tiles of one warp, one behind the other.
+// Tried without gain: 16 warps of 128 registers, a third stage, the next tile's scores between the
 // values' products, K as e4m3 (its mma.sync is emulated), splits joined inside this kernel (20 to 40 us more), the
 // next item's first tiles or its L2 lines asked for ahead (3 to 6 us more).
 struct DirectParams {
