@@ -24,7 +24,7 @@ namespace pa_detail {
 // keys up to 32,768 78.4 / 13.7 / 15.2, half of each length 80.9 / 12.7 / 15.2, 640 up to 6,144 71.0 / 15.4 / 20.5. At the
 // borders, 1 / 8 / 32 sequences of 32 / 8 heads, caches cold, with the shorter split and, a key further, with the longer
 // one: 6,144 keys 20 / 29 / 75 and 24 / 34 / 75 us; 12,288 24 / 50 / 125 and 28 / 42 / 126; 32,768 30 / 95 / 276 and 42 / 106 / 287: a
-// longer split costs the sequences that are few, as said, and gains where one round of items becomes less than one.)
+// longer split costs where sequences are few, with one exception.)
 __host__ __device__ constexpr int64_t q4_split_keys(int32_t ctx) {
     return ctx <= 6144 ? 512 : ctx <= 12288 ? 768 : ctx <= 32768 ? 1024 : 2048;
 }
