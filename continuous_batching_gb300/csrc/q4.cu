@@ -4,7 +4,7 @@
 //
 // Sequences of few rows (tokens x heads of a group, direct_rows or fewer: single tokens, drafted tokens) are
 // computed from the codes themselves, never expanded to memory; see q4_direct_kernel. Sequences with more rows
-// (chunks) have their context expanded once to bf16 in the workspace and go through the tcgen05 step of
+// (chunks) have their context expanded once to 16 bits in the workspace and go through the tcgen05 step of
 // the bf16 cache: the products are then the cost, and an expansion of a few us serves every row tile. V and P are
 // f16 there, three bits more than bf16, where V's magnitudes allow.
 #include <cuda_bf16.h>

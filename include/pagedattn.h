@@ -736,7 +736,7 @@ int32_t paged_kv_read_q4(const int32_t* slot_mapping, int32_t T, const void* k_p
  * pa_plan_step_q4 and copied to the device by the caller. direct_rows parts the sequences: one whose
  * n_q * group is at most direct_rows has its rows computed from the codes as they are (tiles of up to 8 rows, or of
  * 16 where direct_rows is above 8 and either the group is or a step without chunks has more rows than sequences); the
- * context of any other is expanded to bf16 once, 128-token block by
+ * context of any other is expanded to 16 bits once, 128-token block by
  * block, in the workspace, and its rows go through the kernel of paged_attention_step.
  * pa_q4_direct_rows gives a fast choice. */
 typedef struct pa_q4_plan {
